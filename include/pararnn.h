@@ -701,6 +701,167 @@ PARARNN_API int pararnn_lstm_solve_host_streamed(const pararnn_cell *cell, const
 /* Workspace bytes of pararnn_lstm_solve_host_streamed; 0 if the arguments are rejected. */
 PARARNN_API size_t pararnn_lstm_host_streamed_workspace_size(const pararnn_cell *cell, int B, int T, int parts);
 
+/* Activations of pararnn_group_norm: z, z sigmoid(z), z Phi(z) (the exact GELU). */
+typedef enum { PARARNN_ACT_NONE = 0, PARARNN_ACT_SILU = 1, PARARNN_ACT_GELU = 2 } pararnn_activation;
+
+/* An operand [B, T, heads, width] of linear attention, DEVICE: element strides
+ * of the batch, time and head axes (>= 0; the width axis is contiguous), so q,
+ * k and v may be views of one projected tensor.  Aligned to its element; rows
+ * that start on 16-byte boundaries are read fastest. */
+typedef struct {
+    const void *ptr;
+    long long stride_b, stride_t, stride_h;
+} pararnn_rows;
+
+/* Linear attention with a decay for each head.
+ *   B, T     sequences and tokens, >= 1.
+ *   H, Hkv   heads of q and of k, v; H a multiple of Hkv (head h reads key and
+ *            value head h / (H / Hkv)).
+ *   dk, dv   widths of q, k and of v: 1 .. 128.
+ *   dtype    pararnn_dtype of q, k, v and of the outputs and gradients.
+ *   scale    multiplies the outputs (finite). */
+typedef struct {
+    int B, T, H, Hkv, dk, dv;
+    int dtype;
+    float scale;
+} pararnn_attention_shape;
+
+/* pararnn_linear_attention_workspace_size -- bytes pararnn_linear_attention
+ * needs, or 0 for arguments it rejects. */
+PARARNN_API size_t pararnn_linear_attention_workspace_size(const pararnn_attention_shape *shape);
+
+/*
+ * pararnn_linear_attention -- the linear recurrence with a matrix state: for
+ * every sequence b and head h, with g = exp(log_decay[h]),
+ *   S_t = g S_{t-1} + k_t v_t^T   [dk, dv],    o_t = scale * S_t^T q_t,
+ * for t < lengths[b], evaluated for all tokens at once: within a chunk as
+ * masked matrix products, across chunks through the state, and, where there
+ * are few sequences and heads, in segments of time that run at the same time.
+ * (The counterpart of pararnn_affine_scan, whose state is a vector.)
+ *   q        [B, T, H, dk];  k [B, T, Hkv, dk];  v [B, T, Hkv, dv]  (pararnn_rows).
+ *   log_decay  DEVICE float [H], each <= 0 (0: no decay; -inf: only the token
+ *            itself); a positive or NaN value makes that head's results undefined.
+ *   s0       DEVICE float [B, H, dk, dv], the state before the first token, or
+ *            NULL for zero.
+ *   lengths  DEVICE int [B], or NULL for T: tokens at and behind lengths[b]
+ *            (clamped to 0 .. T) are not read, their outputs are zero, and the
+ *            state is the one after lengths[b] tokens.
+ *   o        DEVICE [B, T, H, dv] of shape->dtype, output.
+ *   s        DEVICE float [B, H, dk, dv], output: the last state.  May be s0 itself.
+ *   workspace  DEVICE, pararnn_linear_attention_workspace_size bytes, 256-byte aligned.
+ * The state and all sums are fp32.  With bf16 operands the weighted scores and
+ * a copy of the state are rounded to bf16 where they enter the products for o;
+ * the state itself is updated from products exact to fp32.  A token that is
+ * not finite makes the outputs of the 256 tokens before it undefined as well as
+ * those after it.  Outputs must not overlap inputs or the workspace.  Repeated
+ * calls give the same bits.  Asynchronous: returns PARARNN_OK, INVALID_ARG or
+ * CUDA_ERROR.
+ */
+PARARNN_API int pararnn_linear_attention(const pararnn_attention_shape *shape, const pararnn_rows *q,
+                                         const pararnn_rows *k, const pararnn_rows *v, const float *log_decay,
+                                         const float *s0, const int *lengths, void *o, float *s, void *workspace,
+                                         size_t ws_bytes, pararnn_stream stream);
+
+/* pararnn_linear_attention_backward_workspace_size -- bytes
+ * pararnn_linear_attention_backward needs, or 0 for arguments it rejects. */
+PARARNN_API size_t pararnn_linear_attention_backward_workspace_size(const pararnn_attention_shape *shape);
+
+/*
+ * pararnn_linear_attention_backward -- its backward pass: from dL/do and dL/ds
+ * (the last state's) to dL/dq, dL/dk, dL/dv and dL/ds0.  With the states of the
+ * forward pass and R_t = g R_{t+1} + scale q_t do_t^T, the last R being
+ * ds + scale q do^T,
+ *   dq_t = scale S_t do_t,  dk_t = R_t v_t,  dv_t = R_t^T k_t,  ds0 = g R_0,
+ * dk and dv summed over the heads that share a key and value head, in head
+ * order.  The decays are constants of the model: they get no gradient.
+ *   q, k, v, log_decay, s0, lengths  as given to the forward pass.
+ *   d_o      [B, T, H, dv] of shape->dtype (pararnn_rows).
+ *   ds       DEVICE float [B, H, dk, dv], or NULL for zero.
+ *   dq, dk, dv  DEVICE, dense, shapes and type of q, k, v; zero at and behind lengths[b].
+ *   ds0      DEVICE float [B, H, dk, dv], or NULL where it is not wanted.
+ *   workspace  DEVICE, pararnn_linear_attention_backward_workspace_size bytes.
+ * Outputs must not overlap inputs or the workspace.  Precision, determinism and
+ * the return value as pararnn_linear_attention.
+ */
+PARARNN_API int pararnn_linear_attention_backward(const pararnn_attention_shape *shape, const pararnn_rows *q,
+                                                  const pararnn_rows *k, const pararnn_rows *v,
+                                                  const float *log_decay, const pararnn_rows *d_o, const float *s0,
+                                                  const float *ds, const int *lengths, void *dq, void *dk, void *dv,
+                                                  float *ds0, void *workspace, size_t ws_bytes,
+                                                  pararnn_stream stream);
+
+/*
+ * pararnn_linear_attention_step -- the recurrence for one token of each
+ * sequence (shape->T = 1): S = g S + k v^T, o = scale * S^T q.
+ *   q [B, H, dk], k [B, Hkv, dk], v [B, Hkv, dv]  (pararnn_rows; stride_t unused).
+ *   state    DEVICE float [n_slots, H, dk, dv], the states before the token.
+ *   slots    DEVICE int [B]: row b's state is state[slots[b]]; a row whose slot
+ *            is outside 0 .. n_slots - 1 has no state: its output is zero.  Rows
+ *            that name the same slot are taken one after the other in row
+ *            order, as tokens that follow each other.  NULL: slot b for row b
+ *            (n_slots = B).
+ *   o        DEVICE [B, H, dv] of shape->dtype, output.
+ *   out_state  DEVICE float [n_slots, H, dk, dv]: the states after the token are
+ *            written here, at the same slots (other slots are left as they
+ *            are).  May be `state` itself; must not overlap it otherwise.
+ * Everything is fp32 but the rounding of o.  Asynchronous; no workspace;
+ * returns PARARNN_OK, INVALID_ARG or CUDA_ERROR.
+ */
+PARARNN_API int pararnn_linear_attention_step(const pararnn_attention_shape *shape, const pararnn_rows *q,
+                                              const pararnn_rows *k, const pararnn_rows *v, const float *log_decay,
+                                              const float *state, const int *slots, int n_slots, void *o,
+                                              float *out_state, pararnn_stream stream);
+
+/* Group norm with an activation or a gate over channels-last rows.
+ *   N, S, C   x is [N, S, C]: statistics are taken over the S rows and the
+ *             C / groups channels of each group, for each n (S = 1 normalises
+ *             the groups of every row by themselves, as for the heads of o).
+ *   groups    divides C; at most 2048.
+ *   x_dtype   of x, gate and their gradients;  y_dtype  of y and its gradient.
+ *   act       pararnn_activation;  eps  added to the variance, >= 0. */
+typedef struct {
+    int N, S, C, groups;
+    int x_dtype, y_dtype;
+    int act;
+    float eps;
+} pararnn_norm_shape;
+
+/* Bytes of workspace the two calls below need, or 0 for rejected arguments. */
+PARARNN_API size_t pararnn_group_norm_workspace_size(const pararnn_norm_shape *shape);
+PARARNN_API size_t pararnn_group_norm_backward_workspace_size(const pararnn_norm_shape *shape);
+
+/*
+ * pararnn_group_norm -- what stands between two recurrent layers: with m, r the
+ * mean and 1 / sqrt(variance + eps) of a group,
+ *   z = (x - m) r weight + bias,   y = act(z), or y = z * act(gate) with a gate.
+ * x can be the fp32 states of a solve and y the bf16 input of the next one, or
+ * x the outputs of pararnn_linear_attention (S = 1, a group per head).
+ *   x        DEVICE [N, S, C];  gate  DEVICE [N, S, C] or NULL.
+ *   weight, bias  DEVICE float [C], NULL for ones and zeros.
+ *   lengths  DEVICE int [N] or NULL: rows at and behind lengths[n] (clamped to
+ *            0 .. S) are not read, do not count, and are zero in y.
+ *   y        DEVICE [N, S, C], output;  stats  DEVICE float [N, groups, 2],
+ *            output: m and r (0 and 1 / sqrt(eps) where no row counts).
+ * All sums are fp32, about local means, in a fixed order.  Outputs must not
+ * overlap inputs or the workspace.  Asynchronous: returns PARARNN_OK,
+ * INVALID_ARG or CUDA_ERROR.
+ */
+PARARNN_API int pararnn_group_norm(const pararnn_norm_shape *shape, const void *x, const float *weight,
+                                   const float *bias, const void *gate, const int *lengths, void *y, float *stats,
+                                   void *workspace, size_t ws_bytes, pararnn_stream stream);
+
+/*
+ * pararnn_group_norm_backward -- its backward pass.  stats are the forward's;
+ * dy [N, S, C] of y_dtype.  dx, dgate [N, S, C] of x_dtype (dgate exactly where
+ * there is a gate; zero at and behind lengths[n]); dweight, dbias float [C],
+ * NULL where they are not wanted.  Other arguments, sums and the return value
+ * as pararnn_group_norm.
+ */
+PARARNN_API int pararnn_group_norm_backward(const pararnn_norm_shape *shape, const void *x, const float *stats,
+                                            const void *dy, const float *weight, const float *bias, const void *gate,
+                                            const int *lengths, void *dx, float *dweight, float *dbias, void *dgate,
+                                            void *workspace, size_t ws_bytes, pararnn_stream stream);
+
 /* pararnn_status_string -- a static, human-readable name of a status code. */
 PARARNN_API const char *pararnn_status_string(int status);
 

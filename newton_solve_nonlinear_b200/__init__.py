@@ -6,5 +6,6 @@ The compute lives in ``libpararnn.so`` (CUDA kernels behind the C ABI of
 not load the library; the first call does, and raises if it is missing.
 """
 from .binding import (  # noqa: F401
-    SolveResult, affine_scan, alloc_workspace, newton_solve, solve_workload, workspace_size,
+    SolveResult, affine_scan, alloc_workspace, group_norm, group_norm_backward, linear_attention,
+    linear_attention_backward, linear_attention_step, newton_solve, solve_workload, workspace_size,
 )

@@ -19,6 +19,7 @@ DEER, QUASI, ELK, QUASI_ELK = 0, 1, 2, 3
 MODES = {"DEER": DEER, "QUASI": QUASI, "ELK": ELK, "QUASI_ELK": QUASI_ELK}
 GRU_DENSE, GRU_DIAG, LSTM_DIAG = 0, 1, 2
 F32, BF16 = 0, 1
+ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2}
 STATUS = {0: "OK", 1: "NOT_CONVERGED", 2: "DIVERGED", 3: "INVALID_ARG", 4: "CUDA_ERROR",
           5: "TIMEOUT"}
 EXPORTS = ("pararnn_workspace_size", "pararnn_newton_solve", "pararnn_newton_solve_async",
@@ -34,7 +35,11 @@ EXPORTS = ("pararnn_workspace_size", "pararnn_newton_solve", "pararnn_newton_sol
            "pararnn_adjoint_exact_workspace_size", "pararnn_newton_solve_host_streamed",
            "pararnn_host_streamed_workspace_size", "pararnn_lstm_solve_host_streamed",
            "pararnn_lstm_host_streamed_workspace_size", "pararnn_affine_scan_host",
-           "pararnn_affine_scan_host_workspace_size")
+           "pararnn_affine_scan_host_workspace_size", "pararnn_linear_attention",
+           "pararnn_linear_attention_workspace_size", "pararnn_linear_attention_backward",
+           "pararnn_linear_attention_backward_workspace_size", "pararnn_linear_attention_step",
+           "pararnn_group_norm", "pararnn_group_norm_workspace_size", "pararnn_group_norm_backward",
+           "pararnn_group_norm_backward_workspace_size")
 
 
 class Cell(ctypes.Structure):
@@ -50,6 +55,20 @@ class Params(ctypes.Structure):
 class Info(ctypes.Structure):
     _fields_ = [("iters", ctypes.c_int), ("status", ctypes.c_int),
                 ("delta", ctypes.c_float), ("residual", ctypes.c_float)]
+
+
+class Rows(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("stride_b", ctypes.c_longlong), ("stride_t", ctypes.c_longlong),
+                ("stride_h", ctypes.c_longlong)]
+
+
+class AttentionShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "T", "H", "Hkv", "dk", "dv", "dtype")] + [("scale", ctypes.c_float)]
+
+
+class NormShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("N", "S", "C", "groups", "x_dtype", "y_dtype", "act")] + [
+        ("eps", ctypes.c_float)]
 
 
 _lib = None
@@ -146,6 +165,24 @@ def lib() -> ctypes.CDLL:
         L.pararnn_adjoint_exact.restype = ci
         L.pararnn_adjoint_exact_workspace_size.argtypes = [ctypes.POINTER(Cell), ci, ci]
         L.pararnn_adjoint_exact_workspace_size.restype = sz
+        shape_p, rows_p, norm_p = ctypes.POINTER(AttentionShape), ctypes.POINTER(Rows), ctypes.POINTER(NormShape)
+        for name in ("pararnn_linear_attention_workspace_size", "pararnn_linear_attention_backward_workspace_size"):
+            getattr(L, name).argtypes = [shape_p]
+            getattr(L, name).restype = sz
+        L.pararnn_linear_attention.argtypes = [shape_p, rows_p, rows_p, rows_p, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.pararnn_linear_attention.restype = ci
+        L.pararnn_linear_attention_backward.argtypes = [shape_p, rows_p, rows_p, rows_p, vp, rows_p, vp, vp, vp, vp, vp,
+                                                        vp, vp, vp, sz, vp]
+        L.pararnn_linear_attention_backward.restype = ci
+        L.pararnn_linear_attention_step.argtypes = [shape_p, rows_p, rows_p, rows_p, vp, vp, vp, ci, vp, vp, vp]
+        L.pararnn_linear_attention_step.restype = ci
+        for name in ("pararnn_group_norm_workspace_size", "pararnn_group_norm_backward_workspace_size"):
+            getattr(L, name).argtypes = [norm_p]
+            getattr(L, name).restype = sz
+        L.pararnn_group_norm.argtypes = [norm_p, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.pararnn_group_norm.restype = ci
+        L.pararnn_group_norm_backward.argtypes = [norm_p, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.pararnn_group_norm_backward.restype = ci
         L.pararnn_status_string.argtypes = [ci]
         L.pararnn_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -725,3 +762,235 @@ def affine_scan_host(A_host, b_host, h0_host, *, parts: int = 7, out=None, works
     if rc != 0:
         raise RuntimeError(f"pararnn_affine_scan_host: {L.pararnn_status_string(rc).decode()}")
     return out
+
+
+# ---- sequence layers: linear attention with a decay for each head, group norm -------------------------------
+
+
+class _on:
+    """The launch context of a call on tensors of ``device``: makes it the current device and, where the caller
+    names a stream, allocates on that stream, so that the allocator keeps the call's own memory in order with it."""
+
+    def __init__(self, device, stream):
+        self.enter = []
+        if device.type == "cuda":
+            if stream is not None:
+                self.enter.append(torch.cuda.stream(stream))
+            elif torch.cuda.current_device() != device.index:
+                self.enter.append(torch.cuda.device(device))
+
+    def __enter__(self):
+        for c in self.enter:
+            c.__enter__()
+
+    def __exit__(self, *exc):
+        for c in reversed(self.enter):
+            c.__exit__(*exc)
+
+
+def _like(t, name: str, like, shape, dtype):
+    """Checks an argument's device, shape and type; the address of a dense tensor, None for None."""
+    if t is None:
+        return None
+    if t.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != torch.Size(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return _dev(t, name)
+
+
+def _rows(t, name: str, like, shape):
+    """A [B, T, heads, width] operand of like's type, strided in all but the last axis."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+    if t.shape != torch.Size(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    sb, st, sh, sw = t.stride()
+    if sw != 1 and shape[3] != 1:
+        raise ValueError(f"{name} must be contiguous along its last axis")
+    return Rows(t.data_ptr(), sb, st, sh)
+
+
+def _attention_shape(q, k, v, log_decay, scale):
+    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k and v must be [B, T, heads, width]")
+    B, T, H, dk = q.shape
+    Hkv, dv = k.shape[2], v.shape[3]
+    if min(B, T, H, Hkv) < 1 or H % Hkv:
+        raise ValueError(f"B, T and the head counts must be positive, q's heads a multiple of k's: {H} and {Hkv}")
+    if not (1 <= dk <= 128 and 1 <= dv <= 128):
+        raise ValueError(f"head widths must be 1 to 128: got {dk} and {dv}")
+    if log_decay.requires_grad:
+        raise ValueError("log_decay is a constant of the model: it gets no gradient")
+    shape = AttentionShape(B, T, H, Hkv, dk, dv, _dtype_code(q.dtype), dk ** -0.5 if scale is None else float(scale))
+    return shape, _rows(q, "q", q, (B, T, H, dk)), _rows(k, "k", q, (B, T, Hkv, dk)), _rows(v, "v", q, (B, T, Hkv, dv))
+
+
+def _workspace(need: int, name: str, workspace, device):
+    if need == 0:
+        raise ValueError(f"arguments rejected by {name}_workspace_size")
+    if workspace is None:
+        return alloc_workspace(need, device)
+    return workspace
+
+
+def _checked(rc: int, name: str):
+    if rc != 0:
+        raise RuntimeError(f"{name}: {lib().pararnn_status_string(rc).decode()}")
+
+
+def linear_attention(q, k, v, log_decay, *, s0=None, lengths=None, scale=None, out=None, workspace=None, stream=None):
+    """Linear attention with a decay for each head over whole sequences:
+    S_t = exp(log_decay) S_(t-1) + k_t v_t^T, o_t = scale * S_t^T q_t.
+
+    q [B,T,H,dk], k [B,T,Hkv,dk], v [B,T,Hkv,dv] (fp32 or bf16 CUDA; views with
+    any strides whose last axis is contiguous; Hkv divides H), log_decay [H]
+    fp32 <= 0, s0 [B,H,dk,dv] fp32 the state before (zero if None), lengths [B]
+    int32 (tokens behind them are not read, outputs there are zero), scale
+    dk**-0.5 if None.  Returns (o [B,T,H,dv] of q's type, the last state
+    [B,H,dk,dv] fp32); ``out`` gives both tensors."""
+    with _on(q.device, stream):
+        shape, rq, rk, rv = _attention_shape(q, k, v, log_decay, scale)
+        B, T, H, dk, dv = shape.B, shape.T, shape.H, shape.dk, shape.dv
+        o, s = out if out is not None else (torch.empty(B, T, H, dv, dtype=q.dtype, device=q.device),
+                                            torch.empty(B, H, dk, dv, dtype=torch.float32, device=q.device))
+        L = lib()
+        ws = _workspace(L.pararnn_linear_attention_workspace_size(shape), "pararnn_linear_attention", workspace, q.device)
+        rc = L.pararnn_linear_attention(
+            shape, rq, rk, rv, _like(log_decay, "log_decay", q, (H,), torch.float32),
+            _like(s0, "s0", q, (B, H, dk, dv), torch.float32), _like(lengths, "lengths", q, (B,), torch.int32),
+            _like(o, "out", q, (B, T, H, dv), q.dtype), _like(s, "out", q, (B, H, dk, dv), torch.float32),
+            _dev(ws, "workspace"), ws.numel(), _stream(stream))
+    _checked(rc, "pararnn_linear_attention")
+    return o, s
+
+
+def linear_attention_backward(q, k, v, log_decay, do, *, s0=None, ds=None, lengths=None, scale=None, workspace=None,
+                              stream=None) -> dict:
+    """The backward pass of ``linear_attention``: do [B,T,H,dv] = dL/do (q's
+    type, strided as q), ds [B,H,dk,dv] fp32 the gradient of the last state
+    (zero if None); the rest as given to the forward pass.  Returns dict(dq,
+    dk, dv, ds0) of q's type (ds0 fp32, None without s0)."""
+    with _on(q.device, stream):
+        shape, rq, rk, rv = _attention_shape(q, k, v, log_decay, scale)
+        B, T, H, Hkv, dk, dv = shape.B, shape.T, shape.H, shape.Hkv, shape.dk, shape.dv
+        rdo = _rows(do, "do", q, (B, T, H, dv))
+        new = lambda *s, dtype=q.dtype: torch.empty(*s, dtype=dtype, device=q.device)
+        g = dict(dq=new(B, T, H, dk), dk=new(B, T, Hkv, dk), dv=new(B, T, Hkv, dv),
+                 ds0=None if s0 is None else new(B, H, dk, dv, dtype=torch.float32))
+        L = lib()
+        ws = _workspace(L.pararnn_linear_attention_backward_workspace_size(shape), "pararnn_linear_attention_backward",
+                        workspace, q.device)
+        state = (B, H, dk, dv)
+        rc = L.pararnn_linear_attention_backward(
+            shape, rq, rk, rv, _like(log_decay, "log_decay", q, (H,), torch.float32), rdo,
+            _like(s0, "s0", q, state, torch.float32), _like(ds, "ds", q, state, torch.float32),
+            _like(lengths, "lengths", q, (B,), torch.int32), g["dq"].data_ptr(), g["dk"].data_ptr(),
+            g["dv"].data_ptr(), None if s0 is None else g["ds0"].data_ptr(), _dev(ws, "workspace"), ws.numel(),
+            _stream(stream))
+    _checked(rc, "pararnn_linear_attention_backward")
+    return g
+
+
+def linear_attention_step(q, k, v, log_decay, state, *, slots=None, scale=None, out_state=None, out=None, stream=None):
+    """One token of every sequence: S = exp(log_decay) S + k v^T, o = scale S^T q.
+
+    q [B,H,dk], k [B,Hkv,dk], v [B,Hkv,dv] as for ``linear_attention`` without
+    the time axis; state [n,H,dk,dv] fp32 holds the states, row b's at slots[b]
+    (int32 [B]; outside 0..n-1: no state, o is zero; the same slot twice: tokens
+    in row order), or at b if None (n = B).  The states after the token go to
+    ``out_state``, or replace those in ``state`` if None.  Returns o [B,H,dv]."""
+    with _on(q.device, stream):
+        if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+            raise ValueError("q, k and v must be [B, heads, width]")
+        shape, rq, rk, rv = _attention_shape(q.unsqueeze(1), k.unsqueeze(1), v.unsqueeze(1), log_decay, scale)
+        B, H, dk, dv = shape.B, shape.H, shape.dk, shape.dv
+        if state.dim() != 4 or state.shape[0] < 1:
+            raise ValueError("state must be [n, H, dk, dv]")
+        n = state.shape[0]
+        if slots is None and n != B:
+            raise ValueError(f"state has {n} rows for {B} sequences: slots says which")
+        if out is None:
+            out = torch.empty(B, H, dv, dtype=q.dtype, device=q.device)
+        pool = (n, H, dk, dv)
+        src = _like(state, "state", q, pool, torch.float32)
+        rc = lib().pararnn_linear_attention_step(
+            shape, rq, rk, rv, _like(log_decay, "log_decay", q, (H,), torch.float32), src,
+            _like(slots, "slots", q, (B,), torch.int32), n, _like(out, "out", q, (B, H, dv), q.dtype),
+            src if out_state is None else _like(out_state, "out_state", q, pool, torch.float32), _stream(stream))
+    _checked(rc, "pararnn_linear_attention_step")
+    return out
+
+
+def _norm_shape(x, groups, act, eps, y_dtype):
+    if x.dim() < 2:
+        raise ValueError("x must be [N, ..., C]")
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}")
+    N, C = x.shape[0], x.shape[-1]
+    S = 1
+    for n in x.shape[1:-1]:
+        S *= n
+    if min(N, S, C) < 1 or not 1 <= groups <= 2048 or C % groups:
+        raise ValueError(f"x must not be empty and groups (1 to 2048) must divide its channels: {tuple(x.shape)}, {groups}")
+    return NormShape(N, S, C, groups, _dtype_code(x.dtype), _dtype_code(y_dtype), ACTIVATIONS[act], float(eps))
+
+
+def group_norm(x, groups: int, weight=None, bias=None, *, gate=None, act: str = "silu", eps: float = 1e-5, lengths=None,
+               out_dtype=None, out=None, workspace=None, stream=None):
+    """Group norm, channels last: x [N, ..., C] is normalised over the rows
+    between the first and the last axis and each group's channels, for every n;
+    z = xhat * weight + bias, y = act(z), or z * act(gate) with a gate of x's
+    shape and type.  [N, C] normalises each row's groups by themselves.
+
+    x fp32 or bf16, contiguous CUDA; weight, bias [C] fp32; act "none", "silu" or
+    "gelu"; lengths [N] int32: rows behind them (in the middle axes' order) are
+    not read, do not count, and are zero in y.  Returns (y of ``out_dtype``, x's
+    if None; stats [N, groups, 2] fp32: mean and 1 / sqrt(var + eps))."""
+    with _on(x.device, stream):
+        y_dtype = out.dtype if out is not None else x.dtype if out_dtype is None else out_dtype
+        shape = _norm_shape(x, groups, act, eps, y_dtype)
+        px = _dev(x, "x")
+        y = out if out is not None else torch.empty(x.shape, dtype=y_dtype, device=x.device)
+        stats = torch.empty(shape.N, groups, 2, dtype=torch.float32, device=x.device)
+        L = lib()
+        ws = _workspace(L.pararnn_group_norm_workspace_size(shape), "pararnn_group_norm", workspace, x.device)
+        rc = L.pararnn_group_norm(
+            shape, px, _like(weight, "weight", x, (shape.C,), torch.float32),
+            _like(bias, "bias", x, (shape.C,), torch.float32), _like(gate, "gate", x, x.shape, x.dtype),
+            _like(lengths, "lengths", x, (shape.N,), torch.int32), _like(y, "out", x, x.shape, y_dtype),
+            stats.data_ptr(), _dev(ws, "workspace"), ws.numel(), _stream(stream))
+    _checked(rc, "pararnn_group_norm")
+    return y, stats
+
+
+def group_norm_backward(x, stats, dy, groups: int, weight=None, bias=None, *, gate=None, act: str = "silu",
+                        lengths=None, workspace=None, stream=None) -> dict:
+    """The backward pass of ``group_norm`` from dy [N, ..., C] = dL/dy (y's
+    type) and the forward's stats; the rest as given to the forward pass.
+    Returns dict(dx, dweight, dbias, dgate); dweight, dbias and dgate are None
+    where the forward pass had no weight, bias or gate."""
+    with _on(x.device, stream):
+        shape = _norm_shape(x, groups, act, 0.0, dy.dtype)
+        px = _dev(x, "x")
+        new = lambda t: None if t is None else torch.empty_like(t)
+        ptr = lambda t: None if t is None else t.data_ptr()
+        pw = _like(weight, "weight", x, (shape.C,), torch.float32)
+        pb = _like(bias, "bias", x, (shape.C,), torch.float32)
+        pg = _like(gate, "gate", x, x.shape, x.dtype)
+        g = dict(dx=torch.empty_like(x), dweight=new(weight), dbias=new(bias), dgate=new(gate))
+        L = lib()
+        ws = _workspace(L.pararnn_group_norm_backward_workspace_size(shape), "pararnn_group_norm_backward", workspace,
+                        x.device)
+        rc = L.pararnn_group_norm_backward(
+            shape, px, _like(stats, "stats", x, (shape.N, groups, 2), torch.float32), _like(dy, "dy", x, x.shape, dy.dtype),
+            pw, pb, pg, _like(lengths, "lengths", x, (shape.N,), torch.int32), ptr(g["dx"]), ptr(g["dweight"]),
+            ptr(g["dbias"]), ptr(g["dgate"]), _dev(ws, "workspace"), ws.numel(), _stream(stream))
+    _checked(rc, "pararnn_group_norm_backward")
+    return g

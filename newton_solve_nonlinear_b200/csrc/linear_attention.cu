@@ -1,0 +1,491 @@
+// linear_attention.cu -- linear attention with a decay for each head on CUDA cores (sm_100a): the sweep of
+// linear_attention.cuh in fp32, the join of time segments, the sum over heads that share keys and values, and
+// the single-token step.
+#include <cuda_bf16.h>
+
+#include "linear_attention.cuh"
+
+namespace pararnn {
+namespace {
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T from_f(float x);
+template <>
+__device__ __forceinline__ float from_f<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16(x); }
+
+// Four consecutive elements as fp32; VEC needs 4-element alignment.
+template <bool VEC>
+__device__ __forceinline__ float4 load4(const float *p, int n) {
+    if (VEC) return *reinterpret_cast<const float4 *>(p);
+    return make_float4(n > 0 ? p[0] : 0.f, n > 1 ? p[1] : 0.f, n > 2 ? p[2] : 0.f, n > 3 ? p[3] : 0.f);
+}
+template <bool VEC>
+__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p, int n) {
+    if (VEC) {
+        const uint2 u = *reinterpret_cast<const uint2 *>(p);
+        return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                           __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+    }
+    return make_float4(n > 0 ? to_f(p[0]) : 0.f, n > 1 ? to_f(p[1]) : 0.f, n > 2 ? to_f(p[2]) : 0.f,
+                       n > 3 ? to_f(p[3]) : 0.f);
+}
+
+// log g, kept finite: exp(n * -1e4) is 0 for every n >= 1 and 1 for n = 0, as g = 0 wants it.
+__device__ __forceinline__ float safe_log_decay(float x) { return fmaxf(x, -1e4f); }
+// g^n.  n * log g is formed in fp64 so that far positions keep their digits.
+__device__ __forceinline__ float decay_pow(float ld, long long n) {
+    return expf(static_cast<float>(static_cast<double>(ld) * static_cast<double>(n)));
+}
+
+__device__ __forceinline__ int row_count(const LaSweep &w, int b) {
+    if (w.lengths == nullptr) return w.T;
+    const int n = w.lengths[b];
+    return n < 0 ? 0 : (n > w.T ? w.T : n);
+}
+
+constexpr int kC = 32;     // rows per chunk
+constexpr int kDVT = 64;   // columns of c per CTA
+constexpr int kThr = 128;
+
+template <int DKP>
+constexpr int simt_smem_floats() {
+    return 2 * kC * (DKP + 4) + kC * (kDVT + 4) + kC * (kC + 4) + DKP * (kDVT + 4) + kC + 4;
+}
+
+__device__ __forceinline__ void fma4(float4 &acc, float x, const float4 &y) {
+    acc.x = fmaf(x, y.x, acc.x);
+    acc.y = fmaf(x, y.y, acc.y);
+    acc.z = fmaf(x, y.z, acc.z);
+    acc.w = fmaf(x, y.w, acc.w);
+}
+
+// One CTA: 64 columns of c of one head and one segment, chunk after chunk, the state in shared memory.
+// STATE_ONLY is pass 1 of a split sweep: the segment's own S_out, without a and without outputs.
+template <typename TI, typename TO, bool VEC, int DKP, bool STATE_ONLY>
+__global__ void __launch_bounds__(kThr) la_simt_kernel(const LaSweep w) {
+    constexpr int PK = DKP + 4, PV = kDVT + 4, PP = kC + 4;
+    extern __shared__ __align__(16) float sm[];
+    float *As = sm, *Bs = As + kC * PK, *Cs = Bs + kC * PK, *Ps = Cs + kC * PV, *Ss = Ps + kC * PP;
+    float *pw = Ss + DKP * PV;  // g^0 .. g^C
+
+    const int tid = threadIdx.x;
+    const int n_tile = (w.dv + kDVT - 1) / kDVT;
+    const int bh = blockIdx.x / n_tile, c0 = (blockIdx.x % n_tile) * kDVT;
+    const int b = bh / w.H, h = bh % w.H, sg = blockIdx.y;
+    const int L = row_count(w, b);
+    const long long r_lo = static_cast<long long>(sg) * w.seg;
+    const int lo = r_lo < L ? static_cast<int>(r_lo) : L;
+    const int hi = r_lo + w.seg < L ? static_cast<int>(r_lo + w.seg) : L;
+    const int ncol = min(kDVT, w.dv - c0);
+    const float ld = safe_log_decay(w.log_decay[h]);
+    for (int i = tid; i <= kC; i += kThr) pw[i] = decay_pow(ld, i);
+
+    // the state this segment starts from
+    const long long sbase = static_cast<long long>(bh) * w.dk * w.dv;
+    for (int i = tid; i < DKP * kDVT; i += kThr) {
+        const int d = i / kDVT, c = i % kDVT;
+        float x = 0.f;
+        if (!STATE_ONLY && d < w.dk && c < ncol) {
+            if (w.n_seg > 1)
+                x = w.seg_state[(static_cast<long long>(bh) * w.n_seg + sg) * w.dk * w.dv +
+                                static_cast<long long>(d) * w.dv + c0 + c];
+            else if (w.s_in != nullptr)
+                x = w.s_in[sbase + static_cast<long long>(d) * w.s_i + static_cast<long long>(c0 + c) * w.s_j];
+        }
+        Ss[d * PV + c] = x;
+    }
+
+    const TI *pa = static_cast<const TI *>(w.a.p) + b * w.a.sb + (h / w.a.group) * w.a.sh;
+    const TI *pb = static_cast<const TI *>(w.b.p) + b * w.b.sb + (h / w.b.group) * w.b.sh;
+    const TI *pc = static_cast<const TI *>(w.c.p) + b * w.c.sb + (h / w.c.group) * w.c.sh + c0;
+    TO *po = static_cast<TO *>(w.out) + (static_cast<long long>(b) * w.T * w.H + h) * w.dv + c0;
+    const long long ost = static_cast<long long>(w.H) * w.dv;
+
+    for (int r0 = lo; r0 < hi; r0 += kC) {
+        const int n = min(kC, hi - r0);
+        __syncthreads();
+        // a, b [C][DKP] and c [C][64] as fp32, zeros outside
+        for (int i = tid; i < kC * (DKP / 4); i += kThr) {
+            const int r = i / (DKP / 4), d = (i % (DKP / 4)) * 4;
+            float4 va = make_float4(0.f, 0.f, 0.f, 0.f), vb = va;
+            if (r < n && d < w.dk) {
+                const long long t = w.reverse ? L - 1 - (r0 + r) : r0 + r;
+                if (!STATE_ONLY) va = load4<VEC>(pa + t * w.a.st + d, w.dk - d);
+                vb = load4<VEC>(pb + t * w.b.st + d, w.dk - d);
+            }
+            if (!STATE_ONLY) *reinterpret_cast<float4 *>(As + r * PK + d) = va;
+            *reinterpret_cast<float4 *>(Bs + r * PK + d) = vb;
+        }
+        for (int i = tid; i < kC * (kDVT / 4); i += kThr) {
+            const int r = i / (kDVT / 4), c = (i % (kDVT / 4)) * 4;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < n && c < ncol) {
+                const long long t = w.reverse ? L - 1 - (r0 + r) : r0 + r;
+                v = load4<VEC>(pc + t * w.c.st + c, ncol - c);
+            }
+            *reinterpret_cast<float4 *>(Cs + r * PV + c) = v;
+        }
+        __syncthreads();
+        if (!STATE_ONLY) {
+            {  // P = (a b^T) weighted, 2 x 4 per thread
+                const int i0 = (tid / 8) * 2, j0 = tid % 8;
+                float acc[2][4] = {};
+                if (i0 < n) {
+#pragma unroll 4
+                    for (int d = 0; d < DKP; d += 4) {
+                        float4 x[2], y[4];
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) x[u] = *reinterpret_cast<const float4 *>(As + (i0 + u) * PK + d);
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            y[u] = *reinterpret_cast<const float4 *>(Bs + (j0 + 8 * u) * PK + d);
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                acc[u][q] += x[u].x * y[q].x + x[u].y * y[q].y + x[u].z * y[q].z + x[u].w * y[q].w;
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int i = i0 + u, j = j0 + 8 * q;
+                        Ps[i * PP + j] = i >= j ? acc[u][q] * pw[i >= j ? i - j : 0] * w.intra : 0.f;
+                    }
+            }
+            __syncthreads();
+            {  // out = P c + g^(i+e) (a S): 4 x 4 per thread
+                const int i0 = (tid / 16) * 4, j0 = (tid % 16) * 4;
+                float4 acc[4] = {};
+                if (i0 < n) {
+#pragma unroll 2
+                    for (int d = 0; d < DKP; d += 4) {
+                        float4 x[4], y[4];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            x[u] = *reinterpret_cast<const float4 *>(As + (i0 + u) * PK + d);
+                            y[u] = *reinterpret_cast<const float4 *>(Ss + (d + u) * PV + j0);
+                        }
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            fma4(acc[u], x[u].x, y[0]);
+                            fma4(acc[u], x[u].y, y[1]);
+                            fma4(acc[u], x[u].z, y[2]);
+                            fma4(acc[u], x[u].w, y[3]);
+                        }
+                    }
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const float f = pw[min(i0 + u + w.e, kC)] * w.inter;
+                        acc[u].x *= f, acc[u].y *= f, acc[u].z *= f, acc[u].w *= f;
+                    }
+                    for (int j = 0; j < i0 + 4; j += 4) {
+                        float4 x[4], y[4];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            x[u] = *reinterpret_cast<const float4 *>(Ps + (i0 + u) * PP + j);
+                            y[u] = *reinterpret_cast<const float4 *>(Cs + (j + u) * PV + j0);
+                        }
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            fma4(acc[u], x[u].x, y[0]);
+                            fma4(acc[u], x[u].y, y[1]);
+                            fma4(acc[u], x[u].z, y[2]);
+                            fma4(acc[u], x[u].w, y[3]);
+                        }
+                    }
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (i0 + u < n) {
+                            const long long t = w.reverse ? L - 1 - (r0 + i0 + u) : r0 + i0 + u;
+                            TO *o = po + t * ost + j0;
+                            const float f[4] = {acc[u].x, acc[u].y, acc[u].z, acc[u].w};
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                if (j0 + q < ncol) o[q] = from_f<TO>(f[q]);
+                        }
+                }
+            }
+            __syncthreads();
+        }
+        {  // S = g^n S + update sum_j g^(n-e-j) b_j c_j^T: DKP/16 x 8 per thread
+            constexpr int RD = DKP / 16;
+            const int d0 = (tid / 8) * RD, j0 = (tid % 8) * 4;
+            float4 acc[RD][2];
+            const float gn = pw[n];
+#pragma unroll
+            for (int u = 0; u < RD; ++u)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    acc[u][q] = *reinterpret_cast<const float4 *>(Ss + (d0 + u) * PV + j0 + 32 * q);
+                    acc[u][q].x *= gn, acc[u][q].y *= gn, acc[u][q].z *= gn, acc[u][q].w *= gn;
+                }
+            for (int j = 0; j < n; ++j) {
+                const float f = pw[n - w.e - j] * w.update;
+                float4 y[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    y[q] = *reinterpret_cast<const float4 *>(Cs + j * PV + j0 + 32 * q);
+                    y[q].x *= f, y[q].y *= f, y[q].z *= f, y[q].w *= f;
+                }
+#pragma unroll
+                for (int u = 0; u < RD; ++u) {
+                    const float x = Bs[j * PK + d0 + u];
+                    fma4(acc[u][0], x, y[0]);
+                    fma4(acc[u][1], x, y[1]);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < RD; ++u)
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    *reinterpret_cast<float4 *>(Ss + (d0 + u) * PV + j0 + 32 * q) = acc[u][q];
+        }
+    }
+    __syncthreads();
+    if (STATE_ONLY) {
+        for (int i = tid; i < w.dk * ncol; i += kThr) {
+            const int d = i / ncol, c = i % ncol;
+            w.seg_state[(static_cast<long long>(bh) * w.n_seg + sg) * w.dk * w.dv +
+                        static_cast<long long>(d) * w.dv + c0 + c] = Ss[d * PV + c];
+        }
+        return;
+    }
+    const int last = L > 0 ? (L - 1) / w.seg : 0;  // the segment that holds the last row
+    if (w.s_out != nullptr && sg == last)
+        for (int i = tid; i < w.dk * ncol; i += kThr) {
+            const int d = w.s_j == 1 ? i / ncol : i % w.dk, c = w.s_j == 1 ? i % ncol : i / w.dk;
+            w.s_out[sbase + static_cast<long long>(d) * w.s_i + static_cast<long long>(c0 + c) * w.s_j] =
+                Ss[d * PV + c];
+        }
+    // outputs behind the sequence's length are zero
+    const long long t_hi = r_lo + w.seg < w.T ? r_lo + w.seg : w.T;
+    for (long long t = (r_lo > L ? r_lo : L); t < t_hi; ++t)
+        for (int c = tid; c < ncol; c += kThr) po[t * ost + c] = from_f<TO>(0.f);
+}
+
+// Join of a split sweep, in place: seg_state[s] (segment s's own state) becomes the state segment s starts from.
+__global__ void la_join_kernel(const LaSweep w) {
+    const long long n = static_cast<long long>(w.dk) * w.dv;
+    const int per = static_cast<int>((n + blockDim.x - 1) / blockDim.x);  // CTAs per head
+    const int bh = blockIdx.x / per;
+    const long long i = static_cast<long long>(blockIdx.x % per) * blockDim.x + threadIdx.x;
+    if (i >= n) return;
+    const float ld = safe_log_decay(w.log_decay[bh % w.H]);
+    const float g = decay_pow(ld, w.seg);
+    const int L = row_count(w, bh / w.H);
+    float *p = w.seg_state + static_cast<long long>(bh) * w.n_seg * n + i;
+    float s = w.s_in == nullptr ? 0.f : w.s_in[bh * n + (i / w.dv) * w.s_i + (i % w.dv) * w.s_j];
+    for (int q = 0; q < w.n_seg; ++q) {
+        const float own = p[q * n];
+        p[q * n] = s;
+        // a segment with a next one that holds rows is full
+        if ((q + 1ll) * w.seg < L) s = fmaf(g, s, own);
+    }
+}
+
+template <typename TI, typename TO, bool VEC, int DKP>
+cudaError_t launch_simt(const LaSweep &w, cudaStream_t s) {
+    const int smem = simt_smem_floats<DKP>() * 4;
+    const dim3 grid(static_cast<unsigned>(w.B) * w.H * ((w.dv + kDVT - 1) / kDVT), w.n_seg);
+    cudaError_t e;
+    if (w.n_seg > 1) {
+        auto k1 = la_simt_kernel<TI, TO, VEC, DKP, true>;
+        if ((e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+        k1<<<grid, kThr, smem, s>>>(w);
+        la_join_kernel<<<static_cast<unsigned>(w.B) * w.H * ((w.dk * w.dv + 255) / 256), 256, 0, s>>>(w);
+    }
+    auto k = la_simt_kernel<TI, TO, VEC, DKP, false>;
+    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+    k<<<grid, kThr, smem, s>>>(w);
+    return cudaGetLastError();
+}
+
+template <typename TI, typename TO, bool VEC>
+cudaError_t pick_width(const LaSweep &w, cudaStream_t s) {
+    if (w.dk <= 32) return launch_simt<TI, TO, VEC, 32>(w, s);
+    if (w.dk <= 64) return launch_simt<TI, TO, VEC, 64>(w, s);
+    return launch_simt<TI, TO, VEC, 128>(w, s);
+}
+
+bool rows_vec4(const LaRows &x, size_t esize) {
+    return reinterpret_cast<uintptr_t>(x.p) % (4 * esize) == 0 && x.sb % 4 == 0 && x.st % 4 == 0 && x.sh % 4 == 0;
+}
+
+template <typename TI, typename TO>
+cudaError_t pick_vec(const LaSweep &w, cudaStream_t s) {
+    const bool vec = w.dk % 4 == 0 && w.dv % 4 == 0 && rows_vec4(w.a, sizeof(TI)) && rows_vec4(w.b, sizeof(TI)) &&
+                     rows_vec4(w.c, sizeof(TI));
+    return vec ? pick_width<TI, TO, true>(w, s) : pick_width<TI, TO, false>(w, s);
+}
+
+}  // namespace
+
+LaPlan la_plan(int B, int T, int H, int dk, int dv, int dtype) {
+    (void)dk;
+    (void)dtype;
+    // enough CTAs for two waves of the 148 SMs' resident CTAs, in segments of at least 256 rows
+    const long long ctas = static_cast<long long>(B) * H * ((dv + kDVT - 1) / kDVT);
+    long long want = (148 * 4 + ctas - 1) / ctas;
+    const long long most = T / 256;
+    if (want > most) want = most;
+    if (want > 512) want = 512;
+    if (want < 2) return {1, T};
+    int seg = static_cast<int>((T + want - 1) / want);
+    seg = (seg + kC - 1) / kC * kC;
+    return {(T + seg - 1) / seg, seg};
+}
+
+size_t la_seg_bytes(const LaSweep &w) {
+    return w.n_seg > 1 ? static_cast<size_t>(w.B) * w.H * w.n_seg * w.dk * w.dv * sizeof(float) : 0;
+}
+
+cudaError_t launch_la_sweep(const LaSweep &w, cudaStream_t s) {
+    if (w.dtype == PARARNN_F32) return pick_vec<float, float>(w, s);
+    return w.out_f32 ? pick_vec<__nv_bfloat16, float>(w, s) : pick_vec<__nv_bfloat16, __nv_bfloat16>(w, s);
+}
+
+// ---- sums over the heads that share a key/value head --------------------------------------------------------
+
+namespace {
+
+// out[row, u, :] = sum over the `per` heads of group u of part[row, u * per + i, :], in head order
+template <typename TO>
+__global__ void la_group_sum_kernel(const float *__restrict__ part, TO *__restrict__ out, long long rows, int Hkv,
+                                    int per, int d) {
+    const long long n = rows * Hkv * d;
+    for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
+         i += static_cast<long long>(gridDim.x) * blockDim.x) {
+        const long long ru = i / d;  // row * Hkv + u
+        const int c = static_cast<int>(i % d);
+        const float *p = part + ru * per * d + c;
+        float s = 0.f;
+        for (int q = 0; q < per; ++q) s += p[static_cast<long long>(q) * d];
+        out[i] = from_f<TO>(s);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_la_group_sum(const float *part, void *out, int dtype, long long rows, int Hkv, int per, int d,
+                                cudaStream_t s) {
+    const long long n = rows * Hkv * d;
+    const unsigned grid = static_cast<unsigned>(n / 256 + 1 < 148 * 16 ? n / 256 + 1 : 148 * 16);
+    if (dtype == PARARNN_F32)
+        la_group_sum_kernel<<<grid, 256, 0, s>>>(part, static_cast<float *>(out), rows, Hkv, per, d);
+    else
+        la_group_sum_kernel<<<grid, 256, 0, s>>>(part, static_cast<__nv_bfloat16 *>(out), rows, Hkv, per, d);
+    return cudaGetLastError();
+}
+
+// ---- one token per sequence ---------------------------------------------------------------------------------
+
+namespace {
+
+// One CTA per row and head: S = g S + k v^T, out = scale S^T q.  Thread (ty, tx) holds VW consecutive columns of
+// every NY-th row of S; the column sums meet in shared memory.  Rows of the batch that name the same slot are
+// taken in row order by the first one's CTA: tokens that follow each other.
+template <typename TI, int VW>
+__global__ void __launch_bounds__(256) la_step_kernel(const LaStep w) {
+    __shared__ float qs[128], ks[128], part[256 * VW];
+    __shared__ int next;
+    const int tid = threadIdx.x;
+    const int h = blockIdx.x % w.H;
+    int b = blockIdx.x / w.H;
+    const int NX = (w.dv + VW - 1) / VW, NY = blockDim.x / NX;
+    const int tx = tid % NX, ty = tid / NX;
+    TI *po = static_cast<TI *>(w.out);
+    const int slot = w.slots == nullptr ? b : w.slots[b];
+    if (slot < 0 || slot >= w.n_slots) {  // no state behind this row
+        for (int c = tid; c < w.dv; c += blockDim.x)
+            po[(static_cast<long long>(b) * w.H + h) * w.dv + c] = from_f<TI>(0.f);
+        return;
+    }
+    if (w.slots != nullptr) {
+        int earlier = 0;
+        for (int i = tid; i < b; i += blockDim.x) earlier |= w.slots[i] == slot;
+        if (__syncthreads_or(earlier)) return;
+    }
+    const float g = expf(safe_log_decay(w.log_decay[h]));
+    const long long base = (static_cast<long long>(slot) * w.H + h) * w.dk * w.dv;
+    const float *src = w.state + base;
+    float *dst = w.out_state + base;
+    while (true) {
+        const TI *q = static_cast<const TI *>(w.q.p) + b * w.q.sb + (h / w.q.group) * w.q.sh;
+        const TI *k = static_cast<const TI *>(w.k.p) + b * w.k.sb + (h / w.k.group) * w.k.sh;
+        const TI *v = static_cast<const TI *>(w.v.p) + b * w.v.sb + (h / w.v.group) * w.v.sh;
+        for (int d = tid; d < w.dk; d += blockDim.x) {
+            qs[d] = to_f(q[d]) * w.scale;
+            ks[d] = to_f(k[d]);
+        }
+        if (tid == 0) next = w.B;
+        __syncthreads();
+        float acc[VW] = {};
+        if (ty < NY) {
+            float vv[VW];
+#pragma unroll
+            for (int u = 0; u < VW; ++u) vv[u] = tx * VW + u < w.dv ? to_f(v[tx * VW + u]) : 0.f;
+#pragma unroll 4
+            for (int d = ty; d < w.dk; d += NY) {
+                const long long at = static_cast<long long>(d) * w.dv + tx * VW;
+                float s[VW];
+                if (VW == 4) {
+                    const float4 x = __ldcs(reinterpret_cast<const float4 *>(src + at));
+                    s[0] = x.x, s[VW > 1 ? 1 : 0] = x.y, s[VW > 2 ? 2 : 0] = x.z, s[VW > 3 ? 3 : 0] = x.w;
+                } else {
+                    s[0] = src[at];
+                }
+#pragma unroll
+                for (int u = 0; u < VW; ++u) {
+                    s[u] = fmaf(ks[d], vv[u], g * s[u]);
+                    acc[u] = fmaf(qs[d], s[u], acc[u]);
+                }
+                if (VW == 4)
+                    __stcs(reinterpret_cast<float4 *>(dst + at),
+                           make_float4(s[0], s[VW > 1 ? 1 : 0], s[VW > 2 ? 2 : 0], s[VW > 3 ? 3 : 0]));
+                else
+                    dst[at] = s[0];
+            }
+#pragma unroll
+            for (int u = 0; u < VW; ++u) part[ty * NX * VW + tx * VW + u] = acc[u];
+        }
+        if (w.slots != nullptr)
+            for (int i = b + 1 + tid; i < w.B; i += blockDim.x)
+                if (w.slots[i] == slot) {
+                    atomicMin(&next, i);
+                    break;
+                }
+        __syncthreads();
+        for (int c = tid; c < w.dv; c += blockDim.x) {
+            float s = 0.f;
+            for (int y = 0; y < NY; ++y) s += part[y * NX * VW + c];
+            po[(static_cast<long long>(b) * w.H + h) * w.dv + c] = from_f<TI>(s);
+        }
+        b = next;
+        if (b >= w.B) return;
+        src = dst;  // each thread reads back what it wrote itself
+        __syncthreads();
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_la_step(const LaStep &w, cudaStream_t s) {
+    const unsigned grid = static_cast<unsigned>(w.B) * w.H;
+    const bool vec = w.dv % 4 == 0;
+    if (w.dtype == PARARNN_F32) {
+        if (vec) la_step_kernel<float, 4><<<grid, 256, 0, s>>>(w);
+        else la_step_kernel<float, 1><<<grid, 256, 0, s>>>(w);
+    } else {
+        if (vec) la_step_kernel<__nv_bfloat16, 4><<<grid, 256, 0, s>>>(w);
+        else la_step_kernel<__nv_bfloat16, 1><<<grid, 256, 0, s>>>(w);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace pararnn

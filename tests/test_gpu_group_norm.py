@@ -1,0 +1,239 @@
+"""Group norm with an activation or a gate on the GPU against the fp64 oracle (oracle/group_norm.py).
+
+Tolerances, elementwise.  Sums are fp32 over blocks of at most 32 elements joined pairwise, one after the other per
+thread and then in trees: within 256 roundings for the sizes here, so u = 256 * 2^-24 relative for the standard
+deviation, and for the mean relative to the data's size.  xhat = (x - m) r is then within
+e = u (1 + |xhat|) + 8 * 2^-24 |m| r, z within |w| e + 2^-24 (|z| + |b|), and the activations have slopes below
+1.2 and cost at most 16 roundings.  A bf16 result is rounded once: 2^-8 |result|.  Gradients: dz = dy act' with a
+slope of act' below 1 (gelu, silu: |act''| <= 0.8), so dz is within |dy| (dz_err) and the sums over n terms within
+u of the sums over absolute values.
+"""
+import numpy as np
+import pytest
+import torch
+
+import newton_solve_nonlinear_b200 as fw
+from newton_solve_nonlinear_b200.inputs import make_workload
+from oracle import group_norm as oracle
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+U, EPS24 = 256 * 2.0 ** -24, 2.0 ** -24
+
+
+def _np(t):
+    return None if t is None else t.double().cpu().numpy()
+
+
+def _within(got, want, tol, dtype, what):
+    got = _np(got)
+    assert np.all(np.isfinite(got)), what
+    tol = tol + 1e-30 + (2.0 ** -8 * (np.abs(want) + tol) if dtype == BF16 else 0)
+    worst = float(np.max(np.abs(got - want) / tol)) if got.size else 0.0
+    assert worst <= 1.0, f"{what}: {worst:.3g} times the tolerance"
+
+
+def _make(N, S, C, dtype, seed=0, mean=0.3, std=1.5):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    n = lambda *s, dt=F32, m=0.0, sd=1.0: (torch.randn(*s, device="cuda", generator=g) * sd + m).to(dt)
+    return n(N, S, C, dt=dtype, m=mean, sd=std), n(C, m=1.0, sd=0.3), n(C, sd=0.3), n
+
+
+def _clean(x, lengths):
+    x = _np(x)
+    if x is not None and lengths is not None:
+        for i, L in enumerate(lengths):
+            x[i, max(L, 0):] = 0
+    return x
+
+
+def _errors(x, G, w, b, lengths, eps):
+    """(xhat, z, error of xhat, error of z) in [N, S, C]."""
+    N, S, C = x.shape
+    cg = C // G
+    hat, z, eh = np.zeros((N, S, C)), np.zeros((N, S, C)), np.zeros((N, S, C))
+    for n, L, h, zz, m, r in oracle._parts(x, G, w, b, lengths, eps):
+        hat[n, :L], z[n, :L] = h, zz
+        eh[n, :L] = U * (1 + np.abs(h)) + 8 * EPS24 * np.repeat(np.abs(m) * r, cg)
+    return hat, z, eh, np.abs(w) * eh + 2 * EPS24 * (np.abs(z) + np.abs(b))
+
+
+def _check(x, G, w, b, gate=None, act="silu", lengths=None, out_dtype=None, eps=1e-5, dy=None):
+    shape = x.shape
+    lt = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    y, stats = fw.group_norm(x, G, w, b, gate=gate, act=act, eps=eps, lengths=lt, out_dtype=out_dtype)
+    C = shape[-1]
+    x3 = x.reshape(shape[0], -1, C)
+    g3 = None if gate is None else gate.reshape(x3.shape)
+    xn, gn_, wn, bn = _clean(x3, lengths), _clean(g3, lengths), _np(w), _np(b)
+    want, ws = oracle.forward(xn, G, wn, bn, gn_, act, eps, lengths)
+    wn = np.ones(C) if w is None else wn
+    bn = np.zeros(C) if b is None else bn
+    hat, z, eh, ez = _errors(xn, G, wn, bn, lengths, eps)
+    tol = 1.2 * ez + 16 * EPS24 * np.abs(want)
+    if gate is not None:
+        a = oracle.act(gn_, act)
+        tol = ez * np.abs(a) + 16 * EPS24 * np.abs(z * a)
+    _within(y.reshape(x3.shape), want, tol, y.dtype, "y")
+    # the mean within u of the data's size (its local sums start from values that large), r within u relative
+    _within(stats[..., 0], ws[..., 0], U * (1 / ws[..., 1]) + 8 * EPS24 * np.abs(ws[..., 0]), F32, "mean")
+    _within(stats[..., 1], ws[..., 1], U * ws[..., 1], F32, "rstd")
+    if dy is None:
+        return y, stats
+    got = fw.group_norm_backward(x, stats, dy, G, w, b, gate=gate, act=act, lengths=lt)
+    dn = _clean(dy.reshape(x3.shape), lengths)
+    dx, dw, db, dg = oracle.backward(xn, dn, G, wn, bn, gn_, act, eps, lengths)
+    if gate is None:
+        dz, edz = dn * oracle.slope(z, act), np.abs(dn) * (0.8 * ez + 16 * EPS24)
+    else:
+        dz, edz = dn * oracle.act(gn_, act), np.abs(dn * oracle.act(gn_, act)) * 16 * EPS24
+    ab = np.abs(dz)
+    if w is not None:
+        _within(got["dweight"], dw, (ab * eh + edz * np.abs(hat) + U * ab * np.abs(hat)).sum((0, 1)), F32, "dweight")
+    if b is not None:
+        _within(got["dbias"], db, (edz + U * ab).sum((0, 1)), F32, "dbias")
+    if gate is not None:
+        _within(got["dgate"].reshape(x3.shape), dg, np.abs(dn * oracle.slope(gn_, act)) * (ez + 16 * EPS24 * np.abs(z)) +
+                16 * EPS24 * np.abs(dn * z), x.dtype, "dgate")
+    N, S, _ = x3.shape
+    cg = C // G
+    L = np.array([S if lengths is None else min(max(v, 0), S) for v in (lengths or [S] * N)], float)[:, None, None]
+    mean = lambda v: np.repeat(v.sum(1, keepdims=True).reshape(N, 1, G, cg).sum(3) / (np.maximum(L, 1) * cg), cg, 2)
+    r = np.repeat(_np(stats[..., 1])[:, None], cg, 2)
+    gmag, egz = np.abs(wn) * ab, np.abs(wn) * edz
+    tol = r * (egz + mean(egz + U * gmag) + np.abs(hat) * mean(egz * np.abs(hat) + gmag * (eh + U * np.abs(hat)))
+               + eh * mean(gmag * np.abs(hat)) + (U + 8 * EPS24) * (gmag + mean(gmag) + np.abs(hat) * mean(gmag * np.abs(hat))))
+    _within(got["dx"].reshape(x3.shape), dx, tol, x.dtype, "dx")
+    if lengths is not None:
+        for i, v in enumerate(lengths):
+            assert not y.reshape(x3.shape)[i, max(v, 0):].any() and not got["dx"].reshape(x3.shape)[i, max(v, 0):].any()
+    return y, stats
+
+
+SIZES = [
+    # N, S, G, channels per group
+    (1, 1, 1, 1), (3, 1, 2, 5), (37, 1, 16, 128), (5, 1, 3, 1000), (2, 1, 1, 1024), (3, 1, 1, 1032), (2, 1, 2, 2000),
+    (1000, 1, 4, 16), (70, 1, 64, 8), (9, 1, 7, 33), (300, 1, 2, 256), (2, 2, 1, 1), (3, 5, 2, 3), (2, 100, 4, 16),
+    (4, 1000, 32, 20), (1, 3001, 1, 8), (2, 64, 3, 100), (1, 7, 5, 600), (17, 33, 300, 1), (2, 2100, 2, 31),
+]
+
+
+@pytest.mark.parametrize("dtype,out", [(F32, F32), (F32, BF16), (BF16, BF16), (BF16, F32)])
+@pytest.mark.parametrize("N,S,G,cg", SIZES)
+def test_forward_and_backward(N, S, G, cg, dtype, out):
+    x, w, b, n = _make(N, S, G * cg, dtype)
+    if cg * S == 1:  # one element: xhat is 0 / sqrt(eps)
+        pass
+    _check(x, G, w, b, act="silu", out_dtype=out, dy=n(N, S, G * cg, dt=out))
+    _check(x, G, w, b, gate=n(N, S, G * cg, dt=dtype), act="gelu", out_dtype=out, dy=n(N, S, G * cg, dt=out))
+
+
+@pytest.mark.parametrize("act", ["none", "silu", "gelu"])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("size", [(6, 1, 4, 64), (3, 70, 4, 12)])
+def test_activations_without_weights(size, act, gated):
+    N, S, G, cg = size
+    x, w, b, n = _make(N, S, G * cg, F32)
+    gate = n(N, S, G * cg, sd=4.0) if gated else None
+    _check(x, G, None, None, gate=gate, act=act, dy=n(N, S, G * cg))
+    _check(x, G, w, None, gate=gate, act=act, dy=n(N, S, G * cg))
+    _check(x, G, None, b, gate=gate, act=act, dy=n(N, S, G * cg))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("S,lengths", [(50, [50, 0, 1, 49, 17]), (1, [1, 0, 1, 1, 0]), (900, [0, 900, 899, 513, 2])])
+def test_padded_batch(S, lengths, dtype):
+    x, w, b, n = _make(5, S, 48, dtype)
+    gate, dy = n(5, S, 48, dt=dtype), n(5, S, 48, dt=dtype)
+    for i, L in enumerate(lengths):
+        for t in (x, gate, dy):
+            t[i, L:] = float("nan") if i % 2 else float("inf")
+    _check(x, 4, w, b, act="gelu", lengths=lengths, dy=dy)
+    _check(x, 4, w, b, gate=gate, lengths=lengths, dy=dy)
+    big = torch.tensor([v if v < S else 1 << 30 for v in lengths], dtype=torch.int32, device="cuda")
+    low = torch.tensor([v if v else -7 for v in lengths], dtype=torch.int32, device="cuda")
+    want = fw.group_norm(x, 4, w, b, lengths=torch.tensor(lengths, dtype=torch.int32, device="cuda"))
+    for ln in (big, low):
+        assert all(torch.equal(p, q) for p, q in zip(want, fw.group_norm(x, 4, w, b, lengths=ln)))
+
+
+@pytest.mark.parametrize("size", [(4, 1, 4, 64), (2, 500, 4, 16)])
+def test_large_offset_and_constant_groups(size):
+    """A common offset far above the spread; groups without any spread (xhat = 0, r = 1 / sqrt(eps))."""
+    N, S, G, cg = size
+    x, w, b, n = _make(N, S, G * cg, F32, mean=1000.0, std=0.5)
+    _check(x, G, w, b, dy=n(N, S, G * cg))
+    x.fill_(7.25)
+    y, stats = fw.group_norm(x, G, w, b, act="none", eps=1e-6)
+    assert torch.equal(y, b.expand_as(y)) and bool((stats[..., 0] == 7.25).all())
+
+
+def test_middle_axes_and_rows_of_heads():
+    """[N, H, W, C] is [N, H*W, C]; behind linear attention each token's heads are groups of [B*T, H*dv]."""
+    x, w, b, n = _make(3, 40, 24, F32)
+    y, s = fw.group_norm(x, 3, w, b)
+    y4, s4 = fw.group_norm(x.view(3, 5, 8, 24), 3, w, b)
+    assert torch.equal(y4.view_as(y), y) and torch.equal(s, s4)
+
+
+def test_repeated_and_captured_calls_give_the_same_bits():
+    for shape, G in (((5000, 1, 512), 4), ((2, 3000, 64), 4)):
+        x, w, b, n = _make(*shape, BF16)
+        dy = n(*shape, dt=BF16)
+        y, stats = fw.group_norm(x, G, w, b)
+        g = fw.group_norm_backward(x, stats, dy, G, w, b)
+        xs = x.clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            y2, stats2 = fw.group_norm(xs, G, w, b)
+            g2 = fw.group_norm_backward(xs, stats2, dy, G, w, b)
+        xs.zero_()
+        graph.replay()
+        xs.copy_(x)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, y2) and torch.equal(stats, stats2)
+        assert all(torch.equal(g[m], g2[m]) for m in ("dx", "dweight", "dbias"))
+
+
+def test_two_layers_of_a_sequence_model():
+    """The operators together, as a model uses them: a GRU solve, its states normalised and activated into the next
+    layer's bf16 rows, linear attention on their projections, each token's heads normalised under a gate; and the
+    gradients back to the first layer's states.  The fp64 chain starts from the solve's states."""
+    from oracle import linear_attention as la
+    wl = make_workload("tiny", T=256)
+    h = fw.solve_workload(wl, "QUASI").h
+    B, T, D = h.shape
+    H, d = 2, 32
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rnd = lambda *s, sd=1.0: torch.randn(*s, device="cuda", generator=g) * sd
+    w1, b1, w2, b2 = 1 + rnd(D, sd=0.1), rnd(D, sd=0.1), 1 + rnd(H * d, sd=0.1), rnd(H * d, sd=0.1)
+    W = rnd(D, 4 * H * d, sd=D ** -0.5)
+    ld = torch.tensor([-0.02, -0.2], device="cuda")
+    x, st1 = fw.group_norm(h, 4, w1, b1, act="silu")
+    p = x @ W
+    q, k, v, gate = (t.unflatten(-1, (H, d)) for t in p.split(H * d, -1))
+    o, _ = fw.linear_attention(q, k, v, ld)
+    flat = lambda t: t.reshape(B * T, H * d)
+    y, st2 = fw.group_norm(flat(o), H, w2, b2, gate=flat(gate).contiguous(), act="silu")
+    dy = rnd(B * T, H * d)
+    g2 = fw.group_norm_backward(flat(o), st2, dy, H, w2, b2, gate=flat(gate).contiguous(), act="silu")
+    ga = fw.linear_attention_backward(q, k, v, ld, g2["dx"].view(B, T, H, d))
+    dp = torch.cat([ga[n].reshape(B, T, H * d) for n in ("dq", "dk", "dv")] + [g2["dgate"].view(B, T, H * d)], -1)
+    g1 = fw.group_norm_backward(h, st1, dp @ W.T, 4, w1, b1, act="silu")
+
+    n = lambda t: t.double().cpu().numpy()
+    hx, _ = oracle.forward(n(h), 4, n(w1), n(b1), None, "silu")
+    P = hx @ n(W)
+    Q, K, V, A = (P[..., i * H * d:(i + 1) * H * d].reshape(B, T, H, d) for i in range(4))
+    O, _ = la.forward(Q, K, V, n(ld), None, None, d ** -0.5)
+    f = lambda t: t.reshape(B * T, 1, H * d)
+    Y, _ = oracle.forward(f(O), H, n(w2), n(b2), f(A), "silu")
+    dO, dw2, _, dA = oracle.backward(f(O), f(n(dy)), H, n(w2), n(b2), f(A), "silu")
+    G = la.backward(Q, K, V, n(ld), dO.reshape(B, T, H, d), None, None, None, d ** -0.5)
+    dP = np.concatenate([t.reshape(B, T, H * d) for t in G[:3]] + [dA.reshape(B, T, H * d)], -1)
+    dh, dw1, _, _ = oracle.backward(n(h), dP @ n(W).T, 4, n(w1), n(b1), None, "silu")
+    # fp32 throughout: each of the six stages is within a few hundred roundings of its own scale, in the 2-norm
+    for got, want in ((y, Y[:, 0]), (g2["dweight"], dw2), (g1["dx"], dh), (g1["dweight"], dw1)):
+        assert np.linalg.norm(n(got) - want) <= 6 * U * np.linalg.norm(want)
