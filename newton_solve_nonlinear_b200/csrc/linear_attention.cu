@@ -282,12 +282,21 @@ __global__ void la_join_kernel(const LaSweep w) {
     float *p = w.seg_state + static_cast<long long>(bh) * w.n_seg * n + i;
     float s = w.s_in == nullptr ? 0.f : w.s_in[bh * n + (i / w.dv) * w.s_i + (i % w.dv) * w.s_j];
     for (int q = 0; q < w.n_seg; ++q) {
-        const float own = p[q * n];
+        const float own = q + 1 < w.n_seg ? p[q * n] : 0.f;
         p[q * n] = s;
         // a segment with a next one that holds rows is full
         if ((q + 1ll) * w.seg < L) s = fmaf(g, s, own);
     }
 }
+
+}  // namespace
+
+cudaError_t launch_la_join(const LaSweep &w, cudaStream_t s) {
+    la_join_kernel<<<static_cast<unsigned>(w.B) * w.H * ((w.dk * w.dv + 255) / 256), 256, 0, s>>>(w);
+    return cudaGetLastError();
+}
+
+namespace {
 
 template <typename TI, typename TO, bool VEC, int DKP>
 cudaError_t launch_simt(const LaSweep &w, cudaStream_t s) {
@@ -297,8 +306,8 @@ cudaError_t launch_simt(const LaSweep &w, cudaStream_t s) {
     if (w.n_seg > 1) {
         auto k1 = la_simt_kernel<TI, TO, VEC, DKP, true>;
         if ((e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
-        k1<<<grid, kThr, smem, s>>>(w);
-        la_join_kernel<<<static_cast<unsigned>(w.B) * w.H * ((w.dk * w.dv + 255) / 256), 256, 0, s>>>(w);
+        k1<<<dim3(grid.x, w.n_seg - 1), kThr, smem, s>>>(w);  // the last segment's own state is not needed
+        if ((e = launch_la_join(w, s)) != cudaSuccess) return e;
     }
     auto k = la_simt_kernel<TI, TO, VEC, DKP, false>;
     if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
@@ -326,18 +335,31 @@ cudaError_t pick_vec(const LaSweep &w, cudaStream_t s) {
 
 }  // namespace
 
-LaPlan la_plan(int B, int T, int H, int dk, int dv, int dtype) {
-    (void)dk;
-    (void)dtype;
-    // enough CTAs for two waves of the 148 SMs' resident CTAs, in segments of at least 256 rows
-    const long long ctas = static_cast<long long>(B) * H * ((dv + kDVT - 1) / kDVT);
-    long long want = (148 * 4 + ctas - 1) / ctas;
-    const long long most = T / 256;
+namespace {
+bool use_tc(int T, int dtype) { return dtype == PARARNN_BF16 && T >= 64; }
+}  // namespace
+
+LaPlan la_plan(int B, int T, int H, int, int dv, int dtype) {
+    const long long heads = static_cast<long long>(B) * H;
+    long long want, most;
+    int unit;
+    if (use_tc(T, dtype)) {
+        // one CTA per SM: as many segments as fill the 148 SMs once, of at least 4 chunks of 128 rows
+        want = 148 / heads;
+        most = T / 512;
+        unit = 128;
+    } else {
+        // enough CTAs for several waves of the SMs' resident CTAs, in segments of at least 256 rows
+        const long long ctas = heads * ((dv + kDVT - 1) / kDVT);
+        want = (148 * 4 + ctas - 1) / ctas;
+        most = T / 256;
+        unit = kC;
+    }
     if (want > most) want = most;
     if (want > 512) want = 512;
     if (want < 2) return {1, T};
     int seg = static_cast<int>((T + want - 1) / want);
-    seg = (seg + kC - 1) / kC * kC;
+    seg = (seg + unit - 1) / unit * unit;
     return {(T + seg - 1) / seg, seg};
 }
 
@@ -346,6 +368,7 @@ size_t la_seg_bytes(const LaSweep &w) {
 }
 
 cudaError_t launch_la_sweep(const LaSweep &w, cudaStream_t s) {
+    if (use_tc(w.T, w.dtype)) return launch_la_tc(w, s);
     if (w.dtype == PARARNN_F32) return pick_vec<float, float>(w, s);
     return w.out_f32 ? pick_vec<__nv_bfloat16, float>(w, s) : pick_vec<__nv_bfloat16, __nv_bfloat16>(w, s);
 }

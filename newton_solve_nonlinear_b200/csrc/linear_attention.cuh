@@ -54,6 +54,9 @@ LaPlan la_plan(int B, int T, int H, int dk, int dv, int dtype);
 
 cudaError_t launch_la_sweep(const LaSweep &w, cudaStream_t s);
 
+cudaError_t launch_la_tc(const LaSweep &w, cudaStream_t s);    // bf16 operands, tensor cores
+cudaError_t launch_la_join(const LaSweep &w, cudaStream_t s);  // segments' own states -> their start states
+
 cudaError_t launch_la_group_sum(const float *part, void *out, int dtype, long long rows, int Hkv, int per, int d,
                                 cudaStream_t s);
 
