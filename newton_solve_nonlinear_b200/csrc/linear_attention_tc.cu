@@ -11,10 +11,13 @@
 // copy, each 2^-9 relative as the output's own.  The weighted c is split into three bf16 terms (24 bits), so the
 // state's products are exact to fp32; they are summed smallest term first.
 //
-// Warps: 0-3 output rows (thread = row: weigh scores, scale, store), 4-11 state (lane quarter = columns of c,
-// two warpgroups share the width of b and the rows to be split), 12 issues the products, 13-15 copy the next
-// chunk's tiles with cp.async (zero-filled outside, 128-byte swizzle) into the other of two stages.  Every wait
-// is bounded; a wait that runs out marks this CTA's results NaN.
+// Tiles stand in shared memory in the order of the tokens.  A reversed sweep (logical row i = tile row 127 - x)
+// only mirrors the weights, so tiles come and go by TMA either way.
+//
+// Warps: 0-7 output (lane quarter = rows, two halves of the columns: weigh the scores, scale, stage for the TMA
+// store), 8-15 state (lane quarter = columns of c; two halves of the rows to be split and of b's width), 16
+// issues the products, 17 moves the tiles (two stages).  Every wait is bounded; a wait that runs out marks this
+// CTA's results NaN.
 #include <cuda_bf16.h>
 
 #include "linear_attention.cuh"
@@ -25,29 +28,43 @@ namespace {
 using namespace tc;
 
 constexpr int kC = 128;       // rows per chunk
-constexpr int kThreads = 512;
-constexpr int kLoaders = 96;
+// Five warpgroups of 96 registers a thread at launch, 61440 in all; the state's two take 128 of them each thread
+// (S is 64), the outputs' two keep 88 and the last one 48: 256 * 128 + 256 * 88 + 128 * 48 = 61440.
+constexpr int kThreads = 20 * 32;
+constexpr int kRegsState = 128, kRegsOut = 88, kRegsMove = 48;
+static_assert(256 * kRegsState + 256 * kRegsOut + 128 * kRegsMove <= kThreads * 96, "register split");
 constexpr int kPanel = kC * 128;  // bytes of a [128 rows][64 bf16] panel
 
 template <int DK, int DV>
 struct Lay {
-    static constexpr int A = 0, B = A + DK / 64 * kPanel, C = B + DK / 64 * kPanel;
-    static constexpr int STAGE = C + DV / 64 * kPanel;
-    static constexpr int SS = 2 * STAGE;                    // bf16 S: [DV rows][DK], K-major panels
-    static constexpr int TAB = SS + DK / 64 * DV * 128;     // floats: powers 256, score weights 160
-    static constexpr int BARS = TAB + (256 + 160) * 4;
-    static constexpr int BYTES = BARS + 256 + 1024;
-    // TMEM columns: scores 0-127, of which 0-63 become the weighted scores; out; three terms of c; dS in one or
-    // two 64-column halves, the first in the half of the scores that is free by then
-    static constexpr int T_P = 0, T_O = 128, T_V = 256, T_D0 = DK == 128 ? 64 : 448, T_D1 = 448;
+    static constexpr int A = 0, B = A + DK / 64 * kPanel, C = B + DK / 64 * kPanel, END = C + DV / 64 * kPanel;
+    // a is free once both of its products are done: the outputs are staged there, if it is wide enough
+    static constexpr int OUT = DV <= DK ? A : END, STAGE = DV <= DK ? END : END + DV / 64 * kPanel;
+    static constexpr int SS = 2 * STAGE;                 // bf16 S: [DV rows][DK], K-major panels
+    static constexpr int TAB = SS + DK / 64 * DV * 128;  // floats: score weights 160, row weights 2 x 128, 32
+    static constexpr int BARS = TAB + (160 + 256 + 32) * 4;
+    static constexpr int BYTES = BARS + 128 + 1024;
+    // TMEM columns: scores, whose place dS takes once they are weighted; weighted scores; out; three terms of c
+    static constexpr int T_S = 0, T_P = 128, T_O = 192, T_V = 320;
     static constexpr int STATE_WARPS = 2 * (DV / 32);
     static_assert(BYTES <= 227 * 1024, "shared memory");
 };
 
 struct Bars {
-    unsigned long long full[2], empty[2], scores, inter, p, v, ss, out, ds, out_read, ds_read, drain;
+    unsigned long long full[2], empty[2], scores, inter, p, v, ss, out, ds, out_read, ds_read, staged;
     unsigned tmem;
     int err;
+};
+static_assert(sizeof(Bars) <= 128, "barriers");
+
+// One sweep's arguments: its sizes and pointers, and the tensor maps of its tiles.
+struct TcSweep {
+    LaSweep w;
+    CUtensorMap a, b, c, out;
+    int tma_in, tma_out;  // the operands / the outputs can be moved by TMA
+};
+struct TcBatch {
+    TcSweep s[3];
 };
 
 __device__ __forceinline__ void arrive(unsigned bar) {
@@ -71,6 +88,25 @@ __device__ __forceinline__ unsigned long long nmajor_desc(unsigned addr) {
     return d;
 }
 constexpr unsigned kNMajorB = 1u << 16;  // instruction descriptor: B is N-major
+
+template <int N>
+__device__ __forceinline__ void regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ bool elect_one() {
+    unsigned r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0u;
+}
 
 __device__ __forceinline__ void mma_ss(unsigned d, unsigned long long a, unsigned long long b, unsigned idesc, bool acc) {
     asm volatile(
@@ -125,32 +161,56 @@ __device__ __forceinline__ unsigned pack(float lo, float hi) {
 __device__ __forceinline__ float lo_of(unsigned u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float hi_of(unsigned u) { return __uint_as_float(u & 0xffff0000u); }
 
-// One tile: row r of the chunk is token t0 + dir * r; rows >= n and columns >= width are zero.
+// The weighted c's 16 x (2 x 8) pieces: .16x128b holds row lane / 4 (+ 8 in odd registers), 32-bit column lane % 4 of
+// each group of four, which is the fragment that a transposed ldmatrix of [tokens][columns] delivers.
+__device__ __forceinline__ void tmem_st_frag(unsigned addr, const unsigned (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
+}
+__device__ __forceinline__ void ldmatrix4t(unsigned addr, unsigned &a, unsigned &b, unsigned &c, unsigned &d) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(unsigned dst, const CUtensorMap *map, int x, int t, int h, int b, unsigned bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<unsigned long long>(map)), "r"(x), "r"(t), "r"(h), "r"(b), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap *map, int x, int t, int h, int b, unsigned src) {
+    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
+                     reinterpret_cast<unsigned long long>(map)),
+                 "r"(x), "r"(t), "r"(h), "r"(b), "r"(src)
+                 : "memory");
+}
+
+// One tile by one warp, for operands that TMA cannot read: tile row x is token t0 + x; rows outside [x_lo, x_hi) and
+// columns >= width are zero.
 template <int PANELS>
-__device__ __forceinline__ void copy_tile(unsigned dst, const __nv_bfloat16 *src, long long st, long long t0, int dir,
-                                          int n, int width, bool vec, int lt) {
-    constexpr int CH = PANELS * 8, RP = kLoaders / CH;
-    const int c = lt % CH;
-    const int room = width - c * 8;  // elements of this 16-byte piece that exist
-    const int bytes = room >= 8 ? 16 : (room > 0 ? room * 2 : 0);
-    for (int r = lt / CH; r < kC; r += RP) {
-        const unsigned at = dst + (c >> 3) * kPanel + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-        const __nv_bfloat16 *p = src + (t0 + static_cast<long long>(dir) * r) * st + c * 8;
-        if (vec) {
-            const int sz = r < n ? bytes : 0;
-            if (sz == 0) p = src;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(p), "r"(sz) : "memory");
-        } else {
-            unsigned u[4] = {0u, 0u, 0u, 0u};
-            if (r < n) {
-                const unsigned short *q = reinterpret_cast<const unsigned short *>(p);
+__device__ __forceinline__ void copy_tile(unsigned dst, const __nv_bfloat16 *src, long long st, long long t0, int x_lo,
+                                          int x_hi, int width, int lane) {
+    constexpr int CH = PANELS * 8;
+    const int c = lane % CH, room = width - c * 8;
+#pragma unroll 2
+    for (int x = lane / CH; x < kC; x += 32 / CH) {
+        unsigned u[4] = {0u, 0u, 0u, 0u};
+        if (x >= x_lo && x < x_hi) {
+            const unsigned short *q = reinterpret_cast<const unsigned short *>(src + (t0 + x) * st + c * 8);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (i < room) u[i >> 1] |= static_cast<unsigned>(q[i]) << (16 * (i & 1));
-            }
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3])
-                         : "memory");
+            for (int i = 0; i < 8; ++i)
+                if (i < room) u[i >> 1] |= static_cast<unsigned>(q[i]) << (16 * (i & 1));
         }
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (c >> 3) * kPanel + x * 128 +
+                                                                      (((c & 7) ^ (x & 7)) << 4)),
+                     "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3])
+                     : "memory");
     }
 }
 
@@ -184,14 +244,17 @@ __device__ __forceinline__ void store32<float>(float *p, const float (&v)[32], i
 }
 
 template <typename TO, int DK, int DV, bool STATE_ONLY>
-__global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constant__ LaSweep w) {
+__global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constant__ TcBatch batch) {
     using Y = Lay<DK, DV>;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                             ~static_cast<uintptr_t>(1023));
+    const TcSweep &sweep = batch.s[blockIdx.z];
+    const LaSweep &w = sweep.w;
     const unsigned sm = smem_u32(smem);
-    float *rp = reinterpret_cast<float *>(smem + Y::TAB);  // [256]: g^(128 - x), 0 behind x = 128
-    float *sw = rp + 256 + 32;                             // [-32 .. 127]: intra g^x, 0 below x = 0
+    float *sw = reinterpret_cast<float *>(smem + Y::TAB) + 32;  // [-32 .. 127]: intra g^x, 0 below x = 0
+    float *cw = sw + 128;   // [2][128]: update g^(n - e - j) of tile row x, for a full chunk and for the last one
+    float *uw = cw + 256;   // [32]: g^(31 - y), reversed g^y
     Bars *bars = reinterpret_cast<Bars *>(smem + Y::BARS);
     volatile int *err = &bars->err;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -205,72 +268,98 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
     const int lo = r_lo < L ? static_cast<int>(r_lo) : L;
     const int hi = r_lo + w.seg < L ? static_cast<int>(r_lo + w.seg) : L;
     const int chunks = (hi - lo + kC - 1) / kC;
+    const int n_last = hi - lo - (chunks - 1) * kC;
     const int ncol = min(DV, w.dv - c0);
+    const bool rev = w.reverse != 0;
+    // exp(n * -1e4) is 0 for n >= 1 and 1 for n = 0, as g = 0 wants it
+    const float ld = fmaxf(w.log_decay[h], -1e4f);
+    auto power = [&](int n) { return expf(static_cast<float>(static_cast<double>(ld) * n)); };
+    // first token of chunk c's tile
+    auto first_token = [&](int c) { return rev ? L - kC - (lo + c * kC) : lo + c * kC; };
 
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
-            mbar_init(smem_u32(&bars->full[s]), kLoaders / 32);
+            mbar_init(smem_u32(&bars->full[s]), 1);
             mbar_init(smem_u32(&bars->empty[s]), 1);
         }
         mbar_init(smem_u32(&bars->scores), 1);
         mbar_init(smem_u32(&bars->inter), 1);
         mbar_init(smem_u32(&bars->out), 1);
         mbar_init(smem_u32(&bars->ds), 1);
-        mbar_init(smem_u32(&bars->drain), 1);
-        mbar_init(smem_u32(&bars->p), 4);
-        mbar_init(smem_u32(&bars->out_read), 4);
+        mbar_init(smem_u32(&bars->p), 8);
+        mbar_init(smem_u32(&bars->out_read), 8);
+        mbar_init(smem_u32(&bars->staged), 8);
         mbar_init(smem_u32(&bars->v), Y::STATE_WARPS);
         mbar_init(smem_u32(&bars->ss), Y::STATE_WARPS);
         mbar_init(smem_u32(&bars->ds_read), Y::STATE_WARPS);
         bars->err = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 12) {
+    if (warp == 16) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars->tmem)),
                      "r"(512));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
-    {
-        // exp(n * -1e4) is 0 for n >= 1 and 1 for n = 0, as g = 0 wants it
-        const double ld = fmaxf(w.log_decay[h], -1e4f);
-        if (tid < 256) rp[tid] = tid <= 128 ? expf(static_cast<float>(ld * (128 - tid))) : 0.f;
-        else if (tid < 256 + 160) sw[tid - 288] = tid >= 288 ? expf(static_cast<float>(ld * (tid - 288))) * w.intra : 0.f;
+    if (tid < 160) {
+        sw[tid - 32] = tid >= 32 ? power(tid - 32) * w.intra : 0.f;
+    } else if (tid < 160 + 256) {
+        const int x = (tid - 160) & 127, n = tid - 160 < 128 ? kC : n_last, j = rev ? kC - 1 - x : x;
+        cw[tid - 160] = j < n ? power(n - w.e - j) * w.update : 0.f;
+    } else if (tid < 160 + 256 + 32) {
+        const int y = tid - 416;
+        uw[y] = power(rev ? y : 31 - y);
     }
     fence_before();
     __syncthreads();
     fence_after();
     const unsigned tm = bars->tmem;
 
-    if (warp < 4) {
-        // ---- output rows: thread = row of the chunk
+    if (warp < 8) {
+        // ---- outputs: thread = tile row, half = half of the columns
+        regs_down<kRegsOut>();
         if (!STATE_ONLY) {
-            const int row = tid;
-            const unsigned tl = tm + (static_cast<unsigned>(warp * 32) << 16);
-            const float f = rp[128 - row - w.e] * w.inter;
+            const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;
+            const int i = rev ? kC - 1 - row : row;  // logical row
+            const unsigned tl = tm + (static_cast<unsigned>(quarter * 32) << 16);
+            const float f = power(i + w.e) * w.inter;
             TO *po = static_cast<TO *>(w.out) + (static_cast<long long>(b) * w.T * w.H + h) * w.dv + c0;
             const long long ost = static_cast<long long>(w.H) * w.dv;
             const bool vec = w.dv % 8 == 0;
             for (int c = 0; c < chunks; ++c) {
                 const unsigned ph = c & 1;
-                const int r = lo + c * kC + row;
+                const int n = c + 1 < chunks ? kC : n_last;
                 if (!mbar_wait(smem_u32(&bars->scores), ph, err)) break;
                 fence_after();
 #pragma unroll 1
-                for (int jb = 0; jb < 4; ++jb) {
+                for (int jb = half; jb < 4; jb += 2) {
                     unsigned u[16] = {};
-                    if (jb <= warp) {  // columns behind this warp's last row are zero
+                    if (jb == quarter) {  // the diagonal block; what is masked may hold anything
                         float v[32];
-                        tmem_ld32(tl + Y::T_P + jb * 32, v);
-                        const float *s = sw + row - jb * 32;
+                        tmem_ld32(tl + Y::T_S + jb * 32, v);
+                        const float *s = rev ? sw - lane : sw + lane;
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) u[j] = pack(v[2 * j] * s[-2 * j], v[2 * j + 1] * s[-2 * j - 1]);
+                        for (int j = 0; j < 32; j += 2) {
+                            const float s0 = rev ? s[j] : s[-j], s1 = rev ? s[j + 1] : s[-j - 1];
+                            const bool k0 = rev ? j >= lane : j <= lane, k1 = rev ? j + 1 >= lane : j + 1 <= lane;
+                            u[j / 2] = pack(k0 ? v[j] * s0 : 0.f, k1 ? v[j + 1] * s1 : 0.f);
+                        }
+                    } else if (rev ? jb > quarter : jb < quarter) {  // all of it counts
+                        float v[32];
+                        tmem_ld32(tl + Y::T_S + jb * 32, v);
+                        const float s = rev ? sw[jb * 32 - row] : sw[row - jb * 32 - 31];
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4) {
+                            const float4 y = *reinterpret_cast<const float4 *>(uw + j);
+                            u[j / 2] = pack(v[j] * (s * y.x), v[j + 1] * (s * y.y));
+                            u[j / 2 + 1] = pack(v[j + 2] * (s * y.z), v[j + 3] * (s * y.w));
+                        }
                     }
                     tmem_st16(tl + Y::T_P + jb * 16, u);
                 }
                 if (!mbar_wait(smem_u32(&bars->inter), ph, err)) break;
                 fence_after();
 #pragma unroll 1
-                for (int cb = 0; cb < DV; cb += 32) {
+                for (int cb = half * (DV / 2); cb < (half + 1) * (DV / 2); cb += 32) {
                     float v[32];
                     tmem_ld32(tl + Y::T_O + cb, v);
 #pragma unroll
@@ -283,28 +372,50 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                 if (lane == 0) arrive(smem_u32(&bars->p));
                 if (!mbar_wait(smem_u32(&bars->out), ph, err)) break;
                 fence_after();
-                const long long t = w.reverse ? L - 1 - r : r;
+                const long long t = first_token(c) + row;
+                const bool live = i < n;
+                // a tile that starts before the first token cannot be stored by TMA
+                const bool stage = sweep.tma_out && first_token(c) >= 0;
 #pragma unroll 1
-                for (int cb = 0; cb < DV; cb += 32) {
+                for (int cb = half * (DV / 2); cb < (half + 1) * (DV / 2); cb += 32) {
                     float v[32];
                     tmem_ld32(tl + Y::T_O + cb, v);
-                    if (cb == DV - 32) {
+                    if (cb == (half + 1) * (DV / 2) - 32) {
                         fence_before();
                         __syncwarp();
                         if (lane == 0) arrive(smem_u32(&bars->out_read));
                     }
-                    if (r < hi && cb < ncol) store32<TO>(po + t * ost + cb, v, ncol - cb, vec);
+                    if (sizeof(TO) == 2 && stage) {
+                        const unsigned at = sm + (c & 1) * Y::STAGE + Y::OUT + (cb >> 6) * kPanel + row * 128;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const unsigned d = at + (((((cb & 32) >> 3) + q) ^ (row & 7)) << 4);
+                            unsigned u[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                u[k] = live ? pack(v[8 * q + 2 * k], v[8 * q + 2 * k + 1]) : 0u;
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(d), "r"(u[0]), "r"(u[1]),
+                                         "r"(u[2]), "r"(u[3])
+                                         : "memory");
+                        }
+                    } else if (live && cb < ncol) {
+                        store32<TO>(po + t * ost + cb, v, ncol - cb, vec);
+                    }
                 }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) arrive(smem_u32(&bars->staged));
             }
         }
-    } else if (warp < 12) {
-        // ---- state: lane of TMEM = column of c, half = half of b's width and of the chunk's rows
-        const int quarter = warp & 3, half = (warp - 4) >> 2;
+    } else if (warp < 16) {
+        // ---- state: TMEM lane = column of c; half = half of b's width and of the chunk's rows
+        regs_up<kRegsState>();
+        const int quarter = warp & 3, half = (warp - 8) >> 2;
         if (quarter * 32 < DV) {
             constexpr int KH = DK / 2;
             const int d = quarter * 32 + lane;
             const unsigned tl = tm + (static_cast<unsigned>(quarter * 32) << 16);
-            const unsigned t_ds = tl + (DK == 128 ? (half ? Y::T_D1 : Y::T_D0) : Y::T_D1 + half * KH);
+            const unsigned t_ds = tl + Y::T_S + half * KH;
             float S[KH];
             {
                 const bool have = d < ncol && (w.n_seg > 1 ? !STATE_ONLY : w.s_in != nullptr);
@@ -335,39 +446,69 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                 if (lane == 0) arrive(smem_u32(&bars->ss));
             };
             if (!STATE_ONLY) publish();
+            // ldmatrix: lane l names row l % 8 of matrix l / 8; matrices are (8 tokens) x (8 columns of c), columns
+            // first, then tokens
+            const int m_row = half * 64 + ((lane >> 4) << 3) + (lane & 7);
+            const float g_full = power(kC), g_last = power(n_last);
             for (int c = 0; c < chunks; ++c) {
-                const int st = c & 1, n = min(kC, hi - lo - c * kC);
+                const int st = c & 1;
                 const unsigned ph = c & 1;
+                const bool last = c + 1 == chunks;
+                const int n = last ? n_last : kC;
+                const unsigned tile_b = sm + st * Y::STAGE + Y::B, tile_c = sm + st * Y::STAGE + Y::C;
                 if (!mbar_wait(smem_u32(&bars->full[st]), (c >> 1) & 1, err)) break;
-                const unsigned char *cp = smem + st * Y::STAGE + Y::C + (d >> 6) * kPanel + (d & 7) * 2;
-                const int dc = (d & 63) >> 3;
-                const float *cw = rp + 128 - n + w.e;  // g^(n - e - j); rows j >= n are zero
+                if (!rev && n < kC) {  // tokens behind the sequence's length: this warp's share of c, and of b
+                    for (int x = max(n, half * 64) + (lane >> 2); x < half * 64 + 64; x += 8) {
+                        const int ch = (quarter & 1) * 4 + (lane & 3);
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                         tile_c + (quarter >> 1) * kPanel + x * 128 + ((ch ^ (x & 7)) << 4)),
+                                     "r"(0)
+                                     : "memory");
+                    }
+                    const int me = half * (DV / 32) + quarter;
+                    for (int x = n + me; x < kC; x += Y::STATE_WARPS)
+                        if (lane < DK / 8)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                             tile_b + (lane >> 3) * kPanel + x * 128 + (((lane & 7) ^ (x & 7)) << 4)),
+                                         "r"(0)
+                                         : "memory");
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                }
+                const float *cwt = cw + (last ? 128 : 0) + half * 64 + 2 * (lane & 3);
 #pragma unroll 1
-                for (int jb = half * 64; jb < half * 64 + 64; jb += 32) {
+                for (int sub = 0; sub < 2; ++sub) {  // 16 columns of c at a time
+                    const int ch = (quarter & 1) * 4 + sub * 2 + ((lane >> 3) & 1);
                     unsigned u0[16], u1[16], u2[16];
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        const unsigned short x0 =
-                            *reinterpret_cast<const unsigned short *>(cp + (jb + j) * 128 + ((dc ^ (j & 7)) << 4));
-                        const unsigned short x1 =
-                            *reinterpret_cast<const unsigned short *>(cp + (jb + j + 1) * 128 + ((dc ^ ((j + 1) & 7)) << 4));
-                        float y0 = __uint_as_float(static_cast<unsigned>(x0) << 16) * cw[jb + j];
-                        float y1 = __uint_as_float(static_cast<unsigned>(x1) << 16) * cw[jb + j + 1];
-                        const unsigned p0 = pack(y0, y1);
-                        y0 -= lo_of(p0), y1 -= hi_of(p0);
-                        const unsigned p1 = pack(y0, y1);
-                        y0 -= lo_of(p1), y1 -= hi_of(p1);
-                        u0[j / 2] = p0, u1[j / 2] = p1, u2[j / 2] = pack(y0, y1);
+                    for (int tb = 0; tb < 4; ++tb) {
+                        const unsigned at = tile_c + (quarter >> 1) * kPanel + (m_row + tb * 16) * 128 + ((ch ^ (lane & 7)) << 4);
+                        ldmatrix4t(at, u0[4 * tb], u0[4 * tb + 1], u0[4 * tb + 2], u0[4 * tb + 3]);
                     }
-                    tmem_st16(tl + Y::T_V + jb / 2, u0);
-                    tmem_st16(tl + Y::T_V + 64 + jb / 2, u1);
-                    tmem_st16(tl + Y::T_V + 128 + jb / 2, u2);
+#pragma unroll
+                    for (int k = 0; k < 16; k += 2) {
+                        // registers k, k + 1: the same 8 tokens, columns lane / 4 and lane / 4 + 8
+                        const float2 f = *reinterpret_cast<const float2 *>(cwt + (k >> 1) * 8);
+#pragma unroll
+                        for (int q = k; q < k + 2; ++q) {
+                            float y0 = lo_of(u0[q]) * f.x, y1 = hi_of(u0[q]) * f.y;
+                            u0[q] = pack(y0, y1);
+                            y0 -= lo_of(u0[q]), y1 -= hi_of(u0[q]);
+                            u1[q] = pack(y0, y1);
+                            y0 -= lo_of(u1[q]), y1 -= hi_of(u1[q]);
+                            u2[q] = pack(y0, y1);
+                        }
+                    }
+                    const unsigned ta = tl + (static_cast<unsigned>(sub * 16) << 16) + Y::T_V + half * 32;
+                    tmem_st_frag(ta, u0);
+                    tmem_st_frag(ta + 64, u1);
+                    tmem_st_frag(ta + 128, u2);
                 }
                 tmem_st_wait();
                 fence_before();
                 __syncwarp();
                 if (lane == 0) arrive(smem_u32(&bars->v));
-                const float gn = rp[128 - n];
+                const float gn = last ? g_last : g_full;
                 if (!mbar_wait(smem_u32(&bars->ds), ph, err)) break;
                 fence_after();
 #pragma unroll
@@ -375,20 +516,20 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                     float v[32];
                     tmem_ld32(t_ds + k, v);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) S[k + i] = fmaf(gn, S[k + i], w.update * v[i]);
+                    for (int q = 0; q < 32; ++q) S[k + q] = fmaf(gn, S[k + q], v[q]);
                 }
                 fence_before();
                 __syncwarp();
                 if (lane == 0) arrive(smem_u32(&bars->ds_read));
                 if (!STATE_ONLY) publish();
             }
-            // the last state: segment's own (pass 1) or the sequence's
-            const int last = L > 0 ? (L - 1) / w.seg : 0;
+            // the last state: the segment's own (pass 1) or the sequence's
+            const int last_seg = L > 0 ? (L - 1) / w.seg : 0;
             float *p = nullptr;
             int si = w.dv;
             if (STATE_ONLY) {
                 p = w.seg_state + (static_cast<long long>(bh) * w.n_seg + sg) * w.dk * w.dv + c0 + d;
-            } else if (w.s_out != nullptr && sg == last) {
+            } else if (w.s_out != nullptr && sg == last_seg) {
                 p = w.s_out + static_cast<long long>(bh) * w.dk * w.dv + static_cast<long long>(c0 + d) * w.s_j;
                 si = w.s_i;
             }
@@ -400,100 +541,144 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                         p[static_cast<long long>(half * KH + k) * si] = bad ? __int_as_float(0x7fc00000) : S[k];
             }
         }
-    } else if (warp == 12) {
+    } else {
+    regs_down<kRegsMove>();
+    if (warp == 16) {
         // ---- the products
-        if (lane == 0) {
-            constexpr unsigned id_scores = make_idesc(1u, 128, kC), id_inter = make_idesc(1u, 128, DV);
-            constexpr unsigned id_out = make_idesc(1u, 128, DV) | kNMajorB, id_ds = make_idesc(1u, 128, 64) | kNMajorB;
-            bool ok = true;
-            for (int c = 0; c < chunks; ++c) {
-                const int st = c & 1;
-                const unsigned ph = c & 1;
-                const unsigned ta = sm + st * Y::STAGE + Y::A, tb = sm + st * Y::STAGE + Y::B, tc_ = sm + st * Y::STAGE + Y::C;
-                if (!(ok = mbar_wait(smem_u32(&bars->full[st]), (c >> 1) & 1, err))) break;
-                if (!STATE_ONLY) {
-                    if (c > 0 && !(ok = mbar_wait(smem_u32(&bars->ds_read), ph ^ 1u, err))) break;
-                    fence_after();
+        constexpr unsigned id_scores = make_idesc(1u, 128, kC), id_inter = make_idesc(1u, 128, DV);
+        constexpr unsigned id_out = make_idesc(1u, 128, DV) | kNMajorB, id_ds = make_idesc(1u, 128, DK) | kNMajorB;
+        int done = 0;  // chunks issued whole
+        for (int c = 0; c < chunks; ++c) {
+            const int st = c & 1;
+            const unsigned ph = c & 1;
+            const unsigned ta = sm + st * Y::STAGE + Y::A, tb = sm + st * Y::STAGE + Y::B, tc_ = sm + st * Y::STAGE + Y::C;
+            const bool fixed = !rev && c + 1 == chunks && n_last < kC;  // the state warps clear rows of b and c first
+            if (!mbar_wait(smem_u32(&bars->full[st]), (c >> 1) & 1, err)) break;
+            if (c > 0 && !mbar_wait(smem_u32(&bars->ds_read), ph ^ 1u, err)) break;
+            if (!STATE_ONLY) {
+                fence_after();
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < DK / 16; ++k) {
                         const unsigned off = (k >> 2) * kPanel + (k & 3) * 32;
-                        mma_ss(tm + Y::T_P, sw128_desc(ta + off), sw128_desc(tb + off), id_scores, k > 0);
+                        mma_ss(tm + Y::T_S, sw128_desc(ta + off), sw128_desc(tb + off), id_scores, k > 0);
                     }
                     commit(smem_u32(&bars->scores));
-                    if (!(ok = mbar_wait(smem_u32(&bars->ss), ph, err))) break;
-                    if (c > 0 && !(ok = mbar_wait(smem_u32(&bars->out_read), ph ^ 1u, err))) break;
-                    fence_after();
+                }
+                __syncwarp();
+                if (!mbar_wait(smem_u32(&bars->ss), ph, err)) break;
+                if (c > 0 && !mbar_wait(smem_u32(&bars->out_read), ph ^ 1u, err)) break;
+                fence_after();
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < DK / 16; ++k)
                         mma_ss(tm + Y::T_O, sw128_desc(ta + (k >> 2) * kPanel + (k & 3) * 32),
                                sw128_desc(sm + Y::SS + (k >> 2) * (DV * 128) + (k & 3) * 32), id_inter, k > 0);
                     commit(smem_u32(&bars->inter));
-                    if (!(ok = mbar_wait(smem_u32(&bars->p), ph, err))) break;
-                    fence_after();
+                }
+                __syncwarp();
+                if (fixed && !mbar_wait(smem_u32(&bars->v), ph, err)) break;
+                if (!mbar_wait(smem_u32(&bars->p), ph, err)) break;
+                fence_after();
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < kC / 16; ++k)
                         mma_ts(tm + Y::T_O, tm + Y::T_P + k * 8, nmajor_desc(tc_ + k * 2048), id_out, true);
                     commit(smem_u32(&bars->out));
                 }
-                if (!(ok = mbar_wait(smem_u32(&bars->v), ph, err))) break;
-                fence_after();
-#pragma unroll 1
+                __syncwarp();
+            }
+            if (!mbar_wait(smem_u32(&bars->v), ph, err)) break;
+            fence_after();
+            if (elect_one()) {
+#pragma unroll
                 for (int term = 2; term >= 0; --term)  // smallest first
 #pragma unroll
-                    for (int k = 0; k < kC / 16; ++k) {
-                        const unsigned a = tm + Y::T_V + term * 64 + k * 8;
-                        mma_ts(tm + Y::T_D0, a, nmajor_desc(tb + k * 2048), id_ds, term < 2 || k > 0);
-                        if (DK == 128)
-                            mma_ts(tm + Y::T_D1, a, nmajor_desc(tb + kPanel + k * 2048), id_ds, term < 2 || k > 0);
-                    }
+                    for (int k = 0; k < kC / 16; ++k)
+                        mma_ts(tm + Y::T_S, tm + Y::T_V + term * 64 + k * 8, nmajor_desc(tb + k * 2048), id_ds,
+                               term < 2 || k > 0);
                 commit(smem_u32(&bars->ds));
                 commit(smem_u32(&bars->empty[st]));
             }
-            // everything issued has finished before TMEM is given back
-            commit(smem_u32(&bars->drain));
-            mbar_drain(smem_u32(&bars->drain), 0);
+            __syncwarp();
+            done = c + 1;
         }
-        __syncwarp();
-    } else {
-        // ---- copies
-        const int lt = tid - 13 * 32;
-        const __nv_bfloat16 *pa =
-            static_cast<const __nv_bfloat16 *>(w.a.p) + b * w.a.sb + (h / w.a.group) * w.a.sh;
-        const __nv_bfloat16 *pb =
-            static_cast<const __nv_bfloat16 *>(w.b.p) + b * w.b.sb + (h / w.b.group) * w.b.sh;
-        const __nv_bfloat16 *pc =
-            static_cast<const __nv_bfloat16 *>(w.c.p) + b * w.c.sb + (h / w.c.group) * w.c.sh + c0;
-        auto vec = [](const __nv_bfloat16 *p, long long st) {
-            return reinterpret_cast<uintptr_t>(p) % 16 == 0 && st % 8 == 0;
-        };
-        const bool va = vec(pa, w.a.st), vb = vec(pb, w.b.st), vc = vec(pc, w.c.st);
-        const int dir = w.reverse ? -1 : 1;
-        for (int c = 0; c <= chunks; ++c) {
-            if (c < chunks) {
-                const int st = c & 1;
-                if (c >= 2 && !mbar_wait(smem_u32(&bars->empty[st]), ((c >> 1) & 1) ^ 1u, err)) break;
-                const int r0 = lo + c * kC, n = min(kC, hi - r0);
-                const long long t0 = w.reverse ? L - 1 - r0 : r0;
-                const unsigned base = sm + st * Y::STAGE;
-                if (!STATE_ONLY) copy_tile<DK / 64>(base + Y::A, pa, w.a.st, t0, dir, n, w.dk, va, lt);
-                copy_tile<DK / 64>(base + Y::B, pb, w.b.st, t0, dir, n, w.dk, vb, lt);
-                copy_tile<DV / 64>(base + Y::C, pc, w.c.st, t0, dir, n, ncol, vc, lt);
-                asm volatile("cp.async.commit_group;" ::: "memory");
-            }
-            if (c > 0) {  // the chunk before has arrived
-                if (c < chunks) asm volatile("cp.async.wait_group 1;" ::: "memory");
-                else asm volatile("cp.async.wait_group 0;" ::: "memory");
+        // everything issued has finished before TMEM is given back: each chunk's last commit, or, where a wait ran
+        // out in the middle of a chunk, a last one
+        if (*err) {
+            const int st = done & 1;
+            if (elect_one()) commit(smem_u32(&bars->empty[st]));
+            __syncwarp();
+            mbar_drain(smem_u32(&bars->empty[st]), (done >> 1) & 1);
+        } else if (done > 0) {
+            mbar_drain(smem_u32(&bars->empty[(done - 1) & 1]), ((done - 1) >> 1) & 1);
+        }
+    } else if (warp == 17) {
+        // ---- tiles in, staged outputs out
+        const __nv_bfloat16 *pa = static_cast<const __nv_bfloat16 *>(w.a.p) + b * w.a.sb + (h / w.a.group) * w.a.sh;
+        const __nv_bfloat16 *pb = static_cast<const __nv_bfloat16 *>(w.b.p) + b * w.b.sb + (h / w.b.group) * w.b.sh;
+        const __nv_bfloat16 *pc = static_cast<const __nv_bfloat16 *>(w.c.p) + b * w.c.sb + (h / w.c.group) * w.c.sh + c0;
+        auto load = [&](int c) {
+            const int st = c & 1, t0 = first_token(c), n = c + 1 < chunks ? kC : n_last;
+            const unsigned base = sm + st * Y::STAGE, full = smem_u32(&bars->full[st]);
+            if (sweep.tma_in) {
+                if (elect_one()) {
+                    mbar_expect_tx(full, ((STATE_ONLY ? 1 : 2) * (DK / 64) + DV / 64) * kPanel);
+#pragma unroll
+                    for (int x = 0; x < DV / 64; ++x)
+                        tma_load_4d(base + Y::C + x * kPanel, &sweep.c, c0 + x * 64, t0, h / w.c.group, b, full);
+#pragma unroll
+                    for (int x = 0; x < DK / 64; ++x) {
+                        tma_load_4d(base + Y::B + x * kPanel, &sweep.b, x * 64, t0, h / w.b.group, b, full);
+                        if (!STATE_ONLY)
+                            tma_load_4d(base + Y::A + x * kPanel, &sweep.a, x * 64, t0, h / w.a.group, b, full);
+                    }
+                }
+            } else {
+                const int x_lo = rev ? kC - n : 0, x_hi = rev ? kC : n;
+                copy_tile<DV / 64>(base + Y::C, pc, w.c.st, t0, x_lo, x_hi, ncol, lane);
+                copy_tile<DK / 64>(base + Y::B, pb, w.b.st, t0, x_lo, x_hi, w.dk, lane);
+                if (!STATE_ONLY) copy_tile<DK / 64>(base + Y::A, pa, w.a.st, t0, x_lo, x_hi, w.dk, lane);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) arrive(smem_u32(&bars->full[(c - 1) & 1]));
+                if (lane == 0) arrive(full);
+            }
+            __syncwarp();
+        };
+        int loaded = 0;
+        for (; loaded < min(chunks, 2); ++loaded) load(loaded);
+        for (int c = 0; c < chunks; ++c) {
+            if (!STATE_ONLY) {
+                if (!mbar_wait(smem_u32(&bars->staged), c & 1, err)) break;
+                if (sweep.tma_out && first_token(c) >= 0) {
+                    if (elect_one()) {
+#pragma unroll
+                        for (int x = 0; x < DV / 64; ++x)
+                            if (x * 64 < ncol)
+                                tma_store_4d(&sweep.out, c0 + x * 64, first_token(c), h, b,
+                                             sm + (c & 1) * Y::STAGE + Y::OUT + x * kPanel);
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                        // the store has read its tile before the stage is filled again
+                        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    }
+                    __syncwarp();
+                }
+            }
+            if (c + 2 < chunks) {
+                if (!mbar_wait(smem_u32(&bars->empty[c & 1]), (c >> 1) & 1, err)) break;
+                load(loaded++);
             }
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (*err && sweep.tma_in) {  // copies in flight land before the block ends
+            for (int c = max(loaded - 2, 0); c < loaded; ++c) mbar_drain(smem_u32(&bars->full[c & 1]), (c >> 1) & 1);
+        }
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    }
     }
 
     fence_before();
     __syncthreads();
-    if (warp == 12) {
+    if (warp == 16) {
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512));
     }
@@ -502,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         const long long ost = static_cast<long long>(w.H) * w.dv;
         if (*err)  // a wait ran out: nothing of this segment is to be trusted
             for (long long i = tid; i < static_cast<long long>(hi - lo) * ncol; i += kThreads) {
-                const long long r = lo + i / ncol, t = w.reverse ? L - 1 - r : r;
+                const long long r = lo + i / ncol, t = rev ? L - 1 - r : r;
                 po[t * ost + i % ncol] = static_cast<TO>(__int_as_float(0x7fc00000));
             }
         // outputs behind the sequence's length are zero
@@ -512,38 +697,75 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
     }
 }
 
+// A [B, T, heads, width] operand in boxes of 128 tokens x 64 columns; false where TMA cannot read it (base or a
+// stride off 16 bytes, an axis of stride 0).
+bool make_rows_map(CUtensorMap *m, const void *p, int B, int T, int heads, int width, long long sb, long long st,
+                   long long sh) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn || reinterpret_cast<uintptr_t>(p) % 16 != 0) return false;
+    const long long n[3] = {T, heads, B};
+    const long long s[3] = {st, sh, sb};
+    cuuint64_t dims[4] = {static_cast<cuuint64_t>(width), 0, 0, 0}, strides[3];
+    for (int i = 0; i < 3; ++i) {
+        dims[i + 1] = static_cast<cuuint64_t>(n[i]);
+        if (n[i] > 1 && (s[i] == 0 || s[i] % 8 != 0 || s[i] >= (1ll << 38))) return false;
+        strides[i] = n[i] > 1 ? static_cast<cuuint64_t>(s[i]) * 2 : 256;  // an axis of one entry is never stepped
+    }
+    const cuuint32_t box[4] = {64, kC, 1, 1}, one[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(p), dims, strides, box, one,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+TcSweep with_maps(const LaSweep &w) {
+    TcSweep t{};
+    t.w = w;
+    auto in = [&](CUtensorMap *m, const LaRows &r, int width) {
+        return make_rows_map(m, r.p, w.B, w.T, w.H / r.group, width, r.sb, r.st, r.sh);
+    };
+    t.tma_in = in(&t.a, w.a, w.dk) && in(&t.b, w.b, w.dk) && in(&t.c, w.c, w.dv);
+    const long long row = static_cast<long long>(w.H) * w.dv;
+    t.tma_out = !w.out_f32 && w.dv % 8 == 0 && make_rows_map(&t.out, w.out, w.B, w.T, w.H, w.dv, w.T * row, row, w.dv);
+    return t;
+}
+
 template <typename TO, int DK, int DV, bool STATE_ONLY>
-cudaError_t launch(const LaSweep &w, cudaStream_t s) {
+cudaError_t launch(const TcBatch &t, int n, cudaStream_t s) {
     auto k = la_tc_kernel<TO, DK, DV, STATE_ONLY>;
     constexpr int smem = Lay<DK, DV>::BYTES > 120 * 1024 ? Lay<DK, DV>::BYTES : 120 * 1024;  // one CTA per SM (TMEM)
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
+    const LaSweep &w = t.s[0].w;
     // the last segment's own state is not needed
-    const dim3 grid(static_cast<unsigned>(w.B) * w.H * ((w.dv + DV - 1) / DV), STATE_ONLY ? w.n_seg - 1 : w.n_seg);
-    k<<<grid, kThreads, smem, s>>>(w);
+    const dim3 grid(static_cast<unsigned>(w.B) * w.H * ((w.dv + DV - 1) / DV), STATE_ONLY ? w.n_seg - 1 : w.n_seg, n);
+    k<<<grid, kThreads, smem, s>>>(t);
     return cudaGetLastError();
 }
 
 template <typename TO, int DK, int DV>
-cudaError_t sweep(const LaSweep &w, cudaStream_t s) {
+cudaError_t sweep(const TcBatch &t, int n, cudaStream_t s) {
     cudaError_t e;
-    if (w.n_seg > 1) {
-        if ((e = launch<TO, DK, DV, true>(w, s)) != cudaSuccess) return e;
-        if ((e = launch_la_join(w, s)) != cudaSuccess) return e;
+    if (t.s[0].w.n_seg > 1) {
+        if ((e = launch<TO, DK, DV, true>(t, n, s)) != cudaSuccess) return e;
+        for (int i = 0; i < n; ++i)
+            if ((e = launch_la_join(t.s[i].w, s)) != cudaSuccess) return e;
     }
-    return launch<TO, DK, DV, false>(w, s);
+    return launch<TO, DK, DV, false>(t, n, s);
 }
 
 template <typename TO>
-cudaError_t by_width(const LaSweep &w, cudaStream_t s) {
-    if (w.dk <= 64) return w.dv <= 64 ? sweep<TO, 64, 64>(w, s) : sweep<TO, 64, 128>(w, s);
-    return w.dv <= 64 ? sweep<TO, 128, 64>(w, s) : sweep<TO, 128, 128>(w, s);
+cudaError_t by_width(const TcBatch &t, int n, cudaStream_t s) {
+    const LaSweep &w = t.s[0].w;
+    if (w.dk <= 64) return w.dv <= 64 ? sweep<TO, 64, 64>(t, n, s) : sweep<TO, 64, 128>(t, n, s);
+    return w.dv <= 64 ? sweep<TO, 128, 64>(t, n, s) : sweep<TO, 128, 128>(t, n, s);
 }
 
 }  // namespace
 
 cudaError_t launch_la_tc(const LaSweep &w, cudaStream_t s) {
-    return w.out_f32 ? by_width<float>(w, s) : by_width<__nv_bfloat16>(w, s);
+    TcBatch t{};
+    t.s[0] = with_maps(w);
+    return w.out_f32 ? by_width<float>(t, 1, s) : by_width<__nv_bfloat16>(t, 1, s);
 }
 
 }  // namespace pararnn
