@@ -59,10 +59,9 @@ size_t state_bytes(const pararnn_attention_shape &s) { return static_cast<size_t
 size_t seg_bytes(const pararnn_attention_shape &s, const LaPlan &p) {
     return p.n_seg > 1 ? align256(state_bytes(s) * p.n_seg) : 0;
 }
-// fp32 partial gradients per head where keys and values are shared: the larger of dk's and dv's
-size_t part_bytes(const pararnn_attention_shape &s) {
-    return s.H == s.Hkv ? 0
-                        : align256(static_cast<size_t>(s.B) * s.T * s.H * (s.dk > s.dv ? s.dk : s.dv) * sizeof(float));
+// fp32 partial gradients [B, T, H, width] of each head where keys and values are shared
+size_t part_bytes(const pararnn_attention_shape &s, int width) {
+    return s.H == s.Hkv ? 0 : align256(static_cast<size_t>(s.B) * s.T * s.H * width * sizeof(float));
 }
 
 LaSweep sweep_of(const pararnn_attention_shape &s, const float *log_decay, const int *lengths, int dk, int dv) {
@@ -115,16 +114,16 @@ int pararnn_linear_attention(const pararnn_attention_shape *shape, const pararnn
     w.e = 1;
     w.intra = w.inter = s.scale, w.update = 1.f;
     set_plan(w, la_plan(s.B, s.T, s.H, s.dk, s.dv, s.dtype), workspace);
-    return launch_la_sweep(w, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PARARNN_OK : PARARNN_CUDA_ERROR;
+    return launch_la_sweeps(&w, 1, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PARARNN_OK : PARARNN_CUDA_ERROR;
 }
 
 size_t pararnn_linear_attention_backward_workspace_size(const pararnn_attention_shape *shape) {
     if (!shape_ok(shape)) return 0;
     const pararnn_attention_shape &s = *shape;
-    // the sweeps for dq and dk swap the roles of the widths
-    const size_t a = seg_bytes(s, la_plan(s.B, s.T, s.H, s.dk, s.dv, s.dtype));
-    const size_t b = seg_bytes(s, la_plan(s.B, s.T, s.H, s.dv, s.dk, s.dtype));
-    const size_t n = (a > b ? a : b) + part_bytes(s);
+    // three sweeps that may run at once; those for dq and dk swap the roles of the widths
+    const size_t n = seg_bytes(s, la_plan(s.B, s.T, s.H, s.dk, s.dv, s.dtype)) +
+                     2 * seg_bytes(s, la_plan(s.B, s.T, s.H, s.dv, s.dk, s.dtype)) + part_bytes(s, s.dk) +
+                     part_bytes(s, s.dv);
     return n ? n : 256;
 }
 
@@ -154,47 +153,51 @@ int pararnn_linear_attention_backward(const pararnn_attention_shape *shape, cons
     if (!disjoint(out, 5, in, 8)) return PARARNN_INVALID_ARG;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const int per = s.H / s.Hkv;
-    float *part = static_cast<float *>(workspace);
-    char *seg_state = static_cast<char *>(workspace) + part_bytes(s);
-    const LaPlan plan_v = la_plan(s.B, s.T, s.H, s.dk, s.dv, s.dtype);  // sweeps whose state is [dk, dv]
-    const LaPlan plan_k = la_plan(s.B, s.T, s.H, s.dv, s.dk, s.dtype);  // sweeps whose state is [dv, dk]
+    const LaPlan plan_v = la_plan(s.B, s.T, s.H, s.dk, s.dv, s.dtype);  // the sweep whose state is [dk, dv]
+    const LaPlan plan_k = la_plan(s.B, s.T, s.H, s.dv, s.dk, s.dtype);  // the sweeps whose state is [dv, dk]
+    char *at = static_cast<char *>(workspace);
+    auto take = [&](size_t n) {
+        char *p = at;
+        at += n;
+        return p;
+    };
+    float *part_k = reinterpret_cast<float *>(take(part_bytes(s, s.dk)));
+    float *part_v = reinterpret_cast<float *>(take(part_bytes(s, s.dv)));
+    LaSweep w[3];
 
     // dq: the forward sweep on (do, v, k) from S_0^T
-    LaSweep w = sweep_of(s, log_decay, lengths, s.dv, s.dk);
-    w.a = operand(*d_o, 1), w.b = operand(*v, per), w.c = operand(*k, per);
-    w.s_in = s0, w.s_i = 1, w.s_j = s.dv;
-    w.out = dq;
-    w.e = 1;
-    w.intra = w.inter = s.scale, w.update = 1.f;
-    set_plan(w, plan_k, seg_state);
-    if (launch_la_sweep(w, st) != cudaSuccess) return PARARNN_CUDA_ERROR;
+    w[0] = sweep_of(s, log_decay, lengths, s.dv, s.dk);
+    w[0].a = operand(*d_o, 1), w[0].b = operand(*v, per), w[0].c = operand(*k, per);
+    w[0].s_in = s0, w[0].s_i = 1, w[0].s_j = s.dv;
+    w[0].out = dq;
+    w[0].e = 1;
+    w[0].intra = w[0].inter = s.scale, w[0].update = 1.f;
+    set_plan(w[0], plan_k, take(seg_bytes(s, plan_k)));
 
     // dk: the reversed sweep on (v, do, q) from dS^T
-    w = sweep_of(s, log_decay, lengths, s.dv, s.dk);
-    w.a = operand(*v, per), w.b = operand(*d_o, 1), w.c = operand(*q, 1);
-    w.s_in = ds, w.s_i = 1, w.s_j = s.dv;
-    w.out = per == 1 ? dk : part;
-    w.out_f32 = per != 1;
-    w.reverse = 1;
-    w.intra = w.update = s.scale, w.inter = 1.f;
-    set_plan(w, plan_k, seg_state);
-    if (launch_la_sweep(w, st) != cudaSuccess) return PARARNN_CUDA_ERROR;
-    if (per != 1 &&
-        launch_la_group_sum(part, dk, s.dtype, static_cast<long long>(rows), s.Hkv, per, s.dk, st) != cudaSuccess)
-        return PARARNN_CUDA_ERROR;
+    w[1] = sweep_of(s, log_decay, lengths, s.dv, s.dk);
+    w[1].a = operand(*v, per), w[1].b = operand(*d_o, 1), w[1].c = operand(*q, 1);
+    w[1].s_in = ds, w[1].s_i = 1, w[1].s_j = s.dv;
+    w[1].out = per == 1 ? dk : part_k;
+    w[1].out_f32 = per != 1;
+    w[1].reverse = 1;
+    w[1].intra = w[1].update = s.scale, w[1].inter = 1.f;
+    set_plan(w[1], plan_k, take(seg_bytes(s, plan_k)));
 
     // dv: the reversed sweep on (k, q, do) from dS; its last state is dL/dS_0
-    w = sweep_of(s, log_decay, lengths, s.dk, s.dv);
-    w.a = operand(*k, per), w.b = operand(*q, 1), w.c = operand(*d_o, 1);
-    w.s_in = ds, w.s_out = ds0, w.s_i = s.dv, w.s_j = 1;
-    w.out = per == 1 ? dv : part;
-    w.out_f32 = per != 1;
-    w.reverse = 1;
-    w.intra = w.update = s.scale, w.inter = 1.f;
-    set_plan(w, plan_v, seg_state);
-    if (launch_la_sweep(w, st) != cudaSuccess) return PARARNN_CUDA_ERROR;
-    if (per != 1 &&
-        launch_la_group_sum(part, dv, s.dtype, static_cast<long long>(rows), s.Hkv, per, s.dv, st) != cudaSuccess)
+    w[2] = sweep_of(s, log_decay, lengths, s.dk, s.dv);
+    w[2].a = operand(*k, per), w[2].b = operand(*q, 1), w[2].c = operand(*d_o, 1);
+    w[2].s_in = ds, w[2].s_out = ds0, w[2].s_i = s.dv, w[2].s_j = 1;
+    w[2].out = per == 1 ? dv : part_v;
+    w[2].out_f32 = per != 1;
+    w[2].reverse = 1;
+    w[2].intra = w[2].update = s.scale, w[2].inter = 1.f;
+    set_plan(w[2], plan_v, take(seg_bytes(s, plan_v)));
+
+    if (launch_la_sweeps(w, 3, st) != cudaSuccess) return PARARNN_CUDA_ERROR;
+    const long long n = static_cast<long long>(rows);
+    if (per != 1 && (launch_la_group_sum(part_k, dk, s.dtype, n, s.Hkv, per, s.dk, st) != cudaSuccess ||
+                     launch_la_group_sum(part_v, dv, s.dtype, n, s.Hkv, per, s.dv, st) != cudaSuccess))
         return PARARNN_CUDA_ERROR;
     return PARARNN_OK;
 }

@@ -367,10 +367,22 @@ size_t la_seg_bytes(const LaSweep &w) {
     return w.n_seg > 1 ? static_cast<size_t>(w.B) * w.H * w.n_seg * w.dk * w.dv * sizeof(float) : 0;
 }
 
-cudaError_t launch_la_sweep(const LaSweep &w, cudaStream_t s) {
-    if (use_tc(w.T, w.dtype)) return launch_la_tc(w, s);
-    if (w.dtype == PARARNN_F32) return pick_vec<float, float>(w, s);
-    return w.out_f32 ? pick_vec<__nv_bfloat16, float>(w, s) : pick_vec<__nv_bfloat16, __nv_bfloat16>(w, s);
+cudaError_t launch_la_sweeps(const LaSweep *w, int n, cudaStream_t s) {
+    for (int i = 0; i < n;) {
+        cudaError_t e;
+        int k = 1;
+        if (use_tc(w[i].T, w[i].dtype)) {
+            while (i + k < n && la_tc_together(w[i], w[i + k])) ++k;
+            e = launch_la_tc(w + i, k, s);
+        } else if (w[i].dtype == PARARNN_F32) {
+            e = pick_vec<float, float>(w[i], s);
+        } else {
+            e = w[i].out_f32 ? pick_vec<__nv_bfloat16, float>(w[i], s) : pick_vec<__nv_bfloat16, __nv_bfloat16>(w[i], s);
+        }
+        if (e != cudaSuccess) return e;
+        i += k;
+    }
+    return cudaSuccess;
 }
 
 // ---- sums over the heads that share a key/value head --------------------------------------------------------

@@ -52,9 +52,12 @@ struct LaPlan {
 size_t la_seg_bytes(const LaSweep &w);
 LaPlan la_plan(int B, int T, int H, int dk, int dv, int dtype);
 
-cudaError_t launch_la_sweep(const LaSweep &w, cudaStream_t s);
+// n <= 3 independent sweeps; those that can share a launch do.
+cudaError_t launch_la_sweeps(const LaSweep *w, int n, cudaStream_t s);
 
-cudaError_t launch_la_tc(const LaSweep &w, cudaStream_t s);    // bf16 operands, tensor cores
+// bf16 operands on tensor cores: n <= 3 sweeps in one launch, every one of which goes together with the first
+cudaError_t launch_la_tc(const LaSweep *w, int n, cudaStream_t s);
+bool la_tc_together(const LaSweep &x, const LaSweep &y);
 cudaError_t launch_la_join(const LaSweep &w, cudaStream_t s);  // segments' own states -> their start states
 
 cudaError_t launch_la_group_sum(const float *part, void *out, int dtype, long long rows, int Hkv, int per, int d,

@@ -43,7 +43,7 @@ struct Lay {
     static constexpr int SS = 2 * STAGE;                 // bf16 S: [DV rows][DK], K-major panels
     static constexpr int TAB = SS + DK / 64 * DV * 128;  // floats: score weights 160, row weights 2 x 128, 32
     static constexpr int BARS = TAB + (160 + 256 + 32) * 4;
-    static constexpr int BYTES = BARS + 128 + 1024;
+    static constexpr int BYTES = BARS + 160 + 1024;
     // TMEM columns: scores, whose place dS takes once they are weighted; weighted scores; out; three terms of c
     static constexpr int T_S = 0, T_P = 128, T_O = 192, T_V = 320;
     static constexpr int STATE_WARPS = 2 * (DV / 32);
@@ -51,11 +51,15 @@ struct Lay {
 };
 
 struct Bars {
-    unsigned long long full[2], empty[2], scores, inter, p, v, ss, out, ds, out_read, ds_read, staged;
+    unsigned long long full[2], empty[2], staged[2], scores, inter, p, scaled, v, ss, out, ds, out_read, ds_read;
     unsigned tmem;
     int err;
 };
-static_assert(sizeof(Bars) <= 128, "barriers");
+static_assert(sizeof(Bars) <= 160, "barriers");
+
+// A barrier's next phase completes only after everyone who waits for this one has seen it (the parity would be
+// ambiguous otherwise): the chain scores -> p -> ds -> ds_read -> scores of the next chunk orders all but the
+// mover, whose barriers are one per stage, and a stage is filled again only by the mover itself.
 
 // One sweep's arguments: its sizes and pointers, and the tensor maps of its tiles.
 struct TcSweep {
@@ -70,8 +74,12 @@ struct TcBatch {
 __device__ __forceinline__ void arrive(unsigned bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void commit(unsigned bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar));
+__device__ __forceinline__ void commit(unsigned bar, unsigned on) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(on));
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -108,19 +116,24 @@ __device__ __forceinline__ bool elect_one() {
     return r != 0u;
 }
 
-__device__ __forceinline__ void mma_ss(unsigned d, unsigned long long a, unsigned long long b, unsigned idesc, bool acc) {
+// The warp runs these together and one lane (`on`) issues: without a branch the operands stay in uniform registers.
+__device__ __forceinline__ void mma_ss(unsigned d, unsigned long long a, unsigned long long b, unsigned idesc, bool acc,
+                                       unsigned on) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u));
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u), "r"(on));
 }
-__device__ __forceinline__ void mma_ts(unsigned d, unsigned a, unsigned long long b, unsigned idesc, bool acc) {
+__device__ __forceinline__ void mma_ts(unsigned d, unsigned a, unsigned long long b, unsigned idesc, bool acc,
+                                       unsigned on) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u));
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u), "r"(on));
 }
 
 __device__ __forceinline__ void tmem_ld32(unsigned addr, float (&v)[32]) {
@@ -214,10 +227,8 @@ __device__ __forceinline__ void copy_tile(unsigned dst, const __nv_bfloat16 *src
     }
 }
 
-template <typename TO>
-__device__ __forceinline__ void store32(TO *p, const float (&v)[32], int room, bool vec);
-template <>
-__device__ __forceinline__ void store32<__nv_bfloat16>(__nv_bfloat16 *p, const float (&v)[32], int room, bool vec) {
+// 32 columns of one output row, `room` of which exist.
+__device__ __forceinline__ void store32(__nv_bfloat16 *p, const float (&v)[32], int room, bool vec) {
     if (vec && room >= 32) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -230,8 +241,7 @@ __device__ __forceinline__ void store32<__nv_bfloat16>(__nv_bfloat16 *p, const f
             if (i < room) p[i] = __float2bfloat16(v[i]);
     }
 }
-template <>
-__device__ __forceinline__ void store32<float>(float *p, const float (&v)[32], int room, bool vec) {
+__device__ __forceinline__ void store32(float *p, const float (&v)[32], int room, bool vec) {
     if (vec && room >= 32) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -243,7 +253,7 @@ __device__ __forceinline__ void store32<float>(float *p, const float (&v)[32], i
     }
 }
 
-template <typename TO, int DK, int DV, bool STATE_ONLY>
+template <int DK, int DV, bool STATE_ONLY>
 __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constant__ TcBatch batch) {
     using Y = Lay<DK, DV>;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -279,16 +289,17 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
 
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
-            mbar_init(smem_u32(&bars->full[s]), 1);
+            mbar_init(smem_u32(&bars->full[s]), STATE_ONLY ? 1 : 2);
             mbar_init(smem_u32(&bars->empty[s]), 1);
+            mbar_init(smem_u32(&bars->staged[s]), 8);
         }
         mbar_init(smem_u32(&bars->scores), 1);
         mbar_init(smem_u32(&bars->inter), 1);
         mbar_init(smem_u32(&bars->out), 1);
         mbar_init(smem_u32(&bars->ds), 1);
         mbar_init(smem_u32(&bars->p), 8);
+        mbar_init(smem_u32(&bars->scaled), 8);
         mbar_init(smem_u32(&bars->out_read), 8);
-        mbar_init(smem_u32(&bars->staged), 8);
         mbar_init(smem_u32(&bars->v), Y::STATE_WARPS);
         mbar_init(smem_u32(&bars->ss), Y::STATE_WARPS);
         mbar_init(smem_u32(&bars->ds_read), Y::STATE_WARPS);
@@ -322,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             const int i = rev ? kC - 1 - row : row;  // logical row
             const unsigned tl = tm + (static_cast<unsigned>(quarter * 32) << 16);
             const float f = power(i + w.e) * w.inter;
-            TO *po = static_cast<TO *>(w.out) + (static_cast<long long>(b) * w.T * w.H + h) * w.dv + c0;
+            const long long po = (static_cast<long long>(b) * w.T * w.H + h) * w.dv + c0;
             const long long ost = static_cast<long long>(w.H) * w.dv;
             const bool vec = w.dv % 8 == 0;
             for (int c = 0; c < chunks; ++c) {
@@ -356,6 +367,10 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                     }
                     tmem_st16(tl + Y::T_P + jb * 16, u);
                 }
+                tmem_st_wait();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) arrive(smem_u32(&bars->p));
                 if (!mbar_wait(smem_u32(&bars->inter), ph, err)) break;
                 fence_after();
 #pragma unroll 1
@@ -369,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                 tmem_st_wait();
                 fence_before();
                 __syncwarp();
-                if (lane == 0) arrive(smem_u32(&bars->p));
+                if (lane == 0) arrive(smem_u32(&bars->scaled));
                 if (!mbar_wait(smem_u32(&bars->out), ph, err)) break;
                 fence_after();
                 const long long t = first_token(c) + row;
@@ -385,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                         __syncwarp();
                         if (lane == 0) arrive(smem_u32(&bars->out_read));
                     }
-                    if (sizeof(TO) == 2 && stage) {
+                    if (stage) {
                         const unsigned at = sm + (c & 1) * Y::STAGE + Y::OUT + (cb >> 6) * kPanel + row * 128;
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
@@ -399,12 +414,14 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                                          : "memory");
                         }
                     } else if (live && cb < ncol) {
-                        store32<TO>(po + t * ost + cb, v, ncol - cb, vec);
+                        const long long at = po + t * ost + cb;
+                        if (w.out_f32) store32(static_cast<float *>(w.out) + at, v, ncol - cb, vec);
+                        else store32(static_cast<__nv_bfloat16 *>(w.out) + at, v, ncol - cb, vec);
                     }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) arrive(smem_u32(&bars->staged));
+                if (lane == 0) arrive(smem_u32(&bars->staged[c & 1]));
             }
         }
     } else if (warp < 16) {
@@ -547,68 +564,58 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         // ---- the products
         constexpr unsigned id_scores = make_idesc(1u, 128, kC), id_inter = make_idesc(1u, 128, DV);
         constexpr unsigned id_out = make_idesc(1u, 128, DV) | kNMajorB, id_ds = make_idesc(1u, 128, DK) | kNMajorB;
+        const unsigned on = elect_one() ? 1u : 0u;
+        const unsigned tu = __shfl_sync(0xffffffffu, tm, 0);
         int done = 0;  // chunks issued whole
         for (int c = 0; c < chunks; ++c) {
             const int st = c & 1;
             const unsigned ph = c & 1;
             const unsigned ta = sm + st * Y::STAGE + Y::A, tb = sm + st * Y::STAGE + Y::B, tc_ = sm + st * Y::STAGE + Y::C;
-            const bool fixed = !rev && c + 1 == chunks && n_last < kC;  // the state warps clear rows of b and c first
             if (!mbar_wait(smem_u32(&bars->full[st]), (c >> 1) & 1, err)) break;
             if (c > 0 && !mbar_wait(smem_u32(&bars->ds_read), ph ^ 1u, err)) break;
             if (!STATE_ONLY) {
                 fence_after();
-                if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < DK / 16; ++k) {
-                        const unsigned off = (k >> 2) * kPanel + (k & 3) * 32;
-                        mma_ss(tm + Y::T_S, sw128_desc(ta + off), sw128_desc(tb + off), id_scores, k > 0);
-                    }
-                    commit(smem_u32(&bars->scores));
+                for (int k = 0; k < DK / 16; ++k) {
+                    const unsigned off = (k >> 2) * kPanel + (k & 3) * 32;
+                    mma_ss(tu + Y::T_S, sw128_desc(ta + off), sw128_desc(tb + off), id_scores, k > 0, on);
                 }
-                __syncwarp();
+                commit(smem_u32(&bars->scores), on);
                 if (!mbar_wait(smem_u32(&bars->ss), ph, err)) break;
                 if (c > 0 && !mbar_wait(smem_u32(&bars->out_read), ph ^ 1u, err)) break;
                 fence_after();
-                if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < DK / 16; ++k)
-                        mma_ss(tm + Y::T_O, sw128_desc(ta + (k >> 2) * kPanel + (k & 3) * 32),
-                               sw128_desc(sm + Y::SS + (k >> 2) * (DV * 128) + (k & 3) * 32), id_inter, k > 0);
-                    commit(smem_u32(&bars->inter));
-                }
-                __syncwarp();
-                if (fixed && !mbar_wait(smem_u32(&bars->v), ph, err)) break;
-                if (!mbar_wait(smem_u32(&bars->p), ph, err)) break;
-                fence_after();
-                if (elect_one()) {
-#pragma unroll
-                    for (int k = 0; k < kC / 16; ++k)
-                        mma_ts(tm + Y::T_O, tm + Y::T_P + k * 8, nmajor_desc(tc_ + k * 2048), id_out, true);
-                    commit(smem_u32(&bars->out));
-                }
-                __syncwarp();
+                for (int k = 0; k < DK / 16; ++k)
+                    mma_ss(tu + Y::T_O, sw128_desc(ta + (k >> 2) * kPanel + (k & 3) * 32),
+                           sw128_desc(sm + Y::SS + (k >> 2) * (DV * 128) + (k & 3) * 32), id_inter, k > 0, on);
+                commit(smem_u32(&bars->inter), on);
+                if (!mbar_wait(smem_u32(&bars->p), ph, err)) break;  // the scores' place is free for dS
             }
             if (!mbar_wait(smem_u32(&bars->v), ph, err)) break;
             fence_after();
-            if (elect_one()) {
 #pragma unroll
-                for (int term = 2; term >= 0; --term)  // smallest first
+            for (int term = 2; term >= 0; --term)  // smallest first
 #pragma unroll
-                    for (int k = 0; k < kC / 16; ++k)
-                        mma_ts(tm + Y::T_S, tm + Y::T_V + term * 64 + k * 8, nmajor_desc(tb + k * 2048), id_ds,
-                               term < 2 || k > 0);
-                commit(smem_u32(&bars->ds));
-                commit(smem_u32(&bars->empty[st]));
+                for (int k = 0; k < kC / 16; ++k)
+                    mma_ts(tu + Y::T_S, tu + Y::T_V + term * 64 + k * 8, nmajor_desc(tb + k * 2048), id_ds,
+                           term < 2 || k > 0, on);
+            commit(smem_u32(&bars->ds), on);
+            if (!STATE_ONLY) {
+                if (!mbar_wait(smem_u32(&bars->scaled), ph, err)) break;
+                fence_after();
+#pragma unroll
+                for (int k = 0; k < kC / 16; ++k)
+                    mma_ts(tu + Y::T_O, tu + Y::T_P + k * 8, nmajor_desc(tc_ + k * 2048), id_out, true, on);
+                commit(smem_u32(&bars->out), on);
             }
-            __syncwarp();
+            commit(smem_u32(&bars->empty[st]), on);
             done = c + 1;
         }
         // everything issued has finished before TMEM is given back: each chunk's last commit, or, where a wait ran
         // out in the middle of a chunk, a last one
         if (*err) {
             const int st = done & 1;
-            if (elect_one()) commit(smem_u32(&bars->empty[st]));
-            __syncwarp();
+            commit(smem_u32(&bars->empty[st]), on);
             mbar_drain(smem_u32(&bars->empty[st]), (done >> 1) & 1);
         } else if (done > 0) {
             mbar_drain(smem_u32(&bars->empty[(done - 1) & 1]), ((done - 1) >> 1) & 1);
@@ -618,38 +625,53 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         const __nv_bfloat16 *pa = static_cast<const __nv_bfloat16 *>(w.a.p) + b * w.a.sb + (h / w.a.group) * w.a.sh;
         const __nv_bfloat16 *pb = static_cast<const __nv_bfloat16 *>(w.b.p) + b * w.b.sb + (h / w.b.group) * w.b.sh;
         const __nv_bfloat16 *pc = static_cast<const __nv_bfloat16 *>(w.c.p) + b * w.c.sb + (h / w.c.group) * w.c.sh + c0;
-        auto load = [&](int c) {
+        // first b and c, then a, whose place the staged outputs may hold longer
+        auto load = [&](int c, bool first) {
             const int st = c & 1, t0 = first_token(c), n = c + 1 < chunks ? kC : n_last;
             const unsigned base = sm + st * Y::STAGE, full = smem_u32(&bars->full[st]);
             if (sweep.tma_in) {
                 if (elect_one()) {
-                    mbar_expect_tx(full, ((STATE_ONLY ? 1 : 2) * (DK / 64) + DV / 64) * kPanel);
+                    if (first) {
+                        mbar_expect_tx(full, (DK / 64 + DV / 64) * kPanel);
 #pragma unroll
-                    for (int x = 0; x < DV / 64; ++x)
-                        tma_load_4d(base + Y::C + x * kPanel, &sweep.c, c0 + x * 64, t0, h / w.c.group, b, full);
+                        for (int x = 0; x < DV / 64; ++x)
+                            tma_load_4d(base + Y::C + x * kPanel, &sweep.c, c0 + x * 64, t0, h / w.c.group, b, full);
 #pragma unroll
-                    for (int x = 0; x < DK / 64; ++x) {
-                        tma_load_4d(base + Y::B + x * kPanel, &sweep.b, x * 64, t0, h / w.b.group, b, full);
-                        if (!STATE_ONLY)
+                        for (int x = 0; x < DK / 64; ++x)
+                            tma_load_4d(base + Y::B + x * kPanel, &sweep.b, x * 64, t0, h / w.b.group, b, full);
+                    } else {
+                        mbar_expect_tx(full, DK / 64 * kPanel);
+#pragma unroll
+                        for (int x = 0; x < DK / 64; ++x)
                             tma_load_4d(base + Y::A + x * kPanel, &sweep.a, x * 64, t0, h / w.a.group, b, full);
                     }
                 }
             } else {
                 const int x_lo = rev ? kC - n : 0, x_hi = rev ? kC : n;
-                copy_tile<DV / 64>(base + Y::C, pc, w.c.st, t0, x_lo, x_hi, ncol, lane);
-                copy_tile<DK / 64>(base + Y::B, pb, w.b.st, t0, x_lo, x_hi, w.dk, lane);
-                if (!STATE_ONLY) copy_tile<DK / 64>(base + Y::A, pa, w.a.st, t0, x_lo, x_hi, w.dk, lane);
+                if (first) {
+                    copy_tile<DV / 64>(base + Y::C, pc, w.c.st, t0, x_lo, x_hi, ncol, lane);
+                    copy_tile<DK / 64>(base + Y::B, pb, w.b.st, t0, x_lo, x_hi, w.dk, lane);
+                } else {
+                    copy_tile<DK / 64>(base + Y::A, pa, w.a.st, t0, x_lo, x_hi, w.dk, lane);
+                }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) arrive(full);
             }
             __syncwarp();
         };
-        int loaded = 0;
-        for (; loaded < min(chunks, 2); ++loaded) load(loaded);
+        int loaded = 0;  // chunks of which any tile was asked for
+        for (; loaded < min(chunks, 2); ++loaded) {
+            load(loaded, true);
+            if (!STATE_ONLY) load(loaded, false);
+        }
         for (int c = 0; c < chunks; ++c) {
+            if (c + 2 < chunks) {
+                if (!mbar_wait(smem_u32(&bars->empty[c & 1]), (c >> 1) & 1, err)) break;
+                load(loaded++, true);
+            }
             if (!STATE_ONLY) {
-                if (!mbar_wait(smem_u32(&bars->staged), c & 1, err)) break;
+                if (!mbar_wait(smem_u32(&bars->staged[c & 1]), (c >> 1) & 1, err)) break;
                 if (sweep.tma_out && first_token(c) >= 0) {
                     if (elect_one()) {
 #pragma unroll
@@ -663,10 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                     }
                     __syncwarp();
                 }
-            }
-            if (c + 2 < chunks) {
-                if (!mbar_wait(smem_u32(&bars->empty[c & 1]), (c >> 1) & 1, err)) break;
-                load(loaded++);
+                if (c + 2 < chunks) load(c + 2, false);
             }
         }
         if (*err && sweep.tma_in) {  // copies in flight land before the block ends
@@ -683,17 +702,21 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512));
     }
     if (!STATE_ONLY) {
-        TO *po = static_cast<TO *>(w.out) + (static_cast<long long>(b) * w.T * w.H + h) * w.dv + c0;
+        const long long po = (static_cast<long long>(b) * w.T * w.H + h) * w.dv + c0;
         const long long ost = static_cast<long long>(w.H) * w.dv;
+        auto put = [&](long long at, float x) {
+            if (w.out_f32) static_cast<float *>(w.out)[at] = x;
+            else static_cast<__nv_bfloat16 *>(w.out)[at] = __float2bfloat16(x);
+        };
         if (*err)  // a wait ran out: nothing of this segment is to be trusted
             for (long long i = tid; i < static_cast<long long>(hi - lo) * ncol; i += kThreads) {
                 const long long r = lo + i / ncol, t = rev ? L - 1 - r : r;
-                po[t * ost + i % ncol] = static_cast<TO>(__int_as_float(0x7fc00000));
+                put(po + t * ost + i % ncol, __int_as_float(0x7fc00000));
             }
         // outputs behind the sequence's length are zero
         const long long t_lo = r_lo > L ? r_lo : L, t_hi = r_lo + w.seg < w.T ? r_lo + w.seg : w.T;
         for (long long i = tid; i < (t_hi - t_lo) * ncol; i += kThreads)
-            po[(t_lo + i / ncol) * ost + i % ncol] = static_cast<TO>(0.f);
+            put(po + (t_lo + i / ncol) * ost + i % ncol, 0.f);
     }
 }
 
@@ -729,9 +752,9 @@ TcSweep with_maps(const LaSweep &w) {
     return t;
 }
 
-template <typename TO, int DK, int DV, bool STATE_ONLY>
+template <int DK, int DV, bool STATE_ONLY>
 cudaError_t launch(const TcBatch &t, int n, cudaStream_t s) {
-    auto k = la_tc_kernel<TO, DK, DV, STATE_ONLY>;
+    auto k = la_tc_kernel<DK, DV, STATE_ONLY>;
     constexpr int smem = Lay<DK, DV>::BYTES > 120 * 1024 ? Lay<DK, DV>::BYTES : 120 * 1024;  // one CTA per SM (TMEM)
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -742,30 +765,33 @@ cudaError_t launch(const TcBatch &t, int n, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-template <typename TO, int DK, int DV>
+template <int DK, int DV>
 cudaError_t sweep(const TcBatch &t, int n, cudaStream_t s) {
     cudaError_t e;
     if (t.s[0].w.n_seg > 1) {
-        if ((e = launch<TO, DK, DV, true>(t, n, s)) != cudaSuccess) return e;
+        if ((e = launch<DK, DV, true>(t, n, s)) != cudaSuccess) return e;
         for (int i = 0; i < n; ++i)
             if ((e = launch_la_join(t.s[i].w, s)) != cudaSuccess) return e;
     }
-    return launch<TO, DK, DV, false>(t, n, s);
+    return launch<DK, DV, false>(t, n, s);
 }
 
-template <typename TO>
 cudaError_t by_width(const TcBatch &t, int n, cudaStream_t s) {
     const LaSweep &w = t.s[0].w;
-    if (w.dk <= 64) return w.dv <= 64 ? sweep<TO, 64, 64>(t, n, s) : sweep<TO, 64, 128>(t, n, s);
-    return w.dv <= 64 ? sweep<TO, 128, 64>(t, n, s) : sweep<TO, 128, 128>(t, n, s);
+    if (w.dk <= 64) return w.dv <= 64 ? sweep<64, 64>(t, n, s) : sweep<64, 128>(t, n, s);
+    return w.dv <= 64 ? sweep<128, 64>(t, n, s) : sweep<128, 128>(t, n, s);
 }
 
 }  // namespace
 
-cudaError_t launch_la_tc(const LaSweep &w, cudaStream_t s) {
+cudaError_t launch_la_tc(const LaSweep *w, int n, cudaStream_t s) {
     TcBatch t{};
-    t.s[0] = with_maps(w);
-    return w.out_f32 ? by_width<float>(t, 1, s) : by_width<__nv_bfloat16>(t, 1, s);
+    for (int i = 0; i < n; ++i) t.s[i] = with_maps(w[i]);
+    return by_width(t, n, s);
+}
+
+bool la_tc_together(const LaSweep &x, const LaSweep &y) {
+    return (x.dk <= 64) == (y.dk <= 64) && (x.dv <= 64) == (y.dv <= 64) && x.n_seg == y.n_seg && x.seg == y.seg;
 }
 
 }  // namespace pararnn
