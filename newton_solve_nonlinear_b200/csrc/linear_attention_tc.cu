@@ -41,25 +41,26 @@ struct Lay {
     // a is free once both of its products are done: the outputs are staged there, if it is wide enough
     static constexpr int OUT = DV <= DK ? A : END, STAGE = DV <= DK ? END : END + DV / 64 * kPanel;
     static constexpr int SS = 2 * STAGE;                 // bf16 S: [DV rows][DK], K-major panels
-    static constexpr int TAB = SS + DK / 64 * DV * 128;  // floats: score weights 160, row weights 2 x 128, 32
-    static constexpr int BARS = TAB + (160 + 256 + 32) * 4;
+    static constexpr int TAB = SS + DK / 64 * DV * 128;  // floats: score weights 160, row weights 2 x 128
+    static constexpr int BARS = TAB + (160 + 256) * 4;
     static constexpr int BYTES = BARS + 160 + 1024;
-    // TMEM columns: scores, whose place dS takes once they are weighted; weighted scores; out; three terms of c
-    static constexpr int T_S = 0, T_P = 128, T_O = 192, T_V = 320;
+    // TMEM columns: scores, each half of which becomes the weighted scores of its 64 columns (32-bit columns 0-31 and
+    // 64-95); out; dS; two places for terms of c: the smallest and then the largest, and the middle one
+    static constexpr int T_S = 0, T_O = 128, T_D = 256, T_V = 384;
     static constexpr int STATE_WARPS = 2 * (DV / 32);
     static_assert(BYTES <= 227 * 1024, "shared memory");
 };
 
 struct Bars {
-    unsigned long long full[2], empty[2], staged[2], scores, inter, p, scaled, v, ss, out, ds, out_read, ds_read;
+    unsigned long long full[2], empty[2], staged[2], scores, inter, scaled, v, low, v_high, ss, out, ds, out_read;
     unsigned tmem;
     int err;
 };
 static_assert(sizeof(Bars) <= 160, "barriers");
 
 // A barrier's next phase completes only after everyone who waits for this one has seen it (the parity would be
-// ambiguous otherwise): the chain scores -> p -> ds -> ds_read -> scores of the next chunk orders all but the
-// mover, whose barriers are one per stage, and a stage is filled again only by the mover itself.
+// ambiguous otherwise): the chains scores -> scaled -> out -> scores and v -> low -> v_high -> ds -> v order all but
+// the mover, whose barriers are one per stage, and a stage is filled again only by the mover itself.
 
 // One sweep's arguments: its sizes and pointers, and the tensor maps of its tiles.
 struct TcSweep {
@@ -171,6 +172,24 @@ __device__ __forceinline__ unsigned pack(float lo, float hi) {
     const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const unsigned *>(&p);
 }
+// (a, b) = (a, b) * (x, y), and = (a, b) * g + (x, y): two fp32 lanes at a time
+__device__ __forceinline__ void mul2(float &a, float &b, float x, float y) {
+    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tmul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "f"(x), "f"(y));
+}
+__device__ __forceinline__ void fma2(float &a, float &b, float g, float x, float y) {
+    asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %2};\n\tmov.b64 r, {%3, %4};\n\t"
+        "fma.rn.f32x2 p, p, q, r;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "f"(g), "f"(x), "f"(y));
+}
+// (a, b) -= (x, y), exactly as two subtractions
+__device__ __forceinline__ void sub2(float &a, float &b, float x, float y) {
+    fma2(x, y, -1.f, a, b);
+    a = x, b = y;
+}
+
 __device__ __forceinline__ float lo_of(unsigned u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float hi_of(unsigned u) { return __uint_as_float(u & 0xffff0000u); }
 
@@ -228,28 +247,27 @@ __device__ __forceinline__ void copy_tile(unsigned dst, const __nv_bfloat16 *src
 }
 
 // 32 columns of one output row, `room` of which exist.
-__device__ __forceinline__ void store32(__nv_bfloat16 *p, const float (&v)[32], int room, bool vec) {
-    if (vec && room >= 32) {
+__device__ __forceinline__ void store_few(void *p, bool f32, float4 x, int room) {
+    const float v[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4 *>(p + 8 * i) =
-                make_uint4(pack(v[8 * i], v[8 * i + 1]), pack(v[8 * i + 2], v[8 * i + 3]),
-                           pack(v[8 * i + 4], v[8 * i + 5]), pack(v[8 * i + 6], v[8 * i + 7]));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < room) p[i] = __float2bfloat16(v[i]);
+    for (int i = 0; i < 4; ++i) {
+        if (i >= room) break;
+        if (f32) static_cast<float *>(p)[i] = v[i];
+        else static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16(v[i]);
     }
 }
-__device__ __forceinline__ void store32(float *p, const float (&v)[32], int room, bool vec) {
-    if (vec && room >= 32) {
+__device__ __forceinline__ void store32(void *out, long long at, bool f32, const float (&v)[32], int room, bool vec) {
+    float *pf = static_cast<float *>(out) + at;
+    __nv_bfloat16 *pb = static_cast<__nv_bfloat16 *>(out) + at;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<float4 *>(p + 4 * i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < room) p[i] = v[i];
+    for (int i = 0; i < 32; i += 4) {
+        const float4 x = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        if (vec && room >= i + 4) {
+            if (f32) *reinterpret_cast<float4 *>(pf + i) = x;
+            else *reinterpret_cast<uint2 *>(pb + i) = make_uint2(pack(x.x, x.y), pack(x.z, x.w));
+        } else if (room > i) {
+            store_few(f32 ? static_cast<void *>(pf + i) : static_cast<void *>(pb + i), f32, x, room - i);
+        }
     }
 }
 
@@ -262,9 +280,10 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
     const TcSweep &sweep = batch.s[blockIdx.z];
     const LaSweep &w = sweep.w;
     const unsigned sm = smem_u32(smem);
-    float *sw = reinterpret_cast<float *>(smem + Y::TAB) + 32;  // [-32 .. 127]: intra g^x, 0 below x = 0
-    float *cw = sw + 128;   // [2][128]: update g^(n - e - j) of tile row x, for a full chunk and for the last one
-    float *uw = cw + 256;   // [32]: g^(31 - y), reversed g^y
+    // weight of the score (row x, column y), intra g^|x - y| or 0, at sw[y - x]: of y - x in -127 .. 32 forward, in
+    // -32 .. 127 reversed, as far as any block needs it
+    float *sw = reinterpret_cast<float *>(smem + Y::TAB);
+    float *cw = sw + 160;  // [2][128]: update g^(n - e - j) of tile row x, for a full chunk and for the last one
     Bars *bars = reinterpret_cast<Bars *>(smem + Y::BARS);
     volatile int *err = &bars->err;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -281,6 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
     const int n_last = hi - lo - (chunks - 1) * kC;
     const int ncol = min(DV, w.dv - c0);
     const bool rev = w.reverse != 0;
+    const int e = w.e;
     // exp(n * -1e4) is 0 for n >= 1 and 1 for n = 0, as g = 0 wants it
     const float ld = fmaxf(w.log_decay[h], -1e4f);
     auto power = [&](int n) { return expf(static_cast<float>(static_cast<double>(ld) * n)); };
@@ -297,12 +317,12 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         mbar_init(smem_u32(&bars->inter), 1);
         mbar_init(smem_u32(&bars->out), 1);
         mbar_init(smem_u32(&bars->ds), 1);
-        mbar_init(smem_u32(&bars->p), 8);
+        mbar_init(smem_u32(&bars->low), 1);
         mbar_init(smem_u32(&bars->scaled), 8);
         mbar_init(smem_u32(&bars->out_read), 8);
         mbar_init(smem_u32(&bars->v), Y::STATE_WARPS);
         mbar_init(smem_u32(&bars->ss), Y::STATE_WARPS);
-        mbar_init(smem_u32(&bars->ds_read), Y::STATE_WARPS);
+        mbar_init(smem_u32(&bars->v_high), Y::STATE_WARPS);
         bars->err = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -312,13 +332,11 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     if (tid < 160) {
-        sw[tid - 32] = tid >= 32 ? power(tid - 32) * w.intra : 0.f;
+        const int x = rev ? tid - 32 : 127 - tid;  // row distance, counted towards the past
+        sw[tid] = x >= 0 ? power(x) * w.intra : 0.f;
     } else if (tid < 160 + 256) {
         const int x = (tid - 160) & 127, n = tid - 160 < 128 ? kC : n_last, j = rev ? kC - 1 - x : x;
-        cw[tid - 160] = j < n ? power(n - w.e - j) * w.update : 0.f;
-    } else if (tid < 160 + 256 + 32) {
-        const int y = tid - 416;
-        uw[y] = power(rev ? y : 31 - y);
+        cw[tid - 160] = j < n ? power(n - e - j) * w.update : 0.f;
     }
     fence_before();
     __syncthreads();
@@ -332,45 +350,32 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;
             const int i = rev ? kC - 1 - row : row;  // logical row
             const unsigned tl = tm + (static_cast<unsigned>(quarter * 32) << 16);
-            const float f = power(i + w.e) * w.inter;
+            const float f = power(i + e) * w.inter;
             const long long po = (static_cast<long long>(b) * w.T * w.H + h) * w.dv + c0;
             const long long ost = static_cast<long long>(w.H) * w.dv;
-            const bool vec = w.dv % 8 == 0;
+            const bool vec = w.dv % 8 == 0, tma_out = sweep.tma_out != 0, out_f32 = w.out_f32 != 0;
+            void *const out = w.out;
             for (int c = 0; c < chunks; ++c) {
                 const unsigned ph = c & 1;
                 const int n = c + 1 < chunks ? kC : n_last;
                 if (!mbar_wait(smem_u32(&bars->scores), ph, err)) break;
                 fence_after();
 #pragma unroll 1
-                for (int jb = half; jb < 4; jb += 2) {
+                for (int jb = half * 2; jb < half * 2 + 2; ++jb) {
                     unsigned u[16] = {};
-                    if (jb == quarter) {  // the diagonal block; what is masked may hold anything
+                    if (rev ? jb >= quarter : jb <= quarter) {  // else all of the block is masked
                         float v[32];
                         tmem_ld32(tl + Y::T_S + jb * 32, v);
-                        const float *s = rev ? sw - lane : sw + lane;
+                        const float *s = sw + (rev ? 32 : 127) + jb * 32 - row;
 #pragma unroll
                         for (int j = 0; j < 32; j += 2) {
-                            const float s0 = rev ? s[j] : s[-j], s1 = rev ? s[j + 1] : s[-j - 1];
-                            const bool k0 = rev ? j >= lane : j <= lane, k1 = rev ? j + 1 >= lane : j + 1 <= lane;
-                            u[j / 2] = pack(k0 ? v[j] * s0 : 0.f, k1 ? v[j + 1] * s1 : 0.f);
-                        }
-                    } else if (rev ? jb > quarter : jb < quarter) {  // all of it counts
-                        float v[32];
-                        tmem_ld32(tl + Y::T_S + jb * 32, v);
-                        const float s = rev ? sw[jb * 32 - row] : sw[row - jb * 32 - 31];
-#pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
-                            const float4 y = *reinterpret_cast<const float4 *>(uw + j);
-                            u[j / 2] = pack(v[j] * (s * y.x), v[j + 1] * (s * y.y));
-                            u[j / 2 + 1] = pack(v[j + 2] * (s * y.z), v[j + 3] * (s * y.w));
+                            mul2(v[j], v[j + 1], s[j], s[j + 1]);
+                            u[j / 2] = pack(v[j], v[j + 1]);
                         }
                     }
-                    tmem_st16(tl + Y::T_P + jb * 16, u);
+                    // in the place of scores that this warp has read
+                    tmem_st16(tl + Y::T_S + half * 64 + (jb & 1) * 16, u);
                 }
-                tmem_st_wait();
-                fence_before();
-                __syncwarp();
-                if (lane == 0) arrive(smem_u32(&bars->p));
                 if (!mbar_wait(smem_u32(&bars->inter), ph, err)) break;
                 fence_after();
 #pragma unroll 1
@@ -378,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                     float v[32];
                     tmem_ld32(tl + Y::T_O + cb, v);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] *= f;
+                    for (int j = 0; j < 32; j += 2) mul2(v[j], v[j + 1], f, f);
                     tmem_st32(tl + Y::T_O + cb, v);
                 }
                 tmem_st_wait();
@@ -390,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                 const long long t = first_token(c) + row;
                 const bool live = i < n;
                 // a tile that starts before the first token cannot be stored by TMA
-                const bool stage = sweep.tma_out && first_token(c) >= 0;
+                const bool stage = tma_out && first_token(c) >= 0;
 #pragma unroll 1
                 for (int cb = half * (DV / 2); cb < (half + 1) * (DV / 2); cb += 32) {
                     float v[32];
@@ -401,22 +406,23 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                         if (lane == 0) arrive(smem_u32(&bars->out_read));
                     }
                     if (stage) {
+                        if (!live) {
+#pragma unroll
+                            for (int q = 0; q < 32; ++q) v[q] = 0.f;
+                        }
                         const unsigned at = sm + (c & 1) * Y::STAGE + Y::OUT + (cb >> 6) * kPanel + row * 128;
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             const unsigned d = at + (((((cb & 32) >> 3) + q) ^ (row & 7)) << 4);
                             unsigned u[4];
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                u[k] = live ? pack(v[8 * q + 2 * k], v[8 * q + 2 * k + 1]) : 0u;
+                            for (int k = 0; k < 4; ++k) u[k] = pack(v[8 * q + 2 * k], v[8 * q + 2 * k + 1]);
                             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(d), "r"(u[0]), "r"(u[1]),
                                          "r"(u[2]), "r"(u[3])
                                          : "memory");
                         }
                     } else if (live && cb < ncol) {
-                        const long long at = po + t * ost + cb;
-                        if (w.out_f32) store32(static_cast<float *>(w.out) + at, v, ncol - cb, vec);
-                        else store32(static_cast<__nv_bfloat16 *>(w.out) + at, v, ncol - cb, vec);
+                        store32(out, po + t * ost + cb, out_f32, v, ncol - cb, vec);
                     }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -432,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             constexpr int KH = DK / 2;
             const int d = quarter * 32 + lane;
             const unsigned tl = tm + (static_cast<unsigned>(quarter * 32) << 16);
-            const unsigned t_ds = tl + Y::T_S + half * KH;
+            const unsigned t_ds = tl + Y::T_D + half * KH;
             float S[KH];
             {
                 const bool have = d < ncol && (w.n_seg > 1 ? !STATE_ONLY : w.s_in != nullptr);
@@ -493,38 +499,57 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                     __syncwarp();
                 }
                 const float *cwt = cw + (last ? 128 : 0) + half * 64 + 2 * (lane & 3);
-#pragma unroll 1
-                for (int sub = 0; sub < 2; ++sub) {  // 16 columns of c at a time
+                const unsigned ta = tl + Y::T_V + half * 32;
+                // 16 columns of c (sub), 64 tokens; registers k, k + 1: the same 8 tokens, columns lane / 4 and + 8
+                auto load_c = [&](int sub, unsigned (&u)[16]) {
                     const int ch = (quarter & 1) * 4 + sub * 2 + ((lane >> 3) & 1);
-                    unsigned u0[16], u1[16], u2[16];
+                    const unsigned at = tile_c + (quarter >> 1) * kPanel + m_row * 128 + ((ch ^ (lane & 7)) << 4);
 #pragma unroll
-                    for (int tb = 0; tb < 4; ++tb) {
-                        const unsigned at = tile_c + (quarter >> 1) * kPanel + (m_row + tb * 16) * 128 + ((ch ^ (lane & 7)) << 4);
-                        ldmatrix4t(at, u0[4 * tb], u0[4 * tb + 1], u0[4 * tb + 2], u0[4 * tb + 3]);
+                    for (int tb = 0; tb < 4; ++tb)
+                        ldmatrix4t(at + tb * 2048, u[4 * tb], u[4 * tb + 1], u[4 * tb + 2], u[4 * tb + 3]);
+                };
+#pragma unroll 1
+                for (int sub = 0; sub < 2; ++sub) {
+                    unsigned u1[16], u2[16];
+                    load_c(sub, u1);
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) {
+                        const float2 f = *reinterpret_cast<const float2 *>(cwt + (q >> 1) * 8);
+                        float y0 = lo_of(u1[q]), y1 = hi_of(u1[q]);
+                        mul2(y0, y1, f.x, f.y);
+                        const unsigned u0 = pack(y0, y1);
+                        sub2(y0, y1, lo_of(u0), hi_of(u0));
+                        u1[q] = pack(y0, y1);
+                        sub2(y0, y1, lo_of(u1[q]), hi_of(u1[q]));
+                        u2[q] = pack(y0, y1);
                     }
-#pragma unroll
-                    for (int k = 0; k < 16; k += 2) {
-                        // registers k, k + 1: the same 8 tokens, columns lane / 4 and lane / 4 + 8
-                        const float2 f = *reinterpret_cast<const float2 *>(cwt + (k >> 1) * 8);
-#pragma unroll
-                        for (int q = k; q < k + 2; ++q) {
-                            float y0 = lo_of(u0[q]) * f.x, y1 = hi_of(u0[q]) * f.y;
-                            u0[q] = pack(y0, y1);
-                            y0 -= lo_of(u0[q]), y1 -= hi_of(u0[q]);
-                            u1[q] = pack(y0, y1);
-                            y0 -= lo_of(u1[q]), y1 -= hi_of(u1[q]);
-                            u2[q] = pack(y0, y1);
-                        }
-                    }
-                    const unsigned ta = tl + (static_cast<unsigned>(sub * 16) << 16) + Y::T_V + half * 32;
-                    tmem_st_frag(ta, u0);
-                    tmem_st_frag(ta + 64, u1);
-                    tmem_st_frag(ta + 128, u2);
+                    tmem_st_frag(ta + (static_cast<unsigned>(sub * 16) << 16), u2);
+                    tmem_st_frag(ta + (static_cast<unsigned>(sub * 16) << 16) + 64, u1);
                 }
                 tmem_st_wait();
                 fence_before();
                 __syncwarp();
                 if (lane == 0) arrive(smem_u32(&bars->v));
+                // the smallest term has been used: the largest takes its place (formed again: registers are short)
+                if (!mbar_wait(smem_u32(&bars->low), ph, err)) break;
+                fence_after();
+#pragma unroll 1
+                for (int sub = 0; sub < 2; ++sub) {
+                    unsigned u[16];
+                    load_c(sub, u);
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) {
+                        const float2 f = *reinterpret_cast<const float2 *>(cwt + (q >> 1) * 8);
+                        float y0 = lo_of(u[q]), y1 = hi_of(u[q]);
+                        mul2(y0, y1, f.x, f.y);
+                        u[q] = pack(y0, y1);
+                    }
+                    tmem_st_frag(ta + (static_cast<unsigned>(sub * 16) << 16), u);
+                }
+                tmem_st_wait();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) arrive(smem_u32(&bars->v_high));
                 const float gn = last ? g_last : g_full;
                 if (!mbar_wait(smem_u32(&bars->ds), ph, err)) break;
                 fence_after();
@@ -533,11 +558,9 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                     float v[32];
                     tmem_ld32(t_ds + k, v);
 #pragma unroll
-                    for (int q = 0; q < 32; ++q) S[k + q] = fmaf(gn, S[k + q], v[q]);
+                    for (int q = 0; q < 32; q += 2) fma2(S[k + q], S[k + q + 1], gn, v[q], v[q + 1]);
                 }
                 fence_before();
-                __syncwarp();
-                if (lane == 0) arrive(smem_u32(&bars->ds_read));
                 if (!STATE_ONLY) publish();
             }
             // the last state: the segment's own (pass 1) or the sequence's
@@ -567,49 +590,72 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         const unsigned on = elect_one() ? 1u : 0u;
         const unsigned tu = __shfl_sync(0xffffffffu, tm, 0);
         int done = 0;  // chunks issued whole
-        for (int c = 0; c < chunks; ++c) {
-            const int st = c & 1;
-            const unsigned ph = c & 1;
-            const unsigned ta = sm + st * Y::STAGE + Y::A, tb = sm + st * Y::STAGE + Y::B, tc_ = sm + st * Y::STAGE + Y::C;
-            if (!mbar_wait(smem_u32(&bars->full[st]), (c >> 1) & 1, err)) break;
-            if (c > 0 && !mbar_wait(smem_u32(&bars->ds_read), ph ^ 1u, err)) break;
-            if (!STATE_ONLY) {
-                fence_after();
+        auto scores = [&](int c) {
+            const unsigned ta = sm + (c & 1) * Y::STAGE + Y::A, tb = sm + (c & 1) * Y::STAGE + Y::B;
 #pragma unroll
-                for (int k = 0; k < DK / 16; ++k) {
-                    const unsigned off = (k >> 2) * kPanel + (k & 3) * 32;
-                    mma_ss(tu + Y::T_S, sw128_desc(ta + off), sw128_desc(tb + off), id_scores, k > 0, on);
-                }
-                commit(smem_u32(&bars->scores), on);
-                if (!mbar_wait(smem_u32(&bars->ss), ph, err)) break;
-                if (c > 0 && !mbar_wait(smem_u32(&bars->out_read), ph ^ 1u, err)) break;
-                fence_after();
-#pragma unroll
-                for (int k = 0; k < DK / 16; ++k)
-                    mma_ss(tu + Y::T_O, sw128_desc(ta + (k >> 2) * kPanel + (k & 3) * 32),
-                           sw128_desc(sm + Y::SS + (k >> 2) * (DV * 128) + (k & 3) * 32), id_inter, k > 0, on);
-                commit(smem_u32(&bars->inter), on);
-                if (!mbar_wait(smem_u32(&bars->p), ph, err)) break;  // the scores' place is free for dS
+            for (int k = 0; k < DK / 16; ++k) {
+                const unsigned off = (k >> 2) * kPanel + (k & 3) * 32;
+                mma_ss(tu + Y::T_S, sw128_desc(ta + off), sw128_desc(tb + off), id_scores, k > 0, on);
             }
-            if (!mbar_wait(smem_u32(&bars->v), ph, err)) break;
+            commit(smem_u32(&bars->scores), on);
+        };
+        auto term = [&](int c, int place, bool first) {
+            const unsigned tb = sm + (c & 1) * Y::STAGE + Y::B;
+#pragma unroll
+            for (int k = 0; k < kC / 16; ++k)
+                mma_ts(tu + Y::T_D, tu + Y::T_V + place * 64 + k * 8, nmajor_desc(tb + k * 2048), id_ds, !first || k > 0, on);
+        };
+        // rows behind the sequence's length, which the state warps clear before v
+        const bool unclean = !rev && n_last < kC;
+        if (chunks > 0 && mbar_wait(smem_u32(&bars->full[0]), 0, err) &&
+            !(chunks == 1 && unclean && !mbar_wait(smem_u32(&bars->v), 0, err))) {
             fence_after();
+            if (!STATE_ONLY) scores(0);
+            for (int c = 0; c < chunks; ++c) {
+                const int st = c & 1;
+                const unsigned ph = c & 1;
+                const unsigned ta = sm + st * Y::STAGE + Y::A, tc_ = sm + st * Y::STAGE + Y::C;
+                if (!STATE_ONLY) {
+                    if (!mbar_wait(smem_u32(&bars->ss), ph, err)) break;
+                    if (c > 0 && !mbar_wait(smem_u32(&bars->out_read), ph ^ 1u, err)) break;
+                    fence_after();
 #pragma unroll
-            for (int term = 2; term >= 0; --term)  // smallest first
-#pragma unroll
-                for (int k = 0; k < kC / 16; ++k)
-                    mma_ts(tu + Y::T_S, tu + Y::T_V + term * 64 + k * 8, nmajor_desc(tb + k * 2048), id_ds,
-                           term < 2 || k > 0, on);
-            commit(smem_u32(&bars->ds), on);
-            if (!STATE_ONLY) {
-                if (!mbar_wait(smem_u32(&bars->scaled), ph, err)) break;
+                    for (int k = 0; k < DK / 16; ++k)
+                        mma_ss(tu + Y::T_O, sw128_desc(ta + (k >> 2) * kPanel + (k & 3) * 32),
+                               sw128_desc(sm + Y::SS + (k >> 2) * (DV * 128) + (k & 3) * 32), id_inter, k > 0, on);
+                    commit(smem_u32(&bars->inter), on);
+                }
+                // dS, the smallest term first; dS's place is free: v comes after the state warps have read it
+                if (!mbar_wait(smem_u32(&bars->v), ph, err)) break;
                 fence_after();
+                term(c, 0, true);
+                commit(smem_u32(&bars->low), on);
+                term(c, 1, false);
+                if (!STATE_ONLY) {
+                    if (!mbar_wait(smem_u32(&bars->scaled), ph, err)) break;
+                    fence_after();
 #pragma unroll
-                for (int k = 0; k < kC / 16; ++k)
-                    mma_ts(tu + Y::T_O, tu + Y::T_P + k * 8, nmajor_desc(tc_ + k * 2048), id_out, true, on);
-                commit(smem_u32(&bars->out), on);
+                    for (int k = 0; k < kC / 16; ++k)
+                        mma_ts(tu + Y::T_O, tu + Y::T_S + (k >> 2) * 64 + (k & 3) * 8, nmajor_desc(tc_ + k * 2048), id_out,
+                               true, on);
+                    commit(smem_u32(&bars->out), on);
+                }
+                if (!mbar_wait(smem_u32(&bars->v_high), ph, err)) break;
+                fence_after();
+                term(c, 0, false);
+                commit(smem_u32(&bars->ds), on);
+                commit(smem_u32(&bars->empty[st]), on);
+                done = c + 1;
+                if (c + 1 < chunks) {
+                    if (!mbar_wait(smem_u32(&bars->full[st ^ 1]), ((c + 1) >> 1) & 1, err)) break;
+                    if (!STATE_ONLY) {  // the next scores, as soon as the weighted ones have been used
+                        if (!mbar_wait(smem_u32(&bars->out), ph, err)) break;
+                        if (c + 2 == chunks && unclean && !mbar_wait(smem_u32(&bars->v), ph ^ 1u, err)) break;
+                        fence_after();
+                        scores(c + 1);
+                    }
+                }
             }
-            commit(smem_u32(&bars->empty[st]), on);
-            done = c + 1;
         }
         // everything issued has finished before TMEM is given back: each chunk's last commit, or, where a wait ran
         // out in the middle of a chunk, a last one
@@ -622,37 +668,37 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         }
     } else if (warp == 17) {
         // ---- tiles in, staged outputs out
-        const __nv_bfloat16 *pa = static_cast<const __nv_bfloat16 *>(w.a.p) + b * w.a.sb + (h / w.a.group) * w.a.sh;
-        const __nv_bfloat16 *pb = static_cast<const __nv_bfloat16 *>(w.b.p) + b * w.b.sb + (h / w.b.group) * w.b.sh;
-        const __nv_bfloat16 *pc = static_cast<const __nv_bfloat16 *>(w.c.p) + b * w.c.sb + (h / w.c.group) * w.c.sh + c0;
+        const bool tma_in = sweep.tma_in != 0, tma_out = sweep.tma_out != 0;
+        const int ha = h / w.a.group, hb = h / w.b.group, hc = h / w.c.group;
+        auto head_of = [&](const LaRows &r, int hr) { return static_cast<const __nv_bfloat16 *>(r.p) + b * r.sb + hr * r.sh; };
         // first b and c, then a, whose place the staged outputs may hold longer
         auto load = [&](int c, bool first) {
             const int st = c & 1, t0 = first_token(c), n = c + 1 < chunks ? kC : n_last;
             const unsigned base = sm + st * Y::STAGE, full = smem_u32(&bars->full[st]);
-            if (sweep.tma_in) {
+            if (tma_in) {
                 if (elect_one()) {
                     if (first) {
                         mbar_expect_tx(full, (DK / 64 + DV / 64) * kPanel);
 #pragma unroll
                         for (int x = 0; x < DV / 64; ++x)
-                            tma_load_4d(base + Y::C + x * kPanel, &sweep.c, c0 + x * 64, t0, h / w.c.group, b, full);
+                            tma_load_4d(base + Y::C + x * kPanel, &sweep.c, c0 + x * 64, t0, hc, b, full);
 #pragma unroll
                         for (int x = 0; x < DK / 64; ++x)
-                            tma_load_4d(base + Y::B + x * kPanel, &sweep.b, x * 64, t0, h / w.b.group, b, full);
+                            tma_load_4d(base + Y::B + x * kPanel, &sweep.b, x * 64, t0, hb, b, full);
                     } else {
                         mbar_expect_tx(full, DK / 64 * kPanel);
 #pragma unroll
                         for (int x = 0; x < DK / 64; ++x)
-                            tma_load_4d(base + Y::A + x * kPanel, &sweep.a, x * 64, t0, h / w.a.group, b, full);
+                            tma_load_4d(base + Y::A + x * kPanel, &sweep.a, x * 64, t0, ha, b, full);
                     }
                 }
             } else {
                 const int x_lo = rev ? kC - n : 0, x_hi = rev ? kC : n;
                 if (first) {
-                    copy_tile<DV / 64>(base + Y::C, pc, w.c.st, t0, x_lo, x_hi, ncol, lane);
-                    copy_tile<DK / 64>(base + Y::B, pb, w.b.st, t0, x_lo, x_hi, w.dk, lane);
+                    copy_tile<DV / 64>(base + Y::C, head_of(w.c, hc) + c0, w.c.st, t0, x_lo, x_hi, ncol, lane);
+                    copy_tile<DK / 64>(base + Y::B, head_of(w.b, hb), w.b.st, t0, x_lo, x_hi, w.dk, lane);
                 } else {
-                    copy_tile<DK / 64>(base + Y::A, pa, w.a.st, t0, x_lo, x_hi, w.dk, lane);
+                    copy_tile<DK / 64>(base + Y::A, head_of(w.a, ha), w.a.st, t0, x_lo, x_hi, w.dk, lane);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
@@ -661,18 +707,17 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             __syncwarp();
         };
         int loaded = 0;  // chunks of which any tile was asked for
-        for (; loaded < min(chunks, 2); ++loaded) {
-            load(loaded, true);
-            if (!STATE_ONLY) load(loaded, false);
-        }
-        for (int c = 0; c < chunks; ++c) {
+#pragma unroll 1
+        for (int c = -2; c < chunks; ++c) {
             if (c + 2 < chunks) {
-                if (!mbar_wait(smem_u32(&bars->empty[c & 1]), (c >> 1) & 1, err)) break;
-                load(loaded++, true);
+                if (c >= 0 && !mbar_wait(smem_u32(&bars->empty[c & 1]), (c >> 1) & 1, err)) break;
+                load(c + 2, true);
+                loaded = c + 3;
             }
-            if (!STATE_ONLY) {
+            if (STATE_ONLY) continue;
+            if (c >= 0) {
                 if (!mbar_wait(smem_u32(&bars->staged[c & 1]), (c >> 1) & 1, err)) break;
-                if (sweep.tma_out && first_token(c) >= 0) {
+                if (tma_out && first_token(c) >= 0) {
                     if (elect_one()) {
 #pragma unroll
                         for (int x = 0; x < DV / 64; ++x)
@@ -685,10 +730,10 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                     }
                     __syncwarp();
                 }
-                if (c + 2 < chunks) load(c + 2, false);
             }
+            if (c + 2 < chunks) load(c + 2, false);
         }
-        if (*err && sweep.tma_in) {  // copies in flight land before the block ends
+        if (*err && tma_in) {  // copies in flight land before the block ends
             for (int c = max(loaded - 2, 0); c < loaded; ++c) mbar_drain(smem_u32(&bars->full[c & 1]), (c >> 1) & 1);
         }
         asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
