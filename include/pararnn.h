@@ -727,8 +727,10 @@ typedef struct {
 } pararnn_attention_shape;
 
 /* pararnn_linear_attention_workspace_size -- bytes pararnn_linear_attention
- * needs, or 0 for arguments it rejects. */
-PARARNN_API size_t pararnn_linear_attention_workspace_size(const pararnn_attention_shape *shape);
+ * needs for these operands (bf16 rows off 16 bytes are packed there first), or
+ * 0 for arguments it rejects. */
+PARARNN_API size_t pararnn_linear_attention_workspace_size(const pararnn_attention_shape *shape, const pararnn_rows *q,
+                                                           const pararnn_rows *k, const pararnn_rows *v);
 
 /*
  * pararnn_linear_attention -- the linear recurrence with a matrix state: for
@@ -752,8 +754,8 @@ PARARNN_API size_t pararnn_linear_attention_workspace_size(const pararnn_attenti
  * The state and all sums are fp32.  With bf16 operands the weighted scores and
  * a copy of the state are rounded to bf16 where they enter the products for o;
  * the state itself is updated from products exact to fp32.  A token that is
- * not finite makes the outputs of the 256 tokens before it undefined as well as
- * those after it.  Outputs must not overlap inputs or the workspace.  Repeated
+ * not finite makes the outputs of up to 127 tokens before it undefined as well
+ * as those after it.  Outputs must not overlap inputs or the workspace.  Repeated
  * calls give the same bits.  Asynchronous: returns PARARNN_OK, INVALID_ARG or
  * CUDA_ERROR.
  */
@@ -763,8 +765,11 @@ PARARNN_API int pararnn_linear_attention(const pararnn_attention_shape *shape, c
                                          size_t ws_bytes, pararnn_stream stream);
 
 /* pararnn_linear_attention_backward_workspace_size -- bytes
- * pararnn_linear_attention_backward needs, or 0 for arguments it rejects. */
-PARARNN_API size_t pararnn_linear_attention_backward_workspace_size(const pararnn_attention_shape *shape);
+ * pararnn_linear_attention_backward needs for these operands, or 0 for
+ * arguments it rejects. */
+PARARNN_API size_t pararnn_linear_attention_backward_workspace_size(const pararnn_attention_shape *shape,
+                                                                    const pararnn_rows *q, const pararnn_rows *k,
+                                                                    const pararnn_rows *v, const pararnn_rows *d_o);
 
 /*
  * pararnn_linear_attention_backward -- its backward pass: from dL/do and dL/ds

@@ -166,9 +166,10 @@ def lib() -> ctypes.CDLL:
         L.pararnn_adjoint_exact_workspace_size.argtypes = [ctypes.POINTER(Cell), ci, ci]
         L.pararnn_adjoint_exact_workspace_size.restype = sz
         shape_p, rows_p, norm_p = ctypes.POINTER(AttentionShape), ctypes.POINTER(Rows), ctypes.POINTER(NormShape)
-        for name in ("pararnn_linear_attention_workspace_size", "pararnn_linear_attention_backward_workspace_size"):
-            getattr(L, name).argtypes = [shape_p]
-            getattr(L, name).restype = sz
+        L.pararnn_linear_attention_workspace_size.argtypes = [shape_p, rows_p, rows_p, rows_p]
+        L.pararnn_linear_attention_workspace_size.restype = sz
+        L.pararnn_linear_attention_backward_workspace_size.argtypes = [shape_p, rows_p, rows_p, rows_p, rows_p]
+        L.pararnn_linear_attention_backward_workspace_size.restype = sz
         L.pararnn_linear_attention.argtypes = [shape_p, rows_p, rows_p, rows_p, vp, vp, vp, vp, vp, vp, sz, vp]
         L.pararnn_linear_attention.restype = ci
         L.pararnn_linear_attention_backward.argtypes = [shape_p, rows_p, rows_p, rows_p, vp, rows_p, vp, vp, vp, vp, vp,
@@ -861,7 +862,8 @@ def linear_attention(q, k, v, log_decay, *, s0=None, lengths=None, scale=None, o
         o, s = out if out is not None else (torch.empty(B, T, H, dv, dtype=q.dtype, device=q.device),
                                             torch.empty(B, H, dk, dv, dtype=torch.float32, device=q.device))
         L = lib()
-        ws = _workspace(L.pararnn_linear_attention_workspace_size(shape), "pararnn_linear_attention", workspace, q.device)
+        ws = _workspace(L.pararnn_linear_attention_workspace_size(shape, rq, rk, rv), "pararnn_linear_attention", workspace,
+                        q.device)
         rc = L.pararnn_linear_attention(
             shape, rq, rk, rv, _like(log_decay, "log_decay", q, (H,), torch.float32),
             _like(s0, "s0", q, (B, H, dk, dv), torch.float32), _like(lengths, "lengths", q, (B,), torch.int32),
@@ -885,8 +887,8 @@ def linear_attention_backward(q, k, v, log_decay, do, *, s0=None, ds=None, lengt
         g = dict(dq=new(B, T, H, dk), dk=new(B, T, Hkv, dk), dv=new(B, T, Hkv, dv),
                  ds0=None if s0 is None else new(B, H, dk, dv, dtype=torch.float32))
         L = lib()
-        ws = _workspace(L.pararnn_linear_attention_backward_workspace_size(shape), "pararnn_linear_attention_backward",
-                        workspace, q.device)
+        ws = _workspace(L.pararnn_linear_attention_backward_workspace_size(shape, rq, rk, rv, rdo),
+                        "pararnn_linear_attention_backward", workspace, q.device)
         state = (B, H, dk, dv)
         rc = L.pararnn_linear_attention_backward(
             shape, rq, rk, rv, _like(log_decay, "log_decay", q, (H,), torch.float32), rdo,

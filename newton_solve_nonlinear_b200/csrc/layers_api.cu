@@ -51,29 +51,143 @@ Extent extent(const pararnn_rows &r, long long B, long long T, long long heads, 
     return {r.ptr, last * esize(dtype)};
 }
 LaRows operand(const pararnn_rows &r, int group) { return {r.ptr, r.stride_b, r.stride_t, r.stride_h, group}; }
-LaRows dense(const void *p, long long T, long long heads, long long width, int group) {
-    return {p, T * heads * width, heads * width, width, group};
-}
 
 size_t state_bytes(const pararnn_attention_shape &s) { return static_cast<size_t>(s.B) * s.H * s.dk * s.dv * 4; }
-size_t seg_bytes(const pararnn_attention_shape &s, const LaPlan &p) {
-    return p.n_seg > 1 ? align256(state_bytes(s) * p.n_seg) : 0;
-}
-// fp32 partial gradients [B, T, H, width] of each head where keys and values are shared
-size_t part_bytes(const pararnn_attention_shape &s, int width) {
-    return s.H == s.Hkv ? 0 : align256(static_cast<size_t>(s.B) * s.T * s.H * width * sizeof(float));
+int padded(int width) { return (width + 7) / 8 * 8; }
+
+// Lays a call's workspace out; with no base it only counts.
+struct Carve {
+    char *base;
+    size_t used;
+    char *take(size_t n) {
+        char *p = base + used;
+        used += align256(n);
+        return p;
+    }
+};
+
+// The sweeps of a call, and what is packed before and unpacked after them.  Built the same way for the size query
+// and for the call.
+struct Call {
+    const pararnn_attention_shape &s;
+    Carve ws;
+    LaSweep w[3];
+    struct {
+        LaRows from;
+        void *to;
+        int heads, width;
+    } pack[4];
+    struct {
+        const void *from;
+        void *to;
+        int heads, width;
+    } unpack[3];
+    int n_pack = 0, n_unpack = 0;
+
+    Call(const pararnn_attention_shape &shape, void *workspace)
+        : s(shape), ws{static_cast<char *>(workspace), 0}, w{}, pack{}, unpack{} {}
+
+    // bf16 rows come by TMA: those that it cannot read are packed first
+    LaRows in(const pararnn_rows &r, int heads, int width) {
+        const LaRows x = operand(r, s.H / heads);
+        if (s.dtype != PARARNN_BF16 || la_tc_readable(x, s.B, s.T, heads)) return x;
+        const int wp = padded(width);
+        void *to = ws.take(static_cast<size_t>(s.B) * s.T * heads * wp * 2);
+        pack[n_pack++] = {x, to, heads, width};
+        return {to, static_cast<long long>(s.T) * heads * wp, static_cast<long long>(heads) * wp, wp, x.group};
+    }
+    // outputs of w [B, T, H, width]; bf16 rows leave by TMA, in rows of whole 16 bytes
+    void out(LaSweep &x, void *p, int width) {
+        x.out = p;
+        x.out_w = width;
+        if (s.dtype != PARARNN_BF16 || width % 8 == 0) return;
+        x.out_w = padded(width);
+        x.out = ws.take(static_cast<size_t>(s.B) * s.T * s.H * x.out_w * 2);
+        unpack[n_unpack++] = {x.out, p, s.H, width};
+    }
+    // fp32 partial outputs of each head, where keys and values are shared
+    float *partial(LaSweep &x, int width) {
+        x.out_w = padded(width);
+        x.out_f32 = 1;
+        x.out = ws.take(static_cast<size_t>(s.B) * s.T * s.H * x.out_w * sizeof(float));
+        return static_cast<float *>(x.out);
+    }
+    void sweep(LaSweep &x, const float *log_decay, const int *lengths, int dk, int dv, const LaPlan &p) {
+        x.B = s.B, x.T = s.T, x.H = s.H, x.dk = dk, x.dv = dv, x.dtype = s.dtype;
+        x.log_decay = log_decay, x.lengths = lengths;
+        x.n_seg = p.n_seg, x.seg = p.seg;
+        if (p.n_seg > 1) x.seg_state = reinterpret_cast<float *>(ws.take(state_bytes(s) * p.n_seg));
+    }
+    bool before(cudaStream_t st) const {
+        for (int i = 0; i < n_pack; ++i)
+            if (launch_la_pack(pack[i].from, pack[i].to, s.B, s.T, pack[i].heads, pack[i].width, st) != cudaSuccess)
+                return false;
+        return true;
+    }
+    bool after(cudaStream_t st) const {
+        for (int i = 0; i < n_unpack; ++i)
+            if (launch_la_unpack(unpack[i].from, unpack[i].to, static_cast<long long>(s.B) * s.T * unpack[i].heads,
+                                 unpack[i].width, st) != cudaSuccess)
+                return false;
+        return true;
+    }
+};
+
+void build_forward(Call &c, const pararnn_rows &q, const pararnn_rows &k, const pararnn_rows &v, const float *log_decay,
+                   const float *s0, const int *lengths, void *o, float *s_out) {
+    const pararnn_attention_shape &s = c.s;
+    LaSweep &w = c.w[0];
+    c.sweep(w, log_decay, lengths, s.dk, s.dv, la_plan(s.B, s.T, s.H, s.dv, s.dtype, 1));
+    w.a = c.in(q, s.H, s.dk), w.b = c.in(k, s.Hkv, s.dk), w.c = c.in(v, s.Hkv, s.dv);
+    w.s_in = s0, w.s_out = s_out, w.s_i = s.dv, w.s_j = 1;
+    c.out(w, o, s.dv);
+    w.e = 1;
+    w.intra = w.inter = s.scale, w.update = 1.f;
 }
 
-LaSweep sweep_of(const pararnn_attention_shape &s, const float *log_decay, const int *lengths, int dk, int dv) {
-    LaSweep w{};
-    w.B = s.B, w.T = s.T, w.H = s.H, w.dk = dk, w.dv = dv, w.dtype = s.dtype;
-    w.log_decay = log_decay;
-    w.lengths = lengths;
-    return w;
-}
-void set_plan(LaSweep &w, const LaPlan &p, void *seg_state) {
-    w.n_seg = p.n_seg, w.seg = p.seg;
-    w.seg_state = static_cast<float *>(seg_state);
+struct Partials {
+    float *k, *v;
+};
+Partials build_backward(Call &c, const pararnn_rows &q, const pararnn_rows &k, const pararnn_rows &v,
+                        const float *log_decay, const pararnn_rows &d_o, const float *s0, const float *ds,
+                        const int *lengths, void *dq, void *dk, void *dv, float *ds0) {
+    const pararnn_attention_shape &s = c.s;
+    const bool shared = s.H != s.Hkv;
+    Partials part{};
+    const LaRows rq = c.in(q, s.H, s.dk), rk = c.in(k, s.Hkv, s.dk), rv = c.in(v, s.Hkv, s.dv),
+                 ro = c.in(d_o, s.H, s.dv);
+    const LaPlan plan_v = la_plan(s.B, s.T, s.H, s.dv, s.dtype, 3);  // the sweep whose state is [dk, dv]
+    const LaPlan plan_k = la_plan(s.B, s.T, s.H, s.dk, s.dtype, 3);  // the sweeps whose state is [dv, dk]
+
+    // dq: the forward sweep on (do, v, k) from S_0^T
+    LaSweep &x = c.w[0];
+    c.sweep(x, log_decay, lengths, s.dv, s.dk, plan_k);
+    x.a = ro, x.b = rv, x.c = rk;
+    x.s_in = s0, x.s_i = 1, x.s_j = s.dv;
+    c.out(x, dq, s.dk);
+    x.e = 1;
+    x.intra = x.inter = s.scale, x.update = 1.f;
+
+    // dk: the reversed sweep on (v, do, q) from dS^T
+    LaSweep &y = c.w[1];
+    c.sweep(y, log_decay, lengths, s.dv, s.dk, plan_k);
+    y.a = rv, y.b = ro, y.c = rq;
+    y.s_in = ds, y.s_i = 1, y.s_j = s.dv;
+    if (shared) part.k = c.partial(y, s.dk);
+    else c.out(y, dk, s.dk);
+    y.reverse = 1;
+    y.intra = y.update = s.scale, y.inter = 1.f;
+
+    // dv: the reversed sweep on (k, q, do) from dS; its last state is dL/dS_0
+    LaSweep &z = c.w[2];
+    c.sweep(z, log_decay, lengths, s.dk, s.dv, plan_v);
+    z.a = rk, z.b = rq, z.c = ro;
+    z.s_in = ds, z.s_out = ds0, z.s_i = s.dv, z.s_j = 1;
+    if (shared) part.v = c.partial(z, s.dv);
+    else c.out(z, dv, s.dv);
+    z.reverse = 1;
+    z.intra = z.update = s.scale, z.inter = 1.f;
+    return part;
 }
 
 }  // namespace
@@ -83,20 +197,20 @@ using namespace pararnn;
 
 extern "C" {
 
-size_t pararnn_linear_attention_workspace_size(const pararnn_attention_shape *shape) {
-    if (!shape_ok(shape)) return 0;
-    const pararnn_attention_shape &s = *shape;
-    const size_t n = seg_bytes(s, la_plan(s.B, s.T, s.H, s.dk, s.dv, s.dtype));
-    return n ? n : 256;
+size_t pararnn_linear_attention_workspace_size(const pararnn_attention_shape *shape, const pararnn_rows *q,
+                                               const pararnn_rows *k, const pararnn_rows *v) {
+    if (!shape_ok(shape) || !rows_ok(q, shape->dtype) || !rows_ok(k, shape->dtype) || !rows_ok(v, shape->dtype)) return 0;
+    Call c(*shape, nullptr);
+    build_forward(c, *q, *k, *v, nullptr, nullptr, nullptr, nullptr, nullptr);
+    return c.ws.used ? c.ws.used : 256;
 }
 
 int pararnn_linear_attention(const pararnn_attention_shape *shape, const pararnn_rows *q, const pararnn_rows *k,
                              const pararnn_rows *v, const float *log_decay, const float *s0, const int *lengths,
                              void *o, float *s_out, void *workspace, size_t ws_bytes, pararnn_stream stream) {
-    const size_t need = pararnn_linear_attention_workspace_size(shape);
+    const size_t need = pararnn_linear_attention_workspace_size(shape, q, k, v);
     if (need == 0 || ws_bytes < need || !workspace || !aligned(workspace, 256)) return PARARNN_INVALID_ARG;
     const pararnn_attention_shape &s = *shape;
-    if (!rows_ok(q, s.dtype) || !rows_ok(k, s.dtype) || !rows_ok(v, s.dtype)) return PARARNN_INVALID_ARG;
     if (!log_decay || !aligned(log_decay, 4) || !aligned(s0, 16) || !aligned(lengths, 4) || !o || !aligned(o, 16) ||
         !s_out || !aligned(s_out, 16))
         return PARARNN_INVALID_ARG;
@@ -107,24 +221,21 @@ int pararnn_linear_attention(const pararnn_attention_shape *shape, const pararnn
                          extent(*v, s.B, s.T, s.Hkv, s.dv, s.dtype), {log_decay, s.H * sizeof(float)},
                          {lengths, s.B * sizeof(int)}, {s0 == s_out ? nullptr : s0, state_bytes(s)}};
     if (!disjoint(out, 3, in, 6)) return PARARNN_INVALID_ARG;
-    LaSweep w = sweep_of(s, log_decay, lengths, s.dk, s.dv);
-    w.a = operand(*q, 1), w.b = operand(*k, s.H / s.Hkv), w.c = operand(*v, s.H / s.Hkv);
-    w.s_in = s0, w.s_out = s_out, w.s_i = s.dv, w.s_j = 1;
-    w.out = o;
-    w.e = 1;
-    w.intra = w.inter = s.scale, w.update = 1.f;
-    set_plan(w, la_plan(s.B, s.T, s.H, s.dk, s.dv, s.dtype), workspace);
-    return launch_la_sweeps(&w, 1, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PARARNN_OK : PARARNN_CUDA_ERROR;
+    Call c(s, workspace);
+    build_forward(c, *q, *k, *v, log_decay, s0, lengths, o, s_out);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return c.before(st) && launch_la_sweeps(c.w, 1, st) == cudaSuccess && c.after(st) ? PARARNN_OK : PARARNN_CUDA_ERROR;
 }
 
-size_t pararnn_linear_attention_backward_workspace_size(const pararnn_attention_shape *shape) {
-    if (!shape_ok(shape)) return 0;
-    const pararnn_attention_shape &s = *shape;
-    // three sweeps that may run at once; those for dq and dk swap the roles of the widths
-    const size_t n = seg_bytes(s, la_plan(s.B, s.T, s.H, s.dk, s.dv, s.dtype)) +
-                     2 * seg_bytes(s, la_plan(s.B, s.T, s.H, s.dv, s.dk, s.dtype)) + part_bytes(s, s.dk) +
-                     part_bytes(s, s.dv);
-    return n ? n : 256;
+size_t pararnn_linear_attention_backward_workspace_size(const pararnn_attention_shape *shape, const pararnn_rows *q,
+                                                        const pararnn_rows *k, const pararnn_rows *v,
+                                                        const pararnn_rows *d_o) {
+    if (!shape_ok(shape) || !rows_ok(q, shape->dtype) || !rows_ok(k, shape->dtype) || !rows_ok(v, shape->dtype) ||
+        !rows_ok(d_o, shape->dtype))
+        return 0;
+    Call c(*shape, nullptr);
+    build_backward(c, *q, *k, *v, nullptr, *d_o, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr);
+    return c.ws.used ? c.ws.used : 256;
 }
 
 int pararnn_linear_attention_backward(const pararnn_attention_shape *shape, const pararnn_rows *q,
@@ -132,11 +243,9 @@ int pararnn_linear_attention_backward(const pararnn_attention_shape *shape, cons
                                       const pararnn_rows *d_o, const float *s0, const float *ds, const int *lengths,
                                       void *dq, void *dk, void *dv, float *ds0, void *workspace, size_t ws_bytes,
                                       pararnn_stream stream) {
-    const size_t need = pararnn_linear_attention_backward_workspace_size(shape);
+    const size_t need = pararnn_linear_attention_backward_workspace_size(shape, q, k, v, d_o);
     if (need == 0 || ws_bytes < need || !workspace || !aligned(workspace, 256)) return PARARNN_INVALID_ARG;
     const pararnn_attention_shape &s = *shape;
-    if (!rows_ok(q, s.dtype) || !rows_ok(k, s.dtype) || !rows_ok(v, s.dtype) || !rows_ok(d_o, s.dtype))
-        return PARARNN_INVALID_ARG;
     if (!log_decay || !aligned(log_decay, 4) || !aligned(s0, 16) || !aligned(ds, 16) || !aligned(lengths, 4) || !dq ||
         !dk || !dv || !aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16) || !aligned(ds0, 16))
         return PARARNN_INVALID_ARG;
@@ -151,53 +260,15 @@ int pararnn_linear_attention_backward(const pararnn_attention_shape *shape, cons
                          {log_decay, s.H * sizeof(float)},           {lengths, s.B * sizeof(int)},
                          {s0, state_bytes(s)},                       {ds, state_bytes(s)}};
     if (!disjoint(out, 5, in, 8)) return PARARNN_INVALID_ARG;
+    Call c(s, workspace);
+    const Partials part = build_backward(c, *q, *k, *v, log_decay, *d_o, s0, ds, lengths, dq, dk, dv, ds0);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const int per = s.H / s.Hkv;
-    const LaPlan plan_v = la_plan(s.B, s.T, s.H, s.dk, s.dv, s.dtype);  // the sweep whose state is [dk, dv]
-    const LaPlan plan_k = la_plan(s.B, s.T, s.H, s.dv, s.dk, s.dtype);  // the sweeps whose state is [dv, dk]
-    char *at = static_cast<char *>(workspace);
-    auto take = [&](size_t n) {
-        char *p = at;
-        at += n;
-        return p;
-    };
-    float *part_k = reinterpret_cast<float *>(take(part_bytes(s, s.dk)));
-    float *part_v = reinterpret_cast<float *>(take(part_bytes(s, s.dv)));
-    LaSweep w[3];
-
-    // dq: the forward sweep on (do, v, k) from S_0^T
-    w[0] = sweep_of(s, log_decay, lengths, s.dv, s.dk);
-    w[0].a = operand(*d_o, 1), w[0].b = operand(*v, per), w[0].c = operand(*k, per);
-    w[0].s_in = s0, w[0].s_i = 1, w[0].s_j = s.dv;
-    w[0].out = dq;
-    w[0].e = 1;
-    w[0].intra = w[0].inter = s.scale, w[0].update = 1.f;
-    set_plan(w[0], plan_k, take(seg_bytes(s, plan_k)));
-
-    // dk: the reversed sweep on (v, do, q) from dS^T
-    w[1] = sweep_of(s, log_decay, lengths, s.dv, s.dk);
-    w[1].a = operand(*v, per), w[1].b = operand(*d_o, 1), w[1].c = operand(*q, 1);
-    w[1].s_in = ds, w[1].s_i = 1, w[1].s_j = s.dv;
-    w[1].out = per == 1 ? dk : part_k;
-    w[1].out_f32 = per != 1;
-    w[1].reverse = 1;
-    w[1].intra = w[1].update = s.scale, w[1].inter = 1.f;
-    set_plan(w[1], plan_k, take(seg_bytes(s, plan_k)));
-
-    // dv: the reversed sweep on (k, q, do) from dS; its last state is dL/dS_0
-    w[2] = sweep_of(s, log_decay, lengths, s.dk, s.dv);
-    w[2].a = operand(*k, per), w[2].b = operand(*q, 1), w[2].c = operand(*d_o, 1);
-    w[2].s_in = ds, w[2].s_out = ds0, w[2].s_i = s.dv, w[2].s_j = 1;
-    w[2].out = per == 1 ? dv : part_v;
-    w[2].out_f32 = per != 1;
-    w[2].reverse = 1;
-    w[2].intra = w[2].update = s.scale, w[2].inter = 1.f;
-    set_plan(w[2], plan_v, take(seg_bytes(s, plan_v)));
-
-    if (launch_la_sweeps(w, 3, st) != cudaSuccess) return PARARNN_CUDA_ERROR;
+    if (!c.before(st) || launch_la_sweeps(c.w, 3, st) != cudaSuccess || !c.after(st)) return PARARNN_CUDA_ERROR;
     const long long n = static_cast<long long>(rows);
-    if (per != 1 && (launch_la_group_sum(part_k, dk, s.dtype, n, s.Hkv, per, s.dk, st) != cudaSuccess ||
-                     launch_la_group_sum(part_v, dv, s.dtype, n, s.Hkv, per, s.dv, st) != cudaSuccess))
+    const int per = s.H / s.Hkv;
+    if (per != 1 &&
+        (launch_la_group_sum(part.k, dk, s.dtype, n, s.Hkv, per, s.dk, c.w[1].out_w, st) != cudaSuccess ||
+         launch_la_group_sum(part.v, dv, s.dtype, n, s.Hkv, per, s.dv, c.w[2].out_w, st) != cudaSuccess))
         return PARARNN_CUDA_ERROR;
     return PARARNN_OK;
 }

@@ -1,6 +1,6 @@
-// linear_attention.cu -- linear attention with a decay for each head on CUDA cores (sm_100a): the sweep of
-// linear_attention.cuh in fp32, the join of time segments, the sum over heads that share keys and values, and
-// the single-token step.
+// linear_attention.cu -- linear attention with a decay for each head (sm_100a): the sweep of
+// linear_attention.cuh for fp32 operands on CUDA cores, the join of time segments, the sum over heads that share
+// keys and values, packing for rows that TMA cannot read, and the single-token step.
 #include <cuda_bf16.h>
 
 #include "linear_attention.cuh"
@@ -17,21 +17,11 @@ __device__ __forceinline__ float from_f<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16(x); }
 
-// Four consecutive elements as fp32; VEC needs 4-element alignment.
+// Four consecutive elements, n of which exist; VEC: all four, aligned to 16 bytes.
 template <bool VEC>
 __device__ __forceinline__ float4 load4(const float *p, int n) {
     if (VEC) return *reinterpret_cast<const float4 *>(p);
     return make_float4(n > 0 ? p[0] : 0.f, n > 1 ? p[1] : 0.f, n > 2 ? p[2] : 0.f, n > 3 ? p[3] : 0.f);
-}
-template <bool VEC>
-__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p, int n) {
-    if (VEC) {
-        const uint2 u = *reinterpret_cast<const uint2 *>(p);
-        return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
-                           __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
-    }
-    return make_float4(n > 0 ? to_f(p[0]) : 0.f, n > 1 ? to_f(p[1]) : 0.f, n > 2 ? to_f(p[2]) : 0.f,
-                       n > 3 ? to_f(p[3]) : 0.f);
 }
 
 // log g, kept finite: exp(n * -1e4) is 0 for every n >= 1 and 1 for n = 0, as g = 0 wants it.
@@ -65,7 +55,7 @@ __device__ __forceinline__ void fma4(float4 &acc, float x, const float4 &y) {
 
 // One CTA: 64 columns of c of one head and one segment, chunk after chunk, the state in shared memory.
 // STATE_ONLY is pass 1 of a split sweep: the segment's own S_out, without a and without outputs.
-template <typename TI, typename TO, bool VEC, int DKP, bool STATE_ONLY>
+template <bool VEC, int DKP, bool STATE_ONLY>
 __global__ void __launch_bounds__(kThr) la_simt_kernel(const LaSweep w) {
     constexpr int PK = DKP + 4, PV = kDVT + 4, PP = kC + 4;
     extern __shared__ __align__(16) float sm[];
@@ -77,9 +67,11 @@ __global__ void __launch_bounds__(kThr) la_simt_kernel(const LaSweep w) {
     const int bh = blockIdx.x / n_tile, c0 = (blockIdx.x % n_tile) * kDVT;
     const int b = bh / w.H, h = bh % w.H, sg = blockIdx.y;
     const int L = row_count(w, b);
-    const long long r_lo = static_cast<long long>(sg) * w.seg;
-    const int lo = r_lo < L ? static_cast<int>(r_lo) : L;
-    const int hi = r_lo + w.seg < L ? static_cast<int>(r_lo + w.seg) : L;
+    if (STATE_ONLY && sg == (w.reverse ? 0 : w.n_seg - 1)) return;  // nobody starts from its state
+    // tokens [t_lo, t_hi) of this segment as logical rows [lo, hi)
+    const long long t_lo = static_cast<long long>(sg) * w.seg;
+    const int lo_t = t_lo < L ? static_cast<int>(t_lo) : L, hi_t = t_lo + w.seg < L ? static_cast<int>(t_lo + w.seg) : L;
+    const int lo = w.reverse ? L - hi_t : lo_t, hi = w.reverse ? L - lo_t : hi_t;
     const int ncol = min(kDVT, w.dv - c0);
     const float ld = safe_log_decay(w.log_decay[h]);
     for (int i = tid; i <= kC; i += kThr) pw[i] = decay_pow(ld, i);
@@ -99,11 +91,11 @@ __global__ void __launch_bounds__(kThr) la_simt_kernel(const LaSweep w) {
         Ss[d * PV + c] = x;
     }
 
-    const TI *pa = static_cast<const TI *>(w.a.p) + b * w.a.sb + (h / w.a.group) * w.a.sh;
-    const TI *pb = static_cast<const TI *>(w.b.p) + b * w.b.sb + (h / w.b.group) * w.b.sh;
-    const TI *pc = static_cast<const TI *>(w.c.p) + b * w.c.sb + (h / w.c.group) * w.c.sh + c0;
-    TO *po = static_cast<TO *>(w.out) + (static_cast<long long>(b) * w.T * w.H + h) * w.dv + c0;
-    const long long ost = static_cast<long long>(w.H) * w.dv;
+    const float *pa = static_cast<const float *>(w.a.p) + b * w.a.sb + (h / w.a.group) * w.a.sh;
+    const float *pb = static_cast<const float *>(w.b.p) + b * w.b.sb + (h / w.b.group) * w.b.sh;
+    const float *pc = static_cast<const float *>(w.c.p) + b * w.c.sb + (h / w.c.group) * w.c.sh + c0;
+    float *po = static_cast<float *>(w.out) + (static_cast<long long>(b) * w.T * w.H + h) * w.out_w + c0;
+    const long long ost = static_cast<long long>(w.H) * w.out_w;
 
     for (int r0 = lo; r0 < hi; r0 += kC) {
         const int n = min(kC, hi - r0);
@@ -203,11 +195,11 @@ __global__ void __launch_bounds__(kThr) la_simt_kernel(const LaSweep w) {
                     for (int u = 0; u < 4; ++u)
                         if (i0 + u < n) {
                             const long long t = w.reverse ? L - 1 - (r0 + i0 + u) : r0 + i0 + u;
-                            TO *o = po + t * ost + j0;
+                            float *o = po + t * ost + j0;
                             const float f[4] = {acc[u].x, acc[u].y, acc[u].z, acc[u].w};
 #pragma unroll
                             for (int q = 0; q < 4; ++q)
-                                if (j0 + q < ncol) o[q] = from_f<TO>(f[q]);
+                                if (j0 + q < ncol) o[q] = f[q];
                         }
                 }
             }
@@ -256,7 +248,7 @@ __global__ void __launch_bounds__(kThr) la_simt_kernel(const LaSweep w) {
         }
         return;
     }
-    const int last = L > 0 ? (L - 1) / w.seg : 0;  // the segment that holds the last row
+    const int last = L > 0 && !w.reverse ? (L - 1) / w.seg : 0;  // the segment that holds the last logical row
     if (w.s_out != nullptr && sg == last)
         for (int i = tid; i < w.dk * ncol; i += kThr) {
             const int d = w.s_j == 1 ? i / ncol : i % w.dk, c = w.s_j == 1 ? i % ncol : i / w.dk;
@@ -264,9 +256,9 @@ __global__ void __launch_bounds__(kThr) la_simt_kernel(const LaSweep w) {
                 Ss[d * PV + c];
         }
     // outputs behind the sequence's length are zero
-    const long long t_hi = r_lo + w.seg < w.T ? r_lo + w.seg : w.T;
-    for (long long t = (r_lo > L ? r_lo : L); t < t_hi; ++t)
-        for (int c = tid; c < ncol; c += kThr) po[t * ost + c] = from_f<TO>(0.f);
+    const long long z_hi = t_lo + w.seg < w.T ? t_lo + w.seg : w.T;
+    for (long long t = (t_lo > L ? t_lo : L); t < z_hi; ++t)
+        for (int c = tid; c < ncol; c += kThr) po[t * ost + c] = 0.f;
 }
 
 // Join of a split sweep, in place: seg_state[s] (segment s's own state) becomes the state segment s starts from.
@@ -277,15 +269,16 @@ __global__ void la_join_kernel(const LaSweep w) {
     const long long i = static_cast<long long>(blockIdx.x % per) * blockDim.x + threadIdx.x;
     if (i >= n) return;
     const float ld = safe_log_decay(w.log_decay[bh % w.H]);
-    const float g = decay_pow(ld, w.seg);
     const int L = row_count(w, bh / w.H);
     float *p = w.seg_state + static_cast<long long>(bh) * w.n_seg * n + i;
     float s = w.s_in == nullptr ? 0.f : w.s_in[bh * n + (i / w.dv) * w.s_i + (i % w.dv) * w.s_j];
-    for (int q = 0; q < w.n_seg; ++q) {
-        const float own = q + 1 < w.n_seg ? p[q * n] : 0.f;
+    const float g_full = decay_pow(ld, w.seg);
+    for (int k = 0; k < w.n_seg; ++k) {
+        const int q = w.reverse ? w.n_seg - 1 - k : k;
+        const float own = k + 1 < w.n_seg ? p[q * n] : 0.f;
         p[q * n] = s;
-        // a segment with a next one that holds rows is full
-        if ((q + 1ll) * w.seg < L) s = fmaf(g, s, own);
+        const long long rows = L - static_cast<long long>(q) * w.seg;  // of this segment, if not full
+        if (rows > 0) s = fmaf(rows >= w.seg ? g_full : decay_pow(ld, rows), s, own);
     }
 }
 
@@ -298,54 +291,50 @@ cudaError_t launch_la_join(const LaSweep &w, cudaStream_t s) {
 
 namespace {
 
-template <typename TI, typename TO, bool VEC, int DKP>
+template <bool VEC, int DKP>
 cudaError_t launch_simt(const LaSweep &w, cudaStream_t s) {
     const int smem = simt_smem_floats<DKP>() * 4;
     const dim3 grid(static_cast<unsigned>(w.B) * w.H * ((w.dv + kDVT - 1) / kDVT), w.n_seg);
     cudaError_t e;
     if (w.n_seg > 1) {
-        auto k1 = la_simt_kernel<TI, TO, VEC, DKP, true>;
+        auto k1 = la_simt_kernel<VEC, DKP, true>;
         if ((e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
-        k1<<<dim3(grid.x, w.n_seg - 1), kThr, smem, s>>>(w);  // the last segment's own state is not needed
+        k1<<<grid, kThr, smem, s>>>(w);
         if ((e = launch_la_join(w, s)) != cudaSuccess) return e;
     }
-    auto k = la_simt_kernel<TI, TO, VEC, DKP, false>;
+    auto k = la_simt_kernel<VEC, DKP, false>;
     if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
     k<<<grid, kThr, smem, s>>>(w);
     return cudaGetLastError();
 }
 
-template <typename TI, typename TO, bool VEC>
+template <bool VEC>
 cudaError_t pick_width(const LaSweep &w, cudaStream_t s) {
-    if (w.dk <= 32) return launch_simt<TI, TO, VEC, 32>(w, s);
-    if (w.dk <= 64) return launch_simt<TI, TO, VEC, 64>(w, s);
-    return launch_simt<TI, TO, VEC, 128>(w, s);
+    if (w.dk <= 32) return launch_simt<VEC, 32>(w, s);
+    if (w.dk <= 64) return launch_simt<VEC, 64>(w, s);
+    return launch_simt<VEC, 128>(w, s);
 }
 
-bool rows_vec4(const LaRows &x, size_t esize) {
-    return reinterpret_cast<uintptr_t>(x.p) % (4 * esize) == 0 && x.sb % 4 == 0 && x.st % 4 == 0 && x.sh % 4 == 0;
+bool rows_vec4(const LaRows &x) {
+    return reinterpret_cast<uintptr_t>(x.p) % 16 == 0 && x.sb % 4 == 0 && x.st % 4 == 0 && x.sh % 4 == 0;
 }
 
-template <typename TI, typename TO>
-cudaError_t pick_vec(const LaSweep &w, cudaStream_t s) {
-    const bool vec = w.dk % 4 == 0 && w.dv % 4 == 0 && rows_vec4(w.a, sizeof(TI)) && rows_vec4(w.b, sizeof(TI)) &&
-                     rows_vec4(w.c, sizeof(TI));
-    return vec ? pick_width<TI, TO, true>(w, s) : pick_width<TI, TO, false>(w, s);
+cudaError_t launch_simt_any(const LaSweep &w, cudaStream_t s) {
+    const bool vec = w.dk % 4 == 0 && w.dv % 4 == 0 && rows_vec4(w.a) && rows_vec4(w.b) && rows_vec4(w.c);
+    return vec ? pick_width<true>(w, s) : pick_width<false>(w, s);
 }
 
 }  // namespace
 
-namespace {
-bool use_tc(int T, int dtype) { return dtype == PARARNN_BF16 && T >= 64; }
-}  // namespace
-
-LaPlan la_plan(int B, int T, int H, int, int dv, int dtype) {
-    const long long heads = static_cast<long long>(B) * H;
+LaPlan la_plan(int B, int T, int H, int dv, int dtype, int sweeps) {
+    const long long heads = static_cast<long long>(B) * H * sweeps;
     long long want, most;
     int unit;
-    if (use_tc(T, dtype)) {
-        // one CTA per SM: as many segments as fill the 148 SMs once, of at least 4 chunks of 128 rows
+    if (dtype == PARARNN_BF16) {
+        // one CTA per SM: as many segments as fill the 148 SMs once, of at least 4 chunks of 128 rows.  Two segments
+        // are no gain: pass 1 costs about 0.6 of pass 2, so half the length is run 1.6 times.
         want = 148 / heads;
+        if (want < 3) want = 1;
         most = T / 512;
         unit = 128;
     } else {
@@ -363,21 +352,15 @@ LaPlan la_plan(int B, int T, int H, int, int dv, int dtype) {
     return {(T + seg - 1) / seg, seg};
 }
 
-size_t la_seg_bytes(const LaSweep &w) {
-    return w.n_seg > 1 ? static_cast<size_t>(w.B) * w.H * w.n_seg * w.dk * w.dv * sizeof(float) : 0;
-}
-
 cudaError_t launch_la_sweeps(const LaSweep *w, int n, cudaStream_t s) {
     for (int i = 0; i < n;) {
-        cudaError_t e;
         int k = 1;
-        if (use_tc(w[i].T, w[i].dtype)) {
+        cudaError_t e;
+        if (w[i].dtype == PARARNN_BF16) {
             while (i + k < n && la_tc_together(w[i], w[i + k])) ++k;
             e = launch_la_tc(w + i, k, s);
-        } else if (w[i].dtype == PARARNN_F32) {
-            e = pick_vec<float, float>(w[i], s);
         } else {
-            e = w[i].out_f32 ? pick_vec<__nv_bfloat16, float>(w[i], s) : pick_vec<__nv_bfloat16, __nv_bfloat16>(w[i], s);
+            e = launch_simt_any(w[i], s);
         }
         if (e != cudaSuccess) return e;
         i += k;
@@ -385,22 +368,77 @@ cudaError_t launch_la_sweeps(const LaSweep *w, int n, cudaStream_t s) {
     return cudaSuccess;
 }
 
+// ---- packing ------------------------------------------------------------------------------------------------
+
+namespace {
+
+// bf16 rows from and to a dense [B, T, heads, wp] (wp: width rounded up to 8), 8 columns per thread
+__global__ void la_pack_kernel(const LaRows src, uint4 *__restrict__ dst, int T, int heads, int width, int wp,
+                               long long n) {
+    for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
+         i += static_cast<long long>(gridDim.x) * blockDim.x) {
+        const int c = static_cast<int>(i % (wp / 8)) * 8;
+        const long long row = i / (wp / 8);
+        const int h = static_cast<int>(row % heads);
+        const long long t = row / heads % T, b = row / heads / T;
+        const unsigned short *p =
+            static_cast<const unsigned short *>(src.p) + b * src.sb + t * src.st + h * src.sh + c;
+        unsigned u[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (c + k < width) u[k >> 1] |= static_cast<unsigned>(p[k]) << (16 * (k & 1));
+        dst[i] = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+}
+__global__ void la_unpack_kernel(const uint4 *__restrict__ src, unsigned short *__restrict__ dst, int width, int wp,
+                                 long long n) {
+    for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
+         i += static_cast<long long>(gridDim.x) * blockDim.x) {
+        const int c = static_cast<int>(i % (wp / 8)) * 8;
+        unsigned short *p = dst + i / (wp / 8) * width + c;
+        const uint4 x = src[i];
+        const unsigned u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (c + k < width) p[k] = static_cast<unsigned short>(u[k >> 1] >> (16 * (k & 1)));
+    }
+}
+unsigned pack_grid(long long n) { return static_cast<unsigned>(n / 256 + 1 < 148 * 16 ? n / 256 + 1 : 148 * 16); }
+
+}  // namespace
+
+cudaError_t launch_la_pack(const LaRows &src, void *dst, int B, int T, int heads, int width, cudaStream_t s) {
+    const int wp = (width + 7) / 8 * 8;
+    const long long n = static_cast<long long>(B) * T * heads * (wp / 8);
+    la_pack_kernel<<<pack_grid(n), 256, 0, s>>>(src, static_cast<uint4 *>(dst), T, heads, width, wp, n);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_la_unpack(const void *src, void *dst, long long rows, int width, cudaStream_t s) {
+    const int wp = (width + 7) / 8 * 8;
+    const long long n = rows * (wp / 8);
+    la_unpack_kernel<<<pack_grid(n), 256, 0, s>>>(static_cast<const uint4 *>(src), static_cast<unsigned short *>(dst), width,
+                                                  wp, n);
+    return cudaGetLastError();
+}
+
 // ---- sums over the heads that share a key/value head --------------------------------------------------------
 
 namespace {
 
-// out[row, u, :] = sum over the `per` heads of group u of part[row, u * per + i, :], in head order
+// out[row, u, :d] = sum over the `per` heads of group u of part[row, u * per + i, :d], in head order; rows of part are
+// dp wide
 template <typename TO>
 __global__ void la_group_sum_kernel(const float *__restrict__ part, TO *__restrict__ out, long long rows, int Hkv,
-                                    int per, int d) {
+                                    int per, int d, int dp) {
     const long long n = rows * Hkv * d;
     for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
          i += static_cast<long long>(gridDim.x) * blockDim.x) {
         const long long ru = i / d;  // row * Hkv + u
         const int c = static_cast<int>(i % d);
-        const float *p = part + ru * per * d + c;
+        const float *p = part + ru * per * dp + c;
         float s = 0.f;
-        for (int q = 0; q < per; ++q) s += p[static_cast<long long>(q) * d];
+        for (int q = 0; q < per; ++q) s += p[static_cast<long long>(q) * dp];
         out[i] = from_f<TO>(s);
     }
 }
@@ -408,13 +446,13 @@ __global__ void la_group_sum_kernel(const float *__restrict__ part, TO *__restri
 }  // namespace
 
 cudaError_t launch_la_group_sum(const float *part, void *out, int dtype, long long rows, int Hkv, int per, int d,
-                                cudaStream_t s) {
+                                int dp, cudaStream_t s) {
     const long long n = rows * Hkv * d;
     const unsigned grid = static_cast<unsigned>(n / 256 + 1 < 148 * 16 ? n / 256 + 1 : 148 * 16);
     if (dtype == PARARNN_F32)
-        la_group_sum_kernel<<<grid, 256, 0, s>>>(part, static_cast<float *>(out), rows, Hkv, per, d);
+        la_group_sum_kernel<<<grid, 256, 0, s>>>(part, static_cast<float *>(out), rows, Hkv, per, d, dp);
     else
-        la_group_sum_kernel<<<grid, 256, 0, s>>>(part, static_cast<__nv_bfloat16 *>(out), rows, Hkv, per, d);
+        la_group_sum_kernel<<<grid, 256, 0, s>>>(part, static_cast<__nv_bfloat16 *>(out), rows, Hkv, per, d, dp);
     return cudaGetLastError();
 }
 

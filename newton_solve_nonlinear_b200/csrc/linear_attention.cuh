@@ -36,11 +36,11 @@ struct LaSweep {
     const float *s_in;       // [B, H, .] or null (zero); element (i, j) at i * s_i + j * s_j
     float *s_out;            // or null
     int s_i, s_j;
-    void *out;  // dense [B, T, H, dv]
-    int out_f32;
+    void *out;  // dense [B, T, H, out_w], out_w >= dv (bf16 sweeps: a multiple of 8)
+    int out_w, out_f32;
     int reverse, e;
     float intra, inter, update;
-    int n_seg, seg;  // segments of `seg` rows each (n_seg = 1: the whole sequence)
+    int n_seg, seg;  // segments of `seg` tokens each (n_seg = 1: the whole sequence)
     float *seg_state;  // [B*H, n_seg, dk, dv]: pass 1 writes each segment's own S_out, the join its S_in
 };
 
@@ -49,8 +49,7 @@ struct LaSweep {
 struct LaPlan {
     int n_seg, seg;
 };
-size_t la_seg_bytes(const LaSweep &w);
-LaPlan la_plan(int B, int T, int H, int dk, int dv, int dtype);
+LaPlan la_plan(int B, int T, int H, int dv, int dtype, int sweeps);  // `sweeps` of them run at once
 
 // n <= 3 independent sweeps; those that can share a launch do.
 cudaError_t launch_la_sweeps(const LaSweep *w, int n, cudaStream_t s);
@@ -58,10 +57,16 @@ cudaError_t launch_la_sweeps(const LaSweep *w, int n, cudaStream_t s);
 // bf16 operands on tensor cores: n <= 3 sweeps in one launch, every one of which goes together with the first
 cudaError_t launch_la_tc(const LaSweep *w, int n, cudaStream_t s);
 bool la_tc_together(const LaSweep &x, const LaSweep &y);
+// whether TMA can read the operand: base and strides on 16 bytes, no axis of stride 0
+bool la_tc_readable(const LaRows &r, int B, int T, int heads);
+// bf16 rows to and from a dense [B, T, heads, width rounded up to 8]
+cudaError_t launch_la_pack(const LaRows &src, void *dst, int B, int T, int heads, int width, cudaStream_t s);
+cudaError_t launch_la_unpack(const void *src, void *dst, long long rows, int width, cudaStream_t s);
+
 cudaError_t launch_la_join(const LaSweep &w, cudaStream_t s);  // segments' own states -> their start states
 
 cudaError_t launch_la_group_sum(const float *part, void *out, int dtype, long long rows, int Hkv, int per, int d,
-                                cudaStream_t s);
+                                int dp, cudaStream_t s);
 
 // The single-token step; state row `slots[b]` (or b) of [n_slots, H, dk, dv] belongs to row b.
 struct LaStep {

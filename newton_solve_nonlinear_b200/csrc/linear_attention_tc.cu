@@ -11,8 +11,9 @@
 // copy, each 2^-9 relative as the output's own.  The weighted c is split into three bf16 terms (24 bits), so the
 // state's products are exact to fp32; they are summed smallest term first.
 //
-// Tiles stand in shared memory in the order of the tokens.  A reversed sweep (logical row i = tile row 127 - x)
-// only mirrors the weights, so tiles come and go by TMA either way.
+// Tiles are of 128 consecutive tokens from a multiple of 128 on, in the order of the tokens.  A reversed sweep
+// takes them from the last one down and mirrors the weights (logical row = n - 1 - tile row), so tiles come and go
+// by TMA either way, and only the tile with the sequence's end is not full.
 //
 // Warps: 0-7 output (lane quarter = rows, two halves of the columns: weigh the scores, scale, stage for the TMA
 // store), 8-15 state (lane quarter = columns of c; two halves of the rows to be split and of b's width), 16
@@ -66,7 +67,6 @@ static_assert(sizeof(Bars) <= 160, "barriers");
 struct TcSweep {
     LaSweep w;
     CUtensorMap a, b, c, out;
-    int tma_in, tma_out;  // the operands / the outputs can be moved by TMA
 };
 struct TcBatch {
     TcSweep s[3];
@@ -223,52 +223,11 @@ __device__ __forceinline__ void tma_store_4d(const CUtensorMap *map, int x, int 
                  : "memory");
 }
 
-// One tile by one warp, for operands that TMA cannot read: tile row x is token t0 + x; rows outside [x_lo, x_hi) and
-// columns >= width are zero.
-template <int PANELS>
-__device__ __forceinline__ void copy_tile(unsigned dst, const __nv_bfloat16 *src, long long st, long long t0, int x_lo,
-                                          int x_hi, int width, int lane) {
-    constexpr int CH = PANELS * 8;
-    const int c = lane % CH, room = width - c * 8;
-#pragma unroll 2
-    for (int x = lane / CH; x < kC; x += 32 / CH) {
-        unsigned u[4] = {0u, 0u, 0u, 0u};
-        if (x >= x_lo && x < x_hi) {
-            const unsigned short *q = reinterpret_cast<const unsigned short *>(src + (t0 + x) * st + c * 8);
+// 32 columns of one output row of a padded width (a multiple of 8).
+__device__ __forceinline__ void store32(float *p, const float (&v)[32], int room) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < room) u[i >> 1] |= static_cast<unsigned>(q[i]) << (16 * (i & 1));
-        }
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (c >> 3) * kPanel + x * 128 +
-                                                                      (((c & 7) ^ (x & 7)) << 4)),
-                     "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3])
-                     : "memory");
-    }
-}
-
-// 32 columns of one output row, `room` of which exist.
-__device__ __forceinline__ void store_few(void *p, bool f32, float4 x, int room) {
-    const float v[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (i >= room) break;
-        if (f32) static_cast<float *>(p)[i] = v[i];
-        else static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16(v[i]);
-    }
-}
-__device__ __forceinline__ void store32(void *out, long long at, bool f32, const float (&v)[32], int room, bool vec) {
-    float *pf = static_cast<float *>(out) + at;
-    __nv_bfloat16 *pb = static_cast<__nv_bfloat16 *>(out) + at;
-#pragma unroll
-    for (int i = 0; i < 32; i += 4) {
-        const float4 x = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-        if (vec && room >= i + 4) {
-            if (f32) *reinterpret_cast<float4 *>(pf + i) = x;
-            else *reinterpret_cast<uint2 *>(pb + i) = make_uint2(pack(x.x, x.y), pack(x.z, x.w));
-        } else if (room > i) {
-            store_few(f32 ? static_cast<void *>(pf + i) : static_cast<void *>(pb + i), f32, x, room - i);
-        }
-    }
+    for (int i = 0; i < 32; i += 4)
+        if (i < room) *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
 }
 
 template <int DK, int DV, bool STATE_ONLY>
@@ -283,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
     // weight of the score (row x, column y), intra g^|x - y| or 0, at sw[y - x]: of y - x in -127 .. 32 forward, in
     // -32 .. 127 reversed, as far as any block needs it
     float *sw = reinterpret_cast<float *>(smem + Y::TAB);
-    float *cw = sw + 160;  // [2][128]: update g^(n - e - j) of tile row x, for a full chunk and for the last one
+    float *cw = sw + 160;  // [2][128]: update g^(n - e - j) of tile row x, for a full tile and for the last one
     Bars *bars = reinterpret_cast<Bars *>(smem + Y::BARS);
     volatile int *err = &bars->err;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -293,20 +252,24 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
     const int b = bh / w.H, h = bh % w.H, sg = blockIdx.y;
     int L = w.T;
     if (w.lengths != nullptr) L = min(max(w.lengths[b], 0), w.T);
-    const long long r_lo = static_cast<long long>(sg) * w.seg;
-    const int lo = r_lo < L ? static_cast<int>(r_lo) : L;
-    const int hi = r_lo + w.seg < L ? static_cast<int>(r_lo + w.seg) : L;
+    // tokens [lo, hi) of this segment; the tile with hi has n_part rows
+    const long long t_lo = static_cast<long long>(sg) * w.seg;
+    const int lo = t_lo < L ? static_cast<int>(t_lo) : L;
+    const int hi = t_lo + w.seg < L ? static_cast<int>(t_lo + w.seg) : L;
     const int chunks = (hi - lo + kC - 1) / kC;
-    const int n_last = hi - lo - (chunks - 1) * kC;
+    const int n_part = hi - lo - (chunks - 1) * kC;
     const int ncol = min(DV, w.dv - c0);
     const bool rev = w.reverse != 0;
     const int e = w.e;
+    const int part_chunk = rev ? 0 : chunks - 1;
+    const bool unclean = chunks > 0 && n_part < kC;  // rows to be cleared: behind the sequence's end
     // exp(n * -1e4) is 0 for n >= 1 and 1 for n = 0, as g = 0 wants it
     const float ld = fmaxf(w.log_decay[h], -1e4f);
     auto power = [&](int n) { return expf(static_cast<float>(static_cast<double>(ld) * n)); };
     // first token of chunk c's tile
-    auto first_token = [&](int c) { return rev ? L - kC - (lo + c * kC) : lo + c * kC; };
+    auto first_token = [&](int c) { return lo + (rev ? chunks - 1 - c : c) * kC; };
 
+    if (STATE_ONLY && sg == (rev ? 0 : w.n_seg - 1)) return;
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&bars->full[s]), STATE_ONLY ? 1 : 2);
@@ -335,8 +298,8 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         const int x = rev ? tid - 32 : 127 - tid;  // row distance, counted towards the past
         sw[tid] = x >= 0 ? power(x) * w.intra : 0.f;
     } else if (tid < 160 + 256) {
-        const int x = (tid - 160) & 127, n = tid - 160 < 128 ? kC : n_last, j = rev ? kC - 1 - x : x;
-        cw[tid - 160] = j < n ? power(n - e - j) * w.update : 0.f;
+        const int x = (tid - 160) & 127, n = tid - 160 < 128 ? kC : n_part, j = rev ? n - 1 - x : x;
+        cw[tid - 160] = x < n ? power(n - e - j) * w.update : 0.f;
     }
     fence_before();
     __syncthreads();
@@ -348,16 +311,19 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         regs_down<kRegsOut>();
         if (!STATE_ONLY) {
             const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;
-            const int i = rev ? kC - 1 - row : row;  // logical row
             const unsigned tl = tm + (static_cast<unsigned>(quarter * 32) << 16);
-            const float f = power(i + e) * w.inter;
-            const long long po = (static_cast<long long>(b) * w.T * w.H + h) * w.dv + c0;
-            const long long ost = static_cast<long long>(w.H) * w.dv;
-            const bool vec = w.dv % 8 == 0, tma_out = sweep.tma_out != 0, out_f32 = w.out_f32 != 0;
-            void *const out = w.out;
+            auto row_factor = [&](int n) { return power((rev ? n - 1 - row : row) + e) * w.inter; };
+            const float f_full = row_factor(kC), f_part = row < n_part ? row_factor(n_part) : 0.f;
+            // fp32 outputs (partial gradients): dense rows of w.out_w columns
+            const long long ost = static_cast<long long>(w.H) * w.out_w;
+            float *const pf = w.out_f32 ? static_cast<float *>(w.out) +
+                                              (static_cast<long long>(b) * w.T * w.H + h) * w.out_w + c0 + row * ost
+                                        : nullptr;
+            const int room = w.out_w - c0;
             for (int c = 0; c < chunks; ++c) {
                 const unsigned ph = c & 1;
-                const int n = c + 1 < chunks ? kC : n_last;
+                const bool full = c != part_chunk;
+                const float f = full ? f_full : f_part;
                 if (!mbar_wait(smem_u32(&bars->scores), ph, err)) break;
                 fence_after();
 #pragma unroll 1
@@ -392,10 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                 if (lane == 0) arrive(smem_u32(&bars->scaled));
                 if (!mbar_wait(smem_u32(&bars->out), ph, err)) break;
                 fence_after();
-                const long long t = first_token(c) + row;
-                const bool live = i < n;
-                // a tile that starts before the first token cannot be stored by TMA
-                const bool stage = tma_out && first_token(c) >= 0;
+                const bool live = full || row < n_part;
 #pragma unroll 1
                 for (int cb = half * (DV / 2); cb < (half + 1) * (DV / 2); cb += 32) {
                     float v[32];
@@ -405,7 +368,9 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                         __syncwarp();
                         if (lane == 0) arrive(smem_u32(&bars->out_read));
                     }
-                    if (stage) {
+                    if (pf != nullptr) {
+                        if (live) store32(pf + first_token(c) * ost + cb, v, room - cb);
+                    } else {
                         if (!live) {
 #pragma unroll
                             for (int q = 0; q < 32; ++q) v[q] = 0.f;
@@ -421,8 +386,6 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                                          "r"(u[2]), "r"(u[3])
                                          : "memory");
                         }
-                    } else if (live && cb < ncol) {
-                        store32(out, po + t * ost + cb, out_f32, v, ncol - cb, vec);
                     }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -472,16 +435,15 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             // ldmatrix: lane l names row l % 8 of matrix l / 8; matrices are (8 tokens) x (8 columns of c), columns
             // first, then tokens
             const int m_row = half * 64 + ((lane >> 4) << 3) + (lane & 7);
-            const float g_full = power(kC), g_last = power(n_last);
+            const float g_full = power(kC), g_part = power(n_part);
             for (int c = 0; c < chunks; ++c) {
                 const int st = c & 1;
                 const unsigned ph = c & 1;
-                const bool last = c + 1 == chunks;
-                const int n = last ? n_last : kC;
+                const bool part = c == part_chunk;
                 const unsigned tile_b = sm + st * Y::STAGE + Y::B, tile_c = sm + st * Y::STAGE + Y::C;
                 if (!mbar_wait(smem_u32(&bars->full[st]), (c >> 1) & 1, err)) break;
-                if (!rev && n < kC) {  // tokens behind the sequence's length: this warp's share of c, and of b
-                    for (int x = max(n, half * 64) + (lane >> 2); x < half * 64 + 64; x += 8) {
+                if (part && unclean) {  // tokens behind the sequence's end: this warp's share of c, and of b
+                    for (int x = max(n_part, half * 64) + (lane >> 2); x < half * 64 + 64; x += 8) {
                         const int ch = (quarter & 1) * 4 + (lane & 3);
                         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
                                          tile_c + (quarter >> 1) * kPanel + x * 128 + ((ch ^ (x & 7)) << 4)),
@@ -489,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                                      : "memory");
                     }
                     const int me = half * (DV / 32) + quarter;
-                    for (int x = n + me; x < kC; x += Y::STATE_WARPS)
+                    for (int x = n_part + me; x < kC; x += Y::STATE_WARPS)
                         if (lane < DK / 8)
                             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
                                              tile_b + (lane >> 3) * kPanel + x * 128 + (((lane & 7) ^ (x & 7)) << 4)),
@@ -498,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                 }
-                const float *cwt = cw + (last ? 128 : 0) + half * 64 + 2 * (lane & 3);
+                const float *cwt = cw + (part ? 128 : 0) + half * 64 + 2 * (lane & 3);
                 const unsigned ta = tl + Y::T_V + half * 32;
                 // 16 columns of c (sub), 64 tokens; registers k, k + 1: the same 8 tokens, columns lane / 4 and + 8
                 auto load_c = [&](int sub, unsigned (&u)[16]) {
@@ -550,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                 fence_before();
                 __syncwarp();
                 if (lane == 0) arrive(smem_u32(&bars->v_high));
-                const float gn = last ? g_last : g_full;
+                const float gn = part ? g_part : g_full;
                 if (!mbar_wait(smem_u32(&bars->ds), ph, err)) break;
                 fence_after();
 #pragma unroll
@@ -564,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                 if (!STATE_ONLY) publish();
             }
             // the last state: the segment's own (pass 1) or the sequence's
-            const int last_seg = L > 0 ? (L - 1) / w.seg : 0;
+            const int last_seg = L > 0 && !rev ? (L - 1) / w.seg : 0;
             float *p = nullptr;
             int si = w.dv;
             if (STATE_ONLY) {
@@ -605,10 +567,9 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             for (int k = 0; k < kC / 16; ++k)
                 mma_ts(tu + Y::T_D, tu + Y::T_V + place * 64 + k * 8, nmajor_desc(tb + k * 2048), id_ds, !first || k > 0, on);
         };
-        // rows behind the sequence's length, which the state warps clear before v
-        const bool unclean = !rev && n_last < kC;
+        // a tile whose rows the state warps clear is clean once they have arrived at v
         if (chunks > 0 && mbar_wait(smem_u32(&bars->full[0]), 0, err) &&
-            !(chunks == 1 && unclean && !mbar_wait(smem_u32(&bars->v), 0, err))) {
+            !(part_chunk == 0 && unclean && !mbar_wait(smem_u32(&bars->v), 0, err))) {
             fence_after();
             if (!STATE_ONLY) scores(0);
             for (int c = 0; c < chunks; ++c) {
@@ -650,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                     if (!mbar_wait(smem_u32(&bars->full[st ^ 1]), ((c + 1) >> 1) & 1, err)) break;
                     if (!STATE_ONLY) {  // the next scores, as soon as the weighted ones have been used
                         if (!mbar_wait(smem_u32(&bars->out), ph, err)) break;
-                        if (c + 2 == chunks && unclean && !mbar_wait(smem_u32(&bars->v), ph ^ 1u, err)) break;
+                        if (c + 1 == part_chunk && unclean && !mbar_wait(smem_u32(&bars->v), ph ^ 1u, err)) break;
                         fence_after();
                         scores(c + 1);
                     }
@@ -668,41 +629,27 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         }
     } else if (warp == 17) {
         // ---- tiles in, staged outputs out
-        const bool tma_in = sweep.tma_in != 0, tma_out = sweep.tma_out != 0;
         const int ha = h / w.a.group, hb = h / w.b.group, hc = h / w.c.group;
-        auto head_of = [&](const LaRows &r, int hr) { return static_cast<const __nv_bfloat16 *>(r.p) + b * r.sb + hr * r.sh; };
+        const bool f32 = w.out_f32 != 0;
         // first b and c, then a, whose place the staged outputs may hold longer
         auto load = [&](int c, bool first) {
-            const int st = c & 1, t0 = first_token(c), n = c + 1 < chunks ? kC : n_last;
+            const int st = c & 1, t0 = first_token(c);
             const unsigned base = sm + st * Y::STAGE, full = smem_u32(&bars->full[st]);
-            if (tma_in) {
-                if (elect_one()) {
-                    if (first) {
-                        mbar_expect_tx(full, (DK / 64 + DV / 64) * kPanel);
-#pragma unroll
-                        for (int x = 0; x < DV / 64; ++x)
-                            tma_load_4d(base + Y::C + x * kPanel, &sweep.c, c0 + x * 64, t0, hc, b, full);
-#pragma unroll
-                        for (int x = 0; x < DK / 64; ++x)
-                            tma_load_4d(base + Y::B + x * kPanel, &sweep.b, x * 64, t0, hb, b, full);
-                    } else {
-                        mbar_expect_tx(full, DK / 64 * kPanel);
-#pragma unroll
-                        for (int x = 0; x < DK / 64; ++x)
-                            tma_load_4d(base + Y::A + x * kPanel, &sweep.a, x * 64, t0, ha, b, full);
-                    }
-                }
-            } else {
-                const int x_lo = rev ? kC - n : 0, x_hi = rev ? kC : n;
+            if (elect_one()) {
                 if (first) {
-                    copy_tile<DV / 64>(base + Y::C, head_of(w.c, hc) + c0, w.c.st, t0, x_lo, x_hi, ncol, lane);
-                    copy_tile<DK / 64>(base + Y::B, head_of(w.b, hb), w.b.st, t0, x_lo, x_hi, w.dk, lane);
+                    mbar_expect_tx(full, (DK / 64 + DV / 64) * kPanel);
+#pragma unroll
+                    for (int x = 0; x < DV / 64; ++x)
+                        tma_load_4d(base + Y::C + x * kPanel, &sweep.c, c0 + x * 64, t0, hc, b, full);
+#pragma unroll
+                    for (int x = 0; x < DK / 64; ++x)
+                        tma_load_4d(base + Y::B + x * kPanel, &sweep.b, x * 64, t0, hb, b, full);
                 } else {
-                    copy_tile<DK / 64>(base + Y::A, head_of(w.a, ha), w.a.st, t0, x_lo, x_hi, w.dk, lane);
+                    mbar_expect_tx(full, DK / 64 * kPanel);
+#pragma unroll
+                    for (int x = 0; x < DK / 64; ++x)
+                        tma_load_4d(base + Y::A + x * kPanel, &sweep.a, x * 64, t0, ha, b, full);
                 }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) arrive(full);
             }
             __syncwarp();
         };
@@ -717,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             if (STATE_ONLY) continue;
             if (c >= 0) {
                 if (!mbar_wait(smem_u32(&bars->staged[c & 1]), (c >> 1) & 1, err)) break;
-                if (tma_out && first_token(c) >= 0) {
+                if (!f32) {
                     if (elect_one()) {
 #pragma unroll
                         for (int x = 0; x < DV / 64; ++x)
@@ -733,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             }
             if (c + 2 < chunks) load(c + 2, false);
         }
-        if (*err && tma_in) {  // copies in flight land before the block ends
+        if (*err) {  // copies in flight land before the block ends
             for (int c = max(loaded - 2, 0); c < loaded; ++c) mbar_drain(smem_u32(&bars->full[c & 1]), (c >> 1) & 1);
         }
         asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -747,36 +694,31 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512));
     }
     if (!STATE_ONLY) {
-        const long long po = (static_cast<long long>(b) * w.T * w.H + h) * w.dv + c0;
-        const long long ost = static_cast<long long>(w.H) * w.dv;
+        const long long po = (static_cast<long long>(b) * w.T * w.H + h) * w.out_w + c0;
+        const long long ost = static_cast<long long>(w.H) * w.out_w;
         auto put = [&](long long at, float x) {
             if (w.out_f32) static_cast<float *>(w.out)[at] = x;
             else static_cast<__nv_bfloat16 *>(w.out)[at] = __float2bfloat16(x);
         };
         if (*err)  // a wait ran out: nothing of this segment is to be trusted
-            for (long long i = tid; i < static_cast<long long>(hi - lo) * ncol; i += kThreads) {
-                const long long r = lo + i / ncol, t = rev ? L - 1 - r : r;
-                put(po + t * ost + i % ncol, __int_as_float(0x7fc00000));
-            }
+            for (long long i = tid; i < static_cast<long long>(hi - lo) * ncol; i += kThreads)
+                put(po + (lo + i / ncol) * ost + i % ncol, __int_as_float(0x7fc00000));
         // outputs behind the sequence's length are zero
-        const long long t_lo = r_lo > L ? r_lo : L, t_hi = r_lo + w.seg < w.T ? r_lo + w.seg : w.T;
-        for (long long i = tid; i < (t_hi - t_lo) * ncol; i += kThreads)
-            put(po + (t_lo + i / ncol) * ost + i % ncol, 0.f);
+        const long long z_lo = t_lo > L ? t_lo : L, z_hi = t_lo + w.seg < w.T ? t_lo + w.seg : w.T;
+        for (long long i = tid; i < (z_hi - z_lo) * ncol; i += kThreads) put(po + (z_lo + i / ncol) * ost + i % ncol, 0.f);
     }
 }
 
-// A [B, T, heads, width] operand in boxes of 128 tokens x 64 columns; false where TMA cannot read it (base or a
-// stride off 16 bytes, an axis of stride 0).
+// A [B, T, heads, width] operand in boxes of 128 tokens x 64 columns.
 bool make_rows_map(CUtensorMap *m, const void *p, int B, int T, int heads, int width, long long sb, long long st,
                    long long sh) {
     EncodeTiledFn fn = encode_fn();
-    if (!fn || reinterpret_cast<uintptr_t>(p) % 16 != 0) return false;
+    if (!fn) return false;
     const long long n[3] = {T, heads, B};
     const long long s[3] = {st, sh, sb};
     cuuint64_t dims[4] = {static_cast<cuuint64_t>(width), 0, 0, 0}, strides[3];
     for (int i = 0; i < 3; ++i) {
         dims[i + 1] = static_cast<cuuint64_t>(n[i]);
-        if (n[i] > 1 && (s[i] == 0 || s[i] % 8 != 0 || s[i] >= (1ll << 38))) return false;
         strides[i] = n[i] > 1 ? static_cast<cuuint64_t>(s[i]) * 2 : 256;  // an axis of one entry is never stepped
     }
     const cuuint32_t box[4] = {64, kC, 1, 1}, one[4] = {1, 1, 1, 1};
@@ -785,16 +727,14 @@ bool make_rows_map(CUtensorMap *m, const void *p, int B, int T, int heads, int w
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-TcSweep with_maps(const LaSweep &w) {
-    TcSweep t{};
-    t.w = w;
+bool with_maps(const LaSweep &w, TcSweep *t) {
+    t->w = w;
     auto in = [&](CUtensorMap *m, const LaRows &r, int width) {
         return make_rows_map(m, r.p, w.B, w.T, w.H / r.group, width, r.sb, r.st, r.sh);
     };
-    t.tma_in = in(&t.a, w.a, w.dk) && in(&t.b, w.b, w.dk) && in(&t.c, w.c, w.dv);
-    const long long row = static_cast<long long>(w.H) * w.dv;
-    t.tma_out = !w.out_f32 && w.dv % 8 == 0 && make_rows_map(&t.out, w.out, w.B, w.T, w.H, w.dv, w.T * row, row, w.dv);
-    return t;
+    const long long row = static_cast<long long>(w.H) * w.out_w;
+    return in(&t->a, w.a, w.dk) && in(&t->b, w.b, w.dk) && in(&t->c, w.c, w.dv) &&
+           (w.out_f32 || make_rows_map(&t->out, w.out, w.B, w.T, w.H, w.out_w, w.T * row, row, w.out_w));
 }
 
 template <int DK, int DV, bool STATE_ONLY>
@@ -804,8 +744,8 @@ cudaError_t launch(const TcBatch &t, int n, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const LaSweep &w = t.s[0].w;
-    // the last segment's own state is not needed
-    const dim3 grid(static_cast<unsigned>(w.B) * w.H * ((w.dv + DV - 1) / DV), STATE_ONLY ? w.n_seg - 1 : w.n_seg, n);
+    // pass 1: the state of the segment that comes last is not needed (its blocks return at once)
+    const dim3 grid(static_cast<unsigned>(w.B) * w.H * ((w.dv + DV - 1) / DV), w.n_seg, n);
     k<<<grid, kThreads, smem, s>>>(t);
     return cudaGetLastError();
 }
@@ -831,8 +771,16 @@ cudaError_t by_width(const TcBatch &t, int n, cudaStream_t s) {
 
 cudaError_t launch_la_tc(const LaSweep *w, int n, cudaStream_t s) {
     TcBatch t{};
-    for (int i = 0; i < n; ++i) t.s[i] = with_maps(w[i]);
+    for (int i = 0; i < n; ++i)
+        if (!with_maps(w[i], &t.s[i])) return cudaErrorInvalidValue;
     return by_width(t, n, s);
+}
+
+bool la_tc_readable(const LaRows &r, int B, int T, int heads) {
+    const long long n[3] = {T, heads, B}, s[3] = {r.st, r.sh, r.sb};
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1 && (s[i] == 0 || s[i] % 8 != 0 || s[i] >= (1ll << 38))) return false;
+    return reinterpret_cast<uintptr_t>(r.p) % 16 == 0;
 }
 
 bool la_tc_together(const LaSweep &x, const LaSweep &y) {

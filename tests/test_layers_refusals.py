@@ -29,14 +29,6 @@ BAD_SHAPES = [dict(B=0), dict(T=0), dict(H=0), dict(Hkv=0), dict(Hkv=3), dict(H=
               dict(B=1 << 20, H=32, Hkv=32)]
 
 
-@pytest.mark.parametrize("bad", BAD_SHAPES)
-def test_attention_shapes(L, bad):
-    assert L.pararnn_linear_attention_workspace_size(_shape()) > 0
-    assert L.pararnn_linear_attention_backward_workspace_size(_shape()) > 0
-    assert L.pararnn_linear_attention_workspace_size(_shape(**bad)) == 0
-    assert L.pararnn_linear_attention_backward_workspace_size(_shape(**bad)) == 0
-
-
 # addresses that are only compared, never read: the calls below refuse before any launch
 BASE = 1 << 40
 
@@ -47,10 +39,38 @@ def _rows(at, T=100, heads=4, width=64, **kw):
     return binding.Rows(a["ptr"], a["stride_b"], a["stride_t"], a["stride_h"])
 
 
+@pytest.mark.parametrize("bad", BAD_SHAPES)
+def test_attention_shapes(L, bad):
+    r = _rows(BASE)
+    assert L.pararnn_linear_attention_workspace_size(_shape(), r, r, r) > 0
+    assert L.pararnn_linear_attention_backward_workspace_size(_shape(), r, r, r, r) > 0
+    assert L.pararnn_linear_attention_workspace_size(_shape(**bad), r, r, r) == 0
+    assert L.pararnn_linear_attention_backward_workspace_size(_shape(**bad), r, r, r, r) == 0
+
+
+def test_workspace_by_operands(L):
+    """bf16 rows off 16 bytes, or shared by stride 0, are packed into the workspace; others are not."""
+    s = _shape(dtype=BF16, H=4, Hkv=4, dv=64)
+    r = lambda **kw: _rows(BASE, **kw)
+    size = lambda *x: L.pararnn_linear_attention_workspace_size(s, *x)
+    tensor = 2 * 100 * 4 * 64 * 2
+    assert size(r(), r(), r()) == 256
+    for odd in (r(ptr=BASE + 2), r(stride_t=257), r(stride_h=0)):
+        assert size(odd, r(), r()) == tensor
+        assert size(odd, odd, odd) == 3 * tensor
+    # fp32 needs none of it
+    f = _shape(H=4, Hkv=4, dv=64)
+    assert L.pararnn_linear_attention_workspace_size(f, r(ptr=BASE + 4), r(), r()) == 256
+    # odd widths: the outputs leave through the workspace too
+    s = _shape(dtype=BF16, H=4, Hkv=4, dv=63)
+    assert size(r(), r(), r()) == tensor
+
+
 def _attention(L, **kw):
     s = _shape()
-    need = L.pararnn_linear_attention_workspace_size(s)
-    a = dict(q=_rows(BASE), k=_rows(2 * BASE, heads=2), v=_rows(3 * BASE, heads=2, width=32), ld=4 * BASE, s0=None,
+    good = [_rows(BASE), _rows(2 * BASE, heads=2), _rows(3 * BASE, heads=2, width=32)]
+    need = L.pararnn_linear_attention_workspace_size(s, *good)
+    a = dict(q=good[0], k=good[1], v=good[2], ld=4 * BASE, s0=None,
              lengths=None, o=5 * BASE, s=6 * BASE, ws=7 * BASE, n=need)
     a.update(kw)
     return L.pararnn_linear_attention(s, a["q"], a["k"], a["v"], a["ld"], a["s0"], a["lengths"], a["o"], a["s"], a["ws"],
@@ -70,7 +90,8 @@ def test_attention_arguments(L):
 
 def test_attention_backward_arguments(L):
     s = _shape()
-    need = L.pararnn_linear_attention_backward_workspace_size(s)
+    need = L.pararnn_linear_attention_backward_workspace_size(s, _rows(BASE), _rows(2 * BASE, heads=2),
+                                                              _rows(3 * BASE, heads=2, width=32), _rows(5 * BASE, width=32))
 
     def call(**kw):
         a = dict(q=_rows(BASE), k=_rows(2 * BASE, heads=2), v=_rows(3 * BASE, heads=2, width=32), ld=4 * BASE,
