@@ -84,20 +84,120 @@ __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&v)[V]) {
     }
 }
 
-__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + expf(-z)); }
-// act(z) and act'(z)
-__device__ __forceinline__ float act_of(float z, int act) {
-    if (act == PARARNN_ACT_SILU) return z * sigmoid(z);
-    if (act == PARARNN_ACT_GELU) return z * normcdff(z);
-    return z;
+// d = a * b + c on V elements, two at a time (fma.rn.f32x2 is two fp32 FMAs in one instruction: these kernels are
+// bound by instructions before they are bound by memory)
+__device__ __forceinline__ void fma_pair(float &d0, float &d1, float a0, float a1, float b0, float b1, float c0, float c1) {
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
 }
-__device__ __forceinline__ float act_slope(float z, int act) {
+__device__ __forceinline__ void mul_pair(float &d0, float &d1, float a0, float a1, float b0, float b1) {
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void add_pair(float &d0, float &d1, float a0, float a1, float b0, float b1) {
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+template <int V>
+__device__ __forceinline__ void vfma(float (&d)[V], const float (&a)[V], const float (&b)[V], const float (&c)[V]) {
+    if constexpr (V == 1) d[0] = fmaf(a[0], b[0], c[0]);
+    else
+#pragma unroll
+        for (int i = 0; i < V; i += 2) fma_pair(d[i], d[i + 1], a[i], a[i + 1], b[i], b[i + 1], c[i], c[i + 1]);
+}
+template <int V>
+__device__ __forceinline__ void vmul(float (&d)[V], const float (&a)[V], const float (&b)[V]) {
+    if constexpr (V == 1) d[0] = a[0] * b[0];
+    else
+#pragma unroll
+        for (int i = 0; i < V; i += 2) mul_pair(d[i], d[i + 1], a[i], a[i + 1], b[i], b[i + 1]);
+}
+template <int V>
+__device__ __forceinline__ void vscale(float (&d)[V], const float (&a)[V], float s) {
+    if constexpr (V == 1) d[0] = a[0] * s;
+    else
+#pragma unroll
+        for (int i = 0; i < V; i += 2) mul_pair(d[i], d[i + 1], a[i], a[i + 1], s, s);
+}
+template <int V>
+__device__ __forceinline__ void vshift(float (&d)[V], const float (&a)[V], float s) {
+    if constexpr (V == 1) d[0] = a[0] + s;
+    else
+#pragma unroll
+        for (int i = 0; i < V; i += 2) add_pair(d[i], d[i + 1], a[i], a[i + 1], s, s);
+}
+template <int V>
+__device__ __forceinline__ void vadd(float (&d)[V], const float (&a)[V], const float (&b)[V]) {
+    if constexpr (V == 1) d[0] = a[0] + b[0];
+    else
+#pragma unroll
+        for (int i = 0; i < V; i += 2) add_pair(d[i], d[i + 1], a[i], a[i + 1], b[i], b[i + 1]);
+}
+// sum of V elements, sum of a b
+template <int V>
+__device__ __forceinline__ float vsum(const float (&a)[V]) {
+    if constexpr (V == 1) return a[0];
+    float s0 = a[0], s1 = a[V > 1 ? 1 : 0];
+#pragma unroll
+    for (int i = 2; i < V; i += 2) add_pair(s0, s1, s0, s1, a[i], a[i + 1]);
+    return s0 + s1;
+}
+template <int V>
+__device__ __forceinline__ float vdot(const float (&a)[V], const float (&b)[V]) {
+    if constexpr (V == 1) return a[0] * b[0];
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; i += 2) fma_pair(s0, s1, a[i], a[i + 1], b[i], b[i + 1], s0, s1);
+    return s0 + s1;
+}
+
+// 1 / (1 + exp(-z)).  __expf is off by about (2 + |z|) 2^-24 relative, which the sum with 1 damps where z > 0 and
+// which is below z's own rounding, |z| 2^-24 in the exponent, where z < 0; the reciprocal is off by 2^-23.
+__device__ __forceinline__ float sigmoid(float z) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-z)));
+    return r;
+}
+// z = act(z) for V elements, and with it s = act'(z); one branch on the kind for all of them
+template <int V>
+__device__ __forceinline__ void act_of(float (&z)[V], int act) {
     if (act == PARARNN_ACT_SILU) {
-        const float s = sigmoid(z);
-        return s * fmaf(z, 1.f - s, 1.f);
+        float s[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[i] = sigmoid(z[i]);
+        vmul<V>(z, z, s);
+    } else if (act == PARARNN_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) z[i] *= normcdff(z[i]);
     }
-    if (act == PARARNN_ACT_GELU) return fmaf(z * 0.3989422804014327f, expf(-0.5f * z * z), normcdff(z));
-    return 1.f;
+}
+template <int V>
+__device__ __forceinline__ void act_and_slope(float (&z)[V], float (&s)[V], int act) {
+    if (act == PARARNN_ACT_SILU) {  // a = z g, act' = g + a (1 - g) = (g + a) - a g
+        float g[V], h[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) g[i] = sigmoid(z[i]);
+        vmul<V>(z, z, g);
+#pragma unroll
+        for (int i = 0; i < V; ++i) h[i] = 1.f - g[i];
+        vfma<V>(s, z, h, g);
+    } else if (act == PARARNN_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float p = normcdff(z[i]);
+            s[i] = fmaf(z[i] * 0.3989422804014327f, __expf(-0.5f * z[i] * z[i]), p);
+            z[i] *= p;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[i] = 1.f;
+    }
 }
 
 // (count, mean, sum of squared deviations) of two disjoint sets, joined
@@ -131,89 +231,153 @@ __device__ __forceinline__ void load_wb(const GnArgs &a, int c, float (&w)[V], f
 
 // ---- one row per statistic ----------------------------------------------------------------------------------
 
-// Teams of TL lanes; a lane holds K vectors of V channels of its group: channels (k TL + lane) V + i.
-// A team keeps its group and walks the rows, so weights (and, backward, their gradients) stay in registers.
-struct RowPlan {
-    int team;        // lanes per group, a power of two
-    int grid;        // CTAs
+// A team of `team` lanes (a power of two) holds K vectors of V channels per lane of one group: channels
+// (k team + lane) V + i.  A CTA covers `gpc` groups and `rows` rows at a time (blockIdx.y: which groups), so a team
+// keeps its group and its weights stay in registers.  R rows are loaded before the first is used.
+struct Teams {
+    int team, gpc, rows;
+};
+__device__ __forceinline__ Teams teams_of(int G, int team) {
+    const int per = kThr / team, gpc = min(per, G);
+    return {team, gpc, per / gpc};
+}
+
+template <typename T, int V>
+struct Raw {  // V elements as they come from memory
+    static constexpr int WORDS = sizeof(T) * V / 4 < 1 ? 1 : sizeof(T) * V / 4;
+    unsigned u[WORDS];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) u[i] = 0u;
+    }
+    __device__ __forceinline__ void get(const T *p) {
+        if constexpr (sizeof(T) * V == 2) {
+            u[0] = *reinterpret_cast<const unsigned short *>(p);
+        } else if constexpr (sizeof(T) * V == 4) {
+            u[0] = *reinterpret_cast<const unsigned *>(p);
+        } else if constexpr (sizeof(T) * V == 8) {
+            const uint2 x = *reinterpret_cast<const uint2 *>(p);
+            u[0] = x.x, u[1] = x.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < WORDS; i += 4) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(reinterpret_cast<const unsigned *>(p) + i);
+                u[i] = x.x, u[i + 1] = x.y, u[i + 2] = x.z, u[i + 3] = x.w;
+            }
+        }
+    }
+    __device__ __forceinline__ float at(int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(u[i]);
+        else return (i & 1) ? __uint_as_float(u[i >> 1] & 0xffff0000u) : __uint_as_float(u[i >> 1] << 16);
+    }
 };
 
-template <typename TX, typename TY, int V, int K>
-__global__ void __launch_bounds__(kThr) gn_row_forward_kernel(const GnArgs a, int team) {
+template <typename TX, typename TY, int V, int K, int R>
+__global__ void __launch_bounds__(kThr, V * K <= 8 ? 3 : 1) gn_row_forward_kernel(const GnArgs a, int team) {
     const int cg = a.C / a.G;
-    const int lane = threadIdx.x & (team - 1);
-    const long long teams = static_cast<long long>(gridDim.x) * (kThr / team);
-    const long long me = static_cast<long long>(blockIdx.x) * (kThr / team) + threadIdx.x / team;
+    const Teams tt = teams_of(a.G, team);
+    const int tm = threadIdx.x / team, lane = threadIdx.x & (team - 1);
+    const int g = blockIdx.y * tt.gpc + tm % tt.gpc, rr = tm / tt.gpc;
+    const bool have = g < a.G && rr < tt.rows;
     const TX *x = static_cast<const TX *>(a.x), *gate = static_cast<const TX *>(a.gate);
     TY *y = static_cast<TY *>(a.y);
-    const long long all = static_cast<long long>(a.N) * a.G;
-    const long long trips = (all + teams - 1) / teams;
     const float inv = 1.f / cg;
-    for (long long i = 0; i < trips; ++i) {
-        const long long slab = i * teams + me;
-        const bool on = slab < all;
-        const long long n = on ? slab / a.G : 0;
-        const int g = on ? static_cast<int>(slab % a.G) : 0;
-        const bool live = on && (a.lengths == nullptr || a.lengths[n] > 0);
-        const long long base = n * a.C + static_cast<long long>(g) * cg;
-        float v[K][V];
-        float sum = 0.f;
+    float w[K][V], b[K][V];
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int c = (k * team + lane) * V;
-            if (live && c < cg) {
-                load<V>(x + base + c, v[k]);
-            } else {
+    for (int k = 0; k < K; ++k) {
+        const int c = (k * team + lane) * V;
 #pragma unroll
-                for (int u = 0; u < V; ++u) v[k][u] = 0.f;
-            }
+        for (int u = 0; u < V; ++u) w[k][u] = 1.f, b[k][u] = 0.f;
+        if (have && c < cg) load_wb<V>(a, g * cg + c, w[k], b[k]);
+    }
+    const long long step = static_cast<long long>(gridDim.x) * tt.rows;
+    for (long long n0 = static_cast<long long>(blockIdx.x) * tt.rows + rr; n0 - rr < a.N; n0 += step * R) {
+        Raw<TX, V> v[R][K], q[R][K];
+        bool on[R], live[R];
 #pragma unroll
-            for (int u = 0; u < V; ++u) sum += v[k][u];
-        }
-        for (int m = team >> 1; m > 0; m >>= 1) sum += __shfl_xor_sync(~0u, sum, m);
-        const float mean = sum * inv;
-        float m2 = 0.f;
+        for (int r = 0; r < R; ++r) {
+            const long long n = n0 + r * step;
+            on[r] = have && n < a.N;
+            live[r] = on[r] && (a.lengths == nullptr || a.lengths[n] > 0);
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-            if ((k * team + lane) * V < cg) {
-#pragma unroll
-                for (int u = 0; u < V; ++u) m2 = fmaf(v[k][u] - mean, v[k][u] - mean, m2);
-            }
-        for (int m = team >> 1; m > 0; m >>= 1) m2 += __shfl_xor_sync(~0u, m2, m);
-        const float rstd = rsqrtf(fmaf(live ? m2 : 0.f, inv, a.eps));
-        if (on && lane == 0) *reinterpret_cast<float2 *>(a.stats + slab * 2) = make_float2(mean, rstd);
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int c = (k * team + lane) * V;
-            if (!on || c >= cg) continue;
-            float o[V] = {};
-            if (live) {
-                float w[V], b[V], q[V];
-                load_wb<V>(a, g * cg + c, w, b);
-                if (gate != nullptr) load<V>(gate + base + c, q);
-#pragma unroll
-                for (int u = 0; u < V; ++u) {
-                    const float z = fmaf((v[k][u] - mean) * rstd, w[u], b[u]);
-                    o[u] = gate != nullptr ? z * act_of(q[u], a.act) : act_of(z, a.act);
+            for (int k = 0; k < K; ++k) {
+                const int c = (k * team + lane) * V;
+                v[r][k].zero();
+                q[r][k].zero();
+                if (live[r] && c < cg) {
+                    const long long at = n * a.C + static_cast<long long>(g) * cg + c;
+                    v[r][k].get(x + at);
+                    if (gate != nullptr) q[r][k].get(gate + at);
                 }
             }
-            store<V>(y + base + c, o);
+        }
+        float mean[R], m2[R], d[R][K][V];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            mean[r] = 0.f;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+#pragma unroll
+                for (int u = 0; u < V; ++u) d[r][k][u] = v[r][k].at(u);
+                mean[r] += vsum<V>(d[r][k]);
+            }
+        }
+        for (int m = team >> 1; m > 0; m >>= 1)
+#pragma unroll
+            for (int r = 0; r < R; ++r) mean[r] += __shfl_xor_sync(~0u, mean[r], m);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            mean[r] *= inv;
+            m2[r] = 0.f;
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if ((k * team + lane) * V < cg) {
+                    vshift<V>(d[r][k], d[r][k], -mean[r]);
+                    m2[r] += vdot<V>(d[r][k], d[r][k]);
+                }
+        }
+        for (int m = team >> 1; m > 0; m >>= 1)
+#pragma unroll
+            for (int r = 0; r < R; ++r) m2[r] += __shfl_xor_sync(~0u, m2[r], m);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (!on[r]) continue;
+            const long long n = n0 + r * step;
+            const float rstd = rsqrtf(fmaf(live[r] ? m2[r] : 0.f, inv, a.eps));
+            if (lane == 0) *reinterpret_cast<float2 *>(a.stats + (n * a.G + g) * 2) = make_float2(mean[r], rstd);
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int c = (k * team + lane) * V;
+                if (c >= cg) continue;
+                float o[V] = {};
+                if (live[r]) {
+                    float f[V];
+                    vscale<V>(f, w[k], rstd);
+                    vfma<V>(o, d[r][k], f, b[k]);
+                    if (gate != nullptr) {
+#pragma unroll
+                        for (int u = 0; u < V; ++u) f[u] = q[r][k].at(u);
+                        act_of<V>(f, a.act);
+                        vmul<V>(o, o, f);
+                    } else {
+                        act_of<V>(o, a.act);
+                    }
+                }
+                store<V>(y + n * a.C + static_cast<long long>(g) * cg + c, o);
+            }
         }
     }
 }
 
-// Backward: CTA (bx, by) takes the groups of column block by and the rows bx, bx + gridDim.x, ... ; its sums of
-// dw and db over those rows go to part[bx][2][C].
-template <typename TX, typename TY, int V, int K>
-__global__ void __launch_bounds__(kThr) gn_row_backward_kernel(const GnArgs a, int team, float *part) {
+// Backward: the sums of dw and db over the rows that a CTA took go to part[blockIdx.x][2][C].
+template <typename TX, typename TY, int V, int K, int R>
+__global__ void __launch_bounds__(kThr, V * K <= 8 ? 2 : 1) gn_row_backward_kernel(const GnArgs a, int team, float *part) {
     extern __shared__ float red[];  // [rows in flight][dw, db][this CTA's channels]
     const int cg = a.C / a.G;
-    const int per = kThr / team;                      // teams per CTA
-    const int gpc = min(per, a.G);                    // groups per CTA
-    const int rows = per / gpc;                       // rows in flight
+    const Teams tt = teams_of(a.G, team);
     const int tm = threadIdx.x / team, lane = threadIdx.x & (team - 1);
-    const int g = blockIdx.y * gpc + tm % gpc, rr = tm / gpc;
-    const bool have = g < a.G && rr < rows;
+    const int g = blockIdx.y * tt.gpc + tm % tt.gpc, rr = tm / tt.gpc;
+    const bool have = g < a.G && rr < tt.rows;
     const TX *x = static_cast<const TX *>(a.x), *gate = static_cast<const TX *>(a.gate);
     const TY *dy = static_cast<const TY *>(a.y);
     TX *dx = static_cast<TX *>(a.dx), *dgate = static_cast<TX *>(a.dgate);
@@ -226,93 +390,102 @@ __global__ void __launch_bounds__(kThr) gn_row_backward_kernel(const GnArgs a, i
         for (int u = 0; u < V; ++u) w[k][u] = 1.f, b[k][u] = dw[k][u] = db[k][u] = 0.f;
         if (have && c < cg) load_wb<V>(a, g * cg + c, w[k], b[k]);
     }
-    const long long step = static_cast<long long>(gridDim.x) * rows;
-    for (long long n0 = static_cast<long long>(blockIdx.x) * rows; n0 < a.N; n0 += step) {
-        const long long n = n0 + rr;
-        const bool on = have && n < a.N;
-        const bool live = on && (a.lengths == nullptr || a.lengths[n] > 0);
-        const long long base = n * a.C + static_cast<long long>(g) * cg;
-        float mean = 0.f, rstd = 0.f;
-        if (live) {
-            const float2 st = *reinterpret_cast<const float2 *>(a.stats + (static_cast<long long>(n) * a.G + g) * 2);
-            mean = st.x, rstd = st.y;
-        }
-        float xh[K][V], dh[K][V];  // xhat, w dz
-        float s1 = 0.f, s2 = 0.f;
+    const long long step = static_cast<long long>(gridDim.x) * tt.rows;
+    for (long long n0 = static_cast<long long>(blockIdx.x) * tt.rows + rr; n0 - rr < a.N; n0 += step * R) {
+        Raw<TX, V> v[R][K], q[R][K];
+        Raw<TY, V> t[R][K];
+        bool on[R], live[R];
+        float2 st[R];
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int c = (k * team + lane) * V;
-            const bool in = live && c < cg;
-            float t[V];
+        for (int r = 0; r < R; ++r) {
+            const long long n = n0 + r * step;
+            on[r] = have && n < a.N;
+            live[r] = on[r] && (a.lengths == nullptr || a.lengths[n] > 0);
+            st[r] = live[r] ? *reinterpret_cast<const float2 *>(a.stats + (n * a.G + g) * 2) : make_float2(0.f, 0.f);
 #pragma unroll
-            for (int u = 0; u < V; ++u) xh[k][u] = dh[k][u] = t[u] = 0.f;
-            if (in) {
-                load<V>(x + base + c, xh[k]);
-                load<V>(dy + base + c, t);
-            }
-            if (gate != nullptr) {
-                float q[V] = {}, dg[V];
-                if (in) load<V>(gate + base + c, q);
-#pragma unroll
-                for (int u = 0; u < V; ++u) {
-                    xh[k][u] = (xh[k][u] - mean) * rstd;
-                    const float z = fmaf(xh[k][u], w[k][u], b[k][u]);
-                    dg[u] = t[u] * z * act_slope(q[u], a.act);
-                    t[u] *= act_of(q[u], a.act);
-                }
-                if (on && c < cg) {
-                    if (!live) {
-#pragma unroll
-                        for (int u = 0; u < V; ++u) dg[u] = 0.f;
-                    }
-                    store<V>(dgate + base + c, dg);
-                }
-            } else {
-#pragma unroll
-                for (int u = 0; u < V; ++u) {
-                    xh[k][u] = (xh[k][u] - mean) * rstd;
-                    t[u] *= act_slope(fmaf(xh[k][u], w[k][u], b[k][u]), a.act);
-                }
-            }
-            if (in) {
-#pragma unroll
-                for (int u = 0; u < V; ++u) {
-                    db[k][u] += t[u];
-                    dw[k][u] = fmaf(t[u], xh[k][u], dw[k][u]);
-                    dh[k][u] = t[u] * w[k][u];
-                    s1 += dh[k][u];
-                    s2 = fmaf(dh[k][u], xh[k][u], s2);
+            for (int k = 0; k < K; ++k) {
+                const int c = (k * team + lane) * V;
+                v[r][k].zero();
+                q[r][k].zero();
+                t[r][k].zero();
+                if (live[r] && c < cg) {
+                    const long long at = n * a.C + static_cast<long long>(g) * cg + c;
+                    v[r][k].get(x + at);
+                    t[r][k].get(dy + at);
+                    if (gate != nullptr) q[r][k].get(gate + at);
                 }
             }
         }
-        for (int m = team >> 1; m > 0; m >>= 1) {
-            s1 += __shfl_xor_sync(~0u, s1, m);
-            s2 += __shfl_xor_sync(~0u, s2, m);
-        }
-        s1 *= inv;
-        s2 *= inv;
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int c = (k * team + lane) * V;
-            if (!on || c >= cg) continue;
-            float o[V] = {};
-            if (live) {
+        for (int r = 0; r < R; ++r) {
+            const long long base = (n0 + r * step) * a.C + static_cast<long long>(g) * cg;
+            const float mean = st[r].x, rstd = st[r].y;
+            float xh[K][V], dh[K][V];  // xhat, w dz
+            float s1 = 0.f, s2 = 0.f;
 #pragma unroll
-                for (int u = 0; u < V; ++u) o[u] = rstd * (dh[k][u] - s1 - xh[k][u] * s2);
+            for (int k = 0; k < K; ++k) {
+                const int c = (k * team + lane) * V;
+                float dg[V], z[V], dz[V], slope[V];
+#pragma unroll
+                for (int u = 0; u < V; ++u) {
+                    xh[k][u] = v[r][k].at(u);
+                    dz[u] = t[r][k].at(u);  // zero where there is no element
+                }
+                vshift<V>(xh[k], xh[k], -mean);
+                vscale<V>(xh[k], xh[k], rstd);
+                vfma<V>(z, xh[k], w[k], b[k]);
+                if (gate != nullptr) {
+                    float gt[V];
+#pragma unroll
+                    for (int u = 0; u < V; ++u) gt[u] = q[r][k].at(u);
+                    act_and_slope<V>(gt, slope, a.act);
+                    vmul<V>(dg, dz, z);
+                    vmul<V>(dg, dg, slope);
+                    vmul<V>(dz, dz, gt);
+                } else {
+                    act_and_slope<V>(z, slope, a.act);
+                    vmul<V>(dz, dz, slope);
+                }
+                vadd<V>(db[k], db[k], dz);
+                vfma<V>(dw[k], dz, xh[k], dw[k]);
+                vmul<V>(dh[k], dz, w[k]);
+                s1 += vsum<V>(dh[k]);
+                s2 += vdot<V>(dh[k], xh[k]);
+                if (gate != nullptr && on[r] && c < cg) store<V>(dgate + base + c, dg);
             }
-            store<V>(dx + base + c, o);
+            for (int m = team >> 1; m > 0; m >>= 1) {
+                s1 += __shfl_xor_sync(~0u, s1, m);
+                s2 += __shfl_xor_sync(~0u, s2, m);
+            }
+            s1 *= inv;
+            s2 *= inv;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int c = (k * team + lane) * V;
+                if (!on[r] || c >= cg) continue;
+                float o[V] = {};
+                if (live[r]) {
+                    // rstd (dh - s1 - xhat s2)
+                    vshift<V>(o, dh[k], -s1);
+                    float f[V];
+                    vscale<V>(f, xh[k], -s2);
+                    vadd<V>(o, o, f);
+                    vscale<V>(o, o, rstd);
+                }
+                store<V>(dx + base + c, o);
+            }
         }
     }
     // rows in flight summed in order, then this CTA's partial sums out
-    const int width = gpc * cg;
+    const int width = tt.gpc * cg;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const int c = (k * team + lane) * V;
-        if (rr < rows && c < cg) {
+        if (rr < tt.rows && c < cg) {
 #pragma unroll
             for (int u = 0; u < V; ++u) {
-                red[(rr * 2 + 0) * width + (tm % gpc) * cg + c + u] = dw[k][u];
-                red[(rr * 2 + 1) * width + (tm % gpc) * cg + c + u] = db[k][u];
+                red[(rr * 2 + 0) * width + (tm % tt.gpc) * cg + c + u] = dw[k][u];
+                red[(rr * 2 + 1) * width + (tm % tt.gpc) * cg + c + u] = db[k][u];
             }
         }
     }
@@ -321,22 +494,26 @@ __global__ void __launch_bounds__(kThr) gn_row_backward_kernel(const GnArgs a, i
         const int which = i / width, c = i % width, ch = blockIdx.y * width + c;
         if (ch >= a.C) continue;
         float s = 0.f;
-        for (int q = 0; q < rows; ++q) s += red[(q * 2 + which) * width + c];
+        for (int q = 0; q < tt.rows; ++q) s += red[(q * 2 + which) * width + c];
         part[(static_cast<long long>(blockIdx.x) * 2 + which) * a.C + ch] = s;
     }
 }
 
-// dw, db [C] = sums of part [rows][2][C] in row order: 8 row slices per CTA of 32 channels, then across them
-__global__ void __launch_bounds__(256) gn_param_sum_kernel(const float *part, int rows, int C, float *dw, float *db) {
-    __shared__ float red[8][33];
-    const int c = blockIdx.x * 32 + (threadIdx.x & 31), sl = threadIdx.x >> 5, which = blockIdx.y;
+// dw, db [C] = sums of part [rows][2][C]: 32 slices of the rows per CTA of 32 channels, each in row order, then
+// the slices in order
+__global__ void __launch_bounds__(1024) gn_param_sum_kernel(const float *__restrict__ part, int rows, int C, float *dw,
+                                                            float *db) {
+    __shared__ float red[32][33];
+    const int lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane, sl = threadIdx.x >> 5, which = blockIdx.y;
     float s = 0.f;
-    if (c < C)
-        for (int r = sl; r < rows; r += 8) s += part[(static_cast<long long>(r) * 2 + which) * C + c];
-    red[sl][threadIdx.x & 31] = s;
+    if (c < C) {
+#pragma unroll 8
+        for (int r = sl; r < rows; r += 32) s += part[(static_cast<long long>(r) * 2 + which) * C + c];
+    }
+    red[sl][lane] = s;
     __syncthreads();
     if (sl == 0 && c < C) {
-        for (int q = 1; q < 8; ++q) s += red[q][threadIdx.x];
+        for (int q = 1; q < 32; ++q) s += red[q][lane];
         float *out = which == 0 ? dw : db;
         if (out != nullptr) out[c] = s;
     }
@@ -350,9 +527,15 @@ struct Span {
     int cols, par;  // vectors per row; rows in flight
 };
 template <int V>
-__device__ __forceinline__ Span span_of(const GnArgs &a) {
+__host__ __device__ __forceinline__ Span span_of(const GnArgs &a) {
     const int cols = a.C / V;
     return {cols, cols >= kThr ? 1 : kThr / cols};
+}
+// threads of such a CTA
+template <int V>
+int threads_of(const GnArgs &a) {
+    const Span sp = span_of<V>(a);
+    return sp.par == 1 && sp.cols >= kThr ? kThr : (sp.cols * sp.par + 31) / 32 * 32;
 }
 
 // part[n][chunk][g] = moments of group g in this CTA's rows
@@ -367,7 +550,7 @@ __global__ void __launch_bounds__(kThr) gn_stats_kernel(const GnArgs a, int rows
     const TX *x = static_cast<const TX *>(a.x) + static_cast<long long>(n) * a.S * a.C;
     const Span sp = span_of<V>(a);
     const int cg = a.C / a.G, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int g = threadIdx.x; g < a.G; g += kThr) acc[g] = {0.f, 0.f, 0.f};
+    for (int g = threadIdx.x; g < a.G; g += blockDim.x) acc[g] = {0.f, 0.f, 0.f};
     for (int cb = 0; cb < sp.cols; cb += kThr) {
         const int width = min(kThr, sp.cols - cb);
         const int r0 = sp.par == 1 ? 0 : threadIdx.x / sp.cols;
@@ -408,7 +591,7 @@ __global__ void __launch_bounds__(kThr) gn_stats_kernel(const GnArgs a, int rows
         __syncthreads();
         // the groups of this column block, a warp each: its vectors times the rows in flight
         const int g_lo = cb * V / cg, g_hi = (min(sp.cols, cb + width) * V - 1) / cg;
-        for (int g = g_lo + warp; g <= g_hi; g += kThr / 32) {
+        for (int g = g_lo + warp; g <= g_hi; g += blockDim.x / 32) {
             const int c_lo = max(g * cg / V, cb) - cb, c_hi = min((g + 1) * cg / V, cb + width) - cb;
             const int w = c_hi - c_lo;
             Moments t = {0.f, 0.f, 0.f};
@@ -420,7 +603,7 @@ __global__ void __launch_bounds__(kThr) gn_stats_kernel(const GnArgs a, int rows
     }
     __syncthreads();
     Moments *out = part + static_cast<long long>(blockIdx.x) * a.G;
-    for (int g = threadIdx.x; g < a.G; g += kThr) out[g] = acc[g];
+    for (int g = threadIdx.x; g < a.G; g += blockDim.x) out[g] = acc[g];
 }
 
 __global__ void __launch_bounds__(kThr) gn_stats_join_kernel(const GnArgs a, int chunks, const Moments *part) {
@@ -438,9 +621,11 @@ __global__ void __launch_bounds__(kThr) gn_stats_join_kernel(const GnArgs a, int
     }
 }
 
+// The second pass takes the blocks in reversed order: what the first pass read last is still in L2.
 template <typename TX, typename TY, int V>
 __global__ void __launch_bounds__(kThr) gn_apply_kernel(const GnArgs a, int rows, int chunks) {
-    const int n = static_cast<int>(blockIdx.x / chunks), ch = static_cast<int>(blockIdx.x % chunks), L = row_count(a, n);
+    const unsigned bid = gridDim.x - 1 - blockIdx.x;
+    const int n = static_cast<int>(bid / chunks), ch = static_cast<int>(bid % chunks), L = row_count(a, n);
     const long long lo = static_cast<long long>(ch) * rows;
     const int hi = static_cast<int>(min(lo + rows, static_cast<long long>(a.S)));
     const long long nb = static_cast<long long>(n) * a.S * a.C;
@@ -467,10 +652,13 @@ __global__ void __launch_bounds__(kThr) gn_apply_kernel(const GnArgs a, int rows
                 float v[V], q[V];
                 load<V>(x + at, v);
                 if (gate != nullptr) load<V>(gate + at, q);
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float z = fmaf(v[i] - st.x, w[i], b[i]);
-                    o[i] = gate != nullptr ? z * act_of(q[i], a.act) : act_of(z, a.act);
+                vshift<V>(v, v, -st.x);
+                vfma<V>(o, v, w, b);
+                if (gate != nullptr) {
+                    act_of<V>(q, a.act);
+                    vmul<V>(o, o, q);
+                } else {
+                    act_of<V>(o, a.act);
                 }
             }
             store<V>(y + at, o);
@@ -478,15 +666,23 @@ __global__ void __launch_bounds__(kThr) gn_apply_kernel(const GnArgs a, int rows
     }
 }
 
-// dz of one element, and xhat; with a gate also dgate
-template <bool GATE>
-__device__ __forceinline__ float dz_of(const GnArgs &a, float dy, float xhat, float w, float b, float q, float *dg) {
-    const float z = fmaf(xhat, w, b);
-    if (GATE) {
-        if (dg != nullptr) *dg = dy * z * act_slope(q, a.act);
-        return dy * act_of(q, a.act);
+// From x, dy and the gate's values q to xhat (in v), dz (in t) and, with a gate, dgate (in q)
+template <int V, bool GATE>
+__device__ __forceinline__ void dz_of(const GnArgs &a, float2 st, const float (&w)[V], const float (&b)[V], float (&v)[V],
+                                      float (&t)[V], float (&q)[V]) {
+    float z[V], slope[V];
+    vshift<V>(v, v, -st.x);
+    vscale<V>(v, v, st.y);
+    vfma<V>(z, v, w, b);
+    if constexpr (GATE) {
+        act_and_slope<V>(q, slope, a.act);
+        vmul<V>(z, z, t);
+        vmul<V>(t, t, q);
+        vmul<V>(q, z, slope);
+    } else {
+        act_and_slope<V>(z, slope, a.act);
+        vmul<V>(t, t, slope);
     }
-    return dy * act_slope(z, a.act);
 }
 
 // part[n][chunk][2][C]: sums of dz xhat and of dz over this CTA's rows
@@ -517,13 +713,9 @@ __global__ void __launch_bounds__(kThr) gn_channel_sum_kernel(const GnArgs a, in
                 load<V>(x + s * a.C + c, v);
                 load<V>(dy + s * a.C + c, t);
                 if (GATE) load<V>(gate + s * a.C + c, q);
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float xh = (v[i] - st.x) * st.y;
-                    const float dz = dz_of<GATE>(a, t[i], xh, w[i], b[i], q[i], nullptr);
-                    db[i] += dz;
-                    dw[i] = fmaf(dz, xh, dw[i]);
-                }
+                dz_of<V, GATE>(a, st, w, b, v, t, q);
+                vadd<V>(db, db, t);
+                vfma<V>(dw, t, v, dw);
             }
         }
         if (sp.par == 1) {
@@ -535,7 +727,7 @@ __global__ void __launch_bounds__(kThr) gn_channel_sum_kernel(const GnArgs a, in
 #pragma unroll
             for (int i = 0; i < V; ++i) red[0][threadIdx.x * V + i] = dw[i], red[1][threadIdx.x * V + i] = db[i];
             __syncthreads();
-            for (int i = threadIdx.x; i < 2 * a.C; i += kThr) {
+            for (int i = threadIdx.x; i < 2 * a.C; i += blockDim.x) {
                 const int which = i / a.C, c = i % a.C;
                 float s = 0.f;
                 for (int q = 0; q < sp.par; ++q) s += red[which][q * a.C + c];
@@ -545,36 +737,52 @@ __global__ void __launch_bounds__(kThr) gn_channel_sum_kernel(const GnArgs a, in
     }
 }
 
-// One CTA per n: channel sums over the chunks -> chan[n][2][C], group sums of w dz and w dz xhat -> gsum[n][g][2]
-__global__ void __launch_bounds__(kThr) gn_channel_join_kernel(const GnArgs a, int chunks, const float *part,
+// One CTA per (n, group): channel sums over the chunks -> chan[n][2][C], group sums of w dz and w dz xhat ->
+// gsum[n][g][2].  Threads span the group's channels and, where those are few, slices of the chunks.
+__global__ void __launch_bounds__(kThr) gn_channel_join_kernel(const GnArgs a, int chunks, const float *__restrict__ part,
                                                                float *chan, float *gsum) {
-    const int n = blockIdx.x;
-    const float *p = part + static_cast<long long>(n) * chunks * 2 * a.C;
-    float *ch = chan + static_cast<long long>(n) * 2 * a.C;
-    for (int i = threadIdx.x; i < 2 * a.C; i += kThr) {
-        float s = 0.f;
-#pragma unroll 8
-        for (int q = 0; q < chunks; ++q) s += p[static_cast<long long>(q) * 2 * a.C + i];
-        ch[i] = s;
+    __shared__ float red[2][kThr];
+    const int n = blockIdx.x / a.G, g = blockIdx.x % a.G, cg = a.C / a.G;
+    const int cols = min(cg, kThr), slices = kThr / cols;
+    const int col = threadIdx.x % cols, sl = threadIdx.x / cols;
+    const float *p = part + static_cast<long long>(n) * chunks * 2 * a.C + g * cg;
+    float *ch = chan + static_cast<long long>(n) * 2 * a.C + g * cg;
+    float s1 = 0.f, s2 = 0.f;  // w dz, w dz xhat of this thread's channels
+    for (int c0 = 0; c0 < cg; c0 += cols) {
+        const int c = c0 + col;
+        float dw = 0.f, db = 0.f;
+        if (c < cg && sl < slices) {
+#pragma unroll 4
+            for (int q = sl; q < chunks; q += slices) {
+                dw += p[static_cast<long long>(q) * 2 * a.C + c];
+                db += p[static_cast<long long>(q) * 2 * a.C + a.C + c];
+            }
+        }
+        __syncthreads();
+        red[0][threadIdx.x] = dw, red[1][threadIdx.x] = db;
+        __syncthreads();
+        if (c < cg && sl == 0) {
+            for (int q = 1; q < slices; ++q) dw += red[0][q * cols + col], db += red[1][q * cols + col];
+            ch[c] = dw, ch[a.C + c] = db;
+            const float w = a.weight != nullptr ? a.weight[g * cg + c] : 1.f;
+            s1 = fmaf(w, db, s1), s2 = fmaf(w, dw, s2);
+        }
     }
     __syncthreads();
-    const int cg = a.C / a.G, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int g = warp; g < a.G; g += kThr / 32) {
-        float s1 = 0.f, s2 = 0.f;
-        for (int c = g * cg + lane; c < (g + 1) * cg; c += 32) {
-            const float w = a.weight != nullptr ? a.weight[c] : 1.f;
-            s2 = fmaf(w, ch[c], s2);
-            s1 = fmaf(w, ch[a.C + c], s1);
-        }
-#pragma unroll
-        for (int q = 16; q > 0; q >>= 1) s1 += __shfl_xor_sync(~0u, s1, q), s2 += __shfl_xor_sync(~0u, s2, q);
-        if (lane == 0) *reinterpret_cast<float2 *>(gsum + (static_cast<long long>(n) * a.G + g) * 2) = make_float2(s1, s2);
+    red[0][threadIdx.x] = s1, red[1][threadIdx.x] = s2;
+    __syncthreads();
+    for (int m = kThr / 2; m > 0; m >>= 1) {
+        if (threadIdx.x < m)
+            red[0][threadIdx.x] += red[0][threadIdx.x + m], red[1][threadIdx.x] += red[1][threadIdx.x + m];
+        __syncthreads();
     }
+    if (threadIdx.x == 0) *reinterpret_cast<float2 *>(gsum + static_cast<long long>(blockIdx.x) * 2) = make_float2(red[0][0], red[1][0]);
 }
 
 template <typename TX, typename TY, int V, bool GATE>
 __global__ void __launch_bounds__(kThr) gn_backward_apply_kernel(const GnArgs a, int rows, int chunks, const float *gsum) {
-    const int n = static_cast<int>(blockIdx.x / chunks), ch = static_cast<int>(blockIdx.x % chunks), L = row_count(a, n);
+    const unsigned bid = gridDim.x - 1 - blockIdx.x;
+    const int n = static_cast<int>(bid / chunks), ch = static_cast<int>(bid % chunks), L = row_count(a, n);
     const long long lo = static_cast<long long>(ch) * rows;
     const long long hi = min(lo + rows, static_cast<long long>(a.S));
     const long long nb = static_cast<long long>(n) * a.S * a.C;
@@ -597,21 +805,22 @@ __global__ void __launch_bounds__(kThr) gn_backward_apply_kernel(const GnArgs a,
 #pragma unroll 2
         for (long long s = lo + r0; s < hi; s += sp.par) {
             const long long at = s * a.C + c;
-            float o[V] = {}, dg[V] = {};
+            float o[V] = {}, q[V] = {};
             if (s < L) {
-                float v[V], t[V], q[V] = {};
+                float v[V], t[V];
                 load<V>(x + at, v);
                 load<V>(dy + at, t);
                 if (GATE) load<V>(gate + at, q);
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float xh = (v[i] - st.x) * st.y;
-                    const float dz = dz_of<GATE>(a, t[i], xh, w[i], b[i], q[i], &dg[i]);
-                    o[i] = st.y * (w[i] * dz - gs.x - xh * gs.y);
-                }
+                dz_of<V, GATE>(a, st, w, b, v, t, q);
+                // r (w dz - gs.x - xhat gs.y)
+                vmul<V>(o, w, t);
+                vshift<V>(o, o, -gs.x);
+                vscale<V>(v, v, -gs.y);
+                vadd<V>(o, o, v);
+                vscale<V>(o, o, st.y);
             }
             store<V>(dx + at, o);
-            if (GATE) store<V>(dgate + at, dg);
+            if (GATE) store<V>(dgate + at, q);
         }
     }
 }
@@ -631,46 +840,52 @@ int team_of(const GnArgs &a, int V) {
     while (t < need && t < 32) t *= 2;
     return t;
 }
-// rows per CTA: 8 CTAs of 256 threads per SM, at least about 16K elements each
+// rows per CTA: 8 CTAs of 256 threads per SM, at least about 4K elements each
 int chunk_rows(const GnArgs &a) {
     const long long all = static_cast<long long>(a.N) * a.S;
     long long rows = (all + 148 * 8 - 1) / (148 * 8);
-    const long long least = (16384 + a.C - 1) / a.C;
+    const long long least = (4096 + a.C - 1) / a.C;
     if (rows < least) rows = least;
     if (rows > a.S) rows = a.S;
     return static_cast<int>(rows);
 }
-int row_backward_ctas(const GnArgs &a, int V) {
+// CTAs along the rows: `per_sm` of them per SM, if there are that many rows
+int row_ctas(const GnArgs &a, int V, int per_sm) {
     const int per = kThr / team_of(a, V), gpc = per < a.G ? per : a.G, rows = per / gpc;
     const int by = (a.G + gpc - 1) / gpc;
-    long long bx = (148 * 4 + by - 1) / by;
+    long long bx = (148 * per_sm + by - 1) / by;
     const long long most = (a.N + rows - 1) / rows;
     if (bx > most) bx = most;
     return static_cast<int>(bx < 1 ? 1 : bx);
 }
 size_t al(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
+// rows in flight per team
+template <int V, int K>
+constexpr int rows_held(bool backward) {
+    return V * K <= 8 ? 2 : 1;
+}
+
 template <typename TX, typename TY, int V, int K>
 cudaError_t row_forward(const GnArgs &a, cudaStream_t s) {
-    const int team = team_of(a, V);
-    const long long ctas = (static_cast<long long>(a.N) * a.G * team + kThr - 1) / kThr;
-    const unsigned grid = static_cast<unsigned>(ctas < 148 * 16 ? ctas : 148 * 16);
-    gn_row_forward_kernel<TX, TY, V, K><<<grid, kThr, 0, s>>>(a, team);
+    const int team = team_of(a, V), per = kThr / team, gpc = per < a.G ? per : a.G;
+    const dim3 grid(row_ctas(a, V, 8), (a.G + gpc - 1) / gpc);
+    gn_row_forward_kernel<TX, TY, V, K, rows_held<V, K>(false)><<<grid, kThr, 0, s>>>(a, team);
     return cudaGetLastError();
 }
 
 template <typename TX, typename TY, int V, int K>
 cudaError_t row_backward(const GnArgs &a, cudaStream_t s) {
     const int team = team_of(a, V), per = kThr / team, gpc = per < a.G ? per : a.G, rows = per / gpc;
-    const int bx = row_backward_ctas(a, V);
+    const int bx = row_ctas(a, V, 4);
     const dim3 grid(bx, (a.G + gpc - 1) / gpc);
     const int smem = rows * 2 * gpc * (a.C / a.G) * 4;
-    auto k = gn_row_backward_kernel<TX, TY, V, K>;
+    auto k = gn_row_backward_kernel<TX, TY, V, K, rows_held<V, K>(true)>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     k<<<grid, kThr, smem, s>>>(a, team, reinterpret_cast<float *>(a.ws));
-    gn_param_sum_kernel<<<dim3((a.C + 31) / 32, 2), 256, 0, s>>>(reinterpret_cast<float *>(a.ws), bx, a.C, a.dweight,
-                                                                a.dbias);
+    gn_param_sum_kernel<<<dim3((a.C + 31) / 32, 2), 1024, 0, s>>>(reinterpret_cast<float *>(a.ws), bx, a.C, a.dweight,
+                                                                 a.dbias);
     return cudaGetLastError();
 }
 
@@ -679,10 +894,10 @@ cudaError_t seq_forward(const GnArgs &a, cudaStream_t s) {
     const int rows = chunk_rows(a), chunks = (a.S + rows - 1) / rows;
     Moments *part = reinterpret_cast<Moments *>(a.ws);
     const unsigned grid = static_cast<unsigned>(chunks) * a.N;
-    gn_stats_kernel<TX, V><<<grid, kThr, a.G * sizeof(Moments), s>>>(a, rows, chunks, part);
+    gn_stats_kernel<TX, V><<<grid, threads_of<V>(a), a.G * sizeof(Moments), s>>>(a, rows, chunks, part);
     const long long warps = static_cast<long long>(a.N) * a.G;
     gn_stats_join_kernel<<<static_cast<unsigned>((warps * 32 + kThr - 1) / kThr), kThr, 0, s>>>(a, chunks, part);
-    gn_apply_kernel<TX, TY, V><<<grid, kThr, 0, s>>>(a, rows, chunks);
+    gn_apply_kernel<TX, TY, V><<<grid, threads_of<V>(a), 0, s>>>(a, rows, chunks);
     return cudaGetLastError();
 }
 
@@ -693,10 +908,10 @@ cudaError_t seq_backward_g(const GnArgs &a, cudaStream_t s) {
     float *part = reinterpret_cast<float *>(a.ws);
     float *chan = reinterpret_cast<float *>(a.ws + al(static_cast<size_t>(a.N) * chunks * 2 * a.C * 4));
     float *gsum = reinterpret_cast<float *>(reinterpret_cast<char *>(chan) + al(static_cast<size_t>(a.N) * 2 * a.C * 4));
-    gn_channel_sum_kernel<TX, TY, V, GATE><<<grid, kThr, 0, s>>>(a, rows, chunks, part);
-    gn_channel_join_kernel<<<a.N, kThr, 0, s>>>(a, chunks, part, chan, gsum);
-    gn_backward_apply_kernel<TX, TY, V, GATE><<<grid, kThr, 0, s>>>(a, rows, chunks, gsum);
-    gn_param_sum_kernel<<<dim3((a.C + 31) / 32, 2), 256, 0, s>>>(chan, a.N, a.C, a.dweight, a.dbias);
+    gn_channel_sum_kernel<TX, TY, V, GATE><<<grid, threads_of<V>(a), 0, s>>>(a, rows, chunks, part);
+    gn_channel_join_kernel<<<static_cast<unsigned>(a.N) * a.G, kThr, 0, s>>>(a, chunks, part, chan, gsum);
+    gn_backward_apply_kernel<TX, TY, V, GATE><<<grid, threads_of<V>(a), 0, s>>>(a, rows, chunks, gsum);
+    gn_param_sum_kernel<<<dim3((a.C + 31) / 32, 2), 1024, 0, s>>>(chan, a.N, a.C, a.dweight, a.dbias);
     return cudaGetLastError();
 }
 
@@ -738,7 +953,7 @@ cudaError_t by_type(const GnArgs &a, cudaStream_t s) {
 
 size_t gn_ws_bytes(const GnArgs &a, bool backward) {
     if (row_regime(a))
-        return backward ? al(static_cast<size_t>(row_backward_ctas(a, vec_of(a))) * 2 * a.C * 4) : 256;
+        return backward ? al(static_cast<size_t>(row_ctas(a, vec_of(a), 4)) * 2 * a.C * 4) : 256;
     const int rows = chunk_rows(a), chunks = (a.S + rows - 1) / rows;
     if (!backward) return al(static_cast<size_t>(a.N) * chunks * a.G * sizeof(Moments));
     return al(static_cast<size_t>(a.N) * chunks * 2 * a.C * 4) + al(static_cast<size_t>(a.N) * 2 * a.C * 4) +

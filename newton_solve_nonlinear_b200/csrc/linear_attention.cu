@@ -262,23 +262,34 @@ __global__ void __launch_bounds__(kThr) la_simt_kernel(const LaSweep w) {
 }
 
 // Join of a split sweep, in place: seg_state[s] (segment s's own state) becomes the state segment s starts from.
-__global__ void la_join_kernel(const LaSweep w) {
-    const long long n = static_cast<long long>(w.dk) * w.dv;
-    const int per = static_cast<int>((n + blockDim.x - 1) / blockDim.x);  // CTAs per head
-    const int bh = blockIdx.x / per;
-    const long long i = static_cast<long long>(blockIdx.x % per) * blockDim.x + threadIdx.x;
+// A thread per element; the segments' own states are loaded eight at a time, ahead of the recurrence.
+__global__ void __launch_bounds__(256) la_join_kernel(const LaSweep w) {
+    constexpr int KB = 8;
+    const int n = w.dk * w.dv;
+    const int per = (n + 255) / 256;  // CTAs per head
+    const int bh = blockIdx.x / per, i = (blockIdx.x % per) * 256 + threadIdx.x;
     if (i >= n) return;
     const float ld = safe_log_decay(w.log_decay[bh % w.H]);
     const int L = row_count(w, bh / w.H);
     float *p = w.seg_state + static_cast<long long>(bh) * w.n_seg * n + i;
-    float s = w.s_in == nullptr ? 0.f : w.s_in[bh * n + (i / w.dv) * w.s_i + (i % w.dv) * w.s_j];
+    float s = w.s_in == nullptr ? 0.f : w.s_in[static_cast<long long>(bh) * n + (i / w.dv) * w.s_i + (i % w.dv) * w.s_j];
     const float g_full = decay_pow(ld, w.seg);
-    for (int k = 0; k < w.n_seg; ++k) {
-        const int q = w.reverse ? w.n_seg - 1 - k : k;
-        const float own = k + 1 < w.n_seg ? p[q * n] : 0.f;
-        p[q * n] = s;
-        const long long rows = L - static_cast<long long>(q) * w.seg;  // of this segment, if not full
-        if (rows > 0) s = fmaf(rows >= w.seg ? g_full : decay_pow(ld, rows), s, own);
+    // the segment with the sequence's end, where it is not full
+    const int q_part = L / w.seg;
+    const float g_part = decay_pow(ld, L - q_part * w.seg);
+    const int first = w.reverse ? w.n_seg - 1 : 0, dir = w.reverse ? -1 : 1;
+    for (int k0 = 0; k0 < w.n_seg; k0 += KB) {
+        float own[KB];
+#pragma unroll
+        for (int k = 0; k < KB; ++k)  // the last one's own state is not wanted
+            own[k] = k0 + k + 1 < w.n_seg ? p[static_cast<long long>(first + dir * (k0 + k)) * n] : 0.f;
+#pragma unroll
+        for (int k = 0; k < KB; ++k)
+            if (k0 + k < w.n_seg) {
+                const int q = first + dir * (k0 + k);
+                p[static_cast<long long>(q) * n] = s;
+                if (q <= q_part) s = fmaf(q < q_part ? g_full : g_part, s, own[k]);
+            }
     }
 }
 
@@ -503,26 +514,36 @@ __global__ void __launch_bounds__(256) la_step_kernel(const LaStep w) {
             float vv[VW];
 #pragma unroll
             for (int u = 0; u < VW; ++u) vv[u] = tx * VW + u < w.dv ? to_f(v[tx * VW + u]) : 0.f;
-#pragma unroll 4
-            for (int d = ty; d < w.dk; d += NY) {
-                const long long at = static_cast<long long>(d) * w.dv + tx * VW;
-                float s[VW];
-                if (VW == 4) {
-                    const float4 x = __ldcs(reinterpret_cast<const float4 *>(src + at));
-                    s[0] = x.x, s[VW > 1 ? 1 : 0] = x.y, s[VW > 2 ? 2 : 0] = x.z, s[VW > 3 ? 3 : 0] = x.w;
-                } else {
-                    s[0] = src[at];
+            constexpr int RB = VW == 4 ? 8 : 16;  // rows of S in flight
+            for (int d0 = ty; d0 < w.dk; d0 += RB * NY) {
+                float s[RB][VW];
+#pragma unroll
+                for (int r = 0; r < RB; ++r) {
+                    const int d = d0 + r * NY;
+                    if (d >= w.dk) break;
+                    const float *p = src + d * w.dv + tx * VW;
+                    if constexpr (VW == 4) {
+                        const float4 x = __ldcs(reinterpret_cast<const float4 *>(p));
+                        s[r][0] = x.x, s[r][1] = x.y, s[r][2] = x.z, s[r][3] = x.w;
+                    } else {
+                        s[r][0] = *p;
+                    }
                 }
 #pragma unroll
-                for (int u = 0; u < VW; ++u) {
-                    s[u] = fmaf(ks[d], vv[u], g * s[u]);
-                    acc[u] = fmaf(qs[d], s[u], acc[u]);
+                for (int r = 0; r < RB; ++r) {
+                    const int d = d0 + r * NY;
+                    if (d >= w.dk) break;
+#pragma unroll
+                    for (int u = 0; u < VW; ++u) {
+                        s[r][u] = fmaf(ks[d], vv[u], g * s[r][u]);
+                        acc[u] = fmaf(qs[d], s[r][u], acc[u]);
+                    }
+                    float *p = dst + d * w.dv + tx * VW;
+                    if constexpr (VW == 4)
+                        __stcs(reinterpret_cast<float4 *>(p), make_float4(s[r][0], s[r][1], s[r][2], s[r][3]));
+                    else
+                        *p = s[r][0];
                 }
-                if (VW == 4)
-                    __stcs(reinterpret_cast<float4 *>(dst + at),
-                           make_float4(s[0], s[VW > 1 ? 1 : 0], s[VW > 2 ? 2 : 0], s[VW > 3 ? 3 : 0]));
-                else
-                    dst[at] = s[0];
             }
 #pragma unroll
             for (int u = 0; u < VW; ++u) part[ty * NX * VW + tx * VW + u] = acc[u];

@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         int done = 0;  // chunks issued whole
         auto scores = [&](int c) {
             const unsigned ta = sm + (c & 1) * Y::STAGE + Y::A, tb = sm + (c & 1) * Y::STAGE + Y::B;
-#pragma unroll
+#pragma unroll 2
             for (int k = 0; k < DK / 16; ++k) {
                 const unsigned off = (k >> 2) * kPanel + (k & 3) * 32;
                 mma_ss(tu + Y::T_S, sw128_desc(ta + off), sw128_desc(tb + off), id_scores, k > 0, on);
@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         };
         auto term = [&](int c, int place, bool first) {
             const unsigned tb = sm + (c & 1) * Y::STAGE + Y::B;
-#pragma unroll
+#pragma unroll 2
             for (int k = 0; k < kC / 16; ++k)
                 mma_ts(tu + Y::T_D, tu + Y::T_V + place * 64 + k * 8, nmajor_desc(tb + k * 2048), id_ds, !first || k > 0, on);
         };
@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                     if (!mbar_wait(smem_u32(&bars->ss), ph, err)) break;
                     if (c > 0 && !mbar_wait(smem_u32(&bars->out_read), ph ^ 1u, err)) break;
                     fence_after();
-#pragma unroll
+#pragma unroll 2
                     for (int k = 0; k < DK / 16; ++k)
                         mma_ss(tu + Y::T_O, sw128_desc(ta + (k >> 2) * kPanel + (k & 3) * 32),
                                sw128_desc(sm + Y::SS + (k >> 2) * (DV * 128) + (k & 3) * 32), id_inter, k > 0, on);
@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                 if (!STATE_ONLY) {
                     if (!mbar_wait(smem_u32(&bars->scaled), ph, err)) break;
                     fence_after();
-#pragma unroll
+#pragma unroll 2
                     for (int k = 0; k < kC / 16; ++k)
                         mma_ts(tu + Y::T_O, tu + Y::T_S + (k >> 2) * 64 + (k & 3) * 8, nmajor_desc(tc_ + k * 2048), id_out,
                                true, on);
