@@ -39,11 +39,11 @@ __device__ __forceinline__ int row_count(const LaSweep &w, int b) {
 
 constexpr int kC = 32;     // rows per chunk
 constexpr int kDVT = 64;   // columns of c per CTA
-constexpr int kThr = 128;
+constexpr int kThr = 256;
 
 template <int DKP>
 constexpr int simt_smem_floats() {
-    return 2 * kC * (DKP + 4) + kC * (kDVT + 4) + kC * (kC + 4) + DKP * (kDVT + 4) + kC + 4;
+    return 2 * kC * (DKP + 4) + 2 * kC * (kDVT + 4) + kC * (kC + 4) + DKP * (kDVT + 4) + kC + 4;
 }
 
 __device__ __forceinline__ void fma4(float4 &acc, float x, const float4 &y) {
@@ -52,14 +52,45 @@ __device__ __forceinline__ void fma4(float4 &acc, float x, const float4 &y) {
     acc.z = fmaf(x, y.z, acc.z);
     acc.w = fmaf(x, y.w, acc.w);
 }
+__device__ __forceinline__ float4 *f4(float *p) { return reinterpret_cast<float4 *>(p); }
 
-// One CTA: 64 columns of c of one head and one segment, chunk after chunk, the state in shared memory.
+// acc[u] += sum_d x[i0 + u][d] y[d][j0 .. j0 + 3] for u < 4, rows of x and y PX and PY floats apart
+template <int PX, int PY>
+__device__ __forceinline__ void product4x4(float4 (&acc)[4], float *x, float *y, int depth) {
+#pragma unroll 2
+    for (int d = 0; d < depth; d += 4) {
+        float4 xv[4], yv[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            xv[u] = *f4(x + u * PX + d);
+            yv[u] = *f4(y + (d + u) * PY);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            fma4(acc[u], xv[u].x, yv[0]);
+            fma4(acc[u], xv[u].y, yv[1]);
+            fma4(acc[u], xv[u].z, yv[2]);
+            fma4(acc[u], xv[u].w, yv[3]);
+        }
+    }
+}
+
+struct LaBatch {
+    LaSweep w[3];
+};
+
+// One CTA: 64 columns of c of one head and one segment, 32 rows at a time, the state in shared memory; fp32 FMAs.
+// Warps 0-3 form a S while warps 4-7 form the weighted scores and their product with c; then all update S.  The
+// next chunk's rows are loaded into registers before a chunk's arithmetic.  Bound by FMA issue and shared-memory
+// loads (8 loads of 16 bytes for 64 FMAs); 32 rows, because the scores' share of the arithmetic grows with them.
 // STATE_ONLY is pass 1 of a split sweep: the segment's own S_out, without a and without outputs.
 template <bool VEC, int DKP, bool STATE_ONLY>
-__global__ void __launch_bounds__(kThr) la_simt_kernel(const LaSweep w) {
+__global__ void __launch_bounds__(kThr, 2) la_simt_kernel(const __grid_constant__ LaBatch batch) {
+    const LaSweep &w = batch.w[blockIdx.z];
+    if (blockIdx.x >= w.B * w.H * ((w.dv + kDVT - 1) / kDVT)) return;  // the grid is the widest sweep's
     constexpr int PK = DKP + 4, PV = kDVT + 4, PP = kC + 4;
     extern __shared__ __align__(16) float sm[];
-    float *As = sm, *Bs = As + kC * PK, *Cs = Bs + kC * PK, *Ps = Cs + kC * PV, *Ss = Ps + kC * PP;
+    float *As = sm, *Bs = As + kC * PK, *Cs = Bs + kC * PK, *Os = Cs + kC * PV, *Ps = Os + kC * PV, *Ss = Ps + kC * PP;
     float *pw = Ss + DKP * PV;  // g^0 .. g^C
 
     const int tid = threadIdx.x;
@@ -96,117 +127,112 @@ __global__ void __launch_bounds__(kThr) la_simt_kernel(const LaSweep w) {
     const float *pc = static_cast<const float *>(w.c.p) + b * w.c.sb + (h / w.c.group) * w.c.sh + c0;
     float *po = static_cast<float *>(w.out) + (static_cast<long long>(b) * w.T * w.H + h) * w.out_w + c0;
     const long long ost = static_cast<long long>(w.H) * w.out_w;
+    const bool rev = w.reverse != 0;
+    const int e = w.e;
+    const float intra = w.intra, inter = w.inter, update = w.update;
 
+    // this thread's pieces of the next chunk: a, b [C][DKP] and c [C][64], zeros outside
+    constexpr int NK = kC * DKP / 4 / kThr, NV = kC * kDVT / 4 / kThr;
+    float4 ra[NK], rb[NK], rc[NV];
+    auto fetch = [&](int r0) {
+        const int n = min(kC, hi - r0);
+#pragma unroll
+        for (int k = 0; k < NK; ++k) {
+            const int i = tid + k * kThr, r = i / (DKP / 4), d = (i % (DKP / 4)) * 4;
+            ra[k] = rb[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < n && d < w.dk) {
+                const long long t = rev ? L - 1 - (r0 + r) : r0 + r;
+                if (!STATE_ONLY) ra[k] = load4<VEC>(pa + t * w.a.st + d, w.dk - d);
+                rb[k] = load4<VEC>(pb + t * w.b.st + d, w.dk - d);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int i = tid + k * kThr, r = i / (kDVT / 4), c = (i % (kDVT / 4)) * 4;
+            rc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < n && c < ncol) {
+                const long long t = rev ? L - 1 - (r0 + r) : r0 + r;
+                rc[k] = load4<VEC>(pc + t * w.c.st + c, ncol - c);
+            }
+        }
+    };
+    if (lo < hi) fetch(lo);
     for (int r0 = lo; r0 < hi; r0 += kC) {
         const int n = min(kC, hi - r0);
         __syncthreads();
-        // a, b [C][DKP] and c [C][64] as fp32, zeros outside
-        for (int i = tid; i < kC * (DKP / 4); i += kThr) {
-            const int r = i / (DKP / 4), d = (i % (DKP / 4)) * 4;
-            float4 va = make_float4(0.f, 0.f, 0.f, 0.f), vb = va;
-            if (r < n && d < w.dk) {
-                const long long t = w.reverse ? L - 1 - (r0 + r) : r0 + r;
-                if (!STATE_ONLY) va = load4<VEC>(pa + t * w.a.st + d, w.dk - d);
-                vb = load4<VEC>(pb + t * w.b.st + d, w.dk - d);
-            }
-            if (!STATE_ONLY) *reinterpret_cast<float4 *>(As + r * PK + d) = va;
-            *reinterpret_cast<float4 *>(Bs + r * PK + d) = vb;
+#pragma unroll
+        for (int k = 0; k < NK; ++k) {
+            const int i = tid + k * kThr, at = i / (DKP / 4) * PK + (i % (DKP / 4)) * 4;
+            if (!STATE_ONLY) *f4(As + at) = ra[k];
+            *f4(Bs + at) = rb[k];
         }
-        for (int i = tid; i < kC * (kDVT / 4); i += kThr) {
-            const int r = i / (kDVT / 4), c = (i % (kDVT / 4)) * 4;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < n && c < ncol) {
-                const long long t = w.reverse ? L - 1 - (r0 + r) : r0 + r;
-                v = load4<VEC>(pc + t * w.c.st + c, ncol - c);
-            }
-            *reinterpret_cast<float4 *>(Cs + r * PV + c) = v;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int i = tid + k * kThr;
+            *f4(Cs + i / (kDVT / 4) * PV + (i % (kDVT / 4)) * 4) = rc[k];
         }
         __syncthreads();
+        if (r0 + kC < hi) fetch(r0 + kC);
         if (!STATE_ONLY) {
-            {  // P = (a b^T) weighted, 2 x 4 per thread
-                const int i0 = (tid / 8) * 2, j0 = tid % 8;
-                float acc[2][4] = {};
-                if (i0 < n) {
+            const int t = tid & 127, i0 = (t / 16) * 4, j0 = (t % 16) * 4;  // 4 x 4 outputs of each half's 128 threads
+            float4 acc[4] = {};
+            if (tid < 128) {
+                if (i0 < n) product4x4<PK, PV>(acc, As + i0 * PK, Ss + j0, DKP);
+            } else {
+                // P = (a b^T) weighted, 2 x 4 per thread
+                const int p0 = (t / 8) * 2, q0 = t % 8;
+                float s[2][4] = {};
+                if (p0 < n) {
 #pragma unroll 4
                     for (int d = 0; d < DKP; d += 4) {
                         float4 x[2], y[4];
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) x[u] = *reinterpret_cast<const float4 *>(As + (i0 + u) * PK + d);
+                        for (int u = 0; u < 2; ++u) x[u] = *f4(As + (p0 + u) * PK + d);
 #pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            y[u] = *reinterpret_cast<const float4 *>(Bs + (j0 + 8 * u) * PK + d);
+                        for (int u = 0; u < 4; ++u) y[u] = *f4(Bs + (q0 + 8 * u) * PK + d);
 #pragma unroll
                         for (int u = 0; u < 2; ++u)
 #pragma unroll
                             for (int q = 0; q < 4; ++q)
-                                acc[u][q] += x[u].x * y[q].x + x[u].y * y[q].y + x[u].z * y[q].z + x[u].w * y[q].w;
+                                s[u][q] += x[u].x * y[q].x + x[u].y * y[q].y + x[u].z * y[q].z + x[u].w * y[q].w;
                     }
                 }
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const int i = i0 + u, j = j0 + 8 * q;
-                        Ps[i * PP + j] = i >= j ? acc[u][q] * pw[i >= j ? i - j : 0] * w.intra : 0.f;
+                        const int i = p0 + u, j = q0 + 8 * q;
+                        Ps[i * PP + j] = i >= j ? s[u][q] * pw[i >= j ? i - j : 0] * intra : 0.f;
                     }
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                if (i0 < n) product4x4<PP, PV>(acc, Ps + i0 * PP, Cs + j0, i0 + 4);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) *f4(Os + (i0 + u) * PV + j0) = acc[u];
             }
             __syncthreads();
-            {  // out = P c + g^(i+e) (a S): 4 x 4 per thread
-                const int i0 = (tid / 16) * 4, j0 = (tid % 16) * 4;
-                float4 acc[4] = {};
-                if (i0 < n) {
-#pragma unroll 2
-                    for (int d = 0; d < DKP; d += 4) {
-                        float4 x[4], y[4];
+            if (tid < 128) {
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            x[u] = *reinterpret_cast<const float4 *>(As + (i0 + u) * PK + d);
-                            y[u] = *reinterpret_cast<const float4 *>(Ss + (d + u) * PV + j0);
-                        }
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            fma4(acc[u], x[u].x, y[0]);
-                            fma4(acc[u], x[u].y, y[1]);
-                            fma4(acc[u], x[u].z, y[2]);
-                            fma4(acc[u], x[u].w, y[3]);
-                        }
-                    }
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const float f = pw[min(i0 + u + w.e, kC)] * w.inter;
-                        acc[u].x *= f, acc[u].y *= f, acc[u].z *= f, acc[u].w *= f;
-                    }
-                    for (int j = 0; j < i0 + 4; j += 4) {
-                        float4 x[4], y[4];
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            x[u] = *reinterpret_cast<const float4 *>(Ps + (i0 + u) * PP + j);
-                            y[u] = *reinterpret_cast<const float4 *>(Cs + (j + u) * PV + j0);
-                        }
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            fma4(acc[u], x[u].x, y[0]);
-                            fma4(acc[u], x[u].y, y[1]);
-                            fma4(acc[u], x[u].z, y[2]);
-                            fma4(acc[u], x[u].w, y[3]);
-                        }
-                    }
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        if (i0 + u < n) {
-                            const long long t = w.reverse ? L - 1 - (r0 + i0 + u) : r0 + i0 + u;
-                            float *o = po + t * ost + j0;
-                            const float f[4] = {acc[u].x, acc[u].y, acc[u].z, acc[u].w};
+                for (int u = 0; u < 4; ++u)
+                    if (i0 + u < n) {
+                        const float g = pw[min(i0 + u + e, kC)] * inter;
+                        const float4 y = *f4(Os + (i0 + u) * PV + j0);
+                        const long long tok = rev ? L - 1 - (r0 + i0 + u) : r0 + i0 + u;
+                        float *o = po + tok * ost + j0;
+                        const float4 x = make_float4(fmaf(g, acc[u].x, y.x), fmaf(g, acc[u].y, y.y),
+                                                     fmaf(g, acc[u].z, y.z), fmaf(g, acc[u].w, y.w));
+                        if (VEC) {  // widths are multiples of 4
+                            if (j0 < ncol) *f4(o) = x;
+                        } else {
+                            const float f[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                             for (int q = 0; q < 4; ++q)
                                 if (j0 + q < ncol) o[q] = f[q];
                         }
-                }
+                    }
             }
-            __syncthreads();
         }
-        {  // S = g^n S + update sum_j g^(n-e-j) b_j c_j^T: DKP/16 x 8 per thread
-            constexpr int RD = DKP / 16;
+        {  // S = g^n S + update sum_j g^(n-e-j) b_j c_j^T: DKP/32 x 8 per thread
+            constexpr int RD = DKP / 32;
             const int d0 = (tid / 8) * RD, j0 = (tid % 8) * 4;
             float4 acc[RD][2];
             const float gn = pw[n];
@@ -214,29 +240,31 @@ __global__ void __launch_bounds__(kThr) la_simt_kernel(const LaSweep w) {
             for (int u = 0; u < RD; ++u)
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    acc[u][q] = *reinterpret_cast<const float4 *>(Ss + (d0 + u) * PV + j0 + 32 * q);
+                    acc[u][q] = *f4(Ss + (d0 + u) * PV + j0 + 32 * q);
                     acc[u][q].x *= gn, acc[u][q].y *= gn, acc[u][q].z *= gn, acc[u][q].w *= gn;
                 }
+#pragma unroll 2
             for (int j = 0; j < n; ++j) {
-                const float f = pw[n - w.e - j] * w.update;
-                float4 y[2];
+                const float f = pw[n - e - j] * update;
+                float x[RD];
+                if constexpr (RD == 4) {
+                    const float4 v = *f4(Bs + j * PK + d0);
+                    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+                } else {
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    y[q] = *reinterpret_cast<const float4 *>(Cs + j * PV + j0 + 32 * q);
-                    y[q].x *= f, y[q].y *= f, y[q].z *= f, y[q].w *= f;
+                    for (int u = 0; u < RD; ++u) x[u] = Bs[j * PK + d0 + u];
                 }
+                const float4 y0 = *f4(Cs + j * PV + j0), y1 = *f4(Cs + j * PV + j0 + 32);
 #pragma unroll
                 for (int u = 0; u < RD; ++u) {
-                    const float x = Bs[j * PK + d0 + u];
-                    fma4(acc[u][0], x, y[0]);
-                    fma4(acc[u][1], x, y[1]);
+                    fma4(acc[u][0], x[u] * f, y0);
+                    fma4(acc[u][1], x[u] * f, y1);
                 }
             }
 #pragma unroll
             for (int u = 0; u < RD; ++u)
 #pragma unroll
-                for (int q = 0; q < 2; ++q)
-                    *reinterpret_cast<float4 *>(Ss + (d0 + u) * PV + j0 + 32 * q) = acc[u][q];
+                for (int q = 0; q < 2; ++q) *f4(Ss + (d0 + u) * PV + j0 + 32 * q) = acc[u][q];
         }
     }
     __syncthreads();
@@ -303,36 +331,54 @@ cudaError_t launch_la_join(const LaSweep &w, cudaStream_t s) {
 namespace {
 
 template <bool VEC, int DKP>
-cudaError_t launch_simt(const LaSweep &w, cudaStream_t s) {
+cudaError_t launch_simt(const LaBatch &t, int n, cudaStream_t s) {
     const int smem = simt_smem_floats<DKP>() * 4;
-    const dim3 grid(static_cast<unsigned>(w.B) * w.H * ((w.dv + kDVT - 1) / kDVT), w.n_seg);
+    unsigned tiles = 0;
+    for (int i = 0; i < n; ++i) tiles = max(tiles, static_cast<unsigned>((t.w[i].dv + kDVT - 1) / kDVT));
+    const LaSweep &w = t.w[0];
+    const dim3 grid(static_cast<unsigned>(w.B) * w.H * tiles, w.n_seg, n);
     cudaError_t e;
     if (w.n_seg > 1) {
         auto k1 = la_simt_kernel<VEC, DKP, true>;
         if ((e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
-        k1<<<grid, kThr, smem, s>>>(w);
-        if ((e = launch_la_join(w, s)) != cudaSuccess) return e;
+        k1<<<grid, kThr, smem, s>>>(t);
+        for (int i = 0; i < n; ++i)
+            if ((e = launch_la_join(t.w[i], s)) != cudaSuccess) return e;
     }
     auto k = la_simt_kernel<VEC, DKP, false>;
     if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
-    k<<<grid, kThr, smem, s>>>(w);
+    k<<<grid, kThr, smem, s>>>(t);
     return cudaGetLastError();
 }
 
-template <bool VEC>
-cudaError_t pick_width(const LaSweep &w, cudaStream_t s) {
-    if (w.dk <= 32) return launch_simt<VEC, 32>(w, s);
-    if (w.dk <= 64) return launch_simt<VEC, 64>(w, s);
-    return launch_simt<VEC, 128>(w, s);
-}
+// width of a and b that the kernel is compiled for
+int simt_width(const LaSweep &w) { return w.dk <= 32 ? 32 : w.dk <= 64 ? 64 : w.dk <= 96 ? 96 : 128; }
 
 bool rows_vec4(const LaRows &x) {
     return reinterpret_cast<uintptr_t>(x.p) % 16 == 0 && x.sb % 4 == 0 && x.st % 4 == 0 && x.sh % 4 == 0;
 }
+bool simt_vec(const LaSweep &w) {
+    return w.dk % 4 == 0 && w.dv % 4 == 0 && w.out_w % 4 == 0 && rows_vec4(w.a) && rows_vec4(w.b) && rows_vec4(w.c);
+}
 
-cudaError_t launch_simt_any(const LaSweep &w, cudaStream_t s) {
-    const bool vec = w.dk % 4 == 0 && w.dv % 4 == 0 && rows_vec4(w.a) && rows_vec4(w.b) && rows_vec4(w.c);
-    return vec ? pick_width<true>(w, s) : pick_width<false>(w, s);
+template <bool VEC>
+cudaError_t pick_width(const LaBatch &t, int n, cudaStream_t s) {
+    switch (simt_width(t.w[0])) {
+        case 32: return launch_simt<VEC, 32>(t, n, s);
+        case 64: return launch_simt<VEC, 64>(t, n, s);
+        case 96: return launch_simt<VEC, 96>(t, n, s);
+        default: return launch_simt<VEC, 128>(t, n, s);
+    }
+}
+
+// n <= 3 sweeps in one launch
+cudaError_t launch_la_simt(const LaSweep *w, int n, cudaStream_t s) {
+    LaBatch t{};
+    for (int i = 0; i < n; ++i) t.w[i] = w[i];
+    return simt_vec(w[0]) ? pick_width<true>(t, n, s) : pick_width<false>(t, n, s);
+}
+bool simt_together(const LaSweep &x, const LaSweep &y) {
+    return simt_width(x) == simt_width(y) && simt_vec(x) == simt_vec(y) && x.n_seg == y.n_seg && x.seg == y.seg;
 }
 
 }  // namespace
@@ -349,10 +395,10 @@ LaPlan la_plan(int B, int T, int H, int dv, int dtype, int sweeps) {
         most = T / 512;
         unit = 128;
     } else {
-        // enough CTAs for several waves of the SMs' resident CTAs, in segments of at least 256 rows
+        // enough CTAs for two waves of the SMs' resident CTAs (two each), in segments of at least 128 rows
         const long long ctas = heads * ((dv + kDVT - 1) / kDVT);
         want = (148 * 4 + ctas - 1) / ctas;
-        most = T / 256;
+        most = T / 128;
         unit = kC;
     }
     if (want > most) want = most;
@@ -371,7 +417,8 @@ cudaError_t launch_la_sweeps(const LaSweep *w, int n, cudaStream_t s) {
             while (i + k < n && la_tc_together(w[i], w[i + k])) ++k;
             e = launch_la_tc(w + i, k, s);
         } else {
-            e = launch_simt_any(w[i], s);
+            while (i + k < n && simt_together(w[i], w[i + k])) ++k;
+            e = launch_la_simt(w + i, k, s);
         }
         if (e != cudaSuccess) return e;
         i += k;
