@@ -137,7 +137,7 @@ void build_forward(Call &c, const pararnn_rows &q, const pararnn_rows &k, const 
                    const float *s0, const int *lengths, void *o, float *s_out) {
     const pararnn_attention_shape &s = c.s;
     LaSweep &w = c.w[0];
-    c.sweep(w, log_decay, lengths, s.dk, s.dv, la_plan(s.B, s.T, s.H, s.dv, s.dtype, 1));
+    c.sweep(w, log_decay, lengths, s.dk, s.dv, la_plan(s.B, s.T, s.H, s.dv, s.dtype, 1, lengths != nullptr));
     w.a = c.in(q, s.H, s.dk), w.b = c.in(k, s.Hkv, s.dk), w.c = c.in(v, s.Hkv, s.dv);
     w.s_in = s0, w.s_out = s_out, w.s_i = s.dv, w.s_j = 1;
     c.out(w, o, s.dv);
@@ -156,8 +156,8 @@ Partials build_backward(Call &c, const pararnn_rows &q, const pararnn_rows &k, c
     Partials part{};
     const LaRows rq = c.in(q, s.H, s.dk), rk = c.in(k, s.Hkv, s.dk), rv = c.in(v, s.Hkv, s.dv),
                  ro = c.in(d_o, s.H, s.dv);
-    const LaPlan plan_v = la_plan(s.B, s.T, s.H, s.dv, s.dtype, 3);  // the sweep whose state is [dk, dv]
-    const LaPlan plan_k = la_plan(s.B, s.T, s.H, s.dk, s.dtype, 3);  // the sweeps whose state is [dv, dk]
+    const LaPlan plan_v = la_plan(s.B, s.T, s.H, s.dv, s.dtype, 3, lengths != nullptr);  // the sweep whose state is [dk, dv]
+    const LaPlan plan_k = la_plan(s.B, s.T, s.H, s.dk, s.dtype, 3, lengths != nullptr);  // the sweeps whose state is [dv, dk]
 
     // dq: the forward sweep on (do, v, k) from S_0^T
     LaSweep &x = c.w[0];
@@ -200,9 +200,14 @@ extern "C" {
 size_t pararnn_linear_attention_workspace_size(const pararnn_attention_shape *shape, const pararnn_rows *q,
                                                const pararnn_rows *k, const pararnn_rows *v) {
     if (!shape_ok(shape) || !rows_ok(q, shape->dtype) || !rows_ok(k, shape->dtype) || !rows_ok(v, shape->dtype)) return 0;
-    Call c(*shape, nullptr);
-    build_forward(c, *q, *k, *v, nullptr, nullptr, nullptr, nullptr, nullptr);
-    return c.ws.used ? c.ws.used : 256;
+    size_t most = 256;
+    const int some = 0;
+    for (const int *lengths : {static_cast<const int *>(nullptr), &some}) {  // with lengths or without: the larger
+        Call c(*shape, nullptr);
+        build_forward(c, *q, *k, *v, nullptr, nullptr, lengths, nullptr, nullptr);
+        most = c.ws.used > most ? c.ws.used : most;
+    }
+    return most;
 }
 
 int pararnn_linear_attention(const pararnn_attention_shape *shape, const pararnn_rows *q, const pararnn_rows *k,
@@ -233,9 +238,14 @@ size_t pararnn_linear_attention_backward_workspace_size(const pararnn_attention_
     if (!shape_ok(shape) || !rows_ok(q, shape->dtype) || !rows_ok(k, shape->dtype) || !rows_ok(v, shape->dtype) ||
         !rows_ok(d_o, shape->dtype))
         return 0;
-    Call c(*shape, nullptr);
-    build_backward(c, *q, *k, *v, nullptr, *d_o, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr);
-    return c.ws.used ? c.ws.used : 256;
+    size_t most = 256;
+    const int some = 0;
+    for (const int *lengths : {static_cast<const int *>(nullptr), &some}) {
+        Call c(*shape, nullptr);
+        build_backward(c, *q, *k, *v, nullptr, *d_o, nullptr, nullptr, lengths, nullptr, nullptr, nullptr, nullptr);
+        most = c.ws.used > most ? c.ws.used : most;
+    }
+    return most;
 }
 
 int pararnn_linear_attention_backward(const pararnn_attention_shape *shape, const pararnn_rows *q,

@@ -383,7 +383,7 @@ bool simt_together(const LaSweep &x, const LaSweep &y) {
 
 }  // namespace
 
-LaPlan la_plan(int B, int T, int H, int dv, int dtype, int sweeps) {
+LaPlan la_plan(int B, int T, int H, int dv, int dtype, int sweeps, bool ragged) {
     const long long heads = static_cast<long long>(B) * H * sweeps;
     long long want, most;
     int unit;
@@ -395,9 +395,11 @@ LaPlan la_plan(int B, int T, int H, int dv, int dtype, int sweeps) {
         most = T / 512;
         unit = 128;
     } else {
-        // enough CTAs for two waves of the SMs' resident CTAs (two each), in segments of at least 128 rows
+        // two CTAs per SM, filled once, in segments of at least 128 rows; 1.5 times that many CTAs where lengths may
+        // differ, so that short sequences leave room ([8, 2048, 16 x 64]: 342 us in 2 segments, 377 in 4; five
+        // sequences of up to 2011 tokens, 12 heads of 96 and 80: 377 us in 2, 293 in 4)
         const long long ctas = heads * ((dv + kDVT - 1) / kDVT);
-        want = (148 * 4 + ctas - 1) / ctas;
+        want = ragged ? (444 + ctas - 1) / ctas : 296 / ctas;
         most = T / 128;
         unit = kC;
     }
