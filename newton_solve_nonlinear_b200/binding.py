@@ -768,76 +768,75 @@ def affine_scan_host(A_host, b_host, h0_host, *, parts: int = 7, out=None, works
 # ---- sequence layers: linear attention with a decay for each head, group norm -------------------------------
 
 
-class _on:
-    """The launch context of a call on tensors of ``device``: makes it the current device and, where the caller
-    names a stream, allocates on that stream, so that the allocator keeps the call's own memory in order with it."""
-
-    def __init__(self, device, stream):
-        self.enter = []
-        if device.type == "cuda":
-            if stream is not None:
-                self.enter.append(torch.cuda.stream(stream))
-            elif torch.cuda.current_device() != device.index:
-                self.enter.append(torch.cuda.device(device))
-
-    def __enter__(self):
-        for c in self.enter:
-            c.__enter__()
-
-    def __exit__(self, *exc):
-        for c in reversed(self.enter):
-            c.__exit__(*exc)
+def _context(t, stream):
+    """What a call on ``t`` has to be made under: the caller's stream, so that the call's own allocations belong to it,
+    or t's device where another one is current; None where neither applies."""
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    if t.is_cuda and t.get_device() != torch.cuda.current_device():
+        return torch.cuda.device(t.get_device())
+    return None
 
 
-def _like(t, name: str, like, shape, dtype):
-    """Checks an argument's device, shape and type; the address of a dense tensor, None for None."""
-    if t is None:
-        return None
-    if t.device != like.device:
+def _current(t) -> int:
+    """The current stream of t's device, as a cudaStream_t."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _refuse(t, name: str, like, shape, dtype):
+    if t.get_device() != like.get_device():
         raise ValueError(f"{name} must be on {like.device}, got {t.device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != torch.Size(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return _dev(t, name)
+    raise ValueError(f"{name} must be contiguous{'' if t.is_contiguous() else ' along its last axis'}")
+
+
+def _like(t, name: str, like, shape, dtype):
+    """The address of a dense tensor of this shape and type on like's device, None for None; else raises."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or t.get_device() != like.get_device() or not t.is_contiguous():
+        _refuse(t, name, like, shape, dtype)
+    return t.data_ptr()
 
 
 def _rows(t, name: str, like, shape):
-    """A [B, T, heads, width] operand of like's type, strided in all but the last axis."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device != like.device:
-        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
-    if t.dtype != like.dtype:
-        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
-    if t.shape != torch.Size(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    sb, st, sh, sw = t.stride()
-    if sw != 1 and shape[3] != 1:
-        raise ValueError(f"{name} must be contiguous along its last axis")
-    return Rows(t.data_ptr(), sb, st, sh)
+    """A [B, T, heads, width] operand (or [B, heads, width]) of like's type, strided in all but the last axis."""
+    st = t.stride()
+    if (t.dtype != like.dtype or t.shape != shape or t.get_device() != like.get_device()
+            or (st[-1] != 1 and shape[-1] != 1)):
+        _refuse(t, name, like, shape, like.dtype)
+    return Rows(t.data_ptr(), st[0], st[1] if len(st) == 4 else 0, st[-2])
 
 
-def _attention_shape(q, k, v, log_decay, scale):
-    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
-        raise ValueError("q, k and v must be [B, T, heads, width]")
-    B, T, H, dk = q.shape
-    Hkv, dv = k.shape[2], v.shape[3]
+def _attention_shape(q, k, v, log_decay, scale, dims: int = 4):
+    if q.dim() != dims or k.dim() != dims or v.dim() != dims:
+        raise ValueError("q, k and v must be " + ("[B, T, heads, width]" if dims == 4 else "[B, heads, width]"))
+    lead = q.shape[:-2]
+    B, T = lead[0], lead[1] if dims == 4 else 1
+    (H, dk), Hkv, dv = q.shape[-2:], k.shape[-2], v.shape[-1]
     if min(B, T, H, Hkv) < 1 or H % Hkv:
         raise ValueError(f"B, T and the head counts must be positive, q's heads a multiple of k's: {H} and {Hkv}")
     if not (1 <= dk <= 128 and 1 <= dv <= 128):
         raise ValueError(f"head widths must be 1 to 128: got {dk} and {dv}")
     if log_decay.requires_grad:
         raise ValueError("log_decay is a constant of the model: it gets no gradient")
-    shape = AttentionShape(B, T, H, Hkv, dk, dv, _dtype_code(q.dtype), dk ** -0.5 if scale is None else float(scale))
-    return shape, _rows(q, "q", q, (B, T, H, dk)), _rows(k, "k", q, (B, T, Hkv, dk)), _rows(v, "v", q, (B, T, Hkv, dv))
+    shape = AttentionShape(B, T, H, Hkv, dk, dv, _dtype_code(q.dtype), dk ** -0.5 if scale is None else scale)
+    if not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    return (shape, _rows(q, "q", q, (*lead, H, dk)), _rows(k, "k", q, (*lead, Hkv, dk)),
+            _rows(v, "v", q, (*lead, Hkv, dv)))
 
 
 def _workspace(need: int, name: str, workspace, device):
     if need == 0:
         raise ValueError(f"arguments rejected by {name}_workspace_size")
     if workspace is None:
-        return alloc_workspace(need, device)
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        if workspace.data_ptr() % 256:
+            workspace = alloc_workspace(need, device)
     return workspace
 
 
@@ -855,21 +854,23 @@ def linear_attention(q, k, v, log_decay, *, s0=None, lengths=None, scale=None, o
     fp32 <= 0, s0 [B,H,dk,dv] fp32 the state before (zero if None), lengths [B]
     int32 (tokens behind them are not read, outputs there are zero), scale
     dk**-0.5 if None.  Returns (o [B,T,H,dv] of q's type, the last state
-    [B,H,dk,dv] fp32); ``out`` gives both tensors."""
-    with _on(q.device, stream):
-        shape, rq, rk, rv = _attention_shape(q, k, v, log_decay, scale)
-        B, T, H, dk, dv = shape.B, shape.T, shape.H, shape.dk, shape.dv
-        o, s = out if out is not None else (torch.empty(B, T, H, dv, dtype=q.dtype, device=q.device),
-                                            torch.empty(B, H, dk, dv, dtype=torch.float32, device=q.device))
-        L = lib()
-        ws = _workspace(L.pararnn_linear_attention_workspace_size(shape, rq, rk, rv), "pararnn_linear_attention", workspace,
-                        q.device)
-        rc = L.pararnn_linear_attention(
-            shape, rq, rk, rv, _like(log_decay, "log_decay", q, (H,), torch.float32),
-            _like(s0, "s0", q, (B, H, dk, dv), torch.float32), _like(lengths, "lengths", q, (B,), torch.int32),
-            _like(o, "out", q, (B, T, H, dv), q.dtype), _like(s, "out", q, (B, H, dk, dv), torch.float32),
-            _dev(ws, "workspace"), ws.numel(), _stream(stream))
-    _checked(rc, "pararnn_linear_attention")
+    [B,H,dk,dv] fp32); ``out`` gives both tensors (the state's may be s0)."""
+    under = _context(q, stream)
+    if under is not None:
+        with under:
+            return linear_attention(q, k, v, log_decay, s0=s0, lengths=lengths, scale=scale, out=out, workspace=workspace)
+    shape, rq, rk, rv = _attention_shape(q, k, v, log_decay, scale)
+    B, T, H, dk, dv = shape.B, shape.T, shape.H, shape.dk, shape.dv
+    o, s = out if out is not None else (torch.empty(B, T, H, dv, dtype=q.dtype, device=q.device),
+                                        torch.empty(B, H, dk, dv, dtype=torch.float32, device=q.device))
+    L = lib()
+    ws = _workspace(L.pararnn_linear_attention_workspace_size(shape, rq, rk, rv), "pararnn_linear_attention", workspace,
+                    q.device)
+    _checked(L.pararnn_linear_attention(
+        shape, rq, rk, rv, _like(log_decay, "log_decay", q, (H,), torch.float32),
+        _like(s0, "s0", q, (B, H, dk, dv), torch.float32), _like(lengths, "lengths", q, (B,), torch.int32),
+        _like(o, "out", q, (B, T, H, dv), q.dtype), _like(s, "out", q, (B, H, dk, dv), torch.float32),
+        _dev(ws, "workspace"), ws.numel(), _current(q)), "pararnn_linear_attention")
     return o, s
 
 
@@ -879,24 +880,27 @@ def linear_attention_backward(q, k, v, log_decay, do, *, s0=None, ds=None, lengt
     type, strided as q), ds [B,H,dk,dv] fp32 the gradient of the last state
     (zero if None); the rest as given to the forward pass.  Returns dict(dq,
     dk, dv, ds0) of q's type (ds0 fp32, None without s0)."""
-    with _on(q.device, stream):
-        shape, rq, rk, rv = _attention_shape(q, k, v, log_decay, scale)
-        B, T, H, Hkv, dk, dv = shape.B, shape.T, shape.H, shape.Hkv, shape.dk, shape.dv
-        rdo = _rows(do, "do", q, (B, T, H, dv))
-        new = lambda *s, dtype=q.dtype: torch.empty(*s, dtype=dtype, device=q.device)
-        g = dict(dq=new(B, T, H, dk), dk=new(B, T, Hkv, dk), dv=new(B, T, Hkv, dv),
-                 ds0=None if s0 is None else new(B, H, dk, dv, dtype=torch.float32))
-        L = lib()
-        ws = _workspace(L.pararnn_linear_attention_backward_workspace_size(shape, rq, rk, rv, rdo),
-                        "pararnn_linear_attention_backward", workspace, q.device)
-        state = (B, H, dk, dv)
-        rc = L.pararnn_linear_attention_backward(
-            shape, rq, rk, rv, _like(log_decay, "log_decay", q, (H,), torch.float32), rdo,
-            _like(s0, "s0", q, state, torch.float32), _like(ds, "ds", q, state, torch.float32),
-            _like(lengths, "lengths", q, (B,), torch.int32), g["dq"].data_ptr(), g["dk"].data_ptr(),
-            g["dv"].data_ptr(), None if s0 is None else g["ds0"].data_ptr(), _dev(ws, "workspace"), ws.numel(),
-            _stream(stream))
-    _checked(rc, "pararnn_linear_attention_backward")
+    under = _context(q, stream)
+    if under is not None:
+        with under:
+            return linear_attention_backward(q, k, v, log_decay, do, s0=s0, ds=ds, lengths=lengths, scale=scale,
+                                             workspace=workspace)
+    shape, rq, rk, rv = _attention_shape(q, k, v, log_decay, scale)
+    B, T, H, Hkv, dk, dv = shape.B, shape.T, shape.H, shape.Hkv, shape.dk, shape.dv
+    rdo = _rows(do, "do", q, (B, T, H, dv))
+    new = lambda *s, dtype=q.dtype: torch.empty(*s, dtype=dtype, device=q.device)
+    g = dict(dq=new(B, T, H, dk), dk=new(B, T, Hkv, dk), dv=new(B, T, Hkv, dv),
+             ds0=None if s0 is None else new(B, H, dk, dv, dtype=torch.float32))
+    L = lib()
+    ws = _workspace(L.pararnn_linear_attention_backward_workspace_size(shape, rq, rk, rv, rdo),
+                    "pararnn_linear_attention_backward", workspace, q.device)
+    state = (B, H, dk, dv)
+    _checked(L.pararnn_linear_attention_backward(
+        shape, rq, rk, rv, _like(log_decay, "log_decay", q, (H,), torch.float32), rdo,
+        _like(s0, "s0", q, state, torch.float32), _like(ds, "ds", q, state, torch.float32),
+        _like(lengths, "lengths", q, (B,), torch.int32), g["dq"].data_ptr(), g["dk"].data_ptr(), g["dv"].data_ptr(),
+        None if s0 is None else g["ds0"].data_ptr(), _dev(ws, "workspace"), ws.numel(), _current(q)),
+        "pararnn_linear_attention_backward")
     return g
 
 
@@ -908,25 +912,26 @@ def linear_attention_step(q, k, v, log_decay, state, *, slots=None, scale=None, 
     (int32 [B]; outside 0..n-1: no state, o is zero; the same slot twice: tokens
     in row order), or at b if None (n = B).  The states after the token go to
     ``out_state``, or replace those in ``state`` if None.  Returns o [B,H,dv]."""
-    with _on(q.device, stream):
-        if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
-            raise ValueError("q, k and v must be [B, heads, width]")
-        shape, rq, rk, rv = _attention_shape(q.unsqueeze(1), k.unsqueeze(1), v.unsqueeze(1), log_decay, scale)
-        B, H, dk, dv = shape.B, shape.H, shape.dk, shape.dv
-        if state.dim() != 4 or state.shape[0] < 1:
-            raise ValueError("state must be [n, H, dk, dv]")
-        n = state.shape[0]
-        if slots is None and n != B:
-            raise ValueError(f"state has {n} rows for {B} sequences: slots says which")
-        if out is None:
-            out = torch.empty(B, H, dv, dtype=q.dtype, device=q.device)
-        pool = (n, H, dk, dv)
-        src = _like(state, "state", q, pool, torch.float32)
-        rc = lib().pararnn_linear_attention_step(
-            shape, rq, rk, rv, _like(log_decay, "log_decay", q, (H,), torch.float32), src,
-            _like(slots, "slots", q, (B,), torch.int32), n, _like(out, "out", q, (B, H, dv), q.dtype),
-            src if out_state is None else _like(out_state, "out_state", q, pool, torch.float32), _stream(stream))
-    _checked(rc, "pararnn_linear_attention_step")
+    under = _context(q, stream)
+    if under is not None:
+        with under:
+            return linear_attention_step(q, k, v, log_decay, state, slots=slots, scale=scale, out_state=out_state, out=out)
+    shape, rq, rk, rv = _attention_shape(q, k, v, log_decay, scale, 3)
+    B, H, dk, dv = shape.B, shape.H, shape.dk, shape.dv
+    if state.dim() != 4 or state.shape[0] < 1:
+        raise ValueError("state must be [n, H, dk, dv]")
+    n = state.shape[0]
+    if slots is None and n != B:
+        raise ValueError(f"state has {n} rows for {B} sequences: slots says which")
+    if out is None:
+        out = torch.empty(B, H, dv, dtype=q.dtype, device=q.device)
+    pool = (n, H, dk, dv)
+    src = _like(state, "state", q, pool, torch.float32)
+    _checked(lib().pararnn_linear_attention_step(
+        shape, rq, rk, rv, _like(log_decay, "log_decay", q, (H,), torch.float32), src,
+        _like(slots, "slots", q, (B,), torch.int32), n, _like(out, "out", q, (B, H, dv), q.dtype),
+        src if out_state is None else _like(out_state, "out_state", q, pool, torch.float32), _current(q)),
+        "pararnn_linear_attention_step")
     return out
 
 
@@ -941,7 +946,7 @@ def _norm_shape(x, groups, act, eps, y_dtype):
         S *= n
     if min(N, S, C) < 1 or not 1 <= groups <= 2048 or C % groups:
         raise ValueError(f"x must not be empty and groups (1 to 2048) must divide its channels: {tuple(x.shape)}, {groups}")
-    return NormShape(N, S, C, groups, _dtype_code(x.dtype), _dtype_code(y_dtype), ACTIVATIONS[act], float(eps))
+    return NormShape(N, S, C, groups, _dtype_code(x.dtype), _dtype_code(y_dtype), ACTIVATIONS[act], eps)
 
 
 def group_norm(x, groups: int, weight=None, bias=None, *, gate=None, act: str = "silu", eps: float = 1e-5, lengths=None,
@@ -955,20 +960,23 @@ def group_norm(x, groups: int, weight=None, bias=None, *, gate=None, act: str = 
     "gelu"; lengths [N] int32: rows behind them (in the middle axes' order) are
     not read, do not count, and are zero in y.  Returns (y of ``out_dtype``, x's
     if None; stats [N, groups, 2] fp32: mean and 1 / sqrt(var + eps))."""
-    with _on(x.device, stream):
-        y_dtype = out.dtype if out is not None else x.dtype if out_dtype is None else out_dtype
-        shape = _norm_shape(x, groups, act, eps, y_dtype)
-        px = _dev(x, "x")
-        y = out if out is not None else torch.empty(x.shape, dtype=y_dtype, device=x.device)
-        stats = torch.empty(shape.N, groups, 2, dtype=torch.float32, device=x.device)
-        L = lib()
-        ws = _workspace(L.pararnn_group_norm_workspace_size(shape), "pararnn_group_norm", workspace, x.device)
-        rc = L.pararnn_group_norm(
-            shape, px, _like(weight, "weight", x, (shape.C,), torch.float32),
-            _like(bias, "bias", x, (shape.C,), torch.float32), _like(gate, "gate", x, x.shape, x.dtype),
-            _like(lengths, "lengths", x, (shape.N,), torch.int32), _like(y, "out", x, x.shape, y_dtype),
-            stats.data_ptr(), _dev(ws, "workspace"), ws.numel(), _stream(stream))
-    _checked(rc, "pararnn_group_norm")
+    under = _context(x, stream)
+    if under is not None:
+        with under:
+            return group_norm(x, groups, weight, bias, gate=gate, act=act, eps=eps, lengths=lengths, out_dtype=out_dtype,
+                              out=out, workspace=workspace)
+    y_dtype = out.dtype if out is not None else x.dtype if out_dtype is None else out_dtype
+    shape = _norm_shape(x, groups, act, eps, y_dtype)
+    channels = (shape.C,)
+    y = out if out is not None else torch.empty(x.shape, dtype=y_dtype, device=x.device)
+    stats = torch.empty(shape.N, groups, 2, dtype=torch.float32, device=x.device)
+    L = lib()
+    ws = _workspace(L.pararnn_group_norm_workspace_size(shape), "pararnn_group_norm", workspace, x.device)
+    _checked(L.pararnn_group_norm(
+        shape, _dev(x, "x"), _like(weight, "weight", x, channels, torch.float32),
+        _like(bias, "bias", x, channels, torch.float32), _like(gate, "gate", x, x.shape, x.dtype),
+        _like(lengths, "lengths", x, (shape.N,), torch.int32), _like(y, "out", x, x.shape, y_dtype), stats.data_ptr(),
+        _dev(ws, "workspace"), ws.numel(), _current(x)), "pararnn_group_norm")
     return y, stats
 
 
@@ -978,21 +986,24 @@ def group_norm_backward(x, stats, dy, groups: int, weight=None, bias=None, *, ga
     type) and the forward's stats; the rest as given to the forward pass.
     Returns dict(dx, dweight, dbias, dgate); dweight, dbias and dgate are None
     where the forward pass had no weight, bias or gate."""
-    with _on(x.device, stream):
-        shape = _norm_shape(x, groups, act, 0.0, dy.dtype)
-        px = _dev(x, "x")
-        new = lambda t: None if t is None else torch.empty_like(t)
-        ptr = lambda t: None if t is None else t.data_ptr()
-        pw = _like(weight, "weight", x, (shape.C,), torch.float32)
-        pb = _like(bias, "bias", x, (shape.C,), torch.float32)
-        pg = _like(gate, "gate", x, x.shape, x.dtype)
-        g = dict(dx=torch.empty_like(x), dweight=new(weight), dbias=new(bias), dgate=new(gate))
-        L = lib()
-        ws = _workspace(L.pararnn_group_norm_backward_workspace_size(shape), "pararnn_group_norm_backward", workspace,
-                        x.device)
-        rc = L.pararnn_group_norm_backward(
-            shape, px, _like(stats, "stats", x, (shape.N, groups, 2), torch.float32), _like(dy, "dy", x, x.shape, dy.dtype),
-            pw, pb, pg, _like(lengths, "lengths", x, (shape.N,), torch.int32), ptr(g["dx"]), ptr(g["dweight"]),
-            ptr(g["dbias"]), ptr(g["dgate"]), _dev(ws, "workspace"), ws.numel(), _stream(stream))
-    _checked(rc, "pararnn_group_norm_backward")
+    under = _context(x, stream)
+    if under is not None:
+        with under:
+            return group_norm_backward(x, stats, dy, groups, weight, bias, gate=gate, act=act, lengths=lengths,
+                                       workspace=workspace)
+    shape = _norm_shape(x, groups, act, 0.0, dy.dtype)
+    channels = (shape.C,)
+    new = lambda t: None if t is None else torch.empty_like(t)
+    ptr = lambda t: None if t is None else t.data_ptr()
+    px = _dev(x, "x")
+    pw = _like(weight, "weight", x, channels, torch.float32)
+    pb = _like(bias, "bias", x, channels, torch.float32)
+    pg = _like(gate, "gate", x, x.shape, x.dtype)
+    g = dict(dx=torch.empty_like(x), dweight=new(weight), dbias=new(bias), dgate=new(gate))
+    L = lib()
+    ws = _workspace(L.pararnn_group_norm_backward_workspace_size(shape), "pararnn_group_norm_backward", workspace, x.device)
+    _checked(L.pararnn_group_norm_backward(
+        shape, px, _like(stats, "stats", x, (shape.N, groups, 2), torch.float32), _like(dy, "dy", x, x.shape, dy.dtype),
+        pw, pb, pg, _like(lengths, "lengths", x, (shape.N,), torch.int32), ptr(g["dx"]), ptr(g["dweight"]),
+        ptr(g["dbias"]), ptr(g["dgate"]), _dev(ws, "workspace"), ws.numel(), _current(x)), "pararnn_group_norm_backward")
     return g
