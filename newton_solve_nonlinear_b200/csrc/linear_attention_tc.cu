@@ -46,9 +46,15 @@ struct Lay {
     static constexpr int BARS = TAB + (160 + 256) * 4;
     static constexpr int BYTES = BARS + 160 + 1024;
     // TMEM columns: scores, each half of which becomes the weighted scores of its 64 columns (32-bit columns 0-31 and
-    // 64-95); out; dS; two places for terms of c: the smallest and then the largest, and the middle one
-    static constexpr int T_S = 0, T_O = 128, T_D = 256, T_V = 384;
-    static constexpr int STATE_WARPS = 2 * (DV / 32);
+    // 64-95); out; dS; the weighted c's terms, smallest first, 64 columns each.  All of it fits but for DK = DV = 128,
+    // where the largest term takes the smallest one's place after its use.  Pass 1 has neither scores nor outputs:
+    // dS and two sets of terms, so that the next chunk is split while this one's products run.
+    static constexpr bool THREE = DK + DV <= 192;
+    static constexpr int T_S = 0, T_O = 128, T_D = 128 + DV, T_V = T_D + DK;
+    static constexpr int T_D1 = 0, T_V1 = 128;
+    static constexpr int STATE_WARPS = 8;
+    // lane of column d of c, as a row of dS: with 64 columns, 16 in each warp's quarter, so that all warps have some
+    static constexpr int ROWS = DV / 4;
     static_assert(BYTES <= 227 * 1024, "shared memory");
 };
 
@@ -397,14 +403,16 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         // ---- state: TMEM lane = column of c; half = half of b's width and of the chunk's rows
         regs_up<kRegsState>();
         const int quarter = warp & 3, half = (warp - 8) >> 2;
-        if (quarter * 32 < DV) {
+        {
             constexpr int KH = DK / 2;
-            const int d = quarter * 32 + lane;
+            constexpr bool THREE = STATE_ONLY || Y::THREE;
+            const int d = quarter * Y::ROWS + (lane & (Y::ROWS - 1));  // with 64 columns, lanes 16-31 have none
+            const bool mine = lane < Y::ROWS;
             const unsigned tl = tm + (static_cast<unsigned>(quarter * 32) << 16);
-            const unsigned t_ds = tl + Y::T_D + half * KH;
+            const unsigned t_ds = tl + (STATE_ONLY ? Y::T_D1 : Y::T_D) + half * KH;
             float S[KH];
             {
-                const bool have = d < ncol && (w.n_seg > 1 ? !STATE_ONLY : w.s_in != nullptr);
+                const bool have = mine && d < ncol && (w.n_seg > 1 ? !STATE_ONLY : w.s_in != nullptr);
                 const float *p = w.n_seg > 1
                                      ? w.seg_state + (static_cast<long long>(bh) * w.n_seg + sg) * w.dk * w.dv + c0 + d
                                      : w.s_in + static_cast<long long>(bh) * w.dk * w.dv +
@@ -420,6 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             auto publish = [&]() {
 #pragma unroll
                 for (int k = 0; k < KH; k += 8) {
+                    if (!mine) break;
                     const int kk = half * KH + k;
                     const unsigned at = sm + Y::SS + (kk >> 6) * (DV * 128) + d * 128 + ((((kk & 63) >> 3) ^ (d & 7)) << 4);
                     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(pack(S[k], S[k + 1])),
@@ -436,21 +445,39 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             // first, then tokens
             const int m_row = half * 64 + ((lane >> 4) << 3) + (lane & 7);
             const float g_full = power(kC), g_part = power(n_part);
+            // S = g^n S + dS of chunk c
+            auto absorb = [&](int c) {
+                if (!mbar_wait(smem_u32(&bars->ds), c & 1, err)) return false;
+                fence_after();
+                const float gn = c == part_chunk ? g_part : g_full;
+#pragma unroll
+                for (int k = 0; k < KH; k += 32) {
+                    float v[32];
+                    tmem_ld32(t_ds + k, v);
+#pragma unroll
+                    for (int q = 0; q < 32; q += 2) fma2(S[k + q], S[k + q + 1], gn, v[q], v[q + 1]);
+                }
+                fence_before();
+                return true;
+            };
             for (int c = 0; c < chunks; ++c) {
                 const int st = c & 1;
                 const unsigned ph = c & 1;
                 const bool part = c == part_chunk;
                 const unsigned tile_b = sm + st * Y::STAGE + Y::B, tile_c = sm + st * Y::STAGE + Y::C;
                 if (!mbar_wait(smem_u32(&bars->full[st]), (c >> 1) & 1, err)) break;
+                const int col0 = quarter * Y::ROWS;  // this warp's columns of c
+                const unsigned panel_c = tile_c + (col0 >> 6) * kPanel;
                 if (part && unclean) {  // tokens behind the sequence's end: this warp's share of c, and of b
-                    for (int x = max(n_part, half * 64) + (lane >> 2); x < half * 64 + 64; x += 8) {
-                        const int ch = (quarter & 1) * 4 + (lane & 3);
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                         tile_c + (quarter >> 1) * kPanel + x * 128 + ((ch ^ (x & 7)) << 4)),
+                    constexpr int CH = Y::ROWS / 8;
+                    for (int x = max(n_part, half * 64) + lane / CH; x < half * 64 + 64; x += 32 / CH) {
+                        const int ch = ((col0 & 63) >> 3) + lane % CH;
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(panel_c + x * 128 +
+                                                                                      ((ch ^ (x & 7)) << 4)),
                                      "r"(0)
                                      : "memory");
                     }
-                    const int me = half * (DV / 32) + quarter;
+                    const int me = half * 4 + quarter;
                     for (int x = n_part + me; x < kC; x += Y::STATE_WARPS)
                         if (lane < DK / 8)
                             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
@@ -461,70 +488,68 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                     __syncwarp();
                 }
                 const float *cwt = cw + (part ? 128 : 0) + half * 64 + 2 * (lane & 3);
-                const unsigned ta = tl + Y::T_V + half * 32;
+                const unsigned ta = tl + (STATE_ONLY ? Y::T_V1 + (c & 1) * 192 : Y::T_V) + half * 32;
                 // 16 columns of c (sub), 64 tokens; registers k, k + 1: the same 8 tokens, columns lane / 4 and + 8
                 auto load_c = [&](int sub, unsigned (&u)[16]) {
-                    const int ch = (quarter & 1) * 4 + sub * 2 + ((lane >> 3) & 1);
-                    const unsigned at = tile_c + (quarter >> 1) * kPanel + m_row * 128 + ((ch ^ (lane & 7)) << 4);
+                    const int ch = ((col0 & 63) >> 3) + sub * 2 + ((lane >> 3) & 1);
+                    const unsigned at = panel_c + m_row * 128 + ((ch ^ (lane & 7)) << 4);
 #pragma unroll
                     for (int tb = 0; tb < 4; ++tb)
                         ldmatrix4t(at + tb * 2048, u[4 * tb], u[4 * tb + 1], u[4 * tb + 2], u[4 * tb + 3]);
                 };
 #pragma unroll 1
-                for (int sub = 0; sub < 2; ++sub) {
-                    unsigned u1[16], u2[16];
+                for (int sub = 0; sub < Y::ROWS / 16; ++sub) {
+                    unsigned u0[16], u1[16], u2[16];
                     load_c(sub, u1);
 #pragma unroll
                     for (int q = 0; q < 16; ++q) {
                         const float2 f = *reinterpret_cast<const float2 *>(cwt + (q >> 1) * 8);
                         float y0 = lo_of(u1[q]), y1 = hi_of(u1[q]);
                         mul2(y0, y1, f.x, f.y);
-                        const unsigned u0 = pack(y0, y1);
-                        sub2(y0, y1, lo_of(u0), hi_of(u0));
+                        u0[q] = pack(y0, y1);
+                        sub2(y0, y1, lo_of(u0[q]), hi_of(u0[q]));
                         u1[q] = pack(y0, y1);
                         sub2(y0, y1, lo_of(u1[q]), hi_of(u1[q]));
                         u2[q] = pack(y0, y1);
                     }
-                    tmem_st_frag(ta + (static_cast<unsigned>(sub * 16) << 16), u2);
-                    tmem_st_frag(ta + (static_cast<unsigned>(sub * 16) << 16) + 64, u1);
+                    const unsigned tsub = ta + (static_cast<unsigned>(sub * 16) << 16);
+                    tmem_st_frag(tsub, u2);
+                    tmem_st_frag(tsub + 64, u1);
+                    if (THREE) tmem_st_frag(tsub + 128, u0);
                 }
+                if (STATE_ONLY && c > 0 && !absorb(c - 1)) break;
                 tmem_st_wait();
                 fence_before();
                 __syncwarp();
                 if (lane == 0) arrive(smem_u32(&bars->v));
-                // the smallest term has been used: the largest takes its place (formed again: registers are short)
-                if (!mbar_wait(smem_u32(&bars->low), ph, err)) break;
-                fence_after();
+                if (!THREE) {
+                    // the smallest term has been used: the largest takes its place (formed again: registers are short)
+                    if (!mbar_wait(smem_u32(&bars->low), ph, err)) break;
+                    fence_after();
 #pragma unroll 1
-                for (int sub = 0; sub < 2; ++sub) {
-                    unsigned u[16];
-                    load_c(sub, u);
+                    for (int sub = 0; sub < Y::ROWS / 16; ++sub) {
+                        unsigned u[16];
+                        load_c(sub, u);
 #pragma unroll
-                    for (int q = 0; q < 16; ++q) {
-                        const float2 f = *reinterpret_cast<const float2 *>(cwt + (q >> 1) * 8);
-                        float y0 = lo_of(u[q]), y1 = hi_of(u[q]);
-                        mul2(y0, y1, f.x, f.y);
-                        u[q] = pack(y0, y1);
+                        for (int q = 0; q < 16; ++q) {
+                            const float2 f = *reinterpret_cast<const float2 *>(cwt + (q >> 1) * 8);
+                            float y0 = lo_of(u[q]), y1 = hi_of(u[q]);
+                            mul2(y0, y1, f.x, f.y);
+                            u[q] = pack(y0, y1);
+                        }
+                        tmem_st_frag(ta + (static_cast<unsigned>(sub * 16) << 16), u);
                     }
-                    tmem_st_frag(ta + (static_cast<unsigned>(sub * 16) << 16), u);
+                    tmem_st_wait();
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive(smem_u32(&bars->v_high));
                 }
-                tmem_st_wait();
-                fence_before();
-                __syncwarp();
-                if (lane == 0) arrive(smem_u32(&bars->v_high));
-                const float gn = part ? g_part : g_full;
-                if (!mbar_wait(smem_u32(&bars->ds), ph, err)) break;
-                fence_after();
-#pragma unroll
-                for (int k = 0; k < KH; k += 32) {
-                    float v[32];
-                    tmem_ld32(t_ds + k, v);
-#pragma unroll
-                    for (int q = 0; q < 32; q += 2) fma2(S[k + q], S[k + q + 1], gn, v[q], v[q + 1]);
+                if (!STATE_ONLY) {
+                    if (!absorb(c)) break;
+                    publish();
                 }
-                fence_before();
-                if (!STATE_ONLY) publish();
             }
+            if (STATE_ONLY && chunks > 0) absorb(chunks - 1);
             // the last state: the segment's own (pass 1) or the sequence's
             const int last_seg = L > 0 && !rev ? (L - 1) / w.seg : 0;
             float *p = nullptr;
@@ -535,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                 p = w.s_out + static_cast<long long>(bh) * w.dk * w.dv + static_cast<long long>(c0 + d) * w.s_j;
                 si = w.s_i;
             }
-            if (p != nullptr && d < ncol) {
+            if (p != nullptr && mine && d < ncol) {
                 const bool bad = *err != 0;
 #pragma unroll
                 for (int k = 0; k < KH; ++k)
@@ -551,6 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         constexpr unsigned id_out = make_idesc(1u, 128, DV) | kNMajorB, id_ds = make_idesc(1u, 128, DK) | kNMajorB;
         const unsigned on = elect_one() ? 1u : 0u;
         const unsigned tu = __shfl_sync(0xffffffffu, tm, 0);
+        constexpr bool THREE = STATE_ONLY || Y::THREE;
         int done = 0;  // chunks issued whole
         auto scores = [&](int c) {
             const unsigned ta = sm + (c & 1) * Y::STAGE + Y::A, tb = sm + (c & 1) * Y::STAGE + Y::B;
@@ -563,9 +589,11 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         };
         auto term = [&](int c, int place, bool first) {
             const unsigned tb = sm + (c & 1) * Y::STAGE + Y::B;
+            const unsigned td = tu + (STATE_ONLY ? Y::T_D1 : Y::T_D);
+            const unsigned tv = tu + (STATE_ONLY ? Y::T_V1 + (c & 1) * 192 : Y::T_V) + place * 64;
 #pragma unroll 2
             for (int k = 0; k < kC / 16; ++k)
-                mma_ts(tu + Y::T_D, tu + Y::T_V + place * 64 + k * 8, nmajor_desc(tb + k * 2048), id_ds, !first || k > 0, on);
+                mma_ts(td, tv + k * 8, nmajor_desc(tb + k * 2048), id_ds, !first || k > 0, on);
         };
         // a tile whose rows the state warps clear is clean once they have arrived at v
         if (chunks > 0 && mbar_wait(smem_u32(&bars->full[0]), 0, err) &&
@@ -590,8 +618,12 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                 if (!mbar_wait(smem_u32(&bars->v), ph, err)) break;
                 fence_after();
                 term(c, 0, true);
-                commit(smem_u32(&bars->low), on);
+                if (!THREE) commit(smem_u32(&bars->low), on);
                 term(c, 1, false);
+                if (THREE) {
+                    term(c, 2, false);
+                    commit(smem_u32(&bars->ds), on);
+                }
                 if (!STATE_ONLY) {
                     if (!mbar_wait(smem_u32(&bars->scaled), ph, err)) break;
                     fence_after();
@@ -601,10 +633,12 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                                true, on);
                     commit(smem_u32(&bars->out), on);
                 }
-                if (!mbar_wait(smem_u32(&bars->v_high), ph, err)) break;
-                fence_after();
-                term(c, 0, false);
-                commit(smem_u32(&bars->ds), on);
+                if (!THREE) {
+                    if (!mbar_wait(smem_u32(&bars->v_high), ph, err)) break;
+                    fence_after();
+                    term(c, 0, false);
+                    commit(smem_u32(&bars->ds), on);
+                }
                 commit(smem_u32(&bars->empty[st]), on);
                 done = c + 1;
                 if (c + 1 < chunks) {
