@@ -222,6 +222,13 @@ __device__ __forceinline__ void tma_load_4d(unsigned dst, const CUtensorMap *map
         "l"(reinterpret_cast<unsigned long long>(map)), "r"(x), "r"(t), "r"(h), "r"(b), "r"(bar)
         : "memory");
 }
+// Brings a tile into L2 ahead of its load.
+__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap *map, int x, int t, int h, int b) {
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                     reinterpret_cast<unsigned long long>(map)),
+                 "r"(x), "r"(t), "r"(h), "r"(b)
+                 : "memory");
+}
 __device__ __forceinline__ void tma_store_4d(const CUtensorMap *map, int x, int t, int h, int b, unsigned src) {
     asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
                      reinterpret_cast<unsigned long long>(map)),
@@ -687,6 +694,24 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             }
             __syncwarp();
         };
+        // With small tiles two stages hold too few bytes in flight for DRAM's latency: tiles go to L2 a chunk before
+        // their load (131072 tokens, 8 heads of 64: 207 -> 193 us; with 128 columns it is no gain: 234 -> 244 us on
+        // 8 x 8192 x 16 heads)
+        constexpr int kAhead = DK + DV <= 128 ? 1 : 0;
+        auto prefetch = [&](int c) {
+            if (elect_one()) {
+                const int t0 = first_token(c);
+#pragma unroll
+                for (int x = 0; x < DV / 64; ++x) tma_prefetch_4d(&sweep.c, c0 + x * 64, t0, hc, b);
+#pragma unroll
+                for (int x = 0; x < DK / 64; ++x) {
+                    tma_prefetch_4d(&sweep.b, x * 64, t0, hb, b);
+                    if (!STATE_ONLY) tma_prefetch_4d(&sweep.a, x * 64, t0, ha, b);
+                }
+            }
+            __syncwarp();
+        };
+        for (int c = 2; c < min(chunks, 2 + kAhead); ++c) prefetch(c);
         int loaded = 0;  // chunks of which any tile was asked for
 #pragma unroll 1
         for (int c = -2; c < chunks; ++c) {
@@ -694,6 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                 if (c >= 0 && !mbar_wait(smem_u32(&bars->empty[c & 1]), (c >> 1) & 1, err)) break;
                 load(c + 2, true);
                 loaded = c + 3;
+                if (kAhead > 0 && c >= 0 && c + 2 + kAhead < chunks) prefetch(c + 2 + kAhead);
             }
             if (STATE_ONLY) continue;
             if (c >= 0) {
