@@ -499,24 +499,28 @@ __global__ void __launch_bounds__(kThr, V * K <= 8 ? 2 : 1) gn_row_backward_kern
     }
 }
 
-// dw, db [C] = sums of part [rows][2][C]: 32 slices of the rows per CTA of 32 channels, each in row order, then
-// the slices in order
-__global__ void __launch_bounds__(1024) gn_param_sum_kernel(const float *__restrict__ part, int rows, int C, float *dw,
-                                                            float *db) {
+// dw, db [C] = sums of part [rows][2][C], a block for 32 channels of one of them: a slice of the rows per warp, each
+// in row order, then the slices in order
+__device__ __forceinline__ void param_sum(int block, const float *__restrict__ part, int rows, int C, float *dw, float *db) {
     __shared__ float red[32][33];
-    const int lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane, sl = threadIdx.x >> 5, which = blockIdx.y;
+    const int warps = blockDim.x >> 5, lane = threadIdx.x & 31, sl = threadIdx.x >> 5;
+    const int c = (block >> 1) * 32 + lane, which = block & 1;
     float s = 0.f;
     if (c < C) {
 #pragma unroll 8
-        for (int r = sl; r < rows; r += 32) s += part[(static_cast<long long>(r) * 2 + which) * C + c];
+        for (int r = sl; r < rows; r += warps) s += part[(static_cast<long long>(r) * 2 + which) * C + c];
     }
     red[sl][lane] = s;
     __syncthreads();
     if (sl == 0 && c < C) {
-        for (int q = 1; q < 32; ++q) s += red[q][lane];
+        for (int q = 1; q < warps; ++q) s += red[q][lane];
         float *out = which == 0 ? dw : db;
         if (out != nullptr) out[c] = s;
     }
+}
+int param_blocks(int C) { return (C + 31) / 32 * 2; }
+__global__ void __launch_bounds__(1024) gn_param_sum_kernel(const float *part, int rows, int C, float *dw, float *db) {
+    param_sum(blockIdx.x, part, rows, C, dw, db);
 }
 
 // ---- statistics over a sequence ------------------------------------------------------------------------------
@@ -606,24 +610,29 @@ __global__ void __launch_bounds__(kThr) gn_stats_kernel(const GnArgs a, int rows
     for (int g = threadIdx.x; g < a.G; g += blockDim.x) out[g] = acc[g];
 }
 
+// A warp joins the moments of one (n, group) over the chunks, `step` apart: mean and 1 / sqrt(var + eps)
+__device__ __forceinline__ float2 join_chunks(const Moments *p, int chunks, int step, float eps, int lane) {
+    Moments t = {0.f, 0.f, 0.f};
+    for (int q = lane; q < chunks; q += 32) t = join(t, p[static_cast<long long>(q) * step]);
+#pragma unroll
+    for (int q = 16; q > 0; q >>= 1) t = join(t, shuffle_xor(t, q));
+    return make_float2(t.mean, rsqrtf((t.n > 0.f ? t.m2 / t.n : 0.f) + eps));
+}
+
 __global__ void __launch_bounds__(kThr) gn_stats_join_kernel(const GnArgs a, int chunks, const Moments *part) {
     const long long i = (static_cast<long long>(blockIdx.x) * kThr + threadIdx.x) >> 5;
     const int lane = threadIdx.x & 31;
     if (i >= static_cast<long long>(a.N) * a.G) return;
-    const long long n = i / a.G, g = i % a.G;
-    Moments t = {0.f, 0.f, 0.f};
-    for (int q = lane; q < chunks; q += 32) t = join(t, part[(n * chunks + q) * a.G + g]);
-#pragma unroll
-    for (int q = 16; q > 0; q >>= 1) t = join(t, shuffle_xor(t, q));
-    if (lane == 0) {
-        const float var = t.n > 0.f ? t.m2 / t.n : 0.f;
-        *reinterpret_cast<float2 *>(a.stats + i * 2) = make_float2(t.mean, rsqrtf(var + a.eps));
-    }
+    const float2 st = join_chunks(part + i / a.G * chunks * a.G + i % a.G, chunks, a.G, a.eps, lane);
+    if (lane == 0) *reinterpret_cast<float2 *>(a.stats + i * 2) = st;
 }
 
-// The second pass takes the blocks in reversed order: what the first pass read last is still in L2.
-template <typename TX, typename TY, int V>
-__global__ void __launch_bounds__(kThr) gn_apply_kernel(const GnArgs a, int rows, int chunks) {
+// The second pass takes the blocks in reversed order: what the first pass read last is still in L2.  JOIN: every CTA
+// joins its n's partial statistics by itself, a warp per group, where they are few enough that this costs less than
+// a launch of its own (gn_stats_join_kernel).
+template <typename TX, typename TY, int V, bool JOIN>
+__global__ void __launch_bounds__(kThr) gn_apply_kernel(const GnArgs a, int rows, int chunks, const Moments *part) {
+    extern __shared__ float2 joined[];  // [G]
     const unsigned bid = gridDim.x - 1 - blockIdx.x;
     const int n = static_cast<int>(bid / chunks), ch = static_cast<int>(bid % chunks), L = row_count(a, n);
     const long long lo = static_cast<long long>(ch) * rows;
@@ -633,11 +642,23 @@ __global__ void __launch_bounds__(kThr) gn_apply_kernel(const GnArgs a, int rows
     const TX *gate = a.gate == nullptr ? nullptr : static_cast<const TX *>(a.gate) + nb;
     TY *y = static_cast<TY *>(a.y) + nb;
     const Span sp = span_of<V>(a);
+    if (JOIN) {
+        const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+        for (int g = threadIdx.x >> 5; g < a.G; g += warps) {
+            const float2 st = join_chunks(part + static_cast<long long>(n) * chunks * a.G + g, chunks, a.G, a.eps, lane);
+            if (lane == 0) {
+                joined[g] = st;
+                if (ch == 0) *reinterpret_cast<float2 *>(a.stats + (static_cast<long long>(n) * a.G + g) * 2) = st;
+            }
+        }
+        __syncthreads();
+    }
+    const float2 *stats = JOIN ? joined : reinterpret_cast<const float2 *>(a.stats) + static_cast<long long>(n) * a.G;
     const int r0 = sp.par == 1 ? 0 : threadIdx.x / sp.cols;
     if (r0 >= sp.par) return;
     for (int col = sp.par == 1 ? threadIdx.x : threadIdx.x % sp.cols; col < sp.cols; col += sp.par == 1 ? kThr : sp.cols) {
         const int c = col * V, g = c / (a.C / a.G);
-        const float2 st = *reinterpret_cast<const float2 *>(a.stats + (static_cast<long long>(n) * a.G + g) * 2);
+        const float2 st = stats[g];
         float w[V], b[V];
         load_wb<V>(a, c, w, b);
 #pragma unroll
@@ -780,8 +801,14 @@ __global__ void __launch_bounds__(kThr) gn_channel_join_kernel(const GnArgs a, i
 }
 
 template <typename TX, typename TY, int V, bool GATE>
-__global__ void __launch_bounds__(kThr) gn_backward_apply_kernel(const GnArgs a, int rows, int chunks, const float *gsum) {
-    const unsigned bid = gridDim.x - 1 - blockIdx.x;
+__global__ void __launch_bounds__(kThr) gn_backward_apply_kernel(const GnArgs a, int rows, int chunks, const float *gsum,
+                                                                 const float *chan) {
+    const unsigned blocks = static_cast<unsigned>(chunks) * a.N;
+    if (blockIdx.x >= blocks) {  // the parameters' gradients
+        param_sum(blockIdx.x - blocks, chan, a.N, a.C, a.dweight, a.dbias);
+        return;
+    }
+    const unsigned bid = blocks - 1 - blockIdx.x;
     const int n = static_cast<int>(bid / chunks), ch = static_cast<int>(bid % chunks), L = row_count(a, n);
     const long long lo = static_cast<long long>(ch) * rows;
     const long long hi = min(lo + rows, static_cast<long long>(a.S));
@@ -827,6 +854,7 @@ __global__ void __launch_bounds__(kThr) gn_backward_apply_kernel(const GnArgs a,
 
 // ---- plans and dispatch --------------------------------------------------------------------------------------
 
+constexpr int kJoinMost = 1024;  // partial moments of one n that every CTA of the second pass joins by itself
 constexpr int kRowMost = 1024;  // channels of a group that a warp holds in registers (32 per lane)
 
 bool row_regime(const GnArgs &a) { return a.S == 1 && a.C / a.G <= kRowMost; }
@@ -884,8 +912,7 @@ cudaError_t row_backward(const GnArgs &a, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     k<<<grid, kThr, smem, s>>>(a, team, reinterpret_cast<float *>(a.ws));
-    gn_param_sum_kernel<<<dim3((a.C + 31) / 32, 2), 1024, 0, s>>>(reinterpret_cast<float *>(a.ws), bx, a.C, a.dweight,
-                                                                 a.dbias);
+    gn_param_sum_kernel<<<param_blocks(a.C), 1024, 0, s>>>(reinterpret_cast<float *>(a.ws), bx, a.C, a.dweight, a.dbias);
     return cudaGetLastError();
 }
 
@@ -895,9 +922,13 @@ cudaError_t seq_forward(const GnArgs &a, cudaStream_t s) {
     Moments *part = reinterpret_cast<Moments *>(a.ws);
     const unsigned grid = static_cast<unsigned>(chunks) * a.N;
     gn_stats_kernel<TX, V><<<grid, threads_of<V>(a), a.G * sizeof(Moments), s>>>(a, rows, chunks, part);
-    const long long warps = static_cast<long long>(a.N) * a.G;
-    gn_stats_join_kernel<<<static_cast<unsigned>((warps * 32 + kThr - 1) / kThr), kThr, 0, s>>>(a, chunks, part);
-    gn_apply_kernel<TX, TY, V><<<grid, threads_of<V>(a), 0, s>>>(a, rows, chunks);
+    if (static_cast<long long>(chunks) * a.G <= kJoinMost) {
+        gn_apply_kernel<TX, TY, V, true><<<grid, threads_of<V>(a), a.G * sizeof(float2), s>>>(a, rows, chunks, part);
+    } else {
+        const long long warps = static_cast<long long>(a.N) * a.G;
+        gn_stats_join_kernel<<<static_cast<unsigned>((warps * 32 + kThr - 1) / kThr), kThr, 0, s>>>(a, chunks, part);
+        gn_apply_kernel<TX, TY, V, false><<<grid, threads_of<V>(a), 0, s>>>(a, rows, chunks, part);
+    }
     return cudaGetLastError();
 }
 
@@ -910,8 +941,11 @@ cudaError_t seq_backward_g(const GnArgs &a, cudaStream_t s) {
     float *gsum = reinterpret_cast<float *>(reinterpret_cast<char *>(chan) + al(static_cast<size_t>(a.N) * 2 * a.C * 4));
     gn_channel_sum_kernel<TX, TY, V, GATE><<<grid, threads_of<V>(a), 0, s>>>(a, rows, chunks, part);
     gn_channel_join_kernel<<<static_cast<unsigned>(a.N) * a.G, kThr, 0, s>>>(a, chunks, part, chan, gsum);
-    gn_backward_apply_kernel<TX, TY, V, GATE><<<grid, threads_of<V>(a), 0, s>>>(a, rows, chunks, gsum);
-    gn_param_sum_kernel<<<dim3((a.C + 31) / 32, 2), 1024, 0, s>>>(chan, a.N, a.C, a.dweight, a.dbias);
+    // few rows to sum: blocks of the same launch do it
+    const bool with = a.N <= 256;
+    gn_backward_apply_kernel<TX, TY, V, GATE>
+        <<<grid + (with ? param_blocks(a.C) : 0), threads_of<V>(a), 0, s>>>(a, rows, chunks, gsum, chan);
+    if (!with) gn_param_sum_kernel<<<param_blocks(a.C), 1024, 0, s>>>(chan, a.N, a.C, a.dweight, a.dbias);
     return cudaGetLastError();
 }
 
