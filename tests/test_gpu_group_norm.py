@@ -158,6 +158,34 @@ def test_padded_batch(S, lengths, dtype):
         assert all(torch.equal(p, q) for p, q in zip(want, fw.group_norm(x, 4, w, b, lengths=ln)))
 
 
+@pytest.mark.parametrize("S,G,cg,dtype,out,lengths", [(50001, 4, 16, F32, BF16, None), (12345, 7, 33, F32, F32, True),
+                                                      (30000, 16, 16, BF16, BF16, True)])
+def test_larger_than_l2(S, G, cg, dtype, out, lengths):
+    """Inputs that L2 does not hold, with many rows per statistic: some n against the oracle, twice the same bits."""
+    N, C = 9, G * cg
+    x, w, b, n = _make(N, S, C, dtype)
+    gate = n(N, S, C, dt=dtype) if lengths else None
+    ln = [S, 0, 1, S - 1, 777, S, S // 2, S, 4096] if lengths else None
+    lt = None if ln is None else torch.tensor(ln, dtype=torch.int32, device="cuda")
+    y, stats = fw.group_norm(x, G, w, b, gate=gate, lengths=lt, out_dtype=out)
+    again = fw.group_norm(x, G, w, b, gate=gate, lengths=lt, out_dtype=out, stream=torch.cuda.Stream())
+    torch.cuda.synchronize()
+    assert torch.equal(y, again[0]) and torch.equal(stats, again[1])
+    for i in (0, 1, 4, 8):
+        L = S if ln is None else ln[i]
+        if L == 0:
+            assert not y[i].any()
+            continue
+        xi, gi = _np(x[i:i + 1, :L]), None if gate is None else _np(gate[i:i + 1, :L])
+        want, ws = oracle.forward(xi, G, _np(w), _np(b), gi, "silu")
+        _, z, _, ez = _errors(xi, G, _np(w), _np(b), None, 1e-5)
+        a = 1 if gate is None else np.abs(oracle.act(gi, "silu"))
+        tol = (1.2 * ez if gate is None else ez * a) + 16 * EPS24 * (np.abs(want) if gate is None else np.abs(z) * a)
+        _within(y[i:i + 1, :L], want, tol, out, "y")
+        _within(stats[i:i + 1, :, 1], ws[..., 1], U * ws[..., 1], F32, "rstd")
+        assert not y[i, L:].any()
+
+
 @pytest.mark.parametrize("size", [(4, 1, 4, 64), (2, 500, 4, 16)])
 def test_large_offset_and_constant_groups(size):
     """A common offset far above the spread; groups without any spread (xhat = 0, r = 1 / sqrt(eps))."""
