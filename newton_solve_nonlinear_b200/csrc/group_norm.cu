@@ -273,7 +273,7 @@ struct Raw {  // V elements as they come from memory
 };
 
 template <typename TX, typename TY, int V, int K, int R>
-__global__ void __launch_bounds__(kThr, V * K <= 8 ? 3 : 1) gn_row_forward_kernel(const GnArgs a, int team) {
+__global__ void __launch_bounds__(kThr, V * K <= 16 ? 2 : 1) gn_row_forward_kernel(const GnArgs a, int team) {
     const int cg = a.C / a.G;
     const Teams tt = teams_of(a.G, team);
     const int tm = threadIdx.x / team, lane = threadIdx.x & (team - 1);
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kThr, V * K <= 8 ? 3 : 1) gn_row_forward_kerne
 
 // Backward: the sums of dw and db over the rows that a CTA took go to part[blockIdx.x][2][C].
 template <typename TX, typename TY, int V, int K, int R>
-__global__ void __launch_bounds__(kThr, V * K <= 8 ? 2 : 1) gn_row_backward_kernel(const GnArgs a, int team, float *part) {
+__global__ void __launch_bounds__(kThr, V * K <= 16 ? 2 : 1) gn_row_backward_kernel(const GnArgs a, int team, float *part) {
     extern __shared__ float red[];  // [rows in flight][dw, db][this CTA's channels]
     const int cg = a.C / a.G;
     const Teams tt = teams_of(a.G, team);
@@ -862,8 +862,17 @@ int vec_of(const GnArgs &a) {
     const int cg = a.C / a.G;
     return cg % 8 == 0 ? 8 : cg % 4 == 0 ? 4 : 1;
 }
-int team_of(const GnArgs &a, int V) {
-    const int need = (a.C / a.G + V - 1) / V;
+// vectors that a lane holds of a group: more than one where 32 lanes would not hold it, and in the forward pass two
+// where a group has them, which halves the shuffles per element ([32768, 16 x 128] bf16 gated: 108 -> 96 us; the
+// backward pass has no registers for it: 61 -> 66 us on 8192 rows)
+int vectors_of(const GnArgs &a, bool backward) {
+    const int cg = a.C / a.G, V = vec_of(a);
+    if (V == 8) return cg <= 8 || (backward && cg <= 256) ? 1 : cg <= 512 ? 2 : 4;
+    if (V == 4) return cg <= 128 ? 1 : 8;
+    return cg <= 128 ? 4 : 32;
+}
+int team_of(const GnArgs &a, bool backward) {
+    const int per = vec_of(a) * vectors_of(a, backward), need = (a.C / a.G + per - 1) / per;
     int t = 1;
     while (t < need && t < 32) t *= 2;
     return t;
@@ -878,8 +887,8 @@ int chunk_rows(const GnArgs &a) {
     return static_cast<int>(rows);
 }
 // CTAs along the rows: `per_sm` of them per SM, if there are that many rows
-int row_ctas(const GnArgs &a, int V, int per_sm) {
-    const int per = kThr / team_of(a, V), gpc = per < a.G ? per : a.G, rows = per / gpc;
+int row_ctas(const GnArgs &a, int per_sm, bool backward) {
+    const int per = kThr / team_of(a, backward), gpc = per < a.G ? per : a.G, rows = per / gpc;
     const int by = (a.G + gpc - 1) / gpc;
     long long bx = (148 * per_sm + by - 1) / by;
     const long long most = (a.N + rows - 1) / rows;
@@ -891,21 +900,21 @@ size_t al(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 // rows in flight per team
 template <int V, int K>
 constexpr int rows_held(bool backward) {
-    return V * K <= 8 ? 2 : 1;
+    return V * K <= (backward ? 8 : 16) ? 2 : 1;
 }
 
 template <typename TX, typename TY, int V, int K>
 cudaError_t row_forward(const GnArgs &a, cudaStream_t s) {
-    const int team = team_of(a, V), per = kThr / team, gpc = per < a.G ? per : a.G;
-    const dim3 grid(row_ctas(a, V, 8), (a.G + gpc - 1) / gpc);
+    const int team = team_of(a, false), per = kThr / team, gpc = per < a.G ? per : a.G;
+    const dim3 grid(row_ctas(a, 8, false), (a.G + gpc - 1) / gpc);
     gn_row_forward_kernel<TX, TY, V, K, rows_held<V, K>(false)><<<grid, kThr, 0, s>>>(a, team);
     return cudaGetLastError();
 }
 
 template <typename TX, typename TY, int V, int K>
 cudaError_t row_backward(const GnArgs &a, cudaStream_t s) {
-    const int team = team_of(a, V), per = kThr / team, gpc = per < a.G ? per : a.G, rows = per / gpc;
-    const int bx = row_ctas(a, V, 4);
+    const int team = team_of(a, true), per = kThr / team, gpc = per < a.G ? per : a.G, rows = per / gpc;
+    const int bx = row_ctas(a, 4, true);
     const dim3 grid(bx, (a.G + gpc - 1) / gpc);
     const int smem = rows * 2 * gpc * (a.C / a.G) * 4;
     auto k = gn_row_backward_kernel<TX, TY, V, K, rows_held<V, K>(true)>;
@@ -953,15 +962,21 @@ template <typename TX, typename TY, bool BACK>
 cudaError_t dispatch(const GnArgs &a, cudaStream_t s) {
     const int V = vec_of(a);
     if (row_regime(a)) {
-        const int k = (a.C / a.G + 32 * V - 1) / (32 * V);  // vectors per lane of a full warp
+        const int K = vectors_of(a, BACK);
         if (BACK) {
-            if (V == 8) return k <= 1 ? row_backward<TX, TY, 8, 1>(a, s) : row_backward<TX, TY, 8, 4>(a, s);
-            if (V == 4) return k <= 1 ? row_backward<TX, TY, 4, 1>(a, s) : row_backward<TX, TY, 4, 8>(a, s);
-            return k <= 4 ? row_backward<TX, TY, 1, 4>(a, s) : row_backward<TX, TY, 1, 32>(a, s);
+            if (V == 8)
+                return K == 1   ? row_backward<TX, TY, 8, 1>(a, s)
+                       : K == 2 ? row_backward<TX, TY, 8, 2>(a, s)
+                                : row_backward<TX, TY, 8, 4>(a, s);
+            if (V == 4) return K == 1 ? row_backward<TX, TY, 4, 1>(a, s) : row_backward<TX, TY, 4, 8>(a, s);
+            return K == 4 ? row_backward<TX, TY, 1, 4>(a, s) : row_backward<TX, TY, 1, 32>(a, s);
         }
-        if (V == 8) return k <= 1 ? row_forward<TX, TY, 8, 1>(a, s) : row_forward<TX, TY, 8, 4>(a, s);
-        if (V == 4) return k <= 1 ? row_forward<TX, TY, 4, 1>(a, s) : row_forward<TX, TY, 4, 8>(a, s);
-        return k <= 4 ? row_forward<TX, TY, 1, 4>(a, s) : row_forward<TX, TY, 1, 32>(a, s);
+        if (V == 8)
+            return K == 1   ? row_forward<TX, TY, 8, 1>(a, s)
+                   : K == 2 ? row_forward<TX, TY, 8, 2>(a, s)
+                            : row_forward<TX, TY, 8, 4>(a, s);
+        if (V == 4) return K == 1 ? row_forward<TX, TY, 4, 1>(a, s) : row_forward<TX, TY, 4, 8>(a, s);
+        return K == 4 ? row_forward<TX, TY, 1, 4>(a, s) : row_forward<TX, TY, 1, 32>(a, s);
     }
     if (BACK) {
         if (a.gate != nullptr)
@@ -987,7 +1002,7 @@ cudaError_t by_type(const GnArgs &a, cudaStream_t s) {
 
 size_t gn_ws_bytes(const GnArgs &a, bool backward) {
     if (row_regime(a))
-        return backward ? al(static_cast<size_t>(row_ctas(a, vec_of(a), 4)) * 2 * a.C * 4) : 256;
+        return backward ? al(static_cast<size_t>(row_ctas(a, 4, true)) * 2 * a.C * 4) : 256;
     const int rows = chunk_rows(a), chunks = (a.S + rows - 1) / rows;
     if (!backward) return al(static_cast<size_t>(a.N) * chunks * a.G * sizeof(Moments));
     return al(static_cast<size_t>(a.N) * chunks * 2 * a.C * 4) + al(static_cast<size_t>(a.N) * 2 * a.C * 4) +
