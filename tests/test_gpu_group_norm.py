@@ -265,3 +265,25 @@ def test_two_layers_of_a_sequence_model():
     # fp32 throughout: each of the six stages is within a few hundred roundings of its own scale, in the 2-norm
     for got, want in ((y, Y[:, 0]), (g2["dweight"], dw2), (g1["dx"], dh), (g1["dweight"], dw1)):
         assert np.linalg.norm(n(got) - want) <= 6 * U * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("S,G", [(1, 16), (2100, 4)])
+def test_offsets_beyond_32_bits(S, G):
+    """More than 2^31 elements: the last rows equal those of a call on a copy of them, bit for bit where a row is its
+    own statistic, else within the forward's tolerance for another split of the rows."""
+    torch.cuda.empty_cache()
+    C = 1024
+    N = 2 ** 31 // (S * C) + 5
+    x = torch.empty(N, S, C, dtype=BF16, device="cuda").normal_(generator=torch.Generator(device="cuda").manual_seed(4))
+    assert x.numel() > 2 ** 31
+    w, b = torch.rand(C, device="cuda"), torch.rand(C, device="cuda")
+    y, stats = fw.group_norm(x, G, w, b)
+    ye, se = fw.group_norm(x[-3:].clone(), G, w, b)
+    far = lambda p, q: float((p.float() - q.float()).abs().max())
+    assert far(stats[-3:], se) <= (0 if S == 1 else U * 4) and far(y[-3:], ye) <= (0 if S == 1 else 2.0 ** -8 * 8)
+    dy = x
+    g = fw.group_norm_backward(x, stats, dy, G, w, b)
+    ge = fw.group_norm_backward(x[-3:].clone(), stats[-3:].clone(), dy[-3:].clone(), G, w, b)
+    assert far(g["dx"][-3:], ge["dx"]) <= 2.0 ** -7 * 8
+    del x, y, g
+    torch.cuda.empty_cache()

@@ -331,3 +331,51 @@ def test_captured_calls_on_other_streams_and_memory():
     for i, (o, s) in enumerate(outs):
         want = (want_a, want_b)[i % 2][0]
         assert torch.equal(o, want[0]) and torch.equal(s, want[1])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_offsets_beyond_32_bits(dtype):
+    """More than 2^31 elements in every operand: the last sequence's last tokens equal those of a call on a copy of
+    them (the decay forgets everything before within 40 tokens, 2^-57), forward and backward."""
+    torch.cuda.empty_cache()
+    B, T, H, d, tail = 3, 70003, 84, 128, 256
+    assert B * T * H * d > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.empty(B, T, H, d, dtype=dtype, device="cuda").normal_(generator=g)
+    ld = torch.full((H,), -1.0, device="cuda")
+    end = x[2:, T - tail:].clone()
+    o, s = fw.linear_attention(x, x, x, ld)
+    oe, se = fw.linear_attention(end, end, end, ld)
+    # both evaluate the same sums from another start: twice the tolerance of one (see above), magnitudes below 16 d
+    step = 2.0 ** -7 if dtype == BF16 else 2.0 ** -15
+    assert float((o[2:, T - tail + 64:].float() - oe[:, 64:].float()).abs().max()) <= 2 * step * 16 * d ** 0.5
+    assert float((o[2:, T - tail + 64:].float() - oe[:, 64:].float()).norm() / oe[:, 64:].float().norm()) <= step
+    assert float((s[2:] - se).norm() / se.norm()) <= 2.0 ** -15
+    del o, s
+    grads = fw.linear_attention_backward(x, x, x, ld, x)
+    ge = fw.linear_attention_backward(end, end, end, ld, end)
+    for n in ("dq", "dk", "dv"):
+        a, b = grads[n][2:, T - tail + 64:].float(), ge[n][:, 64:].float()
+        assert float((a - b).norm() / b.norm()) <= step, n
+    del grads, x
+    torch.cuda.empty_cache()
+
+
+def test_step_offsets_beyond_32_bits():
+    torch.cuda.empty_cache()
+    n_slots, H, d = 33000, 4, 128
+    pool = torch.zeros(n_slots, H, d, d, device="cuda")
+    assert pool.numel() > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(2)
+    q, k, v = (torch.randn(2, H, d, device="cuda", generator=g) for _ in range(3))
+    ld = torch.zeros(H, device="cuda")
+    slots = torch.tensor([n_slots - 1, 5], dtype=torch.int32, device="cuda")
+    o = fw.linear_attention_step(q, k, v, ld, pool, slots=slots, scale=1.0)
+    for b, i in enumerate(slots.tolist()):
+        assert torch.equal(pool[i], k[b][:, :, None] * v[b][:, None, :])
+        want = (q[b].double() * k[b].double()).sum(-1, keepdim=True) * v[b].double()
+        mag = (q[b].double() * k[b].double()).abs().sum(-1, keepdim=True) * v[b].double().abs()
+        assert bool(((o[b].double() - want).abs() <= (d + 4) * 2.0 ** -24 * mag).all())
+    assert int((pool.view(n_slots, -1)[:, 0] != 0).sum()) == 2
+    del pool
+    torch.cuda.empty_cache()
