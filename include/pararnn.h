@@ -727,8 +727,8 @@ typedef struct {
 } pararnn_attention_shape;
 
 /* pararnn_linear_attention_workspace_size -- bytes pararnn_linear_attention
- * needs for these operands (bf16 rows off 16 bytes are packed there first), or
- * 0 for arguments it rejects. */
+ * needs for these operands (bf16 rows off 16 bytes are packed there first); 1
+ * where it needs none, and then takes NULL; 0 for arguments it rejects. */
 PARARNN_API size_t pararnn_linear_attention_workspace_size(const pararnn_attention_shape *shape, const pararnn_rows *q,
                                                            const pararnn_rows *k, const pararnn_rows *v);
 
@@ -765,8 +765,8 @@ PARARNN_API int pararnn_linear_attention(const pararnn_attention_shape *shape, c
                                          size_t ws_bytes, pararnn_stream stream);
 
 /* pararnn_linear_attention_backward_workspace_size -- bytes
- * pararnn_linear_attention_backward needs for these operands, or 0 for
- * arguments it rejects. */
+ * pararnn_linear_attention_backward needs for these operands (1: none, 0:
+ * rejected, as above). */
 PARARNN_API size_t pararnn_linear_attention_backward_workspace_size(const pararnn_attention_shape *shape,
                                                                     const pararnn_rows *q, const pararnn_rows *k,
                                                                     const pararnn_rows *v, const pararnn_rows *d_o);
@@ -831,7 +831,8 @@ typedef struct {
     float eps;
 } pararnn_norm_shape;
 
-/* Bytes of workspace the two calls below need, or 0 for rejected arguments. */
+/* Bytes of workspace the two calls below need; 1 where they need none, and then
+ * take NULL; 0 for rejected arguments. */
 PARARNN_API size_t pararnn_group_norm_workspace_size(const pararnn_norm_shape *shape);
 PARARNN_API size_t pararnn_group_norm_backward_workspace_size(const pararnn_norm_shape *shape);
 

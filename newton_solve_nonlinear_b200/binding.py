@@ -831,13 +831,16 @@ def _attention_shape(q, k, v, log_decay, scale, dims: int = 4):
 
 
 def _workspace(need: int, name: str, workspace, device):
+    """(tensor, address, bytes) of a call's workspace; none is allocated where none is needed."""
     if need == 0:
         raise ValueError(f"arguments rejected by {name}_workspace_size")
     if workspace is None:
+        if need == 1:
+            return None, None, 0
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
         if workspace.data_ptr() % 256:
             workspace = alloc_workspace(need, device)
-    return workspace
+    return workspace, _dev(workspace, "workspace"), workspace.numel()
 
 
 def _checked(rc: int, name: str):
@@ -861,16 +864,15 @@ def linear_attention(q, k, v, log_decay, *, s0=None, lengths=None, scale=None, o
             return linear_attention(q, k, v, log_decay, s0=s0, lengths=lengths, scale=scale, out=out, workspace=workspace)
     shape, rq, rk, rv = _attention_shape(q, k, v, log_decay, scale)
     B, T, H, dk, dv = shape.B, shape.T, shape.H, shape.dk, shape.dv
-    o, s = out if out is not None else (torch.empty(B, T, H, dv, dtype=q.dtype, device=q.device),
-                                        torch.empty(B, H, dk, dv, dtype=torch.float32, device=q.device))
+    o, s = out if out is not None else (q.new_empty((B, T, H, dv)), log_decay.new_empty((B, H, dk, dv)))
     L = lib()
-    ws = _workspace(L.pararnn_linear_attention_workspace_size(shape, rq, rk, rv), "pararnn_linear_attention", workspace,
-                    q.device)
+    ws, ws_at, ws_bytes = _workspace(L.pararnn_linear_attention_workspace_size(shape, rq, rk, rv), "pararnn_linear_attention",
+                                       workspace, q.device)
     _checked(L.pararnn_linear_attention(
         shape, rq, rk, rv, _like(log_decay, "log_decay", q, (H,), torch.float32),
         _like(s0, "s0", q, (B, H, dk, dv), torch.float32), _like(lengths, "lengths", q, (B,), torch.int32),
         _like(o, "out", q, (B, T, H, dv), q.dtype), _like(s, "out", q, (B, H, dk, dv), torch.float32),
-        _dev(ws, "workspace"), ws.numel(), _current(q)), "pararnn_linear_attention")
+        ws_at, ws_bytes, _current(q)), "pararnn_linear_attention")
     return o, s
 
 
@@ -888,18 +890,17 @@ def linear_attention_backward(q, k, v, log_decay, do, *, s0=None, ds=None, lengt
     shape, rq, rk, rv = _attention_shape(q, k, v, log_decay, scale)
     B, T, H, Hkv, dk, dv = shape.B, shape.T, shape.H, shape.Hkv, shape.dk, shape.dv
     rdo = _rows(do, "do", q, (B, T, H, dv))
-    new = lambda *s, dtype=q.dtype: torch.empty(*s, dtype=dtype, device=q.device)
-    g = dict(dq=new(B, T, H, dk), dk=new(B, T, Hkv, dk), dv=new(B, T, Hkv, dv),
-             ds0=None if s0 is None else new(B, H, dk, dv, dtype=torch.float32))
+    g = dict(dq=q.new_empty((B, T, H, dk)), dk=q.new_empty((B, T, Hkv, dk)), dv=q.new_empty((B, T, Hkv, dv)),
+             ds0=None if s0 is None else s0.new_empty((B, H, dk, dv)))
     L = lib()
-    ws = _workspace(L.pararnn_linear_attention_backward_workspace_size(shape, rq, rk, rv, rdo),
-                    "pararnn_linear_attention_backward", workspace, q.device)
+    ws, ws_at, ws_bytes = _workspace(L.pararnn_linear_attention_backward_workspace_size(shape, rq, rk, rv, rdo),
+                                       "pararnn_linear_attention_backward", workspace, q.device)
     state = (B, H, dk, dv)
     _checked(L.pararnn_linear_attention_backward(
         shape, rq, rk, rv, _like(log_decay, "log_decay", q, (H,), torch.float32), rdo,
         _like(s0, "s0", q, state, torch.float32), _like(ds, "ds", q, state, torch.float32),
         _like(lengths, "lengths", q, (B,), torch.int32), g["dq"].data_ptr(), g["dk"].data_ptr(), g["dv"].data_ptr(),
-        None if s0 is None else g["ds0"].data_ptr(), _dev(ws, "workspace"), ws.numel(), _current(q)),
+        None if s0 is None else g["ds0"].data_ptr(), ws_at, ws_bytes, _current(q)),
         "pararnn_linear_attention_backward")
     return g
 
@@ -924,7 +925,7 @@ def linear_attention_step(q, k, v, log_decay, state, *, slots=None, scale=None, 
     if slots is None and n != B:
         raise ValueError(f"state has {n} rows for {B} sequences: slots says which")
     if out is None:
-        out = torch.empty(B, H, dv, dtype=q.dtype, device=q.device)
+        out = q.new_empty((B, H, dv))
     pool = (n, H, dk, dv)
     src = _like(state, "state", q, pool, torch.float32)
     _checked(lib().pararnn_linear_attention_step(
@@ -971,12 +972,12 @@ def group_norm(x, groups: int, weight=None, bias=None, *, gate=None, act: str = 
     y = out if out is not None else torch.empty(x.shape, dtype=y_dtype, device=x.device)
     stats = torch.empty(shape.N, groups, 2, dtype=torch.float32, device=x.device)
     L = lib()
-    ws = _workspace(L.pararnn_group_norm_workspace_size(shape), "pararnn_group_norm", workspace, x.device)
+    ws, ws_at, ws_bytes = _workspace(L.pararnn_group_norm_workspace_size(shape), "pararnn_group_norm", workspace, x.device)
     _checked(L.pararnn_group_norm(
         shape, _dev(x, "x"), _like(weight, "weight", x, channels, torch.float32),
         _like(bias, "bias", x, channels, torch.float32), _like(gate, "gate", x, x.shape, x.dtype),
         _like(lengths, "lengths", x, (shape.N,), torch.int32), _like(y, "out", x, x.shape, y_dtype), stats.data_ptr(),
-        _dev(ws, "workspace"), ws.numel(), _current(x)), "pararnn_group_norm")
+        ws_at, ws_bytes, _current(x)), "pararnn_group_norm")
     return y, stats
 
 
@@ -1001,9 +1002,10 @@ def group_norm_backward(x, stats, dy, groups: int, weight=None, bias=None, *, ga
     pg = _like(gate, "gate", x, x.shape, x.dtype)
     g = dict(dx=torch.empty_like(x), dweight=new(weight), dbias=new(bias), dgate=new(gate))
     L = lib()
-    ws = _workspace(L.pararnn_group_norm_backward_workspace_size(shape), "pararnn_group_norm_backward", workspace, x.device)
+    ws, ws_at, ws_bytes = _workspace(L.pararnn_group_norm_backward_workspace_size(shape), "pararnn_group_norm_backward",
+                                       workspace, x.device)
     _checked(L.pararnn_group_norm_backward(
         shape, px, _like(stats, "stats", x, (shape.N, groups, 2), torch.float32), _like(dy, "dy", x, x.shape, dy.dtype),
         pw, pb, pg, _like(lengths, "lengths", x, (shape.N,), torch.int32), ptr(g["dx"]), ptr(g["dweight"]),
-        ptr(g["dbias"]), ptr(g["dgate"]), _dev(ws, "workspace"), ws.numel(), _current(x)), "pararnn_group_norm_backward")
+        ptr(g["dbias"]), ptr(g["dgate"]), ws_at, ws_bytes, _current(x)), "pararnn_group_norm_backward")
     return g

@@ -1002,7 +1002,7 @@ cudaError_t by_type(const GnArgs &a, cudaStream_t s) {
 
 size_t gn_ws_bytes(const GnArgs &a, bool backward) {
     if (row_regime(a))
-        return backward ? al(static_cast<size_t>(row_ctas(a, 4, true)) * 2 * a.C * 4) : 256;
+        return backward ? al(static_cast<size_t>(row_ctas(a, 4, true)) * 2 * a.C * 4) : 0;
     const int rows = chunk_rows(a), chunks = (a.S + rows - 1) / rows;
     if (!backward) return al(static_cast<size_t>(a.N) * chunks * a.G * sizeof(Moments));
     return al(static_cast<size_t>(a.N) * chunks * 2 * a.C * 4) + al(static_cast<size_t>(a.N) * 2 * a.C * 4) +

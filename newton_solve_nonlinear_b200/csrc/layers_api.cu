@@ -1,5 +1,6 @@
 // layers_api.cu -- C entry points of the sequence-layer operators: linear attention with a decay for each head
 // (chunked form, backward pass, single-token step) and group norm with an activation or a gate.
+#include <algorithm>
 #include <cmath>
 
 #include "group_norm.cuh"
@@ -28,6 +29,12 @@ bool disjoint(const Extent *out, int n_out, const Extent *in, int n_in) {
             if (overlaps(out[i], in[j])) return false;
     }
     return true;
+}
+
+// What the size queries answer where a call needs no workspace: it then takes NULL.
+constexpr size_t kNone = 1;
+bool workspace_ok(size_t need, const void *p, size_t bytes) {
+    return need == kNone || (need != 0 && p != nullptr && aligned(p, 256) && bytes >= need);
 }
 
 size_t esize(int dtype) { return dtype == PARARNN_F32 ? 4 : 2; }
@@ -200,7 +207,7 @@ extern "C" {
 size_t pararnn_linear_attention_workspace_size(const pararnn_attention_shape *shape, const pararnn_rows *q,
                                                const pararnn_rows *k, const pararnn_rows *v) {
     if (!shape_ok(shape) || !rows_ok(q, shape->dtype) || !rows_ok(k, shape->dtype) || !rows_ok(v, shape->dtype)) return 0;
-    size_t most = 256;
+    size_t most = kNone;
     const int some = 0;
     for (const int *lengths : {static_cast<const int *>(nullptr), &some}) {  // with lengths or without: the larger
         Call c(*shape, nullptr);
@@ -214,14 +221,14 @@ int pararnn_linear_attention(const pararnn_attention_shape *shape, const pararnn
                              const pararnn_rows *v, const float *log_decay, const float *s0, const int *lengths,
                              void *o, float *s_out, void *workspace, size_t ws_bytes, pararnn_stream stream) {
     const size_t need = pararnn_linear_attention_workspace_size(shape, q, k, v);
-    if (need == 0 || ws_bytes < need || !workspace || !aligned(workspace, 256)) return PARARNN_INVALID_ARG;
+    if (!workspace_ok(need, workspace, ws_bytes)) return PARARNN_INVALID_ARG;
     const pararnn_attention_shape &s = *shape;
     if (!log_decay || !aligned(log_decay, 4) || !aligned(s0, 16) || !aligned(lengths, 4) || !o || !aligned(o, 16) ||
         !s_out || !aligned(s_out, 16))
         return PARARNN_INVALID_ARG;
     const Extent out[] = {{o, static_cast<size_t>(s.B) * s.T * s.H * s.dv * esize(s.dtype)},
                           {s_out, state_bytes(s)},
-                          {workspace, need}};
+                          {workspace, need == kNone ? 0 : need}};
     const Extent in[] = {extent(*q, s.B, s.T, s.H, s.dk, s.dtype), extent(*k, s.B, s.T, s.Hkv, s.dk, s.dtype),
                          extent(*v, s.B, s.T, s.Hkv, s.dv, s.dtype), {log_decay, s.H * sizeof(float)},
                          {lengths, s.B * sizeof(int)}, {s0 == s_out ? nullptr : s0, state_bytes(s)}};
@@ -238,7 +245,7 @@ size_t pararnn_linear_attention_backward_workspace_size(const pararnn_attention_
     if (!shape_ok(shape) || !rows_ok(q, shape->dtype) || !rows_ok(k, shape->dtype) || !rows_ok(v, shape->dtype) ||
         !rows_ok(d_o, shape->dtype))
         return 0;
-    size_t most = 256;
+    size_t most = kNone;
     const int some = 0;
     for (const int *lengths : {static_cast<const int *>(nullptr), &some}) {
         Call c(*shape, nullptr);
@@ -254,7 +261,7 @@ int pararnn_linear_attention_backward(const pararnn_attention_shape *shape, cons
                                       void *dq, void *dk, void *dv, float *ds0, void *workspace, size_t ws_bytes,
                                       pararnn_stream stream) {
     const size_t need = pararnn_linear_attention_backward_workspace_size(shape, q, k, v, d_o);
-    if (need == 0 || ws_bytes < need || !workspace || !aligned(workspace, 256)) return PARARNN_INVALID_ARG;
+    if (!workspace_ok(need, workspace, ws_bytes)) return PARARNN_INVALID_ARG;
     const pararnn_attention_shape &s = *shape;
     if (!log_decay || !aligned(log_decay, 4) || !aligned(s0, 16) || !aligned(ds, 16) || !aligned(lengths, 4) || !dq ||
         !dk || !dv || !aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16) || !aligned(ds0, 16))
@@ -264,7 +271,7 @@ int pararnn_linear_attention_backward(const pararnn_attention_shape *shape, cons
                           {dk, rows * s.Hkv * s.dk * e},
                           {dv, rows * s.Hkv * s.dv * e},
                           {ds0, state_bytes(s)},
-                          {workspace, need}};
+                          {workspace, need == kNone ? 0 : need}};
     const Extent in[] = {extent(*q, s.B, s.T, s.H, s.dk, s.dtype),   extent(*k, s.B, s.T, s.Hkv, s.dk, s.dtype),
                          extent(*v, s.B, s.T, s.Hkv, s.dv, s.dtype), extent(*d_o, s.B, s.T, s.H, s.dv, s.dtype),
                          {log_decay, s.H * sizeof(float)},           {lengths, s.B * sizeof(int)},
@@ -326,24 +333,24 @@ static GnArgs norm_args(const pararnn_norm_shape &s) {
 }
 
 size_t pararnn_group_norm_workspace_size(const pararnn_norm_shape *shape) {
-    return norm_ok(shape) ? gn_ws_bytes(norm_args(*shape), false) : 0;
+    return norm_ok(shape) ? std::max(gn_ws_bytes(norm_args(*shape), false), kNone) : 0;
 }
 
 size_t pararnn_group_norm_backward_workspace_size(const pararnn_norm_shape *shape) {
-    return norm_ok(shape) ? gn_ws_bytes(norm_args(*shape), true) : 0;
+    return norm_ok(shape) ? std::max(gn_ws_bytes(norm_args(*shape), true), kNone) : 0;
 }
 
 int pararnn_group_norm(const pararnn_norm_shape *shape, const void *x, const float *weight, const float *bias,
                        const void *gate, const int *lengths, void *y, float *stats, void *workspace, size_t ws_bytes,
                        pararnn_stream stream) {
     const size_t need = pararnn_group_norm_workspace_size(shape);
-    if (need == 0 || ws_bytes < need || !workspace || !aligned(workspace, 256)) return PARARNN_INVALID_ARG;
+    if (!workspace_ok(need, workspace, ws_bytes)) return PARARNN_INVALID_ARG;
     const pararnn_norm_shape &s = *shape;
     if (!x || !y || !stats || !aligned(x, 16) || !aligned(y, 16) || !aligned(stats, 16) || !aligned(weight, 16) ||
         !aligned(bias, 16) || !aligned(gate, 16) || !aligned(lengths, 4))
         return PARARNN_INVALID_ARG;
     const size_t n = static_cast<size_t>(s.N) * s.S * s.C;
-    const Extent out[] = {{y, n * esize(s.y_dtype)}, {stats, static_cast<size_t>(s.N) * s.groups * 8}, {workspace, need}};
+    const Extent out[] = {{y, n * esize(s.y_dtype)}, {stats, static_cast<size_t>(s.N) * s.groups * 8}, {workspace, need == kNone ? 0 : need}};
     const Extent in[] = {{x, n * esize(s.x_dtype)}, {gate, n * esize(s.x_dtype)}, {weight, s.C * sizeof(float)},
                          {bias, s.C * sizeof(float)}, {lengths, s.N * sizeof(int)}};
     if (!disjoint(out, 3, in, 5)) return PARARNN_INVALID_ARG;
@@ -358,7 +365,7 @@ int pararnn_group_norm_backward(const pararnn_norm_shape *shape, const void *x, 
                                 float *dweight, float *dbias, void *dgate, void *workspace, size_t ws_bytes,
                                 pararnn_stream stream) {
     const size_t need = pararnn_group_norm_backward_workspace_size(shape);
-    if (need == 0 || ws_bytes < need || !workspace || !aligned(workspace, 256)) return PARARNN_INVALID_ARG;
+    if (!workspace_ok(need, workspace, ws_bytes)) return PARARNN_INVALID_ARG;
     const pararnn_norm_shape &s = *shape;
     if (!x || !stats || !dy || !dx || !aligned(x, 16) || !aligned(dy, 16) || !aligned(dx, 16) || !aligned(stats, 16) ||
         !aligned(weight, 16) || !aligned(bias, 16) || !aligned(gate, 16) || !aligned(dgate, 16) ||
@@ -367,7 +374,7 @@ int pararnn_group_norm_backward(const pararnn_norm_shape *shape, const void *x, 
     if ((gate == nullptr) != (dgate == nullptr)) return PARARNN_INVALID_ARG;
     const size_t n = static_cast<size_t>(s.N) * s.S * s.C, par = s.C * sizeof(float);
     const Extent out[] = {{dx, n * esize(s.x_dtype)}, {dgate, n * esize(s.x_dtype)}, {dweight, par}, {dbias, par},
-                          {workspace, need}};
+                          {workspace, need == kNone ? 0 : need}};
     const Extent in[] = {{x, n * esize(s.x_dtype)}, {gate, n * esize(s.x_dtype)}, {dy, n * esize(s.y_dtype)},
                          {stats, static_cast<size_t>(s.N) * s.groups * 8}, {weight, par}, {bias, par},
                          {lengths, s.N * sizeof(int)}};

@@ -54,22 +54,23 @@ def test_workspace_by_operands(L):
     r = lambda **kw: _rows(BASE, **kw)
     size = lambda *x: L.pararnn_linear_attention_workspace_size(s, *x)
     tensor = 2 * 100 * 4 * 64 * 2
-    assert size(r(), r(), r()) == 256
+    assert size(r(), r(), r()) == 1  # none
     for odd in (r(ptr=BASE + 2), r(stride_t=257), r(stride_h=0)):
         assert size(odd, r(), r()) == tensor
         assert size(odd, odd, odd) == 3 * tensor
     # fp32 needs none of it
     f = _shape(H=4, Hkv=4, dv=64)
-    assert L.pararnn_linear_attention_workspace_size(f, r(ptr=BASE + 4), r(), r()) == 256
+    assert L.pararnn_linear_attention_workspace_size(f, r(ptr=BASE + 4), r(), r()) == 1
     # odd widths: the outputs leave through the workspace too
     s = _shape(dtype=BF16, H=4, Hkv=4, dv=63)
     assert size(r(), r(), r()) == tensor
 
 
 def _attention(L, **kw):
-    s = _shape()
-    good = [_rows(BASE), _rows(2 * BASE, heads=2), _rows(3 * BASE, heads=2, width=32)]
+    s = _shape(T=1000)  # few heads: split in time, so it needs a workspace
+    good = [_rows(BASE, T=1000), _rows(2 * BASE, T=1000, heads=2), _rows(3 * BASE, T=1000, heads=2, width=32)]
     need = L.pararnn_linear_attention_workspace_size(s, *good)
+    assert need > 256
     a = dict(q=good[0], k=good[1], v=good[2], ld=4 * BASE, s0=None,
              lengths=None, o=5 * BASE, s=6 * BASE, ws=7 * BASE, n=need)
     a.update(kw)
