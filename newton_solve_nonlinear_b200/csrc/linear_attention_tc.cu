@@ -42,14 +42,15 @@ struct Lay {
     // a is free once both of its products are done: the outputs are staged there, if it is wide enough
     static constexpr int OUT = DV <= DK ? A : END, STAGE = DV <= DK ? END : END + DV / 64 * kPanel;
     static constexpr int SS = 2 * STAGE;                 // bf16 S: [DV rows][DK], K-major panels
-    static constexpr int TAB = SS + DK / 64 * DV * 128;  // floats: score weights 160, row weights 2 x 128
-    static constexpr int BARS = TAB + (160 + 256) * 4;
-    static constexpr int BYTES = BARS + 160 + 1024;
+    static constexpr int TAB = SS + DK / 64 * DV * 128;  // floats: score weights 160, row weights 2 x 160
+    static constexpr int BARS = TAB + (160 + 320) * 4;
+    static constexpr int BYTES = BARS + 136 + 1008;  // + alignment, from 16 bytes up
     // TMEM columns: scores, each half of which becomes the weighted scores of its 64 columns (32-bit columns 0-31 and
-    // 64-95); out; dS; the weighted c's terms, smallest first, 64 columns each.  All of it fits but for DK = DV = 128,
-    // where the largest term takes the smallest one's place after its use.  Pass 1 has neither scores nor outputs:
-    // dS and two sets of terms, so that the next chunk is split while this one's products run.
-    static constexpr bool THREE = DK + DV <= 192;
+    // 64-95); out; dS; the weighted c's terms, smallest first, 64 columns each.  With DK = DV = 128 there is no room for
+    // the third: it takes the columns that the weighted scores leave free (32-63 and 96-127), once the scores have been
+    // read, and the next scores wait for its use.  Pass 1 has neither scores nor outputs: dS and two sets of terms, so
+    // that the next chunk is split while this one's products run.
+    static constexpr bool ROOM = DK + DV <= 192;
     static constexpr int T_S = 0, T_O = 128, T_D = 128 + DV, T_V = T_D + DK;
     static constexpr int T_D1 = 0, T_V1 = 128;
     static constexpr int STATE_WARPS = 8;
@@ -59,15 +60,15 @@ struct Lay {
 };
 
 struct Bars {
-    unsigned long long full[2], empty[2], staged[2], scores, inter, scaled, v, low, v_high, ss, out, ds, out_read;
+    unsigned long long full[2], empty[2], staged[2], scores, inter, p, scaled, v, ss, out, ds, out_read, clean;
     unsigned tmem;
     int err;
 };
-static_assert(sizeof(Bars) <= 160, "barriers");
+static_assert(sizeof(Bars) <= 136, "barriers");
 
 // A barrier's next phase completes only after everyone who waits for this one has seen it (the parity would be
-// ambiguous otherwise): the chains scores -> scaled -> out -> scores and v -> low -> v_high -> ds -> v order all but
-// the mover, whose barriers are one per stage, and a stage is filled again only by the mover itself.
+// ambiguous otherwise): the chains scores -> p -> scaled -> out -> scores and v -> ds -> v order all but the mover,
+// whose barriers are one per stage, and a stage is filled again only by the mover itself.
 
 // One sweep's arguments: its sizes and pointers, and the tensor maps of its tiles.
 struct TcSweep {
@@ -255,7 +256,9 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
     // weight of the score (row x, column y), intra g^|x - y| or 0, at sw[y - x]: of y - x in -127 .. 32 forward, in
     // -32 .. 127 reversed, as far as any block needs it
     float *sw = reinterpret_cast<float *>(smem + Y::TAB);
-    float *cw = sw + 160;  // [2][128]: update g^(n - e - j) of tile row x, for a full tile and for the last one
+    // update g^(n - e - j) of tile row x, for a full tile and for the last one: [2][8][20], row x = 64 h + 8 g + 2 l + i
+    // at [4 h + l][2 g + i], the order in which a lane of the state warps wants them (rows 20 apart: no bank conflicts)
+    float *cw = sw + 160;
     Bars *bars = reinterpret_cast<Bars *>(smem + Y::BARS);
     volatile int *err = &bars->err;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -293,12 +296,12 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         mbar_init(smem_u32(&bars->inter), 1);
         mbar_init(smem_u32(&bars->out), 1);
         mbar_init(smem_u32(&bars->ds), 1);
-        mbar_init(smem_u32(&bars->low), 1);
+        mbar_init(smem_u32(&bars->p), 8);
+        mbar_init(smem_u32(&bars->clean), Y::STATE_WARPS);
         mbar_init(smem_u32(&bars->scaled), 8);
         mbar_init(smem_u32(&bars->out_read), 8);
         mbar_init(smem_u32(&bars->v), Y::STATE_WARPS);
         mbar_init(smem_u32(&bars->ss), Y::STATE_WARPS);
-        mbar_init(smem_u32(&bars->v_high), Y::STATE_WARPS);
         bars->err = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -312,7 +315,8 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         sw[tid] = x >= 0 ? power(x) * w.intra : 0.f;
     } else if (tid < 160 + 256) {
         const int x = (tid - 160) & 127, n = tid - 160 < 128 ? kC : n_part, j = rev ? n - 1 - x : x;
-        cw[tid - 160] = x < n ? power(n - e - j) * w.update : 0.f;
+        cw[(tid - 160 < 128 ? 0 : 160) + ((x >> 6) * 4 + ((x & 7) >> 1)) * 20 + ((x & 63) >> 3) * 2 + (x & 1)] =
+            x < n ? power(n - e - j) * w.update : 0.f;
     }
     fence_before();
     __syncthreads();
@@ -354,6 +358,12 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                     }
                     // in the place of scores that this warp has read
                     tmem_st16(tl + Y::T_S + half * 64 + (jb & 1) * 16, u);
+                }
+                if (!Y::ROOM) {  // the state warps may write where scores were
+                    tmem_st_wait();
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive(smem_u32(&bars->p));
                 }
                 if (!mbar_wait(smem_u32(&bars->inter), ph, err)) break;
                 fence_after();
@@ -412,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         const int quarter = warp & 3, half = (warp - 8) >> 2;
         {
             constexpr int KH = DK / 2;
-            constexpr bool THREE = STATE_ONLY || Y::THREE;
+            constexpr bool HOLES = !STATE_ONLY && !Y::ROOM;  // the largest term stands between the weighted scores
             const int d = quarter * Y::ROWS + (lane & (Y::ROWS - 1));  // with 64 columns, lanes 16-31 have none
             const bool mine = lane < Y::ROWS;
             const unsigned tl = tm + (static_cast<unsigned>(quarter * 32) << 16);
@@ -493,8 +503,9 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                                          : "memory");
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
+                    if (lane == 0) arrive(smem_u32(&bars->clean));
                 }
-                const float *cwt = cw + (part ? 128 : 0) + half * 64 + 2 * (lane & 3);
+                const float *cwt = cw + (part ? 160 : 0) + (half * 4 + (lane & 3)) * 20;
                 const unsigned ta = tl + (STATE_ONLY ? Y::T_V1 + (c & 1) * 192 : Y::T_V) + half * 32;
                 // 16 columns of c (sub), 64 tokens; registers k, k + 1: the same 8 tokens, columns lane / 4 and + 8
                 auto load_c = [&](int sub, unsigned (&u)[16]) {
@@ -504,15 +515,17 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                     for (int tb = 0; tb < 4; ++tb)
                         ldmatrix4t(at + tb * 2048, u[4 * tb], u[4 * tb + 1], u[4 * tb + 2], u[4 * tb + 3]);
                 };
+                bool seen = true;
 #pragma unroll 1
                 for (int sub = 0; sub < Y::ROWS / 16; ++sub) {
                     unsigned u0[16], u1[16], u2[16];
                     load_c(sub, u1);
 #pragma unroll
                     for (int q = 0; q < 16; ++q) {
-                        const float2 f = *reinterpret_cast<const float2 *>(cwt + (q >> 1) * 8);
+                        const float4 f4 = *reinterpret_cast<const float4 *>(cwt + (q >> 2) * 4);
+                        const float f0 = q & 2 ? f4.z : f4.x, f1 = q & 2 ? f4.w : f4.y;
                         float y0 = lo_of(u1[q]), y1 = hi_of(u1[q]);
-                        mul2(y0, y1, f.x, f.y);
+                        mul2(y0, y1, f0, f1);
                         u0[q] = pack(y0, y1);
                         sub2(y0, y1, lo_of(u0[q]), hi_of(u0[q]));
                         u1[q] = pack(y0, y1);
@@ -522,35 +535,19 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                     const unsigned tsub = ta + (static_cast<unsigned>(sub * 16) << 16);
                     tmem_st_frag(tsub, u2);
                     tmem_st_frag(tsub + 64, u1);
-                    if (THREE) tmem_st_frag(tsub + 128, u0);
+                    if (HOLES) {
+                        if (sub == 0 && !(seen = mbar_wait(smem_u32(&bars->p), ph, err))) break;
+                        fence_after();
+                        tmem_st_frag(tl + (static_cast<unsigned>(sub * 16) << 16) + Y::T_S + half * 64 + 32, u0);
+                    } else {
+                        tmem_st_frag(tsub + 128, u0);
+                    }
                 }
-                if (STATE_ONLY && c > 0 && !absorb(c - 1)) break;
+                if (!seen || (STATE_ONLY && c > 0 && !absorb(c - 1))) break;
                 tmem_st_wait();
                 fence_before();
                 __syncwarp();
                 if (lane == 0) arrive(smem_u32(&bars->v));
-                if (!THREE) {
-                    // the smallest term has been used: the largest takes its place (formed again: registers are short)
-                    if (!mbar_wait(smem_u32(&bars->low), ph, err)) break;
-                    fence_after();
-#pragma unroll 1
-                    for (int sub = 0; sub < Y::ROWS / 16; ++sub) {
-                        unsigned u[16];
-                        load_c(sub, u);
-#pragma unroll
-                        for (int q = 0; q < 16; ++q) {
-                            const float2 f = *reinterpret_cast<const float2 *>(cwt + (q >> 1) * 8);
-                            float y0 = lo_of(u[q]), y1 = hi_of(u[q]);
-                            mul2(y0, y1, f.x, f.y);
-                            u[q] = pack(y0, y1);
-                        }
-                        tmem_st_frag(ta + (static_cast<unsigned>(sub * 16) << 16), u);
-                    }
-                    tmem_st_wait();
-                    fence_before();
-                    __syncwarp();
-                    if (lane == 0) arrive(smem_u32(&bars->v_high));
-                }
                 if (!STATE_ONLY) {
                     if (!absorb(c)) break;
                     publish();
@@ -583,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         constexpr unsigned id_out = make_idesc(1u, 128, DV) | kNMajorB, id_ds = make_idesc(1u, 128, DK) | kNMajorB;
         const unsigned on = elect_one() ? 1u : 0u;
         const unsigned tu = __shfl_sync(0xffffffffu, tm, 0);
-        constexpr bool THREE = STATE_ONLY || Y::THREE;
+        constexpr bool HOLES = !STATE_ONLY && !Y::ROOM;
         int done = 0;  // chunks issued whole
         auto scores = [&](int c) {
             const unsigned ta = sm + (c & 1) * Y::STAGE + Y::A, tb = sm + (c & 1) * Y::STAGE + Y::B;
@@ -599,12 +596,14 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             const unsigned td = tu + (STATE_ONLY ? Y::T_D1 : Y::T_D);
             const unsigned tv = tu + (STATE_ONLY ? Y::T_V1 + (c & 1) * 192 : Y::T_V) + place * 64;
 #pragma unroll 2
-            for (int k = 0; k < kC / 16; ++k)
-                mma_ts(td, tv + k * 8, nmajor_desc(tb + k * 2048), id_ds, !first || k > 0, on);
+            for (int k = 0; k < kC / 16; ++k) {
+                const unsigned ta = HOLES && place == 2 ? tu + Y::T_S + 32 + (k >> 2) * 64 + (k & 3) * 8 : tv + k * 8;
+                mma_ts(td, ta, nmajor_desc(tb + k * 2048), id_ds, !first || k > 0, on);
+            }
         };
-        // a tile whose rows the state warps clear is clean once they have arrived at v
+        // scores of the tile whose rows the state warps clear wait for that
         if (chunks > 0 && mbar_wait(smem_u32(&bars->full[0]), 0, err) &&
-            !(part_chunk == 0 && unclean && !mbar_wait(smem_u32(&bars->v), 0, err))) {
+            !(part_chunk == 0 && unclean && !mbar_wait(smem_u32(&bars->clean), 0, err))) {
             fence_after();
             if (!STATE_ONLY) scores(0);
             for (int c = 0; c < chunks; ++c) {
@@ -622,15 +621,17 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                     commit(smem_u32(&bars->inter), on);
                 }
                 // dS, the smallest term first; dS's place is free: v comes after the state warps have read it
-                if (!mbar_wait(smem_u32(&bars->v), ph, err)) break;
-                fence_after();
-                term(c, 0, true);
-                if (!THREE) commit(smem_u32(&bars->low), on);
-                term(c, 1, false);
-                if (THREE) {
+                auto state_products = [&]() {
+                    if (!mbar_wait(smem_u32(&bars->v), ph, err)) return false;
+                    fence_after();
+                    term(c, 0, true);
+                    term(c, 1, false);
                     term(c, 2, false);
                     commit(smem_u32(&bars->ds), on);
-                }
+                    return true;
+                };
+                // which comes first is which operand is ready first
+                if (!HOLES && !state_products()) break;
                 if (!STATE_ONLY) {
                     if (!mbar_wait(smem_u32(&bars->scaled), ph, err)) break;
                     fence_after();
@@ -640,19 +641,15 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                                true, on);
                     commit(smem_u32(&bars->out), on);
                 }
-                if (!THREE) {
-                    if (!mbar_wait(smem_u32(&bars->v_high), ph, err)) break;
-                    fence_after();
-                    term(c, 0, false);
-                    commit(smem_u32(&bars->ds), on);
-                }
+                if (HOLES && !state_products()) break;
                 commit(smem_u32(&bars->empty[st]), on);
                 done = c + 1;
                 if (c + 1 < chunks) {
                     if (!mbar_wait(smem_u32(&bars->full[st ^ 1]), ((c + 1) >> 1) & 1, err)) break;
                     if (!STATE_ONLY) {  // the next scores, as soon as the weighted ones have been used
                         if (!mbar_wait(smem_u32(&bars->out), ph, err)) break;
-                        if (c + 1 == part_chunk && unclean && !mbar_wait(smem_u32(&bars->v), ph ^ 1u, err)) break;
+                        if (HOLES && !mbar_wait(smem_u32(&bars->ds), ph, err)) break;
+                        if (c + 1 == part_chunk && unclean && !mbar_wait(smem_u32(&bars->clean), 0, err)) break;
                         fence_after();
                         scores(c + 1);
                     }
