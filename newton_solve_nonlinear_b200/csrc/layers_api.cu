@@ -144,7 +144,7 @@ void build_forward(Call &c, const pararnn_rows &q, const pararnn_rows &k, const 
                    const float *s0, const int *lengths, void *o, float *s_out) {
     const pararnn_attention_shape &s = c.s;
     LaSweep &w = c.w[0];
-    c.sweep(w, log_decay, lengths, s.dk, s.dv, la_plan(s.B, s.T, s.H, s.dv, s.dtype, 1, lengths != nullptr));
+    c.sweep(w, log_decay, lengths, s.dk, s.dv, la_plan(s.B, s.T, s.H, s.dk, s.dv, s.dtype, 1, lengths != nullptr));
     w.a = c.in(q, s.H, s.dk), w.b = c.in(k, s.Hkv, s.dk), w.c = c.in(v, s.Hkv, s.dv);
     w.s_in = s0, w.s_out = s_out, w.s_i = s.dv, w.s_j = 1;
     c.out(w, o, s.dv);
@@ -163,8 +163,9 @@ Partials build_backward(Call &c, const pararnn_rows &q, const pararnn_rows &k, c
     Partials part{};
     const LaRows rq = c.in(q, s.H, s.dk), rk = c.in(k, s.Hkv, s.dk), rv = c.in(v, s.Hkv, s.dv),
                  ro = c.in(d_o, s.H, s.dv);
-    const LaPlan plan_v = la_plan(s.B, s.T, s.H, s.dv, s.dtype, 3, lengths != nullptr);  // the sweep whose state is [dk, dv]
-    const LaPlan plan_k = la_plan(s.B, s.T, s.H, s.dk, s.dtype, 3, lengths != nullptr);  // the sweeps whose state is [dv, dk]
+    // of the sweep whose state is [dk, dv], and of the two whose state is [dv, dk]
+    const LaPlan plan_v = la_plan(s.B, s.T, s.H, s.dk, s.dv, s.dtype, 3, lengths != nullptr);
+    const LaPlan plan_k = la_plan(s.B, s.T, s.H, s.dv, s.dk, s.dtype, 3, lengths != nullptr);
 
     // dq: the forward sweep on (do, v, k) from S_0^T
     LaSweep &x = c.w[0];

@@ -38,39 +38,54 @@ __device__ __forceinline__ int row_count(const LaSweep &w, int b) {
 }
 
 constexpr int kC = 32;     // rows per chunk
-constexpr int kDVT = 64;   // columns of c per CTA
 constexpr int kThr = 256;
 
-template <int DKP>
+template <int DKP, int DVT>
 constexpr int simt_smem_floats() {
-    return 2 * kC * (DKP + 4) + 2 * kC * (kDVT + 4) + kC * (kC + 4) + DKP * (kDVT + 4) + kC + 4;
+    return 2 * kC * (DKP + 4) + 2 * kC * (DVT + 4) + kC * (kC + 4) + DKP * (DVT + 4) + kC + 4;
 }
 
+// (a, b) += x (u, v): two FMAs in one instruction, for half the issue slots ([5, 2011, 12 x 96 / 80]: 291 -> 270 us)
+__device__ __forceinline__ void fma2(float &a, float &b, float x, float u, float v) {
+    asm("{.reg .b64 p, q, r; mov.b64 p, {%0, %1}; mov.b64 q, {%2, %2}; mov.b64 r, {%3, %4}; fma.rn.f32x2 p, q, r, p; "
+        "mov.b64 {%0, %1}, p;}"
+        : "+f"(a), "+f"(b)
+        : "f"(x), "f"(u), "f"(v));
+}
 __device__ __forceinline__ void fma4(float4 &acc, float x, const float4 &y) {
-    acc.x = fmaf(x, y.x, acc.x);
-    acc.y = fmaf(x, y.y, acc.y);
-    acc.z = fmaf(x, y.z, acc.z);
-    acc.w = fmaf(x, y.w, acc.w);
+    fma2(acc.x, acc.y, x, y.x, y.y);
+    fma2(acc.z, acc.w, x, y.z, y.w);
 }
 __device__ __forceinline__ float4 *f4(float *p) { return reinterpret_cast<float4 *>(p); }
+__device__ __forceinline__ float2 *f2(float *p) { return reinterpret_cast<float2 *>(p); }
 
-// acc[u] += sum_d x[i0 + u][d] y[d][j0 .. j0 + 3] for u < 4, rows of x and y PX and PY floats apart
-template <int PX, int PY>
-__device__ __forceinline__ void product4x4(float4 (&acc)[4], float *x, float *y, int depth) {
+// Four rows of a thread's columns j .. j + 3 and, with WIDE, e and e + 1
+template <bool WIDE>
+struct Piece {
+    float4 v[4];
+    float2 w[WIDE ? 4 : 1];
+};
+// acc[u] += sum_d x[u][d] y[d][columns], rows of x and y PX and PY floats apart
+template <int PX, int PY, bool WIDE>
+__device__ __forceinline__ void product(Piece<WIDE> &acc, float *x, float *y, int j, int e, int depth) {
 #pragma unroll 2
     for (int d = 0; d < depth; d += 4) {
         float4 xv[4], yv[4];
+        float2 zv[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             xv[u] = *f4(x + u * PX + d);
-            yv[u] = *f4(y + (d + u) * PY);
+            yv[u] = *f4(y + (d + u) * PY + j);
+            if (WIDE) zv[u] = *f2(y + (d + u) * PY + e);
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            fma4(acc[u], xv[u].x, yv[0]);
-            fma4(acc[u], xv[u].y, yv[1]);
-            fma4(acc[u], xv[u].z, yv[2]);
-            fma4(acc[u], xv[u].w, yv[3]);
+            const float f[4] = {xv[u].x, xv[u].y, xv[u].z, xv[u].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                fma4(acc.v[u], f[k], yv[k]);
+                if constexpr (WIDE) fma2(acc.w[u].x, acc.w[u].y, f[k], zv[k].x, zv[k].y);
+            }
         }
     }
 }
@@ -79,23 +94,25 @@ struct LaBatch {
     LaSweep w[3];
 };
 
-// One CTA: 64 columns of c of one head and one segment, 32 rows at a time, the state in shared memory; fp32 FMAs.
+// One CTA: DVT columns of c of one head and one segment, 32 rows at a time, the state in shared memory; fp32 FMAs.
 // Warps 0-3 form a S while warps 4-7 form the weighted scores and their product with c; then all update S.  The
 // next chunk's rows are loaded into registers before a chunk's arithmetic.  Bound by FMA issue and shared-memory
 // loads (8 loads of 16 bytes for 64 FMAs); 32 rows, because the scores' share of the arithmetic grows with them.
 // STATE_ONLY is pass 1 of a split sweep: the segment's own S_out, without a and without outputs.
-template <bool VEC, int DKP, bool STATE_ONLY>
+template <bool VEC, int DKP, int DVT, bool STATE_ONLY>
 __global__ void __launch_bounds__(kThr, 2) la_simt_kernel(const __grid_constant__ LaBatch batch) {
     const LaSweep &w = batch.w[blockIdx.z];
-    if (blockIdx.x >= w.B * w.H * ((w.dv + kDVT - 1) / kDVT)) return;  // the grid is the widest sweep's
-    constexpr int PK = DKP + 4, PV = kDVT + 4, PP = kC + 4;
+    if (blockIdx.x >= w.B * w.H * ((w.dv + DVT - 1) / DVT)) return;  // the grid is the widest sweep's
+    constexpr int PK = DKP + 4, PV = DVT + 4, PP = kC + 4;
+    constexpr bool WIDE = DVT > 64;
+    static_assert(DVT == 64 || DVT == 96, "columns per thread");
     extern __shared__ __align__(16) float sm[];
     float *As = sm, *Bs = As + kC * PK, *Cs = Bs + kC * PK, *Os = Cs + kC * PV, *Ps = Os + kC * PV, *Ss = Ps + kC * PP;
     float *pw = Ss + DKP * PV;  // g^0 .. g^C
 
     const int tid = threadIdx.x;
-    const int n_tile = (w.dv + kDVT - 1) / kDVT;
-    const int bh = blockIdx.x / n_tile, c0 = (blockIdx.x % n_tile) * kDVT;
+    const int n_tile = (w.dv + DVT - 1) / DVT;
+    const int bh = blockIdx.x / n_tile, c0 = (blockIdx.x % n_tile) * DVT;
     const int b = bh / w.H, h = bh % w.H, sg = blockIdx.y;
     const int L = row_count(w, b);
     if (STATE_ONLY && sg == (w.reverse ? 0 : w.n_seg - 1)) return;  // nobody starts from its state
@@ -103,14 +120,14 @@ __global__ void __launch_bounds__(kThr, 2) la_simt_kernel(const __grid_constant_
     const long long t_lo = static_cast<long long>(sg) * w.seg;
     const int lo_t = t_lo < L ? static_cast<int>(t_lo) : L, hi_t = t_lo + w.seg < L ? static_cast<int>(t_lo + w.seg) : L;
     const int lo = w.reverse ? L - hi_t : lo_t, hi = w.reverse ? L - lo_t : hi_t;
-    const int ncol = min(kDVT, w.dv - c0);
+    const int ncol = min(DVT, w.dv - c0);
     const float ld = safe_log_decay(w.log_decay[h]);
     for (int i = tid; i <= kC; i += kThr) pw[i] = decay_pow(ld, i);
 
     // the state this segment starts from
     const long long sbase = static_cast<long long>(bh) * w.dk * w.dv;
-    for (int i = tid; i < DKP * kDVT; i += kThr) {
-        const int d = i / kDVT, c = i % kDVT;
+    for (int i = tid; i < DKP * DVT; i += kThr) {
+        const int d = i / DVT, c = i % DVT;
         float x = 0.f;
         if (!STATE_ONLY && d < w.dk && c < ncol) {
             if (w.n_seg > 1)
@@ -131,8 +148,8 @@ __global__ void __launch_bounds__(kThr, 2) la_simt_kernel(const __grid_constant_
     const int e = w.e;
     const float intra = w.intra, inter = w.inter, update = w.update;
 
-    // this thread's pieces of the next chunk: a, b [C][DKP] and c [C][64], zeros outside
-    constexpr int NK = kC * DKP / 4 / kThr, NV = kC * kDVT / 4 / kThr;
+    // this thread's pieces of the next chunk: a, b [C][DKP] and c [C][DVT], zeros outside
+    constexpr int NK = kC * DKP / 4 / kThr, NV = kC * DVT / 4 / kThr;
     float4 ra[NK], rb[NK], rc[NV];
     auto fetch = [&](int r0) {
         const int n = min(kC, hi - r0);
@@ -148,7 +165,7 @@ __global__ void __launch_bounds__(kThr, 2) la_simt_kernel(const __grid_constant_
         }
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int i = tid + k * kThr, r = i / (kDVT / 4), c = (i % (kDVT / 4)) * 4;
+            const int i = tid + k * kThr, r = i / (DVT / 4), c = (i % (DVT / 4)) * 4;
             rc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < n && c < ncol) {
                 const long long t = rev ? L - 1 - (r0 + r) : r0 + r;
@@ -169,15 +186,16 @@ __global__ void __launch_bounds__(kThr, 2) la_simt_kernel(const __grid_constant_
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int i = tid + k * kThr;
-            *f4(Cs + i / (kDVT / 4) * PV + (i % (kDVT / 4)) * 4) = rc[k];
+            *f4(Cs + i / (DVT / 4) * PV + (i % (DVT / 4)) * 4) = rc[k];
         }
         __syncthreads();
         if (r0 + kC < hi) fetch(r0 + kC);
         if (!STATE_ONLY) {
-            const int t = tid & 127, i0 = (t / 16) * 4, j0 = (t % 16) * 4;  // 4 x 4 outputs of each half's 128 threads
-            float4 acc[4] = {};
+            const int t = tid & 127, i0 = (t / 16) * 4, j0 = (t % 16) * 4;  // each half's 128 threads: 4 rows, 4 or 6
+            const int e0 = 64 + (t % 16) * 2;                            // columns each
+            Piece<WIDE> acc = {};
             if (tid < 128) {
-                if (i0 < n) product4x4<PK, PV>(acc, As + i0 * PK, Ss + j0, DKP);
+                if (i0 < n) product<PK, PV, WIDE>(acc, As + i0 * PK, Ss, j0, e0, DKP);
             } else {
                 // P = (a b^T) weighted, 2 x 4 per thread
                 const int p0 = (t / 8) * 2, q0 = t % 8;
@@ -205,9 +223,12 @@ __global__ void __launch_bounds__(kThr, 2) la_simt_kernel(const __grid_constant_
                         Ps[i * PP + j] = i >= j ? s[u][q] * pw[i >= j ? i - j : 0] * intra : 0.f;
                     }
                 asm volatile("bar.sync 1, 128;" ::: "memory");
-                if (i0 < n) product4x4<PP, PV>(acc, Ps + i0 * PP, Cs + j0, i0 + 4);
+                if (i0 < n) product<PP, PV, WIDE>(acc, Ps + i0 * PP, Cs, j0, e0, i0 + 4);
 #pragma unroll
-                for (int u = 0; u < 4; ++u) *f4(Os + (i0 + u) * PV + j0) = acc[u];
+                for (int u = 0; u < 4; ++u) {
+                    *f4(Os + (i0 + u) * PV + j0) = acc.v[u];
+                    if constexpr (WIDE) *f2(Os + (i0 + u) * PV + e0) = acc.w[u];
+                }
             }
             __syncthreads();
             if (tid < 128) {
@@ -217,29 +238,39 @@ __global__ void __launch_bounds__(kThr, 2) la_simt_kernel(const __grid_constant_
                         const float g = pw[min(i0 + u + e, kC)] * inter;
                         const float4 y = *f4(Os + (i0 + u) * PV + j0);
                         const long long tok = rev ? L - 1 - (r0 + i0 + u) : r0 + i0 + u;
-                        float *o = po + tok * ost + j0;
-                        const float4 x = make_float4(fmaf(g, acc[u].x, y.x), fmaf(g, acc[u].y, y.y),
-                                                     fmaf(g, acc[u].z, y.z), fmaf(g, acc[u].w, y.w));
+                        float *o = po + tok * ost;
+                        const float4 x = make_float4(fmaf(g, acc.v[u].x, y.x), fmaf(g, acc.v[u].y, y.y),
+                                                     fmaf(g, acc.v[u].z, y.z), fmaf(g, acc.v[u].w, y.w));
                         if (VEC) {  // widths are multiples of 4
-                            if (j0 < ncol) *f4(o) = x;
+                            if (j0 < ncol) *f4(o + j0) = x;
                         } else {
                             const float f[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                             for (int q = 0; q < 4; ++q)
-                                if (j0 + q < ncol) o[q] = f[q];
+                                if (j0 + q < ncol) o[j0 + q] = f[q];
+                        }
+                        if constexpr (WIDE) {
+                            const float2 z = *f2(Os + (i0 + u) * PV + e0);
+                            const float2 v = make_float2(fmaf(g, acc.w[u].x, z.x), fmaf(g, acc.w[u].y, z.y));
+                            if (VEC) {
+                                if (e0 < ncol) *f2(o + e0) = v;
+                            } else {
+                                if (e0 < ncol) o[e0] = v.x;
+                                if (e0 + 1 < ncol) o[e0 + 1] = v.y;
+                            }
                         }
                     }
             }
         }
-        {  // S = g^n S + update sum_j g^(n-e-j) b_j c_j^T: DKP/32 x 8 per thread
-            constexpr int RD = DKP / 32;
+        {  // S = g^n S + update sum_j g^(n-e-j) b_j c_j^T: DKP / 32 x DVT / 8 per thread
+            constexpr int RD = DKP / 32, CD = DVT / 32;
             const int d0 = (tid / 8) * RD, j0 = (tid % 8) * 4;
-            float4 acc[RD][2];
+            float4 acc[RD][CD];
             const float gn = pw[n];
 #pragma unroll
             for (int u = 0; u < RD; ++u)
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
+                for (int q = 0; q < CD; ++q) {
                     acc[u][q] = *f4(Ss + (d0 + u) * PV + j0 + 32 * q);
                     acc[u][q].x *= gn, acc[u][q].y *= gn, acc[u][q].z *= gn, acc[u][q].w *= gn;
                 }
@@ -254,17 +285,19 @@ __global__ void __launch_bounds__(kThr, 2) la_simt_kernel(const __grid_constant_
 #pragma unroll
                     for (int u = 0; u < RD; ++u) x[u] = Bs[j * PK + d0 + u];
                 }
-                const float4 y0 = *f4(Cs + j * PV + j0), y1 = *f4(Cs + j * PV + j0 + 32);
+                float4 y[CD];
+#pragma unroll
+                for (int q = 0; q < CD; ++q) y[q] = *f4(Cs + j * PV + j0 + 32 * q);
 #pragma unroll
                 for (int u = 0; u < RD; ++u) {
-                    fma4(acc[u][0], x[u] * f, y0);
-                    fma4(acc[u][1], x[u] * f, y1);
+#pragma unroll
+                    for (int q = 0; q < CD; ++q) fma4(acc[u][q], x[u] * f, y[q]);
                 }
             }
 #pragma unroll
             for (int u = 0; u < RD; ++u)
 #pragma unroll
-                for (int q = 0; q < 2; ++q) *f4(Ss + (d0 + u) * PV + j0 + 32 * q) = acc[u][q];
+                for (int q = 0; q < CD; ++q) *f4(Ss + (d0 + u) * PV + j0 + 32 * q) = acc[u][q];
         }
     }
     __syncthreads();
@@ -330,29 +363,31 @@ cudaError_t launch_la_join(const LaSweep &w, cudaStream_t s) {
 
 namespace {
 
-template <bool VEC, int DKP>
+template <bool VEC, int DKP, int DVT>
 cudaError_t launch_simt(const LaBatch &t, int n, cudaStream_t s) {
-    const int smem = simt_smem_floats<DKP>() * 4;
+    const int smem = simt_smem_floats<DKP, DVT>() * 4;
     unsigned tiles = 0;
-    for (int i = 0; i < n; ++i) tiles = max(tiles, static_cast<unsigned>((t.w[i].dv + kDVT - 1) / kDVT));
+    for (int i = 0; i < n; ++i) tiles = max(tiles, static_cast<unsigned>((t.w[i].dv + DVT - 1) / DVT));
     const LaSweep &w = t.w[0];
     const dim3 grid(static_cast<unsigned>(w.B) * w.H * tiles, w.n_seg, n);
     cudaError_t e;
     if (w.n_seg > 1) {
-        auto k1 = la_simt_kernel<VEC, DKP, true>;
+        auto k1 = la_simt_kernel<VEC, DKP, DVT, true>;
         if ((e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
         k1<<<grid, kThr, smem, s>>>(t);
         for (int i = 0; i < n; ++i)
             if ((e = launch_la_join(t.w[i], s)) != cudaSuccess) return e;
     }
-    auto k = la_simt_kernel<VEC, DKP, false>;
+    auto k = la_simt_kernel<VEC, DKP, DVT, false>;
     if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
     k<<<grid, kThr, smem, s>>>(t);
     return cudaGetLastError();
 }
 
 // width of a and b that the kernel is compiled for
-int simt_width(const LaSweep &w) { return w.dk <= 32 ? 32 : w.dk <= 64 ? 64 : w.dk <= 96 ? 96 : 128; }
+int simt_width(int dk) { return dk <= 32 ? 32 : dk <= 64 ? 64 : dk <= 96 ? 96 : 128; }
+// columns of c per CTA: 96 for 65 to 96 of them, where the state leaves shared memory for two CTAs per SM
+int simt_tile(int dk, int dv) { return dk <= 96 && dv > 64 && dv <= 96 ? 96 : 64; }
 
 bool rows_vec4(const LaRows &x) {
     return reinterpret_cast<uintptr_t>(x.p) % 16 == 0 && x.sb % 4 == 0 && x.st % 4 == 0 && x.sh % 4 == 0;
@@ -363,11 +398,12 @@ bool simt_vec(const LaSweep &w) {
 
 template <bool VEC>
 cudaError_t pick_width(const LaBatch &t, int n, cudaStream_t s) {
-    switch (simt_width(t.w[0])) {
-        case 32: return launch_simt<VEC, 32>(t, n, s);
-        case 64: return launch_simt<VEC, 64>(t, n, s);
-        case 96: return launch_simt<VEC, 96>(t, n, s);
-        default: return launch_simt<VEC, 128>(t, n, s);
+    const bool wide = simt_tile(t.w[0].dk, t.w[0].dv) == 96;
+    switch (simt_width(t.w[0].dk)) {
+        case 32: return wide ? launch_simt<VEC, 32, 96>(t, n, s) : launch_simt<VEC, 32, 64>(t, n, s);
+        case 64: return wide ? launch_simt<VEC, 64, 96>(t, n, s) : launch_simt<VEC, 64, 64>(t, n, s);
+        case 96: return wide ? launch_simt<VEC, 96, 96>(t, n, s) : launch_simt<VEC, 96, 64>(t, n, s);
+        default: return launch_simt<VEC, 128, 64>(t, n, s);
     }
 }
 
@@ -378,12 +414,12 @@ cudaError_t launch_la_simt(const LaSweep *w, int n, cudaStream_t s) {
     return simt_vec(w[0]) ? pick_width<true>(t, n, s) : pick_width<false>(t, n, s);
 }
 bool simt_together(const LaSweep &x, const LaSweep &y) {
-    return simt_width(x) == simt_width(y) && simt_vec(x) == simt_vec(y) && x.n_seg == y.n_seg && x.seg == y.seg;
+    return simt_width(x.dk) == simt_width(y.dk) && simt_tile(x.dk, x.dv) == simt_tile(y.dk, y.dv) && simt_vec(x) == simt_vec(y) && x.n_seg == y.n_seg && x.seg == y.seg;
 }
 
 }  // namespace
 
-LaPlan la_plan(int B, int T, int H, int dv, int dtype, int sweeps, bool ragged) {
+LaPlan la_plan(int B, int T, int H, int dk, int dv, int dtype, int sweeps, bool ragged) {
     const long long heads = static_cast<long long>(B) * H * sweeps;
     long long want, most;
     int unit;
@@ -398,7 +434,7 @@ LaPlan la_plan(int B, int T, int H, int dv, int dtype, int sweeps, bool ragged) 
         // two CTAs per SM, filled once, in segments of at least 128 rows; 1.5 times that many CTAs where lengths may
         // differ, so that short sequences leave room ([8, 2048, 16 x 64]: 342 us in 2 segments, 377 in 4; five
         // sequences of up to 2011 tokens, 12 heads of 96 and 80: 377 us in 2, 293 in 4)
-        const long long ctas = heads * ((dv + kDVT - 1) / kDVT);
+        const long long ctas = heads * ((dv + simt_tile(dk, dv) - 1) / simt_tile(dk, dv));
         want = ragged ? (444 + ctas - 1) / ctas : 296 / ctas;
         most = T / 128;
         unit = kC;

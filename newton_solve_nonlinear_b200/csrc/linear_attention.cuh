@@ -50,7 +50,7 @@ struct LaPlan {
     int n_seg, seg;
 };
 // `sweeps` of them run at once; ragged: the sequences' lengths may differ
-LaPlan la_plan(int B, int T, int H, int dv, int dtype, int sweeps, bool ragged);
+LaPlan la_plan(int B, int T, int H, int dk, int dv, int dtype, int sweeps, bool ragged);
 
 // n <= 3 independent sweeps; those that can share a launch do.
 cudaError_t launch_la_sweeps(const LaSweep *w, int n, cudaStream_t s);
