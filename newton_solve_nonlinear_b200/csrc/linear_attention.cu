@@ -431,12 +431,13 @@ LaPlan la_plan(int B, int T, int H, int dk, int dv, int dtype, int sweeps, bool 
         most = T / 512;
         unit = 128;
     } else {
-        // two CTAs per SM, filled once, in segments of at least 128 rows; 1.5 times that many CTAs where lengths may
-        // differ, so that short sequences leave room ([8, 2048, 16 x 64]: 342 us in 2 segments, 377 in 4; five
-        // sequences of up to 2011 tokens, 12 heads of 96 and 80: 377 us in 2, 293 in 4)
+        // two CTAs per SM, filled once, in segments of at least 64 rows ([1, 512, 4 x 64] forward 47 us with at least
+        // 128, 35 with 64, 31 with 32; ragged [3, 517, 6 x 48 / 64] backward 90, 70, 74); 1.5 times that many CTAs
+        // where lengths may differ, so that short sequences leave room ([8, 2048, 16 x 64]: 330 us in 2 segments, 360
+        // in 4; five sequences of up to 2011 tokens, 12 heads of 96 and 80: 242 us in 6, 205 in 8, 250 in 10)
         const long long ctas = heads * ((dv + simt_tile(dk, dv) - 1) / simt_tile(dk, dv));
         want = ragged ? (444 + ctas - 1) / ctas : 296 / ctas;
-        most = T / 128;
+        most = T / 64;
         unit = kC;
     }
     if (want > most) want = most;
