@@ -424,11 +424,16 @@ LaPlan la_plan(int B, int T, int H, int dk, int dv, int dtype, int sweeps, bool 
     long long want, most;
     int unit;
     if (dtype == PARARNN_BF16) {
-        // one CTA per SM: as many segments as fill the 148 SMs once, of at least 4 chunks of 128 rows.  Two segments
-        // are no gain: pass 1 costs about 0.6 of pass 2, so half the length is run 1.6 times.
+        // one CTA per SM: as many segments as fill the 148 SMs once.  A split costs about 1.6 times a segment's chunks,
+        // since pass 1 takes 0.6 of pass 2's time, and its two more launches as much as 6 chunks, or 9 with three joins
+        // in a row; so two segments are no gain, nor are short sequences (unsplit against split, forward 512 tokens of
+        // 8 heads of 64 16.4 / 22.5 us, 1024 24.6 / 24.6, 2048 41 / 26; backward 1024 27 / 31, 2048 43 / 35; backward of
+        // 16 heads of 128, 2048 tokens 68 / 78, 4096 121 / 107)
+        const int chunks = (T + 127) / 128;
         want = 148 / heads;
-        if (want < 3) want = 1;
-        most = T / 512;
+        if (want > chunks) want = chunks;
+        if (want < 3 || 8 * ((chunks + want - 1) / want) + 5 * (sweeps == 1 ? 6 : 9) >= 5 * chunks) want = 1;
+        most = chunks;
         unit = 128;
     } else {
         // two CTAs per SM, filled once, in segments of at least 64 rows ([1, 512, 4 x 64] forward 47 us with at least
