@@ -15,11 +15,16 @@
  *   - "Parallelizing non-linear sequential models over the sequence length",
  *     abstract (DEER).
  *
+ * Beside the solver stand the layers around a recurrence: linear attention, a
+ * recurrence with a matrix state (forward, backward, single token), and group
+ * norm with an activation or gate (forward, backward).
+ *
  * Conventions for every entry point
  *   - Device pointers are CUDA device addresses of the current device; host
  *     pointers are ordinary host memory.  Each argument says which it is.
  *   - Arrays are dense, row-major and contiguous; device arrays start on a
- *     16-byte boundary.
+ *     16-byte boundary.  Operands given as pararnn_rows have strides and need
+ *     only their elements' alignment.
  *   - The caller owns all memory, including the workspace.  The library
  *     allocates no device or host memory.  The host-buffer calls (the
  *     *_host entry points) keep two helper streams and their events per device

@@ -98,6 +98,8 @@ struct LaBatch {
 // Warps 0-3 form a S while warps 4-7 form the weighted scores and their product with c; then all update S.  The
 // next chunk's rows are loaded into registers before a chunk's arithmetic.  Bound by FMA issue and shared-memory
 // loads (8 loads of 16 bytes for 64 FMAs); 32 rows, because the scores' share of the arithmetic grows with them.
+// 8 x 2048 tokens, 16 heads of 128: 766 us, 25 TFLOP/s; five sequences of up to 2011 tokens, 12 heads of 96 and 80:
+// 205 us with tiles of 96 columns, 270 with 64 + 16.
 // STATE_ONLY is pass 1 of a split sweep: the segment's own S_out, without a and without outputs.
 template <bool VEC, int DKP, int DVT, bool STATE_ONLY>
 __global__ void __launch_bounds__(kThr, 2) la_simt_kernel(const __grid_constant__ LaBatch batch) {
@@ -564,7 +566,8 @@ namespace {
 
 // One CTA per row and head: S = g S + k v^T, out = scale S^T q.  Thread (ty, tx) holds VW consecutive columns of
 // every NY-th row of S; the column sums meet in shared memory.  Rows of the batch that name the same slot are
-// taken in row order by the first one's CTA: tokens that follow each other.
+// taken in row order by the first one's CTA: tokens that follow each other.  Bound by HBM, as each state is read and
+// written once: 256 rows, 16 heads of 128 x 128 take 89 us, 541 MB at 0.93 of a copy's rate.
 template <typename TI, int VW>
 __global__ void __launch_bounds__(256) la_step_kernel(const LaStep w) {
     __shared__ float qs[128], ks[128], part[256 * VW];

@@ -8,7 +8,7 @@
 //   dS^T   = (g^(n-e-j) c)^T b          [DV x DK]    weighted c in TMEM as the A operand
 //   S      = g^n S + dS                 in registers, fp32
 // A bf16 product is exact in fp32, so the only roundings below fp32 are those of the weighted scores and of S's
-// copy, each 2^-9 relative as the output's own.  The weighted c is split into three bf16 terms (24 bits), so the
+// copy, each at most 2^-8 relative as the output's own.  The weighted c is split into three bf16 terms (24 bits), so the
 // state's products are exact to fp32; they are summed smallest term first.
 //
 // Tiles are of 128 consecutive tokens from a multiple of 128 on, in the order of the tokens.  A reversed sweep
@@ -19,6 +19,13 @@
 // store), 8-15 state (lane quarter = columns of c; two halves of the rows to be split and of b's width), 16
 // issues the products, 17 moves the tiles (two stages).  Every wait is bounded; a wait that runs out marks this
 // CTA's results NaN.
+//
+// Measured on 8 x 8192 tokens, 16 heads of 128: 229 us alone on the GPU, 0.72 of a copy of its bytes; the tensor pipe is
+// busy 44 % of the time.  It is bound by the chain of a chunk, about 6300 cycles with 128 columns: split of the weighted c
+// (2800, with the scores' weighing beside it), products (1900), state update and its copy (700), which the next chunk's
+// products wait for.  Two chunks in flight would hide it, but at this width one fills 227 KB of shared memory and all 512
+// columns of TMEM.  128 tokens are one row of products for each TMEM lane.  Sixteen state warps with a quarter of the
+// work each gave 236 us: 72 registers a thread are too few for the output warps.
 #include <cuda_bf16.h>
 
 #include "linear_attention.cuh"
