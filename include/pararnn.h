@@ -719,7 +719,7 @@ typedef struct {
 } pararnn_rows;
 
 /* Linear attention with a decay for each head.
- *   B, T     sequences and tokens, >= 1.
+ *   B, T     sequences and tokens, >= 1; T at most 2^30.
  *   H, Hkv   heads of q and of k, v; H a multiple of Hkv (head h reads key and
  *            value head h / (H / Hkv)).
  *   dk, dv   widths of q, k and of v: 1 .. 128.

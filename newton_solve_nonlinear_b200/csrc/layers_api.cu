@@ -44,6 +44,7 @@ bool shape_ok(const pararnn_attention_shape *s) {
     if (s == nullptr || s->B < 1 || s->T < 1 || s->H < 1 || s->Hkv < 1 || s->H % s->Hkv != 0) return false;
     if (s->dk < 1 || s->dk > 128 || s->dv < 1 || s->dv > 128 || !dtype_ok(s->dtype)) return false;
     if (!std::isfinite(s->scale)) return false;
+    if (s->T > 1 << 30) return false;  // tokens are counted in 32 bits, in chunks that may pass the end
     // CTAs are counted in 32 bits: up to 64 per row and head
     return static_cast<long long>(s->B) * s->H <= (1ll << 24);
 }

@@ -223,6 +223,33 @@ def test_backward_padded_batch_and_extreme_decays(dtype):
     _check_backward(a, do, n(4, 4, 48, 64, dt=F32), lengths)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("dk,dv", [(32, 65), (31, 96), (64, 90), (96, 66), (95, 96), (96, 97), (97, 96), (128, 95),
+                                   (72, 72), (8, 94)])
+def test_widths_around_a_tile(dk, dv, dtype):
+    """Widths on both sides of 64 and 96, whole and odd: which columns a block takes, and which it has no more."""
+    B, T, H, Hkv = 2, 201, 2, 1
+    a, n = _make(B, T, H, Hkv, dk, dv, dtype)
+    lengths = torch.tensor([T, 97], dtype=torch.int32, device="cuda")
+    _check_forward(a)
+    _check_forward(a, lengths=lengths)
+    _check_backward(a, n(B, T, H, dv), n(B, H, dk, dv, dt=F32), lengths)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T", [65, 127, 128, 191, 896, 1023, 1024, 1281, 2048, 2177])
+def test_lengths_around_a_split(T, dtype):
+    """Lengths on both sides of where time is split into segments, full ones and one that ends a token early."""
+    B, H, Hkv, dk, dv = 2, 4, 2, 64, 64
+    a, n = _make(B, T, H, Hkv, dk, dv, dtype)
+    do, ds = n(B, T, H, dv), n(B, H, dk, dv, dt=F32)
+    lengths = torch.tensor([T // 2, T - 1], dtype=torch.int32, device="cuda")
+    _check_forward(a)
+    _check_forward(a, lengths=lengths)
+    _check_backward(a, do, ds)
+    _check_backward(a, do, ds, lengths)
+
+
 def test_backward_against_differences_of_the_forward():
     """Directional derivatives in fp32: the forward pass is bilinear in each operand, so a central difference with
     any step has no truncation error; its rounding is that of two forward passes, each within n 2^-24 of its sum

@@ -48,6 +48,18 @@ def test_attention_shapes(L, bad):
     assert L.pararnn_linear_attention_backward_workspace_size(_shape(**bad), r, r, r, r) == 0
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_attention_longest_sequence(L, dtype):
+    """Tokens are counted in 32 bits: up to 2^30 of them."""
+    r = _rows(BASE, T=1 << 30, heads=1, width=8)
+    shape = lambda t: _shape(B=1, T=t, H=1, Hkv=1, dk=8, dv=8, dtype=dtype)
+    size = lambda t: L.pararnn_linear_attention_workspace_size(shape(t), r, r, r)
+    back = lambda t: L.pararnn_linear_attention_backward_workspace_size(shape(t), r, r, r, r)
+    assert size(1 << 30) > 1 and back(1 << 30) > 1
+    for t in ((1 << 30) + 1, (1 << 31) - 100, (1 << 31) - 1):
+        assert size(t) == 0 and back(t) == 0
+
+
 def test_workspace_by_operands(L):
     """bf16 rows off 16 bytes, or shared by stride 0, are packed into the workspace; others are not."""
     s = _shape(dtype=BF16, H=4, Hkv=4, dv=64)
