@@ -96,8 +96,8 @@ struct LaBatch {
 
 // One CTA: DVT columns of c of one head and one segment, 32 rows at a time, the state in shared memory; fp32 FMAs.
 // Warps 0-3 form a S while warps 4-7 form the weighted scores and their product with c; then all update S.  The
-// next chunk's rows are loaded into registers before a chunk's arithmetic.  Bound by FMA issue and shared-memory
-// loads (8 loads of 16 bytes for 64 FMAs); 32 rows, because the scores' share of the arithmetic grows with them.
+// next chunk's rows are loaded into registers before a chunk's arithmetic.  Bound by shared-memory loads (8 of 16
+// bytes for 64 FMAs; the data pipe is busy 72 % of the time, FMA issue 35 %); 32 rows, because the scores' share of the arithmetic grows with them.
 // 8 x 2048 tokens, 16 heads of 128: 766 us, 25 TFLOP/s; five sequences of up to 2011 tokens, 12 heads of 96 and 80:
 // 205 us with tiles of 96 columns, 270 with 64 + 16.
 // STATE_ONLY is pass 1 of a split sweep: the segment's own S_out, without a and without outputs.

@@ -70,6 +70,14 @@ def test_linear_attention(B, T, H, Hkv, dk, dv, ragged, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("ragged", [False, True])
+@pytest.mark.parametrize("B,T,H,Hkv,dk,dv", [(2, 70, 2, 1, 96, 80), (1, 161, 3, 3, 31, 95), (2, 1100, 2, 2, 66, 65),
+                                             (1, 1153, 4, 2, 64, 64)])
+def test_linear_attention_in_wide_tiles_and_segments(B, T, H, Hkv, dk, dv, ragged, dtype):
+    test_linear_attention(B, T, H, Hkv, dk, dv, ragged, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("B,H,Hkv,dk,dv", [(1, 1, 1, 1, 1), (3, 4, 2, 64, 64), (2, 3, 3, 33, 127), (5, 2, 1, 128, 100)])
 def test_step(B, H, Hkv, dk, dv, dtype):
     L = binding.lib()
