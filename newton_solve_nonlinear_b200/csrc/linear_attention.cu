@@ -42,7 +42,7 @@ constexpr int kThr = 256;
 
 template <int DKP, int DVT>
 constexpr int simt_smem_floats() {
-    return 2 * kC * (DKP + 4) + 2 * kC * (DVT + 4) + kC * (kC + 4) + DKP * (DVT + 4) + kC + 4;
+    return 2 * kC * (DKP + 4) + 2 * kC * (DVT + 4) + kC * (kC + 4) + DKP * (DVT + 4) + kC + 4 + 2 * kC;
 }
 
 // (a, b) += x (u, v): two FMAs in one instruction, for half the issue slots ([5, 2011, 12 x 96 / 80]: 291 -> 270 us)
@@ -97,9 +97,10 @@ struct LaBatch {
 // One CTA: DVT columns of c of one head and one segment, 32 rows at a time, the state in shared memory; fp32 FMAs.
 // Warps 0-3 form a S while warps 4-7 form the weighted scores and their product with c; then all update S.  The
 // next chunk's rows are loaded into registers before a chunk's arithmetic.  Bound by shared-memory loads (8 of 16
-// bytes for 64 FMAs; the data pipe is busy 72 % of the time, FMA issue 35 %); 32 rows, because the scores' share of the arithmetic grows with them.
-// 8 x 2048 tokens, 16 heads of 128: 766 us, 25 TFLOP/s; five sequences of up to 2011 tokens, 12 heads of 96 and 80:
-// 205 us with tiles of 96 columns, 270 with 64 + 16.
+// bytes for 64 FMAs; the data pipe is busy 72 % of the time, FMA issue 35 %); 32 rows, because the scores' share of
+// the arithmetic grows with them.
+// 8 x 2048 tokens, 16 heads of 128: 750 us, 26 TFLOP/s; five sequences of up to 2011 tokens, 12 heads of 96 and 80:
+// 201 us with tiles of 96 columns (before the weights of two rows were read at once 205, and 270 with 64 + 16).
 // STATE_ONLY is pass 1 of a split sweep: the segment's own S_out, without a and without outputs.
 template <bool VEC, int DKP, int DVT, bool STATE_ONLY>
 __global__ void __launch_bounds__(kThr, 2) la_simt_kernel(const __grid_constant__ LaBatch batch) {
@@ -111,6 +112,7 @@ __global__ void __launch_bounds__(kThr, 2) la_simt_kernel(const __grid_constant_
     extern __shared__ __align__(16) float sm[];
     float *As = sm, *Bs = As + kC * PK, *Cs = Bs + kC * PK, *Os = Cs + kC * PV, *Ps = Os + kC * PV, *Ss = Ps + kC * PP;
     float *pw = Ss + DKP * PV;  // g^0 .. g^C
+    float *uw = pw + kC + 4;    // update g^(n - e - j) of row j, of a full chunk and of the last one, zero from n on
 
     const int tid = threadIdx.x;
     const int n_tile = (w.dv + DVT - 1) / DVT;
@@ -125,6 +127,10 @@ __global__ void __launch_bounds__(kThr, 2) la_simt_kernel(const __grid_constant_
     const int ncol = min(DVT, w.dv - c0);
     const float ld = safe_log_decay(w.log_decay[h]);
     for (int i = tid; i <= kC; i += kThr) pw[i] = decay_pow(ld, i);
+    for (int i = tid; i < 2 * kC; i += kThr) {
+        const int j = i % kC, n = i < kC ? kC : (hi - lo + kC - 1) % kC + 1;
+        uw[i] = j < n ? decay_pow(ld, n - w.e - j) * w.update : 0.f;
+    }
 
     // the state this segment starts from
     const long long sbase = static_cast<long long>(bh) * w.dk * w.dv;
@@ -148,7 +154,7 @@ __global__ void __launch_bounds__(kThr, 2) la_simt_kernel(const __grid_constant_
     const long long ost = static_cast<long long>(w.H) * w.out_w;
     const bool rev = w.reverse != 0;
     const int e = w.e;
-    const float intra = w.intra, inter = w.inter, update = w.update;
+    const float intra = w.intra, inter = w.inter;
 
     // this thread's pieces of the next chunk: a, b [C][DKP] and c [C][DVT], zeros outside
     constexpr int NK = kC * DKP / 4 / kThr, NV = kC * DVT / 4 / kThr;
@@ -276,24 +282,29 @@ __global__ void __launch_bounds__(kThr, 2) la_simt_kernel(const __grid_constant_
                     acc[u][q] = *f4(Ss + (d0 + u) * PV + j0 + 32 * q);
                     acc[u][q].x *= gn, acc[u][q].y *= gn, acc[u][q].z *= gn, acc[u][q].w *= gn;
                 }
+            const float *wj = uw + (n < kC ? kC : 0);
 #pragma unroll 2
-            for (int j = 0; j < n; ++j) {
-                const float f = pw[n - e - j] * update;
-                float x[RD];
-                if constexpr (RD == 4) {
-                    const float4 v = *f4(Bs + j * PK + d0);
-                    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-                } else {
+            for (int r = 0; r < n; r += 2) {  // rows from n on are zero
+                const float2 f = *reinterpret_cast<const float2 *>(wj + r);
+                const float g[2] = {f.x, f.y};
 #pragma unroll
-                    for (int u = 0; u < RD; ++u) x[u] = Bs[j * PK + d0 + u];
-                }
-                float4 y[CD];
+                for (int k = 0; k < 2; ++k) {
+                    const int j = r + k;
+                    float x[RD];
+                    if constexpr (RD == 4) {
+                        const float4 v = *f4(Bs + j * PK + d0);
+                        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+                    } else {
 #pragma unroll
-                for (int q = 0; q < CD; ++q) y[q] = *f4(Cs + j * PV + j0 + 32 * q);
+                        for (int u = 0; u < RD; ++u) x[u] = Bs[j * PK + d0 + u];
+                    }
+                    float4 y[CD];
 #pragma unroll
-                for (int u = 0; u < RD; ++u) {
+                    for (int q = 0; q < CD; ++q) y[q] = *f4(Cs + j * PV + j0 + 32 * q);
 #pragma unroll
-                    for (int q = 0; q < CD; ++q) fma4(acc[u][q], x[u] * f, y[q]);
+                    for (int u = 0; u < RD; ++u)
+#pragma unroll
+                        for (int q = 0; q < CD; ++q) fma4(acc[u][q], x[u] * g[k], y[q]);
                 }
             }
 #pragma unroll
