@@ -893,6 +893,8 @@ int chunk_rows(const GnArgs &a, bool backward) {
     if (rows > a.S) rows = a.S;
     return static_cast<int>(rows);
 }
+// blocks of `rows` rows in one n; S + rows may pass 32 bits
+int chunks_of(const GnArgs &a, int rows) { return static_cast<int>((static_cast<long long>(a.S) + rows - 1) / rows); }
 // CTAs along the rows: `per_sm` of them per SM, if there are that many rows
 int row_ctas(const GnArgs &a, int per_sm, bool backward) {
     const int per = kThr / team_of(a, backward), gpc = per < a.G ? per : a.G, rows = per / gpc;
@@ -934,7 +936,7 @@ cudaError_t row_backward(const GnArgs &a, cudaStream_t s) {
 
 template <typename TX, typename TY, int V>
 cudaError_t seq_forward(const GnArgs &a, cudaStream_t s) {
-    const int rows = chunk_rows(a, false), chunks = (a.S + rows - 1) / rows;
+    const int rows = chunk_rows(a, false), chunks = chunks_of(a, rows);
     Moments *part = reinterpret_cast<Moments *>(a.ws);
     const unsigned grid = static_cast<unsigned>(chunks) * a.N;
     gn_stats_kernel<TX, V><<<grid, threads_of<V>(a), a.G * sizeof(Moments), s>>>(a, rows, chunks, part);
@@ -950,7 +952,7 @@ cudaError_t seq_forward(const GnArgs &a, cudaStream_t s) {
 
 template <typename TX, typename TY, int V, bool GATE>
 cudaError_t seq_backward_g(const GnArgs &a, cudaStream_t s) {
-    const int rows = chunk_rows(a, true), chunks = (a.S + rows - 1) / rows;
+    const int rows = chunk_rows(a, true), chunks = chunks_of(a, rows);
     const unsigned grid = static_cast<unsigned>(chunks) * a.N;
     float *part = reinterpret_cast<float *>(a.ws);
     float *chan = reinterpret_cast<float *>(a.ws + al(static_cast<size_t>(a.N) * chunks * 2 * a.C * 4));
@@ -1010,7 +1012,7 @@ cudaError_t by_type(const GnArgs &a, cudaStream_t s) {
 size_t gn_ws_bytes(const GnArgs &a, bool backward) {
     if (row_regime(a))
         return backward ? al(static_cast<size_t>(row_ctas(a, 4, true)) * 2 * a.C * 4) : 0;
-    const int rows = chunk_rows(a, backward), chunks = (a.S + rows - 1) / rows;
+    const int rows = chunk_rows(a, backward), chunks = chunks_of(a, rows);
     if (!backward) return al(static_cast<size_t>(a.N) * chunks * a.G * sizeof(Moments));
     return al(static_cast<size_t>(a.N) * chunks * 2 * a.C * 4) + al(static_cast<size_t>(a.N) * 2 * a.C * 4) +
            al(static_cast<size_t>(a.N) * a.G * 8);

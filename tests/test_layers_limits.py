@@ -1,0 +1,19 @@
+"""The largest sizes that linear attention and group norm take, and what is refused above them.  CPU only: the size
+queries and the argument checks run on the host before anything is enqueued."""
+import pytest
+
+from newton_solve_nonlinear_b200 import binding
+from tests.test_layers_refusals import L, _norm  # noqa: F401 (L is a fixture)
+
+INT_MAX = 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("C", [1, 5, 8])
+@pytest.mark.parametrize("N,S", [(1, INT_MAX), (1, INT_MAX - 100), (1, 2 ** 31 - 3_000_000), (3, INT_MAX // 3)])
+def test_norm_workspace_of_the_longest_sequences(L, N, S, C):  # noqa: F811
+    """Rows are dealt to a fixed number of CTAs, so the workspace does not grow with S from some length on."""
+    for size in (L.pararnn_group_norm_workspace_size, L.pararnn_group_norm_backward_workspace_size):
+        shape = lambda s: _norm(N=N, S=s, C=C, groups=1)
+        base = size(shape(2 ** 29 // N))
+        assert base > 256
+        assert base // 2 <= size(shape(S)) <= 2 * base
