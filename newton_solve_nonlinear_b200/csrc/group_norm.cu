@@ -900,7 +900,7 @@ int row_ctas(const GnArgs &a, int per_sm, bool backward) {
     const int per = kThr / team_of(a, backward), gpc = per < a.G ? per : a.G, rows = per / gpc;
     const int by = (a.G + gpc - 1) / gpc;
     long long bx = (148 * per_sm + by - 1) / by;
-    const long long most = (a.N + rows - 1) / rows;
+    const long long most = (static_cast<long long>(a.N) + rows - 1) / rows;
     if (bx > most) bx = most;
     return static_cast<int>(bx < 1 ? 1 : bx);
 }

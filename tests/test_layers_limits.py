@@ -17,3 +17,11 @@ def test_norm_workspace_of_the_longest_sequences(L, N, S, C):  # noqa: F811
         base = size(shape(2 ** 29 // N))
         assert base > 256
         assert base // 2 <= size(shape(S)) <= 2 * base
+
+
+@pytest.mark.parametrize("C,groups", [(8, 1), (7, 7), (64, 4)])
+@pytest.mark.parametrize("N", [INT_MAX, INT_MAX - 1, INT_MAX - 200])
+def test_norm_of_the_most_rows_fills_the_card(L, N, C, groups):  # noqa: F811
+    """One row per statistic: the backward pass keeps a row of partial sums for each CTA, as many as for fewer rows."""
+    size = lambda n: L.pararnn_group_norm_backward_workspace_size(_norm(N=n, S=1, C=C, groups=groups))
+    assert size(N) == size(2 ** 24) >= 148 * 2 * C * 4
