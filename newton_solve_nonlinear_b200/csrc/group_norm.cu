@@ -555,9 +555,10 @@ __global__ void __launch_bounds__(kThr) gn_stats_kernel(const GnArgs a, int rows
     __shared__ Moments red[kThr];
     extern __shared__ Moments acc[];  // [G]
     const int n = static_cast<int>(blockIdx.x / chunks), ch = static_cast<int>(blockIdx.x % chunks), L = row_count(a, n);
-    const int lo = static_cast<int>(min(static_cast<long long>(ch) * rows, static_cast<long long>(L)));
-    const int hi = static_cast<int>(min((ch + 1ll) * rows, static_cast<long long>(L)));
-    const TX *x = static_cast<const TX *>(a.x) + static_cast<long long>(n) * a.S * a.C;
+    // rows are counted from the block's first one: counters step past the last row, and S may be 2^31 - 1
+    const long long lo = static_cast<long long>(ch) * rows;
+    const int count = lo < L ? static_cast<int>(min(static_cast<long long>(rows), L - lo)) : 0;
+    const TX *x = static_cast<const TX *>(a.x) + (static_cast<long long>(n) * a.S + lo) * a.C;
     const Span sp = span_of<V>(a);
     const int cg = a.C / a.G, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int g = threadIdx.x; g < a.G; g += blockDim.x) acc[g] = {0.f, 0.f, 0.f};
@@ -568,13 +569,13 @@ __global__ void __launch_bounds__(kThr) gn_stats_kernel(const GnArgs a, int rows
         Moments m = {0.f, 0.f, 0.f};
         if (col < width && r0 < sp.par) {
             const TX *p = x + static_cast<long long>(cb + col) * V;
-            for (int s = lo + r0; s < hi; s += RB * sp.par) {
+            for (int s = r0; s < count; s += RB * sp.par) {
                 float v[RB][V];
                 int cnt = 0;
                 float sum = 0.f;
 #pragma unroll
                 for (int u = 0; u < RB; ++u)
-                    if (s + u * sp.par < hi) {
+                    if (s + u * sp.par < count) {
                         load<V>(p + static_cast<long long>(s + u * sp.par) * a.C, v[u]);
                         ++cnt;
                     } else {
@@ -642,8 +643,10 @@ __global__ void __launch_bounds__(kThr) gn_apply_kernel(const GnArgs a, int rows
     const unsigned bid = gridDim.x - 1 - blockIdx.x;
     const int n = static_cast<int>(bid / chunks), ch = static_cast<int>(bid % chunks), L = row_count(a, n);
     const long long lo = static_cast<long long>(ch) * rows;
-    const int hi = static_cast<int>(min(lo + rows, static_cast<long long>(a.S)));
-    const long long nb = static_cast<long long>(n) * a.S * a.C;
+    // rows counted from the block's first one, as in gn_stats_kernel: `count` of them, the first `live` within the length
+    const int count = static_cast<int>(min(static_cast<long long>(rows), a.S - lo));
+    const int live = static_cast<int>(L - lo);
+    const long long nb = (static_cast<long long>(n) * a.S + lo) * a.C;
     const TX *x = static_cast<const TX *>(a.x) + nb;
     const TX *gate = a.gate == nullptr ? nullptr : static_cast<const TX *>(a.gate) + nb;
     TY *y = static_cast<TY *>(a.y) + nb;
@@ -672,10 +675,10 @@ __global__ void __launch_bounds__(kThr) gn_apply_kernel(const GnArgs a, int rows
             w[i] *= st.y;
         }
 #pragma unroll 4
-        for (int s = static_cast<int>(lo) + r0; s < hi; s += sp.par) {
+        for (int s = r0; s < count; s += sp.par) {
             const long long at = static_cast<long long>(s) * a.C + c;
             float o[V] = {};
-            if (s < L) {
+            if (s < live) {
                 float v[V], q[V];
                 load<V>(x + at, v);
                 if (gate != nullptr) load<V>(gate + at, q);
@@ -884,7 +887,8 @@ int team_of(const GnArgs &a, bool backward) {
     return t;
 }
 // rows per CTA: forward 4 CTAs of 256 threads per SM, as many as run at once (8: [16, 65536, 64] 139 against 129 us),
-// backward 8 (ragged [8, 1000, 640] 41 against 49 us with 4); at least about 4K elements each
+// backward 8 (ragged [8, 1000, 640] 41 against 49 us with 4); at least about 4K elements each.  N S is below 2^31, so that a
+// block has at most 3.7e6 rows and its kernel counts them in 32 bits
 int chunk_rows(const GnArgs &a, bool backward) {
     const long long all = static_cast<long long>(a.N) * a.S, ctas = 148 * (backward ? 8 : 4);
     long long rows = (all + ctas - 1) / ctas;

@@ -1,0 +1,61 @@
+"""Linear attention and group norm at the largest sizes that they take, and the kernel variants that only some widths
+reach."""
+import pytest
+import torch
+
+import newton_solve_nonlinear_b200 as fw
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+EPS24 = 2.0 ** -24
+
+
+def _slices(n, step=1 << 27):
+    return [slice(i, min(i + step, n)) for i in range(0, n, step)]
+
+
+@pytest.mark.parametrize("behind", [0, 5])
+def test_norm_of_the_longest_sequence(behind):
+    """2^31 - 1 rows of one channel, all of them or all but the last five: every row is read and written once.
+
+    A thread joins 8 of its rows at a time: 3.63e6 rows a block / 256 threads / 8 are 1772 joins in a row, and about 40
+    more across the threads, the warps and the 592 blocks.  Each rounds the mean once and the squares four times, so the
+    mean is within 1850 2^-24 (|mean| + the largest |x - mean|) and r within half of 4 * 1850 2^-24 of itself; y adds a
+    bf16 rounding, 2^-8 |y|.  In the backward pass a sum holds 7085 additions a thread, 256 across the threads and 1184
+    across the blocks: within 8600 2^-24 of the sum of absolute values."""
+    torch.cuda.empty_cache()
+    S = 2 ** 31 - 1
+    L = S - behind
+    x = torch.empty(1, S, 1, dtype=BF16, device="cuda").normal_(0.5, 1.5, generator=torch.Generator("cuda").manual_seed(1))
+    x[0, L:] = float("nan")
+    w, b = torch.tensor([1.25], device="cuda"), torch.tensor([0.75], device="cuda")
+    lengths = torch.tensor([L], dtype=torch.int32, device="cuda") if behind else None
+    y = torch.full_like(x, float("nan"))
+    _, stats = fw.group_norm(x, 1, w, b, act="none", lengths=lengths, out=y)
+    flat, out = x.view(-1), y.view(-1)
+    total = sum(float(flat[s].sum(dtype=torch.float64)) for s in _slices(L))
+    mean = total / L
+    var = sum(float((flat[s].double() - mean).square().sum()) for s in _slices(L)) / L
+    r = (var + 1e-5) ** -0.5
+    most = max(float((flat[s].float() - mean).abs().max()) for s in _slices(L))
+    tol_m, tol_r = 1850 * EPS24 * (abs(mean) + most), 2 * 1850 * EPS24
+    assert abs(float(stats[0, 0, 0]) - mean) <= tol_m
+    assert abs(float(stats[0, 0, 1]) - r) <= tol_r * r
+    for s in _slices(L):
+        hat = (flat[s].double() - mean) * r
+        want = hat * 1.25 + 0.75
+        tol = 1.25 * (r * tol_m + hat.abs() * tol_r) + 8 * EPS24 * (want.abs() + 2)
+        assert bool(((out[s].double() - want).abs() <= tol + 2.0 ** -8 * (want.abs() + tol)).all())
+    assert not out[L:].any()
+    del y, out
+    g = fw.group_norm_backward(x, stats, x, 1, w, b, act="none", lengths=lengths)
+    size = sum(float(flat[s].abs().sum(dtype=torch.float64)) for s in _slices(L))
+    assert abs(float(g["dbias"]) - total) <= 8600 * EPS24 * size
+    dx = g["dx"].view(-1)
+    assert not dx[L:].any() and all(bool(torch.isfinite(dx[s]).all()) for s in _slices(L))
+    # dx = r w (x - mean(x) - xhat mean(x xhat)) is zero here but for eps: |r w (x - mean)| eps r^2, and roundings
+    for s in _slices(L):
+        assert float(dx[s].float().abs().max()) <= 1.25 * r * most * (1e-5 * r * r + 4 * 8600 * EPS24)
+    del x, g, dx, flat
+    torch.cuda.empty_cache()
