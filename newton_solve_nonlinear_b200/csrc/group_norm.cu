@@ -767,46 +767,49 @@ __global__ void __launch_bounds__(kThr) gn_channel_sum_kernel(const GnArgs a, in
     }
 }
 
-// One CTA per (n, group): channel sums over the chunks -> chan[n][2][C], group sums of w dz and w dz xhat ->
-// gsum[n][g][2].  Threads span the group's channels and, where those are few, slices of the chunks.
+// A CTA takes one (n, group) after another, as N G may pass what a grid holds: channel sums over the chunks ->
+// chan[n][2][C], group sums of w dz and w dz xhat -> gsum[n][g][2].  Threads span the group's channels and, where those
+// are few, slices of the chunks.
 __global__ void __launch_bounds__(kThr) gn_channel_join_kernel(const GnArgs a, int chunks, const float *__restrict__ part,
                                                                float *chan, float *gsum) {
     __shared__ float red[2][kThr];
-    const int n = blockIdx.x / a.G, g = blockIdx.x % a.G, cg = a.C / a.G;
-    const int cols = min(cg, kThr), slices = kThr / cols;
+    const int cg = a.C / a.G, cols = min(cg, kThr), slices = kThr / cols;
     const int col = threadIdx.x % cols, sl = threadIdx.x / cols;
-    const float *p = part + static_cast<long long>(n) * chunks * 2 * a.C + g * cg;
-    float *ch = chan + static_cast<long long>(n) * 2 * a.C + g * cg;
-    float s1 = 0.f, s2 = 0.f;  // w dz, w dz xhat of this thread's channels
-    for (int c0 = 0; c0 < cg; c0 += cols) {
-        const int c = c0 + col;
-        float dw = 0.f, db = 0.f;
-        if (c < cg && sl < slices) {
+    for (long long i = blockIdx.x; i < static_cast<long long>(a.N) * a.G; i += gridDim.x) {
+        const int n = static_cast<int>(i / a.G), g = static_cast<int>(i % a.G);
+        const float *p = part + static_cast<long long>(n) * chunks * 2 * a.C + g * cg;
+        float *ch = chan + static_cast<long long>(n) * 2 * a.C + g * cg;
+        float s1 = 0.f, s2 = 0.f;  // w dz, w dz xhat of this thread's channels
+        for (int c0 = 0; c0 < cg; c0 += cols) {
+            const int c = c0 + col;
+            float dw = 0.f, db = 0.f;
+            if (c < cg && sl < slices) {
 #pragma unroll 4
-            for (int q = sl; q < chunks; q += slices) {
-                dw += p[static_cast<long long>(q) * 2 * a.C + c];
-                db += p[static_cast<long long>(q) * 2 * a.C + a.C + c];
+                for (int q = sl; q < chunks; q += slices) {
+                    dw += p[static_cast<long long>(q) * 2 * a.C + c];
+                    db += p[static_cast<long long>(q) * 2 * a.C + a.C + c];
+                }
+            }
+            __syncthreads();
+            red[0][threadIdx.x] = dw, red[1][threadIdx.x] = db;
+            __syncthreads();
+            if (c < cg && sl == 0) {
+                for (int q = 1; q < slices; ++q) dw += red[0][q * cols + col], db += red[1][q * cols + col];
+                ch[c] = dw, ch[a.C + c] = db;
+                const float w = a.weight != nullptr ? a.weight[g * cg + c] : 1.f;
+                s1 = fmaf(w, db, s1), s2 = fmaf(w, dw, s2);
             }
         }
         __syncthreads();
-        red[0][threadIdx.x] = dw, red[1][threadIdx.x] = db;
+        red[0][threadIdx.x] = s1, red[1][threadIdx.x] = s2;
         __syncthreads();
-        if (c < cg && sl == 0) {
-            for (int q = 1; q < slices; ++q) dw += red[0][q * cols + col], db += red[1][q * cols + col];
-            ch[c] = dw, ch[a.C + c] = db;
-            const float w = a.weight != nullptr ? a.weight[g * cg + c] : 1.f;
-            s1 = fmaf(w, db, s1), s2 = fmaf(w, dw, s2);
+        for (int m = kThr / 2; m > 0; m >>= 1) {
+            if (threadIdx.x < m)
+                red[0][threadIdx.x] += red[0][threadIdx.x + m], red[1][threadIdx.x] += red[1][threadIdx.x + m];
+            __syncthreads();
         }
+        if (threadIdx.x == 0) *reinterpret_cast<float2 *>(gsum + i * 2) = make_float2(red[0][0], red[1][0]);
     }
-    __syncthreads();
-    red[0][threadIdx.x] = s1, red[1][threadIdx.x] = s2;
-    __syncthreads();
-    for (int m = kThr / 2; m > 0; m >>= 1) {
-        if (threadIdx.x < m)
-            red[0][threadIdx.x] += red[0][threadIdx.x + m], red[1][threadIdx.x] += red[1][threadIdx.x + m];
-        __syncthreads();
-    }
-    if (threadIdx.x == 0) *reinterpret_cast<float2 *>(gsum + static_cast<long long>(blockIdx.x) * 2) = make_float2(red[0][0], red[1][0]);
 }
 
 template <typename TX, typename TY, int V, bool GATE>
@@ -864,6 +867,7 @@ __global__ void __launch_bounds__(kThr) gn_backward_apply_kernel(const GnArgs a,
 // ---- plans and dispatch --------------------------------------------------------------------------------------
 
 constexpr int kJoinMost = 1024;  // partial moments of one n that every CTA of the second pass joins by itself
+constexpr long long kJoinGrid = 1 << 20;  // CTAs of gn_channel_join_kernel, at most
 constexpr int kRowMost = 1024;  // channels of a group that a warp holds in registers (32 per lane)
 
 bool row_regime(const GnArgs &a) { return a.S == 1 && a.C / a.G <= kRowMost; }
@@ -962,7 +966,9 @@ cudaError_t seq_backward_g(const GnArgs &a, cudaStream_t s) {
     float *chan = reinterpret_cast<float *>(a.ws + al(static_cast<size_t>(a.N) * chunks * 2 * a.C * 4));
     float *gsum = reinterpret_cast<float *>(reinterpret_cast<char *>(chan) + al(static_cast<size_t>(a.N) * 2 * a.C * 4));
     gn_channel_sum_kernel<TX, TY, V, GATE><<<grid, threads_of<V>(a), 0, s>>>(a, rows, chunks, part);
-    gn_channel_join_kernel<<<static_cast<unsigned>(a.N) * a.G, kThr, 0, s>>>(a, chunks, part, chan, gsum);
+    const long long joins = static_cast<long long>(a.N) * a.G;
+    gn_channel_join_kernel<<<static_cast<unsigned>(joins < kJoinGrid ? joins : kJoinGrid), kThr, 0, s>>>(a, chunks, part, chan,
+                                                                                                        gsum);
     // few rows to sum: blocks of the same launch do it
     const bool with = a.N <= 256;
     gn_backward_apply_kernel<TX, TY, V, GATE>

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import newton_solve_nonlinear_b200 as fw
+from tests.test_gpu_group_norm import _check, _make
 
 pytestmark = pytest.mark.gpu
 
@@ -58,4 +59,40 @@ def test_norm_of_the_longest_sequence(behind):
     for s in _slices(L):
         assert float(dx[s].float().abs().max()) <= 1.25 * r * most * (1e-5 * r * r + 4 * 8600 * EPS24)
     del x, g, dx, flat
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("act,gated", [("silu", False), ("none", True)])
+def test_norm_of_more_statistics_than_the_join_has_blocks(act, gated):
+    """N groups just above 2^20, each of two rows of one channel."""
+    N, S, G = 1051, 2, 1000
+    x, w, b, n = _make(N, S, G, F32)
+    _check(x, G, w, b, gate=n(N, S, G) if gated else None, act=act, dy=n(N, S, G))
+
+
+def test_norm_backward_of_more_statistics_than_a_grid_holds():
+    """N groups = 2^31.  The last n's gradients equal those of a call on a copy of them, whose sums are the same ones;
+    dbias is the sum of dy, 2^21 terms in 32 slices of 2^15 and two rows each: within 2^17 2^-24 of the sum of absolute
+    values, and dweight, with terms dy xhat, |xhat| <= 1 within 2^-20, too."""
+    torch.cuda.empty_cache()
+    N, S, G = 2 ** 20, 2, 2048
+    x = torch.empty(N, S, G, dtype=BF16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(2))
+    w, b = torch.rand(G, device="cuda") + 0.5, torch.rand(G, device="cuda")
+    y, stats = fw.group_norm(x, G, w, b, act="none")
+    del y
+    g = fw.group_norm_backward(x, stats, x, G, w, b, act="none")
+    for at in (0, 2 ** 19 - 1, N - 3):
+        part = slice(at, at + 3)
+        e = fw.group_norm_backward(x[part].clone(), stats[part].clone(), x[part].clone(), G, w, b, act="none")
+        assert torch.equal(g["dx"][part], e["dx"])
+    total, size, hats = (torch.zeros(G, dtype=torch.float64, device="cuda") for _ in range(3))
+    for i in range(0, N, 2 ** 15):
+        d, st = x[i:i + 2 ** 15].double(), stats[i:i + 2 ** 15].double()
+        total += d.sum((0, 1))
+        size += d.abs().sum((0, 1))
+        hats += (d * (d - st[:, None, :, 0]) * st[:, None, :, 1]).sum((0, 1))
+    tol = 2.0 ** 17 * EPS24 * size
+    assert bool(((g["dbias"] - total).abs() <= tol).all())
+    assert bool(((g["dweight"] - hats).abs() <= tol).all())
+    del x, stats, g
     torch.cuda.empty_cache()
