@@ -826,6 +826,7 @@ PARARNN_API int pararnn_linear_attention_step(const pararnn_attention_shape *sha
  *   N, S, C   x is [N, S, C]: statistics are taken over the S rows and the
  *             C / groups channels of each group, for each n (S = 1 normalises
  *             the groups of every row by themselves, as for the heads of o).
+ *             N * S is below 2^31, C at most 2^30.
  *   groups    divides C; at most 2048.
  *   x_dtype   of x, gate and their gradients;  y_dtype  of y and its gradient.
  *   act       pararnn_activation;  eps  added to the variance, >= 0. */

@@ -323,6 +323,7 @@ static bool norm_ok(const pararnn_norm_shape *s) {
     if (s->groups > 2048 || !dtype_ok(s->x_dtype) || !dtype_ok(s->y_dtype)) return false;
     if (s->act < PARARNN_ACT_NONE || s->act > PARARNN_ACT_GELU) return false;
     if (!std::isfinite(s->eps) || s->eps < 0.f) return false;
+    if (s->C > 1 << 30) return false;  // channels are counted in 32 bits, twice over and in steps past the end
     // blocks of rows are counted in 32 bits: at most one per row
     return static_cast<long long>(s->N) * s->S <= (1ll << 31) - 1;
 }

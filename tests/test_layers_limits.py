@@ -25,3 +25,13 @@ def test_norm_of_the_most_rows_fills_the_card(L, N, C, groups):  # noqa: F811
     """One row per statistic: the backward pass keeps a row of partial sums for each CTA, as many as for fewer rows."""
     size = lambda n: L.pararnn_group_norm_backward_workspace_size(_norm(N=n, S=1, C=C, groups=groups))
     assert size(N) == size(2 ** 24) >= 148 * 2 * C * 4
+
+
+@pytest.mark.parametrize("S,groups", [(1, 1), (2, 1), (1, 64)])
+def test_norm_channels(L, S, groups):  # noqa: F811
+    """Channels are counted in 32 bits, in two sums a channel and in strides that may pass the end: up to 2^30."""
+    for size in (L.pararnn_group_norm_workspace_size, L.pararnn_group_norm_backward_workspace_size):
+        query = lambda C: size(_norm(N=1, S=S, C=C, groups=groups))
+        assert query(2 ** 30) >= 256
+        for C in (2 ** 30 + groups, INT_MAX // groups * groups):
+            assert query(C) == 0
