@@ -811,6 +811,12 @@ def _rows(t, name: str, like, shape):
     return Rows(t.data_ptr(), st[0], st[1] if len(st) == 4 else 0, st[-2])
 
 
+def _counts(what: str, *counts: int):
+    """Refuses counts that the C ABI's int would cut off."""
+    if max(counts) >= 2 ** 31:
+        raise ValueError(f"{what} must be below 2**31: got {counts}")
+
+
 def _attention_shape(q, k, v, log_decay, scale, dims: int = 4):
     if q.dim() != dims or k.dim() != dims or v.dim() != dims:
         raise ValueError("q, k and v must be " + ("[B, T, heads, width]" if dims == 4 else "[B, heads, width]"))
@@ -821,6 +827,7 @@ def _attention_shape(q, k, v, log_decay, scale, dims: int = 4):
         raise ValueError(f"B, T and the head counts must be positive, q's heads a multiple of k's: {H} and {Hkv}")
     if not (1 <= dk <= 128 and 1 <= dv <= 128):
         raise ValueError(f"head widths must be 1 to 128: got {dk} and {dv}")
+    _counts("sequences, tokens and heads", B, T, H)
     if log_decay.requires_grad:
         raise ValueError("log_decay is a constant of the model: it gets no gradient")
     shape = AttentionShape(B, T, H, Hkv, dk, dv, _dtype_code(q.dtype), dk ** -0.5 if scale is None else scale)
@@ -917,11 +924,12 @@ def linear_attention_step(q, k, v, log_decay, state, *, slots=None, scale=None, 
     if under is not None:
         with under:
             return linear_attention_step(q, k, v, log_decay, state, slots=slots, scale=scale, out_state=out_state, out=out)
-    shape, rq, rk, rv = _attention_shape(q, k, v, log_decay, scale, 3)
-    B, H, dk, dv = shape.B, shape.H, shape.dk, shape.dv
     if state.dim() != 4 or state.shape[0] < 1:
         raise ValueError("state must be [n, H, dk, dv]")
     n = state.shape[0]
+    _counts("states", n)
+    shape, rq, rk, rv = _attention_shape(q, k, v, log_decay, scale, 3)
+    B, H, dk, dv = shape.B, shape.H, shape.dk, shape.dv
     if slots is None and n != B:
         raise ValueError(f"state has {n} rows for {B} sequences: slots says which")
     if out is None:
@@ -947,6 +955,7 @@ def _norm_shape(x, groups, act, eps, y_dtype):
         S *= n
     if min(N, S, C) < 1 or not 1 <= groups <= 2048 or C % groups:
         raise ValueError(f"x must not be empty and groups (1 to 2048) must divide its channels: {tuple(x.shape)}, {groups}")
+    _counts("x's first, middle and last axes", N, S, C)
     return NormShape(N, S, C, groups, _dtype_code(x.dtype), _dtype_code(y_dtype), ACTIVATIONS[act], eps)
 
 

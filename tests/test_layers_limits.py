@@ -1,6 +1,7 @@
 """The largest sizes that linear attention and group norm take, and what is refused above them.  CPU only: the size
 queries and the argument checks run on the host before anything is enqueued."""
 import pytest
+import torch
 
 from newton_solve_nonlinear_b200 import binding
 from tests.test_layers_refusals import L, _norm  # noqa: F401 (L is a fixture)
@@ -35,3 +36,36 @@ def test_norm_channels(L, S, groups):  # noqa: F811
         assert query(2 ** 30) >= 256
         for C in (2 ** 30 + groups, INT_MAX // groups * groups):
             assert query(C) == 0
+
+
+FAR = 2 ** 32 + 3  # what a 32-bit count would take for 3
+
+
+def _far(*shape):
+    return torch.zeros(*(1 for _ in shape)).expand(*shape)  # no memory behind it
+
+
+@pytest.mark.parametrize("shape", [(FAR, 1, 1, 1), (1, FAR, 1, 1), (1, 1, FAR, 1)])
+def test_attention_sizes_beyond_32_bits_are_refused(shape):
+    q = _far(*shape)
+    ld = _far(shape[2])
+    with pytest.raises(ValueError, match="below 2\\*\\*31"):
+        binding.linear_attention(q, q, q, ld)
+    with pytest.raises(ValueError, match="below 2\\*\\*31"):
+        binding.linear_attention_backward(q, q, q, ld, q)
+
+
+@pytest.mark.parametrize("rows,slots", [(FAR, FAR), (3, FAR)])
+def test_step_sizes_beyond_32_bits_are_refused(rows, slots):
+    q, state = _far(rows, 1, 1), _far(slots, 1, 1, 1)
+    with pytest.raises(ValueError, match="below 2\\*\\*31"):
+        binding.linear_attention_step(q, q, q, _far(1), state, slots=torch.zeros(3, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("shape", [(FAR, 1), (1, FAR), (1, FAR, 1), (3, 2 ** 16, 2 ** 16, 1), (1, 3, FAR)])
+def test_norm_sizes_beyond_32_bits_are_refused(shape):
+    x = _far(*shape)
+    with pytest.raises(ValueError, match="below 2\\*\\*31"):
+        binding.group_norm(x, 1)
+    with pytest.raises(ValueError, match="below 2\\*\\*31"):
+        binding.group_norm_backward(x, _far(shape[0], 1, 2), x, 1)
