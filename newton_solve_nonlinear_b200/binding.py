@@ -772,6 +772,8 @@ def _context(t, stream):
     """What a call on ``t`` has to be made under: the caller's stream, so that the call's own allocations belong to it,
     or t's device where another one is current; None where neither applies."""
     if stream is not None:
+        if stream.device != t.device:
+            raise ValueError(f"stream must be one of {t.device}, got one of {stream.device}")
         return torch.cuda.stream(stream)
     if t.is_cuda and t.get_device() != torch.cuda.current_device():
         return torch.cuda.device(t.get_device())

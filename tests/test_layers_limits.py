@@ -69,3 +69,35 @@ def test_norm_sizes_beyond_32_bits_are_refused(shape):
         binding.group_norm(x, 1)
     with pytest.raises(ValueError, match="below 2\\*\\*31"):
         binding.group_norm_backward(x, _far(shape[0], 1, 2), x, 1)
+
+
+class _Elsewhere:
+    """What the binding looks at of a stream or a buffer, on a second device."""
+    device, cuda_stream, is_cuda = torch.device("cuda", 1), 0, True
+
+    def get_device(self):
+        return 1
+
+    def data_ptr(self):
+        return 1 << 40
+
+    def numel(self):
+        return 1 << 20
+
+    def is_contiguous(self):
+        return True
+
+
+def test_streams_of_another_device_are_refused(monkeypatch):
+    """Such a call ran on the current stream of its tensors' device instead, without the order that was asked for."""
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: pytest.fail("entered the stream"))
+    z = torch.zeros
+    q = z(1, 2, 4, 8)
+    other = dict(stream=_Elsewhere())
+    for call in (lambda: binding.linear_attention(q, q, q, z(4), **other),
+                 lambda: binding.linear_attention_backward(q, q, q, z(4), q, **other),
+                 lambda: binding.linear_attention_step(q[:, 0], q[:, 0], q[:, 0], z(4), z(1, 4, 8, 8), **other),
+                 lambda: binding.group_norm(z(3, 4), 1, **other),
+                 lambda: binding.group_norm_backward(z(3, 4), z(3, 1, 2), z(3, 4), 1, **other)):
+        with pytest.raises(ValueError, match="stream"):
+            call()
