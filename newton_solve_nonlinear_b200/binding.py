@@ -849,6 +849,8 @@ def _workspace(need: int, name: str, workspace, device):
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
         if workspace.data_ptr() % 256:
             workspace = alloc_workspace(need, device)
+    elif workspace.device != device:
+        raise ValueError(f"workspace must be on {device}, got {workspace.device}")
     return workspace, _dev(workspace, "workspace"), workspace.numel()
 
 

@@ -101,3 +101,9 @@ def test_streams_of_another_device_are_refused(monkeypatch):
                  lambda: binding.group_norm_backward(z(3, 4), z(3, 1, 2), z(3, 4), 1, **other)):
         with pytest.raises(ValueError, match="stream"):
             call()
+
+
+def test_workspaces_of_another_device_are_refused():
+    with pytest.raises(ValueError, match="workspace"):
+        binding._workspace(1024, "pararnn_group_norm", _Elsewhere(), torch.device("cuda", 0))
+    assert binding._workspace(1024, "pararnn_group_norm", _Elsewhere(), torch.device("cuda", 1))[1:] == (1 << 40, 1 << 20)
