@@ -813,6 +813,15 @@ def _rows(t, name: str, like, shape):
     return Rows(t.data_ptr(), st[0], st[1] if len(st) == 4 else 0, st[-2])
 
 
+def _no_graph(name: str, *operands):
+    """These calls record no graph, so a gradient through them would be lost without a word: it is refused."""
+    if torch.is_grad_enabled():
+        for t in operands:
+            if t is not None and t.requires_grad:
+                raise ValueError(f"{name} records no graph for an operand that requires a gradient: call it under "
+                                 "torch.no_grad(); gradients come from the backward calls")
+
+
 def _counts(what: str, *counts: int):
     """Refuses counts that the C ABI's int would cut off."""
     if max(counts) >= 2 ** 31:
@@ -868,11 +877,14 @@ def linear_attention(q, k, v, log_decay, *, s0=None, lengths=None, scale=None, o
     fp32 <= 0, s0 [B,H,dk,dv] fp32 the state before (zero if None), lengths [B]
     int32 (tokens behind them are not read, outputs there are zero), scale
     dk**-0.5 if None.  Returns (o [B,T,H,dv] of q's type, the last state
-    [B,H,dk,dv] fp32); ``out`` gives both tensors (the state's may be s0)."""
+    [B,H,dk,dv] fp32); ``out`` gives both tensors (the state's may be s0).
+    Records no graph: operands that require a gradient are taken under
+    ``torch.no_grad()`` only, and ``linear_attention_backward`` has the gradients."""
     under = _context(q, stream)
     if under is not None:
         with under:
             return linear_attention(q, k, v, log_decay, s0=s0, lengths=lengths, scale=scale, out=out, workspace=workspace)
+    _no_graph("linear_attention", q, k, v, s0)
     shape, rq, rk, rv = _attention_shape(q, k, v, log_decay, scale)
     B, T, H, dk, dv = shape.B, shape.T, shape.H, shape.dk, shape.dv
     o, s = out if out is not None else (q.new_empty((B, T, H, dv)), log_decay.new_empty((B, H, dk, dv)))
@@ -923,11 +935,13 @@ def linear_attention_step(q, k, v, log_decay, state, *, slots=None, scale=None, 
     the time axis; state [n,H,dk,dv] fp32 holds the states, row b's at slots[b]
     (int32 [B]; outside 0..n-1: no state, o is zero; the same slot twice: tokens
     in row order), or at b if None (n = B).  The states after the token go to
-    ``out_state``, or replace those in ``state`` if None.  Returns o [B,H,dv]."""
+    ``out_state``, or replace those in ``state`` if None.  Returns o [B,H,dv].
+    Records no graph, as ``linear_attention``."""
     under = _context(q, stream)
     if under is not None:
         with under:
             return linear_attention_step(q, k, v, log_decay, state, slots=slots, scale=scale, out_state=out_state, out=out)
+    _no_graph("linear_attention_step", q, k, v, state)
     if state.dim() != 4 or state.shape[0] < 1:
         raise ValueError("state must be [n, H, dk, dv]")
     n = state.shape[0]
@@ -973,12 +987,15 @@ def group_norm(x, groups: int, weight=None, bias=None, *, gate=None, act: str = 
     x fp32 or bf16, contiguous CUDA; weight, bias [C] fp32; act "none", "silu" or
     "gelu"; lengths [N] int32: rows behind them (in the middle axes' order) are
     not read, do not count, and are zero in y.  Returns (y of ``out_dtype``, x's
-    if None; stats [N, groups, 2] fp32: mean and 1 / sqrt(var + eps))."""
+    if None; stats [N, groups, 2] fp32: mean and 1 / sqrt(var + eps)).  Records
+    no graph: operands that require a gradient are taken under ``torch.no_grad()``
+    only, and ``group_norm_backward`` has the gradients."""
     under = _context(x, stream)
     if under is not None:
         with under:
             return group_norm(x, groups, weight, bias, gate=gate, act=act, eps=eps, lengths=lengths, out_dtype=out_dtype,
                               out=out, workspace=workspace)
+    _no_graph("group_norm", x, weight, bias, gate)
     y_dtype = out.dtype if out is not None else x.dtype if out_dtype is None else out_dtype
     shape = _norm_shape(x, groups, act, eps, y_dtype)
     channels = (shape.C,)

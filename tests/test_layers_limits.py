@@ -107,3 +107,32 @@ def test_workspaces_of_another_device_are_refused():
     with pytest.raises(ValueError, match="workspace"):
         binding._workspace(1024, "pararnn_group_norm", _Elsewhere(), torch.device("cuda", 0))
     assert binding._workspace(1024, "pararnn_group_norm", _Elsewhere(), torch.device("cuda", 1))[1:] == (1 << 40, 1 << 20)
+
+
+@pytest.mark.parametrize("which", range(4))
+def test_attention_refuses_to_drop_a_gradient(which):
+    """The calls record no graph; the gradients come from the backward call.  Under no_grad the operands may be leaves."""
+    z = torch.zeros
+    q, k, v, s0 = a = (z(1, 2, 4, 8), z(1, 2, 4, 8), z(1, 2, 4, 8), z(1, 4, 8, 8))
+    a[which].requires_grad_()
+    calls = [lambda: binding.linear_attention(q, k, v, z(4), s0=s0),
+             lambda: binding.linear_attention_step(q[:, 0], k[:, 0], v[:, 0], z(4), s0)]
+    for call in calls:
+        with pytest.raises(ValueError, match="no graph"):
+            call()
+        with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+            call()
+    with pytest.raises(ValueError, match="CUDA"):  # the backward call takes the same leaves
+        binding.linear_attention_backward(q, k, v, z(4), q, s0=s0)
+
+
+@pytest.mark.parametrize("which", range(4))
+def test_norm_refuses_to_drop_a_gradient(which):
+    x, w, b, gate = a = (torch.zeros(3, 4), torch.zeros(4), torch.zeros(4), torch.zeros(3, 4))
+    a[which].requires_grad_()
+    with pytest.raises(ValueError, match="no graph"):
+        binding.group_norm(x, 1, w, b, gate=gate)
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+        binding.group_norm(x, 1, w, b, gate=gate)
+    with pytest.raises(ValueError, match="CUDA"):
+        binding.group_norm_backward(x, torch.zeros(3, 1, 2), torch.zeros(3, 4), 1, w, b, gate=gate)
