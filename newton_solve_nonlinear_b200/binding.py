@@ -828,7 +828,7 @@ def _counts(what: str, *counts: int):
         raise ValueError(f"{what} must be below 2**31: got {counts}")
 
 
-def _attention_shape(q, k, v, log_decay, scale, dims: int = 4):
+def _attention_shape(q, k, v, log_decay, scale, dims: int = 4, back: bool = False):
     if q.dim() != dims or k.dim() != dims or v.dim() != dims:
         raise ValueError("q, k and v must be " + ("[B, T, heads, width]" if dims == 4 else "[B, heads, width]"))
     lead = q.shape[:-2]
@@ -839,7 +839,7 @@ def _attention_shape(q, k, v, log_decay, scale, dims: int = 4):
     if not (1 <= dk <= 128 and 1 <= dv <= 128):
         raise ValueError(f"head widths must be 1 to 128: got {dk} and {dv}")
     _counts("sequences, tokens and heads", B, T, H)
-    if log_decay.requires_grad:
+    if log_decay.requires_grad and (back or torch.is_grad_enabled()):
         raise ValueError("log_decay is a constant of the model: it gets no gradient")
     shape = AttentionShape(B, T, H, Hkv, dk, dv, _dtype_code(q.dtype), dk ** -0.5 if scale is None else scale)
     if not q.is_cuda:
@@ -910,7 +910,7 @@ def linear_attention_backward(q, k, v, log_decay, do, *, s0=None, ds=None, lengt
         with under:
             return linear_attention_backward(q, k, v, log_decay, do, s0=s0, ds=ds, lengths=lengths, scale=scale,
                                              workspace=workspace)
-    shape, rq, rk, rv = _attention_shape(q, k, v, log_decay, scale)
+    shape, rq, rk, rv = _attention_shape(q, k, v, log_decay, scale, back=True)
     B, T, H, Hkv, dk, dv = shape.B, shape.T, shape.H, shape.Hkv, shape.dk, shape.dv
     rdo = _rows(do, "do", q, (B, T, H, dv))
     g = dict(dq=q.new_empty((B, T, H, dk)), dk=q.new_empty((B, T, Hkv, dk)), dv=q.new_empty((B, T, Hkv, dv)),

@@ -136,3 +136,18 @@ def test_norm_refuses_to_drop_a_gradient(which):
         binding.group_norm(x, 1, w, b, gate=gate)
     with pytest.raises(ValueError, match="CUDA"):
         binding.group_norm_backward(x, torch.zeros(3, 1, 2), torch.zeros(3, 4), 1, w, b, gate=gate)
+
+
+def test_decays_that_are_leaves_serve_under_no_grad():
+    """No gradient is lost there; the backward call, which has none for the decays, refuses them always."""
+    z = torch.zeros
+    q, ld = z(1, 2, 4, 8), z(4).requires_grad_()
+    with torch.no_grad():
+        for call in (lambda: binding.linear_attention(q, q, q, ld),
+                     lambda: binding.linear_attention_step(q[:, 0], q[:, 0], q[:, 0], ld, z(1, 4, 8, 8))):
+            with pytest.raises(ValueError, match="CUDA"):
+                call()
+        with pytest.raises(ValueError, match="gradient"):
+            binding.linear_attention_backward(q, q, q, ld, q)
+    with pytest.raises(ValueError, match="gradient"):
+        binding.linear_attention_step(q[:, 0], q[:, 0], q[:, 0], ld, z(1, 4, 8, 8))
