@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import newton_solve_nonlinear_b200 as fw
+from tests import test_gpu_layers_guard_bands as bands
 from tests.test_gpu_group_norm import _check, _make
 
 pytestmark = pytest.mark.gpu
@@ -96,3 +97,28 @@ def test_norm_backward_of_more_statistics_than_a_grid_holds():
     assert bool(((g["dweight"] - hats).abs() <= tol).all())
     del x, stats, g
     torch.cuda.empty_cache()
+
+
+# One row per statistic, by the vectors that a lane holds of a group: widths that are multiples of 4 but not of 8 from
+# 132 to 1020 (8 vectors of 4), that are not multiples of 4 from 129 to 1023 (32 of 1), and multiples of 8 from 264 to
+# 512 (2 of 8); few rows, and more than all CTAs take at once
+WIDTHS = [(7, 3, 132), (5, 2, 1020), (4, 9, 516), (9, 3, 129), (3, 2, 1023), (6, 5, 386), (6, 2, 264), (4, 3, 512)]
+MANY = [(5001, 3, 132), (2503, 2, 513), (3001, 2, 264)]
+TYPES = [(F32, F32), (F32, BF16), (BF16, BF16), (BF16, F32)]
+
+
+@pytest.mark.parametrize("dtype,out", TYPES)
+@pytest.mark.parametrize("N,G,cg", WIDTHS + MANY)
+def test_norm_of_rows_with_several_vectors_a_lane(N, G, cg, dtype, out):
+    x, w, b, n = _make(N, 1, G * cg, dtype)
+    dy = n(N, 1, G * cg, dt=out)
+    lengths = [i % 3 for i in range(N)]  # a third of the rows are empty
+    _check(x, G, w, b, act="silu", out_dtype=out, dy=dy)
+    _check(x, G, w, b, gate=n(N, 1, G * cg, dt=dtype), act="gelu", out_dtype=out, dy=dy, lengths=lengths)
+
+
+@pytest.mark.parametrize("dtype,out", TYPES)
+@pytest.mark.parametrize("gated,ragged", [(False, False), (True, True)])
+@pytest.mark.parametrize("N,G,cg", WIDTHS)
+def test_norm_of_rows_between_guard_bands(N, G, cg, gated, ragged, dtype, out):
+    bands.test_group_norm(N, 1, G, cg, gated, ragged, dtype, out)
