@@ -122,3 +122,13 @@ def test_norm_of_rows_with_several_vectors_a_lane(N, G, cg, dtype, out):
 @pytest.mark.parametrize("N,G,cg", WIDTHS)
 def test_norm_of_rows_between_guard_bands(N, G, cg, gated, ragged, dtype, out):
     bands.test_group_norm(N, 1, G, cg, gated, ragged, dtype, out)
+
+
+@pytest.mark.parametrize("dtype,out", TYPES)
+@pytest.mark.parametrize("N,S,G,cg", [(256, 3, 2, 5), (257, 3, 2, 5), (700, 2, 4, 12), (1500, 7, 3, 16), (300, 1, 1, 1100)])
+def test_norm_parameters_of_many_sequences(N, S, G, cg, dtype, out):
+    """Up to 256 sequences the last launch sums the parameters' gradients, beyond them a launch of its own."""
+    x, w, b, n = _make(N, S, G * cg, dtype)
+    dy = n(N, S, G * cg, dt=out)
+    _check(x, G, w, b, act="gelu", out_dtype=out, dy=dy)
+    _check(x, G, w, b, gate=n(N, S, G * cg, dt=dtype), out_dtype=out, dy=dy, lengths=[i % (S + 1) for i in range(N)])
