@@ -1,0 +1,89 @@
+"""How exact linear attention's state and group norm's activations are, by inputs that leave nothing else to round."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import newton_solve_nonlinear_b200 as fw
+from oracle import group_norm as gn
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+EPS24, EPS23 = 2.0 ** -24, 2.0 ** -23
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("T,t,tol", [(6, 0, 2.0 ** -20), (128, 100, 2.0 ** -20), (1024, 890, 2.0 ** -19)])
+def test_state_products_are_exact_to_fp32(T, t, tol, dk, dv):
+    """bf16 operands, all tokens zero but one: the state is w k v^T with one weight w.
+
+    w is within 2 ulp, 2^-22; y = w v is rounded once, 2^-24, and its three bf16 terms are exact (24 bits); their products
+    with k are exact in fp32 and added in two steps, each within an ulp, 2^-23: 2.25 2^-22 < 2^-20 in all.  With 1024
+    tokens of one head time is split into segments of 128: the state of the second but last one is multiplied by one
+    more weight, 1.25 2^-22 more.  Two terms would leave up to 2^-16 of y."""
+    g = torch.Generator("cuda").manual_seed(dk + dv + T)
+    q, k, v = (torch.zeros(1, T, 1, d, dtype=BF16, device="cuda") for d in (dk, dk, dv))
+    k[0, t, 0].normal_(generator=g)
+    v[0, t, 0].normal_(generator=g)
+    ld = torch.tensor([-0.017], device="cuda")
+    _, s = fw.linear_attention(q, k, v, ld)
+    w = torch.exp(ld.double() * (T - 1 - t))
+    want = k[0, t, 0].double()[:, None] * (w * v[0, t, 0].double())[None]
+    assert bool(((s[0, 0].double() - want).abs() <= tol * want.abs()).all())
+    # what these inputs would show of a kernel with two terms
+    y = (w.float() * v[0, t, 0].float())
+    u0 = y.to(BF16).float()
+    two = u0 + (y - u0).to(BF16).float()
+    assert float(((y - two).abs() / y.abs()).max()) > 2.0 ** -18 > tol
+
+
+def _points(low, high):
+    z = np.concatenate([np.linspace(low, high, 1500), np.linspace(-3.0, 3.0, 547), [0.0]]).astype(np.float32)
+    return torch.from_numpy(z[: 2048]).cuda()
+
+
+def _act_error(z, act):
+    """(value, its error, slope, its error) of the activation in fp32.
+
+    __expf(x) is within 2 + floor(|1.173 x|) ulp, the approximate reciprocal within one, each of 2^-23; normcdff within 5.
+    The sigmoid s = 1 / (1 + E) takes E's error by 1 - s, and the value and the slope, s + z s (1 - s), where 1 - s is
+    within the absolute error of s, a rounding for each operation."""
+    if act == "silu":
+        s = 1 / (1 + np.exp(-z))
+        es = s * ((1 - s) * (2 + 1.173 * np.abs(z)) + 1 + 0.5) * EPS23
+        a = z * s
+        ea = np.abs(z) * es + EPS24 * np.abs(a)
+        slope = s + a * (1 - s)
+        return a, ea, slope, es + ea * (1 - s) + np.abs(a) * (es + EPS24 * (1 - s)) + EPS24 * (np.abs(slope) + np.abs(a * (1 - s)))
+    p = gn._phi(z)
+    h = z * z / 2
+    d = np.abs(z) * np.exp(-h) / math.sqrt(2 * math.pi)
+    slope = gn.slope(z, "gelu")
+    # the exponent is rounded twice, z times the constant twice (the constant itself once)
+    return z * p, 5.5 * EPS23 * np.abs(z * p), slope, d * ((2 + 1.173 * h) * EPS23 + 2 * h * EPS24 + 2 * EPS24) + 5 * EPS23 * p + EPS24 * np.abs(slope)
+
+
+@pytest.mark.parametrize("act,low,high", [("silu", -80.0, 80.0), ("gelu", -12.0, 12.0)])
+@pytest.mark.parametrize("shape", [(1, 1, 2048), (1, 3, 2048)])
+def test_activations_far_from_zero(shape, act, low, high):
+    """With a weight of zero z is the bias itself, and y, dgate and dbias are the activation and its slope."""
+    N, S, C = shape
+    z = _points(low, high)
+    zero, one = torch.zeros(C, device="cuda"), torch.ones(C, device="cuda")
+    x = torch.randn(N, S, C, device="cuda")
+    zn = z.double().cpu().numpy()
+    a, ea, s, es = _act_error(zn, act)
+    floor = 1e-37  # results below are subnormal
+    near = lambda got, want, tol: np.all(np.abs(got.double().cpu().numpy() - want) <= tol + floor)
+    y, stats = fw.group_norm(x, 4, zero, z, act=act)
+    assert all(near(y[0, i], a, ea) for i in range(S))
+    dy = torch.zeros_like(x)
+    dy[0, 0] = 1
+    assert near(fw.group_norm_backward(x, stats, dy, 4, zero, z, act=act)["dbias"], s, es)
+    gate = z.expand(N, S, C).contiguous()
+    y, stats = fw.group_norm(x, 4, zero, one, act=act, gate=gate)
+    assert all(near(y[0, i], a, ea) for i in range(S))
+    dgate = fw.group_norm_backward(x, stats, torch.ones_like(x), 4, zero, one, act=act, gate=gate)["dgate"]
+    assert all(near(dgate[0, i], s, es) for i in range(S))
