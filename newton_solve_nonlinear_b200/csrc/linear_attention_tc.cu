@@ -1,7 +1,7 @@
 // linear_attention_tc.cu -- the sweep of linear_attention.cuh for bf16 operands on the 5th-generation tensor
 // cores (tcgen05, sm_100a).
 //
-// One CTA carries one head's state (dv columns of it) through one segment of time, 128 rows at a time:
+// One CTA carries one head's state through one segment of time, 128 rows at a time:
 //   scores = a b^T                      [128 x 128]  operands in shared memory
 //   out    = g^(i+e) (a S)              [128 x DV]   S as a bf16 copy in shared memory
 //   out   += (scores * g^(i-j)) c       [128 x DV]   weighted scores rounded to bf16 in TMEM as the A operand
@@ -270,9 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
     volatile int *err = &bars->err;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    const int n_tile = (w.dv + DV - 1) / DV;
-    const int bh = blockIdx.x / n_tile, c0 = (blockIdx.x % n_tile) * DV;
-    const int b = bh / w.H, h = bh % w.H, sg = blockIdx.y;
+    const int bh = blockIdx.x, b = bh / w.H, h = bh % w.H, sg = blockIdx.y;
     int L = w.T;
     if (w.lengths != nullptr) L = min(max(w.lengths[b], 0), w.T);
     // tokens [lo, hi) of this segment; the tile with hi has n_part rows
@@ -281,7 +279,6 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
     const int hi = t_lo + w.seg < L ? static_cast<int>(t_lo + w.seg) : L;
     const int chunks = (hi - lo + kC - 1) / kC;
     const int n_part = hi - lo - (chunks - 1) * kC;
-    const int ncol = min(DV, w.dv - c0);
     const bool rev = w.reverse != 0;
     const int e = w.e;
     const int part_chunk = rev ? 0 : chunks - 1;
@@ -341,9 +338,8 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             // fp32 outputs (partial gradients): dense rows of w.out_w columns
             const long long ost = static_cast<long long>(w.H) * w.out_w;
             float *const pf = w.out_f32 ? static_cast<float *>(w.out) +
-                                              (static_cast<long long>(b) * w.T * w.H + h) * w.out_w + c0 + row * ost
+                                              (static_cast<long long>(b) * w.T * w.H + h) * w.out_w + row * ost
                                         : nullptr;
-            const int room = w.out_w - c0;
             for (int c = 0; c < chunks; ++c) {
                 const unsigned ph = c & 1;
                 const bool full = c != part_chunk;
@@ -399,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                         if (lane == 0) arrive(smem_u32(&bars->out_read));
                     }
                     if (pf != nullptr) {
-                        if (live) store32(pf + first_token(c) * ost + cb, v, room - cb);
+                        if (live) store32(pf + first_token(c) * ost + cb, v, w.out_w - cb);
                     } else {
                         if (!live) {
 #pragma unroll
@@ -436,11 +432,11 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             const unsigned t_ds = tl + (STATE_ONLY ? Y::T_D1 : Y::T_D) + half * KH;
             float S[KH];
             {
-                const bool have = mine && d < ncol && (w.n_seg > 1 ? !STATE_ONLY : w.s_in != nullptr);
+                const bool have = mine && d < w.dv && (w.n_seg > 1 ? !STATE_ONLY : w.s_in != nullptr);
                 const float *p = w.n_seg > 1
-                                     ? w.seg_state + (static_cast<long long>(bh) * w.n_seg + sg) * w.dk * w.dv + c0 + d
+                                     ? w.seg_state + (static_cast<long long>(bh) * w.n_seg + sg) * w.dk * w.dv + d
                                      : w.s_in + static_cast<long long>(bh) * w.dk * w.dv +
-                                           static_cast<long long>(c0 + d) * w.s_j;
+                                           static_cast<long long>(d) * w.s_j;
                 const int si = w.n_seg > 1 ? w.dv : w.s_i;
 #pragma unroll
                 for (int k = 0; k < KH; ++k) {
@@ -566,12 +562,12 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             float *p = nullptr;
             int si = w.dv;
             if (STATE_ONLY) {
-                p = w.seg_state + (static_cast<long long>(bh) * w.n_seg + sg) * w.dk * w.dv + c0 + d;
+                p = w.seg_state + (static_cast<long long>(bh) * w.n_seg + sg) * w.dk * w.dv + d;
             } else if (w.s_out != nullptr && sg == last_seg) {
-                p = w.s_out + static_cast<long long>(bh) * w.dk * w.dv + static_cast<long long>(c0 + d) * w.s_j;
+                p = w.s_out + static_cast<long long>(bh) * w.dk * w.dv + static_cast<long long>(d) * w.s_j;
                 si = w.s_i;
             }
-            if (p != nullptr && mine && d < ncol) {
+            if (p != nullptr && mine && d < w.dv) {
                 const bool bad = *err != 0;
 #pragma unroll
                 for (int k = 0; k < KH; ++k)
@@ -685,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                     mbar_expect_tx(full, (DK / 64 + DV / 64) * kPanel);
 #pragma unroll
                     for (int x = 0; x < DV / 64; ++x)
-                        tma_load_4d(base + Y::C + x * kPanel, &sweep.c, c0 + x * 64, t0, hc, b, full);
+                        tma_load_4d(base + Y::C + x * kPanel, &sweep.c, x * 64, t0, hc, b, full);
 #pragma unroll
                     for (int x = 0; x < DK / 64; ++x)
                         tma_load_4d(base + Y::B + x * kPanel, &sweep.b, x * 64, t0, hb, b, full);
@@ -706,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             if (elect_one()) {
                 const int t0 = first_token(c);
 #pragma unroll
-                for (int x = 0; x < DV / 64; ++x) tma_prefetch_4d(&sweep.c, c0 + x * 64, t0, hc, b);
+                for (int x = 0; x < DV / 64; ++x) tma_prefetch_4d(&sweep.c, x * 64, t0, hc, b);
 #pragma unroll
                 for (int x = 0; x < DK / 64; ++x) {
                     tma_prefetch_4d(&sweep.b, x * 64, t0, hb, b);
@@ -732,8 +728,8 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                     if (elect_one()) {
 #pragma unroll
                         for (int x = 0; x < DV / 64; ++x)
-                            if (x * 64 < ncol)
-                                tma_store_4d(&sweep.out, c0 + x * 64, first_token(c), h, b,
+                            if (x * 64 < w.dv)
+                                tma_store_4d(&sweep.out, x * 64, first_token(c), h, b,
                                              sm + (c & 1) * Y::STAGE + Y::OUT + x * kPanel);
                         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                         // the store has read its tile before the stage is filled again
@@ -758,18 +754,18 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512));
     }
     if (!STATE_ONLY) {
-        const long long po = (static_cast<long long>(b) * w.T * w.H + h) * w.out_w + c0;
+        const long long po = (static_cast<long long>(b) * w.T * w.H + h) * w.out_w;
         const long long ost = static_cast<long long>(w.H) * w.out_w;
         auto put = [&](long long at, float x) {
             if (w.out_f32) static_cast<float *>(w.out)[at] = x;
             else static_cast<__nv_bfloat16 *>(w.out)[at] = __float2bfloat16(x);
         };
         if (*err)  // a wait ran out: nothing of this segment is to be trusted
-            for (long long i = tid; i < static_cast<long long>(hi - lo) * ncol; i += kThreads)
-                put(po + (lo + i / ncol) * ost + i % ncol, __int_as_float(0x7fc00000));
+            for (long long i = tid; i < static_cast<long long>(hi - lo) * w.dv; i += kThreads)
+                put(po + (lo + i / w.dv) * ost + i % w.dv, __int_as_float(0x7fc00000));
         // outputs behind the sequence's length are zero
         const long long z_lo = t_lo > L ? t_lo : L, z_hi = t_lo + w.seg < w.T ? t_lo + w.seg : w.T;
-        for (long long i = tid; i < (z_hi - z_lo) * ncol; i += kThreads) put(po + (z_lo + i / ncol) * ost + i % ncol, 0.f);
+        for (long long i = tid; i < (z_hi - z_lo) * w.dv; i += kThreads) put(po + (z_lo + i / w.dv) * ost + i % w.dv, 0.f);
     }
 }
 
@@ -809,7 +805,7 @@ cudaError_t launch(const TcBatch &t, int n, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const LaSweep &w = t.s[0].w;
     // pass 1: the state of the segment that comes last is not needed (its blocks return at once)
-    const dim3 grid(static_cast<unsigned>(w.B) * w.H * ((w.dv + DV - 1) / DV), w.n_seg, n);
+    const dim3 grid(static_cast<unsigned>(w.B) * w.H, w.n_seg, n);
     k<<<grid, kThreads, smem, s>>>(t);
     return cudaGetLastError();
 }
