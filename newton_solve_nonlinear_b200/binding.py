@@ -813,19 +813,13 @@ def _rows(t, name: str, like, shape):
     return Rows(t.data_ptr(), st[0], st[1] if len(st) == 4 else 0, st[-2])
 
 
-def _no_graph(name: str, *operands):
+_INT = 2 ** 31  # the C ABI counts in int
+
+
+def _no_graph(name: str):
     """These calls record no graph, so a gradient through them would be lost without a word: it is refused."""
-    if torch.is_grad_enabled():
-        for t in operands:
-            if t is not None and t.requires_grad:
-                raise ValueError(f"{name} records no graph for an operand that requires a gradient: call it under "
-                                 "torch.no_grad(); gradients come from the backward calls")
-
-
-def _counts(what: str, *counts: int):
-    """Refuses counts that the C ABI's int would cut off."""
-    if max(counts) >= 2 ** 31:
-        raise ValueError(f"{what} must be below 2**31: got {counts}")
+    raise ValueError(f"{name} records no graph for an operand that requires a gradient: call it under torch.no_grad(); "
+                     "gradients come from the backward calls")
 
 
 def _attention_shape(q, k, v, log_decay, scale, dims: int = 4, back: bool = False):
@@ -834,11 +828,12 @@ def _attention_shape(q, k, v, log_decay, scale, dims: int = 4, back: bool = Fals
     lead = q.shape[:-2]
     B, T = lead[0], lead[1] if dims == 4 else 1
     (H, dk), Hkv, dv = q.shape[-2:], k.shape[-2], v.shape[-1]
-    if min(B, T, H, Hkv) < 1 or H % Hkv:
+    if not (0 < B < _INT and 0 < T < _INT and 0 < H < _INT and 0 < Hkv) or H % Hkv:
+        if max(B, T, H) >= _INT:
+            raise ValueError(f"B, T and the head counts must be below 2**31: got {B}, {T} and {H}")
         raise ValueError(f"B, T and the head counts must be positive, q's heads a multiple of k's: {H} and {Hkv}")
     if not (1 <= dk <= 128 and 1 <= dv <= 128):
         raise ValueError(f"head widths must be 1 to 128: got {dk} and {dv}")
-    _counts("sequences, tokens and heads", B, T, H)
     if log_decay.requires_grad and (back or torch.is_grad_enabled()):
         raise ValueError("log_decay is a constant of the model: it gets no gradient")
     shape = AttentionShape(B, T, H, Hkv, dk, dv, _dtype_code(q.dtype), dk ** -0.5 if scale is None else scale)
@@ -884,7 +879,9 @@ def linear_attention(q, k, v, log_decay, *, s0=None, lengths=None, scale=None, o
     if under is not None:
         with under:
             return linear_attention(q, k, v, log_decay, s0=s0, lengths=lengths, scale=scale, out=out, workspace=workspace)
-    _no_graph("linear_attention", q, k, v, s0)
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad
+                                    or (s0 is not None and s0.requires_grad)):
+        _no_graph("linear_attention")
     shape, rq, rk, rv = _attention_shape(q, k, v, log_decay, scale)
     B, T, H, dk, dv = shape.B, shape.T, shape.H, shape.dk, shape.dv
     o, s = out if out is not None else (q.new_empty((B, T, H, dv)), log_decay.new_empty((B, H, dk, dv)))
@@ -941,11 +938,13 @@ def linear_attention_step(q, k, v, log_decay, state, *, slots=None, scale=None, 
     if under is not None:
         with under:
             return linear_attention_step(q, k, v, log_decay, state, slots=slots, scale=scale, out_state=out_state, out=out)
-    _no_graph("linear_attention_step", q, k, v, state)
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad or state.requires_grad):
+        _no_graph("linear_attention_step")
     if state.dim() != 4 or state.shape[0] < 1:
         raise ValueError("state must be [n, H, dk, dv]")
     n = state.shape[0]
-    _counts("states", n)
+    if n >= _INT:
+        raise ValueError(f"states must be below 2**31: got {n}")
     shape, rq, rk, rv = _attention_shape(q, k, v, log_decay, scale, 3)
     B, H, dk, dv = shape.B, shape.H, shape.dk, shape.dv
     if slots is None and n != B:
@@ -973,7 +972,8 @@ def _norm_shape(x, groups, act, eps, y_dtype):
         S *= n
     if min(N, S, C) < 1 or not 1 <= groups <= 2048 or C % groups:
         raise ValueError(f"x must not be empty and groups (1 to 2048) must divide its channels: {tuple(x.shape)}, {groups}")
-    _counts("x's first, middle and last axes", N, S, C)
+    if max(N, S, C) >= _INT:
+        raise ValueError(f"x's first, middle and last axes must be below 2**31: got {N}, {S} and {C}")
     return NormShape(N, S, C, groups, _dtype_code(x.dtype), _dtype_code(y_dtype), ACTIVATIONS[act], eps)
 
 
@@ -995,7 +995,10 @@ def group_norm(x, groups: int, weight=None, bias=None, *, gate=None, act: str = 
         with under:
             return group_norm(x, groups, weight, bias, gate=gate, act=act, eps=eps, lengths=lengths, out_dtype=out_dtype,
                               out=out, workspace=workspace)
-    _no_graph("group_norm", x, weight, bias, gate)
+    if torch.is_grad_enabled() and (x.requires_grad or (weight is not None and weight.requires_grad)
+                                    or (bias is not None and bias.requires_grad)
+                                    or (gate is not None and gate.requires_grad)):
+        _no_graph("group_norm")
     y_dtype = out.dtype if out is not None else x.dtype if out_dtype is None else out_dtype
     shape = _norm_shape(x, groups, act, eps, y_dtype)
     channels = (shape.C,)
