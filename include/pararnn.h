@@ -719,7 +719,7 @@ typedef struct {
 } pararnn_rows;
 
 /* Linear attention with a decay for each head.
- *   B, T     sequences and tokens, >= 1; T at most 2^30.
+ *   B, T     sequences and tokens, >= 1; T at most 2^30, B * H at most 2^24.
  *   H, Hkv   heads of q and of k, v; H a multiple of Hkv (head h reads key and
  *            value head h / (H / Hkv)).
  *   dk, dv   widths of q, k and of v: 1 .. 128.
@@ -762,7 +762,10 @@ PARARNN_API size_t pararnn_linear_attention_workspace_size(const pararnn_attenti
  * not finite makes the outputs of up to 127 tokens before it undefined as well
  * as those after it.  Outputs must not overlap inputs or the workspace.  Repeated
  * calls give the same bits.  Asynchronous: returns PARARNN_OK, INVALID_ARG or
- * CUDA_ERROR.
+ * CUDA_ERROR.  The bf16 kernels wait on copies and products of their own block
+ * only, with a limit.  Should a wait ever run out (a fault of the hardware or of
+ * the library, not of the arguments), the block does not hang: the call has
+ * returned PARARNN_OK, and that block's rows of o and its state are NaN.
  */
 PARARNN_API int pararnn_linear_attention(const pararnn_attention_shape *shape, const pararnn_rows *q,
                                          const pararnn_rows *k, const pararnn_rows *v, const float *log_decay,
@@ -790,8 +793,9 @@ PARARNN_API size_t pararnn_linear_attention_backward_workspace_size(const pararn
  *   dq, dk, dv  DEVICE, dense, shapes and type of q, k, v; zero at and behind lengths[b].
  *   ds0      DEVICE float [B, H, dk, dv], or NULL where it is not wanted.
  *   workspace  DEVICE, pararnn_linear_attention_backward_workspace_size bytes.
- * Outputs must not overlap inputs or the workspace.  Precision, determinism and
- * the return value as pararnn_linear_attention.
+ * Outputs must not overlap inputs or the workspace.  Precision, determinism,
+ * the return value and what a wait that runs out leaves (NaN gradients) as
+ * pararnn_linear_attention.
  */
 PARARNN_API int pararnn_linear_attention_backward(const pararnn_attention_shape *shape, const pararnn_rows *q,
                                                   const pararnn_rows *k, const pararnn_rows *v,
