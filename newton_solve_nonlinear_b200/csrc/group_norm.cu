@@ -11,11 +11,13 @@
 // and squared deviations are formed about a local mean and joined by the pairwise update of Chan, Golub and
 // LeVeque (1979), so a large common offset costs no digits; sums are taken in a fixed order.
 //
-// Measured: 32768 rows of 16 heads of 128, bf16 under a gate, 92 us, 0.67 of a copy of its bytes (instructions: about 30
-// per element, most of them unpacking and the sigmoid; loading the next rows during a row's arithmetic gave 106 us, since
-// registers run out), its backward pass on 8192 rows 60 us, 0.43; [16, 65536, 64] fp32 to bf16 126 us, 47 of them for the
-// statistics and 80 to read x again and write y, each near HBM's rate; ragged [8, 1000, 640] backward 41 us, three
-// launches that wait for one another.
+// Measured: 32768 rows of 16 heads of 128, bf16 under a gate, 92 us, 0.67 of a copy of its bytes.  It waits for loads: 128
+// registers a thread leave a quarter of the warps (24 %), and these issue in 54 % of the cycles, about 30 instructions per
+// element, most of them unpacking and the sigmoid; loading the next rows during a row's arithmetic gave 106 us, since
+// registers run out.  Its backward pass on 8192 rows 60 us, 0.43, of which the sum of the CTAs' partial rows takes 5.
+// [16, 65536, 64] fp32 to bf16 126 us: 57 for the statistics and 69 to read x again and write y, 0.72 and 0.89 of a copy's
+// rate, as they follow one another in a call (47 and 80 alone under a profiler, from cold caches); registers limit the
+// warps in flight.  Ragged [8, 1000, 640] backward 43 us, three launches that wait for one another (16, 6 and 17).
 #include <cuda_bf16.h>
 
 #include "group_norm.cuh"
@@ -164,8 +166,8 @@ __device__ __forceinline__ float vdot(const float (&a)[V], const float (&b)[V]) 
 }
 
 // 1 / (1 + exp(-z)), by the fast exponential, which is documented as within 2 + floor(|1.173 z|) ulp, and the approximate
-// reciprocal, within one: the result is within (1 - s)(2 + 1.173 |z|) + 1.5 ulp, so within 2 where z > 0, and, as the
-// exponential's argument is large, more relative to a small result where z is far below zero (14 at -10, 96 at -80).
+// reciprocal, within one: the result is within (1 - s)(2 + 1.173 |z|) + 1.5 ulp, so within 3 where z > 0, and, as the
+// exponential's argument is large, more relative to a small result where z is far below zero (15 at -10, 97 at -80).
 // GELU's slope takes the same exponential of -z^2 / 2.
 __device__ __forceinline__ float sigmoid(float z) {
     float r;
@@ -871,7 +873,9 @@ __global__ void __launch_bounds__(kThr) gn_backward_apply_kernel(const GnArgs a,
 
 constexpr int kJoinMost = 1024;  // partial moments of one n that every CTA of the second pass joins by itself
 constexpr long long kJoinGrid = 1 << 20;  // CTAs of gn_channel_join_kernel, at most
-constexpr int kRowMost = 1024;  // channels of a group that a warp holds in registers (32 per lane)
+// channels of a group that a warp holds, 32 per lane: in registers forward; the backward kernels of 16 and 32 per lane
+// also use local memory (up to 268 bytes a thread)
+constexpr int kRowMost = 1024;
 
 bool row_regime(const GnArgs &a) { return a.S == 1 && a.C / a.G <= kRowMost; }
 int vec_of(const GnArgs &a) {

@@ -451,8 +451,10 @@ LaPlan la_plan(int B, int T, int H, int dk, int dv, int dtype, int sweeps, bool 
     } else {
         // two CTAs per SM, filled once, in segments of at least 64 rows ([1, 512, 4 x 64] forward 47 us with at least
         // 128, 35 with 64, 31 with 32; ragged [3, 517, 6 x 48 / 64] backward 90, 70, 74); 1.5 times that many CTAs
-        // where lengths may differ, so that short sequences leave room ([8, 2048, 16 x 64]: 330 us in 2 segments, 360
-        // in 4; five sequences of up to 2011 tokens, 12 heads of 96 and 80: 242 us in 6, 205 in 8, 250 in 10)
+        // where lengths may differ, so that short sequences leave room.  On eight ragged shapes with two sets of lengths
+        // each (2 to 16 sequences of up to 700 to 8192 tokens, 4 to 24 heads of 64 to 128) the best count of segments
+        // varies with the lengths, as the longest sequences' segments fall on SMs; 444 CTAs are 1.06 times the best one's
+        // time in the geometric mean, 1.27 at most, 296 are 1.15 and 1.43, 592 are 1.11 and 1.31
         const long long ctas = heads * ((dv + simt_tile(dk, dv) - 1) / simt_tile(dk, dv));
         want = ragged ? (444 + ctas - 1) / ctas : 296 / ctas;
         most = T / 64;

@@ -25,7 +25,8 @@
 // (2800, with the scores' weighing beside it), products (1900), state update and its copy (700), which the next chunk's
 // products wait for.  Two chunks in flight would hide it, but at this width one fills 227 KB of shared memory and all 512
 // columns of TMEM.  128 tokens are one row of products for each TMEM lane.  Sixteen state warps with a quarter of the
-// work each gave 236 us: 72 registers a thread are too few for the output warps.
+// work each gave 236 us: 72 registers a thread are too few for the output warps.  The 128-wide kernels use local memory
+// beside their registers, 72 bytes of stores a thread (248 in the state-only pass).
 #include <cuda_bf16.h>
 
 #include "linear_attention.cuh"
