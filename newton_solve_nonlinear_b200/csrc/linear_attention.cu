@@ -580,7 +580,9 @@ namespace {
 // One CTA per row and head: S = g S + k v^T, out = scale S^T q.  Thread (ty, tx) holds VW consecutive columns of
 // every NY-th row of S; the column sums meet in shared memory.  Rows of the batch that name the same slot are
 // taken in row order by the first one's CTA: tokens that follow each other.  Bound by HBM, as each state is read and
-// written once: 256 rows, 16 heads of 128 x 128 take 89 us, 541 MB at 0.93 of a copy's rate.
+// written once: 256 rows, 16 heads of 128 x 128 take 89 us, 541 MB at 0.93 of a copy's rate.  Each CTA reads all slots
+// once, without a workspace: 108 against 103 us without slots on those 256 rows from cold caches, 1459 against 1291 on 4096,
+// 7673 against 5091 on 16384.
 template <typename TI, int VW>
 __global__ void __launch_bounds__(256) la_step_kernel(const LaStep w) {
     __shared__ float qs[128], ks[128], part[256 * VW];
