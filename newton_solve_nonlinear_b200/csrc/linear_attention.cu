@@ -30,6 +30,12 @@ __device__ __forceinline__ float safe_log_decay(float x) { return fmaxf(x, -1e4f
 __device__ __forceinline__ float decay_pow(float ld, long long n) {
     return expf(static_cast<float>(static_cast<double>(ld) * static_cast<double>(n)));
 }
+// What decay_pow leaves of g^n.  A weight that the state is multiplied by again and again takes both parts: rounded to
+// fp32 it would be another decay, off by as many roundings as there are chunks (memories of 1e5 tokens, 16384 of them:
+// 9e-6 of the state)
+__device__ __forceinline__ float decay_rest(float ld, long long n) {
+    return static_cast<float>(exp(static_cast<double>(ld) * static_cast<double>(n)) - static_cast<double>(decay_pow(ld, n)));
+}
 
 __device__ __forceinline__ int row_count(const LaSweep &w, int b) {
     if (w.lengths == nullptr) return w.T;
@@ -111,7 +117,7 @@ __global__ void __launch_bounds__(kThr, 2) la_simt_kernel(const __grid_constant_
     static_assert(DVT == 64 || DVT == 96, "columns per thread");
     extern __shared__ __align__(16) float sm[];
     float *As = sm, *Bs = As + kC * PK, *Cs = Bs + kC * PK, *Os = Cs + kC * PV, *Ps = Os + kC * PV, *Ss = Ps + kC * PP;
-    float *pw = Ss + DKP * PV;  // g^0 .. g^C
+    float *pw = Ss + DKP * PV;  // g^0 .. g^C, and what is left of g^C and of the last chunk's g^n
     float *uw = pw + kC + 4;    // update g^(n - e - j) of row j, of a full chunk and of the last one, zero from n on
 
     const int tid = threadIdx.x;
@@ -127,8 +133,10 @@ __global__ void __launch_bounds__(kThr, 2) la_simt_kernel(const __grid_constant_
     const int ncol = min(DVT, w.dv - c0);
     const float ld = safe_log_decay(w.log_decay[h]);
     for (int i = tid; i <= kC; i += kThr) pw[i] = decay_pow(ld, i);
+    const int n_last = (hi - lo + kC - 1) % kC + 1;
+    if (tid >= kThr - 2) pw[kC + 1 + kThr - 1 - tid] = decay_rest(ld, tid == kThr - 1 ? kC : n_last);
     for (int i = tid; i < 2 * kC; i += kThr) {
-        const int j = i % kC, n = i < kC ? kC : (hi - lo + kC - 1) % kC + 1;
+        const int j = i % kC, n = i < kC ? kC : n_last;
         uw[i] = j < n ? decay_pow(ld, n - w.e - j) * w.update : 0.f;
     }
 
@@ -270,18 +278,12 @@ __global__ void __launch_bounds__(kThr, 2) la_simt_kernel(const __grid_constant_
                     }
             }
         }
-        {  // S = g^n S + update sum_j g^(n-e-j) b_j c_j^T: DKP / 32 x DVT / 8 per thread
+        {  // S = g^n S + update sum_j g^(n-e-j) b_j c_j^T: DKP / 32 x DVT / 8 per thread; the chunk's sum by itself, so that
+           // a state of many chunks is rounded once each and not once a token
             constexpr int RD = DKP / 32, CD = DVT / 32;
             const int d0 = (tid / 8) * RD, j0 = (tid % 8) * 4;
-            float4 acc[RD][CD];
-            const float gn = pw[n];
-#pragma unroll
-            for (int u = 0; u < RD; ++u)
-#pragma unroll
-                for (int q = 0; q < CD; ++q) {
-                    acc[u][q] = *f4(Ss + (d0 + u) * PV + j0 + 32 * q);
-                    acc[u][q].x *= gn, acc[u][q].y *= gn, acc[u][q].z *= gn, acc[u][q].w *= gn;
-                }
+            float4 acc[RD][CD] = {};
+            const float gn = pw[n], gn_rest = pw[n < kC ? kC + 2 : kC + 1];
             const float *wj = uw + (n < kC ? kC : 0);
 #pragma unroll 2
             for (int r = 0; r < n; r += 2) {  // rows from n on are zero
@@ -310,7 +312,13 @@ __global__ void __launch_bounds__(kThr, 2) la_simt_kernel(const __grid_constant_
 #pragma unroll
             for (int u = 0; u < RD; ++u)
 #pragma unroll
-                for (int q = 0; q < CD; ++q) *f4(Ss + (d0 + u) * PV + j0 + 32 * q) = acc[u][q];
+                for (int q = 0; q < CD; ++q) {
+                    float4 *const at = f4(Ss + (d0 + u) * PV + j0 + 32 * q);
+                    const float4 s = *at;
+                    fma4(acc[u][q], gn_rest, s);
+                    fma4(acc[u][q], gn, s);
+                    *at = acc[u][q];
+                }
         }
     }
     __syncthreads();
@@ -342,14 +350,17 @@ __global__ void __launch_bounds__(256) la_join_kernel(const LaSweep w) {
     const int n = w.dk * w.dv;
     const int per = (n + 255) / 256;  // CTAs per head
     const int bh = blockIdx.x / per, i = (blockIdx.x % per) * 256 + threadIdx.x;
-    if (i >= n) return;
     const float ld = safe_log_decay(w.log_decay[bh % w.H]);
     const int L = row_count(w, bh / w.H);
+    // the segment with the sequence's end, where it is not full
+    const int q_part = L / w.seg;
+    __shared__ float rest[2];  // of a full segment's weight and of that one's
+    if (threadIdx.x < 2) rest[threadIdx.x] = decay_rest(ld, threadIdx.x == 0 ? w.seg : L - q_part * w.seg);
+    __syncthreads();
+    if (i >= n) return;
     float *p = w.seg_state + static_cast<long long>(bh) * w.n_seg * n + i;
     float s = w.s_in == nullptr ? 0.f : w.s_in[static_cast<long long>(bh) * n + (i / w.dv) * w.s_i + (i % w.dv) * w.s_j];
     const float g_full = decay_pow(ld, w.seg);
-    // the segment with the sequence's end, where it is not full
-    const int q_part = L / w.seg;
     const float g_part = decay_pow(ld, L - q_part * w.seg);
     const int first = w.reverse ? w.n_seg - 1 : 0, dir = w.reverse ? -1 : 1;
     for (int k0 = 0; k0 < w.n_seg; k0 += KB) {
@@ -362,7 +373,7 @@ __global__ void __launch_bounds__(256) la_join_kernel(const LaSweep w) {
             if (k0 + k < w.n_seg) {
                 const int q = first + dir * (k0 + k);
                 p[static_cast<long long>(q) * n] = s;
-                if (q <= q_part) s = fmaf(q < q_part ? g_full : g_part, s, own[k]);
+                if (q <= q_part) s = fmaf(q < q_part ? g_full : g_part, s, fmaf(rest[q < q_part ? 0 : 1], s, own[k]));
             }
     }
 }
