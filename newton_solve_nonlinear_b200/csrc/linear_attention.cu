@@ -24,19 +24,6 @@ __device__ __forceinline__ float4 load4(const float *p, int n) {
     return make_float4(n > 0 ? p[0] : 0.f, n > 1 ? p[1] : 0.f, n > 2 ? p[2] : 0.f, n > 3 ? p[3] : 0.f);
 }
 
-// log g, kept finite: exp(n * -1e4) is 0 for every n >= 1 and 1 for n = 0, as g = 0 wants it.
-__device__ __forceinline__ float safe_log_decay(float x) { return fmaxf(x, -1e4f); }
-// g^n.  n * log g is formed in fp64 so that far positions keep their digits.
-__device__ __forceinline__ float decay_pow(float ld, long long n) {
-    return expf(static_cast<float>(static_cast<double>(ld) * static_cast<double>(n)));
-}
-// What decay_pow leaves of g^n.  A weight that the state is multiplied by again and again takes both parts: rounded to
-// fp32 it would be another decay, off by as many roundings as there are chunks (memories of 1e5 tokens, 16384 of them:
-// 9e-6 of the state)
-__device__ __forceinline__ float decay_rest(float ld, long long n) {
-    return static_cast<float>(exp(static_cast<double>(ld) * static_cast<double>(n)) - static_cast<double>(decay_pow(ld, n)));
-}
-
 __device__ __forceinline__ int row_count(const LaSweep &w, int b) {
     if (w.lengths == nullptr) return w.T;
     const int n = w.lengths[b];

@@ -81,4 +81,17 @@ struct LaStep {
 };
 cudaError_t launch_la_step(const LaStep &w, cudaStream_t s);
 
+// log g, kept finite: exp(n * -1e4) is 0 for every n >= 1 and 1 for n = 0, as g = 0 wants it.
+__device__ __forceinline__ float safe_log_decay(float x) { return fmaxf(x, -1e4f); }
+// g^n.  n * log g is formed in fp64 so that far positions keep their digits.
+__device__ __forceinline__ float decay_pow(float ld, long long n) {
+    return expf(static_cast<float>(static_cast<double>(ld) * static_cast<double>(n)));
+}
+// What decay_pow leaves of g^n.  A weight that the state is multiplied by again and again takes both parts: rounded to
+// fp32 it would be another decay, off by as many roundings as there are chunks (memories of 1e5 tokens, 16384 of them:
+// 9e-6 of the state)
+__device__ __forceinline__ float decay_rest(float ld, long long n) {
+    return static_cast<float>(exp(static_cast<double>(ld) * static_cast<double>(n)) - static_cast<double>(decay_pow(ld, n)));
+}
+
 }  // namespace pararnn

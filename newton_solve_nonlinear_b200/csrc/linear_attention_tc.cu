@@ -26,7 +26,7 @@
 // products wait for.  Two chunks in flight would hide it, but at this width one fills 227 KB of shared memory and all 512
 // columns of TMEM.  128 tokens are one row of products for each TMEM lane.  Sixteen state warps with a quarter of the
 // work each gave 236 us: 72 registers a thread are too few for the output warps.  The 128-wide kernels use local memory
-// beside their registers, 72 bytes of stores a thread (248 in the state-only pass).
+// beside their registers, 96 bytes of stores a thread (268 in the state-only pass).
 #include <cuda_bf16.h>
 
 #include "linear_attention.cuh"
@@ -265,7 +265,8 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
     // -32 .. 127 reversed, as far as any block needs it
     float *sw = reinterpret_cast<float *>(smem + Y::TAB);
     // update g^(n - e - j) of tile row x, for a full tile and for the last one: [2][8][20], row x = 64 h + 8 g + 2 l + i
-    // at [4 h + l][2 g + i], the order in which a lane of the state warps wants them (rows 20 apart: no bank conflicts)
+    // at [4 h + l][2 g + i], the order in which a lane of the state warps wants them (rows 20 apart: no bank conflicts); in
+    // the first gap, at 16, what rounding leaves of g^n for a full tile
     float *cw = sw + 160;
     Bars *bars = reinterpret_cast<Bars *>(smem + Y::BARS);
     volatile int *err = &bars->err;
@@ -284,9 +285,8 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
     const int e = w.e;
     const int part_chunk = rev ? 0 : chunks - 1;
     const bool unclean = chunks > 0 && n_part < kC;  // rows to be cleared: behind the sequence's end
-    // exp(n * -1e4) is 0 for n >= 1 and 1 for n = 0, as g = 0 wants it
-    const float ld = fmaxf(w.log_decay[h], -1e4f);
-    auto power = [&](int n) { return expf(static_cast<float>(static_cast<double>(ld) * n)); };
+    const float ld = safe_log_decay(w.log_decay[h]);
+    auto power = [&](int n) { return decay_pow(ld, n); };
     // first token of chunk c's tile
     auto first_token = [&](int c) { return lo + (rev ? chunks - 1 - c : c) * kC; };
 
@@ -322,6 +322,8 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         const int x = (tid - 160) & 127, n = tid - 160 < 128 ? kC : n_part, j = rev ? n - 1 - x : x;
         cw[(tid - 160 < 128 ? 0 : 160) + ((x >> 6) * 4 + ((x & 7) >> 1)) * 20 + ((x & 63) >> 3) * 2 + (x & 1)] =
             x < n ? power(n - e - j) * w.update : 0.f;
+    } else if (tid == 160 + 256) {
+        cw[16] = decay_rest(ld, kC);
     }
     fence_before();
     __syncthreads();
@@ -466,11 +468,18 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             // first, then tokens
             const int m_row = half * 64 + ((lane >> 4) << 3) + (lane & 7);
             const float g_full = power(kC), g_part = power(n_part);
-            // S = g^n S + dS of chunk c
+            // S = g^n S + dS of chunk c.  What rounding leaves of g^n is handed from full tile to full tile and taken when it
+            // makes a step of the weight, so that the weights' product is off by one rounding and not by one a chunk
+            float owed = 0.f;
             auto absorb = [&](int c) {
+                float gn = g_part;
+                if (c != part_chunk) {
+                    owed += cw[16];
+                    gn = g_full + owed;
+                    owed -= gn - g_full;
+                }
                 if (!mbar_wait(smem_u32(&bars->ds), c & 1, err)) return false;
                 fence_after();
-                const float gn = c == part_chunk ? g_part : g_full;
 #pragma unroll
                 for (int k = 0; k < KH; k += 32) {
                     float v[32];

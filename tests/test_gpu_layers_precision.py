@@ -120,3 +120,46 @@ def test_slow_decays_keep_fp32(B, T, H, d, decay):
     rel = lambda a, b: float((a.double() - b).norm() / b.norm())
     assert rel(s, ws) <= 2.0 ** -20
     assert rel(o[:, -1], wo) <= 2.0 ** -20
+
+
+@pytest.mark.parametrize("decay", [-2.4e-4, -1e-5, -1e-6])
+@pytest.mark.parametrize("B,T,H,dk,dv", [(2, 8192, 80, 32, 64), (2, 16384, 80, 64, 64), (2, 16384, 74, 128, 100),
+                                         (1, 16384, 1, 64, 128), (1, 65536, 8, 64, 64)])
+def test_slow_decays_keep_the_state_of_bf16_operands(B, T, H, dk, dv, decay):
+    """As above for the state, whose products are exact and whose chunks have 128 tokens: K is 128 at most in one sweep."""
+    g = torch.Generator("cuda").manual_seed(T + H)
+    q, k, v = (torch.randn(B, T, H, d, device="cuda", generator=g).to(BF16) for d in (dk, dk, dv))
+    s0 = torch.randn(B, H, dk, dv, device="cuda", generator=g)
+    ld = decay * torch.linspace(0.7, 1.3, H, device="cuda")
+    _, s = fw.linear_attention(q, k, v, ld, s0=s0)
+    ws, _ = _state_and_last_output(q, k, v, ld, s0)
+    assert float((s.double() - ws).norm() / ws.norm()) <= 2.0 ** -20
+    # backward: the same of the state carried in reversed time, dL/ds0
+    do = torch.randn(B, T, H, dv, device="cuda", generator=g).to(BF16)
+    got = fw.linear_attention_backward(q, k, v, ld, do, s0=s0, ds=s0)["ds0"]
+    age = torch.arange(1, T + 1, dtype=torch.float64, device="cuda")
+    want = torch.empty_like(ws)
+    for h in range(H):
+        w = torch.exp(age * ld[h].double())[None, :, None]
+        want[:, h] = dk ** -0.5 * ((q[:, :, h].double() * w).transpose(1, 2) @ do[:, :, h].double())
+        want[:, h] += torch.exp(T * ld[h].double()) * s0[:, h].double()
+    assert float((got.double() - want).norm() / want.norm()) <= 2.0 ** -20
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("decay", [-0.05, -0.3, -0.6, -5.0, -50.0])
+@pytest.mark.parametrize("T", [333, 700, 1100])
+def test_a_state_that_decays_to_nothing(T, decay, dtype):
+    """No inputs but a start state (forward) or a last gradient (backward), which is carried alone: g^T of it, by factors
+    that are each within 2 ulp of g^n and one rounding for each of up to 36 chunks: 36 * 2.5 * 2^-23 < 2^-16, relative
+    however small it gets."""
+    B, H, d = 2, 4, 64
+    q, k, v, do = (torch.zeros(B, T, H, d, dtype=dtype, device="cuda") for _ in range(4))
+    s0 = torch.randn(B, H, d, d, device="cuda", generator=torch.Generator("cuda").manual_seed(T))
+    ld = torch.full((H,), decay, device="cuda")
+    lengths = torch.tensor([T, T - 130], dtype=torch.int32, device="cuda")
+    _, s = fw.linear_attention(q, k, v, ld, s0=s0, lengths=lengths)
+    ds0 = fw.linear_attention_backward(q, k, v, ld, do, s0=s0, ds=s0, lengths=lengths)["ds0"]
+    want = torch.exp(lengths.double() * ld[0].double())[:, None, None, None] * s0.double()
+    for got in (s, ds0):
+        assert bool(((got.double() - want).abs() <= 2.0 ** -16 * want.abs() + 2.0 ** -126).all())
