@@ -602,7 +602,10 @@ __global__ void __launch_bounds__(256) la_step_kernel(const LaStep w) {
         for (int i = tid; i < b; i += blockDim.x) earlier |= w.slots[i] == slot;
         if (__syncthreads_or(earlier)) return;
     }
-    const float g = expf(safe_log_decay(w.log_decay[h]));
+    // g and what rounding leaves of it: one fp32 would be another decay, taken at every token (4096 tokens with a memory of
+    // 1e6: 5e-5 of the state).  Below e^-1/2 a state is forgotten before that counts.
+    const float ld = safe_log_decay(w.log_decay[h]), below = ld > -0.5f ? expm1f(ld) : 0.f;
+    const float g = ld > -0.5f ? 1.f + below : expf(ld), g_rest = ld > -0.5f ? below - (g - 1.f) : 0.f;
     const long long base = (static_cast<long long>(slot) * w.H + h) * w.dk * w.dv;
     const float *src = w.state + base;
     float *dst = w.out_state + base;
@@ -642,7 +645,7 @@ __global__ void __launch_bounds__(256) la_step_kernel(const LaStep w) {
                     if (d >= w.dk) break;
 #pragma unroll
                     for (int u = 0; u < VW; ++u) {
-                        s[r][u] = fmaf(ks[d], vv[u], g * s[r][u]);
+                        s[r][u] = fmaf(g, s[r][u], fmaf(ks[d], vv[u], g_rest * s[r][u]));
                         acc[u] = fmaf(qs[d], s[r][u], acc[u]);
                     }
                     float *p = dst + d * w.dv + tx * VW;

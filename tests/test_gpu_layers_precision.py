@@ -163,3 +163,44 @@ def test_a_state_that_decays_to_nothing(T, decay, dtype):
     want = torch.exp(lengths.double() * ld[0].double())[:, None, None, None] * s0.double()
     for got in (s, ds0):
         assert bool(((got.double() - want).abs() <= 2.0 ** -16 * want.abs() + 2.0 ** -126).all())
+
+
+@pytest.mark.parametrize("decay,tol", [(-1e-6, 2.0 ** -12), (-3.3e-5, 2.0 ** -18), (-1e-3, 2.0 ** -18)])
+def test_slow_decays_token_by_token(decay, tol):
+    """4096 single-token steps without inputs: the state is g^4096 of what it was.  A step rounds it once, 2^-23 / sqrt(12)
+    in the root mean square at most: sqrt(4096) of that is 2.2e-6 < 2^-18.  A weight of one fp32 would be off by up to 2^-25
+    each time, all in one direction: 1.2e-4.
+
+    That takes roundings that differ from step to step.  A step takes |decay| 2^23 to |decay| 2^24 ulp off the state, which
+    changes by |decay| of itself: at -1e-3 by 8 ulp and more, at -3.3e-5 by 0.009 ulp, so 37 ulp over the steps.  At -1e-6 8
+    to 17 ulp change by less than 0.07 ulp in all 4096 steps: they are rounded alike, by up to half an ulp, 4096 2^-24."""
+    B, H, d, n = 2, 3, 32, 4096
+    state = torch.randn(B, H, d, d, device="cuda", generator=torch.Generator("cuda").manual_seed(11))
+    start, zero = state.double(), torch.zeros(B, H, d, device="cuda")
+    ld = decay * torch.tensor([0.77, 1.0, 1.23], device="cuda")
+    for _ in range(n):
+        fw.linear_attention_step(zero, zero, zero, ld, state)
+    want = torch.exp(n * ld.double())[None, :, None, None] * start
+    off = (state.double() - want).flatten(2).norm(dim=2) / want.flatten(2).norm(dim=2)
+    assert float(off.max()) <= tol
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("decay,tol", [(-1e-6, 2.0 ** -16), (-3.3e-5, 2.0 ** -18), (-1e-3, 2.0 ** -18)])
+def test_slow_decays_token_by_token_with_inputs(decay, tol, dtype):
+    """As above with tokens that differ, so that the roundings do: two a step (the product's and the state's, the first one
+    smaller), sqrt(4096) of them, and less while the state grows: 2^-18.
+
+    Products of bf16 values have 16 bits, multiples of a state's ulp once it is some 2^6 large, so that only what a step
+    takes off is rounded.  It changes with the state by |decay| |k v|, at -1e-6 by some 0.1 ulp (2^-17) a step, and wanders
+    over half an ulp in (0.5 / 0.1)^2 = 25 steps, which are rounded alike: sqrt(25) 2.2e-6 < 2^-16 there."""
+    B, H, d, n = 2, 3, 32, 4096
+    g = torch.Generator("cuda").manual_seed(12)
+    q, k, v = (torch.randn(B, n, H, d, device="cuda", generator=g).to(dtype) for _ in range(3))
+    state = torch.randn(B, H, d, d, device="cuda", generator=g)
+    ld = decay * torch.tensor([0.77, 1.0, 1.23], device="cuda")
+    want, _ = _state_and_last_output(q, k, v, ld, state)
+    for t in range(n):
+        fw.linear_attention_step(q[:, t], k[:, t], v[:, t], ld, state)
+    off = (state.double() - want).flatten(2).norm(dim=2) / want.flatten(2).norm(dim=2)
+    assert float(off.max()) <= tol
