@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(256) la_step_kernel(const LaStep w) {
         if (__syncthreads_or(earlier)) return;
     }
     // g and what rounding leaves of it: one fp32 would be another decay, taken at every token (4096 tokens with a memory of
-    // 1e6: 5e-5 of the state).  Below e^-1/2 a state is forgotten before that counts.
+    // 1e6: 2e-4 of the state).  Below e^-1/2 a state is forgotten before that counts.
     const float ld = safe_log_decay(w.log_decay[h]), below = ld > -0.5f ? expm1f(ld) : 0.f;
     const float g = ld > -0.5f ? 1.f + below : expf(ld), g_rest = ld > -0.5f ? below - (g - 1.f) : 0.f;
     const long long base = (static_cast<long long>(slot) * w.H + h) * w.dk * w.dv;
