@@ -881,6 +881,221 @@ PARARNN_API int pararnn_group_norm_backward(const pararnn_norm_shape *shape, con
                                             const int *lengths, void *dx, float *dweight, float *dbias, void *dgate,
                                             void *workspace, size_t ws_bytes, pararnn_stream stream);
 
+/* A selective state space scan.
+ *   B, T     sequences and tokens, >= 1; T at most 2^30, B * D at most 2^30.
+ *   D, G     channels, and groups of them that share b and c (G divides D:
+ *            channel d reads group d / (D / G)).
+ *   N        states of a channel, 1 .. 64.
+ *   dtype    pararnn_dtype of x, dt, b, c, gate, of the outputs and of their gradients.
+ *   softplus 1: the step is softplus(dt + dt_bias); 0: dt + dt_bias. */
+typedef struct {
+    int B, T, D, G, N;
+    int dtype;
+    int softplus;
+} pararnn_scan_shape;
+
+/* pararnn_selective_scan_workspace_size -- bytes pararnn_selective_scan needs;
+ * 1 where it needs none, and then takes NULL; 0 for a rejected shape. */
+PARARNN_API size_t pararnn_selective_scan_workspace_size(const pararnn_scan_shape *shape);
+
+/*
+ * pararnn_selective_scan -- the diagonal linear recurrence whose coefficients
+ * come from the input: for every sequence, channel d (of group g) and state n,
+ * with s_t the step of the token,
+ *   h_t = exp(s_t a[d,n]) h_(t-1) + s_t x_t b_t[g,n],
+ *   y_t = (sum_n c_t[g,n] h_t[n] + skip[d] x_t) * silu(gate_t),
+ * for t < lengths[b].  (pararnn_affine_scan on coefficients that are formed on
+ * the fly and never stored; where there are few sequences and channels, time is
+ * split into segments that run at once.)
+ *   x, dt    [B, T, D] (pararnn_rows, stride_h unused: views of one projected
+ *            tensor will do);  gate likewise, or NULL for no gate.
+ *   b, c     [B, T, G, N] (pararnn_rows).
+ *   a        DEVICE float [D, N], the rates: < 0 for states that decay.
+ *   skip, dt_bias  DEVICE float [D], or NULL for zero.
+ *   h0       DEVICE float [B, D, N], the states before the first token, or NULL for zero.
+ *   lengths  DEVICE int [B], or NULL for T: tokens at and behind lengths[b]
+ *            (clamped to 0 .. T) are not read, their outputs are zero, and the
+ *            state is the one after lengths[b] tokens.
+ *   y        DEVICE [B, T, D] of shape->dtype, output.
+ *   h        DEVICE float [B, D, N], output: the last states.  May be h0 itself.
+ *   kept     DEVICE float [B, ceil(T / 8), D, N], output, or NULL: the states
+ *            before every eighth token, for the backward pass.  Those at and
+ *            behind lengths[b] are not written.
+ *   workspace  DEVICE, pararnn_selective_scan_workspace_size bytes, 256-byte aligned.
+ * Steps, decays, states and sums are fp32; exp(s a) enters as the difference
+ * from 1, so that slow decays keep their rate.  Outputs must not overlap inputs
+ * or the workspace.  Repeated calls give the same bits.  Asynchronous: returns
+ * PARARNN_OK, INVALID_ARG or CUDA_ERROR.
+ */
+PARARNN_API int pararnn_selective_scan(const pararnn_scan_shape *shape, const pararnn_rows *x, const pararnn_rows *dt,
+                                       const float *a, const pararnn_rows *b, const pararnn_rows *c, const float *skip,
+                                       const pararnn_rows *gate, const float *dt_bias, const float *h0,
+                                       const int *lengths, void *y, float *h, float *kept, void *workspace,
+                                       size_t ws_bytes, pararnn_stream stream);
+
+/* Bytes pararnn_selective_scan_backward needs, with the kept states given (has_kept
+ * != 0) or not; 0 for a rejected shape. */
+PARARNN_API size_t pararnn_selective_scan_backward_workspace_size(const pararnn_scan_shape *shape, int has_kept);
+
+/*
+ * pararnn_selective_scan_backward -- its backward pass, from dL/dy and dL/dh
+ * (the last states') to the gradients of everything that the scan reads.
+ *   x .. lengths  as given to the forward pass.
+ *   dy       [B, T, D] of shape->dtype (pararnn_rows).
+ *   dh       DEVICE float [B, D, N], or NULL for zero.
+ *   kept     what the forward pass kept of the same inputs, or NULL: then the
+ *            states are formed again in the workspace.
+ *   dx, ddt, dgate  DEVICE [B, T, D], db, dc  DEVICE [B, T, G, N], dense, of
+ *            shape->dtype, zero at and behind lengths[b]; dgate exactly where there is a gate.
+ *   da       DEVICE float [D, N];  dskip, ddt_bias  DEVICE float [D];  dh0  DEVICE
+ *            float [B, D, N]; the last three NULL where they are not wanted.
+ *   workspace  DEVICE, pararnn_selective_scan_backward_workspace_size bytes, 256-byte aligned.
+ * Outputs must not overlap inputs or the workspace.  Sums are fp32 in a fixed
+ * order: repeated calls give the same bits.  Asynchronous: returns PARARNN_OK,
+ * INVALID_ARG or CUDA_ERROR.
+ */
+PARARNN_API int pararnn_selective_scan_backward(const pararnn_scan_shape *shape, const pararnn_rows *x,
+                                                const pararnn_rows *dt, const float *a, const pararnn_rows *b,
+                                                const pararnn_rows *c, const float *skip, const pararnn_rows *gate,
+                                                const float *dt_bias, const pararnn_rows *dy, const float *h0,
+                                                const float *dh, const int *lengths, const float *kept, void *dx,
+                                                void *ddt, float *da, void *db, void *dc, float *dskip, void *dgate,
+                                                float *ddt_bias, float *dh0, void *workspace, size_t ws_bytes,
+                                                pararnn_stream stream);
+
+/*
+ * pararnn_selective_scan_step -- the recurrence for one token of each sequence
+ * (shape->T = 1).
+ *   x, dt, gate [B, D], b, c [B, G, N]  (pararnn_rows; stride_t unused).
+ *   state, out_state  DEVICE float [n_slots, D, N]: the states before and after
+ *            the token; out_state may be `state` itself and must not overlap it otherwise.
+ *   slots    DEVICE int [B], as in pararnn_linear_attention_step: row b's state
+ *            is state[slots[b]], a slot outside 0 .. n_slots - 1 gives a zero
+ *            output, rows that name the same slot follow each other in row
+ *            order.  NULL: slot b for row b (n_slots = B).
+ *   y        DEVICE [B, D] of shape->dtype, output.
+ * Asynchronous; no workspace; returns PARARNN_OK, INVALID_ARG or CUDA_ERROR.
+ */
+PARARNN_API int pararnn_selective_scan_step(const pararnn_scan_shape *shape, const pararnn_rows *x,
+                                            const pararnn_rows *dt, const float *a, const pararnn_rows *b,
+                                            const pararnn_rows *c, const float *skip, const pararnn_rows *gate,
+                                            const float *dt_bias, const float *state, const int *slots, int n_slots,
+                                            void *y, float *out_state, pararnn_stream stream);
+
+/* A short causal convolution over time, one filter per channel.
+ *   B, T, D  sequences, tokens (at most 2^30) and channels; B * D at most 2^30.
+ *   W        taps, 2 .. 8.
+ *   dtype    of x, y, the states and their gradients.
+ *   act      PARARNN_ACT_NONE or PARARNN_ACT_SILU. */
+typedef struct {
+    int B, T, D, W;
+    int dtype;
+    int act;
+} pararnn_conv_shape;
+
+/*
+ * pararnn_causal_conv -- y_t = act(bias[d] + sum_j weight[d,j] x_(t-W+1+j)) for
+ * t < lengths[b], channels last.
+ *   x        [B, T, D] (pararnn_rows, stride_h unused).
+ *   weight   DEVICE float [D, W], the last tap for the token itself;  bias
+ *            DEVICE float [D], or NULL for zero.
+ *   state    DEVICE [B, W - 1, D] of shape->dtype, the inputs before the first, or NULL for zero.
+ *   lengths  DEVICE int [B], or NULL for T: tokens at and behind lengths[b]
+ *            (clamped to 0 .. T) are not read and their outputs are zero.
+ *   y        DEVICE [B, T, D], output;  last  DEVICE [B, W - 1, D], output: the
+ *            last W - 1 inputs (of the state where the sequence is shorter).
+ * Sums are fp32.  Outputs must not overlap inputs.  Asynchronous; no workspace;
+ * returns PARARNN_OK, INVALID_ARG or CUDA_ERROR.
+ */
+PARARNN_API int pararnn_causal_conv(const pararnn_conv_shape *shape, const pararnn_rows *x, const float *weight,
+                                    const float *bias, const void *state, const int *lengths, void *y, void *last,
+                                    pararnn_stream stream);
+
+/* Bytes pararnn_causal_conv_backward needs; 0 for a rejected shape. */
+PARARNN_API size_t pararnn_causal_conv_backward_workspace_size(const pararnn_conv_shape *shape);
+
+/*
+ * pararnn_causal_conv_backward -- its backward pass, from dL/dy and dL/dlast.
+ *   x .. lengths  as given to the forward pass;  dy [B, T, D] (pararnn_rows).
+ *   dlast    DEVICE [B, W - 1, D] of shape->dtype, or NULL for zero.
+ *   dx       DEVICE [B, T, D], zero at and behind lengths[b];  dstate  DEVICE
+ *            [B, W - 1, D], or NULL where it is not wanted.
+ *   dweight  DEVICE float [D, W];  dbias  DEVICE float [D], or NULL.
+ *   workspace  DEVICE, pararnn_causal_conv_backward_workspace_size bytes, 256-byte aligned.
+ * Outputs must not overlap inputs or the workspace.  Sums are fp32 in a fixed
+ * order.  Asynchronous: returns PARARNN_OK, INVALID_ARG or CUDA_ERROR.
+ */
+PARARNN_API int pararnn_causal_conv_backward(const pararnn_conv_shape *shape, const pararnn_rows *x, const float *weight,
+                                             const float *bias, const pararnn_rows *dy, const void *state,
+                                             const void *dlast, const int *lengths, void *dx, float *dweight,
+                                             float *dbias, void *dstate, void *workspace, size_t ws_bytes,
+                                             pararnn_stream stream);
+
+/*
+ * pararnn_causal_conv_step -- one token of each sequence (shape->T = 1): y of x
+ * [B, D] (pararnn_rows, stride_b alone used), and the inputs moved up by one.
+ *   state, out_state  DEVICE [n_slots, W - 1, D] of shape->dtype;  slots, n_slots
+ *            and what is returned as in pararnn_selective_scan_step.
+ */
+PARARNN_API int pararnn_causal_conv_step(const pararnn_conv_shape *shape, const pararnn_rows *x, const float *weight,
+                                         const float *bias, const void *state, const int *slots, int n_slots, void *y,
+                                         void *out_state, pararnn_stream stream);
+
+/* The norm of a residual stream.
+ *   N, S, C   rows are [N, S, C]; N * S below 2^31, C at most 2^30.
+ *   x_dtype   of the branch x and its gradient;  r_dtype  of the stream and its
+ *             gradient;  y_dtype  of y and its gradient.
+ *   rms       1: without the mean;  eps  added to the mean square, >= 0. */
+typedef struct {
+    int N, S, C;
+    int x_dtype, r_dtype, y_dtype;
+    int rms;
+    float eps;
+} pararnn_stream_shape;
+
+/*
+ * pararnn_layer_norm -- a block's entry: the branch is added to the stream and
+ * the sum's rows are normalised.  With m the mean of a row of r = residual + x
+ * (zero in the rms form) and k = 1 / sqrt(mean (r - m)^2 + eps),
+ *   y = (r - m) k weight + bias.
+ *   x        DEVICE [N, S, C] of x_dtype;  residual  DEVICE [N, S, C] of r_dtype,
+ *            or NULL: then r = x, and the argument r is NULL too.
+ *   weight, bias  DEVICE float [C], NULL for ones and zeros.
+ *   lengths  DEVICE int [N], or NULL: rows at and behind lengths[n] (clamped to
+ *            0 .. S) are not read; y and r are zero there.
+ *   y        DEVICE [N, S, C] of y_dtype, output;  r  DEVICE [N, S, C] of r_dtype,
+ *            output, may be residual itself;  stats  DEVICE float [N, S, 2],
+ *            output: m and k (0 and 1 / sqrt(eps) where a row does not count).
+ * y is formed from the sum before it is rounded to r_dtype.  Sums are fp32,
+ * squares about the mean.  Outputs must not overlap inputs otherwise.
+ * Asynchronous; no workspace; returns PARARNN_OK, INVALID_ARG or CUDA_ERROR.
+ */
+PARARNN_API int pararnn_layer_norm(const pararnn_stream_shape *shape, const void *x, const void *residual,
+                                   const float *weight, const float *bias, const int *lengths, void *y, void *r,
+                                   float *stats, pararnn_stream stream);
+
+/* Bytes pararnn_layer_norm_backward needs; 0 for a rejected shape. */
+PARARNN_API size_t pararnn_layer_norm_backward_workspace_size(const pararnn_stream_shape *shape);
+
+/*
+ * pararnn_layer_norm_backward -- its backward pass.  r is the stream as stored
+ * (x where there was no residual), stats the forward's, dy [N, S, C] of y_dtype,
+ * dr_in [N, S, C] of r_dtype the gradient that reaches the stream from behind
+ * (NULL for zero).
+ *   dr       DEVICE [N, S, C] of r_dtype, output: the gradient of the sum, which
+ *            is that of the residual and of the branch; may be dr_in itself.
+ *   dx       DEVICE [N, S, C] of x_dtype, output: the same rounded to the branch's
+ *            type, or NULL where it is not wanted.
+ *   dweight, dbias  DEVICE float [C], NULL where they are not wanted.
+ *   workspace  DEVICE, pararnn_layer_norm_backward_workspace_size bytes, 256-byte aligned.
+ * Other arguments, sums and the return value as pararnn_layer_norm; sums over
+ * rows are taken in a fixed order.
+ */
+PARARNN_API int pararnn_layer_norm_backward(const pararnn_stream_shape *shape, const void *r, const float *stats,
+                                            const void *dy, const float *weight, const void *dr_in, const int *lengths,
+                                            void *dr, void *dx, float *dweight, float *dbias, void *workspace,
+                                            size_t ws_bytes, pararnn_stream stream);
+
 /* pararnn_status_string -- a static, human-readable name of a status code. */
 PARARNN_API const char *pararnn_status_string(int status);
 

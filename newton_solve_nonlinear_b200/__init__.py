@@ -6,6 +6,8 @@ The compute lives in ``libpararnn.so`` (CUDA kernels behind the C ABI of
 not load the library; the first call does, and raises if it is missing.
 """
 from .binding import (  # noqa: F401
-    SolveResult, affine_scan, alloc_workspace, group_norm, group_norm_backward, linear_attention,
-    linear_attention_backward, linear_attention_step, newton_solve, solve_workload, workspace_size,
+    SolveResult, affine_scan, alloc_workspace, causal_conv, causal_conv_backward, causal_conv_step, group_norm,
+    group_norm_backward, layer_norm, layer_norm_backward, linear_attention, linear_attention_backward,
+    linear_attention_step, newton_solve, selective_scan, selective_scan_backward, selective_scan_step, solve_workload,
+    workspace_size,
 )

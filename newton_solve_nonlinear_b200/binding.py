@@ -39,7 +39,11 @@ EXPORTS = ("pararnn_workspace_size", "pararnn_newton_solve", "pararnn_newton_sol
            "pararnn_linear_attention_workspace_size", "pararnn_linear_attention_backward",
            "pararnn_linear_attention_backward_workspace_size", "pararnn_linear_attention_step",
            "pararnn_group_norm", "pararnn_group_norm_workspace_size", "pararnn_group_norm_backward",
-           "pararnn_group_norm_backward_workspace_size")
+           "pararnn_group_norm_backward_workspace_size", "pararnn_selective_scan",
+           "pararnn_selective_scan_workspace_size", "pararnn_selective_scan_backward",
+           "pararnn_selective_scan_backward_workspace_size", "pararnn_selective_scan_step", "pararnn_causal_conv",
+           "pararnn_causal_conv_backward", "pararnn_causal_conv_backward_workspace_size", "pararnn_causal_conv_step",
+           "pararnn_layer_norm", "pararnn_layer_norm_backward", "pararnn_layer_norm_backward_workspace_size")
 
 
 class Cell(ctypes.Structure):
@@ -68,6 +72,19 @@ class AttentionShape(ctypes.Structure):
 
 class NormShape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in ("N", "S", "C", "groups", "x_dtype", "y_dtype", "act")] + [
+        ("eps", ctypes.c_float)]
+
+
+class ScanShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "T", "D", "G", "N", "dtype", "softplus")]
+
+
+class ConvShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "T", "D", "W", "dtype", "act")]
+
+
+class StreamShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("N", "S", "C", "x_dtype", "r_dtype", "y_dtype", "rms")] + [
         ("eps", ctypes.c_float)]
 
 
@@ -184,6 +201,23 @@ def lib() -> ctypes.CDLL:
         L.pararnn_group_norm.restype = ci
         L.pararnn_group_norm_backward.argtypes = [norm_p, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.pararnn_group_norm_backward.restype = ci
+        scan_p, conv_p, stream_p = ctypes.POINTER(ScanShape), ctypes.POINTER(ConvShape), ctypes.POINTER(StreamShape)
+        scan_in = [scan_p, rows_p, rows_p, vp, rows_p, rows_p, vp, rows_p, vp]
+        for name, args, res in (
+                ("pararnn_selective_scan_workspace_size", [scan_p], sz),
+                ("pararnn_selective_scan", scan_in + [vp] * 6 + [sz, vp], ci),
+                ("pararnn_selective_scan_backward_workspace_size", [scan_p, ci], sz),
+                ("pararnn_selective_scan_backward", scan_in + [rows_p] + [vp] * 14 + [sz, vp], ci),
+                ("pararnn_selective_scan_step", scan_in + [vp, vp, ci, vp, vp, vp], ci),
+                ("pararnn_causal_conv", [conv_p, rows_p] + [vp] * 7, ci),
+                ("pararnn_causal_conv_backward_workspace_size", [conv_p], sz),
+                ("pararnn_causal_conv_backward", [conv_p, rows_p, vp, vp, rows_p] + [vp] * 8 + [sz, vp], ci),
+                ("pararnn_causal_conv_step", [conv_p, rows_p, vp, vp, vp, vp, ci, vp, vp, vp], ci),
+                ("pararnn_layer_norm", [stream_p] + [vp] * 9, ci),
+                ("pararnn_layer_norm_backward_workspace_size", [stream_p], sz),
+                ("pararnn_layer_norm_backward", [stream_p] + [vp] * 11 + [sz, vp], ci)):
+            getattr(L, name).argtypes = args
+            getattr(L, name).restype = res
         L.pararnn_status_string.argtypes = [ci]
         L.pararnn_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -1041,4 +1075,352 @@ def group_norm_backward(x, stats, dy, groups: int, weight=None, bias=None, *, ga
         shape, px, _like(stats, "stats", x, (shape.N, groups, 2), torch.float32), _like(dy, "dy", x, x.shape, dy.dtype),
         pw, pb, pg, _like(lengths, "lengths", x, (shape.N,), torch.int32), ptr(g["dx"]), ptr(g["dweight"]),
         ptr(g["dbias"]), ptr(g["dgate"]), ws_at, ws_bytes, _current(x)), "pararnn_group_norm_backward")
+    return g
+
+
+# ---- the selective state space block: its scan, its short convolution, the norm of its stream ---------------
+
+
+def _wants_grad(*tensors) -> bool:
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
+def _plain_rows(t, name: str, like, shape):
+    """A [B, T, D] operand (or [B, D]) of like's type, strided in all but the last axis; None for None."""
+    if t is None:
+        return None
+    st = t.stride()
+    if (t.dtype != like.dtype or t.shape != shape or t.get_device() != like.get_device()
+            or (st[-1] != 1 and shape[-1] != 1)):
+        _refuse(t, name, like, shape, like.dtype)
+    return Rows(t.data_ptr(), st[0], st[1] if len(st) == 3 else 0, 0)
+
+
+def _scan_operands(x, dt, a, b, c, skip, gate, dt_bias, softplus, dims: int = 3):
+    """The shape and the operands that all three calls begin with."""
+    if x.dim() != dims or b.dim() != dims + 1 or a.dim() != 2:
+        raise ValueError("x must be [B, T, D], b and c [B, T, G, N], a [D, N]" if dims == 3
+                         else "x must be [B, D], b and c [B, G, N], a [D, N]")
+    lead, D = x.shape[:-1], x.shape[-1]
+    B, T = lead[0], lead[1] if dims == 3 else 1
+    G, N = b.shape[-2:]
+    if max(B, T, D) >= _INT:
+        raise ValueError(f"B, T and D must be below 2**31: got {B}, {T} and {D}")
+    if min(B, T, D, G) < 1 or D % G:
+        raise ValueError(f"B, T, D and G must be positive, D a multiple of G: got {B}, {T}, {D} and {G}")
+    if not 1 <= N <= 64:
+        raise ValueError(f"a channel has 1 to 64 states: got {N}")
+    shape = ScanShape(B, T, D, G, N, _dtype_code(x.dtype), 1 if softplus else 0)
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    f32 = torch.float32
+    return (shape, _plain_rows(x, "x", x, (*lead, D)), _plain_rows(dt, "dt", x, (*lead, D)), _like(a, "a", x, (D, N), f32),
+            _rows(b, "b", x, (*lead, G, N)), _rows(c, "c", x, (*lead, G, N)), _like(skip, "skip", x, (D,), f32),
+            _plain_rows(gate, "gate", x, (*lead, D)), _like(dt_bias, "dt_bias", x, (D,), f32))
+
+
+def selective_scan(x, dt, a, b, c, *, skip=None, gate=None, dt_bias=None, softplus: bool = True, h0=None, lengths=None,
+                   keep: bool = False, out=None, workspace=None, stream=None):
+    """The selective state space scan over whole sequences: with the step s_t =
+    softplus(dt_t + dt_bias) (without ``softplus``: dt_t + dt_bias),
+    h_t = exp(s_t a) h_(t-1) + s_t x_t b_t, y_t = (sum_n c_t h_t + skip x_t) silu(gate_t).
+
+    x, dt, gate [B,T,D], b, c [B,T,G,N] (fp32 or bf16 CUDA; views with any
+    strides whose last axis is contiguous; G divides D, N up to 64), a [D,N],
+    skip, dt_bias [D] fp32, h0 [B,D,N] fp32 the states before (zero if None),
+    lengths [B] int32 (tokens behind them are not read, outputs there are zero).
+    Returns (y [B,T,D] of x's type, the last states [B,D,N] fp32), and with
+    ``keep`` the states before every eighth token [B,ceil(T/8),D,N] fp32, which
+    spare ``selective_scan_backward`` a pass; ``out`` gives y and the last states
+    (these may be h0).  Records no graph: operands that require a gradient are
+    taken under ``torch.no_grad()`` only."""
+    under = _context(x, stream)
+    if under is not None:
+        with under:
+            return selective_scan(x, dt, a, b, c, skip=skip, gate=gate, dt_bias=dt_bias, softplus=softplus, h0=h0,
+                                  lengths=lengths, keep=keep, out=out, workspace=workspace)
+    if _wants_grad(x, dt, a, b, c, skip, gate, dt_bias, h0):
+        _no_graph("selective_scan")
+    ops = _scan_operands(x, dt, a, b, c, skip, gate, dt_bias, softplus)
+    s = ops[0]
+    states = (s.B, s.D, s.N)
+    y, h = out if out is not None else (x.new_empty((s.B, s.T, s.D)), a.new_empty(states))
+    kept = a.new_empty((s.B, (s.T + 7) // 8, s.D, s.N)) if keep else None
+    L = lib()
+    ws, ws_at, ws_bytes = _workspace(L.pararnn_selective_scan_workspace_size(s), "pararnn_selective_scan", workspace, x.device)
+    f32 = torch.float32
+    _checked(L.pararnn_selective_scan(
+        *ops, _like(h0, "h0", x, states, f32), _like(lengths, "lengths", x, (s.B,), torch.int32),
+        _like(y, "out", x, (s.B, s.T, s.D), x.dtype), _like(h, "out", x, states, f32),
+        None if kept is None else kept.data_ptr(), ws_at, ws_bytes, _current(x)), "pararnn_selective_scan")
+    return (y, h, kept) if keep else (y, h)
+
+
+def selective_scan_backward(x, dt, a, b, c, dy, *, skip=None, gate=None, dt_bias=None, softplus: bool = True, h0=None,
+                            dh=None, lengths=None, kept=None, workspace=None, stream=None) -> dict:
+    """The backward pass of ``selective_scan``: dy [B,T,D] = dL/dy (x's type,
+    strided as x), dh [B,D,N] fp32 the gradient of the last states (zero if
+    None), kept what the forward pass kept of the same inputs (formed again if
+    None); the rest as given to the forward pass.  Returns dict(dx, ddt, da, db,
+    dc, dskip, dgate, ddt_bias, dh0), each of its operand's type, None where the
+    forward pass had no such operand."""
+    under = _context(x, stream)
+    if under is not None:
+        with under:
+            return selective_scan_backward(x, dt, a, b, c, dy, skip=skip, gate=gate, dt_bias=dt_bias, softplus=softplus,
+                                           h0=h0, dh=dh, lengths=lengths, kept=kept, workspace=workspace)
+    ops = _scan_operands(x, dt, a, b, c, skip, gate, dt_bias, softplus)
+    s = ops[0]
+    rows, shared, states = (s.B, s.T, s.D), (s.B, s.T, s.G, s.N), (s.B, s.D, s.N)
+    rdy = _plain_rows(dy, "dy", x, rows)
+    dense = lambda t, shape: None if t is None else t.new_empty(shape)
+    ptr = lambda t: None if t is None else t.data_ptr()
+    g = dict(dx=x.new_empty(rows), ddt=x.new_empty(rows), da=a.new_empty((s.D, s.N)), db=x.new_empty(shared),
+             dc=x.new_empty(shared), dskip=dense(skip, (s.D,)), dgate=dense(gate, rows), ddt_bias=dense(dt_bias, (s.D,)),
+             dh0=dense(h0, states))
+    L = lib()
+    ws, ws_at, ws_bytes = _workspace(L.pararnn_selective_scan_backward_workspace_size(s, 0 if kept is None else 1),
+                                       "pararnn_selective_scan_backward", workspace, x.device)
+    f32 = torch.float32
+    _checked(L.pararnn_selective_scan_backward(
+        *ops, rdy, _like(h0, "h0", x, states, f32), _like(dh, "dh", x, states, f32),
+        _like(lengths, "lengths", x, (s.B,), torch.int32),
+        _like(kept, "kept", x, (s.B, (s.T + 7) // 8, s.D, s.N), f32),
+        *(ptr(g[n]) for n in ("dx", "ddt", "da", "db", "dc", "dskip", "dgate", "ddt_bias", "dh0")), ws_at, ws_bytes,
+        _current(x)), "pararnn_selective_scan_backward")
+    return g
+
+
+def selective_scan_step(x, dt, a, b, c, state, *, skip=None, gate=None, dt_bias=None, softplus: bool = True, slots=None,
+                        out_state=None, out=None, stream=None):
+    """One token of every sequence through ``selective_scan``'s recurrence.
+
+    x, dt, gate [B,D], b, c [B,G,N]; state [n,D,N] fp32 holds the states, row
+    b's at slots[b] (int32 [B]; outside 0..n-1: no state, y is zero; the same
+    slot twice: tokens in row order), or at b if None (n = B).  The states after
+    the token go to ``out_state``, or replace those in ``state`` if None.
+    Returns y [B,D].  Records no graph, as ``selective_scan``."""
+    under = _context(x, stream)
+    if under is not None:
+        with under:
+            return selective_scan_step(x, dt, a, b, c, state, skip=skip, gate=gate, dt_bias=dt_bias, softplus=softplus,
+                                       slots=slots, out_state=out_state, out=out)
+    if _wants_grad(x, dt, a, b, c, skip, gate, dt_bias, state):
+        _no_graph("selective_scan_step")
+    n = _pool(state, 3, "[n, D, N]", slots, x)
+    ops = _scan_operands(x, dt, a, b, c, skip, gate, dt_bias, softplus, 2)
+    s = ops[0]
+    if out is None:
+        out = x.new_empty((s.B, s.D))
+    pool = (n, s.D, s.N)
+    src = _like(state, "state", x, pool, torch.float32)
+    _checked(lib().pararnn_selective_scan_step(
+        *ops, src, _like(slots, "slots", x, (s.B,), torch.int32), n, _like(out, "out", x, (s.B, s.D), x.dtype),
+        src if out_state is None else _like(out_state, "out_state", x, pool, torch.float32), _current(x)),
+        "pararnn_selective_scan_step")
+    return out
+
+
+def _pool(state, dims: int, what: str, slots, x) -> int:
+    """The rows of a pool of states."""
+    if state.dim() != dims or state.shape[0] < 1:
+        raise ValueError(f"state must be {what}")
+    n = state.shape[0]
+    if n >= _INT:
+        raise ValueError(f"states must be below 2**31: got {n}")
+    if slots is None and x.dim() and n != x.shape[0]:
+        raise ValueError(f"state has {n} rows for {x.shape[0]} sequences: slots says which")
+    return n
+
+
+def _conv_shape(x, weight, act, dims: int = 3):
+    if x.dim() != dims or weight.dim() != 2:
+        raise ValueError(f"x must be [B, {'T, ' if dims == 3 else ''}D] and weight [D, W]")
+    if act not in ("none", "silu"):
+        raise ValueError("act must be none or silu")
+    B, T, D, W = x.shape[0], x.shape[1] if dims == 3 else 1, x.shape[-1], weight.shape[1]
+    if max(B, T, D) >= _INT:
+        raise ValueError(f"B, T and D must be below 2**31: got {B}, {T} and {D}")
+    if min(B, T, D) < 1 or not 2 <= W <= 8:
+        raise ValueError(f"x must not be empty and a filter has 2 to 8 taps: {tuple(x.shape)}, {W}")
+    shape = ConvShape(B, T, D, W, _dtype_code(x.dtype), ACTIVATIONS[act])
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    return shape
+
+
+def causal_conv(x, weight, bias=None, *, act: str = "silu", state=None, lengths=None, out=None, stream=None):
+    """The short causal convolution over time, one filter per channel:
+    y_t = act(bias + sum_j weight[:, j] x_(t-W+1+j)).
+
+    x [B,T,D] (fp32 or bf16 CUDA; any strides with a contiguous last axis),
+    weight [D,W] (2 to 8 taps) and bias [D] fp32, act "none" or "silu", state
+    [B,W-1,D] of x's type the inputs before the first (zero if None), lengths
+    [B] int32 (tokens behind them are not read, outputs there are zero).
+    Returns (y [B,T,D], the last W-1 inputs [B,W-1,D]); ``out`` gives both.
+    Records no graph: operands that require a gradient are taken under
+    ``torch.no_grad()`` only, and ``causal_conv_backward`` has the gradients."""
+    under = _context(x, stream)
+    if under is not None:
+        with under:
+            return causal_conv(x, weight, bias, act=act, state=state, lengths=lengths, out=out)
+    if _wants_grad(x, weight, bias, state):
+        _no_graph("causal_conv")
+    s = _conv_shape(x, weight, act)
+    ends = (s.B, s.W - 1, s.D)
+    y, last = out if out is not None else (x.new_empty((s.B, s.T, s.D)), x.new_empty(ends))
+    f32 = torch.float32
+    _checked(lib().pararnn_causal_conv(
+        s, _plain_rows(x, "x", x, (s.B, s.T, s.D)), _like(weight, "weight", x, (s.D, s.W), f32),
+        _like(bias, "bias", x, (s.D,), f32), _like(state, "state", x, ends, x.dtype),
+        _like(lengths, "lengths", x, (s.B,), torch.int32), _like(y, "out", x, (s.B, s.T, s.D), x.dtype),
+        _like(last, "out", x, ends, x.dtype), _current(x)), "pararnn_causal_conv")
+    return y, last
+
+
+def causal_conv_backward(x, weight, dy, bias=None, *, act: str = "silu", state=None, dlast=None, lengths=None,
+                         workspace=None, stream=None) -> dict:
+    """The backward pass of ``causal_conv``: dy [B,T,D] = dL/dy (x's type,
+    strided as x), dlast [B,W-1,D] the gradient of the last inputs (zero if
+    None); the rest as given to the forward pass.  Returns dict(dx, dweight,
+    dbias, dstate); dbias and dstate are None where there was no bias or state."""
+    under = _context(x, stream)
+    if under is not None:
+        with under:
+            return causal_conv_backward(x, weight, dy, bias, act=act, state=state, dlast=dlast, lengths=lengths,
+                                        workspace=workspace)
+    s = _conv_shape(x, weight, act)
+    rows, ends, f32 = (s.B, s.T, s.D), (s.B, s.W - 1, s.D), torch.float32
+    px, pdy = _plain_rows(x, "x", x, rows), _plain_rows(dy, "dy", x, rows)
+    ptr = lambda t: None if t is None else t.data_ptr()
+    g = dict(dx=x.new_empty(rows), dweight=weight.new_empty((s.D, s.W)),
+             dbias=None if bias is None else bias.new_empty((s.D,)), dstate=None if state is None else x.new_empty(ends))
+    L = lib()
+    ws, ws_at, ws_bytes = _workspace(L.pararnn_causal_conv_backward_workspace_size(s), "pararnn_causal_conv_backward",
+                                       workspace, x.device)
+    _checked(L.pararnn_causal_conv_backward(
+        s, px, _like(weight, "weight", x, (s.D, s.W), f32), _like(bias, "bias", x, (s.D,), f32), pdy,
+        _like(state, "state", x, ends, x.dtype), _like(dlast, "dlast", x, ends, x.dtype),
+        _like(lengths, "lengths", x, (s.B,), torch.int32), g["dx"].data_ptr(), g["dweight"].data_ptr(), ptr(g["dbias"]),
+        ptr(g["dstate"]), ws_at, ws_bytes, _current(x)), "pararnn_causal_conv_backward")
+    return g
+
+
+def causal_conv_step(x, weight, state, bias=None, *, act: str = "silu", slots=None, out_state=None, out=None, stream=None):
+    """One token of every sequence through ``causal_conv``: x [B,D]; state
+    [n,W-1,D] of x's type holds the last inputs, row b's at slots[b] (as in
+    ``selective_scan_step``), or at b if None (n = B).  They move up by one and
+    go to ``out_state``, or replace those in ``state`` if None.  Returns y
+    [B,D].  Records no graph, as ``causal_conv``."""
+    under = _context(x, stream)
+    if under is not None:
+        with under:
+            return causal_conv_step(x, weight, state, bias, act=act, slots=slots, out_state=out_state, out=out)
+    if _wants_grad(x, weight, bias, state):
+        _no_graph("causal_conv_step")
+    n = _pool(state, 3, "[n, W - 1, D]", slots, x)
+    s = _conv_shape(x, weight, act, 2)
+    if out is None:
+        out = x.new_empty((s.B, s.D))
+    pool, f32 = (n, s.W - 1, s.D), torch.float32
+    src = _like(state, "state", x, pool, x.dtype)
+    _checked(lib().pararnn_causal_conv_step(
+        s, _plain_rows(x, "x", x, (s.B, s.D)), _like(weight, "weight", x, (s.D, s.W), f32),
+        _like(bias, "bias", x, (s.D,), f32), src, _like(slots, "slots", x, (s.B,), torch.int32), n,
+        _like(out, "out", x, (s.B, s.D), x.dtype),
+        src if out_state is None else _like(out_state, "out_state", x, pool, x.dtype), _current(x)),
+        "pararnn_causal_conv_step")
+    return out
+
+
+def _stream_shape(x, rms, eps, x_dtype, r_dtype, y_dtype):
+    if x.dim() < 2:
+        raise ValueError("rows must be [N, ..., C]")
+    N, C = x.shape[0], x.shape[-1]
+    S = 1
+    for n in x.shape[1:-1]:
+        S *= n
+    if min(N, S, C) < 1:
+        raise ValueError(f"rows must not be empty: {tuple(x.shape)}")
+    if max(N, S, C) >= _INT:
+        raise ValueError(f"the rows' first, middle and last axes must be below 2**31: got {N}, {S} and {C}")
+    shape = StreamShape(N, S, C, _dtype_code(x_dtype), _dtype_code(r_dtype), _dtype_code(y_dtype), 1 if rms else 0, eps)
+    if not x.is_cuda:
+        raise ValueError("rows must be a CUDA tensor")
+    return shape
+
+
+def layer_norm(x, weight=None, bias=None, *, residual=None, rms: bool = False, eps: float = 1e-5, lengths=None,
+               out_dtype=None, out=None, stream=None):
+    """A block's entry: the branch x is added to the residual stream and the
+    sum's rows are normalised: r = residual + x, y = (r - mean) / sqrt(mean
+    (r - mean)^2 + eps) * weight + bias, without the mean if ``rms``.
+
+    x [N, ..., C] and residual of its shape, each fp32 or bf16, contiguous CUDA;
+    weight, bias [C] fp32; lengths [N] int32: rows behind them (in the middle
+    axes' order) are not read, and zero in y and r.  Returns (y of
+    ``out_dtype``, x's if None; r of residual's type, x itself without one;
+    stats [rows, 2] of x's leading shape, fp32: mean (0 if ``rms``) and
+    1 / sqrt(mean square + eps)).  ``out`` gives y and, with a residual, r (this
+    may be the residual).  Records no graph: operands that require a gradient
+    are taken under ``torch.no_grad()`` only, and ``layer_norm_backward`` has
+    the gradients."""
+    under = _context(x, stream)
+    if under is not None:
+        with under:
+            return layer_norm(x, weight, bias, residual=residual, rms=rms, eps=eps, lengths=lengths, out_dtype=out_dtype,
+                              out=out)
+    if _wants_grad(x, weight, bias, residual):
+        _no_graph("layer_norm")
+    y, r = out if out is not None else (None, None)
+    y_dtype = y.dtype if y is not None else x.dtype if out_dtype is None else out_dtype
+    s = _stream_shape(x, rms, eps, x.dtype, x.dtype if residual is None else residual.dtype, y_dtype)
+    if residual is None:
+        if r is not None:
+            raise ValueError("out has a stream, but there is no residual")
+    elif r is None:
+        r = torch.empty(x.shape, dtype=residual.dtype, device=x.device)
+    if y is None:
+        y = torch.empty(x.shape, dtype=y_dtype, device=x.device)
+    stats = torch.empty((*x.shape[:-1], 2), dtype=torch.float32, device=x.device)
+    f32, rd = torch.float32, x.dtype if residual is None else residual.dtype
+    _checked(lib().pararnn_layer_norm(
+        s, _like(x, "x", x, x.shape, x.dtype), _like(residual, "residual", x, x.shape, rd),
+        _like(weight, "weight", x, (s.C,), f32), _like(bias, "bias", x, (s.C,), f32),
+        _like(lengths, "lengths", x, (s.N,), torch.int32), _like(y, "out", x, x.shape, y_dtype),
+        _like(r, "out", x, x.shape, rd), stats.data_ptr(), _current(x)), "pararnn_layer_norm")
+    return y, x if residual is None else r, stats
+
+
+def layer_norm_backward(r, stats, dy, weight=None, bias=None, *, dr=None, rms: bool = False, lengths=None, dx_dtype=None,
+                        workspace=None, stream=None) -> dict:
+    """The backward pass of ``layer_norm`` from dy [N, ..., C] = dL/dy (y's
+    type), the stream r and the forward's stats; dr [N, ..., C] of r's type is
+    the gradient that reaches r from behind (zero if None); the rest as given to
+    the forward pass.  Returns dict(dr, dx, dweight, dbias): dr is the gradient
+    of the sum, so of the residual, in r's type, dx the same in the branch's
+    (``dx_dtype``; dr itself where they are equal or it is None); dweight and
+    dbias are None where there was no weight or bias."""
+    under = _context(r, stream)
+    if under is not None:
+        with under:
+            return layer_norm_backward(r, stats, dy, weight, bias, dr=dr, rms=rms, lengths=lengths, dx_dtype=dx_dtype,
+                                       workspace=workspace)
+    dx_dtype = r.dtype if dx_dtype is None else dx_dtype
+    s = _stream_shape(r, rms, 0.0, dx_dtype, r.dtype, dy.dtype)
+    f32, channels = torch.float32, (s.C,)
+    new = lambda t: None if t is None else torch.empty_like(t)
+    ptr = lambda t: None if t is None else t.data_ptr()
+    pr, pw = _like(r, "r", r, r.shape, r.dtype), _like(weight, "weight", r, channels, f32)
+    _like(bias, "bias", r, channels, f32)
+    g = dict(dr=torch.empty_like(r), dx=None, dweight=new(weight), dbias=new(bias))
+    g["dx"] = g["dr"] if dx_dtype == r.dtype else torch.empty(r.shape, dtype=dx_dtype, device=r.device)
+    L = lib()
+    ws, ws_at, ws_bytes = _workspace(L.pararnn_layer_norm_backward_workspace_size(s), "pararnn_layer_norm_backward",
+                                       workspace, r.device)
+    _checked(L.pararnn_layer_norm_backward(
+        s, pr, _like(stats, "stats", r, (*r.shape[:-1], 2), f32), _like(dy, "dy", r, r.shape, dy.dtype), pw,
+        _like(dr, "dr", r, r.shape, r.dtype), _like(lengths, "lengths", r, (s.N,), torch.int32), g["dr"].data_ptr(),
+        None if dx_dtype == r.dtype else g["dx"].data_ptr(), ptr(g["dweight"]), ptr(g["dbias"]), ws_at, ws_bytes,
+        _current(r)), "pararnn_layer_norm_backward")
     return g
