@@ -9,27 +9,29 @@ using namespace ss;
 namespace {
 
 constexpr int kThr = 128;
-constexpr int kS = 4;     // states of a thread
-constexpr int kTC = 16;   // tokens between two barriers
+constexpr int tokens_of(int L) { return L >= 4 ? 16 : 8; }  // between two barriers
 
 enum Pass { kOutputs, kSums, kStates, kReverseSums };
 
-// One CTA: kThr / L channels of one group, one segment of one sequence; L lanes of four states each hold a channel.
-// Tokens come in chunks of kTC: between two barriers every thread prepares (token, channel) pairs for all (s and s x, by
-// element loads that ask nothing of strides or alignment, along the channels so that they coalesce), then runs its states
-// through the chunk.
+// One CTA: 2 kThr / L channels of one group, one segment of one sequence.  A thread holds S states of each of two channels,
+// so that what it reads of b and c from shared memory serves both (every lane's bytes count there, the same address or
+// not: with one channel to a thread these reads took as long as the arithmetic); L lanes share the two channels.  Tokens
+// come in chunks of TC: between two barriers the threads prepare (token, channel pair)s for all (s and s x; VEC: pairs,
+// and quads of b and c, lie on their own alignment), then each runs its states through the chunk; the next chunk's
+// elements are on their way meanwhile, and y's parts meet in shared memory.
 //   kOutputs      from the start state: y, the kept states, and the last segment's last state
 //   kStates       from the start state: the kept states alone
 //   kSums         from zero: the segment's last state and sum of s
 //   kReverseSums  from zero, backward in time: P before the segment
-template <typename T, int L, Pass PASS>
+template <typename T, int S, int L, Pass PASS, bool VEC>
 __global__ void __launch_bounds__(kThr) ss_sweep_kernel(const SsArgs w) {
-    constexpr int CH = kThr / L, NP = kS * L, PER = kTC / L;  // PER: tokens that a thread prepares per chunk
+    constexpr int TC = tokens_of(L), CH = 2 * kThr / L, NP = S * L, Q = S / 2;  // Q pairs of states
+    constexpr int LT = kThr / (CH / 2), PER = (TC + LT - 1) / LT;  // threads along the tokens, and tokens of each, in preparing
     constexpr bool OUT = PASS == kOutputs, REV = PASS == kReverseSums, SUMS = PASS == kSums || REV;
-    __shared__ float4 s_du[kTC][CH];                       // s, s, s x, s x (REV: v, v)
-    __shared__ __align__(16) float s_b[kTC][NP], s_c[OUT ? kTC : 1][NP];
-    __shared__ __align__(16) float s_y[OUT ? kTC : 1][kThr];
-    __shared__ float s_sum[SUMS ? kThr : 1];
+    __shared__ float4 s_du[TC][CH / 2];  // s and s x of two channels (REV: s and v)
+    __shared__ __align__(16) float s_b[TC][NP], s_c[OUT ? TC : 1][NP];
+    __shared__ __align__(16) float2 s_y[OUT ? TC : 1][kThr];
+    __shared__ u64 s_sum[SUMS ? kThr : 1];
 
     const int tid = threadIdx.x, per = w.D / w.G;
     const int tiles = (per + CH - 1) / CH, blocks = tiles * w.G;
@@ -39,143 +41,209 @@ __global__ void __launch_bounds__(kThr) ss_sweep_kernel(const SsArgs w) {
     const int t_first = seg * w.seg, t_end = min(w.T, t_first + w.seg), t_len = min(t_end, len);
 
     // as owner of states
-    const int ch = tid / L, n0 = tid % L * kS, d = g * per + tile * CH + ch;
-    const bool owner = tile * CH + ch < per;
+    const int pair = tid / L, n0 = tid % L * S, d = g * per + tile * CH + 2 * pair;
+    const int owns = min(2, max(0, per - tile * CH - 2 * pair));
     const bool vec = w.N % 4 == 0;
     const long long state_at = (static_cast<long long>(b) * w.D + d) * w.N;
     const long long all = static_cast<long long>(w.B) * w.D * w.N;
-    u64 h[2] = {0, 0}, a[2] = {0, 0};
-    if (owner) {
-        load_states(a, w.a + static_cast<long long>(d) * w.N, n0, w.N, false);
+    u64 h[2][Q] = {};
+    float a[2][S] = {};
 #pragma unroll
-        for (int i = 0; i < 2; ++i) a[i] = mul2(a[i], splat(kLog2eF));
+    for (int q = 0; q < 2; ++q) {
+        if (q >= owns) continue;
+#pragma unroll
+        for (int i = 0; i < S; ++i)
+            if (n0 + i < w.N) a[q][i] = w.a[(static_cast<long long>(d) + q) * w.N + n0 + i] * kLog2eF;
         if (!SUMS) {
             const float *from = w.n_seg > 1 ? w.seg_state + seg * all : w.h0;
-            if (from != nullptr) load_states(h, from + state_at, n0, w.N, false);
+            if (from != nullptr) load_states(h[q], from + state_at + q * w.N, n0, w.N, false);
         }
     }
-    // as the one who prepares tokens t0 + lt + i L of channel lch
-    const int lch = tid % CH, lt = tid / CH, ld = g * per + tile * CH + lch;
-    const bool loads = tile * CH + lch < per;
-    const float bias = loads && w.dt_bias != nullptr ? w.dt_bias[ld] : 0.f;
-    const float skip = OUT && loads && w.skip != nullptr ? w.skip[ld] : 0.f;
+    // as the one who prepares and finishes tokens t0 + lt + i LT of the channels lc and lc + 1
+    const int lc = tid % (CH / 2) * 2, lt = tid / (CH / 2), ld = g * per + tile * CH + lc;
+    const int have = min(2, max(0, per - tile * CH - lc));
+    float bias[2] = {}, skip[2] = {};
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        if (q < have && w.dt_bias != nullptr) bias[q] = w.dt_bias[ld + q];
+        if (OUT && q < have && w.skip != nullptr) skip[q] = w.skip[ld + q];
+    }
     const bool gated = w.gate.p != nullptr;
-    const T *px = static_cast<const T *>(REV ? w.dy.p : w.x.p) + b * (REV ? w.dy.sb : w.x.sb) + ld;
-    const long long stx = REV ? w.dy.st : w.x.st;
-    const T *pdt = static_cast<const T *>(w.dt.p) + b * w.dt.sb + ld;
-    const T *pg = static_cast<const T *>(w.gate.p) + b * w.gate.sb + ld;
-    const SsRows &rb = REV ? w.c : w.b;
-    const T *pb = static_cast<const T *>(rb.p) + b * rb.sb + g * rb.sg;
-    const T *pc = static_cast<const T *>(w.c.p) + b * w.c.sb + g * w.c.sg;
-    constexpr int NB = kTC * NP / kThr;  // elements of b that a thread brings per chunk (kS * kTC * L / kThr)
-    constexpr int NBE = NB > 0 ? NB : 1;
+    const SsRows &rx = REV ? w.dy : w.x, &rb = REV ? w.c : w.b;
+    const int n_chunk = (max(t_len - t_first, 0) + TC - 1) / TC;
+    const int t_start = t_first + (REV ? max(n_chunk - 1, 0) * TC : 0);  // the chunks go on from here, TC tokens at a time
+    constexpr int STEP = REV ? -TC : TC;
+    // where this thread's next elements are
+    const T *px = static_cast<const T *>(rx.p) + b * rx.sb + ld + (t_start + lt) * rx.st;
+    const T *pdt = static_cast<const T *>(w.dt.p) + b * w.dt.sb + ld + (t_start + lt) * w.dt.st;
+    const T *pg = static_cast<const T *>(w.gate.p) + b * w.gate.sb + ld + (t_start + lt) * w.gate.st;
+    constexpr int BW = VEC ? 4 : 1, BROW = NP / BW, NB = (TC * BROW + kThr - 1) / kThr;  // of b and c, BW at a time
+    const int bt = tid / BROW, bn = tid % BROW * BW;
+    const T *pb = static_cast<const T *>(rb.p) + b * rb.sb + g * rb.sg + (t_start + bt) * rb.st + bn;
+    const T *pc = static_cast<const T *>(w.c.p) + b * w.c.sb + g * w.c.sg + (t_start + bt) * w.c.st + bn;
 
-    float nx[PER], ndt[PER], ng[PER], cx[PER], cg[PER], nb[NBE], nc[NBE], sum = 0.f;
+    Raw<T> nx[PER], ndt[PER], ng[PER], cx[PER], cg[PER];
+    RawN<T, BW> nb[NB], nc[NB];
+    u64 sum = 0;
     auto fetch = [&](int t0) {
+        const int left = t_len - t0;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int t = t0 + lt + i * L;
-            const bool on = loads && t < t_len;
-            nx[i] = on ? to_f(px[t * stx]) : 0.f;
-            ndt[i] = on ? to_f(pdt[t * w.dt.st]) : 0.f;
-            if (OUT || REV) ng[i] = on && gated ? to_f(pg[t * w.gate.st]) : 0.f;
+            const int t = lt + i * LT, n = t < TC && t < left ? have : 0;
+            nx[i] = load_raw<VEC>(px + i * LT * rx.st, n);
+            ndt[i] = load_raw<VEC>(pdt + i * LT * w.dt.st, n);
+            if (OUT || REV) ng[i] = load_raw<VEC>(pg + i * LT * w.gate.st, gated ? n : 0);
         }
+        px += STEP * rx.st, pdt += STEP * w.dt.st, pg += STEP * w.gate.st;
 #pragma unroll
-        for (int i = 0; i < NBE; ++i) {
-            const int e = tid + i * kThr, t = t0 + e / NP, n = e % NP;
-            const bool on = e < kTC * NP && n < w.N && t < t_len;
-            nb[i] = on ? to_f(pb[t * rb.st + n]) : 0.f;
-            if (OUT) nc[i] = on ? to_f(pc[t * w.c.st + n]) : 0.f;
+        for (int i = 0; i < NB; ++i) {
+            const int t = bt + i * (kThr / BROW);
+            const bool on = t < TC && t < left && bn < w.N;
+            nb[i] = load_n<BW>(pb + i * (kThr / BROW) * rb.st, on);
+            if (OUT) nc[i] = load_n<BW>(pc + i * (kThr / BROW) * w.c.st, on);
         }
+        pb += STEP * rb.st, pc += STEP * w.c.st;
     };
+    // (each step for all of the thread's tokens before the next step: chains of dependent operations side by side)
     auto stage = [&](int t0) {
+        float st[PER][2], u[PER][2];
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int t = lt + i * L;
-            float s = 0.f, u = 0.f;
-            if (loads && t0 + t < t_len) {
-                s = ndt[i] + bias;
-                if (w.softplus) s = softplus(s);
-                if (REV) u = gated ? gate_with(nx[i], ng[i]) : nx[i];
-                else u = s * nx[i];
+            upk(value(ndt[i]), st[i][0], st[i][1]);
+            st[i][0] += bias[0], st[i][1] += bias[1];
+        }
+        if (w.softplus) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) st[i][0] = softplus(st[i][0]), st[i][1] = softplus(st[i][1]);
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const bool on = t0 + lt + i * LT < t_len;
+            st[i][0] = on ? st[i][0] : 0.f, st[i][1] = on ? st[i][1] : 0.f;
+            upk(value(nx[i]), u[i][0], u[i][1]);
+            if (!REV) u[i][0] *= st[i][0], u[i][1] *= st[i][1];
+        }
+        if (REV && gated) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                float z[2];
+                upk(value(ng[i]), z[0], z[1]);
+                u[i][0] = gate_with(u[i][0], z[0]), u[i][1] = gate_with(u[i][1], z[1]);
             }
-            s_du[t][lch] = make_float4(s, s, u, u);
-            if (SUMS) sum += s;
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int t = lt + i * LT;
+            if (t < TC) {
+                s_du[t][lc / 2] = make_float4(st[i][0], st[i][1], u[i][0], u[i][1]);
+                if (SUMS) sum = add2(sum, pk(st[i][0], st[i][1]));
+            }
             cx[i] = nx[i], cg[i] = ng[i];
         }
 #pragma unroll
-        for (int i = 0; i < NBE; ++i) {
-            const int e = tid + i * kThr;
-            if (e < kTC * NP) {
-                s_b[e / NP][e % NP] = nb[i];
-                if (OUT) s_c[e / NP][e % NP] = nc[i];
+        for (int i = 0; i < NB; ++i) {
+            const int t = bt + i * (kThr / BROW);
+            if (t < TC) {
+                store_n(&s_b[t][bn], nb[i]);
+                if (OUT) store_n(&s_c[t][bn], nc[i]);
             }
         }
     };
 
-    const int n_chunk = (max(t_len - t_first, 0) + kTC - 1) / kTC;
-    auto chunk_at = [&](int k) { return t_first + (REV ? n_chunk - 1 - k : k) * kTC; };
+    T *py = static_cast<T *>(w.y) + (static_cast<long long>(b) * w.T + t_start + lt) * w.D + ld;
     if (n_chunk > 0) {
-        fetch(chunk_at(0));
-        stage(chunk_at(0));
+        fetch(t_start);
+        stage(t_start);
     }
-    for (int k = 0; k < n_chunk; ++k) {
-        const int t0 = chunk_at(k);
+    for (int k = 0, t0 = t_start; k < n_chunk; ++k, t0 += STEP) {
         __syncthreads();
-        if (k + 1 < n_chunk) fetch(chunk_at(k + 1));
-#pragma unroll 4
-        for (int j = 0; j < kTC; ++j) {
-            const int t = REV ? kTC - 1 - j : j;
-            if (!SUMS && (j & (kSsKeep - 1)) == 0 && w.kept != nullptr && owner && t0 + t < t_len)
-                store_states(h, w.kept + ((static_cast<long long>(b) * ((w.T + kSsKeep - 1) / kSsKeep) +
-                                           (t0 + t) / kSsKeep) * w.D + d) * w.N, n0, w.N, vec);
-            const ulonglong2 du = *reinterpret_cast<const ulonglong2 *>(&s_du[t][ch]);
-            u64 bb[2], cc[2], y = 0;
-            load_pairs(bb, &s_b[t][n0]);
-            if (OUT) load_pairs(cc, &s_c[t][n0]);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const u64 e = decay_less_one(mul2(du.x, a[i]));
-                if (REV) {
-                    h[i] = fma2(du.y, bb[i], h[i]);
-                    h[i] = fma2(e, h[i], h[i]);
-                } else {
-                    h[i] = fma2(e, h[i], fma2(du.y, bb[i], h[i]));
-                }
-                if (OUT) y = fma2(cc[i], h[i], y);
+        if (k + 1 < n_chunk) fetch(t0 + STEP);
+#pragma unroll 1
+        for (int j0 = 0; j0 < TC; j0 += kSsKeep) {
+            if (!SUMS && w.kept != nullptr && t0 + j0 < t_len) {
+                float *to = w.kept + ((static_cast<long long>(b) * ((w.T + kSsKeep - 1) / kSsKeep) + (t0 + j0) / kSsKeep) *
+                                          w.D + d) * w.N;
+                if (owns > 0) store_states(h[0], to, n0, w.N, vec);
+                if (owns > 1) store_states(h[1], to + w.N, n0, w.N, vec);
             }
-            if (OUT) s_y[t][tid] = pair_sum(y);
+#pragma unroll
+            for (int j = 0; j < kSsKeep; ++j) {
+                const int t = REV ? TC - 1 - j0 - j : j0 + j;
+                const float4 du = s_du[t][pair];
+                u64 bb[Q], cc[Q];
+                float y[2];
+                load_pairs(bb, &s_b[t][n0]);
+                if (OUT) load_pairs(cc, &s_c[t][n0]);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const float st = q == 0 ? du.x : du.y, u = q == 0 ? du.z : du.w;
+                    u64 part = 0;
+#pragma unroll
+                    for (int i = 0; i < Q; ++i) {
+                        const u64 e = decay_less_one(pk(st * a[q][2 * i], st * a[q][2 * i + 1]));
+                        // one factor for both of a pair: two instructions, as moving it beside itself would take
+                        float b0, b1, h0, h1;
+                        upk(bb[i], b0, b1), upk(h[q][i], h0, h1);
+                        const u64 moved = pk(fmaf(u, b0, h0), fmaf(u, b1, h1));
+                        h[q][i] = REV ? fma2(e, moved, moved) : fma2(e, h[q][i], moved);
+                        if (OUT) part = i == 0 ? mul2(cc[i], h[q][i]) : fma2(cc[i], h[q][i], part);
+                    }
+                    if (OUT) y[q] = pair_sum(part);
+                }
+                if (OUT) s_y[t][tid] = make_float2(y[0], y[1]);
+            }
         }
         __syncthreads();
         if (OUT) {
-            T *py = static_cast<T *>(w.y) + (static_cast<long long>(b) * w.T + t0) * w.D + ld;
+            float y[PER][2];
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                const int t = lt + i * L;
-                float y = 0.f;
+                float part[2 * L], v[2];
+                upk(value(cx[i]), v[0], v[1]);
+                load_floats<2 * L>(part, &s_y[min(lt + i * LT, TC - 1)][lc / 2 * L].x);
 #pragma unroll
-                for (int j = 0; j < L; ++j) y += s_y[t][lch * L + j];
-                y = fmaf(skip, cx[i], y);
-                if (gated) y = gate_with(y, cg[i]);
-                if (loads && t0 + t < t_len) py[static_cast<long long>(t) * w.D] = from_f<T>(y);
+                for (int q = 1; q < L; ++q) part[0] += part[2 * q], part[1] += part[2 * q + 1];
+                y[i][0] = fmaf(skip[0], v[0], part[0]), y[i][1] = fmaf(skip[1], v[1], part[1]);
             }
+            if (gated) {
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    float z[2];
+                    upk(value(cg[i]), z[0], z[1]);
+                    y[i][0] = gate_with(y[i][0], z[0]), y[i][1] = gate_with(y[i][1], z[1]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int t = lt + i * LT;
+                store_pair<VEC>(py + static_cast<long long>(i * LT) * w.D, pk(y[i][0], y[i][1]),
+                                t < TC && t0 + t < t_len ? have : 0);
+            }
+            py += static_cast<long long>(TC) * w.D;
         }
-        if (k + 1 < n_chunk) stage(chunk_at(k + 1));
+        if (k + 1 < n_chunk) stage(t0 + STEP);
     }
-    if (OUT && loads) {  // nothing stands behind a sequence
+    if (OUT) {  // nothing stands behind a sequence
         T *py = static_cast<T *>(w.y) + static_cast<long long>(b) * w.T * w.D + ld;
-        for (int t = max(t_len, t_first) + lt; t < t_end; t += L) py[static_cast<long long>(t) * w.D] = from_f<T>(0.f);
+        for (int t = max(t_len, t_first) + lt; t < t_end; t += LT) store_pair<VEC>(py + static_cast<long long>(t) * w.D, 0ull, have);
     }
-    if (OUT && seg == w.n_seg - 1 && owner) store_states(h, w.h + state_at, n0, w.N, false);
+    float *last = SUMS ? (REV ? w.rev_state : w.seg_state) + seg * all : w.h;
+    if (SUMS || (OUT && seg == w.n_seg - 1)) {
+        if (owns > 0) store_states(h[0], last + state_at, n0, w.N, false);
+        if (owns > 1) store_states(h[1], last + state_at + w.N, n0, w.N, false);
+    }
     if (SUMS) {
-        if (owner) store_states(h, (REV ? w.rev_state : w.seg_state) + seg * all + state_at, n0, w.N, false);
         s_sum[tid] = sum;
         __syncthreads();
-        if (tid < CH && tile * CH + tid < per) {
-            float s = 0.f;
+        if (tid < CH / 2) {
+            u64 s = 0;
 #pragma unroll
-            for (int i = 0; i < L; ++i) s += s_sum[tid + i * CH];
-            w.seg_dt[(static_cast<long long>(seg) * w.B + b) * w.D + g * per + tile * CH + tid] = s;
+            for (int i = 0; i < LT; ++i) s = add2(s, s_sum[tid + i * (CH / 2)]);
+            float s0, s1;
+            upk(s, s0, s1);
+            float *to = w.seg_dt + (static_cast<long long>(seg) * w.B + b) * w.D + ld;
+            if (have > 0) to[0] = s0;
+            if (have > 1) to[1] = s1;
         }
     }
 }
@@ -199,31 +267,67 @@ __global__ void ss_join_kernel(const SsArgs w) {
     }
 }
 
-template <typename T, int L>
-void launch_sweep(const SsArgs &a, Pass pass, cudaStream_t s) {
-    const int per = a.D / a.G, tiles = (per + kThr / L - 1) / (kThr / L);
-    const unsigned grid = static_cast<unsigned>(tiles) * a.G * a.n_seg * a.B;
-    if (pass == kOutputs) ss_sweep_kernel<T, L, kOutputs><<<grid, kThr, 0, s>>>(a);
-    else if (pass == kSums) ss_sweep_kernel<T, L, kSums><<<grid, kThr, 0, s>>>(a);
-    else if (pass == kStates) ss_sweep_kernel<T, L, kStates><<<grid, kThr, 0, s>>>(a);
-    else ss_sweep_kernel<T, L, kReverseSums><<<grid, kThr, 0, s>>>(a);
+// Lanes of a channel: as many as its states take, four to each, or two where there are too few warps otherwise.
+struct Lanes {
+    int s, l;
+};
+Lanes lanes_of(int N, int s) {
+    int l = 2;
+    while (l * s < N) l *= 2;
+    return {s, l};
+}
+long long ctas(const SsArgs &a, Lanes f) {
+    const int per = a.D / a.G, ch = 2 * kThr / f.l;
+    return static_cast<long long>((per + ch - 1) / ch) * a.G * a.B;
+}
+Lanes lanes_for(const SsArgs &a) {
+    const Lanes four = lanes_of(a.N, 4);
+    return ctas(a, four) * a.n_seg < 148 && a.N > 2 ? lanes_of(a.N, 2) : four;
+}
+// pairs of channels and quads of b and c on their own alignment
+bool pairs_ok(const SsArgs &a) {
+    const size_t e = a.dtype == PARARNN_F32 ? 8 : 4;
+    bool ok = a.D / a.G % 2 == 0 && a.N % 4 == 0;
+    for (const SsRows *r : {&a.b, &a.c})
+        ok = ok && reinterpret_cast<uintptr_t>(r->p) % (2 * e) == 0 && r->sb % 4 == 0 && r->st % 4 == 0 && r->sg % 4 == 0;
+    for (const SsRows *r : {&a.x, &a.dt, &a.gate, &a.dy})
+        ok = ok && reinterpret_cast<uintptr_t>(r->p) % e == 0 && r->sb % 2 == 0 && r->st % 2 == 0;
+    return ok;
 }
 
-int lanes(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
-
-template <typename T>
+template <typename T, int S, int L, bool VEC>
+void launch_sweep(const SsArgs &a, Pass pass, cudaStream_t s) {
+    const unsigned grid = static_cast<unsigned>(ctas(a, {S, L}) * a.n_seg);
+    if (pass == kOutputs) ss_sweep_kernel<T, S, L, kOutputs, VEC><<<grid, kThr, 0, s>>>(a);
+    else if (pass == kSums) ss_sweep_kernel<T, S, L, kSums, VEC><<<grid, kThr, 0, s>>>(a);
+    else if (pass == kStates) ss_sweep_kernel<T, S, L, kStates, VEC><<<grid, kThr, 0, s>>>(a);
+    else ss_sweep_kernel<T, S, L, kReverseSums, VEC><<<grid, kThr, 0, s>>>(a);
+}
+template <typename T, bool VEC>
 void sweep_of(const SsArgs &a, Pass pass, cudaStream_t s) {
-    switch (lanes(a.N)) {
-        case 1: return launch_sweep<T, 1>(a, pass, s);
-        case 2: return launch_sweep<T, 2>(a, pass, s);
-        case 4: return launch_sweep<T, 4>(a, pass, s);
-        case 8: return launch_sweep<T, 8>(a, pass, s);
-        default: return launch_sweep<T, 16>(a, pass, s);
-    }
+    const Lanes f = lanes_for(a);
+#define PARARNN_SS(S_, L_) \
+    if (f.s == S_ && f.l == L_) return launch_sweep<T, S_, L_, VEC>(a, pass, s)
+    PARARNN_SS(4, 2);
+    PARARNN_SS(4, 4);
+    PARARNN_SS(4, 8);
+    PARARNN_SS(4, 16);
+    PARARNN_SS(2, 2);
+    PARARNN_SS(2, 4);
+    PARARNN_SS(2, 8);
+    PARARNN_SS(2, 16);
+    PARARNN_SS(2, 32);
+#undef PARARNN_SS
 }
 cudaError_t sweep(const SsArgs &a, Pass pass, cudaStream_t s) {
-    if (a.dtype == PARARNN_F32) sweep_of<float>(a, pass, s);
-    else sweep_of<__nv_bfloat16>(a, pass, s);
+    const bool vec = pairs_ok(a);
+    if (a.dtype == PARARNN_F32) {
+        if (vec) sweep_of<float, true>(a, pass, s);
+        else sweep_of<float, false>(a, pass, s);
+    } else {
+        if (vec) sweep_of<__nv_bfloat16, true>(a, pass, s);
+        else sweep_of<__nv_bfloat16, false>(a, pass, s);
+    }
     return cudaGetLastError();
 }
 cudaError_t join(const SsArgs &a, bool reverse, cudaStream_t s) {
@@ -240,13 +344,10 @@ cudaError_t start_states(const SsArgs &a, cudaStream_t s) {
 
 }  // namespace
 
-// Segments: as many as it takes to give every scheduler of the card about two warps, of at least 64 tokens each.
+// Segments: as many as it takes to give the card three CTAs per SM, of at least 64 tokens each.
 SsPlan ss_plan(const SsArgs &a, bool) {
-    const int per = a.D / a.G, ch = kThr / lanes(a.N);
-    const long long ctas = static_cast<long long>((per + ch - 1) / ch) * a.G * a.B;
-    long long want = (148 * 2 + ctas - 1) / ctas;
-    if (want < 2) return {1, a.T};
-    want = std::min<long long>(want, (a.T + 63) / 64);
+    const long long have = ctas(a, lanes_of(a.N, a.N > 2 ? 2 : 4));
+    long long want = std::min<long long>((148 * 3 + have - 1) / have, (a.T + 63) / 64);
     if (want < 2) return {1, a.T};
     const int seg = static_cast<int>(((a.T + want - 1) / want + 15) / 16 * 16);
     return {(a.T + seg - 1) / seg, seg};
@@ -354,7 +455,7 @@ void launch_step(const SsStep &w, cudaStream_t s) {
 }
 template <typename T>
 void step_of(const SsStep &w, cudaStream_t s) {
-    switch (lanes(w.N)) {
+    switch (w.N <= 4 ? 1 : lanes_of(w.N, 4).l) {
         case 1: return launch_step<T, 1>(w, s);
         case 2: return launch_step<T, 2>(w, s);
         case 4: return launch_step<T, 4>(w, s);

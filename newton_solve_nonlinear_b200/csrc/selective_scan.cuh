@@ -86,21 +86,157 @@ __device__ __forceinline__ int row_count(const int *lengths, int b, int T) {
     return n < 0 ? 0 : (n > T ? T : n);
 }
 
-__device__ __forceinline__ float softplus(float v) { return v > 20.f ? v : log1pf(expf(v)); }
-__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + expf(-v)); }
-__device__ __forceinline__ float gate_with(float y, float z) { return y * (z * sigmoid(z)); }
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN where either is
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+// exp(v), |v| at most 150: ex2 of v log2(e) rounded, times what that rounding left out.  (One value at a time: a constant
+// of a packed operation takes two registers and two instructions to fill them.)
+__device__ __forceinline__ float exp_of(float v) {
+    const float t = v * kLog2eF, rest = fmaf(v, kLog2eF, -t);
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+    return fmaf(e, rest * 0.693147181f, e);
+}
+// log(1 + exp(v)) = max(v, 0) + log(1 + e), e = exp(-|v|) in (0, 1]; log(1 + e) / e is a polynomial fitted for the smallest
+// largest relative error on [0, 1], 1.6e-7 as evaluated.  -inf gives 0, as the limit does.
+__device__ __forceinline__ float softplus(float v) {
+    const float e = exp_of(max_nan(-fabsf(v), -150.f));
+    float p = fmaf(0.00523268804f, e, -0.0295052137f);
+    p = fmaf(p, e, 0.0782259107f);
+    p = fmaf(p, e, -0.136632428f);
+    p = fmaf(p, e, 0.191060051f);
+    p = fmaf(p, e, -0.24842982f);
+    p = fmaf(p, e, 0.333190978f);
+    p = fmaf(p, e, -0.499994934f);
+    p = fmaf(p, e, 0.99999994f);
+    return fmaf(p, e, max_nan(v, 0.f));
+}
+// 1 / (1 + exp(-z))
+__device__ __forceinline__ float sigmoid_of(float z) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + exp_of(min_nan(max_nan(-z, -80.f), 80.f))));
+    return r;
+}
+__device__ __forceinline__ float gate_with(float y, float z) { return y * (z * sigmoid_of(z)); }
+
+// Two neighbouring channels' elements, as they lie in memory: fetched long before they are used.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<__nv_bfloat16> {
+    unsigned v;
+};
+template <>
+struct Raw<float> {
+    u64 v;
+};
+// VEC: both exist and are aligned as a pair; n of them exist
+template <bool VEC>
+__device__ __forceinline__ Raw<__nv_bfloat16> load_raw(const __nv_bfloat16 *p, int n) {
+    if constexpr (VEC) return {n > 0 ? *reinterpret_cast<const unsigned *>(p) : 0u};
+    const unsigned short *q = reinterpret_cast<const unsigned short *>(p);
+    return {(n > 0 ? q[0] : 0u) | (n > 1 ? static_cast<unsigned>(q[1]) << 16 : 0u)};
+}
+template <bool VEC>
+__device__ __forceinline__ Raw<float> load_raw(const float *p, int n) {
+    if constexpr (VEC) return {n > 0 ? *reinterpret_cast<const u64 *>(p) : 0ull};
+    return {pk(n > 0 ? p[0] : 0.f, n > 1 ? p[1] : 0.f)};
+}
+// the same of one or four elements of b or c
+template <typename T, int W>
+struct RawN;
+template <>
+struct RawN<__nv_bfloat16, 1> {
+    unsigned short v;
+};
+template <>
+struct RawN<__nv_bfloat16, 4> {
+    uint2 v;
+};
+template <>
+struct RawN<float, 1> {
+    float v;
+};
+template <>
+struct RawN<float, 4> {
+    float4 v;
+};
+template <int W, typename T>
+__device__ __forceinline__ RawN<T, W> load_n(const T *p, bool on) {
+    RawN<T, W> r{};
+    if (on) r = *reinterpret_cast<const RawN<T, W> *>(p);
+    return r;
+}
+__device__ __forceinline__ void store_n(float *p, RawN<__nv_bfloat16, 1> r) {
+    *p = __uint_as_float(static_cast<unsigned>(r.v) << 16);
+}
+__device__ __forceinline__ void store_n(float *p, RawN<__nv_bfloat16, 4> r) {
+    *reinterpret_cast<float4 *>(p) = make_float4(__uint_as_float(r.v.x << 16), __uint_as_float(r.v.x & 0xffff0000u),
+                                                 __uint_as_float(r.v.y << 16), __uint_as_float(r.v.y & 0xffff0000u));
+}
+__device__ __forceinline__ void store_n(float *p, RawN<float, 1> r) { *p = r.v; }
+__device__ __forceinline__ void store_n(float *p, RawN<float, 4> r) { *reinterpret_cast<float4 *>(p) = r.v; }
+template <int N>
+__device__ __forceinline__ void load_floats(float (&v)[N], const float *p) {
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const float4 q = *reinterpret_cast<const float4 *>(p + i);
+            v[i] = q.x, v[i + 1] = q.y, v[i + 2] = q.z, v[i + 3] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            const float2 q = *reinterpret_cast<const float2 *>(p + i);
+            v[i] = q.x, v[i + 1] = q.y;
+        }
+    }
+}
+__device__ __forceinline__ u64 value(Raw<__nv_bfloat16> r) {
+    return pk(__uint_as_float(r.v << 16), __uint_as_float(r.v & 0xffff0000u));
+}
+__device__ __forceinline__ u64 value(Raw<float> r) { return r.v; }
+template <bool VEC>
+__device__ __forceinline__ void store_pair(__nv_bfloat16 *p, u64 v, int n) {
+    float a, b;
+    upk(v, a, b);
+    const __nv_bfloat162 q = __floats2bfloat162_rn(a, b);
+    if constexpr (VEC) {
+        if (n > 0) *reinterpret_cast<__nv_bfloat162 *>(p) = q;
+    } else {
+        if (n > 0) p[0] = q.x;
+        if (n > 1) p[1] = q.y;
+    }
+}
+template <bool VEC>
+__device__ __forceinline__ void store_pair(float *p, u64 v, int n) {
+    if constexpr (VEC) {
+        if (n > 0) *reinterpret_cast<u64 *>(p) = v;
+    } else {
+        float a, b;
+        upk(v, a, b);
+        if (n > 0) p[0] = a;
+        if (n > 1) p[1] = b;
+    }
+}
 
 // exp(s a) - 1 for a pair of states, from x = s a log2(e).  The state is updated as h + (exp(s a) - 1) h: rounded to fp32,
 // exp(s a) of a slow decay would be another decay, taken at every token.  Near zero the difference comes from its series
-// (the first term left out is below (ln 2 / 16)^4 / 120 = 3e-8 of it), further away from ex2, whose 1.3e-7 is then below
-// 3e-6 of it.
+// (the first term left out is (ln 2 / 64)^3 / 24 = 5e-8 of it), further away from ex2, whose 1.3e-7 counts for no more than
+// the 92 tokens that such a state remembers.
 __device__ __forceinline__ u64 decay_less_one(u64 x) {
-    const u64 p = mul2(x, fma2(x, fma2(x, fma2(x, splat(0.00961812910f), splat(0.0555041087f)), splat(0.240226507f)),
-                               splat(0.693147181f)));
+    const u64 p = mul2(x, fma2(x, fma2(x, splat(0.0555041087f), splat(0.240226507f)), splat(0.693147181f)));
     const u64 e = add2(ex2_2(x), splat(-1.f));
     float x0, x1, p0, p1, e0, e1;
     upk(x, x0, x1), upk(p, p0, p1), upk(e, e0, e1);
-    return pk(fabsf(x0) < 0.0625f ? p0 : e0, fabsf(x1) < 0.0625f ? p1 : e1);
+    return pk(fabsf(x0) < 0.015625f ? p0 : e0, fabsf(x1) < 0.015625f ? p1 : e1);
 }
 
 template <int PAIRS>
@@ -119,9 +255,9 @@ __device__ __forceinline__ void load_pairs(u64 (&v)[PAIRS], const float *p) {
 // states n0 .. of [.., N] fp32 rows in global memory; zero behind N
 template <int PAIRS>
 __device__ __forceinline__ void load_states(u64 (&v)[PAIRS], const float *p, int n0, int N, bool vec) {
-    if (vec) {
+    if (PAIRS % 2 == 0 && vec) {
 #pragma unroll
-        for (int i = 0; i < PAIRS; i += 2) {
+        for (int i = 0; i + 1 < PAIRS; i += 2) {
             const float4 q = n0 + 2 * i < N ? *reinterpret_cast<const float4 *>(p + n0 + 2 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
             v[i] = pk(q.x, q.y), v[i + 1] = pk(q.z, q.w);
         }
@@ -135,17 +271,18 @@ __device__ __forceinline__ void load_states(u64 (&v)[PAIRS], const float *p, int
 }
 template <int PAIRS>
 __device__ __forceinline__ void store_states(const u64 (&v)[PAIRS], float *p, int n0, int N, bool vec) {
+    if (PAIRS % 2 == 0 && vec) {
 #pragma unroll
-    for (int i = 0; i < PAIRS; i += 2) {
-        float q[4];
-        upk(v[i], q[0], q[1]), upk(v[i + 1], q[2], q[3]);
-        const int n = n0 + 2 * i;
-        if (vec) {
-            if (n < N) *reinterpret_cast<float4 *>(p + n) = make_float4(q[0], q[1], q[2], q[3]);
-        } else {
+        for (int i = 0; i + 1 < PAIRS; i += 2)
+            if (n0 + 2 * i < N) *reinterpret_cast<ulonglong2 *>(p + n0 + 2 * i) = make_ulonglong2(v[i], v[i + 1]);
+    } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (n + j < N) p[n + j] = q[j];
+        for (int i = 0; i < PAIRS; ++i) {
+            float a, b;
+            upk(v[i], a, b);
+            const int n = n0 + 2 * i;
+            if (n < N) p[n] = a;
+            if (n + 1 < N) p[n + 1] = b;
         }
     }
 }

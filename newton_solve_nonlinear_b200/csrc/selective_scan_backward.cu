@@ -201,14 +201,14 @@ __global__ void __launch_bounds__(kThr) ss_backward_kernel(const SsArgs w) {
             const float4 du = s_du[t * CH + lch];
             const float v = s_v[t * CH + lch].x;
             float ds = fmaf(cx[i], e1, e2 * 0.693147181f);
-            if (w.softplus) ds *= sigmoid(cr[i]);
+            if (w.softplus) ds *= sigmoid_of(cr[i]);
             const long long to = out + static_cast<long long>(t) * w.D;
             static_cast<T *>(w.dx)[to] = from_f<T>(fmaf(skip, v, du.x * e1));
             static_cast<T *>(w.ddt)[to] = from_f<T>(ds);
             dskip = fmaf(v, cx[i], dskip);
             dbias += ds;
             if (gated) {
-                const float z = sigmoid(cg[i]), y = fmaf(skip, cx[i], e3);
+                const float z = sigmoid_of(cg[i]), y = fmaf(skip, cx[i], e3);
                 static_cast<T *>(w.dgate)[to] = from_f<T>(cy[i] * y * z * fmaf(cg[i], 1.f - z, 1.f));
             }
         }
