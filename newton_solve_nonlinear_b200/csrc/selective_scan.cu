@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(kThr) ss_sweep_kernel(const SsArgs w) {
     // as owner of states
     const int pair = tid / L, n0 = tid % L * S, d = g * per + tile * CH + 2 * pair;
     const int owns = min(2, max(0, per - tile * CH - 2 * pair));
-    const bool vec = w.N % 4 == 0;
+    const bool vec = w.N % S == 0;
     const long long state_at = (static_cast<long long>(b) * w.D + d) * w.N;
     const long long all = static_cast<long long>(w.B) * w.D * w.N;
     u64 h[2][Q] = {};
@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(kThr) ss_sweep_kernel(const SsArgs w) {
             if (n0 + i < w.N) a[q][i] = w.a[(static_cast<long long>(d) + q) * w.N + n0 + i] * kLog2eF;
         if (!SUMS) {
             const float *from = w.n_seg > 1 ? w.seg_state + seg * all : w.h0;
-            if (from != nullptr) load_states(h[q], from + state_at + q * w.N, n0, w.N, false);
+            if (from != nullptr) load_states(h[q], from + state_at + q * w.N, n0, w.N, vec);
         }
     }
     // as the one who prepares and finishes tokens t0 + lt + i LT of the channels lc and lc + 1
@@ -229,8 +229,8 @@ __global__ void __launch_bounds__(kThr) ss_sweep_kernel(const SsArgs w) {
     }
     float *last = SUMS ? (REV ? w.rev_state : w.seg_state) + seg * all : w.h;
     if (SUMS || (OUT && seg == w.n_seg - 1)) {
-        if (owns > 0) store_states(h[0], last + state_at, n0, w.N, false);
-        if (owns > 1) store_states(h[1], last + state_at + w.N, n0, w.N, false);
+        if (owns > 0) store_states(h[0], last + state_at, n0, w.N, vec);
+        if (owns > 1) store_states(h[1], last + state_at + w.N, n0, w.N, vec);
     }
     if (SUMS) {
         s_sum[tid] = sum;
@@ -284,17 +284,6 @@ Lanes lanes_for(const SsArgs &a) {
     const Lanes four = lanes_of(a.N, 4);
     return ctas(a, four) * a.n_seg < 148 && a.N > 2 ? lanes_of(a.N, 2) : four;
 }
-// pairs of channels and quads of b and c on their own alignment
-bool pairs_ok(const SsArgs &a) {
-    const size_t e = a.dtype == PARARNN_F32 ? 8 : 4;
-    bool ok = a.D / a.G % 2 == 0 && a.N % 4 == 0;
-    for (const SsRows *r : {&a.b, &a.c})
-        ok = ok && reinterpret_cast<uintptr_t>(r->p) % (2 * e) == 0 && r->sb % 4 == 0 && r->st % 4 == 0 && r->sg % 4 == 0;
-    for (const SsRows *r : {&a.x, &a.dt, &a.gate, &a.dy})
-        ok = ok && reinterpret_cast<uintptr_t>(r->p) % e == 0 && r->sb % 2 == 0 && r->st % 2 == 0;
-    return ok;
-}
-
 template <typename T, int S, int L, bool VEC>
 void launch_sweep(const SsArgs &a, Pass pass, cudaStream_t s) {
     const unsigned grid = static_cast<unsigned>(ctas(a, {S, L}) * a.n_seg);
@@ -320,7 +309,7 @@ void sweep_of(const SsArgs &a, Pass pass, cudaStream_t s) {
 #undef PARARNN_SS
 }
 cudaError_t sweep(const SsArgs &a, Pass pass, cudaStream_t s) {
-    const bool vec = pairs_ok(a);
+    const bool vec = ss_pairs_ok(a);
     if (a.dtype == PARARNN_F32) {
         if (vec) sweep_of<float, true>(a, pass, s);
         else sweep_of<float, false>(a, pass, s);
@@ -344,10 +333,22 @@ cudaError_t start_states(const SsArgs &a, cudaStream_t s) {
 
 }  // namespace
 
-// Segments: as many as it takes to give the card three CTAs per SM, of at least 64 tokens each.
+bool ss_pairs_ok(const SsArgs &a) {
+    const size_t e = a.dtype == PARARNN_F32 ? 8 : 4;
+    bool ok = a.D / a.G % 2 == 0 && a.N % 4 == 0;
+    for (const SsRows *r : {&a.b, &a.c})
+        ok = ok && reinterpret_cast<uintptr_t>(r->p) % (2 * e) == 0 && r->sb % 4 == 0 && r->st % 4 == 0 && r->sg % 4 == 0;
+    for (const SsRows *r : {&a.x, &a.dt, &a.gate, &a.dy})
+        ok = ok && reinterpret_cast<uintptr_t>(r->p) % e == 0 && r->sb % 2 == 0 && r->st % 2 == 0;
+    return ok;
+}
+
+
+// Segments: none where two states to a thread fill two thirds of the SMs, since what they cost is a second pass; otherwise as
+// many as it takes to give the card three CTAs per SM, of at least 64 tokens each.
 SsPlan ss_plan(const SsArgs &a, bool) {
-    const long long have = ctas(a, lanes_of(a.N, a.N > 2 ? 2 : 4));
-    long long want = std::min<long long>((148 * 3 + have - 1) / have, (a.T + 63) / 64);
+    const long long most = ctas(a, lanes_of(a.N, a.N > 2 ? 2 : 4)), have = ctas(a, lanes_of(a.N, 4));
+    const long long want = most >= 100 ? 1 : std::min<long long>((148 * 3 + have - 1) / have, (a.T + 63) / 64);
     if (want < 2) return {1, a.T};
     const int seg = static_cast<int>(((a.T + want - 1) / want + 15) / 16 * 16);
     return {(a.T + seg - 1) / seg, seg};

@@ -51,6 +51,7 @@ struct SsPlan {
     int n_seg, seg;
 };
 SsPlan ss_plan(const SsArgs &a, bool backward);
+bool ss_pairs_ok(const SsArgs &a);       // pairs of channels and quads of b and c on their own alignment
 int ss_backward_tiles(const SsArgs &a);  // CTAs along a group's channels in the backward pass
 cudaError_t launch_ss_forward(const SsArgs &a, cudaStream_t s);
 cudaError_t launch_ss_kept(const SsArgs &a, cudaStream_t s);  // the kept states alone
@@ -106,8 +107,12 @@ __device__ __forceinline__ float exp_of(float v) {
 }
 // log(1 + exp(v)) = max(v, 0) + log(1 + e), e = exp(-|v|) in (0, 1]; log(1 + e) / e is a polynomial fitted for the smallest
 // largest relative error on [0, 1], 1.6e-7 as evaluated.  -inf gives 0, as the limit does.
-__device__ __forceinline__ float softplus(float v) {
+// With its slope 1 / (1 + exp(-v)).
+__device__ __forceinline__ float softplus(float v, float &slope) {
     const float e = exp_of(max_nan(-fabsf(v), -150.f));
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    slope = v >= 0.f ? r : e * r;
     float p = fmaf(0.00523268804f, e, -0.0295052137f);
     p = fmaf(p, e, 0.0782259107f);
     p = fmaf(p, e, -0.136632428f);
@@ -117,6 +122,10 @@ __device__ __forceinline__ float softplus(float v) {
     p = fmaf(p, e, -0.499994934f);
     p = fmaf(p, e, 0.99999994f);
     return fmaf(p, e, max_nan(v, 0.f));
+}
+__device__ __forceinline__ float softplus(float v) {
+    float unused;
+    return softplus(v, unused);
 }
 // 1 / (1 + exp(-z))
 __device__ __forceinline__ float sigmoid_of(float z) {
@@ -252,14 +261,20 @@ __device__ __forceinline__ void load_pairs(u64 (&v)[PAIRS], const float *p) {
         for (int i = 0; i < PAIRS; ++i) v[i] = *reinterpret_cast<const u64 *>(p + 2 * i);
     }
 }
-// states n0 .. of [.., N] fp32 rows in global memory; zero behind N
+template <int PAIRS>
+__device__ __forceinline__ void store_pairs(float *p, const u64 (&v)[PAIRS]) {
+    if constexpr (PAIRS == 2) *reinterpret_cast<ulonglong2 *>(p) = make_ulonglong2(v[0], v[1]);
+    else *reinterpret_cast<u64 *>(p) = v[0];
+}
+// states n0 .. of [.., N] fp32 rows in global memory; zero behind N.  vec: the row's start and N are multiples of 2 PAIRS
 template <int PAIRS>
 __device__ __forceinline__ void load_states(u64 (&v)[PAIRS], const float *p, int n0, int N, bool vec) {
-    if (PAIRS % 2 == 0 && vec) {
-#pragma unroll
-        for (int i = 0; i + 1 < PAIRS; i += 2) {
-            const float4 q = n0 + 2 * i < N ? *reinterpret_cast<const float4 *>(p + n0 + 2 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
-            v[i] = pk(q.x, q.y), v[i + 1] = pk(q.z, q.w);
+    if (vec) {
+        if constexpr (PAIRS == 2) {
+            const ulonglong2 q = n0 < N ? *reinterpret_cast<const ulonglong2 *>(p + n0) : make_ulonglong2(0, 0);
+            v[0] = q.x, v[1] = q.y;
+        } else {
+            v[0] = n0 < N ? *reinterpret_cast<const u64 *>(p + n0) : 0ull;
         }
     } else {
 #pragma unroll
@@ -271,10 +286,10 @@ __device__ __forceinline__ void load_states(u64 (&v)[PAIRS], const float *p, int
 }
 template <int PAIRS>
 __device__ __forceinline__ void store_states(const u64 (&v)[PAIRS], float *p, int n0, int N, bool vec) {
-    if (PAIRS % 2 == 0 && vec) {
-#pragma unroll
-        for (int i = 0; i + 1 < PAIRS; i += 2)
-            if (n0 + 2 * i < N) *reinterpret_cast<ulonglong2 *>(p + n0 + 2 * i) = make_ulonglong2(v[i], v[i + 1]);
+    if (vec) {
+        if (n0 >= N) return;
+        if constexpr (PAIRS == 2) *reinterpret_cast<ulonglong2 *>(p + n0) = make_ulonglong2(v[0], v[1]);
+        else *reinterpret_cast<u64 *>(p + n0) = v[0];
     } else {
 #pragma unroll
         for (int i = 0; i < PAIRS; ++i) {

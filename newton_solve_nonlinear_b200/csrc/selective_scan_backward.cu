@@ -9,29 +9,30 @@ namespace {
 constexpr int kThr = 128;
 constexpr int kK = kSsKeep;  // tokens whose states are formed again at a time
 
-template <int L>
-struct Tile {
-    static constexpr int CH = 2 * kThr / L, NP = 4 * L, ROWS = kThr / L;
-    static constexpr int ES = CH + 32 / L;                      // a row of the sums over states, off the banks of the next
-    static constexpr int TS = ROWS * NP + (NP < 32 ? NP : 0);   // a token's sums over channels
-    // floats: s, s, s x, s x and v, v of each token and channel; b and c; sums over states (3); sums over channels (2)
-    static constexpr int FLOATS = kK * CH * 6 + 2 * kK * NP + 3 * kK * L * ES + 2 * kK * TS;
+template <int S, int L>
+struct Smem {
+    static constexpr int CH = 2 * kThr / L, NP = S * L, ROWS = kThr / L;
+    static constexpr int ES = CH + (L < 16 ? 32 / L : 2);      // a row of the sums over states, off the banks of the next
+    static constexpr int TS = ROWS * NP + (NP < 32 ? NP : 0);  // a token's sums over channels, likewise
+    float4 du[kK][CH / 2];  // s and s x of two channels
+    float2 v[kK][CH / 2];
+    float b[kK][NP], c[kK][NP];
+    float e[3][kK][L][ES];        // parts of sum G b, sum a P h and sum c h, summed over L
+    float pb[kK][TS], pc[kK][TS];  // parts of db and dc, [ROWS][NP], summed over the rows
 };
 
-// One CTA: 256 / L channels of one group, one segment of one sequence, backward in time.  A thread holds two channels and
-// four states of each: what it sums over its channels (for db, dc) and over its states (for dx, ds and the inner y) leaves
-// half and a quarter of the values for shared memory to sum.  Eight tokens at a time: from the kept state their decays and
-// states are formed again into registers, then walked backward.
-template <typename T, int L>
-__global__ void __launch_bounds__(kThr) ss_backward_kernel(const SsArgs w) {
-    using TL = Tile<L>;
-    constexpr int CH = TL::CH, NP = TL::NP, PER = kK * CH / kThr, LT = kThr / CH;
-    extern __shared__ __align__(16) float smem[];
-    float4 *s_du = reinterpret_cast<float4 *>(smem);                   // [kK][CH]
-    float2 *s_v = reinterpret_cast<float2 *>(smem + kK * CH * 4);      // [kK][CH]
-    float *s_b = smem + kK * CH * 6, *s_c = s_b + kK * NP;             // [kK][NP]
-    float *s_e = s_c + kK * NP;                                        // [3][kK][L][ES]
-    float *s_pb = s_e + 3 * kK * L * TL::ES, *s_pc = s_pb + kK * TL::TS;  // [kK][ROWS][NP]
+// One CTA: 2 kThr / L channels of one group, one segment of one sequence, backward in time.  A thread holds S states of
+// each of two channels: what it sums over its channels (for db, dc) and over its states (for dx, ds and the inner y)
+// leaves 1 / 2 and 1 / S of the values to pass through shared memory, whose bytes are what bounds this kernel next to its
+// arithmetic.  Eight tokens at a time: from the kept state their decays and states are formed again into registers, then
+// walked backward.  VEC: pairs of channels, and quads of b and c, lie on their own alignment.
+template <typename T, int S, int L, bool VEC>
+__global__ void __launch_bounds__(kThr, S == 2 ? 3 : 2) ss_backward_kernel(const SsArgs w) {
+    using SM = Smem<S, L>;
+    constexpr int CH = SM::CH, NP = SM::NP, Q = S / 2;
+    constexpr int LT = kThr / (CH / 2), PER = (kK + LT - 1) / LT;
+    extern __shared__ __align__(16) char smem[];
+    SM &sm = *reinterpret_cast<SM *>(smem);
 
     const int tid = threadIdx.x, per = w.D / w.G;
     const int tiles = (per + CH - 1) / CH, blocks = tiles * w.G;
@@ -40,189 +41,228 @@ __global__ void __launch_bounds__(kThr) ss_backward_kernel(const SsArgs w) {
     const int len = row_count(w.lengths, b, w.T);
     const int t_first = seg * w.seg, t_end = min(w.T, t_first + w.seg), t_len = min(t_end, len);
     const long long all = static_cast<long long>(w.B) * w.D * w.N;
-    const int groups = (w.T + kK - 1) / kK;
-    const bool vec = w.N % 4 == 0, gated = w.gate.p != nullptr;
+    const bool vec = w.N % S == 0, gated = w.gate.p != nullptr;
 
     // as owner of the states of two channels
-    const int row = tid / L, n0 = tid % L * 4, c0 = 2 * row;
-    u64 a[2][2] = {}, p[2][2] = {}, da[2][2] = {};
-    bool owner[2];
-    long long state_at[2];
+    const int pair = tid / L, n0 = tid % L * S, d = g * per + tile * CH + 2 * pair;
+    const int owns = min(2, max(0, per - tile * CH - 2 * pair));
+    const long long state_at = (static_cast<long long>(b) * w.D + d) * w.N;
+    u64 p[2][Q] = {}, da[2][Q] = {};
+    float a[2][S] = {};
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-        const int c = tile * CH + c0 + q, d = g * per + c;
-        owner[q] = c < per;
-        state_at[q] = (static_cast<long long>(b) * w.D + d) * w.N;
-        if (owner[q]) {
-            load_states(a[q], w.a + static_cast<long long>(d) * w.N, n0, w.N, false);
+        if (q >= owns) continue;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) a[q][i] = mul2(a[q][i], splat(kLog2eF));
-            const float *from = w.n_seg > 1 ? w.rev_state + seg * all : w.dh;
-            if (from != nullptr) load_states(p[q], from + state_at[q], n0, w.N, false);
-        }
+        for (int i = 0; i < S; ++i)
+            if (n0 + i < w.N) a[q][i] = w.a[(static_cast<long long>(d) + q) * w.N + n0 + i] * kLog2eF;
+        const float *from = w.n_seg > 1 ? w.rev_state + seg * all : w.dh;
+        if (from != nullptr) load_states(p[q], from + state_at + q * w.N, n0, w.N, vec);
     }
-    // as the one who prepares and finishes tokens lt + i LT of channel lch
-    const int lch = tid % CH, lt = tid / CH, ld = g * per + tile * CH + lch;
-    const bool loads = tile * CH + lch < per;
-    const float bias = loads && w.dt_bias != nullptr ? w.dt_bias[ld] : 0.f;
-    const float skip = loads && w.skip != nullptr ? w.skip[ld] : 0.f;
-    const T *px = static_cast<const T *>(w.x.p) + b * w.x.sb + ld;
-    const T *pdt = static_cast<const T *>(w.dt.p) + b * w.dt.sb + ld;
-    const T *pg = static_cast<const T *>(w.gate.p) + b * w.gate.sb + ld;
-    const T *pdy = static_cast<const T *>(w.dy.p) + b * w.dy.sb + ld;
-    const T *pb = static_cast<const T *>(w.b.p) + b * w.b.sb + g * w.b.sg;
-    const T *pc = static_cast<const T *>(w.c.p) + b * w.c.sb + g * w.c.sg;
-    constexpr int NB = (kK * NP + kThr - 1) / kThr;
+    // as the one who prepares and finishes tokens lt + i LT of the channels lc and lc + 1
+    const int lc = tid % (CH / 2) * 2, lt = tid / (CH / 2), ld = g * per + tile * CH + lc;
+    const int have = min(2, max(0, per - tile * CH - lc));
+    float bias[2] = {}, skip[2] = {}, dskip[2] = {}, dbias[2] = {};
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        if (q < have && w.dt_bias != nullptr) bias[q] = w.dt_bias[ld + q];
+        if (q < have && w.skip != nullptr) skip[q] = w.skip[ld + q];
+    }
+    const int n_chunk = (max(t_len - t_first, 0) + kK - 1) / kK;
+    const int t_start = t_first + max(n_chunk - 1, 0) * kK;
+    const T *px = static_cast<const T *>(w.x.p) + b * w.x.sb + ld + (t_start + lt) * w.x.st;
+    const T *pdt = static_cast<const T *>(w.dt.p) + b * w.dt.sb + ld + (t_start + lt) * w.dt.st;
+    const T *pg = static_cast<const T *>(w.gate.p) + b * w.gate.sb + ld + (t_start + lt) * w.gate.st;
+    const T *pdy = static_cast<const T *>(w.dy.p) + b * w.dy.sb + ld + (t_start + lt) * w.dy.st;
+    constexpr int BW = VEC ? 4 : 1, BROW = NP / BW, NB = (kK * BROW + kThr - 1) / kThr;
+    const int bt = tid / BROW, bn = tid % BROW * BW;
+    const T *pb = static_cast<const T *>(w.b.p) + b * w.b.sb + g * w.b.sg + (t_start + bt) * w.b.st + bn;
+    const T *pc = static_cast<const T *>(w.c.p) + b * w.c.sb + g * w.c.sg + (t_start + bt) * w.c.st + bn;
+    const float *pk_at = w.kept + ((static_cast<long long>(b) * ((w.T + kK - 1) / kK) + t_start / kK) * w.D + d) * w.N;
 
-    float nx[PER], nt[PER], ng[PER], ny[PER], nb[NB], nc[NB];  // the next tokens, as they are
-    float cx[PER], cr[PER], cg[PER], cy[PER];                  // the present ones: x, raw step, gate, dy
-    u64 hk[2][2] = {};                                         // the next kept states
-    float dskip = 0.f, dbias = 0.f;
+    Raw<T> nx[PER], nt[PER], ng[PER], ny[PER], cx[PER], cg[PER], cy[PER];  // the next tokens' elements, and the present ones'
+    RawN<T, BW> nb[NB], nc[NB];
+    float slope[PER][2], sig[PER][2];  // of the softplus; the gate's sigmoid
+    u64 hk[2][Q] = {};                 // the next kept states
     auto fetch = [&](int t0) {
+        const int left = t_len - t0;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int t = t0 + lt + i * LT;
-            const bool on = loads && t < t_len;
-            nx[i] = on ? to_f(px[t * w.x.st]) : 0.f;
-            nt[i] = on ? to_f(pdt[t * w.dt.st]) : 0.f;
-            ny[i] = on ? to_f(pdy[t * w.dy.st]) : 0.f;
-            ng[i] = on && gated ? to_f(pg[t * w.gate.st]) : 0.f;
+            const int t = lt + i * LT, n = t < kK && t < left ? have : 0;
+            nx[i] = load_raw<VEC>(px + i * LT * w.x.st, n);
+            nt[i] = load_raw<VEC>(pdt + i * LT * w.dt.st, n);
+            ng[i] = load_raw<VEC>(pg + i * LT * w.gate.st, gated ? n : 0);
+            ny[i] = load_raw<VEC>(pdy + i * LT * w.dy.st, n);
         }
+        px -= kK * w.x.st, pdt -= kK * w.dt.st, pg -= kK * w.gate.st, pdy -= kK * w.dy.st;
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
-            const int e = tid + i * kThr, t = t0 + e / NP, n = e % NP;
-            const bool on = e < kK * NP && n < w.N && t < t_len;
-            nb[i] = on ? to_f(pb[t * w.b.st + n]) : 0.f;
-            nc[i] = on ? to_f(pc[t * w.c.st + n]) : 0.f;
+            const int t = bt + i * (kThr / BROW);
+            const bool on = t < kK && t < left && bn < w.N;
+            nb[i] = load_n<BW>(pb + i * (kThr / BROW) * w.b.st, on);
+            nc[i] = load_n<BW>(pc + i * (kThr / BROW) * w.c.st, on);
         }
+        pb -= kK * w.b.st, pc -= kK * w.c.st;
 #pragma unroll
         for (int q = 0; q < 2; ++q)
-            if (owner[q])
-                load_states(hk[q], w.kept + ((static_cast<long long>(b) * groups + t0 / kK) * w.D + g * per + tile * CH + c0 + q) * w.N,
-                            n0, w.N, vec);
+            if (q < owns) load_states(hk[q], pk_at + q * w.N, n0, w.N, vec);
+        pk_at -= static_cast<long long>(w.D) * w.N;
     };
     auto stage = [&](int t0) {
+        float s[PER][2], v[PER][2];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            upk(value(nt[i]), s[i][0], s[i][1]), upk(value(ny[i]), v[i][0], v[i][1]);
+            s[i][0] += bias[0], s[i][1] += bias[1];
+            slope[i][0] = slope[i][1] = 1.f;
+        }
+        if (w.softplus) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) s[i][0] = softplus(s[i][0], slope[i][0]), s[i][1] = softplus(s[i][1], slope[i][1]);
+        }
+        if (gated) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                float z[2];
+                upk(value(ng[i]), z[0], z[1]);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) sig[i][q] = sigmoid_of(z[q]), v[i][q] *= z[q] * sig[i][q];
+            }
+        }
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int t = lt + i * LT;
-            float s = 0.f, v = 0.f;
-            cx[i] = nx[i], cg[i] = ng[i], cy[i] = ny[i], cr[i] = nt[i] + bias;
-            if (loads && t0 + t < t_len) {
-                s = w.softplus ? softplus(cr[i]) : cr[i];
-                v = gated ? gate_with(ny[i], ng[i]) : ny[i];
+            const bool on = t0 + t < t_len;
+            float x[2];
+            upk(value(nx[i]), x[0], x[1]);
+            s[i][0] = on ? s[i][0] : 0.f, s[i][1] = on ? s[i][1] : 0.f;
+            if (t < kK) {
+                sm.du[t][lc / 2] = make_float4(s[i][0], s[i][1], s[i][0] * x[0], s[i][1] * x[1]);
+                sm.v[t][lc / 2] = make_float2(v[i][0], v[i][1]);
             }
-            const float u = s * nx[i];
-            s_du[t * CH + lch] = make_float4(s, s, u, u);
-            s_v[t * CH + lch] = make_float2(v, v);
+            cx[i] = nx[i], cg[i] = ng[i], cy[i] = ny[i];
         }
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
-            const int e = tid + i * kThr;
-            if (e < kK * NP) s_b[e] = nb[i], s_c[e] = nc[i];
+            const int t = bt + i * (kThr / BROW);
+            if (t < kK) store_n(&sm.b[t][bn], nb[i]), store_n(&sm.c[t][bn], nc[i]);
         }
     };
 
-    const int n_chunk = (max(t_len - t_first, 0) + kK - 1) / kK;
     if (n_chunk > 0) {
-        fetch(t_first + (n_chunk - 1) * kK);
-        stage(t_first + (n_chunk - 1) * kK);
+        fetch(t_start);
+        stage(t_start);
     }
-    for (int k = n_chunk - 1; k >= 0; --k) {
-        const int t0 = t_first + k * kK;
+    for (int k = n_chunk - 1, t0 = t_start; k >= 0; --k, t0 -= kK) {
         __syncthreads();
-        u64 first[2][2], h[kK][2][2], e[kK][2][2];
+        u64 first[2][Q], h[kK][2][Q], e[kK][2][Q];
 #pragma unroll
         for (int q = 0; q < 2; ++q)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) first[q][i] = hk[q][i];
+            for (int i = 0; i < Q; ++i) first[q][i] = hk[q][i];
         if (k > 0) fetch(t0 - kK);
 #pragma unroll
         for (int t = 0; t < kK; ++t) {
-            u64 bb[2];
-            load_pairs(bb, s_b + t * NP + n0);
+            const float4 du = sm.du[t][pair];
+            u64 bb[Q];
+            load_pairs(bb, &sm.b[t][n0]);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const ulonglong2 du = *reinterpret_cast<const ulonglong2 *>(s_du + t * CH + c0 + q);
+                const float st = q == 0 ? du.x : du.y, u = q == 0 ? du.z : du.w;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
+                for (int i = 0; i < Q; ++i) {
                     const u64 before = t == 0 ? first[q][i] : h[t == 0 ? 0 : t - 1][q][i];
-                    e[t][q][i] = decay_less_one(mul2(du.x, a[q][i]));
-                    h[t][q][i] = fma2(e[t][q][i], before, fma2(du.y, bb[i], before));
+                    float b0, b1, h0, h1;
+                    upk(bb[i], b0, b1), upk(before, h0, h1);
+                    e[t][q][i] = decay_less_one(pk(st * a[q][2 * i], st * a[q][2 * i + 1]));
+                    h[t][q][i] = fma2(e[t][q][i], before, pk(fmaf(u, b0, h0), fmaf(u, b1, h1)));
                 }
             }
         }
 #pragma unroll
         for (int t = kK - 1; t >= 0; --t) {
-            u64 bb[2], cc[2], db[2] = {0, 0}, dc[2] = {0, 0};
-            load_pairs(bb, s_b + t * NP + n0);
-            load_pairs(cc, s_c + t * NP + n0);
+            const float4 du = sm.du[t][pair];
+            const float2 vv = sm.v[t][pair];
+            u64 bb[Q], cc[Q], db[Q], dc[Q];
+            load_pairs(bb, &sm.b[t][n0]);
+            load_pairs(cc, &sm.c[t][n0]);
             float e1[2], e2[2], e3[2];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const ulonglong2 du = *reinterpret_cast<const ulonglong2 *>(s_du + t * CH + c0 + q);
-                const u64 v = *reinterpret_cast<const u64 *>(s_v + t * CH + c0 + q);
+                const float st = q == 0 ? du.x : du.y, u = q == 0 ? du.z : du.w, v = q == 0 ? vv.x : vv.y;
                 u64 x1 = 0, x2 = 0, x3 = 0;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
+                for (int i = 0; i < Q; ++i) {
                     const u64 before = t == 0 ? first[q][i] : h[t == 0 ? 0 : t - 1][q][i];
-                    const u64 G = fma2(v, cc[i], p[q][i]);
-                    dc[i] = fma2(v, h[t][q][i], dc[i]);
-                    db[i] = fma2(G, du.y, db[i]);
-                    x1 = fma2(G, bb[i], x1);
+                    float c0, c1, p0, p1, h0, h1, g0, g1, m0, m1, d0, d1;
+                    upk(cc[i], c0, c1), upk(p[q][i], p0, p1), upk(h[t][q][i], h0, h1);
+                    g0 = fmaf(v, c0, p0), g1 = fmaf(v, c1, p1);
+                    const u64 G = pk(g0, g1);
+                    if (q == 0) {
+                        dc[i] = pk(v * h0, v * h1), db[i] = pk(u * g0, u * g1);
+                    } else {
+                        upk(dc[i], d0, d1);
+                        dc[i] = pk(fmaf(v, h0, d0), fmaf(v, h1, d1));
+                        upk(db[i], d0, d1);
+                        db[i] = pk(fmaf(u, g0, d0), fmaf(u, g1, d1));
+                    }
+                    x1 = i == 0 ? mul2(G, bb[i]) : fma2(G, bb[i], x1);
                     p[q][i] = fma2(e[t][q][i], G, G);
-                    const u64 m = mul2(p[q][i], before);
-                    x2 = fma2(m, a[q][i], x2);
-                    da[q][i] = fma2(m, du.x, da[q][i]);
-                    x3 = fma2(cc[i], h[t][q][i], x3);
+                    const u64 m = mul2(p[q][i], before), aa = pk(a[q][2 * i], a[q][2 * i + 1]);
+                    x2 = i == 0 ? mul2(m, aa) : fma2(m, aa, x2);
+                    upk(m, m0, m1), upk(da[q][i], d0, d1);
+                    da[q][i] = pk(fmaf(st, m0, d0), fmaf(st, m1, d1));
+                    if (gated) x3 = i == 0 ? mul2(cc[i], h[t][q][i]) : fma2(cc[i], h[t][q][i], x3);
                 }
                 e1[q] = pair_sum(x1), e2[q] = pair_sum(x2), e3[q] = pair_sum(x3);
             }
-            const int at = (t * L + tid % L) * TL::ES + c0;
-            *reinterpret_cast<float2 *>(s_e + at) = make_float2(e1[0], e1[1]);
-            *reinterpret_cast<float2 *>(s_e + kK * L * TL::ES + at) = make_float2(e2[0], e2[1]);
-            if (gated) *reinterpret_cast<float2 *>(s_e + 2 * kK * L * TL::ES + at) = make_float2(e3[0], e3[1]);
-            *reinterpret_cast<ulonglong2 *>(s_pb + t * TL::TS + row * NP + n0) = make_ulonglong2(db[0], db[1]);
-            *reinterpret_cast<ulonglong2 *>(s_pc + t * TL::TS + row * NP + n0) = make_ulonglong2(dc[0], dc[1]);
+            *reinterpret_cast<float2 *>(&sm.e[0][t][tid % L][2 * pair]) = make_float2(e1[0], e1[1]);
+            *reinterpret_cast<float2 *>(&sm.e[1][t][tid % L][2 * pair]) = make_float2(e2[0], e2[1]);
+            if (gated) *reinterpret_cast<float2 *>(&sm.e[2][t][tid % L][2 * pair]) = make_float2(e3[0], e3[1]);
+            store_pairs(&sm.pb[t][pair * NP + n0], db);
+            store_pairs(&sm.pc[t][pair * NP + n0], dc);
         }
         __syncthreads();
         // the sums over the states: dx, ddt, dgate
-        const long long out = (static_cast<long long>(b) * w.T + t0) * w.D + ld;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int t = lt + i * LT;
-            float e1 = 0.f, e2 = 0.f, e3 = 0.f;
+            const int t = lt + i * LT, n = t < kK && t0 + t < t_len ? have : 0;
+            if (n == 0) continue;
+            float e1[2] = {}, e2[2] = {}, e3[2] = {}, x[2], z[2], y[2], ddt[2], dx[2], dg[2];
 #pragma unroll
             for (int l = 0; l < L; ++l) {
-                const int at = (t * L + l) * TL::ES + lch;
-                e1 += s_e[at], e2 += s_e[kK * L * TL::ES + at];
-                if (gated) e3 += s_e[2 * kK * L * TL::ES + at];
+                const float2 q1 = *reinterpret_cast<const float2 *>(&sm.e[0][t][l][lc]);
+                const float2 q2 = *reinterpret_cast<const float2 *>(&sm.e[1][t][l][lc]);
+                e1[0] += q1.x, e1[1] += q1.y, e2[0] += q2.x, e2[1] += q2.y;
+                if (gated) {
+                    const float2 q3 = *reinterpret_cast<const float2 *>(&sm.e[2][t][l][lc]);
+                    e3[0] += q3.x, e3[1] += q3.y;
+                }
             }
-            if (!loads || t0 + t >= t_len) continue;
-            const float4 du = s_du[t * CH + lch];
-            const float v = s_v[t * CH + lch].x;
-            float ds = fmaf(cx[i], e1, e2 * 0.693147181f);
-            if (w.softplus) ds *= sigmoid_of(cr[i]);
-            const long long to = out + static_cast<long long>(t) * w.D;
-            static_cast<T *>(w.dx)[to] = from_f<T>(fmaf(skip, v, du.x * e1));
-            static_cast<T *>(w.ddt)[to] = from_f<T>(ds);
-            dskip = fmaf(v, cx[i], dskip);
-            dbias += ds;
-            if (gated) {
-                const float z = sigmoid_of(cg[i]), y = fmaf(skip, cx[i], e3);
-                static_cast<T *>(w.dgate)[to] = from_f<T>(cy[i] * y * z * fmaf(cg[i], 1.f - z, 1.f));
+            upk(value(cx[i]), x[0], x[1]), upk(value(cg[i]), z[0], z[1]), upk(value(cy[i]), y[0], y[1]);
+            const float4 du = sm.du[t][lc / 2];
+            const float2 vv = sm.v[t][lc / 2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const float v = q == 0 ? vv.x : vv.y;
+                ddt[q] = fmaf(x[q], e1[q], e2[q] * 0.693147181f) * slope[i][q];
+                dx[q] = fmaf(skip[q], v, (q == 0 ? du.x : du.y) * e1[q]);
+                dskip[q] = fmaf(v, x[q], dskip[q]);
+                dbias[q] += ddt[q];
+                if (gated) dg[q] = y[q] * fmaf(skip[q], x[q], e3[q]) * sig[i][q] * fmaf(z[q], 1.f - sig[i][q], 1.f);
             }
+            const long long to = (static_cast<long long>(b) * w.T + t0 + t) * w.D + ld;
+            store_pair<VEC>(static_cast<T *>(w.dx) + to, pk(dx[0], dx[1]), n);
+            store_pair<VEC>(static_cast<T *>(w.ddt) + to, pk(ddt[0], ddt[1]), n);
+            if (gated) store_pair<VEC>(static_cast<T *>(w.dgate) + to, pk(dg[0], dg[1]), n);
         }
         // the sums over the CTA's channels: its part of db and dc
 #pragma unroll
-        for (int i = 0; i < NB; ++i) {
-            const int o = tid + i * kThr, t = o / NP, n = o % NP;
-            if (o < kK * NP && n < w.N && t0 + t < t_len) {
+        for (int o = tid; o < kK * NP; o += kThr) {
+            const int t = o / NP, n = o % NP;
+            if (n < w.N && t0 + t < t_len) {
                 float sb = 0.f, sc = 0.f;
-#pragma unroll 8
-                for (int r = 0; r < TL::ROWS; ++r) {
-                    sb += s_pb[t * TL::TS + r * NP + n];
-                    sc += s_pc[t * TL::TS + r * NP + n];
-                }
+#pragma unroll
+                for (int r = 0; r < SM::ROWS; ++r) sb += sm.pb[t][r * NP + n], sc += sm.pc[t][r * NP + n];
                 const long long to = (((static_cast<long long>(tile) * w.B + b) * w.T + t0 + t) * w.G + g) * w.N + n;
                 w.part_b[to] = sb;
                 w.part_c[to] = sc;
@@ -233,34 +273,37 @@ __global__ void __launch_bounds__(kThr) ss_backward_kernel(const SsArgs w) {
             stage(t0 - kK);
         }
     }
-    if (loads) {  // nothing stands behind a sequence
+    {  // nothing stands behind a sequence
         const long long out = static_cast<long long>(b) * w.T * w.D + ld;
         for (int t = max(t_len, t_first) + lt; t < t_end; t += LT) {
             const long long to = out + static_cast<long long>(t) * w.D;
-            static_cast<T *>(w.dx)[to] = from_f<T>(0.f);
-            static_cast<T *>(w.ddt)[to] = from_f<T>(0.f);
-            if (gated) static_cast<T *>(w.dgate)[to] = from_f<T>(0.f);
+            store_pair<VEC>(static_cast<T *>(w.dx) + to, 0ull, have);
+            store_pair<VEC>(static_cast<T *>(w.ddt) + to, 0ull, have);
+            if (gated) store_pair<VEC>(static_cast<T *>(w.dgate) + to, 0ull, have);
         }
     }
 #pragma unroll
     for (int q = 0; q < 2; ++q)
-        if (owner[q]) {
-            store_states(da[q], w.part_a + seg * all + state_at[q], n0, w.N, false);
-            if (seg == 0 && w.dh0 != nullptr) store_states(p[q], w.dh0 + state_at[q], n0, w.N, false);
+        if (q < owns) {
+            store_states(da[q], w.part_a + seg * all + state_at + q * w.N, n0, w.N, vec);
+            if (seg == 0 && w.dh0 != nullptr) store_states(p[q], w.dh0 + state_at + q * w.N, n0, w.N, vec);
         }
     __syncthreads();
-    smem[tid] = dskip, smem[kThr + tid] = dbias;
+    float2 *s_sum = reinterpret_cast<float2 *>(smem);
+    s_sum[tid] = make_float2(dskip[0], dskip[1]), s_sum[kThr + tid] = make_float2(dbias[0], dbias[1]);
     __syncthreads();
-    if (tid < CH && loads) {
-        float s = 0.f, q = 0.f;
+    if (tid < CH / 2) {
+        float2 s = make_float2(0.f, 0.f), q = s;
 #pragma unroll
-        for (int i = 0; i < LT; ++i) s += smem[tid + i * CH], q += smem[kThr + tid + i * CH];
+        for (int i = 0; i < LT; ++i) {
+            const float2 u = s_sum[tid + i * (CH / 2)], v = s_sum[kThr + tid + i * (CH / 2)];
+            s.x += u.x, s.y += u.y, q.x += v.x, q.y += v.y;
+        }
         const long long to = (static_cast<long long>(seg) * w.B + b) * w.D + ld;
-        w.part_skip[to] = s;
-        w.part_bias[to] = q;
+        if (have > 0) w.part_skip[to] = s.x, w.part_bias[to] = q.x;
+        if (have > 1) w.part_skip[to + 1] = s.y, w.part_bias[to + 1] = q.y;
     }
 }
-
 
 // db, dc = the sums over the tiles of a group; zero behind the sequences
 template <typename T>
@@ -277,26 +320,28 @@ __global__ void __launch_bounds__(256) ss_tiles_sum_kernel(const SsArgs w, int t
     }
 }
 
-template <typename T, int L>
+template <typename T, int S, int L, bool VEC>
 cudaError_t launch(const SsArgs &a, cudaStream_t s) {
-    constexpr int bytes = Tile<L>::FLOATS * 4;
+    constexpr int bytes = sizeof(Smem<S, L>);
     static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
-    const cudaError_t e = cudaFuncSetAttribute(ss_backward_kernel<T, L>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    const auto kernel = ss_backward_kernel<T, S, L, VEC>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    const unsigned grid = static_cast<unsigned>(ss_backward_tiles(a)) * a.G * a.n_seg * a.B;
-    ss_backward_kernel<T, L><<<grid, kThr, bytes, s>>>(a);
+    kernel<<<static_cast<unsigned>(ss_backward_tiles(a)) * a.G * a.n_seg * a.B, kThr, bytes, s>>>(a);
     return cudaGetLastError();
 }
-int lanes(int N) { return N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
-template <typename T>
+int lanes(int N) { return N <= 4 ? 2 : N <= 8 ? 4 : N <= 16 ? 8 : N <= 32 ? 16 : 32; }
+template <typename T, bool VEC>
 cudaError_t launch_of(const SsArgs &a, cudaStream_t s) {
     switch (lanes(a.N)) {
-        case 2: return launch<T, 2>(a, s);
-        case 4: return launch<T, 4>(a, s);
-        case 8: return launch<T, 8>(a, s);
-        default: return launch<T, 16>(a, s);
+        case 2: return launch<T, 2, 2, VEC>(a, s);
+        case 4: return launch<T, 2, 4, VEC>(a, s);
+        case 8: return launch<T, 2, 8, VEC>(a, s);
+        case 16: return launch<T, 2, 16, VEC>(a, s);
+        default: return launch<T, 2, 32, VEC>(a, s);
     }
 }
+
 }  // namespace
 
 int ss_backward_tiles(const SsArgs &a) {
@@ -306,7 +351,11 @@ int ss_backward_tiles(const SsArgs &a) {
 
 cudaError_t launch_ss_backward(const SsArgs &a, cudaStream_t s) {
     cudaError_t e = launch_ss_reverse_states(a, s);
-    if (e == cudaSuccess) e = a.dtype == PARARNN_F32 ? launch_of<float>(a, s) : launch_of<__nv_bfloat16>(a, s);
+    const bool vec = ss_pairs_ok(a);
+    if (e == cudaSuccess) {
+        if (a.dtype == PARARNN_F32) e = vec ? launch_of<float, true>(a, s) : launch_of<float, false>(a, s);
+        else e = vec ? launch_of<__nv_bfloat16, true>(a, s) : launch_of<__nv_bfloat16, false>(a, s);
+    }
     const long long n = static_cast<long long>(a.B) * a.T * a.G * a.N, rows = static_cast<long long>(a.n_seg) * a.B;
     const long long dn = static_cast<long long>(a.D) * a.N;
     if (e == cudaSuccess) {
