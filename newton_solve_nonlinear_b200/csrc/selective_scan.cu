@@ -8,58 +8,128 @@ namespace pararnn {
 using namespace ss;
 namespace {
 
-constexpr int kThr = 128;
+constexpr int kThr = 128;  // threads that hold states; as many again prepare and finish tokens
 constexpr int tokens_of(int L) { return L >= 4 ? 16 : 8; }  // between two barriers
 
 enum Pass { kOutputs, kSums, kStates, kReverseSums };
 
-// One CTA: 2 kThr / L channels of one group, one segment of one sequence.  A thread holds S states of each of two channels,
-// so that what it reads of b and c from shared memory serves both (every lane's bytes count there, the same address or
-// not: with one channel to a thread these reads took as long as the arithmetic); L lanes share the two channels.  Tokens
-// come in chunks of TC: between two barriers the threads prepare (token, channel pair)s for all (s and s x; VEC: pairs,
-// and quads of b and c, lie on their own alignment), then each runs its states through the chunk; the next chunk's
-// elements are on their way meanwhile, and y's parts meet in shared memory.
+template <int S, int L, bool OUT>
+struct SweepSmem {  // two of each, for chunks in turn
+    static constexpr int TC = tokens_of(L), CH = 2 * kThr / L, NP = S * L;
+    float4 du[2][TC][CH / 2];  // s and s x of two channels (reversed: s and v)
+    float b[2][TC][NP], c[OUT ? 2 : 1][OUT ? TC : 1][NP];
+    float2 y[OUT ? 2 : 1][OUT ? TC : 1][kThr];
+};
+
+// all threads of the CTA, which come from different places of the code
+__device__ __forceinline__ void meet() { asm volatile("bar.sync 1, %0;" ::"n"(2 * kThr) : "memory"); }
+
+// One CTA: 2 kThr / L channels of one group, one segment of one sequence, in chunks of TC tokens.
+//   Four warps hold the states: a thread has S states of each of two channels, so that what it reads of b and c from shared
+// memory serves both (every lane's bytes count there, the same address or not: with one channel to a thread these reads took
+// as long as the arithmetic); L lanes share the two channels.
+//   Four more prepare the next chunk (s and s x of each token and channel; VEC: pairs of channels, and quads of b and c, lie
+// on their own alignment) and finish the last one (the sum over the lanes, skip, gate), in the gaps that the chains of
+// dependent operations leave the others.
 //   kOutputs      from the start state: y, the kept states, and the last segment's last state
 //   kStates       from the start state: the kept states alone
 //   kSums         from zero: the segment's last state and sum of s
 //   kReverseSums  from zero, backward in time: P before the segment
 template <typename T, int S, int L, Pass PASS, bool VEC>
-__global__ void __launch_bounds__(kThr) ss_sweep_kernel(const SsArgs w) {
-    constexpr int TC = tokens_of(L), CH = 2 * kThr / L, NP = S * L, Q = S / 2;  // Q pairs of states
-    constexpr int LT = kThr / (CH / 2), PER = (TC + LT - 1) / LT;  // threads along the tokens, and tokens of each, in preparing
+__global__ void __launch_bounds__(2 * kThr, 2) ss_sweep_kernel(const SsArgs w) {
     constexpr bool OUT = PASS == kOutputs, REV = PASS == kReverseSums, SUMS = PASS == kSums || REV;
-    __shared__ float4 s_du[TC][CH / 2];  // s and s x of two channels (REV: s and v)
-    __shared__ __align__(16) float s_b[TC][NP], s_c[OUT ? TC : 1][NP];
-    __shared__ __align__(16) float2 s_y[OUT ? TC : 1][kThr];
-    __shared__ u64 s_sum[SUMS ? kThr : 1];
+    using SM = SweepSmem<S, L, OUT>;
+    constexpr int TC = SM::TC, CH = SM::CH, NP = SM::NP, Q = S / 2;  // Q pairs of states
+    extern __shared__ __align__(16) char smem[];
+    SM &sm = *reinterpret_cast<SM *>(smem);
 
-    const int tid = threadIdx.x, per = w.D / w.G;
-    const int tiles = (per + CH - 1) / CH, blocks = tiles * w.G;
+    const int per = w.D / w.G, tiles = (per + CH - 1) / CH, blocks = tiles * w.G;
     const int tile = blockIdx.x % blocks % tiles, g = blockIdx.x % blocks / tiles;
     const int seg = blockIdx.x / blocks % w.n_seg, b = blockIdx.x / blocks / w.n_seg;
     const int len = row_count(w.lengths, b, w.T);
     const int t_first = seg * w.seg, t_end = min(w.T, t_first + w.seg), t_len = min(t_end, len);
+    const int n_chunk = (max(t_len - t_first, 0) + TC - 1) / TC;
+    const int t_start = t_first + (REV ? max(n_chunk - 1, 0) * TC : 0);  // the chunks go on from here, TC tokens at a time
+    constexpr int STEP = REV ? -TC : TC;
 
-    // as owner of states
-    const int pair = tid / L, n0 = tid % L * S, d = g * per + tile * CH + 2 * pair;
-    const int owns = min(2, max(0, per - tile * CH - 2 * pair));
-    const bool vec = w.N % S == 0;
-    const long long state_at = (static_cast<long long>(b) * w.D + d) * w.N;
-    const long long all = static_cast<long long>(w.B) * w.D * w.N;
-    u64 h[2][Q] = {};
-    float a[2][S] = {};
+    if (threadIdx.x < kThr) {
+        const int tid = threadIdx.x, pair = tid / L, n0 = tid % L * S, d = g * per + tile * CH + 2 * pair;
+        const int owns = min(2, max(0, per - tile * CH - 2 * pair));
+        const bool vec = w.N % S == 0;
+        const long long at_d = (static_cast<long long>(b) * w.D + d) * w.N, all = static_cast<long long>(w.B) * w.D * w.N;
+        u64 h[2][Q] = {};
+        float a[2][S] = {};
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        if (q >= owns) continue;
+        for (int q = 0; q < 2; ++q) {
+            if (q >= owns) continue;
 #pragma unroll
-        for (int i = 0; i < S; ++i)
-            if (n0 + i < w.N) a[q][i] = w.a[(static_cast<long long>(d) + q) * w.N + n0 + i] * kLog2eF;
-        if (!SUMS) {
-            const float *from = w.n_seg > 1 ? w.seg_state + seg * all : w.h0;
-            if (from != nullptr) load_states(h[q], from + state_at + q * w.N, n0, w.N, vec);
+            for (int i = 0; i < S; ++i)
+                if (n0 + i < w.N) a[q][i] = w.a[(static_cast<long long>(d) + q) * w.N + n0 + i] * kLog2eF;
+            if (!SUMS) {
+                const float *from = w.n_seg > 1 ? w.seg_state + seg * all : w.h0;
+                if (from != nullptr) load_states(h[q], from + at_d + q * w.N, n0, w.N, vec);
+            }
         }
+        const long long row = static_cast<long long>(w.D) * w.N;
+        float *kept = SUMS || w.kept == nullptr
+                          ? nullptr
+                          : w.kept + (static_cast<long long>(b) * ((w.T + kSsKeep - 1) / kSsKeep) + t_start / kSsKeep) * row +
+                                static_cast<long long>(d) * w.N;
+        meet();
+        for (int k = 0, t0 = t_start; k < n_chunk; ++k, t0 += STEP) {
+            const auto &du_at = sm.du[k & 1];
+            const auto &b_at = sm.b[k & 1];
+            const auto &c_at = sm.c[OUT ? k & 1 : 0];
+            auto &y_at = sm.y[OUT ? k & 1 : 0];
+#pragma unroll 1
+            for (int j0 = 0; j0 < TC; j0 += kSsKeep) {
+                if (!SUMS && kept != nullptr) {
+                    if (t0 + j0 < t_len) {
+                        if (owns > 0) store_states(h[0], kept, n0, w.N, vec);
+                        if (owns > 1) store_states(h[1], kept + w.N, n0, w.N, vec);
+                    }
+                    kept += row;
+                }
+#pragma unroll
+                for (int j = 0; j < kSsKeep; ++j) {
+                    const int t = REV ? TC - 1 - j0 - j : j0 + j;
+                    const float4 du = du_at[t][pair];
+                    u64 bb[Q], cc[Q];
+                    float y[2];
+                    load_pairs(bb, &b_at[t][n0]);
+                    if (OUT) load_pairs(cc, &c_at[t][n0]);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const float st = q == 0 ? du.x : du.y, u = q == 0 ? du.z : du.w;
+                        u64 part = 0;
+#pragma unroll
+                        for (int i = 0; i < Q; ++i) {
+                            const u64 e = decay_less_one(pk(st * a[q][2 * i], st * a[q][2 * i + 1]));
+                            // one factor for both of a pair: two instructions, as moving it beside itself would take
+                            float b0, b1, h0, h1;
+                            upk(bb[i], b0, b1), upk(h[q][i], h0, h1);
+                            const u64 moved = pk(fmaf(u, b0, h0), fmaf(u, b1, h1));
+                            h[q][i] = REV ? fma2(e, moved, moved) : fma2(e, h[q][i], moved);
+                            if (OUT) part = i == 0 ? mul2(cc[i], h[q][i]) : fma2(cc[i], h[q][i], part);
+                        }
+                        if (OUT) y[q] = pair_sum(part);
+                    }
+                    if (OUT) y_at[t][tid] = make_float2(y[0], y[1]);
+                }
+            }
+            meet();
+        }
+        float *last = SUMS ? (REV ? w.rev_state : w.seg_state) + seg * all : w.h;
+        if (SUMS || (OUT && seg == w.n_seg - 1)) {
+            if (owns > 0) store_states(h[0], last + at_d, n0, w.N, vec);
+            if (owns > 1) store_states(h[1], last + at_d + w.N, n0, w.N, vec);
+        }
+        return;
     }
-    // as the one who prepares and finishes tokens t0 + lt + i LT of the channels lc and lc + 1
+
+    // tokens lt + i LT of a chunk, channels lc and lc + 1
+    constexpr int LT = kThr / (CH / 2), PER = (TC + LT - 1) / LT;
+    const int tid = threadIdx.x - kThr;
     const int lc = tid % (CH / 2) * 2, lt = tid / (CH / 2), ld = g * per + tile * CH + lc;
     const int have = min(2, max(0, per - tile * CH - lc));
     float bias[2] = {}, skip[2] = {};
@@ -70,9 +140,6 @@ __global__ void __launch_bounds__(kThr) ss_sweep_kernel(const SsArgs w) {
     }
     const bool gated = w.gate.p != nullptr;
     const SsRows &rx = REV ? w.dy : w.x, &rb = REV ? w.c : w.b;
-    const int n_chunk = (max(t_len - t_first, 0) + TC - 1) / TC;
-    const int t_start = t_first + (REV ? max(n_chunk - 1, 0) * TC : 0);  // the chunks go on from here, TC tokens at a time
-    constexpr int STEP = REV ? -TC : TC;
     // where this thread's next elements are
     const T *px = static_cast<const T *>(rx.p) + b * rx.sb + ld + (t_start + lt) * rx.st;
     const T *pdt = static_cast<const T *>(w.dt.p) + b * w.dt.sb + ld + (t_start + lt) * w.dt.st;
@@ -81,8 +148,9 @@ __global__ void __launch_bounds__(kThr) ss_sweep_kernel(const SsArgs w) {
     const int bt = tid / BROW, bn = tid % BROW * BW;
     const T *pb = static_cast<const T *>(rb.p) + b * rb.sb + g * rb.sg + (t_start + bt) * rb.st + bn;
     const T *pc = static_cast<const T *>(w.c.p) + b * w.c.sb + g * w.c.sg + (t_start + bt) * w.c.st + bn;
+    T *py = static_cast<T *>(w.y) + (static_cast<long long>(b) * w.T + t_start + lt) * w.D + ld;
 
-    Raw<T> nx[PER], ndt[PER], ng[PER], cx[PER], cg[PER];
+    Raw<T> nx[PER], ndt[PER], ng[PER], cx[PER], cg[PER], ox[PER], og[PER];  // of the next chunk, the present and the last one
     RawN<T, BW> nb[NB], nc[NB];
     u64 sum = 0;
     auto fetch = [&](int t0) {
@@ -105,7 +173,7 @@ __global__ void __launch_bounds__(kThr) ss_sweep_kernel(const SsArgs w) {
         pb += STEP * rb.st, pc += STEP * w.c.st;
     };
     // (each step for all of the thread's tokens before the next step: chains of dependent operations side by side)
-    auto stage = [&](int t0) {
+    auto stage = [&](int t0, int to) {
         float st[PER][2], u[PER][2];
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
@@ -135,106 +203,71 @@ __global__ void __launch_bounds__(kThr) ss_sweep_kernel(const SsArgs w) {
         for (int i = 0; i < PER; ++i) {
             const int t = lt + i * LT;
             if (t < TC) {
-                s_du[t][lc / 2] = make_float4(st[i][0], st[i][1], u[i][0], u[i][1]);
+                sm.du[to][t][lc / 2] = make_float4(st[i][0], st[i][1], u[i][0], u[i][1]);
                 if (SUMS) sum = add2(sum, pk(st[i][0], st[i][1]));
             }
-            cx[i] = nx[i], cg[i] = ng[i];
+            if (OUT) ox[i] = cx[i], og[i] = cg[i], cx[i] = nx[i], cg[i] = ng[i];
         }
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
             const int t = bt + i * (kThr / BROW);
             if (t < TC) {
-                store_n(&s_b[t][bn], nb[i]);
-                if (OUT) store_n(&s_c[t][bn], nc[i]);
+                store_n(&sm.b[to][t][bn], nb[i]);
+                if (OUT) store_n(&sm.c[to][t][bn], nc[i]);
             }
         }
     };
+    auto finish = [&](int t0, int from, const Raw<T> (&x)[PER], const Raw<T> (&z)[PER]) {
+        float y[PER][2];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            float part[2 * L], v[2];
+            upk(value(x[i]), v[0], v[1]);
+            load_floats<2 * L>(part, &sm.y[from][min(lt + i * LT, TC - 1)][lc / 2 * L].x);
+#pragma unroll
+            for (int q = 1; q < L; ++q) part[0] += part[2 * q], part[1] += part[2 * q + 1];
+            y[i][0] = fmaf(skip[0], v[0], part[0]), y[i][1] = fmaf(skip[1], v[1], part[1]);
+        }
+        if (gated) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                float g2[2];
+                upk(value(z[i]), g2[0], g2[1]);
+                y[i][0] = gate_with(y[i][0], g2[0]), y[i][1] = gate_with(y[i][1], g2[1]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int t = lt + i * LT;
+            store_pair<VEC>(py + static_cast<long long>(i * LT) * w.D, pk(y[i][0], y[i][1]), t < TC && t0 + t < t_len ? have : 0);
+        }
+        py += static_cast<long long>(TC) * w.D;
+    };
 
-    T *py = static_cast<T *>(w.y) + (static_cast<long long>(b) * w.T + t_start + lt) * w.D + ld;
     if (n_chunk > 0) {
         fetch(t_start);
-        stage(t_start);
+        stage(t_start, 0);
+        if (n_chunk > 1) fetch(t_start + STEP);
     }
+    meet();
     for (int k = 0, t0 = t_start; k < n_chunk; ++k, t0 += STEP) {
-        __syncthreads();
-        if (k + 1 < n_chunk) fetch(t0 + STEP);
-#pragma unroll 1
-        for (int j0 = 0; j0 < TC; j0 += kSsKeep) {
-            if (!SUMS && w.kept != nullptr && t0 + j0 < t_len) {
-                float *to = w.kept + ((static_cast<long long>(b) * ((w.T + kSsKeep - 1) / kSsKeep) + (t0 + j0) / kSsKeep) *
-                                          w.D + d) * w.N;
-                if (owns > 0) store_states(h[0], to, n0, w.N, vec);
-                if (owns > 1) store_states(h[1], to + w.N, n0, w.N, vec);
-            }
-#pragma unroll
-            for (int j = 0; j < kSsKeep; ++j) {
-                const int t = REV ? TC - 1 - j0 - j : j0 + j;
-                const float4 du = s_du[t][pair];
-                u64 bb[Q], cc[Q];
-                float y[2];
-                load_pairs(bb, &s_b[t][n0]);
-                if (OUT) load_pairs(cc, &s_c[t][n0]);
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const float st = q == 0 ? du.x : du.y, u = q == 0 ? du.z : du.w;
-                    u64 part = 0;
-#pragma unroll
-                    for (int i = 0; i < Q; ++i) {
-                        const u64 e = decay_less_one(pk(st * a[q][2 * i], st * a[q][2 * i + 1]));
-                        // one factor for both of a pair: two instructions, as moving it beside itself would take
-                        float b0, b1, h0, h1;
-                        upk(bb[i], b0, b1), upk(h[q][i], h0, h1);
-                        const u64 moved = pk(fmaf(u, b0, h0), fmaf(u, b1, h1));
-                        h[q][i] = REV ? fma2(e, moved, moved) : fma2(e, h[q][i], moved);
-                        if (OUT) part = i == 0 ? mul2(cc[i], h[q][i]) : fma2(cc[i], h[q][i], part);
-                    }
-                    if (OUT) y[q] = pair_sum(part);
-                }
-                if (OUT) s_y[t][tid] = make_float2(y[0], y[1]);
-            }
+        if (OUT && k > 0) finish(t0 - TC, k - 1 & 1, ox, og);
+        if (k + 1 < n_chunk) {
+            stage(t0 + STEP, k + 1 & 1);
+            if (k + 2 < n_chunk) fetch(t0 + 2 * STEP);
         }
-        __syncthreads();
-        if (OUT) {
-            float y[PER][2];
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                float part[2 * L], v[2];
-                upk(value(cx[i]), v[0], v[1]);
-                load_floats<2 * L>(part, &s_y[min(lt + i * LT, TC - 1)][lc / 2 * L].x);
-#pragma unroll
-                for (int q = 1; q < L; ++q) part[0] += part[2 * q], part[1] += part[2 * q + 1];
-                y[i][0] = fmaf(skip[0], v[0], part[0]), y[i][1] = fmaf(skip[1], v[1], part[1]);
-            }
-            if (gated) {
-#pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    float z[2];
-                    upk(value(cg[i]), z[0], z[1]);
-                    y[i][0] = gate_with(y[i][0], z[0]), y[i][1] = gate_with(y[i][1], z[1]);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int t = lt + i * LT;
-                store_pair<VEC>(py + static_cast<long long>(i * LT) * w.D, pk(y[i][0], y[i][1]),
-                                t < TC && t0 + t < t_len ? have : 0);
-            }
-            py += static_cast<long long>(TC) * w.D;
-        }
-        if (k + 1 < n_chunk) stage(t0 + STEP);
+        meet();
     }
-    if (OUT) {  // nothing stands behind a sequence
-        T *py = static_cast<T *>(w.y) + static_cast<long long>(b) * w.T * w.D + ld;
+    if (OUT) {
+        if (n_chunk > 0) finish(t_start + (n_chunk - 1) * TC, n_chunk - 1 & 1, cx, cg);
+        // nothing stands behind a sequence
+        py = static_cast<T *>(w.y) + static_cast<long long>(b) * w.T * w.D + ld;
         for (int t = max(t_len, t_first) + lt; t < t_end; t += LT) store_pair<VEC>(py + static_cast<long long>(t) * w.D, 0ull, have);
     }
-    float *last = SUMS ? (REV ? w.rev_state : w.seg_state) + seg * all : w.h;
-    if (SUMS || (OUT && seg == w.n_seg - 1)) {
-        if (owns > 0) store_states(h[0], last + state_at, n0, w.N, vec);
-        if (owns > 1) store_states(h[1], last + state_at + w.N, n0, w.N, vec);
-    }
     if (SUMS) {
+        u64 *s_sum = reinterpret_cast<u64 *>(smem);  // the states' threads are done with it
         s_sum[tid] = sum;
-        __syncthreads();
+        asm volatile("bar.sync 2, %0;" ::"n"(kThr) : "memory");
         if (tid < CH / 2) {
             u64 s = 0;
 #pragma unroll
@@ -282,18 +315,28 @@ long long ctas(const SsArgs &a, Lanes f) {
 }
 Lanes lanes_for(const SsArgs &a) {
     const Lanes four = lanes_of(a.N, 4);
-    return ctas(a, four) * a.n_seg < 148 && a.N > 2 ? lanes_of(a.N, 2) : four;
+    return ctas(a, four) * a.n_seg < 100 && a.N > 2 ? lanes_of(a.N, 2) : four;
+}
+template <typename T, int S, int L, Pass PASS, bool VEC>
+cudaError_t launch_pass(const SsArgs &a, cudaStream_t s) {
+    const auto kernel = ss_sweep_kernel<T, S, L, PASS, VEC>;
+    constexpr int bytes = sizeof(SweepSmem<S, L, PASS == kOutputs>);
+    if (bytes > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+    }
+    kernel<<<static_cast<unsigned>(ctas(a, {S, L}) * a.n_seg), 2 * kThr, bytes, s>>>(a);
+    return cudaGetLastError();
 }
 template <typename T, int S, int L, bool VEC>
-void launch_sweep(const SsArgs &a, Pass pass, cudaStream_t s) {
-    const unsigned grid = static_cast<unsigned>(ctas(a, {S, L}) * a.n_seg);
-    if (pass == kOutputs) ss_sweep_kernel<T, S, L, kOutputs, VEC><<<grid, kThr, 0, s>>>(a);
-    else if (pass == kSums) ss_sweep_kernel<T, S, L, kSums, VEC><<<grid, kThr, 0, s>>>(a);
-    else if (pass == kStates) ss_sweep_kernel<T, S, L, kStates, VEC><<<grid, kThr, 0, s>>>(a);
-    else ss_sweep_kernel<T, S, L, kReverseSums, VEC><<<grid, kThr, 0, s>>>(a);
+cudaError_t launch_sweep(const SsArgs &a, Pass pass, cudaStream_t s) {
+    if (pass == kOutputs) return launch_pass<T, S, L, kOutputs, VEC>(a, s);
+    if (pass == kSums) return launch_pass<T, S, L, kSums, VEC>(a, s);
+    if (pass == kStates) return launch_pass<T, S, L, kStates, VEC>(a, s);
+    return launch_pass<T, S, L, kReverseSums, VEC>(a, s);
 }
 template <typename T, bool VEC>
-void sweep_of(const SsArgs &a, Pass pass, cudaStream_t s) {
+cudaError_t sweep_of(const SsArgs &a, Pass pass, cudaStream_t s) {
     const Lanes f = lanes_for(a);
 #define PARARNN_SS(S_, L_) \
     if (f.s == S_ && f.l == L_) return launch_sweep<T, S_, L_, VEC>(a, pass, s)
@@ -307,17 +350,12 @@ void sweep_of(const SsArgs &a, Pass pass, cudaStream_t s) {
     PARARNN_SS(2, 16);
     PARARNN_SS(2, 32);
 #undef PARARNN_SS
+    return cudaErrorInvalidValue;
 }
 cudaError_t sweep(const SsArgs &a, Pass pass, cudaStream_t s) {
     const bool vec = ss_pairs_ok(a);
-    if (a.dtype == PARARNN_F32) {
-        if (vec) sweep_of<float, true>(a, pass, s);
-        else sweep_of<float, false>(a, pass, s);
-    } else {
-        if (vec) sweep_of<__nv_bfloat16, true>(a, pass, s);
-        else sweep_of<__nv_bfloat16, false>(a, pass, s);
-    }
-    return cudaGetLastError();
+    if (a.dtype == PARARNN_F32) return vec ? sweep_of<float, true>(a, pass, s) : sweep_of<float, false>(a, pass, s);
+    return vec ? sweep_of<__nv_bfloat16, true>(a, pass, s) : sweep_of<__nv_bfloat16, false>(a, pass, s);
 }
 cudaError_t join(const SsArgs &a, bool reverse, cudaStream_t s) {
     const unsigned grid = static_cast<unsigned>((static_cast<long long>(a.B) * a.D * a.N + 255) / 256);
