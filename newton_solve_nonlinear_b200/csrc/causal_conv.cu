@@ -8,84 +8,212 @@
 
 #include "causal_conv.cuh"
 #include "rows.cuh"
+#include "selective_scan.cuh"
 
 namespace pararnn {
 using namespace rows;
 namespace {
 
-__device__ __forceinline__ float act_of(float p, bool silu) {
-    return silu ? p * __fdividef(1.f, 1.f + expf(-p)) : p;
+// V neighbouring channels of a token as they lie in memory: V 32-bit words, or V / 2 of them (half a one) in bf16
+template <typename T, int V>
+struct Raw {
+    static constexpr int WORDS = sizeof(T) == 4 ? V : (V + 1) / 2;
+    unsigned v[WORDS];
+    __device__ __forceinline__ void get(const T *p) {
+        if constexpr (sizeof(T) * V == 16) {
+            const uint4 q = *reinterpret_cast<const uint4 *>(p);
+            v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+        } else if constexpr (sizeof(T) * V == 8) {
+            const uint2 q = *reinterpret_cast<const uint2 *>(p);
+            v[0] = q.x, v[1] = q.y;
+        } else if constexpr (sizeof(T) * V == 4) {
+            v[0] = *reinterpret_cast<const unsigned *>(p);
+        } else {
+            v[0] = *reinterpret_cast<const unsigned short *>(p);
+        }
+    }
+    __device__ __forceinline__ void to(float (&f)[V]) const {
+#pragma unroll
+        for (int u = 0; u < V; ++u) {
+            if constexpr (sizeof(T) == 4) f[u] = __uint_as_float(v[u]);
+            else f[u] = __uint_as_float(u % 2 == 0 ? v[u / 2] << 16 : v[u / 2] & 0xffff0000u);
+        }
+    }
+};
+template <typename T, int V>
+__device__ __forceinline__ void put(T *p, const float (&f)[V]) {
+    if constexpr (sizeof(T) == 4) {
+        if constexpr (V == 4) *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
+        else if constexpr (V == 2) *reinterpret_cast<float2 *>(p) = make_float2(f[0], f[1]);
+        else *p = f[0];
+    } else if constexpr (V == 1) {
+        *p = __float2bfloat16(f[0]);
+    } else {
+        unsigned v[V / 2];
+#pragma unroll
+        for (int u = 0; u < V; u += 2) {
+            const __nv_bfloat162 q = __floats2bfloat162_rn(f[u], f[u + 1]);
+            v[u / 2] = *reinterpret_cast<const unsigned *>(&q);
+        }
+        if constexpr (V == 4) *reinterpret_cast<uint2 *>(p) = make_uint2(v[0], v[1]);
+        else *reinterpret_cast<unsigned *>(p) = v[0];
+    }
 }
+
+// 1 / (1 + exp(-p)).  bf16 results round 2^-9 of the value away: there the exponent need not carry p log2(e)'s last digits.
+template <typename T>
+__device__ __forceinline__ float sigmoid_t(float p) {
+    if constexpr (sizeof(T) == 4) return ss::sigmoid_of(p);
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(p * -kLog2eF));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ float act_of(float p, bool silu) {
+    return silu ? p * sigmoid_t<T>(p) : p;
+}
+template <typename T>
 __device__ __forceinline__ float slope_of(float p, bool silu) {
     if (!silu) return 1.f;
-    const float s = __fdividef(1.f, 1.f + expf(-p));
+    const float s = sigmoid_t<T>(p);
     return s * fmaf(p, 1.f - s, 1.f);
 }
 
-// x_t of V channels from c on; before the first token the state's rows
+// Where the inputs of one sequence's V channels are.  x_t; before the first token the state's rows; zero elsewhere.
 template <typename T, int V>
-__device__ __forceinline__ void input(const CcArgs &w, int b, long long t, int c, int len, float (&v)[V]) {
-#pragma unroll
-    for (int u = 0; u < V; ++u) v[u] = 0.f;
-    if (t >= 0) {
-        if (t < len) load<V>(static_cast<const T *>(w.x.p) + b * w.x.sb + t * w.x.st + c, v);
-    } else if (w.state != nullptr && t >= 1 - w.W) {
-        load<V>(static_cast<const T *>(w.state) + (static_cast<long long>(b) * (w.W - 1) + t + w.W - 1) * w.D + c, v);
+struct Inputs {
+    const T *x, *state;  // x_0; the state's row W - 1, which would be x_0
+    long long st, D;
+    int len, W;
+    __device__ Inputs(const CcArgs &w, int b, int c)
+        : x(static_cast<const T *>(w.x.p) + b * w.x.sb + c),
+          state(w.state == nullptr ? nullptr
+                                   : static_cast<const T *>(w.state) + (static_cast<long long>(b) * (w.W - 1) + w.W - 1) * w.D + c),
+          st(w.x.st), D(w.D), len(count(w.lengths, b, w.T)), W(w.W) {}
+    __device__ __forceinline__ Raw<T, V> later(long long t) const {  // t >= 0
+        Raw<T, V> r{};
+        if (t < len) r.get(x + t * st);
+        return r;
     }
-}
+    __device__ __forceinline__ Raw<T, V> at(long long t) const {
+        if (t >= 0) return later(t);
+        Raw<T, V> r{};
+        if (state != nullptr && t >= 1 - W) r.get(state + t * D);
+        return r;
+    }
+};
 
-constexpr int kRun = 32;  // tokens of a thread
-
-// A thread takes V channels through kRun tokens with the last W inputs in registers; consecutive threads take consecutive
-// channels.  Bound by HBM.
-template <typename T, int W, int V>
-__global__ void __launch_bounds__(256) cc_forward_kernel(const CcArgs w) {
-    const int nv = w.D / V, runs = (w.T + kRun - 1) / kRun;
-    const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= static_cast<long long>(nv) * runs * w.B) return;
-    const int c = static_cast<int>(i % nv) * V, run = static_cast<int>(i / nv % runs), b = static_cast<int>(i / nv / runs);
-    const int len = count(w.lengths, b, w.T), t0 = run * kRun, t_end = min(w.T, t0 + kRun);
-    const bool silu = w.act == PARARNN_ACT_SILU;
-    float wk[W][V], bias[V] = {}, win[W][V];  // win[k]: x_(t-k)
+template <int W, int V>
+__device__ __forceinline__ void load_filter(const CcArgs &w, int c, float (&wk)[W][V], float (&bias)[V]) {
+    const float *p = w.weight + static_cast<long long>(c) * W;
+    float f[V * W];
+    if constexpr (V == 4) {  // the four filters lie one after the other
+        if (reinterpret_cast<uintptr_t>(w.weight) % 16 == 0) {
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                const float4 q = reinterpret_cast<const float4 *>(p)[i];
+                f[4 * i] = q.x, f[4 * i + 1] = q.y, f[4 * i + 2] = q.z, f[4 * i + 3] = q.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V * W; ++i) f[i] = p[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V * W; ++i) f[i] = p[i];
+    }
 #pragma unroll
     for (int u = 0; u < V; ++u) {
 #pragma unroll
-        for (int k = 0; k < W; ++k) wk[k][u] = w.weight[static_cast<long long>(c + u) * W + W - 1 - k];
-        if (w.bias != nullptr) bias[u] = w.bias[c + u];
+        for (int k = 0; k < W; ++k) wk[k][u] = f[u * W + W - 1 - k];
+        bias[u] = w.bias != nullptr ? w.bias[c + u] : 0.f;
     }
+}
+// p of a token from the window win[k] = x_(t-k), two channels in an operation
+template <int W, int V>
+__device__ __forceinline__ void pre(const float (&wk)[W][V], const float (&bias)[V], const float (&win)[W][V], float (&p)[V]) {
+    if constexpr (V == 1) {
+        p[0] = bias[0];
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) input<T, V>(w, b, t0 - 1 - k, c, len, win[k]);
-    T *y = static_cast<T *>(w.y) + static_cast<long long>(b) * w.T * w.D + c;
-    constexpr int AHEAD = 8;
-    for (int t = t0; t < t_end; t += AHEAD) {
-        float x[AHEAD][V];
+        for (int k = W - 1; k >= 0; --k) p[0] = fmaf(wk[k][0], win[k][0], p[0]);
+    } else {
 #pragma unroll
-        for (int j = 0; j < AHEAD; ++j) input<T, V>(w, b, t + j, c, len, x[j]);
+        for (int u = 0; u < V; u += 2) {
+            u64 s = pk(bias[u], bias[u + 1]);
 #pragma unroll
-        for (int j = 0; j < AHEAD; ++j) {
-#pragma unroll
-            for (int k = W - 1; k > 0; --k)
-#pragma unroll
-                for (int u = 0; u < V; ++u) win[k][u] = win[k - 1][u];
-            float out[V];
-#pragma unroll
-            for (int u = 0; u < V; ++u) {
-                win[0][u] = x[j][u];
-                float p = bias[u];
-#pragma unroll
-                for (int k = W - 1; k >= 0; --k) p = fmaf(wk[k][u], win[k][u], p);
-                out[u] = t + j < len ? act_of(p, silu) : 0.f;
-            }
-            if (t + j < t_end) store<V>(y + static_cast<long long>(t + j) * w.D, out);
+            for (int k = W - 1; k >= 0; --k) s = fma2(pk(wk[k][u], wk[k][u + 1]), pk(win[k][u], win[k][u + 1]), s);
+            upk(s, p[u], p[u + 1]);
         }
     }
-    if (run == 0) {
+}
+// c += a b
+template <int V>
+__device__ __forceinline__ void add_product(const float (&a)[V], const float (&b)[V], float (&c)[V]) {
+    if constexpr (V == 1) {
+        c[0] = fmaf(a[0], b[0], c[0]);
+    } else {
+#pragma unroll
+        for (int u = 0; u < V; u += 2) upk(fma2(pk(a[u], a[u + 1]), pk(b[u], b[u + 1]), pk(c[u], c[u + 1])), c[u], c[u + 1]);
+    }
+}
+template <int W, int V>
+__device__ __forceinline__ void shift(float (&win)[W][V], const float (&x)[V]) {
+#pragma unroll
+    for (int k = W - 1; k > 0; --k)
+#pragma unroll
+        for (int u = 0; u < V; ++u) win[k][u] = win[k - 1][u];
+#pragma unroll
+    for (int u = 0; u < V; ++u) win[0][u] = x[u];
+}
+
+// A thread takes V channels (four where they are aligned) through `run` tokens with the last W inputs in registers and the
+// next tokens' loads on their way; consecutive threads take consecutive channels.  Bound by HBM.
+template <typename T, int W, int V>
+__global__ void __launch_bounds__(256, W <= 4 ? 3 : 2) cc_forward_kernel(const CcArgs w, int run) {
+    const int nv = w.D / V, runs = (w.T + run - 1) / run;
+    const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= static_cast<long long>(nv) * runs * w.B) return;
+    const int c = static_cast<int>(i % nv) * V, r = static_cast<int>(i / nv % runs), b = static_cast<int>(i / nv / runs);
+    const Inputs<T, V> in(w, b, c);
+    const int t0 = r * run, t_end = min(w.T, t0 + run);
+    const bool silu = w.act == PARARNN_ACT_SILU;
+    constexpr int AHEAD = sizeof(T) == 2 ? 8 : 4;
+    Raw<T, V> next[AHEAD];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) next[j] = in.later(t0 + j);
+    float wk[W][V], bias[V], win[W][V], x[V];
+    load_filter(w, c, wk, bias);
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) in.at(t0 - 1 - k).to(win[k]);
+    T *y = static_cast<T *>(w.y) + (static_cast<long long>(b) * w.T + t0) * w.D + c;
+    for (int t = t0; t < t_end; t += AHEAD) {
+        Raw<T, V> now[AHEAD];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) now[j] = next[j];
+        if (t + AHEAD < t_end) {
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) next[j] = in.later(t + AHEAD + j);
+        }
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            now[j].to(x);
+            shift(win, x);
+            float p[V];
+            pre(wk, bias, win, p);
+            const bool on = t + j < in.len;
+#pragma unroll
+            for (int u = 0; u < V; ++u) p[u] = on ? act_of<T>(p[u], silu) : 0.f;
+            if (t + j < t_end) put<T, V>(y, p);
+            y += w.D;
+        }
+    }
+    if (r == 0) {
         T *last = static_cast<T *>(w.last) + static_cast<long long>(b) * (W - 1) * w.D + c;
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
-            float x[V];
-            input<T, V>(w, b, static_cast<long long>(len) - (W - 1) + j, c, len, x);
-            store<V>(last + static_cast<long long>(j) * w.D, x);
+            in.at(static_cast<long long>(in.len) - (W - 1) + j).to(x);
+            put<T, V>(last + static_cast<long long>(j) * w.D, x);
         }
     }
 }
@@ -93,81 +221,83 @@ __global__ void __launch_bounds__(256) cc_forward_kernel(const CcArgs w) {
 // The same walk for dx, W - 1 tokens behind p; a CTA is tx vectors of channels by 256 / tx runs, and keeps its sums for the
 // parameters in registers over all the runs it takes.
 template <typename T, int W, int V>
-__global__ void __launch_bounds__(256) cc_backward_kernel(const CcArgs w, int tx) {
-    extern __shared__ float s_part[];  // [256][V (W + 1)] turned to [V (W + 1)][256]
+__global__ void __launch_bounds__(256, W <= 4 ? 3 : 2) cc_backward_kernel(const CcArgs w, int tx, int run) {
+    extern __shared__ float s_part[];  // [V (W + 1)][256]
     const int x_of = threadIdx.x % tx, y_of = threadIdx.x / tx, ty = 256 / tx;
     const int c = (blockIdx.x * tx + x_of) * V;
-    const int runs = (w.T + kRun - 1) / kRun;
+    const int runs = (w.T + run - 1) / run;
     const long long all = static_cast<long long>(runs) * w.B;
     const bool silu = w.act == PARARNN_ACT_SILU, on = c < w.D;
     float wk[W][V] = {}, bias[V] = {}, dw[W][V] = {}, db[V] = {};
     if (on) {
-#pragma unroll
-        for (int u = 0; u < V; ++u) {
-#pragma unroll
-            for (int k = 0; k < W; ++k) wk[k][u] = w.weight[static_cast<long long>(c + u) * W + W - 1 - k];
-            if (w.bias != nullptr) bias[u] = w.bias[c + u];
-        }
+        load_filter(w, c, wk, bias);
         for (long long i = static_cast<long long>(blockIdx.y) * ty + y_of; i < all; i += static_cast<long long>(gridDim.y) * ty) {
-            const int run = static_cast<int>(i % runs), b = static_cast<int>(i / runs);
-            const int len = count(w.lengths, b, w.T), t0 = run * kRun, t_end = min(w.T, t0 + kRun);
-            const int from = run == 0 ? 1 - W : t0;  // of dx, the state's rows among it
-            float win[W][V] = {}, q[W][V] = {};       // win[k]: x_(t-k); q[k]: q_(t-k)
-            // x before the first q that is needed: of token max(from, 0)
-#pragma unroll
-            for (int k = 0; k < W - 1; ++k) input<T, V>(w, b, max(from, 0) - 1 - k, c, len, win[k]);
+            const int r = static_cast<int>(i % runs), b = static_cast<int>(i / runs);
+            const Inputs<T, V> in(w, b, c);
+            const int t0 = r * run, t_end = min(w.T, t0 + run), len = in.len;
+            const int from = r == 0 ? 1 - W : t0;  // of dx, the state's rows among it
             const T *pdy = static_cast<const T *>(w.dy.p) + b * w.dy.sb + c;
+            auto grad = [&](int t) {
+                Raw<T, V> g{};
+                if (t < len) g.get(pdy + t * w.dy.st);
+                return g;
+            };
             constexpr int AHEAD = 4;
-            for (int t = max(from, 0); t < t_end + W - 1; t += AHEAD) {
-                float x[AHEAD][V], g[AHEAD][V];
+            Raw<T, V> nx[AHEAD], ng[AHEAD];
 #pragma unroll
-                for (int j = 0; j < AHEAD; ++j) {
-                    input<T, V>(w, b, t + j, c, len, x[j]);
+            for (int j = 0; j < AHEAD; ++j) nx[j] = in.later(t0 + j), ng[j] = grad(t0 + j);
+            float win[W][V], q[W][V] = {}, x[V], g[V];  // win[k]: x_(t-k); q[k]: q_(t-k)
 #pragma unroll
-                    for (int u = 0; u < V; ++u) g[j][u] = 0.f;
-                    if (t + j < len) load<V>(pdy + (t + j) * w.dy.st, g[j]);
+            for (int k = 0; k < W - 1; ++k) in.at(t0 - 1 - k).to(win[k]);
+            const int stop = t_end + W - 1;
+            for (int t = t0; t < stop; t += AHEAD) {
+                Raw<T, V> cx[AHEAD], cg[AHEAD];
+#pragma unroll
+                for (int j = 0; j < AHEAD; ++j) cx[j] = nx[j], cg[j] = ng[j];
+                if (t + AHEAD < stop) {
+#pragma unroll
+                    for (int j = 0; j < AHEAD; ++j) nx[j] = in.later(t + AHEAD + j), ng[j] = grad(t + AHEAD + j);
                 }
 #pragma unroll
                 for (int j = 0; j < AHEAD; ++j) {
                     const int at = t + j, back = at - (W - 1);  // dx that is complete with q_at
+                    cx[j].to(x), cg[j].to(g);
+                    shift(win, x);
+                    float p[V], out[V];
+                    pre(wk, bias, win, p);
 #pragma unroll
-                    for (int k = W - 1; k > 0; --k)
-#pragma unroll
-                        for (int u = 0; u < V; ++u) win[k][u] = win[k - 1][u], q[k][u] = q[k - 1][u];
-                    float out[V];
+                    for (int u = 0; u < V; ++u) p[u] = at < len ? g[u] * slope_of<T>(p[u], silu) : 0.f;
+                    shift(q, p);
+                    const bool own = at < t_end;
+                    float mine[V];
 #pragma unroll
                     for (int u = 0; u < V; ++u) {
-                        win[0][u] = x[j][u];
-                        float p = bias[u];
+                        mine[u] = own ? p[u] : 0.f;
+                        db[u] += mine[u];
+                        out[u] = 0.f;
+                    }
 #pragma unroll
-                        for (int k = W - 1; k >= 0; --k) p = fmaf(wk[k][u], win[k][u], p);
-                        q[0][u] = at < len ? g[j][u] * slope_of(p, silu) : 0.f;
-                        const float own = at < t_end ? q[0][u] : 0.f;
-                        db[u] += own;
-                        float sum = 0.f;
-#pragma unroll
-                        for (int k = 0; k < W; ++k) {
-                            dw[k][u] = fmaf(own, win[k][u], dw[k][u]);
-                            sum = fmaf(wk[W - 1 - k][u], q[k][u], sum);
-                        }
-                        out[u] = sum;
+                    for (int k = 0; k < W; ++k) {
+                        add_product(mine, win[k], dw[k]);
+                        add_product(wk[W - 1 - k], q[k], out);
                     }
                     if (back >= from && back < t_end) {
                         const int j_last = back - len + W - 1;  // the row of dlast that is x_back
                         if (w.dlast != nullptr && j_last >= 0 && j_last < W - 1) {
-                            float l[V];
-                            load<V>(static_cast<const T *>(w.dlast) + (static_cast<long long>(b) * (W - 1) + j_last) * w.D + c, l);
+                            Raw<T, V> l;
+                            l.get(static_cast<const T *>(w.dlast) + (static_cast<long long>(b) * (W - 1) + j_last) * w.D + c);
+                            l.to(x);
 #pragma unroll
-                            for (int u = 0; u < V; ++u) out[u] += l[u];
+                            for (int u = 0; u < V; ++u) out[u] += x[u];
                         }
                         if (back >= 0) {
                             if (back >= len) {
 #pragma unroll
                                 for (int u = 0; u < V; ++u) out[u] = 0.f;
                             }
-                            store<V>(static_cast<T *>(w.dx) + (static_cast<long long>(b) * w.T + back) * w.D + c, out);
+                            put<T, V>(static_cast<T *>(w.dx) + (static_cast<long long>(b) * w.T + back) * w.D + c, out);
                         } else if (w.dstate != nullptr) {
-                            store<V>(static_cast<T *>(w.dstate) + (static_cast<long long>(b) * (W - 1) + back + W - 1) * w.D + c, out);
+                            put<T, V>(static_cast<T *>(w.dstate) + (static_cast<long long>(b) * (W - 1) + back + W - 1) * w.D + c, out);
                         }
                     }
                 }
@@ -237,7 +367,7 @@ __global__ void __launch_bounds__(128) cc_step_kernel(const CcStep w) {
                 if (j > 0) store<V>(dst + static_cast<long long>(j - 1) * w.D, x);
             }
 #pragma unroll
-            for (int u = 0; u < V; ++u) p[u] = act_of(p[u], silu);
+            for (int u = 0; u < V; ++u) p[u] = act_of<T>(p[u], silu);
             store<V>(py + static_cast<long long>(b) * w.D + c, p);
         }
         if (w.slots == nullptr) return;
@@ -256,36 +386,44 @@ __global__ void __launch_bounds__(128) cc_step_kernel(const CcStep w) {
 
 size_t esize(int dtype) { return dtype == PARARNN_F32 ? 4 : 2; }
 bool on16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
-// rows whose vectors of four start on their own alignment
-bool rows4(const CcRows &r, int dtype) {
-    return reinterpret_cast<uintptr_t>(r.p) % (4 * esize(dtype)) == 0 && r.sb % 4 == 0 && r.st % 4 == 0;
+// rows whose vectors of v channels start on their own alignment
+bool rows_on(const CcRows &r, int dtype, int v) {
+    return reinterpret_cast<uintptr_t>(r.p) % (v * esize(dtype)) == 0 && r.sb % v == 0 && r.st % v == 0;
 }
 
+// Tokens of a thread: long runs read less of their neighbours, short ones fill the card (two waves of 2048 threads per SM)
+int run_of(const CcArgs &a, int v) {
+    const long long at_64 = static_cast<long long>(a.D / v) * a.B * ((a.T + 63) / 64);
+    for (int run = 64; run > 8; run /= 2)
+        if (at_64 * (64 / run) >= 148 * 4096) return run;
+    return 8;
+}
 template <typename T, int W>
 void forward_of(const CcArgs &a, bool vec, cudaStream_t s) {
-    const long long n = static_cast<long long>(a.D / (vec ? 4 : 1)) * ((a.T + kRun - 1) / kRun) * a.B;
+    const int v = vec ? 4 : 1, run = run_of(a, v);
+    const long long n = static_cast<long long>(a.D / v) * ((a.T + run - 1) / run) * a.B;
     const unsigned grid = static_cast<unsigned>((n + 255) / 256);
-    if (vec) cc_forward_kernel<T, W, 4><<<grid, 256, 0, s>>>(a);
-    else cc_forward_kernel<T, W, 1><<<grid, 256, 0, s>>>(a);
+    if (vec) cc_forward_kernel<T, W, 4><<<grid, 256, 0, s>>>(a, run);
+    else cc_forward_kernel<T, W, 1><<<grid, 256, 0, s>>>(a, run);
 }
 struct Grid {
-    int tx, x, y;
+    int tx, x, y, run;
 };
 Grid backward_grid(const CcArgs &a, int v) {
-    const int nv = (a.D + v - 1) / v;
+    const int nv = (a.D + v - 1) / v, run = std::min(run_of(a, v), 32);
     int tx = 1;
     while (tx < nv && tx < 32) tx *= 2;
     const int x = (nv + tx - 1) / tx, ty = 256 / tx;
-    const long long all = static_cast<long long>((a.T + kRun - 1) / kRun) * a.B;
+    const long long all = static_cast<long long>((a.T + run - 1) / run) * a.B;
     const long long y = std::min<long long>((all + ty - 1) / ty, std::max(1, (148 * 4 + x - 1) / x));
-    return {tx, x, static_cast<int>(y)};
+    return {tx, x, static_cast<int>(y), run};
 }
 template <typename T, int W>
 void backward_of(const CcArgs &a, bool vec, cudaStream_t s) {
-    const Grid g = backward_grid(a, vec ? 4 : 1);
+    const Grid g = backward_grid(a, vec ? 2 : 1);
     const dim3 grid(g.x, g.y);
-    if (vec) cc_backward_kernel<T, W, 4><<<grid, 256, 256 * 4 * (W + 1) * sizeof(float), s>>>(a, g.tx);
-    else cc_backward_kernel<T, W, 1><<<grid, 256, 256 * (W + 1) * sizeof(float), s>>>(a, g.tx);
+    if (vec) cc_backward_kernel<T, W, 2><<<grid, 256, 256 * 2 * (W + 1) * sizeof(float), s>>>(a, g.tx, g.run);
+    else cc_backward_kernel<T, W, 1><<<grid, 256, 256 * (W + 1) * sizeof(float), s>>>(a, g.tx, g.run);
 }
 
 template <typename T, int W>
@@ -309,30 +447,30 @@ void launch_width(const CcArgs &a, bool back, bool vec, cudaStream_t s) {
 }  // namespace
 
 int cc_backward_rows(const CcArgs &a) {
-    return std::max(backward_grid(a, 1).y, a.D % 4 == 0 ? backward_grid(a, 4).y : 1);
+    return std::max(backward_grid(a, 1).y, a.D % 2 == 0 ? backward_grid(a, 2).y : 1);
 }
 
 cudaError_t launch_cc_forward(const CcArgs &a, cudaStream_t s) {
-    const bool vec = a.D % 4 == 0 && rows4(a.x, a.dtype) && on16(a.state) && on16(a.y) && on16(a.last);
+    const bool vec = a.D % 4 == 0 && rows_on(a.x, a.dtype, 4) && on16(a.state) && on16(a.y) && on16(a.last);
     if (a.dtype == PARARNN_F32) launch_width<float>(a, false, vec, s);
     else launch_width<__nv_bfloat16>(a, false, vec, s);
     return cudaGetLastError();
 }
 
 cudaError_t launch_cc_backward(const CcArgs &a, cudaStream_t s) {
-    const bool vec = a.D % 4 == 0 && rows4(a.x, a.dtype) && rows4(a.dy, a.dtype) && on16(a.state) && on16(a.dlast);
+    const bool vec = a.D % 2 == 0 && rows_on(a.x, a.dtype, 2) && rows_on(a.dy, a.dtype, 2) && on16(a.state) && on16(a.dlast);
     if (a.dtype == PARARNN_F32) launch_width<float>(a, true, vec, s);
     else launch_width<__nv_bfloat16>(a, true, vec, s);
     cudaError_t e = cudaGetLastError();
     const long long n = static_cast<long long>(a.D) * a.W, stride = n + a.D;
-    const int parts = backward_grid(a, vec ? 4 : 1).y;
+    const int parts = backward_grid(a, vec ? 2 : 1).y;
     if (e == cudaSuccess) e = launch_rows_sum(a.part, a.dweight, parts, n, stride, s);
     if (e == cudaSuccess) e = launch_rows_sum(a.part + n, a.dbias, parts, a.D, stride, s);
     return e;
 }
 
 cudaError_t launch_cc_step(const CcStep &w, cudaStream_t s) {
-    const bool vec = w.D % 4 == 0 && rows4(w.x, w.dtype);
+    const bool vec = w.D % 4 == 0 && rows_on(w.x, w.dtype, 4);
     const int nv = w.D / (vec ? 4 : 1);
     const unsigned grid = static_cast<unsigned>((nv + 127) / 128) * w.B;
     if (w.dtype == PARARNN_F32) {
