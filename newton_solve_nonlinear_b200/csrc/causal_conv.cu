@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(256, W <= 4 ? 3 : 2) cc_forward_kernel(const C
     const Inputs<T, V> in(w, b, c);
     const int t0 = r * run, t_end = min(w.T, t0 + run);
     const bool silu = w.act == PARARNN_ACT_SILU;
-    constexpr int AHEAD = sizeof(T) == 2 ? 8 : 4;
+    constexpr int AHEAD = 4;
     Raw<T, V> next[AHEAD];
 #pragma unroll
     for (int j = 0; j < AHEAD; ++j) next[j] = in.later(t0 + j);
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(256, W <= 4 ? 3 : 2) cc_forward_kernel(const C
 // The same walk for dx, W - 1 tokens behind p; a CTA is tx vectors of channels by 256 / tx runs, and keeps its sums for the
 // parameters in registers over all the runs it takes.
 template <typename T, int W, int V>
-__global__ void __launch_bounds__(256, W <= 4 ? 3 : 2) cc_backward_kernel(const CcArgs w, int tx, int run) {
+__global__ void __launch_bounds__(256, 2) cc_backward_kernel(const CcArgs w, int tx, int run) {
     extern __shared__ float s_part[];  // [V (W + 1)][256]
     const int x_of = threadIdx.x % tx, y_of = threadIdx.x / tx, ty = 256 / tx;
     const int c = (blockIdx.x * tx + x_of) * V;
@@ -246,9 +246,52 @@ __global__ void __launch_bounds__(256, W <= 4 ? 3 : 2) cc_backward_kernel(const 
             Raw<T, V> nx[AHEAD], ng[AHEAD];
 #pragma unroll
             for (int j = 0; j < AHEAD; ++j) nx[j] = in.later(t0 + j), ng[j] = grad(t0 + j);
-            float win[W][V], q[W][V] = {}, x[V], g[V];  // win[k]: x_(t-k); q[k]: q_(t-k)
+            float win[W][V] = {}, q[W][V] = {}, x[V], g[V];  // win[k]: x_(t-k); q[k]: q_(t-k)
 #pragma unroll
             for (int k = 0; k < W - 1; ++k) in.at(t0 - 1 - k).to(win[k]);
+            // token `at`: its q, and dx of token at - (W - 1), which is complete with it; own: not one behind the run
+            T *dx = static_cast<T *>(w.dx) + (static_cast<long long>(b) * w.T + t0 - (W - 1)) * w.D + c;
+            const int plain = max(len - W, -1) + 1;  // dx of tokens 0 .. plain - 1 has no part of dlast and counts
+            auto token = [&](int at, bool own, const Raw<T, V> &rx, const Raw<T, V> &rg) {
+                rx.to(x), rg.to(g);
+                shift(win, x);
+                float p[V], out[V] = {};
+                pre(wk, bias, win, p);
+#pragma unroll
+                for (int u = 0; u < V; ++u) p[u] = g[u] * slope_of<T>(p[u], silu);  // g is zero behind the sequence
+                shift(q, p);
+#pragma unroll
+                for (int u = 0; u < V; ++u) {
+                    if (!own) p[u] = 0.f;
+                    db[u] += p[u];
+                }
+#pragma unroll
+                for (int k = 0; k < W; ++k) {
+                    add_product(p, win[k], dw[k]);
+                    add_product(wk[W - 1 - k], q[k], out);
+                }
+                const int back = at - (W - 1);
+                if (back >= from && back < t_end) {
+                    if (static_cast<unsigned>(back) >= static_cast<unsigned>(plain)) {
+                        const int j_last = back - len + W - 1;  // the row of dlast that is x_back
+                        if (w.dlast != nullptr && j_last >= 0 && j_last < W - 1) {
+                            Raw<T, V> l;
+                            l.get(static_cast<const T *>(w.dlast) + (static_cast<long long>(b) * (W - 1) + j_last) * w.D + c);
+                            l.to(x);
+#pragma unroll
+                            for (int u = 0; u < V; ++u) out[u] += x[u];
+                        }
+                        if (back >= len) {
+#pragma unroll
+                            for (int u = 0; u < V; ++u) out[u] = 0.f;
+                        }
+                    }
+                    if (back >= 0) put<T, V>(dx, out);
+                    else if (w.dstate != nullptr)
+                        put<T, V>(static_cast<T *>(w.dstate) + (static_cast<long long>(b) * (W - 1) + back + W - 1) * w.D + c, out);
+                }
+                dx += w.D;
+            };
             const int stop = t_end + W - 1;
             for (int t = t0; t < stop; t += AHEAD) {
                 Raw<T, V> cx[AHEAD], cg[AHEAD];
@@ -258,48 +301,12 @@ __global__ void __launch_bounds__(256, W <= 4 ? 3 : 2) cc_backward_kernel(const 
 #pragma unroll
                     for (int j = 0; j < AHEAD; ++j) nx[j] = in.later(t + AHEAD + j), ng[j] = grad(t + AHEAD + j);
                 }
+                if (t + AHEAD <= t_end) {
 #pragma unroll
-                for (int j = 0; j < AHEAD; ++j) {
-                    const int at = t + j, back = at - (W - 1);  // dx that is complete with q_at
-                    cx[j].to(x), cg[j].to(g);
-                    shift(win, x);
-                    float p[V], out[V];
-                    pre(wk, bias, win, p);
+                    for (int j = 0; j < AHEAD; ++j) token(t + j, true, cx[j], cg[j]);
+                } else {
 #pragma unroll
-                    for (int u = 0; u < V; ++u) p[u] = at < len ? g[u] * slope_of<T>(p[u], silu) : 0.f;
-                    shift(q, p);
-                    const bool own = at < t_end;
-                    float mine[V];
-#pragma unroll
-                    for (int u = 0; u < V; ++u) {
-                        mine[u] = own ? p[u] : 0.f;
-                        db[u] += mine[u];
-                        out[u] = 0.f;
-                    }
-#pragma unroll
-                    for (int k = 0; k < W; ++k) {
-                        add_product(mine, win[k], dw[k]);
-                        add_product(wk[W - 1 - k], q[k], out);
-                    }
-                    if (back >= from && back < t_end) {
-                        const int j_last = back - len + W - 1;  // the row of dlast that is x_back
-                        if (w.dlast != nullptr && j_last >= 0 && j_last < W - 1) {
-                            Raw<T, V> l;
-                            l.get(static_cast<const T *>(w.dlast) + (static_cast<long long>(b) * (W - 1) + j_last) * w.D + c);
-                            l.to(x);
-#pragma unroll
-                            for (int u = 0; u < V; ++u) out[u] += x[u];
-                        }
-                        if (back >= 0) {
-                            if (back >= len) {
-#pragma unroll
-                                for (int u = 0; u < V; ++u) out[u] = 0.f;
-                            }
-                            put<T, V>(static_cast<T *>(w.dx) + (static_cast<long long>(b) * w.T + back) * w.D + c, out);
-                        } else if (w.dstate != nullptr) {
-                            put<T, V>(static_cast<T *>(w.dstate) + (static_cast<long long>(b) * (W - 1) + back + W - 1) * w.D + c, out);
-                        }
-                    }
+                    for (int j = 0; j < AHEAD; ++j) token(t + j, t + j < t_end, cx[j], cg[j]);
                 }
             }
         }
