@@ -21,17 +21,84 @@ __device__ __forceinline__ float warp_sum(float v) {
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
-// the sum over a team's threads, to all of them; s: one float per warp of the CTA, two of them used in turn
+// The sums of a and b over a team's threads, to all of them.  s: a pair per warp of the CTA, twice, used in turn (`turn`
+// counts the calls): one barrier is enough, as the next call writes elsewhere.
 template <int TEAM>
-__device__ __forceinline__ float team_sum(float v, float *s) {
-    v = warp_sum(v);
+__device__ __forceinline__ float2 team_sum(float a, float b, float2 (*s)[32], int &turn) {
+    a = warp_sum(a), b = warp_sum(b);
     if constexpr (TEAM > 32) {
+        float2 *at = s[turn++ & 1];
+        if ((threadIdx.x & 31) == 0) at[threadIdx.x >> 5] = make_float2(a, b);
         __syncthreads();
-        if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-        __syncthreads();
-        v = warp_sum((threadIdx.x & 31) < TEAM / 32 ? s[threadIdx.x & 31] : 0.f);
+        const float2 v = (threadIdx.x & 31) < TEAM / 32 ? at[threadIdx.x & 31] : make_float2(0.f, 0.f);
+        a = warp_sum(v.x), b = warp_sum(v.y);
     }
-    return v;
+    return make_float2(a, b);
+}
+template <int TEAM>
+__device__ __forceinline__ float team_sum(float a, float2 (*s)[32], int &turn) {
+    return team_sum<TEAM>(a, 0.f, s, turn).x;
+}
+
+// K vectors of a row, `step` vectors apart, n of them in all: first as they lie in memory, so that nothing waits for a load
+// before all are under way; the branch on the type stands outside the loop for the same reason.
+template <int V>
+struct Bits {
+    unsigned w[V];
+};
+template <int V, int K>
+__device__ __forceinline__ void fetch(const void *p, long long base, bool f32, int at, int step, int n, Bits<V> (&r)[K]) {
+    if (f32) {
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            const float *q = static_cast<const float *>(p) + base + (at + i * step) * V;
+            if (at + i * step >= n) continue;
+            if constexpr (V == 4) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(q);
+                r[i].w[0] = x.x, r[i].w[1] = x.y, r[i].w[2] = x.z, r[i].w[3] = x.w;
+            } else {
+                r[i].w[0] = *reinterpret_cast<const unsigned *>(q);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p) + base + (at + i * step) * V;
+            if (at + i * step >= n) continue;
+            if constexpr (V == 4) {
+                const uint2 x = *reinterpret_cast<const uint2 *>(q);
+                r[i].w[0] = x.x, r[i].w[1] = x.y;
+            } else {
+                r[i].w[0] = *reinterpret_cast<const unsigned short *>(q);
+            }
+        }
+    }
+}
+template <int V, int K>
+__device__ __forceinline__ void values(const Bits<V> (&r)[K], bool f32, float (&v)[K][V]) {
+    if (f32) {
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+#pragma unroll
+            for (int u = 0; u < V; ++u) v[i][u] = __uint_as_float(r[i].w[u]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+#pragma unroll
+            for (int u = 0; u < V; ++u) v[i][u] = __uint_as_float(u % 2 == 0 ? r[i].w[u / 2] << 16 : r[i].w[u / 2] & 0xffff0000u);
+    }
+}
+template <int V, int K>
+__device__ __forceinline__ void store_all(void *p, long long base, bool f32, int at, int step, int n, const float (&v)[K][V]) {
+    if (f32) {
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+            if (at + i * step < n) store<V>(static_cast<float *>(p) + base + (at + i * step) * V, v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+            if (at + i * step < n) store<V>(static_cast<__nv_bfloat16 *>(p) + base + (at + i * step) * V, v[i]);
+    }
 }
 
 template <int TEAM>
@@ -41,7 +108,8 @@ constexpr int cta_of() { return TEAM > 256 ? TEAM : 256; }
 template <int V, int TEAM, int K>
 __global__ void __launch_bounds__(cta_of<TEAM>()) ln_forward_kernel(const LnArgs w) {
     constexpr int TEAMS = cta_of<TEAM>() / TEAM;
-    __shared__ float s_sum[32];
+    __shared__ float2 s_sum[2][32];
+    int turn = 0;
     const int lane = threadIdx.x % TEAM, nv = w.C / V;
     const long long rows = static_cast<long long>(w.N) * w.S;
     const long long row = static_cast<long long>(blockIdx.x) * TEAMS + threadIdx.x / TEAM;
@@ -86,30 +154,49 @@ __global__ void __launch_bounds__(cta_of<TEAM>()) ln_forward_kernel(const LnArgs
     float m = 0.f, k;
     if constexpr (K > 0) {
         float v[K][V], sum = 0.f;
+        {
+            Bits<V> rx[K] = {}, rr[K] = {};
+            const int n = on ? nv : 0;
+            fetch(w.x, base, xf, lane, TEAM, n, rx);
+            if (w.residual != nullptr) fetch(w.residual, base, rf, lane, TEAM, n, rr);
+            values(rx, xf, v);
+            if (w.residual != nullptr) {
+                float q[K][V];
+                values(rr, rf, q);
 #pragma unroll
-        for (int i = 0; i < K; ++i) {
-            const int at = lane + i * TEAM;
-            if (at < nv) {
-                read(at * V, v[i]);
-            } else {
+                for (int i = 0; i < K; ++i)
 #pragma unroll
-                for (int u = 0; u < V; ++u) v[i][u] = 0.f;
+                    for (int u = 0; u < V; ++u) v[i][u] += q[i][u];
             }
+        }
+        if (w.r != nullptr) store_all(w.r, base, rf, lane, TEAM, nv, v);
+#pragma unroll
+        for (int i = 0; i < K; ++i)
 #pragma unroll
             for (int u = 0; u < V; ++u) sum += v[i][u];
-        }
-        if (!w.rms) m = team_sum<TEAM>(sum, s_sum) * per;
+        if (!w.rms) m = team_sum<TEAM>(sum, s_sum, turn) * per;
         sum = 0.f;
 #pragma unroll
         for (int i = 0; i < K; ++i)
             if (lane + i * TEAM < nv) {
 #pragma unroll
-                for (int u = 0; u < V; ++u) sum = fmaf(v[i][u] - m, v[i][u] - m, sum);
+                for (int u = 0; u < V; ++u) v[i][u] -= m, sum = fmaf(v[i][u], v[i][u], sum);
             }
-        k = rsqrtf(team_sum<TEAM>(sum, s_sum) * per + w.eps);
+        k = rsqrtf(team_sum<TEAM>(sum, s_sum, turn) * per + w.eps);
+        const float scale = on ? k : 0.f;
 #pragma unroll
-        for (int i = 0; i < K; ++i)
-            if (lane + i * TEAM < nv) write((lane + i * TEAM) * V, v[i], m, k);
+        for (int i = 0; i < K; ++i) {
+            if (lane + i * TEAM >= nv) continue;
+            const int c = (lane + i * TEAM) * V;
+            float g[V], o[V];
+#pragma unroll
+            for (int u = 0; u < V; ++u) g[u] = 1.f, o[u] = 0.f;
+            if (w.weight != nullptr) load<V>(w.weight + c, g);
+            if (w.bias != nullptr && on) load<V>(w.bias + c, o);
+#pragma unroll
+            for (int u = 0; u < V; ++u) v[i][u] = fmaf(v[i][u] * scale, g[u], o[u]);
+        }
+        store_all(w.y, base, yf, lane, TEAM, nv, v);
     } else {
         float v[V], sum = 0.f;
         if (!w.rms) {
@@ -118,7 +205,7 @@ __global__ void __launch_bounds__(cta_of<TEAM>()) ln_forward_kernel(const LnArgs
 #pragma unroll
                 for (int u = 0; u < V; ++u) sum += v[u];
             }
-            m = team_sum<TEAM>(sum, s_sum) * per;
+            m = team_sum<TEAM>(sum, s_sum, turn) * per;
         }
         sum = 0.f;
         for (int at = lane; at < nv; at += TEAM) {
@@ -126,7 +213,7 @@ __global__ void __launch_bounds__(cta_of<TEAM>()) ln_forward_kernel(const LnArgs
 #pragma unroll
             for (int u = 0; u < V; ++u) sum = fmaf(v[u] - m, v[u] - m, sum);
         }
-        k = rsqrtf(team_sum<TEAM>(sum, s_sum) * per + w.eps);
+        k = rsqrtf(team_sum<TEAM>(sum, s_sum, turn) * per + w.eps);
         for (int at = lane; at < nv; at += TEAM) {
             read(at * V, v);
             write(at * V, v, m, k);
@@ -140,7 +227,8 @@ __global__ void __launch_bounds__(cta_of<TEAM>()) ln_forward_kernel(const LnArgs
 template <int V, int TEAM, int K>
 __global__ void __launch_bounds__(cta_of<TEAM>()) ln_backward_kernel(const LnArgs w) {
     constexpr int TEAMS = cta_of<TEAM>() / TEAM, KK = K > 0 ? K : 1;
-    __shared__ float s_sum[32];
+    __shared__ float2 s_sum[2][32];
+    int turn = 0;
     extern __shared__ float s_part[];  // TEAM = 32: [8][2 C]
     const int lane = threadIdx.x % TEAM, team = threadIdx.x / TEAM, nv = w.C / V;
     const long long rows = static_cast<long long>(w.N) * w.S;
@@ -188,24 +276,47 @@ __global__ void __launch_bounds__(cta_of<TEAM>()) ln_backward_kernel(const LnArg
         const float m = w.stats[2 * row], k = w.stats[2 * row + 1];
         float su = 0.f, suh = 0.f;
         if constexpr (K > 0) {
-            float u[K][V], h[K][V];
+            float u[K][V], h[K][V], dys[K][V];
+            Bits<V> ri[K];
+            {
+                Bits<V> rr[K], ry[K];
+                fetch(w.r, base, rf, lane, TEAM, nv, rr);
+                fetch(w.y, base, yf, lane, TEAM, nv, ry);
+                if (w.dr_in != nullptr) fetch(w.dr_in, base, rf, lane, TEAM, nv, ri);
+                values(rr, rf, h), values(ry, yf, dys);
+            }
 #pragma unroll
             for (int i = 0; i < K; ++i) {
                 const int at = lane + i * TEAM;
                 if (at >= nv) continue;
-                float dy[V];
-                read(base, at * V, m, k, u[i], h[i], dy);
+                const float(&dy)[V] = dys[i];
+                float g[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) g[j] = 1.f;
+                if (w.weight != nullptr) load<V>(w.weight + at * V, g);
+#pragma unroll
+                for (int j = 0; j < V; ++j) h[i][j] = (h[i][j] - m) * k, u[i][j] = dy[j] * g[j];
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     su += u[i][j], suh = fmaf(u[i][j], h[i][j], suh);
                     dw[i][j] = fmaf(dy[j], h[i][j], dw[i][j]), db[i][j] += dy[j];
                 }
             }
-            su = w.rms ? 0.f : team_sum<TEAM>(su, s_sum) * per;
-            suh = team_sum<TEAM>(suh, s_sum) * per;
+            const float2 sums = team_sum<TEAM>(su, suh, s_sum, turn);
+            su = w.rms ? 0.f : sums.x * per, suh = sums.y * per;
 #pragma unroll
             for (int i = 0; i < K; ++i)
-                if (lane + i * TEAM < nv) write(base, (lane + i * TEAM) * V, k, su, suh, u[i], h[i]);
+#pragma unroll
+                for (int j = 0; j < V; ++j) u[i][j] = k * (u[i][j] - su - h[i][j] * suh);
+            if (w.dr_in != nullptr) {
+                values(ri, rf, h);
+#pragma unroll
+                for (int i = 0; i < K; ++i)
+#pragma unroll
+                    for (int j = 0; j < V; ++j) u[i][j] += h[i][j];
+            }
+            store_all(w.dr, base, rf, lane, TEAM, nv, u);
+            if (w.dx != nullptr) store_all(w.dx, base, xf, lane, TEAM, nv, u);
         } else {
             float u[V], h[V], dy[V];
             for (int at = lane; at < nv; at += TEAM) {
@@ -213,8 +324,8 @@ __global__ void __launch_bounds__(cta_of<TEAM>()) ln_backward_kernel(const LnArg
 #pragma unroll
                 for (int j = 0; j < V; ++j) su += u[j], suh = fmaf(u[j], h[j], suh);
             }
-            su = w.rms ? 0.f : team_sum<TEAM>(su, s_sum) * per;
-            suh = team_sum<TEAM>(suh, s_sum) * per;
+            const float2 sums = team_sum<TEAM>(su, suh, s_sum, turn);
+            su = w.rms ? 0.f : sums.x * per, suh = sums.y * per;
             for (int at = lane; at < nv; at += TEAM) {
                 read(base, at * V, m, k, u, h, dy);
                 write(base, at * V, k, su, suh, u, h);
@@ -268,15 +379,20 @@ __global__ void __launch_bounds__(256) ln_columns_kernel(const LnArgs w) {
     }
 }
 
-// Which kernel takes a row: threads of a team and vectors of a thread.
+// Which kernel takes a row: threads of a team and vectors of a thread.  A warp needs no barrier, and forward holds up to
+// 512 vectors of a row; backward, with its sums for the parameters, 128.
 struct Fit {
     int v, team, k;
 };
-Fit fit(const LnArgs &a) {
+Fit fit(const LnArgs &a, bool back) {
     const int v = a.C % 4 == 0 ? 4 : 1, nv = a.C / v;
     if (nv <= 32) return {v, 32, 1};
     if (nv <= 64) return {v, 32, 2};
     if (nv <= 128) return {v, 32, 4};
+    if (!back && static_cast<long long>(a.N) * a.S >= 148 * 8) {  // rows for eight warps of each SM
+        if (nv <= 256) return {v, 32, 8};
+        if (nv <= 512) return {v, 32, 16};
+    }
     if (nv <= 256) return {v, 256, 1};
     if (nv <= 512) return {v, 256, 2};
     if (nv <= 1024) return {v, 256, 4};
@@ -296,13 +412,22 @@ void backward(const LnArgs &a, cudaStream_t s) {
     const size_t smem = TEAM == 32 ? 8 * 2 * static_cast<size_t>(a.C) * sizeof(float) : 0;
     ln_backward_kernel<V, TEAM, K><<<ln_backward_rows(a), cta_of<TEAM>(), smem, s>>>(a);
 }
-template <int V>
-void launch(const LnArgs &a, const Fit &f, bool back, cudaStream_t s) {
+template <int V, bool BACK, int TEAM, int K>
+void launch_fit(const LnArgs &a, cudaStream_t s) {
+    if constexpr (BACK) backward<V, TEAM, K>(a, s);
+    else forward<V, TEAM, K>(a, s);
+}
+template <int V, bool BACK>
+void launch(const LnArgs &a, const Fit &f, cudaStream_t s) {
 #define PARARNN_LN(TEAM_, K_) \
-    if (f.team == TEAM_ && f.k == K_) return back ? backward<V, TEAM_, K_>(a, s) : forward<V, TEAM_, K_>(a, s)
+    if (f.team == TEAM_ && f.k == K_) return launch_fit<V, BACK, TEAM_, K_>(a, s)
     PARARNN_LN(32, 1);
     PARARNN_LN(32, 2);
     PARARNN_LN(32, 4);
+    if constexpr (!BACK) {
+        PARARNN_LN(32, 8);
+        PARARNN_LN(32, 16);
+    }
     PARARNN_LN(256, 1);
     PARARNN_LN(256, 2);
     PARARNN_LN(256, 4);
@@ -314,24 +439,24 @@ void launch(const LnArgs &a, const Fit &f, bool back, cudaStream_t s) {
 
 }  // namespace
 
-// CTAs of the backward pass, each of which leaves a row of sums: two per SM, fewer where there are fewer rows
+// CTAs of the backward pass, each of which leaves a row of sums: what fits the card at once, fewer where there are fewer rows
 int ln_backward_rows(const LnArgs &a) {
-    const Fit f = fit(a);
+    const Fit f = fit(a, true);
     const long long rows = static_cast<long long>(a.N) * a.S, teams = f.team == 32 ? 8 : 1;
-    return static_cast<int>(std::min<long long>((rows + teams - 1) / teams, f.team > 256 ? 148 : 296));
+    return static_cast<int>(std::min<long long>((rows + teams - 1) / teams, 148 * (f.team > 256 ? 1 : f.k > 4 ? 2 : 4)));
 }
 
 cudaError_t launch_ln_forward(const LnArgs &a, cudaStream_t s) {
-    const Fit f = fit(a);
-    if (f.v == 4) launch<4>(a, f, false, s);
-    else launch<1>(a, f, false, s);
+    const Fit f = fit(a, false);
+    if (f.v == 4) launch<4, false>(a, f, s);
+    else launch<1, false>(a, f, s);
     return cudaGetLastError();
 }
 
 cudaError_t launch_ln_backward(const LnArgs &a, cudaStream_t s) {
-    const Fit f = fit(a);
-    if (f.v == 4) launch<4>(a, f, true, s);
-    else launch<1>(a, f, true, s);
+    const Fit f = fit(a, true);
+    if (f.v == 4) launch<4, true>(a, f, s);
+    else launch<1, true>(a, f, s);
     cudaError_t e = cudaGetLastError();
     const int rows = ln_backward_rows(a);
     if (e == cudaSuccess && f.k == 0) {

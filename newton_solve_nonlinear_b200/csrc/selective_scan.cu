@@ -410,70 +410,97 @@ cudaError_t launch_ss_reverse_states(const SsArgs &a, cudaStream_t s) {
 
 namespace {
 
-// CTAs along the channels of each row; L lanes of four states hold a channel, each with one vector of the state.  Rows
-// that name the same slot are taken in row order by the first one's CTA, as tokens that follow each other.
-template <typename T, int L>
+// CTAs along the channels of each row; L lanes of four states hold a channel, each thread of R channels that stand CH apart.
+// Everything that a row needs is asked for at once, behind its slot alone.  Rows that name the same slot are taken in row
+// order by the first one's CTA, as tokens that follow each other.  Bound by HBM.
+template <typename T, int L, int R, bool VEC>
 __global__ void __launch_bounds__(256) ss_step_kernel(const SsStep w) {
-    constexpr int CH = 256 / L;
+    constexpr int CH = 256 / L, BW = VEC ? 4 : 1;
     __shared__ int next;
-    const int tid = threadIdx.x, tiles = (w.D + CH - 1) / CH;
+    const int tid = threadIdx.x, tiles = (w.D + CH * R - 1) / (CH * R);
     int b = blockIdx.x / tiles;
-    const int d = blockIdx.x % tiles * CH + tid / L, n0 = tid % L * 4, g = d / (w.D / w.G);
-    const bool on = d < w.D;
+    const int d0 = blockIdx.x % tiles * CH * R + tid / L, n0 = tid % L * 4, per = w.D / w.G;
     T *py = static_cast<T *>(w.y);
     const int slot = w.slots == nullptr ? b : w.slots[b];
     if (slot < 0 || slot >= w.n_slots) {  // no state behind this row
-        if (on && n0 == 0) py[static_cast<long long>(b) * w.D + d] = from_f<T>(0.f);
+        for (int r = 0; r < R; ++r)
+            if (d0 + r * CH < w.D && n0 == 0) py[static_cast<long long>(b) * w.D + d0 + r * CH] = from_f<T>(0.f);
         return;
     }
+    const bool vec = w.N % 4 == 0, vec_a = vec && (reinterpret_cast<uintptr_t>(w.a) & 15) == 0;
+    const long long at = (static_cast<long long>(slot) * w.D + d0) * w.N;
+    u64 h[R][2] = {}, a[R][2] = {};
+    float bias[R] = {}, skip[R] = {};
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int d = d0 + r * CH;
+        if (d >= w.D) continue;
+        load_states(h[r], w.state + at + static_cast<long long>(r) * CH * w.N, n0, w.N, vec);
+        load_states(a[r], w.a + static_cast<long long>(d) * w.N, n0, w.N, vec_a);
+        if (w.dt_bias != nullptr) bias[r] = w.dt_bias[d];
+        if (w.skip != nullptr) skip[r] = w.skip[d];
+    }
+    T x[R], s[R], z[R];
+    RawN<T, BW> rb[R][4 / BW], rc[R][4 / BW];
+    auto fetch = [&]() {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int d = d0 + r * CH;
+            const bool on = d < w.D;
+            const int g = on && w.G > 1 ? d / per : 0;
+            x[r] = s[r] = z[r] = from_f<T>(0.f);
+            if (on) x[r] = static_cast<const T *>(w.x.p)[b * w.x.sb + d], s[r] = static_cast<const T *>(w.dt.p)[b * w.dt.sb + d];
+            if (on && w.gate.p != nullptr) z[r] = static_cast<const T *>(w.gate.p)[b * w.gate.sb + d];
+#pragma unroll
+            for (int i = 0; i < 4 / BW; ++i) {
+                const int n = n0 + i * BW;
+                rb[r][i] = load_n<BW>(static_cast<const T *>(w.b.p) + b * w.b.sb + g * w.b.sg + n, on && n < w.N);
+                rc[r][i] = load_n<BW>(static_cast<const T *>(w.c.p) + b * w.c.sb + g * w.c.sg + n, on && n < w.N);
+            }
+        }
+    };
+    auto token = [&]() {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int d = d0 + r * CH;
+            const float xf = to_f(x[r]);
+            float st = to_f(s[r]) + bias[r];
+            if (w.softplus) st = softplus(st);
+            __align__(16) float bf[4], cf[4];
+#pragma unroll
+            for (int i = 0; i < 4 / BW; ++i) unpack_n(bf + i * BW, rb[r][i]), unpack_n(cf + i * BW, rc[r][i]);
+            u64 y = 0;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const u64 e = decay_less_one(mul2(splat(st), mul2(a[r][i], splat(kLog2eF))));
+                h[r][i] = fma2(e, h[r][i], fma2(splat(st * xf), pk(bf[2 * i], bf[2 * i + 1]), h[r][i]));
+                y = fma2(pk(cf[2 * i], cf[2 * i + 1]), h[r][i], y);
+            }
+            float out = pair_sum(y);
+#pragma unroll
+            for (int o = L / 2; o > 0; o >>= 1) out += __shfl_xor_sync(0xffffffffu, out, o);
+            if (d < w.D && n0 == 0) {
+                out = fmaf(skip[r], xf, out);
+                if (w.gate.p != nullptr) out = gate_with(out, to_f(z[r]));
+                py[static_cast<long long>(b) * w.D + d] = from_f<T>(out);
+            }
+        }
+    };
+    fetch();
+    bool more = false;
     if (w.slots != nullptr) {
-        int earlier = 0;
-        for (int i = tid; i < b; i += 256) earlier |= w.slots[i] == slot;
+        int earlier = 0, later = 0;
+        for (int i = tid; i < w.B; i += 256) {
+            const int same = w.slots[i] == slot;
+            earlier |= same & i < b, later |= same & i > b;
+        }
         if (__syncthreads_or(earlier)) return;
+        more = __syncthreads_or(later);
     }
-    const bool vec = w.N % 4 == 0;
-    const long long at = (static_cast<long long>(slot) * w.D + d) * w.N;
-    u64 h[2] = {0, 0}, a[2] = {0, 0};
-    float bias = 0.f, skip = 0.f;
-    if (on) {
-        load_states(h, w.state + at, n0, w.N, vec);
-        load_states(a, w.a + static_cast<long long>(d) * w.N, n0, w.N, vec && (reinterpret_cast<uintptr_t>(w.a) & 15) == 0);
-        if (w.dt_bias != nullptr) bias = w.dt_bias[d];
-        if (w.skip != nullptr) skip = w.skip[d];
-    }
-    while (true) {
-        if (w.slots != nullptr) {
-            if (tid == 0) next = w.B;
-            __syncthreads();
-        }
-        float x = 0.f, s = 0.f;
-        if (on) {
-            x = to_f(static_cast<const T *>(w.x.p)[b * w.x.sb + d]);
-            s = to_f(static_cast<const T *>(w.dt.p)[b * w.dt.sb + d]) + bias;
-            if (w.softplus) s = softplus(s);
-        }
-        const T *pb = static_cast<const T *>(w.b.p) + b * w.b.sb + g * w.b.sg;
-        const T *pc = static_cast<const T *>(w.c.p) + b * w.c.sb + g * w.c.sg;
-        u64 y = 0;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int n = n0 + 2 * i;
-            const bool one = on && n < w.N, two = on && n + 1 < w.N;
-            const u64 bb = pk(one ? to_f(pb[n]) : 0.f, two ? to_f(pb[n + 1]) : 0.f);
-            const u64 cc = pk(one ? to_f(pc[n]) : 0.f, two ? to_f(pc[n + 1]) : 0.f);
-            const u64 e = decay_less_one(mul2(splat(s), mul2(a[i], splat(kLog2eF))));
-            h[i] = fma2(e, h[i], fma2(splat(s * x), bb, h[i]));
-            y = fma2(cc, h[i], y);
-        }
-        float out = pair_sum(y);
-#pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) out += __shfl_xor_sync(0xffffffffu, out, o);
-        if (on && n0 == 0) {
-            out = fmaf(skip, x, out);
-            if (w.gate.p != nullptr) out = gate_with(out, to_f(static_cast<const T *>(w.gate.p)[b * w.gate.sb + d]));
-            py[static_cast<long long>(b) * w.D + d] = from_f<T>(out);
-        }
-        if (w.slots == nullptr) break;
+    token();
+    while (more) {
+        if (tid == 0) next = w.B;
+        __syncthreads();
         for (int i = b + 1 + tid; i < w.B; i += 256)
             if (w.slots[i] == slot) {
                 atomicMin(&next, i);
@@ -483,14 +510,26 @@ __global__ void __launch_bounds__(256) ss_step_kernel(const SsStep w) {
         b = next;
         if (b >= w.B) break;
         __syncthreads();
+        fetch();
+        token();
     }
-    if (on) store_states(h, w.out_state + at, n0, w.N, vec);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        if (d0 + r * CH < w.D) store_states(h[r], w.out_state + at + static_cast<long long>(r) * CH * w.N, n0, w.N, vec);
 }
 
 template <typename T, int L>
 void launch_step(const SsStep &w, cudaStream_t s) {
-    const unsigned grid = static_cast<unsigned>((w.D + 256 / L - 1) / (256 / L)) * w.B;
-    ss_step_kernel<T, L><<<grid, 256, 0, s>>>(w);
+    constexpr int CH = 256 / L;
+    const long long one = static_cast<long long>((w.D + CH - 1) / CH) * w.B;
+    const size_t e = 4 * sizeof(T);
+    bool quads = w.N % 4 == 0;
+    for (const SsRows *r : {&w.b, &w.c})
+        quads = quads && reinterpret_cast<uintptr_t>(r->p) % e == 0 && r->sb % 4 == 0 && r->sg % 4 == 0;
+    const unsigned two = static_cast<unsigned>((w.D + 2 * CH - 1) / (2 * CH)) * w.B;
+    if (!quads) ss_step_kernel<T, L, 1, false><<<static_cast<unsigned>(one), 256, 0, s>>>(w);
+    else if (one <= 148 * 6) ss_step_kernel<T, L, 1, true><<<static_cast<unsigned>(one), 256, 0, s>>>(w);  // one wave
+    else ss_step_kernel<T, L, 2, true><<<two, 256, 0, s>>>(w);
 }
 template <typename T>
 void step_of(const SsStep &w, cudaStream_t s) {

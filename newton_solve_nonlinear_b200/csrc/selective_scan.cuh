@@ -192,6 +192,13 @@ __device__ __forceinline__ void store_n(float *p, RawN<__nv_bfloat16, 4> r) {
 }
 __device__ __forceinline__ void store_n(float *p, RawN<float, 1> r) { *p = r.v; }
 __device__ __forceinline__ void store_n(float *p, RawN<float, 4> r) { *reinterpret_cast<float4 *>(p) = r.v; }
+__device__ __forceinline__ void unpack_n(float *f, RawN<__nv_bfloat16, 1> r) { *f = __uint_as_float(static_cast<unsigned>(r.v) << 16); }
+__device__ __forceinline__ void unpack_n(float *f, RawN<__nv_bfloat16, 4> r) {
+    f[0] = __uint_as_float(r.v.x << 16), f[1] = __uint_as_float(r.v.x & 0xffff0000u);
+    f[2] = __uint_as_float(r.v.y << 16), f[3] = __uint_as_float(r.v.y & 0xffff0000u);
+}
+__device__ __forceinline__ void unpack_n(float *f, RawN<float, 1> r) { *f = r.v; }
+__device__ __forceinline__ void unpack_n(float *f, RawN<float, 4> r) { f[0] = r.v.x, f[1] = r.v.y, f[2] = r.v.z, f[3] = r.v.w; }
 template <int N>
 __device__ __forceinline__ void load_floats(float (&v)[N], const float *p) {
     if constexpr (N % 4 == 0) {
