@@ -469,11 +469,9 @@ cudaError_t launch_cc_backward(const CcArgs &a, cudaStream_t s) {
     if (a.dtype == PARARNN_F32) launch_width<float>(a, true, vec, s);
     else launch_width<__nv_bfloat16>(a, true, vec, s);
     cudaError_t e = cudaGetLastError();
-    const long long n = static_cast<long long>(a.D) * a.W, stride = n + a.D;
-    const int parts = backward_grid(a, vec ? 2 : 1).y;
-    if (e == cudaSuccess) e = launch_rows_sum(a.part, a.dweight, parts, n, stride, s);
-    if (e == cudaSuccess) e = launch_rows_sum(a.part + n, a.dbias, parts, a.D, stride, s);
-    return e;
+    if (e != cudaSuccess) return e;
+    const long long n = static_cast<long long>(a.D) * a.W;
+    return launch_rows_sum({a.part, backward_grid(a, vec ? 2 : 1).y, n + a.D, {a.dweight, a.dbias, nullptr}, {n, a.D, 0}}, s);
 }
 
 cudaError_t launch_cc_step(const CcStep &w, cudaStream_t s) {

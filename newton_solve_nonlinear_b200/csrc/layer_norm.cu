@@ -379,20 +379,16 @@ __global__ void __launch_bounds__(256) ln_columns_kernel(const LnArgs w) {
     }
 }
 
-// Which kernel takes a row: threads of a team and vectors of a thread.  A warp needs no barrier, and forward holds up to
-// 512 vectors of a row; backward, with its sums for the parameters, 128.
+// Which kernel takes a row: threads of a team and vectors of a thread.  (A warp needs no barrier, but 16 vectors to a lane
+// leave one CTA to an SM: [32768, 2048] forward 172 us against 130.)
 struct Fit {
     int v, team, k;
 };
-Fit fit(const LnArgs &a, bool back) {
+Fit fit(const LnArgs &a) {
     const int v = a.C % 4 == 0 ? 4 : 1, nv = a.C / v;
     if (nv <= 32) return {v, 32, 1};
     if (nv <= 64) return {v, 32, 2};
     if (nv <= 128) return {v, 32, 4};
-    if (!back && static_cast<long long>(a.N) * a.S >= 148 * 8) {  // rows for eight warps of each SM
-        if (nv <= 256) return {v, 32, 8};
-        if (nv <= 512) return {v, 32, 16};
-    }
     if (nv <= 256) return {v, 256, 1};
     if (nv <= 512) return {v, 256, 2};
     if (nv <= 1024) return {v, 256, 4};
@@ -424,10 +420,6 @@ void launch(const LnArgs &a, const Fit &f, cudaStream_t s) {
     PARARNN_LN(32, 1);
     PARARNN_LN(32, 2);
     PARARNN_LN(32, 4);
-    if constexpr (!BACK) {
-        PARARNN_LN(32, 8);
-        PARARNN_LN(32, 16);
-    }
     PARARNN_LN(256, 1);
     PARARNN_LN(256, 2);
     PARARNN_LN(256, 4);
@@ -441,20 +433,20 @@ void launch(const LnArgs &a, const Fit &f, cudaStream_t s) {
 
 // CTAs of the backward pass, each of which leaves a row of sums: what fits the card at once, fewer where there are fewer rows
 int ln_backward_rows(const LnArgs &a) {
-    const Fit f = fit(a, true);
+    const Fit f = fit(a);
     const long long rows = static_cast<long long>(a.N) * a.S, teams = f.team == 32 ? 8 : 1;
-    return static_cast<int>(std::min<long long>((rows + teams - 1) / teams, 148 * (f.team > 256 ? 1 : f.k > 4 ? 2 : 4)));
+    return static_cast<int>(std::min<long long>((rows + teams - 1) / teams, 148 * (f.team > 256 ? 1 : f.k > 4 ? 2 : 3)));
 }
 
 cudaError_t launch_ln_forward(const LnArgs &a, cudaStream_t s) {
-    const Fit f = fit(a, false);
+    const Fit f = fit(a);
     if (f.v == 4) launch<4, false>(a, f, s);
     else launch<1, false>(a, f, s);
     return cudaGetLastError();
 }
 
 cudaError_t launch_ln_backward(const LnArgs &a, cudaStream_t s) {
-    const Fit f = fit(a, true);
+    const Fit f = fit(a);
     if (f.v == 4) launch<4, true>(a, f, s);
     else launch<1, true>(a, f, s);
     cudaError_t e = cudaGetLastError();
@@ -463,9 +455,8 @@ cudaError_t launch_ln_backward(const LnArgs &a, cudaStream_t s) {
         ln_columns_kernel<<<dim3((a.C + 31) / 32, rows), 256, 0, s>>>(a);
         e = cudaGetLastError();
     }
-    if (e == cudaSuccess) e = launch_rows_sum(a.part, a.dweight, rows, a.C, 2ll * a.C, s);
-    if (e == cudaSuccess) e = launch_rows_sum(a.part + a.C, a.dbias, rows, a.C, 2ll * a.C, s);
-    return e;
+    if (e != cudaSuccess) return e;
+    return launch_rows_sum({a.part, rows, 2ll * a.C, {a.dweight, a.dbias, nullptr}, {a.C, a.C, 0}}, s);
 }
 
 }  // namespace pararnn

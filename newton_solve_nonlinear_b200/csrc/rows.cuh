@@ -63,7 +63,14 @@ __device__ __forceinline__ int count(const int *lengths, int b, int T) {
 
 }  // namespace rows
 
-// out[c] = sum over r of part[r * width + c] for c < width, in a fixed order; nothing where out is null.
-cudaError_t launch_rows_sum(const float *part, float *out, long long rows, long long width, long long stride, cudaStream_t s);
+// Sums over the rows of part [rows, width], in a fixed order: the columns go one output after the other to out[i] [n[i]]
+// (the n add up to width); nothing where an output is null.
+struct RowsSum {
+    const float *part;
+    long long rows, width;
+    float *out[3];
+    long long n[3];
+};
+cudaError_t launch_rows_sum(const RowsSum &a, cudaStream_t s);
 
 }  // namespace pararnn

@@ -51,9 +51,7 @@ struct ScanCall {
         if (!has_kept) a.kept = floats(kept());
         const size_t part = static_cast<size_t>(ss_backward_tiles(a)) * tokens() * s.G * s.N;
         a.part_b = floats(part), a.part_c = floats(part);
-        a.part_a = floats(a.n_seg * states());
-        a.part_skip = floats(static_cast<size_t>(a.n_seg) * s.B * s.D);
-        a.part_bias = floats(static_cast<size_t>(a.n_seg) * s.B * s.D);
+        a.part_a = floats(static_cast<size_t>(a.n_seg) * s.B * s.D * (s.N + 2));
     }
 };
 

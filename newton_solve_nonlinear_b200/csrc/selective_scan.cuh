@@ -44,7 +44,7 @@ struct SsArgs {
     void *dx, *ddt, *dgate, *db, *dc;
     float *da, *dskip, *ddt_bias, *dh0;
     float *part_b, *part_c;                // [tiles of a group, B, T, G, N]
-    float *part_a, *part_skip, *part_bias;  // [n_seg, B, D, N], [n_seg, B, D]
+    float *part_a;                         // [n_seg, B, D N + D + D]: da, dskip and ddt_bias of each segment
 };
 
 struct SsPlan {

@@ -282,10 +282,12 @@ __global__ void __launch_bounds__(kThr, S == 2 ? 3 : 2) ss_backward_kernel(const
             if (gated) store_pair<VEC>(static_cast<T *>(w.dgate) + to, 0ull, have);
         }
     }
+    // a row of the parameters' sums: da, dskip, ddt_bias
+    float *part = w.part_a + (static_cast<long long>(seg) * w.B + b) * w.D * (w.N + 2);
 #pragma unroll
     for (int q = 0; q < 2; ++q)
         if (q < owns) {
-            store_states(da[q], w.part_a + seg * all + state_at + q * w.N, n0, w.N, vec);
+            store_states(da[q], part + (static_cast<long long>(d) + q) * w.N, n0, w.N, vec && w.D % 2 == 0);
             if (seg == 0 && w.dh0 != nullptr) store_states(p[q], w.dh0 + state_at + q * w.N, n0, w.N, vec);
         }
     __syncthreads();
@@ -299,9 +301,9 @@ __global__ void __launch_bounds__(kThr, S == 2 ? 3 : 2) ss_backward_kernel(const
             const float2 u = s_sum[tid + i * (CH / 2)], v = s_sum[kThr + tid + i * (CH / 2)];
             s.x += u.x, s.y += u.y, q.x += v.x, q.y += v.y;
         }
-        const long long to = (static_cast<long long>(seg) * w.B + b) * w.D + ld;
-        if (have > 0) w.part_skip[to] = s.x, w.part_bias[to] = q.x;
-        if (have > 1) w.part_skip[to + 1] = s.y, w.part_bias[to + 1] = q.y;
+        float *to = part + static_cast<long long>(w.D) * w.N + ld;
+        if (have > 0) to[0] = s.x, to[w.D] = q.x;
+        if (have > 1) to[1] = s.y, to[w.D + 1] = q.y;
     }
 }
 
@@ -365,10 +367,8 @@ cudaError_t launch_ss_backward(const SsArgs &a, cudaStream_t s) {
         else ss_tiles_sum_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a, tiles);
         e = cudaGetLastError();
     }
-    if (e == cudaSuccess) e = launch_rows_sum(a.part_a, a.da, rows, dn, dn, s);
-    if (e == cudaSuccess) e = launch_rows_sum(a.part_skip, a.dskip, rows, a.D, a.D, s);
-    if (e == cudaSuccess) e = launch_rows_sum(a.part_bias, a.ddt_bias, rows, a.D, a.D, s);
-    return e;
+    if (e != cudaSuccess) return e;
+    return launch_rows_sum({a.part_a, rows, dn + 2ll * a.D, {a.da, a.dskip, a.ddt_bias}, {dn, a.D, a.D}}, s);
 }
 
 }  // namespace pararnn
