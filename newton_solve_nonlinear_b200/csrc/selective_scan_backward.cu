@@ -6,59 +6,175 @@ namespace pararnn {
 using namespace ss;
 namespace {
 
-constexpr int kThr = 128;
+constexpr int kThr = 128;    // threads that hold states; as many again prepare and finish tokens
 constexpr int kK = kSsKeep;  // tokens whose states are formed again at a time
 
 template <int S, int L>
-struct Smem {
+struct Smem {  // two of each, for groups of kK tokens in turn
     static constexpr int CH = 2 * kThr / L, NP = S * L, ROWS = kThr / L;
     static constexpr int ES = CH + (L < 16 ? 32 / L : 2);      // a row of the sums over states, off the banks of the next
     static constexpr int TS = ROWS * NP + (NP < 32 ? NP : 0);  // a token's sums over channels, likewise
-    float4 du[kK][CH / 2];  // s and s x of two channels
-    float2 v[kK][CH / 2];
-    float b[kK][NP], c[kK][NP];
-    float e[3][kK][L][ES];        // parts of sum G b, sum a P h and sum c h, summed over L
-    float pb[kK][TS], pc[kK][TS];  // parts of db and dc, [ROWS][NP], summed over the rows
+    float4 du[2][kK][CH / 2];  // s and s x of two channels
+    float2 v[2][kK][CH / 2];
+    float b[2][kK][NP], c[2][kK][NP];
+    float e[2][3][kK][L][ES];            // parts of sum G b, sum a P h and sum c h, summed over L
+    float pb[2][kK][TS], pc[2][kK][TS];  // parts of db and dc, [ROWS][NP], summed over the rows
 };
 
-// One CTA: 2 kThr / L channels of one group, one segment of one sequence, backward in time.  A thread holds S states of
-// each of two channels: what it sums over its channels (for db, dc) and over its states (for dx, ds and the inner y)
-// leaves 1 / 2 and 1 / S of the values to pass through shared memory, whose bytes are what bounds this kernel next to its
-// arithmetic.  Eight tokens at a time: from the kept state their decays and states are formed again into registers, then
-// walked backward.  VEC: pairs of channels, and quads of b and c, lie on their own alignment.
+// all threads of the CTA, which come from different places of the code
+__device__ __forceinline__ void meet() { asm volatile("bar.sync 1, %0;" ::"n"(2 * kThr) : "memory"); }
+
+// A launch has 128 registers to a thread.  The threads that hold states take more of them, the others, which have PER
+// tokens and channel pairs each, make do with less; the two together are what was there.
+constexpr int kRegs = 128;
+constexpr int state_regs(int L) { return L >= 8 ? 168 : L == 4 ? 152 : kRegs; }
+template <int N>
+__device__ __forceinline__ void take_registers() {
+    if constexpr (N > kRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void give_registers() {
+    if constexpr (N < kRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// One CTA: 2 kThr / L channels of one group, one segment of one sequence, backward in time, eight tokens at a time.
+//   Four warps hold the states: a thread has S of each of two channels.  From the kept state its decays and states are formed
+// again into registers, then walked backward.  What it sums over its channels (for db, dc) and over its states (for dx, ds
+// and the inner y) leaves 1 / 2 and 1 / S of the values to pass through shared memory.
+//   Four more prepare the next eight tokens, and finish the last ones: those sums, the gradients of each token and channel,
+// and the CTA's part of db and dc.  VEC: pairs of channels, and quads of b and c, lie on their own alignment.
 template <typename T, int S, int L, bool VEC>
-__global__ void __launch_bounds__(kThr, S == 2 ? 3 : 2) ss_backward_kernel(const SsArgs w) {
+__global__ void __launch_bounds__(2 * kThr, 2) ss_backward_kernel(const SsArgs w) {
     using SM = Smem<S, L>;
     constexpr int CH = SM::CH, NP = SM::NP, Q = S / 2;
-    constexpr int LT = kThr / (CH / 2), PER = (kK + LT - 1) / LT;
     extern __shared__ __align__(16) char smem[];
     SM &sm = *reinterpret_cast<SM *>(smem);
 
-    const int tid = threadIdx.x, per = w.D / w.G;
-    const int tiles = (per + CH - 1) / CH, blocks = tiles * w.G;
+    const int per = w.D / w.G, tiles = (per + CH - 1) / CH, blocks = tiles * w.G;
     const int tile = blockIdx.x % blocks % tiles, g = blockIdx.x % blocks / tiles;
     const int seg = blockIdx.x / blocks % w.n_seg, b = blockIdx.x / blocks / w.n_seg;
     const int len = row_count(w.lengths, b, w.T);
     const int t_first = seg * w.seg, t_end = min(w.T, t_first + w.seg), t_len = min(t_end, len);
-    const long long all = static_cast<long long>(w.B) * w.D * w.N;
-    const bool vec = w.N % S == 0, gated = w.gate.p != nullptr;
+    const bool gated = w.gate.p != nullptr;
+    const int n_chunk = (max(t_len - t_first, 0) + kK - 1) / kK;
+    const int t_start = t_first + max(n_chunk - 1, 0) * kK;
+    // a row of the parameters' sums: da, dskip, ddt_bias
+    float *part = w.part_a + (static_cast<long long>(seg) * w.B + b) * w.D * (w.N + 2);
 
-    // as owner of the states of two channels
-    const int pair = tid / L, n0 = tid % L * S, d = g * per + tile * CH + 2 * pair;
-    const int owns = min(2, max(0, per - tile * CH - 2 * pair));
-    const long long state_at = (static_cast<long long>(b) * w.D + d) * w.N;
-    u64 p[2][Q] = {}, da[2][Q] = {};
-    float a[2][S] = {};
+    if (threadIdx.x < kThr) {
+        take_registers<state_regs(L)>();
+        const int tid = threadIdx.x, pair = tid / L, n0 = tid % L * S, d = g * per + tile * CH + 2 * pair;
+        const int owns = min(2, max(0, per - tile * CH - 2 * pair));
+        const bool vec = w.N % S == 0;
+        const long long at_d = (static_cast<long long>(b) * w.D + d) * w.N, all = static_cast<long long>(w.B) * w.D * w.N;
+        u64 p[2][Q] = {}, da[2][Q] = {}, hk[2][Q] = {};  // hk: the next kept states
+        float a[2][S] = {};
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        if (q >= owns) continue;
+        for (int q = 0; q < 2; ++q) {
+            if (q >= owns) continue;
 #pragma unroll
-        for (int i = 0; i < S; ++i)
-            if (n0 + i < w.N) a[q][i] = w.a[(static_cast<long long>(d) + q) * w.N + n0 + i] * kLog2eF;
-        const float *from = w.n_seg > 1 ? w.rev_state + seg * all : w.dh;
-        if (from != nullptr) load_states(p[q], from + state_at + q * w.N, n0, w.N, vec);
+            for (int i = 0; i < S; ++i)
+                if (n0 + i < w.N) a[q][i] = w.a[(static_cast<long long>(d) + q) * w.N + n0 + i] * kLog2eF;
+            const float *from = w.n_seg > 1 ? w.rev_state + seg * all : w.dh;
+            if (from != nullptr) load_states(p[q], from + at_d + q * w.N, n0, w.N, vec);
+        }
+        const long long row = static_cast<long long>(w.D) * w.N;
+        const float *kept = w.kept + (static_cast<long long>(b) * ((w.T + kK - 1) / kK) + t_start / kK) * row + static_cast<long long>(d) * w.N;
+        auto fetch = [&]() {
+            if (owns > 0) load_states(hk[0], kept, n0, w.N, vec);
+            if (owns > 1) load_states(hk[1], kept + w.N, n0, w.N, vec);
+            kept -= row;
+        };
+        if (n_chunk > 0) fetch();
+        meet();
+        for (int k = n_chunk - 1; k >= 0; --k) {
+            const auto &du_at = sm.du[k & 1];
+            const auto &v_at = sm.v[k & 1];
+            const auto &b_at = sm.b[k & 1];
+            const auto &c_at = sm.c[k & 1];
+            auto &e_at = sm.e[k & 1];
+            u64 first[2][Q], h[kK][2][Q], e[kK][2][Q];
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int i = 0; i < Q; ++i) first[q][i] = hk[q][i];
+            if (k > 0) fetch();
+#pragma unroll
+            for (int t = 0; t < kK; ++t) {
+                const float4 du = du_at[t][pair];
+                u64 bb[Q];
+                load_pairs(bb, &b_at[t][n0]);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const float st = q == 0 ? du.x : du.y, u = q == 0 ? du.z : du.w;
+#pragma unroll
+                    for (int i = 0; i < Q; ++i) {
+                        const u64 before = t == 0 ? first[q][i] : h[t == 0 ? 0 : t - 1][q][i];
+                        float b0, b1, h0, h1;
+                        upk(bb[i], b0, b1), upk(before, h0, h1);
+                        e[t][q][i] = decay_less_one(pk(st * a[q][2 * i], st * a[q][2 * i + 1]));
+                        h[t][q][i] = fma2(e[t][q][i], before, pk(fmaf(u, b0, h0), fmaf(u, b1, h1)));
+                    }
+                }
+            }
+#pragma unroll
+            for (int t = kK - 1; t >= 0; --t) {
+                const float4 du = du_at[t][pair];
+                const float2 vv = v_at[t][pair];
+                u64 bb[Q], cc[Q], db[Q], dc[Q];
+                load_pairs(bb, &b_at[t][n0]);
+                load_pairs(cc, &c_at[t][n0]);
+                float e1[2], e2[2], e3[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const float st = q == 0 ? du.x : du.y, u = q == 0 ? du.z : du.w, v = q == 0 ? vv.x : vv.y;
+                    u64 x1 = 0, x2 = 0, x3 = 0;
+#pragma unroll
+                    for (int i = 0; i < Q; ++i) {
+                        const u64 before = t == 0 ? first[q][i] : h[t == 0 ? 0 : t - 1][q][i];
+                        float c0, c1, p0, p1, h0, h1, m0, m1, d0, d1;
+                        upk(cc[i], c0, c1), upk(p[q][i], p0, p1), upk(h[t][q][i], h0, h1);
+                        const float g0 = fmaf(v, c0, p0), g1 = fmaf(v, c1, p1);
+                        const u64 G = pk(g0, g1);
+                        if (q == 0) {
+                            dc[i] = pk(v * h0, v * h1), db[i] = pk(u * g0, u * g1);
+                        } else {
+                            upk(dc[i], d0, d1);
+                            dc[i] = pk(fmaf(v, h0, d0), fmaf(v, h1, d1));
+                            upk(db[i], d0, d1);
+                            db[i] = pk(fmaf(u, g0, d0), fmaf(u, g1, d1));
+                        }
+                        x1 = i == 0 ? mul2(G, bb[i]) : fma2(G, bb[i], x1);
+                        p[q][i] = fma2(e[t][q][i], G, G);
+                        const u64 m = mul2(p[q][i], before), aa = pk(a[q][2 * i], a[q][2 * i + 1]);
+                        x2 = i == 0 ? mul2(m, aa) : fma2(m, aa, x2);
+                        upk(m, m0, m1), upk(da[q][i], d0, d1);
+                        da[q][i] = pk(fmaf(st, m0, d0), fmaf(st, m1, d1));
+                        if (gated) x3 = i == 0 ? mul2(cc[i], h[t][q][i]) : fma2(cc[i], h[t][q][i], x3);
+                    }
+                    e1[q] = pair_sum(x1), e2[q] = pair_sum(x2), e3[q] = pair_sum(x3);
+                }
+                *reinterpret_cast<float2 *>(&e_at[0][t][tid % L][2 * pair]) = make_float2(e1[0], e1[1]);
+                *reinterpret_cast<float2 *>(&e_at[1][t][tid % L][2 * pair]) = make_float2(e2[0], e2[1]);
+                if (gated) *reinterpret_cast<float2 *>(&e_at[2][t][tid % L][2 * pair]) = make_float2(e3[0], e3[1]);
+                store_pairs(&sm.pb[k & 1][t][pair * NP + n0], db);
+                store_pairs(&sm.pc[k & 1][t][pair * NP + n0], dc);
+            }
+            meet();
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            if (q < owns) {
+                store_states(da[q], part + (static_cast<long long>(d) + q) * w.N, n0, w.N, false);
+                if (seg == 0 && w.dh0 != nullptr) store_states(p[q], w.dh0 + at_d + q * w.N, n0, w.N, vec);
+            }
+        return;
     }
-    // as the one who prepares and finishes tokens lt + i LT of the channels lc and lc + 1
+
+    // tokens lt + i LT of a group of eight, channels lc and lc + 1
+    give_registers<2 * kRegs - state_regs(L)>();
+    constexpr int LT = kThr / (CH / 2), PER = (kK + LT - 1) / LT;
+    const int tid = threadIdx.x - kThr;
     const int lc = tid % (CH / 2) * 2, lt = tid / (CH / 2), ld = g * per + tile * CH + lc;
     const int have = min(2, max(0, per - tile * CH - lc));
     float bias[2] = {}, skip[2] = {}, dskip[2] = {}, dbias[2] = {};
@@ -67,8 +183,6 @@ __global__ void __launch_bounds__(kThr, S == 2 ? 3 : 2) ss_backward_kernel(const
         if (q < have && w.dt_bias != nullptr) bias[q] = w.dt_bias[ld + q];
         if (q < have && w.skip != nullptr) skip[q] = w.skip[ld + q];
     }
-    const int n_chunk = (max(t_len - t_first, 0) + kK - 1) / kK;
-    const int t_start = t_first + max(n_chunk - 1, 0) * kK;
     const T *px = static_cast<const T *>(w.x.p) + b * w.x.sb + ld + (t_start + lt) * w.x.st;
     const T *pdt = static_cast<const T *>(w.dt.p) + b * w.dt.sb + ld + (t_start + lt) * w.dt.st;
     const T *pg = static_cast<const T *>(w.gate.p) + b * w.gate.sb + ld + (t_start + lt) * w.gate.st;
@@ -77,12 +191,14 @@ __global__ void __launch_bounds__(kThr, S == 2 ? 3 : 2) ss_backward_kernel(const
     const int bt = tid / BROW, bn = tid % BROW * BW;
     const T *pb = static_cast<const T *>(w.b.p) + b * w.b.sb + g * w.b.sg + (t_start + bt) * w.b.st + bn;
     const T *pc = static_cast<const T *>(w.c.p) + b * w.c.sb + g * w.c.sg + (t_start + bt) * w.c.st + bn;
-    const float *pk_at = w.kept + ((static_cast<long long>(b) * ((w.T + kK - 1) / kK) + t_start / kK) * w.D + d) * w.N;
 
-    Raw<T> nx[PER], nt[PER], ng[PER], ny[PER], cx[PER], cg[PER], cy[PER];  // the next tokens' elements, and the present ones'
+    struct Kept {  // of a token and its two channels from its preparation on
+        Raw<T> x, g, y;
+        float s[2], v[2], slope[2], sig[2];  // the step, v, the softplus' slope, the gate's sigmoid
+    };
+    Raw<T> nx[PER], nt[PER], ng[PER], ny[PER];  // the next tokens' elements
     RawN<T, BW> nb[NB], nc[NB];
-    float slope[PER][2], sig[PER][2];  // of the softplus; the gate's sigmoid
-    u64 hk[2][Q] = {};                 // the next kept states
+    Kept now[PER], last[PER];
     auto fetch = [&](int t0) {
         const int left = t_len - t0;
 #pragma unroll
@@ -102,22 +218,22 @@ __global__ void __launch_bounds__(kThr, S == 2 ? 3 : 2) ss_backward_kernel(const
             nc[i] = load_n<BW>(pc + i * (kThr / BROW) * w.c.st, on);
         }
         pb -= kK * w.b.st, pc -= kK * w.c.st;
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-            if (q < owns) load_states(hk[q], pk_at + q * w.N, n0, w.N, vec);
-        pk_at -= static_cast<long long>(w.D) * w.N;
     };
-    auto stage = [&](int t0) {
-        float s[PER][2], v[PER][2];
+    auto stage = [&](int t0, int to) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            upk(value(nt[i]), s[i][0], s[i][1]), upk(value(ny[i]), v[i][0], v[i][1]);
-            s[i][0] += bias[0], s[i][1] += bias[1];
-            slope[i][0] = slope[i][1] = 1.f;
+            last[i] = now[i];
+            Kept &n = now[i];
+            n.x = nx[i], n.g = ng[i], n.y = ny[i];
+            upk(value(nt[i]), n.s[0], n.s[1]), upk(value(ny[i]), n.v[0], n.v[1]);
+            n.s[0] += bias[0], n.s[1] += bias[1];
+            n.slope[0] = n.slope[1] = 1.f;
         }
         if (w.softplus) {
 #pragma unroll
-            for (int i = 0; i < PER; ++i) s[i][0] = softplus(s[i][0], slope[i][0]), s[i][1] = softplus(s[i][1], slope[i][1]);
+            for (int i = 0; i < PER; ++i)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) now[i].s[q] = softplus(now[i].s[q], now[i].slope[q]);
         }
         if (gated) {
 #pragma unroll
@@ -125,103 +241,30 @@ __global__ void __launch_bounds__(kThr, S == 2 ? 3 : 2) ss_backward_kernel(const
                 float z[2];
                 upk(value(ng[i]), z[0], z[1]);
 #pragma unroll
-                for (int q = 0; q < 2; ++q) sig[i][q] = sigmoid_of(z[q]), v[i][q] *= z[q] * sig[i][q];
+                for (int q = 0; q < 2; ++q) now[i].sig[q] = sigmoid_of(z[q]), now[i].v[q] *= z[q] * now[i].sig[q];
             }
         }
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int t = lt + i * LT;
+            Kept &n = now[i];
             const bool on = t0 + t < t_len;
             float x[2];
             upk(value(nx[i]), x[0], x[1]);
-            s[i][0] = on ? s[i][0] : 0.f, s[i][1] = on ? s[i][1] : 0.f;
+            n.s[0] = on ? n.s[0] : 0.f, n.s[1] = on ? n.s[1] : 0.f;
             if (t < kK) {
-                sm.du[t][lc / 2] = make_float4(s[i][0], s[i][1], s[i][0] * x[0], s[i][1] * x[1]);
-                sm.v[t][lc / 2] = make_float2(v[i][0], v[i][1]);
+                sm.du[to][t][lc / 2] = make_float4(n.s[0], n.s[1], n.s[0] * x[0], n.s[1] * x[1]);
+                sm.v[to][t][lc / 2] = make_float2(n.v[0], n.v[1]);
             }
-            cx[i] = nx[i], cg[i] = ng[i], cy[i] = ny[i];
         }
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
             const int t = bt + i * (kThr / BROW);
-            if (t < kK) store_n(&sm.b[t][bn], nb[i]), store_n(&sm.c[t][bn], nc[i]);
+            if (t < kK) store_n(&sm.b[to][t][bn], nb[i]), store_n(&sm.c[to][t][bn], nc[i]);
         }
     };
-
-    if (n_chunk > 0) {
-        fetch(t_start);
-        stage(t_start);
-    }
-    for (int k = n_chunk - 1, t0 = t_start; k >= 0; --k, t0 -= kK) {
-        __syncthreads();
-        u64 first[2][Q], h[kK][2][Q], e[kK][2][Q];
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int i = 0; i < Q; ++i) first[q][i] = hk[q][i];
-        if (k > 0) fetch(t0 - kK);
-#pragma unroll
-        for (int t = 0; t < kK; ++t) {
-            const float4 du = sm.du[t][pair];
-            u64 bb[Q];
-            load_pairs(bb, &sm.b[t][n0]);
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const float st = q == 0 ? du.x : du.y, u = q == 0 ? du.z : du.w;
-#pragma unroll
-                for (int i = 0; i < Q; ++i) {
-                    const u64 before = t == 0 ? first[q][i] : h[t == 0 ? 0 : t - 1][q][i];
-                    float b0, b1, h0, h1;
-                    upk(bb[i], b0, b1), upk(before, h0, h1);
-                    e[t][q][i] = decay_less_one(pk(st * a[q][2 * i], st * a[q][2 * i + 1]));
-                    h[t][q][i] = fma2(e[t][q][i], before, pk(fmaf(u, b0, h0), fmaf(u, b1, h1)));
-                }
-            }
-        }
-#pragma unroll
-        for (int t = kK - 1; t >= 0; --t) {
-            const float4 du = sm.du[t][pair];
-            const float2 vv = sm.v[t][pair];
-            u64 bb[Q], cc[Q], db[Q], dc[Q];
-            load_pairs(bb, &sm.b[t][n0]);
-            load_pairs(cc, &sm.c[t][n0]);
-            float e1[2], e2[2], e3[2];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const float st = q == 0 ? du.x : du.y, u = q == 0 ? du.z : du.w, v = q == 0 ? vv.x : vv.y;
-                u64 x1 = 0, x2 = 0, x3 = 0;
-#pragma unroll
-                for (int i = 0; i < Q; ++i) {
-                    const u64 before = t == 0 ? first[q][i] : h[t == 0 ? 0 : t - 1][q][i];
-                    float c0, c1, p0, p1, h0, h1, g0, g1, m0, m1, d0, d1;
-                    upk(cc[i], c0, c1), upk(p[q][i], p0, p1), upk(h[t][q][i], h0, h1);
-                    g0 = fmaf(v, c0, p0), g1 = fmaf(v, c1, p1);
-                    const u64 G = pk(g0, g1);
-                    if (q == 0) {
-                        dc[i] = pk(v * h0, v * h1), db[i] = pk(u * g0, u * g1);
-                    } else {
-                        upk(dc[i], d0, d1);
-                        dc[i] = pk(fmaf(v, h0, d0), fmaf(v, h1, d1));
-                        upk(db[i], d0, d1);
-                        db[i] = pk(fmaf(u, g0, d0), fmaf(u, g1, d1));
-                    }
-                    x1 = i == 0 ? mul2(G, bb[i]) : fma2(G, bb[i], x1);
-                    p[q][i] = fma2(e[t][q][i], G, G);
-                    const u64 m = mul2(p[q][i], before), aa = pk(a[q][2 * i], a[q][2 * i + 1]);
-                    x2 = i == 0 ? mul2(m, aa) : fma2(m, aa, x2);
-                    upk(m, m0, m1), upk(da[q][i], d0, d1);
-                    da[q][i] = pk(fmaf(st, m0, d0), fmaf(st, m1, d1));
-                    if (gated) x3 = i == 0 ? mul2(cc[i], h[t][q][i]) : fma2(cc[i], h[t][q][i], x3);
-                }
-                e1[q] = pair_sum(x1), e2[q] = pair_sum(x2), e3[q] = pair_sum(x3);
-            }
-            *reinterpret_cast<float2 *>(&sm.e[0][t][tid % L][2 * pair]) = make_float2(e1[0], e1[1]);
-            *reinterpret_cast<float2 *>(&sm.e[1][t][tid % L][2 * pair]) = make_float2(e2[0], e2[1]);
-            if (gated) *reinterpret_cast<float2 *>(&sm.e[2][t][tid % L][2 * pair]) = make_float2(e3[0], e3[1]);
-            store_pairs(&sm.pb[t][pair * NP + n0], db);
-            store_pairs(&sm.pc[t][pair * NP + n0], dc);
-        }
-        __syncthreads();
+    auto finish = [&](int t0, int from, const Kept (&of)[PER]) {
+        const auto &e_at = sm.e[from];
         // the sums over the states: dx, ddt, dgate
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
@@ -230,25 +273,26 @@ __global__ void __launch_bounds__(kThr, S == 2 ? 3 : 2) ss_backward_kernel(const
             float e1[2] = {}, e2[2] = {}, e3[2] = {}, x[2], z[2], y[2], ddt[2], dx[2], dg[2];
 #pragma unroll
             for (int l = 0; l < L; ++l) {
-                const float2 q1 = *reinterpret_cast<const float2 *>(&sm.e[0][t][l][lc]);
-                const float2 q2 = *reinterpret_cast<const float2 *>(&sm.e[1][t][l][lc]);
+                const float2 q1 = *reinterpret_cast<const float2 *>(&e_at[0][t][l][lc]);
+                const float2 q2 = *reinterpret_cast<const float2 *>(&e_at[1][t][l][lc]);
                 e1[0] += q1.x, e1[1] += q1.y, e2[0] += q2.x, e2[1] += q2.y;
-                if (gated) {
-                    const float2 q3 = *reinterpret_cast<const float2 *>(&sm.e[2][t][l][lc]);
+            }
+            if (gated) {
+#pragma unroll
+                for (int l = 0; l < L; ++l) {
+                    const float2 q3 = *reinterpret_cast<const float2 *>(&e_at[2][t][l][lc]);
                     e3[0] += q3.x, e3[1] += q3.y;
                 }
             }
-            upk(value(cx[i]), x[0], x[1]), upk(value(cg[i]), z[0], z[1]), upk(value(cy[i]), y[0], y[1]);
-            const float4 du = sm.du[t][lc / 2];
-            const float2 vv = sm.v[t][lc / 2];
+            const Kept &o = of[i];
+            upk(value(o.x), x[0], x[1]), upk(value(o.g), z[0], z[1]), upk(value(o.y), y[0], y[1]);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const float v = q == 0 ? vv.x : vv.y;
-                ddt[q] = fmaf(x[q], e1[q], e2[q] * 0.693147181f) * slope[i][q];
-                dx[q] = fmaf(skip[q], v, (q == 0 ? du.x : du.y) * e1[q]);
-                dskip[q] = fmaf(v, x[q], dskip[q]);
+                ddt[q] = fmaf(x[q], e1[q], e2[q] * 0.693147181f) * o.slope[q];
+                dx[q] = fmaf(skip[q], o.v[q], o.s[q] * e1[q]);
+                dskip[q] = fmaf(o.v[q], x[q], dskip[q]);
                 dbias[q] += ddt[q];
-                if (gated) dg[q] = y[q] * fmaf(skip[q], x[q], e3[q]) * sig[i][q] * fmaf(z[q], 1.f - sig[i][q], 1.f);
+                if (gated) dg[q] = y[q] * fmaf(skip[q], x[q], e3[q]) * o.sig[q] * fmaf(z[q], 1.f - o.sig[q], 1.f);
             }
             const long long to = (static_cast<long long>(b) * w.T + t0 + t) * w.D + ld;
             store_pair<VEC>(static_cast<T *>(w.dx) + to, pk(dx[0], dx[1]), n);
@@ -262,17 +306,29 @@ __global__ void __launch_bounds__(kThr, S == 2 ? 3 : 2) ss_backward_kernel(const
             if (n < w.N && t0 + t < t_len) {
                 float sb = 0.f, sc = 0.f;
 #pragma unroll
-                for (int r = 0; r < SM::ROWS; ++r) sb += sm.pb[t][r * NP + n], sc += sm.pc[t][r * NP + n];
+                for (int r = 0; r < SM::ROWS; ++r) sb += sm.pb[from][t][r * NP + n], sc += sm.pc[from][t][r * NP + n];
                 const long long to = (((static_cast<long long>(tile) * w.B + b) * w.T + t0 + t) * w.G + g) * w.N + n;
                 w.part_b[to] = sb;
                 w.part_c[to] = sc;
             }
         }
-        if (k > 0) {
-            __syncthreads();  // du and v of this chunk have been read
-            stage(t0 - kK);
-        }
+    };
+
+    if (n_chunk > 0) {
+        fetch(t_start);
+        stage(t_start, n_chunk - 1 & 1);
+        if (n_chunk > 1) fetch(t_start - kK);
     }
+    meet();
+    for (int k = n_chunk - 1, t0 = t_start; k >= 0; --k, t0 -= kK) {
+        if (k + 1 < n_chunk) finish(t0 + kK, k + 1 & 1, last);
+        if (k > 0) {
+            stage(t0 - kK, k - 1 & 1);
+            if (k > 1) fetch(t0 - 2 * kK);
+        }
+        meet();
+    }
+    if (n_chunk > 0) finish(t_first, 0, now);
     {  // nothing stands behind a sequence
         const long long out = static_cast<long long>(b) * w.T * w.D + ld;
         for (int t = max(t_len, t_first) + lt; t < t_end; t += LT) {
@@ -282,28 +338,20 @@ __global__ void __launch_bounds__(kThr, S == 2 ? 3 : 2) ss_backward_kernel(const
             if (gated) store_pair<VEC>(static_cast<T *>(w.dgate) + to, 0ull, have);
         }
     }
-    // a row of the parameters' sums: da, dskip, ddt_bias
-    float *part = w.part_a + (static_cast<long long>(seg) * w.B + b) * w.D * (w.N + 2);
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-        if (q < owns) {
-            store_states(da[q], part + (static_cast<long long>(d) + q) * w.N, n0, w.N, vec && w.D % 2 == 0);
-            if (seg == 0 && w.dh0 != nullptr) store_states(p[q], w.dh0 + state_at + q * w.N, n0, w.N, vec);
-        }
-    __syncthreads();
-    float2 *s_sum = reinterpret_cast<float2 *>(smem);
-    s_sum[tid] = make_float2(dskip[0], dskip[1]), s_sum[kThr + tid] = make_float2(dbias[0], dbias[1]);
-    __syncthreads();
+    asm volatile("bar.sync 2, %0;" ::"n"(kThr) : "memory");  // the last group has been read, the others are done
+    float4 *s_sum = reinterpret_cast<float4 *>(smem);
+    s_sum[tid] = make_float4(dskip[0], dskip[1], dbias[0], dbias[1]);
+    asm volatile("bar.sync 2, %0;" ::"n"(kThr) : "memory");
     if (tid < CH / 2) {
-        float2 s = make_float2(0.f, 0.f), q = s;
+        float4 s = s_sum[tid];
 #pragma unroll
-        for (int i = 0; i < LT; ++i) {
-            const float2 u = s_sum[tid + i * (CH / 2)], v = s_sum[kThr + tid + i * (CH / 2)];
-            s.x += u.x, s.y += u.y, q.x += v.x, q.y += v.y;
+        for (int i = 1; i < LT; ++i) {
+            const float4 u = s_sum[tid + i * (CH / 2)];
+            s.x += u.x, s.y += u.y, s.z += u.z, s.w += u.w;
         }
         float *to = part + static_cast<long long>(w.D) * w.N + ld;
-        if (have > 0) to[0] = s.x, to[w.D] = q.x;
-        if (have > 1) to[1] = s.y, to[w.D + 1] = q.y;
+        if (have > 0) to[0] = s.x, to[w.D] = s.z;
+        if (have > 1) to[1] = s.y, to[w.D + 1] = s.w;
     }
 }
 
@@ -327,9 +375,15 @@ cudaError_t launch(const SsArgs &a, cudaStream_t s) {
     constexpr int bytes = sizeof(Smem<S, L>);
     static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
     const auto kernel = ss_backward_kernel<T, S, L, VEC>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    kernel<<<static_cast<unsigned>(ss_backward_tiles(a)) * a.G * a.n_seg * a.B, kThr, bytes, s>>>(a);
+    // taking registers that the launch has not got would wait for ever
+    static const int regs = [kernel] {
+        cudaFuncAttributes f{};
+        return cudaFuncGetAttributes(&f, kernel) == cudaSuccess ? f.numRegs : 0;
+    }();
+    if (regs != kRegs) return cudaErrorInvalidDeviceFunction;
+    kernel<<<static_cast<unsigned>(ss_backward_tiles(a)) * a.G * a.n_seg * a.B, 2 * kThr, bytes, s>>>(a);
     return cudaGetLastError();
 }
 int lanes(int N) { return N <= 4 ? 2 : N <= 8 ? 4 : N <= 16 ? 8 : N <= 32 ? 16 : 32; }
