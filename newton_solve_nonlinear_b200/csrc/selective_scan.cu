@@ -383,10 +383,10 @@ bool ss_pairs_ok(const SsArgs &a) {
 
 
 // Segments: none where two states to a thread fill two thirds of the SMs, since what they cost is a second pass; otherwise as
-// many as it takes to give the card three CTAs per SM, of at least 64 tokens each.
+// many as it takes to give every SM two CTAs at once, of at least 64 tokens each.
 SsPlan ss_plan(const SsArgs &a, bool) {
     const long long most = ctas(a, lanes_of(a.N, a.N > 2 ? 2 : 4)), have = ctas(a, lanes_of(a.N, 4));
-    const long long want = most >= 100 ? 1 : std::min<long long>((148 * 3 + have - 1) / have, (a.T + 63) / 64);
+    const long long want = most >= 100 ? 1 : std::min<long long>(148 * 2 / have, (a.T + 63) / 64);
     if (want < 2) return {1, a.T};
     const int seg = static_cast<int>(((a.T + want - 1) / want + 15) / 16 * 16);
     return {(a.T + seg - 1) / seg, seg};
