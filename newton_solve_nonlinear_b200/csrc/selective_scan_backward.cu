@@ -24,18 +24,11 @@ struct Smem {  // two of each, for groups of kK tokens in turn
 // all threads of the CTA, which come from different places of the code
 __device__ __forceinline__ void meet() { asm volatile("bar.sync 1, %0;" ::"n"(2 * kThr) : "memory"); }
 
-// A launch has 128 registers to a thread.  The threads that hold states take more of them, the others, which have PER
-// tokens and channel pairs each, make do with less; the two together are what was there.
-constexpr int kRegs = 128;
-constexpr int state_regs(int L) { return L >= 8 ? 168 : L == 4 ? 152 : kRegs; }
-template <int N>
-__device__ __forceinline__ void take_registers() {
-    if constexpr (N > kRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void give_registers() {
-    if constexpr (N < kRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
+// A launch has 128 registers to a thread.  The threads that hold states take 168, the others make do with 88; the two
+// together are what was there.
+constexpr int kRegs = 128, kStateRegs = 168;
+__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kStateRegs)); }
+__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(2 * kRegs - kStateRegs)); }
 
 // One CTA: 2 kThr / L channels of one group, one segment of one sequence, backward in time, eight tokens at a time.
 //   Four warps hold the states: a thread has S of each of two channels.  From the kept state its decays and states are formed
@@ -62,12 +55,13 @@ __global__ void __launch_bounds__(2 * kThr, 2) ss_backward_kernel(const SsArgs w
     float *part = w.part_a + (static_cast<long long>(seg) * w.B + b) * w.D * (w.N + 2);
 
     if (threadIdx.x < kThr) {
-        take_registers<state_regs(L)>();
+        take_registers();
         const int tid = threadIdx.x, pair = tid / L, n0 = tid % L * S, d = g * per + tile * CH + 2 * pair;
         const int owns = min(2, max(0, per - tile * CH - 2 * pair));
         const bool vec = w.N % S == 0;
         const long long at_d = (static_cast<long long>(b) * w.D + d) * w.N, all = static_cast<long long>(w.B) * w.D * w.N;
-        u64 p[2][Q] = {}, da[2][Q] = {}, hk[2][Q] = {};  // hk: the next kept states
+        u64 p[2][Q] = {}, hk[2][Q] = {};         // hk: the next kept states
+        u64 sum_a[2][Q] = {}, da[2][Q] = {};     // da, of sums over 64 tokens: one long chain would lose digits
         float a[2][S] = {};
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -160,22 +154,30 @@ __global__ void __launch_bounds__(2 * kThr, 2) ss_backward_kernel(const SsArgs w
                 store_pairs(&sm.pb[k & 1][t][pair * NP + n0], db);
                 store_pairs(&sm.pc[k & 1][t][pair * NP + n0], dc);
             }
+            if ((k & 7) == 0) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int i = 0; i < Q; ++i) sum_a[q][i] = add2(sum_a[q][i], da[q][i]), da[q][i] = 0;
+            }
             meet();
         }
 #pragma unroll
         for (int q = 0; q < 2; ++q)
             if (q < owns) {
-                store_states(da[q], part + (static_cast<long long>(d) + q) * w.N, n0, w.N, false);
+                store_states(sum_a[q], part + (static_cast<long long>(d) + q) * w.N, n0, w.N, false);
                 if (seg == 0 && w.dh0 != nullptr) store_states(p[q], w.dh0 + at_d + q * w.N, n0, w.N, vec);
             }
         return;
     }
 
-    // tokens lt + i LT of a group of eight, channels lc and lc + 1
-    give_registers<2 * kRegs - state_regs(L)>();
-    constexpr int LT = kThr / (CH / 2), PER = (kK + LT - 1) / LT;
+    // SUB threads to each token of a group of eight and each pair of channels lc and lc + 1: they share the sums over the
+    // lanes, of which there are more where there are fewer pairs
+    give_registers();
+    constexpr int LT = kK, PER = 1, SUB = kThr / (CH / 2) / kK;
+    static_assert(SUB >= 1 && CH / 2 * SUB <= 32, "the threads of a token and pair are in one warp");
     const int tid = threadIdx.x - kThr;
-    const int lc = tid % (CH / 2) * 2, lt = tid / (CH / 2), ld = g * per + tile * CH + lc;
+    const int lc = tid % (CH / 2) * 2, sub = tid / (CH / 2) % SUB, lt = tid / (CH / 2) / SUB, ld = g * per + tile * CH + lc;
     const int have = min(2, max(0, per - tile * CH - lc));
     float bias[2] = {}, skip[2] = {}, dskip[2] = {}, dbias[2] = {};
 #pragma unroll
@@ -203,7 +205,7 @@ __global__ void __launch_bounds__(2 * kThr, 2) ss_backward_kernel(const SsArgs w
         const int left = t_len - t0;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int t = lt + i * LT, n = t < kK && t < left ? have : 0;
+            const int t = lt + i * LT, n = sub == 0 && t < left ? have : 0;
             nx[i] = load_raw<VEC>(px + i * LT * w.x.st, n);
             nt[i] = load_raw<VEC>(pdt + i * LT * w.dt.st, n);
             ng[i] = load_raw<VEC>(pg + i * LT * w.gate.st, gated ? n : 0);
@@ -252,7 +254,7 @@ __global__ void __launch_bounds__(2 * kThr, 2) ss_backward_kernel(const SsArgs w
             float x[2];
             upk(value(nx[i]), x[0], x[1]);
             n.s[0] = on ? n.s[0] : 0.f, n.s[1] = on ? n.s[1] : 0.f;
-            if (t < kK) {
+            if (sub == 0) {
                 sm.du[to][t][lc / 2] = make_float4(n.s[0], n.s[1], n.s[0] * x[0], n.s[1] * x[1]);
                 sm.v[to][t][lc / 2] = make_float2(n.v[0], n.v[1]);
             }
@@ -268,22 +270,31 @@ __global__ void __launch_bounds__(2 * kThr, 2) ss_backward_kernel(const SsArgs w
         // the sums over the states: dx, ddt, dgate
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int t = lt + i * LT, n = t < kK && t0 + t < t_len ? have : 0;
-            if (n == 0) continue;
+            const int t = lt + i * LT, n = sub == 0 && t0 + t < t_len ? have : 0;
             float e1[2] = {}, e2[2] = {}, e3[2] = {}, x[2], z[2], y[2], ddt[2], dx[2], dg[2];
 #pragma unroll
-            for (int l = 0; l < L; ++l) {
+            for (int l0 = 0; l0 < L / SUB; ++l0) {
+                const int l = sub * (L / SUB) + l0;
                 const float2 q1 = *reinterpret_cast<const float2 *>(&e_at[0][t][l][lc]);
                 const float2 q2 = *reinterpret_cast<const float2 *>(&e_at[1][t][l][lc]);
                 e1[0] += q1.x, e1[1] += q1.y, e2[0] += q2.x, e2[1] += q2.y;
             }
             if (gated) {
 #pragma unroll
-                for (int l = 0; l < L; ++l) {
-                    const float2 q3 = *reinterpret_cast<const float2 *>(&e_at[2][t][l][lc]);
+                for (int l0 = 0; l0 < L / SUB; ++l0) {
+                    const float2 q3 = *reinterpret_cast<const float2 *>(&e_at[2][t][sub * (L / SUB) + l0][lc]);
                     e3[0] += q3.x, e3[1] += q3.y;
                 }
             }
+#pragma unroll
+            for (int o = CH / 2; o < CH / 2 * SUB; o *= 2)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    e1[q] += __shfl_xor_sync(0xffffffffu, e1[q], o);
+                    e2[q] += __shfl_xor_sync(0xffffffffu, e2[q], o);
+                    e3[q] += __shfl_xor_sync(0xffffffffu, e3[q], o);
+                }
+            if (n == 0) continue;
             const Kept &o = of[i];
             upk(value(o.x), x[0], x[1]), upk(value(o.g), z[0], z[1]), upk(value(o.y), y[0], y[1]);
 #pragma unroll
@@ -331,7 +342,7 @@ __global__ void __launch_bounds__(2 * kThr, 2) ss_backward_kernel(const SsArgs w
     if (n_chunk > 0) finish(t_first, 0, now);
     {  // nothing stands behind a sequence
         const long long out = static_cast<long long>(b) * w.T * w.D + ld;
-        for (int t = max(t_len, t_first) + lt; t < t_end; t += LT) {
+        for (int t = max(t_len, t_first) + lt; t < t_end && sub == 0; t += LT) {
             const long long to = out + static_cast<long long>(t) * w.D;
             store_pair<VEC>(static_cast<T *>(w.dx) + to, 0ull, have);
             store_pair<VEC>(static_cast<T *>(w.ddt) + to, 0ull, have);
@@ -345,7 +356,7 @@ __global__ void __launch_bounds__(2 * kThr, 2) ss_backward_kernel(const SsArgs w
     if (tid < CH / 2) {
         float4 s = s_sum[tid];
 #pragma unroll
-        for (int i = 1; i < LT; ++i) {
+        for (int i = 1; i < LT * SUB; ++i) {
             const float4 u = s_sum[tid + i * (CH / 2)];
             s.x += u.x, s.y += u.y, s.z += u.z, s.w += u.w;
         }
@@ -386,12 +397,12 @@ cudaError_t launch(const SsArgs &a, cudaStream_t s) {
     kernel<<<static_cast<unsigned>(ss_backward_tiles(a)) * a.G * a.n_seg * a.B, 2 * kThr, bytes, s>>>(a);
     return cudaGetLastError();
 }
-int lanes(int N) { return N <= 4 ? 2 : N <= 8 ? 4 : N <= 16 ? 8 : N <= 32 ? 16 : 32; }
+// eight lanes even where four or two would hold the states: those have more tokens to a preparing thread than registers for
+// them (8 states: 69 us per million tokens and channels against 42)
+int lanes(int N) { return N <= 16 ? 8 : N <= 32 ? 16 : 32; }
 template <typename T, bool VEC>
 cudaError_t launch_of(const SsArgs &a, cudaStream_t s) {
     switch (lanes(a.N)) {
-        case 2: return launch<T, 2, 2, VEC>(a, s);
-        case 4: return launch<T, 2, 4, VEC>(a, s);
         case 8: return launch<T, 2, 8, VEC>(a, s);
         case 16: return launch<T, 2, 16, VEC>(a, s);
         default: return launch<T, 2, 32, VEC>(a, s);
