@@ -1379,10 +1379,10 @@ def layer_norm(x, weight=None, bias=None, *, residual=None, rms: bool = False, e
         if r is not None:
             raise ValueError("out has a stream, but there is no residual")
     elif r is None:
-        r = torch.empty(x.shape, dtype=residual.dtype, device=x.device)
+        r = residual.new_empty(x.shape)
     if y is None:
-        y = torch.empty(x.shape, dtype=y_dtype, device=x.device)
-    stats = torch.empty((*x.shape[:-1], 2), dtype=torch.float32, device=x.device)
+        y = x.new_empty(x.shape, dtype=y_dtype)
+    stats = x.new_empty((*x.shape[:-1], 2), dtype=torch.float32)
     f32, rd = torch.float32, x.dtype if residual is None else residual.dtype
     _checked(lib().pararnn_layer_norm(
         s, _like(x, "x", x, x.shape, x.dtype), _like(residual, "residual", x, x.shape, rd),
