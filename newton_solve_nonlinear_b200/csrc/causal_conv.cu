@@ -5,6 +5,7 @@
 //   q_t = dy_t act'(p_t),   dx_t = sum_k w_k q_(t+k),   dweight[W-1-k] = sum q_t x_(t-k),   dbias = sum q_t
 // Inputs before the first are the state's rows, or zero; the last W - 1 inputs are the next state.
 #include <algorithm>
+#include <type_traits>
 
 #include "causal_conv.cuh"
 #include "rows.cuh"
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(256, 2) cc_backward_kernel(const CcArgs w, int
             // token `at`: its q, and dx of token at - (W - 1), which is complete with it; own: not one behind the run
             T *dx = static_cast<T *>(w.dx) + (static_cast<long long>(b) * w.T + t0 - (W - 1)) * w.D + c;
             const int plain = max(len - W, -1) + 1;  // dx of tokens 0 .. plain - 1 has no part of dlast and counts
-            auto token = [&](int at, bool own, const Raw<T, V> &rx, const Raw<T, V> &rg) {
+            auto token = [&](auto inside, int at, bool own, const Raw<T, V> &rx, const Raw<T, V> &rg) {
                 rx.to(x), rg.to(g);
                 shift(win, x);
                 float p[V], out[V] = {};
@@ -271,7 +272,9 @@ __global__ void __launch_bounds__(256, 2) cc_backward_kernel(const CcArgs w, int
                     add_product(wk[W - 1 - k], q[k], out);
                 }
                 const int back = at - (W - 1);
-                if (back >= from && back < t_end) {
+                if constexpr (decltype(inside)::value) {
+                    put<T, V>(dx, out);
+                } else if (back >= from && back < t_end) {
                     if (static_cast<unsigned>(back) >= static_cast<unsigned>(plain)) {
                         const int j_last = back - len + W - 1;  // the row of dlast that is x_back
                         if (w.dlast != nullptr && j_last >= 0 && j_last < W - 1) {
@@ -293,20 +296,26 @@ __global__ void __launch_bounds__(256, 2) cc_backward_kernel(const CcArgs w, int
                 dx += w.D;
             };
             const int stop = t_end + W - 1;
+            const T *px = in.x + static_cast<long long>(t0 + AHEAD) * in.st, *pg = pdy + static_cast<long long>(t0 + AHEAD) * w.dy.st;
             for (int t = t0; t < stop; t += AHEAD) {
                 Raw<T, V> cx[AHEAD], cg[AHEAD];
 #pragma unroll
                 for (int j = 0; j < AHEAD; ++j) cx[j] = nx[j], cg[j] = ng[j];
-                if (t + AHEAD < stop) {
+                if (t + 2 * AHEAD <= len) {
+#pragma unroll
+                    for (int j = 0; j < AHEAD; ++j) nx[j].get(px + j * w.x.st), ng[j].get(pg + j * w.dy.st);
+                } else if (t + AHEAD < stop) {
 #pragma unroll
                     for (int j = 0; j < AHEAD; ++j) nx[j] = in.later(t + AHEAD + j), ng[j] = grad(t + AHEAD + j);
                 }
-                if (t + AHEAD <= t_end) {
+                px += AHEAD * w.x.st, pg += AHEAD * w.dy.st;
+                // inside a run nothing has to be asked: dx is of its own tokens, which count and have no part of dlast
+                if (t >= t0 + W - 1 && t + AHEAD <= t_end && t + AHEAD - W < plain) {
 #pragma unroll
-                    for (int j = 0; j < AHEAD; ++j) token(t + j, true, cx[j], cg[j]);
+                    for (int j = 0; j < AHEAD; ++j) token(std::true_type{}, t + j, true, cx[j], cg[j]);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < AHEAD; ++j) token(t + j, t + j < t_end, cx[j], cg[j]);
+                    for (int j = 0; j < AHEAD; ++j) token(std::false_type{}, t + j, t + j < t_end, cx[j], cg[j]);
                 }
             }
         }
@@ -417,13 +426,15 @@ struct Grid {
     int tx, x, y, run;
 };
 Grid backward_grid(const CcArgs &a, int v) {
-    const int nv = (a.D + v - 1) / v, run = std::min(run_of(a, v), 32);
+    const int nv = (a.D + v - 1) / v;
     int tx = 1;
     while (tx < nv && tx < 32) tx *= 2;
-    const int x = (nv + tx - 1) / tx, ty = 256 / tx;
+    // one wave of two CTAs per SM, and a run for each of their threads: every run's start waits for its first loads
+    const int x = (nv + tx - 1) / tx, ty = 256 / tx, rows = std::max(1, 148 * 2 / x) * ty;
+    const int splits = std::max(1, rows / a.B);
+    const int run = std::max(8, ((a.T + splits - 1) / splits + 3) / 4 * 4);
     const long long all = static_cast<long long>((a.T + run - 1) / run) * a.B;
-    const long long y = std::min<long long>((all + ty - 1) / ty, std::max(1, (148 * 4 + x - 1) / x));
-    return {tx, x, static_cast<int>(y), run};
+    return {tx, x, static_cast<int>(std::min<long long>((all + ty - 1) / ty, rows / ty)), run};
 }
 template <typename T, int W>
 void backward_of(const CcArgs &a, bool vec, cudaStream_t s) {
