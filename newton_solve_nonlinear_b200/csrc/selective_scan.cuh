@@ -127,10 +127,10 @@ __device__ __forceinline__ float softplus(float v) {
     float unused;
     return softplus(v, unused);
 }
-// 1 / (1 + exp(-z))
+// 1 / (1 + exp(-z)); below -88 it is zero, as exp(88.7) is still finite and its inverse no longer a normal number
 __device__ __forceinline__ float sigmoid_of(float z) {
     float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + exp_of(min_nan(max_nan(-z, -80.f), 80.f))));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + exp_of(min_nan(max_nan(-z, -88.7f), 88.7f))));
     return r;
 }
 __device__ __forceinline__ float gate_with(float y, float z) { return y * (z * sigmoid_of(z)); }
