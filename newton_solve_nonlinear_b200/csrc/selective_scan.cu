@@ -410,9 +410,9 @@ cudaError_t launch_ss_reverse_states(const SsArgs &a, cudaStream_t s) {
 
 namespace {
 
-// CTAs along the channels of each row; L lanes of four states hold a channel, each thread of R channels that stand CH apart.
-// Everything that a row needs is asked for at once, behind its slot alone.  Rows that name the same slot are taken in row
-// order by the first one's CTA, as tokens that follow each other.  Bound by HBM.
+// CTAs along the channels of each row; L lanes of four states hold a channel, each thread of R channels that stand CH apart,
+// of which it prepares and finishes one (the lanes take turns).  Everything that a row needs is asked for at once, behind its
+// slot alone.  Rows that name the same slot are taken in row order by the first one's CTA, as tokens that follow each other.
 template <typename T, int L, int R, bool VEC>
 __global__ void __launch_bounds__(256) ss_step_kernel(const SsStep w) {
     constexpr int CH = 256 / L, BW = VEC ? 4 : 1;
@@ -429,62 +429,71 @@ __global__ void __launch_bounds__(256) ss_step_kernel(const SsStep w) {
     }
     const bool vec = w.N % 4 == 0, vec_a = vec && (reinterpret_cast<uintptr_t>(w.a) & 15) == 0;
     const long long at = (static_cast<long long>(slot) * w.D + d0) * w.N;
+    static_assert(R <= L, "a lane for each channel");
+    const int mine = R == 1 ? 0 : tid & 1, dm = d0 + mine * CH;
     u64 h[R][2] = {}, a[R][2] = {};
-    float bias[R] = {}, skip[R] = {};
+    float bias = 0.f, skip = 0.f;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const int d = d0 + r * CH;
         if (d >= w.D) continue;
         load_states(h[r], w.state + at + static_cast<long long>(r) * CH * w.N, n0, w.N, vec);
         load_states(a[r], w.a + static_cast<long long>(d) * w.N, n0, w.N, vec_a);
-        if (w.dt_bias != nullptr) bias[r] = w.dt_bias[d];
-        if (w.skip != nullptr) skip[r] = w.skip[d];
     }
-    T x[R], s[R], z[R];
+    if (dm < w.D && w.dt_bias != nullptr) bias = w.dt_bias[dm];
+    if (dm < w.D && w.skip != nullptr) skip = w.skip[dm];
+    T x, s, z;
     RawN<T, BW> rb[R][4 / BW], rc[R][4 / BW];
     auto fetch = [&]() {
+        x = s = z = from_f<T>(0.f);
+        if (dm < w.D) {
+            x = static_cast<const T *>(w.x.p)[b * w.x.sb + dm], s = static_cast<const T *>(w.dt.p)[b * w.dt.sb + dm];
+            if (w.gate.p != nullptr) z = static_cast<const T *>(w.gate.p)[b * w.gate.sb + dm];
+        }
+        const T *pb = static_cast<const T *>(w.b.p) + b * w.b.sb + n0, *pc = static_cast<const T *>(w.c.p) + b * w.c.sb + n0;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int d = d0 + r * CH;
             const bool on = d < w.D;
+            if (r > 0 && w.G == 1) {  // one group: the same b and c
+#pragma unroll
+                for (int i = 0; i < 4 / BW; ++i) rb[r][i] = rb[0][i], rc[r][i] = rc[0][i];
+                continue;
+            }
             const int g = on && w.G > 1 ? d / per : 0;
-            x[r] = s[r] = z[r] = from_f<T>(0.f);
-            if (on) x[r] = static_cast<const T *>(w.x.p)[b * w.x.sb + d], s[r] = static_cast<const T *>(w.dt.p)[b * w.dt.sb + d];
-            if (on && w.gate.p != nullptr) z[r] = static_cast<const T *>(w.gate.p)[b * w.gate.sb + d];
 #pragma unroll
             for (int i = 0; i < 4 / BW; ++i) {
-                const int n = n0 + i * BW;
-                rb[r][i] = load_n<BW>(static_cast<const T *>(w.b.p) + b * w.b.sb + g * w.b.sg + n, on && n < w.N);
-                rc[r][i] = load_n<BW>(static_cast<const T *>(w.c.p) + b * w.c.sb + g * w.c.sg + n, on && n < w.N);
+                rb[r][i] = load_n<BW>(pb + g * w.b.sg + i * BW, on && n0 + i * BW < w.N);
+                rc[r][i] = load_n<BW>(pc + g * w.c.sg + i * BW, on && n0 + i * BW < w.N);
             }
         }
     };
     auto token = [&]() {
+        const float xf = to_f(x);
+        float st = to_f(s) + bias, out[R];
+        if (w.softplus) st = softplus(st);
+        const float u = st * xf;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int d = d0 + r * CH;
-            const float xf = to_f(x[r]);
-            float st = to_f(s[r]) + bias[r];
-            if (w.softplus) st = softplus(st);
-            __align__(16) float bf[4], cf[4];
+            const int from = R == 1 ? tid & 31 : (tid & 30) | r;
+            const u64 st2 = splat(__shfl_sync(0xffffffffu, st, from)), u2 = splat(__shfl_sync(0xffffffffu, u, from));
+            float bf[4], cf[4];
 #pragma unroll
             for (int i = 0; i < 4 / BW; ++i) unpack_n(bf + i * BW, rb[r][i]), unpack_n(cf + i * BW, rc[r][i]);
             u64 y = 0;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const u64 e = decay_less_one(mul2(splat(st), mul2(a[r][i], splat(kLog2eF))));
-                h[r][i] = fma2(e, h[r][i], fma2(splat(st * xf), pk(bf[2 * i], bf[2 * i + 1]), h[r][i]));
-                y = fma2(pk(cf[2 * i], cf[2 * i + 1]), h[r][i], y);
+                const u64 e = decay_less_one(mul2(st2, mul2(a[r][i], splat(kLog2eF))));
+                h[r][i] = fma2(e, h[r][i], fma2(u2, pk(bf[2 * i], bf[2 * i + 1]), h[r][i]));
+                y = i == 0 ? mul2(pk(cf[0], cf[1]), h[r][0]) : fma2(pk(cf[2], cf[3]), h[r][1], y);
             }
-            float out = pair_sum(y);
+            out[r] = pair_sum(y);
 #pragma unroll
-            for (int o = L / 2; o > 0; o >>= 1) out += __shfl_xor_sync(0xffffffffu, out, o);
-            if (d < w.D && n0 == 0) {
-                out = fmaf(skip[r], xf, out);
-                if (w.gate.p != nullptr) out = gate_with(out, to_f(z[r]));
-                py[static_cast<long long>(b) * w.D + d] = from_f<T>(out);
-            }
+            for (int o = L / 2; o > 0; o >>= 1) out[r] += __shfl_xor_sync(0xffffffffu, out[r], o);
         }
+        float v = fmaf(skip, xf, mine == 0 ? out[0] : out[R - 1]);
+        if (w.gate.p != nullptr) v = gate_with(v, to_f(z));
+        if (dm < w.D && tid % L < R) py[static_cast<long long>(b) * w.D + dm] = from_f<T>(v);
     };
     fetch();
     bool more = false;
@@ -528,8 +537,8 @@ void launch_step(const SsStep &w, cudaStream_t s) {
         quads = quads && reinterpret_cast<uintptr_t>(r->p) % e == 0 && r->sb % 4 == 0 && r->sg % 4 == 0;
     const unsigned two = static_cast<unsigned>((w.D + 2 * CH - 1) / (2 * CH)) * w.B;
     if (!quads) ss_step_kernel<T, L, 1, false><<<static_cast<unsigned>(one), 256, 0, s>>>(w);
-    else if (one <= 148 * 6) ss_step_kernel<T, L, 1, true><<<static_cast<unsigned>(one), 256, 0, s>>>(w);  // one wave
-    else ss_step_kernel<T, L, 2, true><<<two, 256, 0, s>>>(w);
+    else if (L == 1 || one <= 148 * 6) ss_step_kernel<T, L, 1, true><<<static_cast<unsigned>(one), 256, 0, s>>>(w);  // one wave
+    else ss_step_kernel<T, L, L == 1 ? 1 : 2, true><<<two, 256, 0, s>>>(w);
 }
 template <typename T>
 void step_of(const SsStep &w, cudaStream_t s) {
