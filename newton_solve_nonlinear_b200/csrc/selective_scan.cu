@@ -416,7 +416,7 @@ namespace {
 // of which it prepares and finishes one (the lanes take turns).  Everything that a row needs is asked for at once, behind its
 // slot alone.  Rows that name the same slot are taken in row order by the first one's CTA, as tokens that follow each other.
 // 256 rows of 4096 channels of 16: 43.5 us, 0.48 of HBM's rate, bound by instructions (one channel to a thread, prepared by
-// all of its lanes, with its loads in four rounds: 83).
+// all of its lanes, with its loads in four steps: 83).
 template <typename T, int L, int R, bool VEC>
 __global__ void __launch_bounds__(256) ss_step_kernel(const SsStep w) {
     constexpr int CH = 256 / L, BW = VEC ? 4 : 1;
