@@ -922,9 +922,9 @@ PARARNN_API size_t pararnn_selective_scan_workspace_size(const pararnn_scan_shap
  *            before every eighth token, for the backward pass.  Those at and
  *            behind lengths[b] are not written.
  *   workspace  DEVICE, pararnn_selective_scan_workspace_size bytes, 256-byte aligned.
- * Steps, decays, states and sums are fp32; exp(s a) enters as the difference
- * from 1, so that slow decays keep their rate.  Outputs must not overlap inputs
- * or the workspace.  Repeated calls give the same bits.  Asynchronous: returns
+ * Steps, decays, states and sums are fp32; exp(s a) of a slow decay enters as the
+ * difference from 1, so that it keeps its rate, any other as itself, so that it
+ * keeps its digits.  Outputs must not overlap inputs or the workspace.  Repeated calls give the same bits.  Asynchronous: returns
  * PARARNN_OK, INVALID_ARG or CUDA_ERROR.
  */
 PARARNN_API int pararnn_selective_scan(const pararnn_scan_shape *shape, const pararnn_rows *x, const pararnn_rows *dt,

@@ -106,12 +106,12 @@ __global__ void __launch_bounds__(2 * kThr, 2) ss_sweep_kernel(const SsArgs w) {
                         u64 part = 0;
 #pragma unroll
                         for (int i = 0; i < Q; ++i) {
-                            const u64 e = decay_less_one(pk(st * a[q][2 * i], st * a[q][2 * i + 1]));
+                            const u64 xx = pk(st * a[q][2 * i], st * a[q][2 * i + 1]), f = decay_factor(xx);
                             // one factor for both of a pair: two instructions, as moving it beside itself would take
                             float b0, b1, h0, h1;
-                            upk(bb[i], b0, b1), upk(h[q][i], h0, h1);
+                            upk(bb[i], b0, b1), upk(REV ? h[q][i] : decay_rest(xx, h[q][i]), h0, h1);
                             const u64 moved = pk(fmaf(u, b0, h0), fmaf(u, b1, h1));
-                            h[q][i] = REV ? fma2(e, moved, moved) : fma2(e, h[q][i], moved);
+                            h[q][i] = REV ? fma2(f, moved, decay_rest(xx, moved)) : fma2(f, h[q][i], moved);
                             if (OUT) part = i == 0 ? mul2(cc[i], h[q][i]) : fma2(cc[i], h[q][i], part);
                         }
                         if (OUT) y[q] = pair_sum(part);
@@ -487,8 +487,8 @@ __global__ void __launch_bounds__(256) ss_step_kernel(const SsStep w) {
             u64 y = 0;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const u64 e = decay_less_one(mul2(st2, mul2(a[r][i], splat(kLog2eF))));
-                h[r][i] = fma2(e, h[r][i], fma2(u2, pk(bf[2 * i], bf[2 * i + 1]), h[r][i]));
+                const u64 xx = mul2(st2, mul2(a[r][i], splat(kLog2eF)));
+                h[r][i] = fma2(decay_factor(xx), h[r][i], fma2(u2, pk(bf[2 * i], bf[2 * i + 1]), decay_rest(xx, h[r][i])));
                 y = i == 0 ? mul2(pk(cf[0], cf[1]), h[r][0]) : fma2(pk(cf[2], cf[3]), h[r][1], y);
             }
             out[r] = pair_sum(y);

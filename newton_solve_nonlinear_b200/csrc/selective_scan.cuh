@@ -243,16 +243,24 @@ __device__ __forceinline__ void store_pair(float *p, u64 v, int n) {
     }
 }
 
-// exp(s a) - 1 for a pair of states, from x = s a log2(e).  The state is updated as h + (exp(s a) - 1) h: rounded to fp32,
-// exp(s a) of a slow decay would be another decay, taken at every token.  Near zero the difference comes from its series
-// (the first term left out is (ln 2 / 64)^3 / 24 = 5e-8 of it), further away from ex2, whose 1.3e-7 counts for no more than
-// the 92 tokens that such a state remembers.
-__device__ __forceinline__ u64 decay_less_one(u64 x) {
+// A decay takes v to f v + (slow ? v : 0), for a pair of states with x = s a log2(e): f is exp(s a) - 1 where the decay is slow
+// and exp(s a) elsewhere.  Rounded to fp32, exp(s a) of a slow decay would be another decay, taken at every token; the
+// difference from 1 of a fast one would leave 2^-24 of the old value behind, where exp(s a) may be far below that.  Near zero
+// the difference comes from its series (the first term left out is (ln 2 / 64)^3 / 24 = 5e-8 of it), further away exp(s a)
+// from ex2, whose 1.3e-7 counts for no more than the 92 tokens that such a state remembers.
+__device__ __forceinline__ bool slow_decay(float x) { return fabsf(x) < 0.015625f; }
+__device__ __forceinline__ u64 decay_factor(u64 x) {
     const u64 p = mul2(x, fma2(x, fma2(x, splat(0.0555041087f), splat(0.240226507f)), splat(0.693147181f)));
-    const u64 e = add2(ex2_2(x), splat(-1.f));
+    const u64 e = ex2_2(x);
     float x0, x1, p0, p1, e0, e1;
     upk(x, x0, x1), upk(p, p0, p1), upk(e, e0, e1);
-    return pk(fabsf(x0) < 0.015625f ? p0 : e0, fabsf(x1) < 0.015625f ? p1 : e1);
+    return pk(slow_decay(x0) ? p0 : e0, slow_decay(x1) ? p1 : e1);
+}
+// what stays beside f v
+__device__ __forceinline__ u64 decay_rest(u64 x, u64 v) {
+    float x0, x1, v0, v1;
+    upk(x, x0, x1), upk(v, v0, v1);
+    return pk(slow_decay(x0) ? v0 : 0.f, slow_decay(x1) ? v1 : 0.f);
 }
 
 template <int PAIRS>

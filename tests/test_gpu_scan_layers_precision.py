@@ -1,0 +1,100 @@
+"""Digits that the selective state space block keeps: decays that forget, rates without end, slopes far from zero, long sums and
+rows behind a length.  Every tolerance counts half steps, U = 2^-24 of a value, and is stated beside its test."""
+import pytest
+import torch
+
+import newton_solve_nonlinear_b200 as fw
+from tests.test_gpu_selective_scan import BF16, F32
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+
+
+def _relative(got, want, steps, what):
+    """got is within `steps` half steps of want, element by element, and its rounding to bf16."""
+    tol = steps * U + (2.0 ** -8 if got.dtype == BF16 else 0.0)
+    worst = float(((got.double() - want).abs() / want.abs()).max())
+    assert worst <= tol, f"{what}: {worst:.3g} of the value, {tol:.3g} allowed"
+
+
+def _forgetting(B, T, G, per, N, dtype, seed):
+    """A step of 1 and rates of 8 to 30: each token replaces the state.  All is positive, so that no sum cancels; inputs lie
+    between 1e-5 and 1e4, so that a small one often follows a large one."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    u = lambda lo, hi, *s: lo + (hi - lo) * torch.rand(*s, device="cuda", generator=g)
+    D = G * per
+    p = dict(x=10 ** u(-5, 4, B, T, D), dt=torch.ones(B, T, D, device="cuda"), a=-u(8, 30, D, N), b=u(0.5, 1.5, B, T, G, N),
+             c=u(0.5, 1.5, B, T, G, N))
+    p = {k: v if k == "a" else v.to(dtype) for k, v in p.items()}
+    return p, u(1, 100, B, D, N), u(0.5, 1.5, B, T, D).to(dtype), u(0.5, 1.5, B, D, N)
+
+
+def _forgetting64(p, h0, dy, dh):
+    """The formulas in 64 bits: the states, y and every gradient."""
+    x, a, dy, h, P = p["x"].double(), p["a"].double(), dy.double(), h0.double(), dh.double()
+    B, T, D = x.shape
+    G, N = p["b"].shape[2:]
+    b, c = (p[k].double().repeat_interleave(D // G, dim=2) for k in "bc")
+    w, hs = torch.exp(a), [h]
+    for t in range(T):
+        hs.append(w * hs[-1] + x[:, t, :, None] * b[:, t])
+    y = torch.stack([(c[:, t] * hs[t + 1]).sum(-1) for t in range(T)], 1)
+    da, out = torch.zeros_like(a), dict(dx=[], ddt=[], db=[], dc=[])
+    shared = lambda v: v.reshape(B, G, D // G, N).sum(2)
+    for t in reversed(range(T)):
+        g = P + dy[:, t, :, None] * c[:, t]
+        gb = (g * b[:, t]).sum(-1)
+        out["dc"].insert(0, shared(dy[:, t, :, None] * hs[t + 1]))
+        out["db"].insert(0, shared(g * x[:, t, :, None]))
+        out["dx"].insert(0, gb)
+        P = w * g
+        da += (P * hs[t]).sum(0)
+        out["ddt"].insert(0, (a * P * hs[t]).sum(-1) + x[:, t] * gb)
+    return y, hs[-1], dict({k: torch.stack(v, 1) for k, v in out.items()}, da=da, dh0=P)
+
+
+# one token and a few; segments of time; each width of a full card: 104 groups give 104 CTAs, which take four states a thread
+FORGETTING = [(2, 1, 1, 6, 16), (1, 5, 1, 3, 2), (2, 300, 2, 20, 16), (1, 200, 1, 9, 64), (1, 9, 104, 1, 3), (1, 20, 104, 1, 7),
+              (1, 20, 104, 2, 16), (2, 17, 52, 66, 16), (1, 20, 104, 1, 30), (1, 20, 104, 2, 64)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("size", FORGETTING)
+def test_a_decay_that_forgets_keeps_its_own_digits(size, dtype):
+    """exp(z) is off by U for each of z's two roundings and the constant's, times |z| <= 30, and by ex2's four U: 94 U; the
+    product and the sum round twice more.  What a token inherits is at most e^-8 of errors like these once more, so 100 U
+    hold for a state and for P, 200 U for their product, and every sum of n positive terms adds n U."""
+    B, T, G, per, N = size
+    p, h0, dy, dh = _forgetting(*size, dtype, seed=N)
+    y, h, kept = fw.selective_scan(*p.values(), softplus=False, h0=h0, keep=True)
+    wy, wh, want = _forgetting64(p, h0, dy, dh)
+    _relative(h, wh, 110, "h")
+    _relative(y, wy, 110 + N, "y")
+    for given in (kept, None):
+        g = fw.selective_scan_backward(*p.values(), dy, softplus=False, h0=h0, dh=dh, kept=given)
+        for k, steps in dict(dh0=110, da=220 + T + B, dx=110 + N, db=110 + per, dc=110 + per).items():
+            _relative(g[k], want[k], steps, k)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("size", [(2, 1, 1, 6, 16), (1, 2, 1, 5, 64), (1, 2, 104, 2, 16)])
+def test_a_step_s_gradient_through_decays_that_forget(size, dtype):
+    """Without inputs ddt is the sum of a P h alone, of one sign: 200 U for P h, one for the rate and N for the sum."""
+    p, h0, dy, dh = _forgetting(*size, dtype, seed=3)
+    p["x"].zero_()
+    g = fw.selective_scan_backward(*p.values(), dy, softplus=False, h0=h0, dh=dh)
+    _relative(g["ddt"], _forgetting64(p, h0, dy, dh)[2]["ddt"], 230 + size[-1], "ddt")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,G,per,N", [(1, 1, 5, 1), (3, 2, 21, 5), (2, 1, 300, 16), (5, 1, 40, 64)])
+def test_a_step_that_forgets(B, G, per, N, dtype):
+    """As above, for one token of each sequence."""
+    p, h0, dy, dh = _forgetting(B, 1, G, per, N, dtype, seed=4)
+    q = {k: v if k == "a" else v[:, 0] for k, v in p.items()}
+    state = h0.clone()
+    y = fw.selective_scan_step(*q.values(), state, softplus=False)
+    wy, wh, _ = _forgetting64(p, h0, dy, dh)
+    _relative(state, wh, 110, "state")
+    _relative(y[:, None], wy, 110 + N, "y")
