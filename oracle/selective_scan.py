@@ -59,7 +59,10 @@ def _per_group(x, G):
 class Scan:
     """One call's operands; ``forward`` and ``backward`` give {name: (value, bound on fp32's error)}."""
 
-    def __init__(self, x, dt, a, b, c, skip=None, gate=None, dt_bias=None, use_softplus=True, h0=None, lengths=None):
+    def __init__(self, x, dt, a, b, c, skip=None, gate=None, dt_bias=None, use_softplus=True, h0=None, lengths=None,
+                 joined=None):
+        """joined: of how many terms the sums of steps are that join segments of time; as many as there are tokens if None, 0
+        where time is not split."""
         B, T, D = x.shape
         self.G, N = b.shape[2:]
         self.on = on = _on(lengths, B, T)
@@ -77,10 +80,12 @@ class Scan:
         # what fp32 makes of the step: the sum rounds, softplus is within eight steps
         es = U * (np.abs(self.raw) * bounds.sigmoid(self.raw) + 16 * self.s) if use_softplus else U * np.abs(self.s)
         es = np.where(on[..., None], es, 0.0)
-        # exp(z) - 1: z's error (the step's, two roundings, and those of a sum of T steps where segments join), its series or
-        # ex2's 1.3e-7, and the two roundings of h + (exp(z) - 1) h
-        ez = es[..., None] * np.abs(a) + (2 + T) * U * np.abs(z)
-        ed = self.decay * ez + 8 * U * np.abs(np.expm1(z)) + 4 * U * (np.abs(z) > 0.04) + 2 * U
+        # z's error: the step's, two roundings, and those of a sum of steps where segments join
+        ez = es[..., None] * np.abs(a) + (2 + (T if joined is None else joined)) * U * np.abs(z)
+        # a slow decay enters as exp(z) - 1, from its series, and as a product beside the old value, whose sum with the input
+        # rounds once more; any other as exp(z) from ex2, within 1.3e-7 of itself.  (Above 0.01: a kernel may take the
+        # difference a little further.)
+        ed = self.decay * ez + np.where(np.abs(z) < 0.01, 8 * U * np.abs(np.expm1(z)) + 2 * U, 4 * U * self.decay)
         self.bs, self.bdecay = Bound(self.s, es), Bound(self.decay, np.where(on[..., None, None], ed, 0.0))
 
     def _bounds(self):
