@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(2 * kThr, 2) ss_sweep_kernel(const SsArgs w) {
             if (q >= owns) continue;
 #pragma unroll
             for (int i = 0; i < S; ++i)
-                if (n0 + i < w.N) a[q][i] = w.a[(static_cast<long long>(d) + q) * w.N + n0 + i] * kLog2eF;
+                if (n0 + i < w.N) a[q][i] = rate_of(w.a[(static_cast<long long>(d) + q) * w.N + n0 + i]);
             if (!SUMS) {
                 const float *from = w.n_seg > 1 ? w.seg_state + seg * all : w.h0;
                 if (from != nullptr) load_states(h[q], from + at_d + q * w.N, n0, w.N, vec);
@@ -290,7 +290,7 @@ __global__ void ss_join_kernel(const SsArgs w) {
     const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
     if (i >= all) return;
     const long long bd = i / w.N;
-    const float a = w.a[bd % w.D * w.N + i % w.N];
+    const float a = finite(w.a[bd % w.D * w.N + i % w.N]);
     const float *first = REV ? w.dh : w.h0;
     float *at = (REV ? w.rev_state : w.seg_state) + i;
     float h = first == nullptr ? 0.f : first[i];
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(256) ss_step_kernel(const SsStep w) {
             u64 y = 0;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const u64 xx = mul2(st2, mul2(a[r][i], splat(kLog2eF)));
+                const u64 xx = mul2(st2, a[r][i]);
                 h[r][i] = fma2(decay_factor(xx), h[r][i], fma2(u2, pk(bf[2 * i], bf[2 * i + 1]), decay_rest(xx, h[r][i])));
                 y = i == 0 ? mul2(pk(cf[0], cf[1]), h[r][0]) : fma2(pk(cf[2], cf[3]), h[r][1], y);
             }
@@ -500,6 +500,14 @@ __global__ void __launch_bounds__(256) ss_step_kernel(const SsStep w) {
         if (dm < w.D && tid % L < R) py[static_cast<long long>(b) * w.D + dm] = from_f<T>(v);
     };
     fetch();
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float a0, a1;
+            upk(a[r][i], a0, a1);
+            a[r][i] = pk(rate_of(a0), rate_of(a1));
+        }
     bool more = false;
     if (w.slots != nullptr) {
         int earlier = 0, later = 0;

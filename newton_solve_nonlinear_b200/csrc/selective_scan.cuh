@@ -97,6 +97,10 @@ __device__ __forceinline__ float min_nan(float a, float b) {
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
+// A rate as the kernels take it, in powers of two.  Kept finite: -inf forgets at every token, but where a step is zero (in the
+// places behind a sequence, too) nothing decays, and zero times infinity would be NaN.
+__device__ __forceinline__ float finite(float v) { return min_nan(max_nan(v, -3.402823466e38f), 3.402823466e38f); }
+__device__ __forceinline__ float rate_of(float a) { return finite(a * kLog2eF); }
 // exp(v), |v| at most 150: ex2 of v log2(e) rounded, times what that rounding left out.  (One value at a time: a constant
 // of a packed operation takes two registers and two instructions to fill them.)
 __device__ __forceinline__ float exp_of(float v) {

@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(2 * kThr, 2) ss_backward_kernel(const SsArgs w
             if (q >= owns) continue;
 #pragma unroll
             for (int i = 0; i < S; ++i)
-                if (n0 + i < w.N) a[q][i] = w.a[(static_cast<long long>(d) + q) * w.N + n0 + i] * kLog2eF;
+                if (n0 + i < w.N) a[q][i] = rate_of(w.a[(static_cast<long long>(d) + q) * w.N + n0 + i]);
             const float *from = w.n_seg > 1 ? w.rev_state + seg * all : w.dh;
             if (from != nullptr) load_states(p[q], from + at_d + q * w.N, n0, w.N, vec);
         }

@@ -98,3 +98,37 @@ def test_a_step_that_forgets(B, G, per, N, dtype):
     wy, wh, _ = _forgetting64(p, h0, dy, dh)
     _relative(state, wh, 110, "state")
     _relative(y[:, None], wy, 110 + N, "y")
+
+
+@pytest.mark.parametrize("rate", [float("-inf"), -3e38])
+@pytest.mark.parametrize("size", [(3, 13, 1, 6, 16), (3, 300, 1, 5, 9), (3, 13, 35, 2, 16)])
+def test_rates_without_end(size, rate):
+    """A rate of -inf forgets at every token, and only there: the places behind a length, the empty segments and tokens of
+    step zero (softplus of -inf) decay nothing.  -1e30 takes the same steps with finite products, to the same bits."""
+    B, T, G, per, N = size
+    D = G * per
+    g = torch.Generator(device="cuda").manual_seed(9)
+    n = lambda *s: torch.randn(*s, device="cuda", generator=g)
+    p = dict(x=n(B, T, D), dt=n(B, T, D), a=-torch.exp(n(D, N)), b=n(B, T, G, N), c=n(B, T, G, N))
+    p["a"][:, ::2] = -1e30
+    o = dict(h0=n(B, D, N), lengths=torch.tensor([T, 0, min(T - 2, 70)], dtype=torch.int32, device="cuda"))
+    dy, dh = n(B, T, D), n(B, D, N)
+
+    def run(a):
+        q = dict(p, a=a)
+        y, h, kept = fw.selective_scan(*q.values(), keep=True, **o)
+        back = fw.selective_scan_backward(*q.values(), dy, dh=dh, **o)
+        q["dt"] = p["dt"].clone()
+        q["dt"][:, 5:8] = float("-inf")
+        z, k = fw.selective_scan(*q.values(), **o)
+        pool = o["h0"].clone()
+        one = {k: v if k == "a" else v[:, 5] for k, v in q.items()}
+        out = fw.selective_scan_step(*one.values(), pool)
+        return dict(back, y=y, h=h, z=z, k=k, step=out, pool=pool)
+
+    want, got = run(p["a"]), run(torch.where(p["a"] == -1e30, rate, p["a"]))
+    for k, v in want.items():
+        if v is not None:
+            assert torch.isfinite(v).all() and torch.equal(got[k], v), k
+    assert torch.equal(got["pool"], o["h0"]) and torch.equal(got["h"][1], o["h0"][1])
+    assert torch.equal(got["dh0"][1], dh[1])
