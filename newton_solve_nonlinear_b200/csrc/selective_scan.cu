@@ -298,7 +298,8 @@ __global__ void ss_join_kernel(const SsArgs w) {
         const int seg = REV ? w.n_seg - 1 - k : k;
         const float own = at[seg * all];
         at[seg * all] = h;
-        h = fmaf(expf(a * w.seg_dt[seg * (all / w.N) + bd]), h, own);
+        // (a state that is zero stays so, whatever a segment's growth: infinity times zero would be NaN)
+        h = h == 0.f ? own : fmaf(expf(a * w.seg_dt[seg * (all / w.N) + bd]), h, own);
     }
 }
 

@@ -1,5 +1,6 @@
 """Digits that the selective state space block keeps: decays that forget, rates without end, slopes far from zero, long sums and
 rows behind a length.  Every tolerance counts half steps, U = 2^-24 of a value, and is stated beside its test."""
+import numpy as np
 import pytest
 import torch
 
@@ -132,3 +133,20 @@ def test_rates_without_end(size, rate):
             assert torch.isfinite(v).all() and torch.equal(got[k], v), k
     assert torch.equal(got["pool"], o["h0"]) and torch.equal(got["h"][1], o["h0"][1])
     assert torch.equal(got["dh0"][1], dh[1])
+
+
+def test_growth_past_fp32_of_a_state_that_is_zero():
+    """Rates above zero over segments of time whose growth, exp(a times the segment's steps), passes fp32: a state that is
+    zero stays zero, as it does token by token."""
+    T, D, N = 6000, 3, 4
+    x, a = torch.zeros(1, T, D, device="cuda"), torch.full((D, N), 3.0, device="cuda")
+    dt, b = torch.ones_like(x), torch.ones(1, T, 1, N, device="cuda")
+    x[:, -1] = 2.0
+    y, h = fw.selective_scan(x, dt, a, b, b, softplus=False)
+    assert not y[:, :-1].any() and (y[:, -1] == 2.0 * N).all() and (h == 2.0).all()
+    dy = torch.zeros_like(x)
+    dy[:, 0] = 3.0
+    x.zero_()
+    g = fw.selective_scan_backward(x, dt, a, b, b, dy, softplus=False, h0=torch.zeros(1, D, N, device="cuda"))
+    assert (g["dx"][:, 0] == 3.0 * N).all() and not g["dx"][:, 1:].any() and not g["da"].any()
+    torch.testing.assert_close(g["dh0"], torch.full_like(g["dh0"], 3.0 * float(np.exp(3.0))), rtol=20 * U, atol=0)
