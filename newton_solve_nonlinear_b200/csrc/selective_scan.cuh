@@ -101,10 +101,10 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 // places behind a sequence, too) nothing decays, and zero times infinity would be NaN.
 __device__ __forceinline__ float finite(float v) { return min_nan(max_nan(v, -3.402823466e38f), 3.402823466e38f); }
 __device__ __forceinline__ float rate_of(float a) { return finite(a * kLog2eF); }
-// exp(v), |v| at most 150: ex2 of v log2(e) rounded, times what that rounding left out.  (One value at a time: a constant
+// exp(v), |v| at most 150: ex2 of v log2(e) rounded, times what that rounding and log2(e)'s own left out.  (One value at a time: a constant
 // of a packed operation takes two registers and two instructions to fill them.)
 __device__ __forceinline__ float exp_of(float v) {
-    const float t = v * kLog2eF, rest = fmaf(v, kLog2eF, -t);
+    const float t = v * kLog2eF, rest = fmaf(v, 1.92596299e-8f, fmaf(v, kLog2eF, -t));
     float e;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
     return fmaf(e, rest * 0.693147181f, e);

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import newton_solve_nonlinear_b200 as fw
+from oracle import bounds
 from tests.test_gpu_selective_scan import BF16, F32
 
 pytestmark = pytest.mark.gpu
@@ -150,3 +151,33 @@ def test_growth_past_fp32_of_a_state_that_is_zero():
     g = fw.selective_scan_backward(x, dt, a, b, b, dy, softplus=False, h0=torch.zeros(1, D, N, device="cuda"))
     assert (g["dx"][:, 0] == 3.0 * N).all() and not g["dx"][:, 1:].any() and not g["da"].any()
     torch.testing.assert_close(g["dh0"], torch.full_like(g["dh0"], 3.0 * float(np.exp(3.0))), rtol=20 * U, atol=0)
+
+
+def test_steps_far_from_zero():
+    """One token of one state from zero leaves h = softplus(dt): off by 16 U of it at most, at exp(-85) as near zero."""
+    dt = torch.cat([torch.arange(-85, 20, 0.37), torch.arange(-1, 1, 0.01)]).cuda()
+    D = dt.numel()
+    one = torch.ones(1, 1, D, device="cuda")
+    b = torch.ones(1, 1, 1, 1, device="cuda")
+    _, h = fw.selective_scan(one, dt.reshape(1, 1, D), torch.full((D, 1), -1e4, device="cuda"), b, b)
+    z = dt.double()
+    want = z.clamp(min=0) + torch.log1p(torch.exp(-z.abs()))
+    assert float(((h.flatten().double() - want).abs() / want).max()) <= 16 * U
+
+
+@pytest.mark.parametrize("dtype", [F32])
+def test_slopes_far_from_zero(dtype):
+    """dweight and dbias are fp32 whatever the inputs' type.  One token, one tap and dy = 1: the bias' gradient is silu's slope
+    at x, which bf16 holds exactly, and the tap's is that times x.  bounds.silu_slope_bound counts what fp32 makes of it."""
+    x = torch.cat([-torch.arange(1, 85, 0.5), torch.arange(0, 20, 0.5)]).to(dtype).cuda()
+    D = x.numel()
+    w = torch.zeros(D, 4, device="cuda")
+    w[:, 3] = 1.0
+    g = fw.causal_conv_backward(x.reshape(1, 1, D), w, torch.ones(1, 1, D, device="cuda", dtype=dtype), torch.zeros(D, device="cuda"))
+    z = x.double().cpu().numpy()
+    want, tol = bounds.silu_slope(z), bounds.silu_slope_bound(z).e
+    off = np.abs(g["dbias"].double().cpu().numpy() - want)
+    assert (off <= tol + 1e-37).all(), float((off / (tol + 1e-37)).max())
+    off = np.abs(g["dweight"][:, 3].double().cpu().numpy() - want * z)
+    assert (off <= (tol + U * np.abs(want)) * np.abs(z) + 1e-35).all()
+    assert not g["dweight"][:, :3].any()
