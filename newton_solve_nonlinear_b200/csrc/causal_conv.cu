@@ -61,7 +61,7 @@ __device__ __forceinline__ void put(T *p, const float (&f)[V]) {
     }
 }
 
-// 1 / (1 + exp(-p)).  bf16 results round 2^-9 of the value away: there the exponent need not carry p log2(e)'s last digits.
+// 1 / (1 + exp(-p)) for y.  A bf16 y rounds 2^-9 of the value away: there the exponent need not carry p log2(e)'s last digits.
 template <typename T>
 __device__ __forceinline__ float sigmoid_t(float p) {
     if constexpr (sizeof(T) == 4) return ss::sigmoid_of(p);
@@ -74,10 +74,10 @@ template <typename T>
 __device__ __forceinline__ float act_of(float p, bool silu) {
     return silu ? p * sigmoid_t<T>(p) : p;
 }
-template <typename T>
+// with all digits whatever the type: it goes into dweight and dbias, which are fp32
 __device__ __forceinline__ float slope_of(float p, bool silu) {
     if (!silu) return 1.f;
-    const float s = sigmoid_t<T>(p);
+    const float s = ss::sigmoid_of(p);
     return s * fmaf(p, 1.f - s, 1.f);
 }
 
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(256, 2) cc_backward_kernel(const CcArgs w, int
                 float p[V], out[V] = {};
                 pre(wk, bias, win, p);
 #pragma unroll
-                for (int u = 0; u < V; ++u) p[u] = g[u] * slope_of<T>(p[u], silu);  // g is zero behind the sequence
+                for (int u = 0; u < V; ++u) p[u] = g[u] * slope_of(p[u], silu);  // g is zero behind the sequence
                 shift(q, p);
 #pragma unroll
                 for (int u = 0; u < V; ++u) {

@@ -165,7 +165,7 @@ def test_steps_far_from_zero():
     assert float(((h.flatten().double() - want).abs() / want).max()) <= 16 * U
 
 
-@pytest.mark.parametrize("dtype", [F32])
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_slopes_far_from_zero(dtype):
     """dweight and dbias are fp32 whatever the inputs' type.  One token, one tap and dy = 1: the bias' gradient is silu's slope
     at x, which bf16 holds exactly, and the tap's is that times x.  bounds.silu_slope_bound counts what fp32 makes of it."""
