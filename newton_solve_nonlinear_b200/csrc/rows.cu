@@ -14,11 +14,15 @@ __global__ void __launch_bounds__(1024) rows_sum_kernel(const RowsSum a) {
     if (c < a.width) {
         const float *p = a.part + c;
         long long r = k;
-        for (; r + 96 < a.rows; r += 128) {
-            float v[4];
+        while (r + 96 < a.rows) {  // pieces of 64 rows: one long chain would lose digits
+            float piece = 0.f;
+            for (int j = 0; j < 16 && r + 96 < a.rows; ++j, r += 128) {
+                float v[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = p[(r + 32 * i) * a.width];
-            sum += (v[0] + v[1]) + (v[2] + v[3]);
+                for (int i = 0; i < 4; ++i) v[i] = p[(r + 32 * i) * a.width];
+                piece += (v[0] + v[1]) + (v[2] + v[3]);
+            }
+            sum += piece;
         }
         for (; r < a.rows; r += 32) sum += p[r * a.width];
     }

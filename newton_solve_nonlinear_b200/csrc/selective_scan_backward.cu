@@ -19,16 +19,22 @@ struct Smem {  // two of each, for groups of kK tokens in turn
     float b[2][kK][NP], c[2][kK][NP];
     float e[2][3][kK][L][ES];            // parts of sum G b, sum a P h and sum c h, summed over L
     float pb[2][kK][TS], pc[2][kK][TS];  // parts of db and dc, [ROWS][NP], summed over the rows
+    float4 sums[kThr];                   // dskip and ddt_bias of each finishing thread's two channels
 };
 
 // all threads of the CTA, which come from different places of the code
 __device__ __forceinline__ void meet() { asm volatile("bar.sync 1, %0;" ::"n"(2 * kThr) : "memory"); }
 
-// A launch has 128 registers to a thread.  The threads that hold states take 168, the others make do with 88; the two
-// together are what was there.
-constexpr int kRegs = 128, kStateRegs = 168;
-__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kStateRegs)); }
-__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(2 * kRegs - kStateRegs)); }
+// A launch has 128 registers to a thread.  The threads that hold states take more, the others make do with the rest: the two
+// together are what was there.  The others hold more in fp32, and spill with fewer (training step of 4 x 4096 x 2048 x 16 in
+// bf16: 1777 us with 168 to the states' threads, 1523 with 160, 1540 with 152; 4 x 2048 x 2048 x 16 in fp32: 1152, 1073, 885).
+constexpr int kRegs = 128;
+template <typename T>
+constexpr int kStateRegs = sizeof(T) == 4 ? 152 : 160;
+template <typename T>
+__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kStateRegs<T>)); }
+template <typename T>
+__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(2 * kRegs - kStateRegs<T>)); }
 
 // One CTA: 2 kThr / L channels of one group, one segment of one sequence, backward in time, eight tokens at a time.
 //   Four warps hold the states: a thread has S of each of two channels.  From the kept state its decays and states are formed
@@ -56,7 +62,7 @@ __global__ void __launch_bounds__(2 * kThr, 2) ss_backward_kernel(const SsArgs w
     float *part = w.part_a + (static_cast<long long>(seg) * w.B + b) * w.D * (w.N + 2);
 
     if (threadIdx.x < kThr) {
-        take_registers();
+        take_registers<T>();
         const int tid = threadIdx.x, pair = tid / L, n0 = tid % L * S, d = g * per + tile * CH + 2 * pair;
         const int owns = min(2, max(0, per - tile * CH - 2 * pair));
         const bool vec = w.N % S == 0;
@@ -182,7 +188,7 @@ __global__ void __launch_bounds__(2 * kThr, 2) ss_backward_kernel(const SsArgs w
 
     // SUB threads to each token of a group of eight and each pair of channels lc and lc + 1: they share the sums over the
     // lanes, of which there are more where there are fewer pairs
-    give_registers();
+    give_registers<T>();
     constexpr int LT = kK, PER = 1, SUB = kThr / (CH / 2) / kK;
     static_assert(SUB >= 1 && CH / 2 * SUB <= 32, "the threads of a token and pair are in one warp");
     const int tid = threadIdx.x - kThr;
@@ -339,16 +345,28 @@ __global__ void __launch_bounds__(2 * kThr, 2) ss_backward_kernel(const SsArgs w
         stage(t_start, n_chunk - 1 & 1);
         if (n_chunk > 1) fetch(t_start - kK);
     }
+    // dskip and ddt_bias, of sums over 64 of this thread's tokens: one long chain would lose digits.  (Kept in shared memory,
+    // and added outside the loop below: with a condition inside it a training step takes 10 % longer.)
+    float4 &sums = sm.sums[tid];
+    sums = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add_up = [&]() {
+        sums.x += dskip[0], sums.y += dskip[1], sums.z += dbias[0], sums.w += dbias[1];
+        dskip[0] = dskip[1] = dbias[0] = dbias[1] = 0.f;
+    };
     meet();
-    for (int k = n_chunk - 1, t0 = t_start; k >= 0; --k, t0 -= kK) {
-        if (k + 1 < n_chunk) finish(t0 + kK, k + 1 & 1, last);
-        if (k > 0) {
-            stage(t0 - kK, k - 1 & 1);
-            if (k > 1) fetch(t0 - 2 * kK);
-        }
-        meet();
+    for (int k = n_chunk - 1, t0 = t_start; k >= 0; add_up()) {
+        do {
+            if (k + 1 < n_chunk) finish(t0 + kK, k + 1 & 1, last);
+            if (k > 0) {
+                stage(t0 - kK, k - 1 & 1);
+                if (k > 1) fetch(t0 - 2 * kK);
+            }
+            meet();
+            t0 -= kK;
+        } while ((k-- & 63) != 0);
     }
     if (n_chunk > 0) finish(t_first, 0, now);
+    add_up();
     {  // nothing stands behind a sequence
         const long long out = static_cast<long long>(b) * w.T * w.D + ld;
         for (int t = max(t_len, t_first) + lt; t < t_end && sub == 0; t += LT) {
@@ -358,15 +376,12 @@ __global__ void __launch_bounds__(2 * kThr, 2) ss_backward_kernel(const SsArgs w
             if (gated) store_pair<VEC>(static_cast<T *>(w.dgate) + to, 0ull, have);
         }
     }
-    asm volatile("bar.sync 2, %0;" ::"n"(kThr) : "memory");  // the last group has been read, the others are done
-    float4 *s_sum = reinterpret_cast<float4 *>(smem);
-    s_sum[tid] = make_float4(dskip[0], dskip[1], dbias[0], dbias[1]);
     asm volatile("bar.sync 2, %0;" ::"n"(kThr) : "memory");
     if (tid < CH / 2) {
-        float4 s = s_sum[tid];
+        float4 s = sums;
 #pragma unroll
         for (int i = 1; i < LT * SUB; ++i) {
-            const float4 u = s_sum[tid + i * (CH / 2)];
+            const float4 u = sm.sums[tid + i * (CH / 2)];
             s.x += u.x, s.y += u.y, s.z += u.z, s.w += u.w;
         }
         float *to = part + static_cast<long long>(w.D) * w.N + ld;

@@ -181,3 +181,39 @@ def test_slopes_far_from_zero(dtype):
     off = np.abs(g["dweight"][:, 3].double().cpu().numpy() - want * z)
     assert (off <= (tol + U * np.abs(want)) * np.abs(z) + 1e-35).all()
     assert not g["dweight"][:, :3].any()
+
+
+def _sum_is_exact_to(got, want, steps, what):
+    off = float((got.double() - want).abs().max() / abs(want))
+    assert off <= steps * U, f"{what}: {off / U:.0f} half steps, {steps:.0f} allowed"
+
+
+def test_long_sums_of_the_scan_s_parameters():
+    """dskip, ddt_bias and da over 65536 tokens that are all alike: an fp32 chain loses the same part of each term, again and
+    again: n of them by up to n / 2 half steps of the sum.  Pieces of at most 64 tokens lose 32 U, the eight chains of T / 512
+    of them T / 1024 U, the sums over chains and rows 40 U; a term is a product of up to four factors, 8 U.  (100 groups: a card full of CTAs, so time is not split.)"""
+    T, D = 65536, 100
+    x, v = 0.63, 0.77
+    full = lambda *s, value: torch.full(s, value, device="cuda")
+    a = full(D, 1, value=-1e4)  # a token replaces the state
+    one = full(1, T, D, 1, value=1.0)
+    g = fw.selective_scan_backward(full(1, T, D, value=x), full(1, T, D, value=1.0), a, one, one, full(1, T, D, value=v),
+                                   skip=full(D, value=0.0), dt_bias=full(D, value=0.0), softplus=False)
+    term = float(np.float32(x)) * float(np.float32(v))
+    steps = 32 + T / 1024 + 40 + 8
+    _sum_is_exact_to(g["dskip"], T * term, steps, "dskip")
+    _sum_is_exact_to(g["ddt_bias"], T * term, steps, "ddt_bias")
+
+
+def test_long_sums_over_sequences():
+    """The same over 2^21 sequences of one token: 32 warps take the rows of partial sums, pieces of 64 in chains of 16, 8 U and two
+    more, and a chain of pieces, B / 4096 U; 8 U for the warps' sum, 8 U for a term."""
+    B = 1 << 21
+    full = lambda *s, value: torch.full(s, value, device="cuda")
+    one, p = full(B, 1, 1, 1, value=1.0), full(1, value=0.0)
+    g = fw.selective_scan_backward(full(B, 1, 1, value=0.63), full(B, 1, 1, value=1.0), full(1, 1, value=-1e4), one, one,
+                                   full(B, 1, 1, value=0.77), skip=p, dt_bias=p, softplus=False)
+    term = float(np.float32(0.63)) * float(np.float32(0.77))
+    steps = 10 + B / 4096 + 8 + 8
+    _sum_is_exact_to(g["dskip"], B * term, steps, "dskip")
+    _sum_is_exact_to(g["ddt_bias"], B * term, steps, "ddt_bias")
