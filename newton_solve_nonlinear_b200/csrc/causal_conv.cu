@@ -222,8 +222,8 @@ __global__ void __launch_bounds__(256, W <= 4 ? 3 : 2) cc_forward_kernel(const C
 }
 
 // The same walk for dx, W - 1 tokens behind p; a CTA is tx vectors of channels by 256 / tx runs, and keeps its sums for the
-// parameters in registers over all the runs it takes.  8 x 4096 x 2048 in bf16, 4 taps: 158 us, 0.39 of HBM's rate, bound by
-// its 37 instructions to an element (four channels to a thread: 239; checks at every token and runs of 32: 222).
+// parameters over all the runs it takes.  8 x 4096 x 2048 in bf16, 4 taps: 123 us, 0.50 of HBM's rate (four channels to a
+// thread, checks at every token or runs of 32 took half as long again).
 template <typename T, int W, int V>
 __global__ void __launch_bounds__(256, 2) cc_backward_kernel(const CcArgs w, int tx, int run) {
     extern __shared__ float s_part[];  // [V (W + 1)][256]
@@ -233,6 +233,18 @@ __global__ void __launch_bounds__(256, 2) cc_backward_kernel(const CcArgs w, int
     const long long all = static_cast<long long>(runs) * w.B;
     const bool silu = w.act == PARARNN_ACT_SILU, on = c < w.D;
     float wk[W][V] = {}, bias[V] = {}, dw[W][V] = {}, db[V] = {};
+    // the sums so far, of sums over 64 tokens: one long chain would lose digits
+    auto add_up = [&](bool first) {
+#pragma unroll
+        for (int u = 0; u < V; ++u)
+#pragma unroll
+            for (int k = 0; k <= W; ++k) {
+                float &part = s_part[(u * (W + 1) + k) * 256 + threadIdx.x], &own = k < W ? dw[W - 1 - k][u] : db[u];
+                part = first ? own : part + own;
+                own = 0.f;
+            }
+    };
+    add_up(true);
     if (on) {
         load_filter(w, c, wk, bias);
         for (long long i = static_cast<long long>(blockIdx.y) * ty + y_of; i < all; i += static_cast<long long>(gridDim.y) * ty) {
@@ -300,36 +312,33 @@ __global__ void __launch_bounds__(256, 2) cc_backward_kernel(const CcArgs w, int
             };
             const int stop = t_end + W - 1;
             const T *px = in.x + static_cast<long long>(t0 + AHEAD) * in.st, *pg = pdy + static_cast<long long>(t0 + AHEAD) * w.dy.st;
-            for (int t = t0; t < stop; t += AHEAD) {
-                Raw<T, V> cx[AHEAD], cg[AHEAD];
+            for (int t = t0; t < stop; add_up(false)) {
+                do {
+                    Raw<T, V> cx[AHEAD], cg[AHEAD];
 #pragma unroll
-                for (int j = 0; j < AHEAD; ++j) cx[j] = nx[j], cg[j] = ng[j];
-                if (t + 2 * AHEAD <= len) {
+                    for (int j = 0; j < AHEAD; ++j) cx[j] = nx[j], cg[j] = ng[j];
+                    if (t + 2 * AHEAD <= len) {
 #pragma unroll
-                    for (int j = 0; j < AHEAD; ++j) nx[j].get(px + j * w.x.st), ng[j].get(pg + j * w.dy.st);
-                } else if (t + AHEAD < stop) {
+                        for (int j = 0; j < AHEAD; ++j) nx[j].get(px + j * w.x.st), ng[j].get(pg + j * w.dy.st);
+                    } else if (t + AHEAD < stop) {
 #pragma unroll
-                    for (int j = 0; j < AHEAD; ++j) nx[j] = in.later(t + AHEAD + j), ng[j] = grad(t + AHEAD + j);
-                }
-                px += AHEAD * w.x.st, pg += AHEAD * w.dy.st;
-                // inside a run nothing has to be asked: dx is of its own tokens, which count and have no part of dlast
-                if (t >= t0 + W - 1 && t + AHEAD <= t_end && t + AHEAD - W < plain) {
+                        for (int j = 0; j < AHEAD; ++j) nx[j] = in.later(t + AHEAD + j), ng[j] = grad(t + AHEAD + j);
+                    }
+                    px += AHEAD * w.x.st, pg += AHEAD * w.dy.st;
+                    // inside a run nothing has to be asked: dx is of its own tokens, which count and have no part of dlast
+                    if (t >= t0 + W - 1 && t + AHEAD <= t_end && t + AHEAD - W < plain) {
 #pragma unroll
-                    for (int j = 0; j < AHEAD; ++j) token(std::true_type{}, t + j, true, cx[j], cg[j]);
-                } else {
+                        for (int j = 0; j < AHEAD; ++j) token(std::true_type{}, t + j, true, cx[j], cg[j]);
+                    } else {
 #pragma unroll
-                    for (int j = 0; j < AHEAD; ++j) token(std::false_type{}, t + j, t + j < t_end, cx[j], cg[j]);
-                }
+                        for (int j = 0; j < AHEAD; ++j) token(std::false_type{}, t + j, t + j < t_end, cx[j], cg[j]);
+                    }
+                    t += AHEAD;
+                } while (t < stop && (t - t0 & 63) != 0);
             }
         }
     }
     // the CTA's sums, over its rows of threads in order
-#pragma unroll
-    for (int u = 0; u < V; ++u) {
-#pragma unroll
-        for (int k = 0; k < W; ++k) s_part[(u * (W + 1) + W - 1 - k) * 256 + threadIdx.x] = dw[k][u];
-        s_part[(u * (W + 1) + W) * 256 + threadIdx.x] = db[u];
-    }
     __syncthreads();
     for (int o = threadIdx.x; o < tx * V * (W + 1); o += 256) {
         const int k = o / tx, xx = o % tx, u = k / (W + 1);

@@ -217,3 +217,19 @@ def test_long_sums_over_sequences():
     steps = 10 + B / 4096 + 8 + 8
     _sum_is_exact_to(g["dskip"], B * term, steps, "dskip")
     _sum_is_exact_to(g["ddt_bias"], B * term, steps, "ddt_bias")
+
+
+@pytest.mark.parametrize("B,T,D", [(1, 16384, 32768), (16, 4096, 32768), (3, 16384, 32767)])
+def test_long_sums_of_the_convolution_s_parameters(B, T, D):
+    """As above for taps and bias: a thread has whole sequences, or 2048 tokens and more of one.  Pieces of at most 64 tokens
+    lose 32 U and a chain of them, B T / 8 tokens to a thread at most, B T / 1024 U; 40 U for the sums over a CTA's threads and
+    over the CTAs, and for the product.  (x and dy are one value, expanded.)"""
+    x = torch.full((1, 1, 1), 0.63, device="cuda").expand(1, 1, D).contiguous().expand(B, T, D)
+    dy = torch.full((D,), 0.77, device="cuda").expand(B, T, D)
+    g = fw.causal_conv_backward(x, torch.zeros(D, 4, device="cuda"), dy, torch.zeros(D, device="cuda"), act="none")
+    assert not g["dx"].any()
+    x, v = float(np.float32(0.63)), float(np.float32(0.77))
+    steps = 32 + B * T / 1024 + 40
+    _sum_is_exact_to(g["dbias"], B * T * v, steps, "dbias")
+    for j in range(4):
+        _sum_is_exact_to(g["dweight"][:, j], B * (T - 3 + j) * x * v, steps, f"tap {j}")
