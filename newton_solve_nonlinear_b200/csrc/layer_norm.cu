@@ -432,11 +432,14 @@ void launch(const LnArgs &a, const Fit &f, cudaStream_t s) {
 
 }  // namespace
 
-// CTAs of the backward pass, each of which leaves a row of sums: what fits the card at once, fewer where there are fewer rows
+// CTAs of the backward pass, each of which leaves a row of sums: three to an SM, two and one where a thread has more vectors;
+// fewer where there are fewer rows, and further waves where a team would otherwise add up more than 128 rows in one chain,
+// which loses digits (444 CTAs on 2^20 rows: 370 half steps of dbias).
 int ln_backward_rows(const LnArgs &a) {
     const Fit f = fit(a);
-    const long long rows = static_cast<long long>(a.N) * a.S, teams = f.team == 32 ? 8 : 1;
-    return static_cast<int>(std::min<long long>((rows + teams - 1) / teams, 148 * (f.team > 256 ? 1 : f.k > 4 ? 2 : 3)));
+    const long long teams = f.team == 32 ? 8 : 1, groups = (static_cast<long long>(a.N) * a.S + teams - 1) / teams;
+    const long long wave = 148 * (f.team > 256 ? 1 : f.k > 4 ? 2 : 3), waves = f.k == 0 ? 1 : (groups + 128 * wave - 1) / (128 * wave);
+    return static_cast<int>(std::min(groups, wave * waves));
 }
 
 cudaError_t launch_ln_forward(const LnArgs &a, cudaStream_t s) {

@@ -233,3 +233,17 @@ def test_long_sums_of_the_convolution_s_parameters(B, T, D):
     _sum_is_exact_to(g["dbias"], B * T * v, steps, "dbias")
     for j in range(4):
         _sum_is_exact_to(g["dweight"][:, j], B * (T - 3 + j) * x * v, steps, f"tap {j}")
+
+
+@pytest.mark.parametrize("rows,C,teams", [(1 << 22, 8, 8), (1 << 20, 1024, 1), (1 << 18, 4096, 1), (1 << 18, 8192, 1), (1 << 17, 9216, 1),
+                                          (1 << 16, 32769, 8)])
+def test_long_sums_of_the_norm_s_parameters(rows, C, teams):
+    """As above for weight and bias: at least 148 CTAs of `teams` each take a row at a time, add up pieces of at most 64 rows, 32 U,
+    and a chain of the pieces; 40 U for the sums over the teams."""
+    r, dy = (torch.full((rows, C), value, device="cuda") for value in (0.63, 0.1))
+    stats = torch.tensor([0.0, 1.0], device="cuda").repeat(rows, 1)
+    g = fw.layer_norm_backward(r, stats, dy, torch.ones(C, device="cuda"), torch.zeros(C, device="cuda"), rms=True)
+    steps = 32 + rows / 148 / teams / 128 + 40 + 1
+    want = float(np.float32(0.1))
+    _sum_is_exact_to(g["dbias"], rows * want, steps, "dbias")
+    _sum_is_exact_to(g["dweight"], rows * want * float(np.float32(0.63)), steps, "dweight")
