@@ -192,7 +192,8 @@ __global__ void __launch_bounds__(cta_of<TEAM>()) ln_forward_kernel(const LnArgs
             float g[V], o[V];
 #pragma unroll
             for (int u = 0; u < V; ++u) g[u] = 1.f, o[u] = 0.f;
-            if (w.weight != nullptr) load<V>(w.weight + c, g);
+            // neither where the row does not count: it is zero whatever they hold
+            if (w.weight != nullptr && on) load<V>(w.weight + c, g);
             if (w.bias != nullptr && on) load<V>(w.bias + c, o);
 #pragma unroll
             for (int u = 0; u < V; ++u) v[i][u] = fmaf(v[i][u] * scale, g[u], o[u]);

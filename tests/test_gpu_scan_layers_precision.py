@@ -247,3 +247,16 @@ def test_long_sums_of_the_norm_s_parameters(rows, C, teams):
     want = float(np.float32(0.1))
     _sum_is_exact_to(g["dbias"], rows * want, steps, "dbias")
     _sum_is_exact_to(g["dweight"], rows * want * float(np.float32(0.63)), steps, "dweight")
+
+
+@pytest.mark.parametrize("C", [24, 33, 500, 1100, 9000, 33000])
+@pytest.mark.parametrize("rms", [False, True])
+def test_rows_behind_a_length_are_zero_whatever_the_weight(C, rms):
+    """A weight or bias that is not finite reaches the rows that count, and no others."""
+    g = torch.Generator(device="cuda").manual_seed(C)
+    x, res = (torch.randn(2, 3, C, device="cuda", generator=g) for _ in range(2))
+    w, b = torch.ones(C, device="cuda"), torch.zeros(C, device="cuda")
+    w[1], w[C - 1], b[2] = float("inf"), float("nan"), float("nan")
+    y, r, stats = fw.layer_norm(x, w, b, residual=res, rms=rms, lengths=torch.tensor([1, 0], dtype=torch.int32, device="cuda"))
+    assert not y[0, 1:].any() and not y[1].any() and not r[0, 1:].any() and not r[1].any()
+    assert torch.isinf(y[0, 0, 1]) and torch.isnan(y[0, 0, C - 1]) and torch.isnan(y[0, 0, 2])
