@@ -36,17 +36,16 @@ struct ScanCall {
     size_t states() const { return static_cast<size_t>(s.B) * s.D * s.N; }
     size_t tokens() const { return static_cast<size_t>(s.B) * s.T; }
     size_t kept() const { return static_cast<size_t>((s.T + kSsKeep - 1) / kSsKeep) * states(); }
-    void plan(bool backward) {
-        const SsPlan p = ss_plan(a, backward);
+    void forward() {
+        const SsPlan p = ss_plan(a);
         a.n_seg = p.n_seg, a.seg = p.seg;
         if (a.n_seg > 1) {
             a.seg_state = floats(a.n_seg * states());
             a.seg_dt = floats(static_cast<size_t>(a.n_seg) * s.B * s.D);
         }
     }
-    void forward() { plan(false); }
     void backward(bool has_kept) {
-        plan(true);
+        forward();
         if (a.n_seg > 1) a.rev_state = floats(a.n_seg * states());
         if (!has_kept) a.kept = floats(kept());
         const size_t part = static_cast<size_t>(ss_backward_tiles(a)) * tokens() * s.G * s.N;
@@ -65,7 +64,6 @@ struct ScanInputs {
     }
     static constexpr int kExtents = 8;
     void extents(const pararnn_scan_shape &s, Extent *e) const {
-        const pararnn_rows none{};
         e[0] = extent(*x, s.B, s.T, 1, s.D, s.dtype), e[1] = extent(*dt, s.B, s.T, 1, s.D, s.dtype);
         e[2] = extent(*b, s.B, s.T, s.G, s.N, s.dtype), e[3] = extent(*c, s.B, s.T, s.G, s.N, s.dtype);
         e[4] = gate == nullptr ? Extent{nullptr, 0} : extent(*gate, s.B, s.T, 1, s.D, s.dtype);

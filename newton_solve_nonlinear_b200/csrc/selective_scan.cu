@@ -384,10 +384,9 @@ bool ss_pairs_ok(const SsArgs &a) {
     return ok;
 }
 
-
 // Segments: none where two states to a thread fill two thirds of the SMs, since what they cost is a second pass; otherwise as
 // many as it takes to give every SM two CTAs at once, of at least 64 tokens each.
-SsPlan ss_plan(const SsArgs &a, bool) {
+SsPlan ss_plan(const SsArgs &a) {
     const long long most = ctas(a, lanes_of(a.N, a.N > 2 ? 2 : 4)), have = ctas(a, lanes_of(a.N, 4));
     const long long want = most >= 100 ? 1 : std::min<long long>(148 * 2 / have, (a.T + 63) / 64);
     if (want < 2) return {1, a.T};

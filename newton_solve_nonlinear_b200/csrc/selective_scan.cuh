@@ -50,7 +50,7 @@ struct SsArgs {
 struct SsPlan {
     int n_seg, seg;
 };
-SsPlan ss_plan(const SsArgs &a, bool backward);
+SsPlan ss_plan(const SsArgs &a);
 bool ss_pairs_ok(const SsArgs &a);       // pairs of channels and quads of b and c on their own alignment
 int ss_backward_tiles(const SsArgs &a);  // CTAs along a group's channels in the backward pass
 cudaError_t launch_ss_forward(const SsArgs &a, cudaStream_t s);
