@@ -296,10 +296,12 @@ __global__ void ss_join_kernel(const SsArgs w) {
     float h = first == nullptr ? 0.f : first[i];
     for (int k = 0; k < w.n_seg; ++k) {
         const int seg = REV ? w.n_seg - 1 - k : k;
-        const float own = at[seg * all];
+        // (both loads before the store and outside of the condition: a step of this chain is their latency)
+        const float own = at[seg * all], decay = expf(a * w.seg_dt[seg * (all / w.N) + bd]);
         at[seg * all] = h;
-        // (a state that is zero stays so, whatever a segment's growth: infinity times zero would be NaN)
-        h = h == 0.f ? own : fmaf(expf(a * w.seg_dt[seg * (all / w.N) + bd]), h, own);
+        // a state that is zero stays so, whatever a segment's growth: infinity times zero would be NaN
+        const float kept = h == 0.f ? 0.f : decay;
+        h = fmaf(kept, h, own);
     }
 }
 
