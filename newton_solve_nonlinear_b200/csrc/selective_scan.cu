@@ -109,9 +109,14 @@ __global__ void __launch_bounds__(2 * kThr, 2) ss_sweep_kernel(const SsArgs w) {
                             const u64 xx = pk(st * a[q][2 * i], st * a[q][2 * i + 1]), f = decay_factor(xx);
                             // one factor for both of a pair: two instructions, as moving it beside itself would take
                             float b0, b1, h0, h1;
-                            upk(bb[i], b0, b1), upk(REV ? h[q][i] : decay_rest(xx, h[q][i]), h0, h1);
-                            const u64 moved = pk(fmaf(u, b0, h0), fmaf(u, b1, h1));
-                            h[q][i] = REV ? fma2(f, moved, decay_rest(xx, moved)) : fma2(f, h[q][i], moved);
+                            upk(bb[i], b0, b1), upk(h[q][i], h0, h1);
+                            if constexpr (REV) {
+                                const u64 moved = pk(fmaf(u, b0, h0), fmaf(u, b1, h1));
+                                upk(mul2(f, moved), h0, h1);
+                                h[q][i] = with_rest(xx, h0, h1, moved);
+                            } else {
+                                h[q][i] = fma2(f, h[q][i], with_rest(xx, u * b0, u * b1, h[q][i]));
+                            }
                             if (OUT) part = i == 0 ? mul2(cc[i], h[q][i]) : fma2(cc[i], h[q][i], part);
                         }
                         if (OUT) y[q] = pair_sum(part);
@@ -290,7 +295,7 @@ __global__ void ss_join_kernel(const SsArgs w) {
     const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
     if (i >= all) return;
     const long long bd = i / w.N;
-    const float a = finite(w.a[bd % w.D * w.N + i % w.N]);
+    const float a = above_inf(w.a[bd % w.D * w.N + i % w.N]);
     const float *first = REV ? w.dh : w.h0;
     float *at = (REV ? w.rev_state : w.seg_state) + i;
     float h = first == nullptr ? 0.f : first[i];
@@ -490,7 +495,9 @@ __global__ void __launch_bounds__(256) ss_step_kernel(const SsStep w) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const u64 xx = mul2(st2, a[r][i]);
-                h[r][i] = fma2(decay_factor(xx), h[r][i], fma2(u2, pk(bf[2 * i], bf[2 * i + 1]), decay_rest(xx, h[r][i])));
+                float b0, b1;
+                upk(mul2(u2, pk(bf[2 * i], bf[2 * i + 1])), b0, b1);
+                h[r][i] = fma2(decay_factor(xx), h[r][i], with_rest(xx, b0, b1, h[r][i]));
                 y = i == 0 ? mul2(pk(cf[0], cf[1]), h[r][0]) : fma2(pk(cf[2], cf[3]), h[r][1], y);
             }
             out[r] = pair_sum(y);

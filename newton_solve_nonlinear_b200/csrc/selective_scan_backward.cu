@@ -114,14 +114,12 @@ __global__ void __launch_bounds__(2 * kThr, 2) ss_backward_kernel(const SsArgs w
                     for (int i = 0; i < Q; ++i) {
                         const u64 before = t == 0 ? first[q][i] : h[t == 0 ? 0 : t - 1][q][i];
                         const u64 xx = pk(st * a[q][2 * i], st * a[q][2 * i + 1]);
-                        float b0, b1, h0, h1;
-                        upk(bb[i], b0, b1), upk(decay_rest(xx, before), h0, h1);
-                        float x0, x1;
-                        upk(xx, x0, x1);
+                        float b0, b1, x0, x1;
+                        upk(bb[i], b0, b1), upk(xx, x0, x1);
                         if (slow_decay(x0)) slow |= 1u << ((t * 2 + q) * S + 2 * i);
                         if (slow_decay(x1)) slow |= 2u << ((t * 2 + q) * S + 2 * i);
                         e[t][q][i] = decay_factor(xx);
-                        h[t][q][i] = fma2(e[t][q][i], before, pk(fmaf(u, b0, h0), fmaf(u, b1, h1)));
+                        h[t][q][i] = fma2(e[t][q][i], before, with_rest(xx, u * b0, u * b1, before));
                     }
                 }
             }
@@ -154,7 +152,10 @@ __global__ void __launch_bounds__(2 * kThr, 2) ss_backward_kernel(const SsArgs w
                         }
                         x1 = i == 0 ? mul2(G, bb[i]) : fma2(G, bb[i], x1);
                         const int bit = (t * 2 + q) * S + 2 * i;
-                        p[q][i] = fma2(e[t][q][i], G, pk(slow & 1u << bit ? g0 : 0.f, slow & 2u << bit ? g1 : 0.f));
+                        upk(mul2(e[t][q][i], G), p0, p1);
+                        if (slow & 1u << bit) p0 += g0;
+                        if (slow & 2u << bit) p1 += g1;
+                        p[q][i] = pk(p0, p1);
                         const u64 m = mul2(p[q][i], before), aa = pk(a[q][2 * i], a[q][2 * i + 1]);
                         x2 = i == 0 ? mul2(m, aa) : fma2(m, aa, x2);
                         upk(m, m0, m1), upk(da[q][i], d0, d1);
