@@ -910,7 +910,8 @@ PARARNN_API size_t pararnn_selective_scan_workspace_size(const pararnn_scan_shap
  *   x, dt    [B, T, D] (pararnn_rows, stride_h unused: views of one projected
  *            tensor will do);  gate likewise, or NULL for no gate.
  *   b, c     [B, T, G, N] (pararnn_rows).
- *   a        DEVICE float [D, N], the rates: < 0 for states that decay.
+ *   a        DEVICE float [D, N], the rates: < 0 for states that decay, -inf for
+ *            states that every token replaces.
  *   skip, dt_bias  DEVICE float [D], or NULL for zero.
  *   h0       DEVICE float [B, D, N], the states before the first token, or NULL for zero.
  *   lengths  DEVICE int [B], or NULL for T: tokens at and behind lengths[b]

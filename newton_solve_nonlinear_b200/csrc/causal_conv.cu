@@ -170,8 +170,8 @@ __device__ __forceinline__ void shift(float (&win)[W][V], const float (&x)[V]) {
 
 // A thread takes V channels (four where they are aligned) through `run` tokens with the last W inputs in registers and the
 // next tokens' loads on their way; consecutive threads take consecutive channels.
-// Bound by HBM: 8 x 4096 x 4096 in bf16 with SiLU 120 us, 0.68 of its rate (eight channels to a thread: 311, one CTA to an SM;
-// eight tokens ahead: 132).
+// 8 x 4096 x 4096 in bf16 with SiLU 120 us, 0.68 of HBM's rate, with issue slots 65 % and the MUFU pipe 51 % busy at 34 % of the
+// warps (eight channels to a thread: 311, one CTA to an SM; eight tokens ahead: 132).
 template <typename T, int W, int V>
 __global__ void __launch_bounds__(256, W <= 4 ? 3 : 2) cc_forward_kernel(const CcArgs w, int run) {
     const int nv = w.D / V, runs = (w.T + run - 1) / run;
@@ -222,8 +222,9 @@ __global__ void __launch_bounds__(256, W <= 4 ? 3 : 2) cc_forward_kernel(const C
 }
 
 // The same walk for dx, W - 1 tokens behind p; a CTA is tx vectors of channels by 256 / tx runs, and keeps its sums for the
-// parameters over all the runs it takes.  8 x 4096 x 2048 in bf16, 4 taps: 123 us, 0.50 of HBM's rate (four channels to a
-// thread, checks at every token or runs of 32 took half as long again).
+// parameters over all the runs it takes.  8 x 4096 x 2048 in bf16, 4 taps: 122 us, 0.50 of HBM's rate: 37 instructions to an
+// element in 60 % of the issue slots, at 23 % of the warps (four channels to a thread, checks at every token or runs of 32 took
+// 1.4 to 1.5 times as long).
 template <typename T, int W, int V>
 __global__ void __launch_bounds__(256, 2) cc_backward_kernel(const CcArgs w, int tx, int run) {
     extern __shared__ float s_part[];  // [V (W + 1)][256]

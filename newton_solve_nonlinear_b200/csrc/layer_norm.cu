@@ -7,7 +7,10 @@
 //
 // A row lives in the registers of a team of 32, 256 or 1024 threads, so that it is read once and its variance is formed
 // about its mean; longer rows (more than 32768 channels, 8192 off alignment) are read again.
-// Bound by HBM: 32768 rows of 2048, bf16 onto an fp32 stream, 130 us, 0.94 of its rate; backward 16384 rows 109 us, 0.75.
+// Bound by HBM: 32768 rows of 2048, bf16 onto an fp32 stream, 129 us, 0.95 of its rate; backward 16384 rows 108 us, 0.75.
+// With more than four vectors to a thread registers run short: backward rows of 4096 and 8192 channels, one or two CTAs to an
+// SM, move at 0.50 and 0.54 of HBM's rate, and rows of 8193 to 32768 aligned channels go through local memory in part (16384:
+// forward 0.65, backward 0.08).
 #include <algorithm>
 
 #include "layer_norm.cuh"
@@ -433,13 +436,15 @@ void launch(const LnArgs &a, const Fit &f, cudaStream_t s) {
 
 }  // namespace
 
-// CTAs of the backward pass, each of which leaves a row of sums: three to an SM, two and one where a thread has more vectors;
-// fewer where there are fewer rows, and further waves where a team would otherwise add up more than 128 rows in one chain,
-// which loses digits (444 CTAs on 2^20 rows: 370 half steps of dbias).
+// CTAs of the backward pass, each of which leaves a row of sums: three to an SM, as fit it at 2048 channels (fewer do where a
+// thread has more vectors, or a warp a row), two and one for the widest; fewer where there are fewer rows, and further waves
+// where a team would otherwise add up more than 128 rows in one chain, which loses digits (444 CTAs on 2^20 rows: 370 half
+// steps of dbias).
 int ln_backward_rows(const LnArgs &a) {
     const Fit f = fit(a);
     const long long teams = f.team == 32 ? 8 : 1, groups = (static_cast<long long>(a.N) * a.S + teams - 1) / teams;
-    const long long wave = 148 * (f.team > 256 ? 1 : f.k > 4 ? 2 : 3), waves = f.k == 0 ? 1 : (groups + 128 * wave - 1) / (128 * wave);
+    const long long wave = 148 * (f.team > 256 ? 1 : f.k > 4 ? 2 : 3);
+    const long long waves = f.k == 0 ? 1 : (groups + 128 * wave - 1) / (128 * wave);
     return static_cast<int>(std::min(groups, wave * waves));
 }
 

@@ -31,7 +31,7 @@ __device__ __forceinline__ void meet() { asm volatile("bar.sync 1, %0;" ::"n"(2 
 //   Four more prepare the next chunk (s and s x of each token and channel; VEC: pairs of channels, and quads of b and c, lie
 // on their own alignment) and finish the last one (the sum over the lanes, skip, gate), in the gaps that the chains of
 // dependent operations leave the others.
-//   Bound by instructions, 13 to a state, issued in 61 % of the cycles: 8 x 4096 x 2048 x 16 in bf16 708 us, where the
+//   Bound by instructions, 13 to a state, issued in 61 % of the cycles: 8 x 4096 x 2048 x 16 in bf16 680 us, where the
 // exponentials alone take 239 and the bytes 82.  (Preparing and finishing in the states' own warps: 762.)
 //   kOutputs      from the start state: y, the kept states, and the last segment's last state
 //   kStates       from the start state: the kept states alone
@@ -422,8 +422,8 @@ namespace {
 // CTAs along the channels of each row; L lanes of four states hold a channel, each thread of R channels that stand CH apart,
 // of which it prepares and finishes one (the lanes take turns).  Everything that a row needs is asked for at once, behind its
 // slot alone.  Rows that name the same slot are taken in row order by the first one's CTA, as tokens that follow each other.
-// 256 rows of 4096 channels of 16: 43.5 us, 0.48 of HBM's rate, bound by instructions (one channel to a thread, prepared by
-// all of its lanes, with its loads in four steps: 83).
+// 256 rows of 4096 channels of 16: 45 us, 0.48 of HBM's rate; issue slots 73 % busy with 63 instructions to a state, most of them
+// the row's and the channel's own (one channel to a thread, prepared by all of its lanes, with its loads in four steps: 83).
 template <typename T, int L, int R, bool VEC>
 __global__ void __launch_bounds__(256) ss_step_kernel(const SsStep w) {
     constexpr int CH = 256 / L, BW = VEC ? 4 : 1;
@@ -558,7 +558,9 @@ void launch_step(const SsStep &w, cudaStream_t s) {
         quads = quads && reinterpret_cast<uintptr_t>(r->p) % e == 0 && r->sb % 4 == 0 && r->sg % 4 == 0;
     const unsigned two = static_cast<unsigned>((w.D + 2 * CH - 1) / (2 * CH)) * w.B;
     if (!quads) ss_step_kernel<T, L, 1, false><<<static_cast<unsigned>(one), 256, 0, s>>>(w);
-    else if (L == 1 || one <= 148 * 6) ss_step_kernel<T, L, 1, true><<<static_cast<unsigned>(one), 256, 0, s>>>(w);  // one wave
+    // one channel to a thread while that is little more than a wave (five of these CTAs fit an SM): 256 CTAs 2.6 us against 2.7
+    // with two, 704 3.7 against 3.3, 896 4.9 against 3.8
+    else if (L == 1 || one <= 148 * 6) ss_step_kernel<T, L, 1, true><<<static_cast<unsigned>(one), 256, 0, s>>>(w);
     else ss_step_kernel<T, L, L == 1 ? 1 : 2, true><<<two, 256, 0, s>>>(w);
 }
 template <typename T>

@@ -101,8 +101,8 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 // is zero (in the places behind a sequence, too) nothing decays, and zero times infinity would be NaN.
 __device__ __forceinline__ float above_inf(float v) { return max_nan(v, -3.402823466e38f); }
 __device__ __forceinline__ float rate_of(float a) { return above_inf(a * kLog2eF); }
-// exp(v), |v| at most 150: ex2 of v log2(e) rounded, times what that rounding and log2(e)'s own left out.  (One value at a time: a constant
-// of a packed operation takes two registers and two instructions to fill them.)
+// exp(v), |v| at most 150: ex2 of v log2(e) rounded, times what that rounding and log2(e)'s own left out.  (One value at a
+// time: a constant of a packed operation takes two registers and two instructions to fill them.)
 __device__ __forceinline__ float exp_of(float v) {
     const float t = v * kLog2eF, rest = fmaf(v, 1.92596299e-8f, fmaf(v, kLog2eF, -t));
     float e;

@@ -41,8 +41,9 @@ __device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.
 // again into registers, then walked backward.  What it sums over its channels (for db, dc) and over its states (for dx, ds
 // and the inner y) leaves 1 / 2 and 1 / S of the values to pass through shared memory.
 //   Four more prepare the next eight tokens, and finish the last ones: those sums, the gradients of each token and channel,
-// and the CTA's part of db and dc.  4 x 4096 x 2048 x 16 in bf16: 1070 us, 37 instructions to a state issued in 55 % of the
-// cycles (preparing and finishing in the states' own warps: 1310).  VEC: pairs of channels, and quads of b and c, lie on their own alignment.
+// and the CTA's part of db and dc.  4 x 4096 x 2048 x 16 in bf16: 975 us, 40 instructions to a state issued in 62 % of the
+// cycles.  (Preparing and finishing in the states' own warps took a fifth longer.)  VEC: pairs of channels, and quads of b and
+// c, lie on their own alignment.
 template <typename T, int S, int L, bool VEC>
 __global__ void __launch_bounds__(2 * kThr, 2) ss_backward_kernel(const SsArgs w) {
     using SM = Smem<S, L>;
